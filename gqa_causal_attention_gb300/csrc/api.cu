@@ -5,6 +5,7 @@
 
 #include "../../include/gqa_attn.h"
 #include "kernels.h"
+#include "kv_q4.cuh"
 
 namespace {
 
@@ -88,6 +89,14 @@ struct Finite {
     gqa::FiniteRegion& r = j.r[j.n++];
     r.p = p; r.B = B; r.NH = NH; r.R = R; r.C = C; r.ld = ld > 0 ? ld : C;
     r.mode = mode; r.info = info; r.window = window;
+  }
+  // The scales of 4-bit records [B, Hkv, capacity]: mode kFiniteCache or kFiniteSpan.
+  void add_q4(const void* cache, int B, int Hkv, long capacity, int D, int mode,
+              const int32_t* info, int window, int span) {
+    add(static_cast<const float*>(cache), B, Hkv, capacity, D, mode, info, window);
+    gqa::FiniteRegion& r = j.r[j.n - 1];
+    r.q4 = D / 32;
+    r.span = span;
   }
   int gate(int32_t* status, cudaStream_t s, const int32_t** skip) {
     *skip = nullptr;
@@ -1133,6 +1142,245 @@ int gqa_attn_decode_step(const float* q, const float* k, const float* v, float* 
   gqa::decode_split_plan(B, Hkv, max_pos + 1, window, &j.nsplit, &j.chunk);
   j.partial = reinterpret_cast<float*>(ws + lay.part);
   return cuda_status(gqa::launch_decode(j, s, fused ? &st : nullptr));
+}
+
+
+// ---------------------------------------------------------------- the cache in 4 bits
+
+namespace {
+
+bool q4_dims_ok(int B, int Hx, int Hkv, int L, int D) {
+  return dims_ok(B, Hx, L, D) && Hkv >= 1 && Hx % Hkv == 0 && D % 32 == 0;
+}
+
+// The number of blocks of a launch is bounded by 2^31 - 1: rows and heads stay far below.
+bool q4_grid_ok(int B, int H) { return static_cast<int64_t>(B) * H <= (1 << 20); }
+
+// Host checks that an append and a decode step share; fills the job's cache part.
+int q4_append_check(const attn_rope_params* rp, const float* table, const float* k_norm_w,
+                    float norm_eps, int D, int L, int32_t max_start, const int32_t* pos,
+                    int32_t max_pos, int capacity, int window, gqa::AppendQ4Job* j) {
+  if (rp ? !table : (table || k_norm_w)) return rp ? ATTN_ERR_NULL : ATTN_ERR_PARAM;
+  if (rp && !rope_params_ok(rp, D)) return ATTN_ERR_PARAM;
+  if (!(norm_eps >= 0.f)) return ATTN_ERR_PARAM;
+  const int max_positions = rp ? max_pos_of(rp) : 0x7fffffff;
+  const int32_t last = pos ? max_pos : max_start;
+  if (max_start < 0 || (int64_t)max_start + L > 0x7fffffff) return ATTN_ERR_POSITION;
+  if (last < 0 || (int64_t)last + L > (int64_t)max_positions) return ATTN_ERR_POSITION;
+  if (window == 0 && (int64_t)max_start + L > (int64_t)capacity) return ATTN_ERR_CAPACITY;
+  j->L = L; j->D = D; j->R = rp ? rope_dim_of(rp, D) : D;
+  j->pos = pos;
+  j->table = reinterpret_cast<const float2*>(table);
+  j->norm_w = k_norm_w; j->norm_eps = norm_eps; j->max_positions = max_positions;
+  j->capacity = capacity; j->window = window;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+size_t kv_q4_record_bytes(int D) {
+  if (D < 32 || D > gqa::kMaxHeadDim || D % 32) return 0;
+  return gqa::q4::record_bytes(D / 32);
+}
+
+int kv_cache_append_q4(const float* k, const float* v, float* k_out, int B, int Hkv, int L, int D,
+                       const int32_t* start, int32_t max_start, const int32_t* pos,
+                       int32_t max_pos, const attn_rope_params* rp, const float* table,
+                       const float* k_norm_w, float norm_eps, void* cache, int capacity,
+                       int window, int32_t* status, void* stream) {
+  if (!q4_dims_ok(B, Hkv, Hkv, L, D) || capacity < 1 || window < 0 || !q4_grid_ok(B, Hkv))
+    return ATTN_ERR_SHAPE;
+  if (window > 0 && capacity != window) return ATTN_ERR_SHAPE;
+  if (B == 0 || L == 0) return ATTN_OK;
+  if (!k || !v || !start || !cache) return ATTN_ERR_NULL;
+  gqa::AppendQ4Job j{};
+  if (const int rc = q4_append_check(rp, table, k_norm_w, norm_eps, D, L, max_start, pos, max_pos,
+                                     capacity, window, &j))
+    return rc;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || (k_out && !aligned16(k_out)) ||
+      (table && !aligned16(table)) || (k_norm_w && !aligned16(k_norm_w)))
+    return ATTN_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Finite fin;
+  fin.add(k, B, Hkv, L, D);
+  fin.add(v, B, Hkv, L, D);
+  fin.add(k_norm_w, 1, 1, 1, D);
+  if (const int rc = fin.gate(status, s, &j.skip)) return rc;
+  j.k = k; j.v = v; j.k_out = k_out; j.cache = static_cast<uint8_t*>(cache);
+  j.B = B; j.Hkv = Hkv; j.start = start; j.status = status;
+  return cuda_status(gqa::launch_append_q4(j, s));
+}
+
+int kv_cache_read_q4(const void* cache, int capacity, int window, float* k, float* v, int B,
+                     int Hkv, int L, int D, const int32_t* start, int32_t max_start,
+                     int32_t* status, void* stream) {
+  if (!q4_dims_ok(B, Hkv, Hkv, L, D) || capacity < 1 || window < 0 || !q4_grid_ok(B, Hkv))
+    return ATTN_ERR_SHAPE;
+  if (window > 0 && (capacity != window || L > window)) return ATTN_ERR_SHAPE;
+  if (B == 0 || L == 0) return ATTN_OK;
+  if (!cache || !k || !v || !start) return ATTN_ERR_NULL;
+  if (max_start < 0 || (int64_t)max_start + L > 0x7fffffff) return ATTN_ERR_POSITION;
+  if (window == 0 && (int64_t)max_start + L > (int64_t)capacity) return ATTN_ERR_CAPACITY;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v)) return ATTN_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  gqa::ReadQ4Job j{};
+  Finite fin;
+  fin.add_q4(cache, B, Hkv, capacity, D, gqa::kFiniteSpan, start, window, L);
+  if (const int rc = fin.gate(status, s, &j.skip)) return rc;
+  j.cache = static_cast<const uint8_t*>(cache); j.k = k; j.v = v;
+  j.B = B; j.Hkv = Hkv; j.L = L; j.D = D; j.capacity = capacity; j.window = window;
+  j.start = start; j.status = status;
+  return cuda_status(gqa::launch_read_q4(j, s));
+}
+
+size_t gqa_attn_decode_q4_workspace_size(int B, int H, int Hkv, int D, int max_cache_len,
+                                         int window, int with_weights) {
+  if (B < 1 || !q4_dims_ok(B, H, Hkv, 1, D) || !q4_grid_ok(B, H) || max_cache_len < 1 ||
+      window < 0)
+    return 0;
+  return gqa::decode_q4_bytes(B, H, Hkv, D, max_cache_len, window, with_weights != 0, true);
+}
+
+namespace {
+// Checks that a decode and a decode step share; fills the attention job.
+int q4_decode_check(int B, int H, int Hkv, int D, int capacity, int window, float softcap,
+                    float scale, const float* weights, gqa::DecodeQ4Job* j) {
+  if (!q4_dims_ok(B, H, Hkv, 1, D) || !q4_grid_ok(B, H) || window < 0 || capacity < 1)
+    return ATTN_ERR_SHAPE;
+  if (window > 0 && (capacity != window || weights)) return ATTN_ERR_SHAPE;
+  if (!isfinite(softcap) || !isfinite(scale)) return ATTN_ERR_PARAM;
+  j->B = B; j->H = H; j->Hkv = Hkv; j->D = D; j->capacity = capacity; j->window = window;
+  j->softcap = softcap > 0.f ? softcap : 0.f;
+  j->scale = scale > 0.f ? scale : 1.0f / sqrtf((float)D);
+  return ATTN_OK;
+}
+}  // namespace
+
+int gqa_attn_decode_q4(const float* q, const void* cache, const int32_t* cache_len,
+                       int32_t max_cache_len, float* out, float* weights, int B, int H, int Hkv,
+                       int D, int capacity, int window, float softcap, float scale,
+                       void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  gqa::DecodeQ4Job j{};
+  if (const int rc = q4_decode_check(B, H, Hkv, D, capacity, window, softcap, scale, weights, &j))
+    return rc;
+  if (B == 0) return ATTN_OK;
+  if (max_cache_len < 1) return ATTN_ERR_SHAPE;
+  if (window == 0 && max_cache_len > capacity) return ATTN_ERR_CAPACITY;
+  if (!q || !cache || !cache_len || !out) return ATTN_ERR_NULL;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return ATTN_ERR_ALIGN;
+  const size_t need =
+      gqa::decode_q4_bytes(B, H, Hkv, D, max_cache_len, window, weights != nullptr, false);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Finite fin;
+  fin.add(q, B, H, 1, D);
+  fin.add_q4(cache, B, Hkv, capacity, D, gqa::kFiniteCache, cache_len, window, 0);
+  if (const int rc = fin.gate(status, s, &j.skip)) return rc;
+  j.q = q; j.cache = static_cast<const uint8_t*>(cache); j.cache_len = cache_len;
+  j.max_cache_len = max_cache_len; j.out = out; j.weights = weights; j.status = status;
+  gqa::decode_q4_workspace(&j, workspace);
+  return cuda_status(gqa::launch_decode_q4(j, s));
+}
+
+namespace {
+// Workspace of gqa_attn_decode_step_q4: rotated q [B, H, D] | cache lengths [B] | the
+// decode's.
+struct StepQ4Layout {
+  size_t cl, part, total;
+};
+StepQ4Layout step_q4_layout(int B, int H, int Hkv, int D, int len, int window, bool weights,
+                            bool bound) {
+  StepQ4Layout y{};
+  y.cl = round256((size_t)B * H * D * sizeof(float));
+  y.part = y.cl + round256((size_t)B * sizeof(int32_t));
+  y.total = y.part + round256(gqa::decode_q4_bytes(B, H, Hkv, D, len, window, weights, bound));
+  return y;
+}
+}  // namespace
+
+size_t gqa_attn_decode_step_q4_workspace_size(int B, int H, int Hkv, int D, int32_t max_start,
+                                              int window, int with_weights) {
+  if (B < 1 || !q4_dims_ok(B, H, Hkv, 1, D) || !q4_grid_ok(B, H) || max_start < 0 ||
+      max_start == 0x7fffffff || window < 0)
+    return 0;
+  return step_q4_layout(B, H, Hkv, D, max_start + 1, window, with_weights != 0, true).total;
+}
+
+int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, float* out, int B,
+                            int H, int Hkv, int D, const int32_t* start, int32_t max_start,
+                            const int32_t* pos, int32_t max_pos, const attn_rope_params* rp,
+                            const float* table, const float* q_norm_w, const float* k_norm_w,
+                            float norm_eps, void* cache, float* weights, int capacity, int window,
+                            float softcap, float scale, void* workspace, size_t workspace_bytes,
+                            int32_t* status, void* stream) {
+  gqa::DecodeQ4Job j{};
+  if (const int rc = q4_decode_check(B, H, Hkv, D, capacity, window, softcap, scale, weights, &j))
+    return rc;
+  if (!rp) return ATTN_ERR_NULL;
+  if (!rope_params_ok(rp, D)) return ATTN_ERR_PARAM;
+  if (B == 0) return ATTN_OK;
+  if (!q || !k || !v || !out || !start || !table || !cache) return ATTN_ERR_NULL;
+  gqa::PrepQ4Job p{};
+  if (const int rc = q4_append_check(rp, table, k_norm_w, norm_eps, D, 1, max_start, pos, max_pos,
+                                     capacity, window, &p.kv))
+    return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(table) ||
+      !aligned16(cache) || (q_norm_w && !aligned16(q_norm_w)) ||
+      (k_norm_w && !aligned16(k_norm_w)))
+    return ATTN_ERR_ALIGN;
+  const StepQ4Layout lay =
+      step_q4_layout(B, H, Hkv, D, max_start + 1, window, weights != nullptr, false);
+  if (!workspace || workspace_bytes < lay.total) return ATTN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Finite fin;
+  fin.add(q, B, H, 1, D);
+  fin.add(k, B, Hkv, 1, D);
+  fin.add(v, B, Hkv, 1, D);
+  fin.add_q4(cache, B, Hkv, capacity, D, gqa::kFiniteCache, start, window, 0);
+  fin.add(q_norm_w, 1, 1, 1, D);
+  fin.add(k_norm_w, 1, 1, 1, D);
+  if (const int rc = fin.gate(status, s, &j.skip)) return rc;
+  p.kv.k = k; p.kv.v = v; p.kv.cache = static_cast<uint8_t*>(cache);
+  p.kv.B = B; p.kv.Hkv = Hkv; p.kv.start = start; p.kv.status = status; p.kv.skip = j.skip;
+  p.q = q; p.qrot = reinterpret_cast<float*>(ws); p.q_norm_w = q_norm_w;
+  p.cache_len = reinterpret_cast<int32_t*>(ws + lay.cl); p.H = H;
+  if (const cudaError_t e = gqa::launch_prep_q4(p, s); e != cudaSuccess) return cuda_status(e);
+  j.q = p.qrot; j.cache = p.kv.cache; j.cache_len = p.cache_len;
+  j.max_cache_len = max_start + 1; j.out = out; j.weights = weights; j.status = status;
+  gqa::decode_q4_workspace(&j, ws + lay.part);
+  return cuda_status(gqa::launch_decode_q4(j, s));
+}
+
+int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* cache_len,
+                      int32_t max_cache_len, int budget, int recent, void* cache_out,
+                      float* weights_out, int32_t* index, int32_t* len_out, int B, int Hkv, int D,
+                      int capacity, int capacity_out, int32_t* status, void* stream) {
+  if (!q4_dims_ok(B, Hkv, Hkv, 1, D) || capacity < 1 || budget < 1 || recent < 0 ||
+      recent > budget || (int64_t)B * Hkv > 65535)
+    return ATTN_ERR_SHAPE;
+  if (B == 0) return ATTN_OK;
+  if (max_cache_len < 0) return ATTN_ERR_SHAPE;
+  if (max_cache_len > capacity || budget > capacity_out) return ATTN_ERR_CAPACITY;
+  if (!cache || !weights || !cache_len || !cache_out || !weights_out || !index || !len_out)
+    return ATTN_ERR_NULL;
+  if (cache == cache_out || weights == weights_out || cache_len == len_out) return ATTN_ERR_PARAM;
+  if (!aligned16(cache) || !aligned16(cache_out)) return ATTN_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  gqa::EvictQ4Job j{};
+  Finite fin;
+  fin.add_q4(cache, B, Hkv, capacity, D, gqa::kFiniteCache, cache_len, 0, 0);
+  if (const int rc = fin.gate(status, s, &j.skip)) return rc;
+  j.cache = static_cast<const uint8_t*>(cache); j.weights = weights; j.cache_len = cache_len;
+  j.max_cache_len = max_cache_len; j.budget = budget; j.recent = recent;
+  j.cache_out = static_cast<uint8_t*>(cache_out); j.weights_out = weights_out; j.index = index;
+  j.len_out = len_out; j.B = B; j.Hkv = Hkv; j.D = D; j.capacity = capacity;
+  j.capacity_out = capacity_out; j.status = status;
+  return cuda_status(gqa::launch_evict_q4(j, s));
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv_q4.cuh"
 
 namespace gqa {
 
@@ -52,6 +53,18 @@ __device__ __forceinline__ RowSet rows_of(const FiniteRegion& g, int b) {
       s.ring_lo = (st - pre) % g.window;
       s.hi = pre;
     }
+  } else if (g.mode == kFiniteSpan) {
+    const long st = g.info[b];
+    if (st < 0) {
+      s.hi = 0;
+    } else if (g.window == 0) {
+      s.lo = st;
+      s.hi = st + g.span;
+    } else {
+      s.W = g.window;
+      s.ring_lo = st % g.window;
+      s.hi = g.span;
+    }
   }
   return s;
 }
@@ -76,6 +89,13 @@ __global__ void __launch_bounds__(256) finite_check_kernel(FiniteJob j) {
       const bool in = s.W > 0 ? ((r - s.ring_lo) % s.W + s.W) % s.W < s.hi
                               : (r >= s.lo && r < s.hi);
       if (!in) continue;
+      if (g.q4 > 0) {
+        const uint8_t* rec = reinterpret_cast<const uint8_t*>(g.p) +
+                             (o * g.R + r) * q4::record_bytes(g.q4) + 32 * g.q4;
+        for (int c = lane; c < 2 * g.q4; c += 32)
+          bad |= (reinterpret_cast<const uint16_t*>(rec)[c] & 0x7f80u) == 0x7f80u;
+        continue;
+      }
       const float* row = g.p + (o * g.R + r) * g.ld;
       if (vec) {
         const float4* r4 = reinterpret_cast<const float4*>(row);

@@ -315,8 +315,9 @@ cudaError_t launch_append_vt(const AppendVtJob& j, cudaStream_t stream);
 enum { kFiniteAll = 0,       // every row
        kFiniteLen = 1,       // rows < info[b] (a ragged row's length)
        kFiniteCache = 2,     // cache slots live at cache length info[b]: rows < min(info[b], R)
-       kFinitePrefix = 3 };  // slots of the positions a chunk at start info[b] reads from the
+       kFinitePrefix = 3,    // slots of the positions a chunk at start info[b] reads from the
                              // cache: all below it, or the last window - 1 of them in a ring
+       kFiniteSpan = 4 };    // slots of positions info[b] .. info[b] + span - 1 (mod window in a ring)
 struct FiniteRegion {
   const float* p;
   int B, NH;
@@ -324,6 +325,9 @@ struct FiniteRegion {
   int mode;
   const int32_t* info;
   int window;
+  int q4;                    // > 0: rows are 4-bit records of 32 q4 dims (p: the first record);
+                             // their scales are checked
+  int span;                  // kFiniteSpan
 };
 constexpr int kMaxFiniteRegions = 12;
 struct FiniteJob {
@@ -343,5 +347,88 @@ size_t decode_partial_bytes(int B, int H, int Hkv, int D, int max_cache_len, int
 cudaError_t launch_decode(const DecodeJob& j, cudaStream_t stream,
                           const DecodeStepArgs* step = nullptr);
 int decode_launches(const DecodeJob& j, bool step);   // kernels launch_decode launches
+
+// The cache held in 4 bits (kv_q4.cuh: one record per slot, key and value; kernels in
+// kv_q4.cu and decode_q4.cu). D % 32 == 0 throughout.
+
+// Rows of k and v, [B, Hkv, L, D], into the records of their slots.
+struct AppendQ4Job {
+  const float* k;
+  const float* v;
+  float* k_out;             // [B, Hkv, L, D] normed and rotated keys in fp32 (may be k), or nullptr
+  uint8_t* cache;           // [B, Hkv, capacity, record_bytes]
+  int B, Hkv, L, D, R;
+  const int32_t* start;     // [B] row b's first slot position
+  const int32_t* pos;       // [B] its first rotary position, or nullptr: start
+  const float2* table;      // nullptr: no rotation
+  const float* norm_w;
+  float norm_eps;
+  int max_positions, capacity, window;
+  int32_t* status;
+  const int32_t* skip = nullptr;
+};
+cudaError_t launch_append_q4(const AppendQ4Job& j, cudaStream_t stream);
+
+// Records of slots of positions start[b] .. start[b] + L - 1 back to fp32.
+struct ReadQ4Job {
+  const uint8_t* cache;
+  float* k;                 // [B, Hkv, L, D]
+  float* v;
+  int B, Hkv, L, D, capacity, window;
+  const int32_t* start;
+  int32_t* status;
+  const int32_t* skip = nullptr;
+};
+cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream);
+
+// Of each head's live slots, the budget ones to keep, compacted into another cache.
+struct EvictQ4Job {
+  const uint8_t* cache;     // [B, Hkv, capacity, record_bytes]
+  const float* weights;     // [B, Hkv, capacity]
+  const int32_t* cache_len; // [B]
+  int max_cache_len, budget, recent;
+  uint8_t* cache_out;       // [B, Hkv, capacity_out, record_bytes]
+  float* weights_out;       // [B, Hkv, capacity_out]
+  int32_t* index;           // [B, Hkv, budget]
+  int32_t* len_out;         // [B]
+  int B, Hkv, D, capacity, capacity_out;
+  int32_t* status;
+  const int32_t* skip = nullptr;
+};
+cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream);
+
+struct DecodeQ4Job {
+  const float* q;           // [B, H, D]
+  const uint8_t* cache;
+  const int32_t* cache_len; // [B]
+  int max_cache_len;
+  float* out;               // [B, H, D]
+  float* weights;           // [B, Hkv, capacity] or nullptr: += each slot's softmax weights
+  int B, H, Hkv, D, capacity, window;
+  float softcap, scale;
+  float* partial;           // [B * H * nsplit, D] outputs, then (m, l) pairs
+  float* scores;            // weights only: [B * H, pitch] scores in log2 units
+  int nsplit, chunk, pitch;
+  int32_t* status;
+  const int32_t* skip = nullptr;
+};
+void decode_q4_plan(int B, int H, int Hkv, int max_cache_len, int window, int* nsplit, int* chunk);
+// Workspace of a decode: its partials (for exactly this length, or the most for any
+// length up to it) and, with weights, its scores.
+size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights,
+                       bool bound);
+void decode_q4_workspace(DecodeQ4Job* j, void* workspace);   // plan and pointers into it
+cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream);
+
+// A decode step's first pass: the rows' q normed and rotated, their k and v appended.
+struct PrepQ4Job {
+  AppendQ4Job kv;           // L = 1
+  const float* q;           // [B, H, D] raw
+  float* qrot;              // [B, H, D]
+  const float* q_norm_w;
+  int32_t* cache_len;       // [B] out: start + 1, 0 for a row that is skipped
+  int H;
+};
+cudaError_t launch_prep_q4(const PrepQ4Job& j, cudaStream_t stream);
 
 }  // namespace gqa

@@ -1,0 +1,526 @@
+// Writing, reading back and trimming the 4-bit KV cache (record format: kv_q4.cuh).
+//
+// The cache is the caller-owned TransformerState of "mojolearn.transformer" with
+// quantised storage ("dew.nn.backbones.causal_transformer": caches dense or paged,
+// full or quantized); slots follow the same rules as kv_cache_append's.
+//
+// All of it is memory-bound: a warp per row with 16-byte reads of fp32 rows, and the
+// records moved in 16-byte pieces.
+#include "common.cuh"
+#include "kernels.h"
+#include "kv_q4.cuh"
+
+namespace gqa {
+
+namespace {
+
+__host__ __device__ constexpr int quads_per_lane(int M) { return (8 * M + 31) / 32; }
+
+// Calls f(std::integral_constant-like tag) for the runtime group count m = D / 32.
+template <int M>
+struct Groups {
+  static constexpr int value = M;
+};
+template <class F>
+cudaError_t with_groups(int m, F f) {
+  switch (m) {
+    case 1: return f(Groups<1>{});
+    case 2: return f(Groups<2>{});
+    case 3: return f(Groups<3>{});
+    case 4: return f(Groups<4>{});
+    case 5: return f(Groups<5>{});
+    case 6: return f(Groups<6>{});
+    case 7: return f(Groups<7>{});
+    case 8: return f(Groups<8>{});
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// A lane's quads of a raw row with their rotary partners, angles and norm weights,
+// then y = RoPE(RMSNorm(x)) in fp32 and its error bound. Every lane of the warp calls it.
+template <int M, int NC>
+__device__ __forceinline__ void rotated_quads(const float* x, const float2* tab, int R,
+                                              const float* nw, float eps, int lane,
+                                              q4::Quad (&q)[NC]) {
+  using q4::Quad;
+  constexpr int D = 32 * M;
+  const int half = R / 2;
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    Quad& u = q[k];
+    const int d0 = 4 * (lane + 32 * k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u.own[e] = u.oth[e] = u.s[e] = 0.f;
+      u.c[e] = u.wo[e] = u.wt[e] = 1.f;
+    }
+    if (d0 >= D) continue;
+    const float4 t = *reinterpret_cast<const float4*>(x + d0);
+    u.own[0] = t.x; u.own[1] = t.y; u.own[2] = t.z; u.own[3] = t.w;
+    if (nw) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(nw + d0));
+      u.wo[0] = w.x; u.wo[1] = w.y; u.wo[2] = w.z; u.wo[3] = w.w;
+    }
+    if (half % 4 == 0) {                     // the quad lies within one half, so do its partners
+      if (d0 < R) {
+        const bool low = d0 < half;
+        const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
+        const float4 o = *reinterpret_cast<const float4*>(x + p);
+        u.oth[0] = o.x; u.oth[1] = o.y; u.oth[2] = o.z; u.oth[3] = o.w;
+        const float4* a = reinterpret_cast<const float4*>(tab + i);
+        const float4 a0 = __ldg(a), a1 = __ldg(a + 1);
+        u.c[0] = a0.x; u.c[1] = a0.z; u.c[2] = a1.x; u.c[3] = a1.z;
+        u.s[0] = a0.y; u.s[1] = a0.w; u.s[2] = a1.y; u.s[3] = a1.w;
+        if (low) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u.s[e] = -u.s[e];
+        }
+        if (nw) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(nw + p));
+          u.wt[0] = w.x; u.wt[1] = w.y; u.wt[2] = w.z; u.wt[3] = w.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = d0 + e;
+        if (d < R) {
+          const bool low = d < half;
+          const int i = low ? d : d - half, p = low ? d + half : i;
+          u.oth[e] = x[p];
+          const float2 a = __ldg(tab + i);
+          u.c[e] = a.x;
+          u.s[e] = low ? -a.y : a.y;
+          if (nw) u.wt[e] = __ldg(nw + p);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ss = fmaf(u.own[e], u.own[e], ss);
+  }
+  float inv = 1.f;
+  if (nw) inv = 1.0f / sqrtf(warp_sum(ss) / static_cast<float>(D) + eps);
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    Quad& u = q[k];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = nw ? u.own[e] * inv * u.wo[e] : u.own[e];
+      const float b = nw ? u.oth[e] * inv * u.wt[e] : u.oth[e];
+      const float ac = a * u.c[e], bs = b * u.s[e];
+      u.y[e] = fmaf(a, u.c[e], bs);
+      // fewer than sixteen roundings of 2^-24 of either term: at most nine in the row's
+      // sum of squares, halved by the root, and one each in the quotient, the root, its
+      // reciprocal, the two products, the rotation's product and its sum
+      u.err[e] = (fabsf(ac) + fabsf(bs)) * 0x1p-20f;
+    }
+  }
+}
+
+struct RowAt {
+  long bh;      // b * Hkv + hkv
+  int b, l;
+};
+__device__ __forceinline__ RowAt row_at(long row, long rows, int Hkv, int L) {
+  RowAt r;
+  if (rows < (1L << 31)) {
+    const uint32_t h = static_cast<uint32_t>(row) / static_cast<uint32_t>(L);
+    r.l = static_cast<int>(static_cast<uint32_t>(row) - h * static_cast<uint32_t>(L));
+    r.bh = h;
+    r.b = static_cast<int>(h / static_cast<uint32_t>(Hkv));
+  } else {
+    r.bh = row / L;
+    r.l = static_cast<int>(row - r.bh * L);
+    r.b = static_cast<int>(r.bh / Hkv);
+  }
+  return r;
+}
+
+// One row of k and v by one warp: key normed and rotated, both quantised and stored.
+template <int M, bool ROT>
+__device__ __forceinline__ void append_row(const AppendQ4Job& j, long row, long rows, int lane) {
+  using namespace q4;
+  constexpr int D = 32 * M, NC = quads_per_lane(M);
+  const RowAt at = row_at(row, rows, j.Hkv, j.L);
+  const int s0 = j.start[at.b], p0 = j.pos ? j.pos[at.b] : s0;
+  const bool first = at.l == 0 && at.bh % j.Hkv == 0 && lane == 0;     // one report per batch row
+  if (s0 < 0 || p0 < 0 || (ROT && static_cast<long>(p0) + j.L > j.max_positions)) {
+    if (first) report(j.status, ATTN_DEV_POSITION);
+    return;
+  }
+  if (j.window == 0 && static_cast<long>(s0) + j.L > j.capacity) {
+    if (first) report(j.status, ATTN_DEV_CAPACITY);
+    return;
+  }
+  const bool store = j.window == 0 || at.l >= j.L - j.window;
+  if (!store && !j.k_out) return;
+  const float* x = j.k + row * D;
+  Quad kq[NC], vq[NC];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int d0 = 4 * (lane + 32 * k);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (store && d0 < D) t = *reinterpret_cast<const float4*>(j.v + row * D + d0);
+    vq[k].own[0] = vq[k].y[0] = t.x; vq[k].own[1] = vq[k].y[1] = t.y;
+    vq[k].own[2] = vq[k].y[2] = t.z; vq[k].own[3] = vq[k].y[3] = t.w;
+  }
+  if (ROT) {
+    rotated_quads<M>(x, j.table + static_cast<long>(p0 + at.l) * (j.R / 2), j.R, j.norm_w,
+                     j.norm_eps, lane, kq);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int d0 = 4 * (lane + 32 * k);
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (d0 < D) t = *reinterpret_cast<const float4*>(x + d0);
+      kq[k].own[0] = kq[k].y[0] = t.x; kq[k].own[1] = kq[k].y[1] = t.y;
+      kq[k].own[2] = kq[k].y[2] = t.z; kq[k].own[3] = kq[k].y[3] = t.w;
+    }
+  }
+  if (j.k_out) {
+    __syncwarp();                            // in place: every lane has read its partners
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int d0 = 4 * (lane + 32 * k);
+      if (d0 < D)
+        *reinterpret_cast<float4*>(j.k_out + row * D + d0) =
+            make_float4(kq[k].y[0], kq[k].y[1], kq[k].y[2], kq[k].y[3]);
+    }
+  }
+  if (!store) return;
+  const long p = static_cast<long>(s0) + at.l;
+  const long slot = j.window > 0 ? p % j.window : p;
+  uint8_t* rec = j.cache + (at.bh * j.capacity + slot) * record_bytes(M);
+  Coded kc[NC], vc[NC];
+  quantise_row<NC, !ROT>(kq, ROT && j.norm_w != nullptr, D, j.norm_eps, kc);
+  quantise_row<NC, true>(vq, false, D, 0.f, vc);
+  store_part<M>(rec, 0, kc, lane);
+  store_part<M>(rec, 1, vc, lane);
+}
+
+template <int M, bool ROT>
+__global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j) {
+  if (gated_off(j.skip)) return;
+  const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
+  const long step = static_cast<long>(gridDim.x) * 8;
+  for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < rows; row += step)
+    append_row<M, ROT>(j, row, rows, threadIdx.x & 31);
+}
+
+// Records back to fp32: a warp per row, each lane four dims of key and value.
+template <int M>
+__global__ void __launch_bounds__(256) read_q4_kernel(ReadQ4Job j) {
+  if (gated_off(j.skip)) return;
+  constexpr int D = 32 * M, NC = quads_per_lane(M);
+  const int lane = threadIdx.x & 31;
+  const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
+  const long step = static_cast<long>(gridDim.x) * 8;
+  for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < rows; row += step) {
+    const RowAt at = row_at(row, rows, j.Hkv, j.L);
+    const int s0 = j.start[at.b];
+    const bool first = at.l == 0 && at.bh % j.Hkv == 0 && lane == 0;
+    if (s0 < 0) {
+      if (first) report(j.status, ATTN_DEV_POSITION);
+      continue;
+    }
+    if (j.window == 0 && static_cast<long>(s0) + j.L > j.capacity) {
+      if (first) report(j.status, ATTN_DEV_CAPACITY);
+      continue;
+    }
+    const long p = static_cast<long>(s0) + at.l;
+    const long slot = j.window > 0 ? p % j.window : p;
+    const uint8_t* rec = j.cache + (at.bh * j.capacity + slot) * q4::record_bytes(M);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int ch = lane + 32 * k;
+      if (ch >= 8 * M) continue;
+      const int g = ch >> 3, e = ch & 7;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int off = part ? 16 * M + 2 * (e * M + g) : 4 * ((e >> 1) * M + g) + 2 * (e & 1);
+        const uint32_t c = *reinterpret_cast<const uint16_t*>(rec + off);
+        const float s = q4::bf16_to_float(
+            *reinterpret_cast<const uint16_t*>(rec + (32 + 2 * part) * M + 2 * g));
+        float4 y;
+        y.x = static_cast<float>(static_cast<int>(c & 15u) - 8) * s;
+        y.y = static_cast<float>(static_cast<int>((c >> 4) & 15u) - 8) * s;
+        y.z = static_cast<float>(static_cast<int>((c >> 8) & 15u) - 8) * s;
+        y.w = static_cast<float>(static_cast<int>(c >> 12) - 8) * s;
+        *reinterpret_cast<float4*>((part ? j.v : j.k) + row * D + 4 * ch) = y;
+      }
+    }
+  }
+}
+
+// A step's first pass: a warp per row, the q rows (normed, rotated, fp32) first, then
+// the k and v rows.
+template <int M>
+__global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
+  if (gated_off(j.kv.skip)) return;
+  constexpr int D = 32 * M, NC = quads_per_lane(M);
+  const AppendQ4Job& a = j.kv;
+  const int lane = threadIdx.x & 31;
+  const long qrows = static_cast<long>(a.B) * j.H, kvrows = static_cast<long>(a.B) * a.Hkv;
+  const long step = static_cast<long>(gridDim.x) * 8;
+  for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < qrows + kvrows;
+       row += step) {
+    if (row >= qrows) {
+      append_row<M, true>(a, row - qrows, kvrows, lane);
+      continue;
+    }
+    const int b = static_cast<int>(row / j.H);
+    const int s0 = a.start[b], p0 = a.pos ? a.pos[b] : s0;
+    const bool ok = s0 >= 0 && p0 >= 0 && p0 < a.max_positions &&
+                    (a.window > 0 || s0 < a.capacity);
+    if (row % j.H == 0 && lane == 0) j.cache_len[b] = ok ? s0 + 1 : 0;
+    if (!ok) continue;                       // the row's key rows report it
+    q4::Quad q[NC];
+    rotated_quads<M>(j.q + row * D, a.table + static_cast<long>(p0) * (a.R / 2), a.R, j.q_norm_w,
+                     a.norm_eps, lane, q);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int d0 = 4 * (lane + 32 * k);
+      if (d0 < D)
+        *reinterpret_cast<float4*>(j.qrot + row * D + d0) =
+            make_float4(q[k].y[0], q[k].y[1], q[k].y[2], q[k].y[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- eviction
+
+// Order of weights as unsigned keys: larger weight, larger key; -0 and +0 alike; NaN
+// above everything (a slot whose weight is unknown is kept).
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(w == 0.f ? 0.f : w);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelItems = 4;                 // slots per thread and compaction tile
+constexpr int kSelKeys = 40960;              // keys held in shared memory at most (160 KB)
+
+// One block per (row, head): the need-th largest of the old slots' keys by three radix
+// passes (11, 11, 10 bits from the top), then one ordered pass that writes the kept
+// slots' numbers and weights. The keys are read once from memory where they fit in
+// shared memory, else again from L2 in each pass.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held) {
+  extern __shared__ uint32_t keys[];
+  __shared__ uint32_t hist[2048];
+  __shared__ uint32_t wsum[32];
+  __shared__ uint32_t found_bin, found_left;
+  if (gated_off(j.skip)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long bh = blockIdx.x;
+  const int b = static_cast<int>(bh / j.Hkv);
+  const int n = j.cache_len[b];
+  if (n < 0 || n > j.max_cache_len || n > j.capacity) {
+    if (tid == 0 && bh % j.Hkv == 0) report(j.status, ATTN_DEV_LENGTH);
+    return;
+  }
+  const float* w = j.weights + bh * j.capacity;
+  float* wo = j.weights_out + bh * j.capacity_out;
+  int32_t* index = j.index + bh * j.budget;
+  const int kept = min(n, j.budget);
+  if (tid == 0 && bh % j.Hkv == 0) j.len_out[b] = kept;
+  for (long i = kept + tid; i < j.capacity_out; i += kSelThreads) wo[i] = 0.f;
+  for (int i = kept + tid; i < j.budget; i += kSelThreads) index[i] = -1;
+  if (n <= j.budget) {
+    for (int i = tid; i < n; i += kSelThreads) {
+      index[i] = i;
+      wo[i] = w[i];
+    }
+    return;
+  }
+  const int old = n - j.recent;              // recent <= budget < n
+  const bool in_smem = old <= held;
+  if (in_smem) {
+    for (int i = tid; i < old; i += kSelThreads) keys[i] = weight_key(w[i]);
+    __syncthreads();
+  }
+  auto key_of = [&](int i) { return in_smem ? keys[i] : weight_key(w[i]); };
+
+  // Threshold: keys above T are kept, and the first `left` of those equal to it.
+  uint32_t T = 0, left = static_cast<uint32_t>(j.budget - j.recent);
+  const bool any_old = left > 0;
+  if (any_old) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const int bits = pass == 2 ? 10 : 11;
+      const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < old; i += kSelThreads) {
+        const uint32_t k = key_of(i);
+        if ((k & above) == (T & above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+      }
+      __syncthreads();
+      // bins from the top: thread t holds bins 2047 - 2 t and 2046 - 2 t
+      const uint32_t h0 = hist[2047 - 2 * tid], h1 = hist[2046 - 2 * tid];
+      uint32_t incl = h0 + h1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) wsum[warp] = incl;
+      __syncthreads();
+      uint32_t base = 0;
+      for (int i = 0; i < warp; ++i) base += wsum[i];
+      const uint32_t end = base + incl, begin = end - h0 - h1;
+      if (begin < left && end >= left) {      // exactly one thread
+        const bool second = begin + h0 < left;
+        found_bin = second ? 2046 - 2 * tid : 2047 - 2 * tid;
+        found_left = left - begin - (second ? h0 : 0);
+      }
+      __syncthreads();
+      T |= found_bin << shift;
+      left = found_left;
+    }
+  }
+  // Ordered pass. Kept before a slot: those above T, and at most `left` equal to it.
+  uint32_t base_up = 0, base_eq = 0;
+  for (int t0 = 0; t0 < n; t0 += kSelThreads * kSelItems) {
+    const int i0 = t0 + tid * kSelItems;
+    uint32_t up = 0, eq = 0;                  // bit e: slot i0 + e
+#pragma unroll
+    for (int e = 0; e < kSelItems; ++e) {
+      const int i = i0 + e;
+      if (i >= old) {
+        if (i < n) up |= 1u << e;
+      } else if (any_old) {
+        const uint32_t k = key_of(i);
+        if (k > T) up |= 1u << e;
+        if (k == T) eq |= 1u << e;
+      }
+    }
+    // counts of both in one word: at most 4096 each
+    const uint32_t own = __popc(up) | static_cast<uint32_t>(__popc(eq)) << 16;
+    uint32_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();                          // wsum of the tile before is read
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - own, total = 0;
+    for (int i = 0; i < 32; ++i) {
+      if (i < warp) before += wsum[i];
+      total += wsum[i];
+    }
+    uint32_t nup = base_up + (before & 0xffffu), neq = base_eq + (before >> 16);
+#pragma unroll
+    for (int e = 0; e < kSelItems; ++e) {
+      const bool is_up = up >> e & 1u, is_eq = eq >> e & 1u;
+      if (is_up || (is_eq && neq < left)) {
+        const uint32_t at = nup + min(neq, left);
+        index[at] = i0 + e;
+        wo[at] = w[i0 + e];
+      }
+      nup += is_up;
+      neq += is_eq;
+    }
+    base_up += total & 0xffffu;
+    base_eq += total >> 16;
+  }
+}
+
+// The kept records, 16 bytes a thread.
+template <int M>
+__global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j) {
+  if (gated_off(j.skip)) return;
+  constexpr int P = q4::record_bytes(M) / 16, U = 4;
+  const long bh = blockIdx.y;
+  const int b = static_cast<int>(bh / j.Hkv);
+  const int n = j.cache_len[b];
+  if (n < 0 || n > j.max_cache_len || n > j.capacity) return;
+  const long pieces = static_cast<long>(min(n, j.budget)) * P;
+  const uint4* src = reinterpret_cast<const uint4*>(j.cache) + bh * j.capacity * P;
+  uint4* dst = reinterpret_cast<uint4*>(j.cache_out) + bh * j.capacity_out * P;
+  const int32_t* index = j.index + bh * j.budget;
+  for (long i0 = static_cast<long>(blockIdx.x) * 256 * U + threadIdx.x; i0 < pieces;
+       i0 += static_cast<long>(gridDim.x) * 256 * U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long i = i0 + 256 * u;
+      if (i < pieces) {
+        const uint32_t r = static_cast<uint32_t>(i / P);
+        v[u] = src[static_cast<long>(index[r]) * P + (i - static_cast<long>(r) * P)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long i = i0 + 256 * u;
+      if (i < pieces) dst[i] = v[u];
+    }
+  }
+}
+
+unsigned row_blocks(long rows) {
+  const long blocks = (rows + 7) / 8;
+  return static_cast<unsigned>(blocks < 152L * 64 ? blocks : 152L * 64);
+}
+
+}  // namespace
+
+cudaError_t launch_append_q4(const AppendQ4Job& j, cudaStream_t stream) {
+  const unsigned grid = row_blocks(static_cast<long>(j.B) * j.Hkv * j.L);
+  return with_groups(j.D / 32, [&](auto g) {
+    constexpr int M = decltype(g)::value;
+    if (j.table)
+      append_q4_kernel<M, true><<<grid, 256, 0, stream>>>(j);
+    else
+      append_q4_kernel<M, false><<<grid, 256, 0, stream>>>(j);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream) {
+  const unsigned grid = row_blocks(static_cast<long>(j.B) * j.Hkv * j.L);
+  return with_groups(j.D / 32, [&](auto g) {
+    read_q4_kernel<decltype(g)::value><<<grid, 256, 0, stream>>>(j);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_prep_q4(const PrepQ4Job& j, cudaStream_t stream) {
+  const unsigned grid = row_blocks(static_cast<long>(j.kv.B) * (j.H + j.kv.Hkv));
+  return with_groups(j.kv.D / 32, [&](auto g) {
+    prep_q4_kernel<decltype(g)::value><<<grid, 256, 0, stream>>>(j);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream) {
+  static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
+  const cudaError_t e = allowed.get(
+      [] {
+        return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSelKeys * 4);
+      },
+      cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
+  if (e != cudaSuccess) return e;
+  const int held = j.max_cache_len < kSelKeys ? j.max_cache_len : kSelKeys;
+  const unsigned heads = static_cast<unsigned>(j.B) * j.Hkv;
+  evict_select_kernel<<<heads, kSelThreads, held * 4, stream>>>(j, held);
+  if (const cudaError_t l = cudaGetLastError(); l != cudaSuccess) return l;
+  return with_groups(j.D / 32, [&](auto g) {
+    constexpr int M = decltype(g)::value;
+    const long pieces = static_cast<long>(j.max_cache_len < j.budget ? j.max_cache_len : j.budget) *
+                        (q4::record_bytes(M) / 16);
+    if (pieces == 0) return cudaSuccess;
+    long blocks = (pieces + 1023) / 1024;
+    if (blocks > 65536) blocks = 65536;
+    // heads on the y axis: the host check keeps B * Hkv <= 65535
+    evict_move_kernel<M><<<dim3(static_cast<unsigned>(blocks), heads), 256, 0, stream>>>(j);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace gqa

@@ -13,7 +13,8 @@
  * Conventions shared by every call
  * --------------------------------
  * - All tensors are fp32, contiguous, row-major, in DEVICE memory owned by the
- *   caller, except the host buffers of gqa_attn_prefill_from_host. No call
+ *   caller, except the host buffers of gqa_attn_prefill_from_host and the 4-bit
+ *   records of the _q4 calls. No call
  *   allocates or frees device memory; the only device memory the library keeps
  *   is the fixed scratch array of gqa_attn_decode_static, and the only other
  *   state is the pair of copy streams per device of gqa_attn_prefill_from_host
@@ -507,6 +508,121 @@ int gqa_attn_decode_step(const float* q, const float* k, const float* v, float* 
  */
 int gqa_attn_decode_launches(int B, int H, int Hkv, int D, int32_t max_cache_len, int window,
                              int step_rope_dim);
+
+/*
+ * A KV cache held in 4 bits ("dew.nn.backbones.causal_transformer": a cache full or
+ * quantized; slots, rings and carried state as in "mojolearn.transformer",
+ * TransformerState). The cache is one caller-owned buffer of records,
+ *   cache [B, Hkv, capacity, kv_q4_record_bytes(D)] bytes, 16-byte aligned,
+ * D % 32 == 0, 32 <= D <= 256 (ATTN_ERR_SHAPE otherwise): one record per slot holds the
+ * key and the value of one position, 144 bytes at D = 128 where fp32 caches take 1024.
+ * Every 32 dims share a scale: s = max|x| / 7 rounded to bf16, codes
+ * c = x / s rounded to nearest (ties to even, both decided as in exact arithmetic on
+ * the normed and rotated values), |c| <= 7, and the slot stands for c * s, which fp32
+ * holds exactly. A group that is all zero stands for zeros; one that holds an inf or a
+ * NaN stands for NaNs. With m = D / 32 and little-endian words, a record is
+ *   bytes [0, 16 m)      key codes: word a * m + g (a < 4, g < m) holds dims 32 g + 8 a + i,
+ *                        i < 8, as c + 8 at bits 4 i .. 4 i + 3
+ *   bytes [16 m, 32 m)   value codes: 16-bit unit n * m + g (n < 8) holds dims
+ *                        32 g + 4 n + j, j < 4, as c + 8 at bits 4 j .. 4 j + 3
+ *   bytes [32 m, 34 m)   key scales, [34 m, 36 m) value scales, bf16; then zero padding.
+ * Slots behind the live ones are never interpreted. B * H <= 2^20 in every call below.
+ * The non-finite check (attn_set_check_finite) covers these calls: of records it reads
+ * the scales.
+ */
+size_t kv_q4_record_bytes(int D);   /* 36 m rounded up to 16; 0 for an invalid D */
+
+/*
+ * Cache append, as kv_cache_append, into 4-bit records: for each row b, kv head, token l
+ *   y = RoPE(RMSNorm(k[b,hkv,l,:]))   (norm if k_norm_w; both only if rp)
+ *   record at slot(start[b] + l)  <-  y and v[b,hkv,l,:], quantised as above
+ *   k_out[b,hkv,l,:] <- y in fp32     (k_out NULL: not wanted; k_out == k: in place)
+ * k and v [B, Hkv, L, D] are only read, unless k_out is k. slot(p) = p without a window
+ * (capacity > every p), p mod window with one (capacity == window; of a longer chunk
+ * only its last window positions are stored).
+ *   start    device int32 [B], slot positions; max_start bounds them (host)
+ *   pos      device int32 [B]: token l is rotated to position pos[b] + l, for rows whose
+ *            slots no longer count positions (after an eviction); max_pos bounds them.
+ *            NULL: start (max_pos is then not read)
+ * A row whose start or pos breaks a rule sets ATTN_DEV_POSITION or ATTN_DEV_CAPACITY
+ * and is skipped.
+ */
+int kv_cache_append_q4(const float* k, const float* v, float* k_out, int B, int Hkv, int L, int D,
+                       const int32_t* start, int32_t max_start, const int32_t* pos,
+                       int32_t max_pos, const attn_rope_params* rp, const float* table,
+                       const float* k_norm_w, float norm_eps, void* cache, int capacity,
+                       int window, int32_t* status, void* stream);
+
+/*
+ * The fp32 keys and values that records stand for: k, v [B, Hkv, L, D] <- slots of
+ * positions start[b] .. start[b] + L - 1 (mod window in a ring; L <= window then). With
+ * start 0 the result is a k_cache, v_cache of capacity L for gqa_attn_prefill_cached: a
+ * prompt chunk that continues a 4-bit cache.
+ */
+int kv_cache_read_q4(const void* cache, int capacity, int window, float* k, float* v, int B,
+                     int Hkv, int L, int D, const int32_t* start, int32_t max_start,
+                     int32_t* status, void* stream);
+
+/*
+ * gqa_attn_decode over a 4-bit cache: same q, out, cache_len, window, softcap and scale,
+ * with the keys and values the records stand for. Products and sums keep fp32's
+ * accuracy (the queries and softmax weights are split in two fp16 parts, the codes are
+ * exact). |q| must stay below 2^112.
+ *   weights   device fp32 [B, Hkv, capacity] or NULL. weights[b,hkv,n] += the sum over
+ *             the kv head's query heads of slot n's softmax weight, for every live slot;
+ *             others are left alone. What kv_cache_evict_q4 ranks slots by. Not with a
+ *             window (ATTN_ERR_SHAPE).
+ *   workspace gqa_attn_decode_q4_workspace_size bytes (never shrinking as max_cache_len
+ *             grows; 0, and NULL allowed, where one pass finishes)
+ * Results do not depend on timing. Calls that overlap on the GPU need workspaces of
+ * their own.
+ */
+size_t gqa_attn_decode_q4_workspace_size(int B, int H, int Hkv, int D, int max_cache_len,
+                                         int window, int with_weights);
+int gqa_attn_decode_q4(const float* q, const void* cache, const int32_t* cache_len,
+                       int32_t max_cache_len, float* out, float* weights, int B, int H, int Hkv,
+                       int D, int capacity, int window, float softcap, float scale,
+                       void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * gqa_attn_decode_step over a 4-bit cache: row b's new token, at slot position start[b]
+ * (= the slots already live) and rotary position pos[b] (NULL: start[b]), is appended as
+ * kv_cache_append_q4 does (without k_out), and out = its attention over
+ * cache_len[b] = start[b] + 1 slots as gqa_attn_decode_q4 computes it, q normed and rotated
+ * here. q [B, H, 1, D], k, v [B, Hkv, 1, D] raw, only read. rp is required.
+ *   workspace gqa_attn_decode_step_q4_workspace_size bytes
+ * A row that breaks a rule sets ATTN_DEV_POSITION (ATTN_DEV_CAPACITY) and
+ * ATTN_DEV_LENGTH and is skipped.
+ */
+size_t gqa_attn_decode_step_q4_workspace_size(int B, int H, int Hkv, int D, int32_t max_start,
+                                              int window, int with_weights);
+int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, float* out, int B,
+                            int H, int Hkv, int D, const int32_t* start, int32_t max_start,
+                            const int32_t* pos, int32_t max_pos, const attn_rope_params* rp,
+                            const float* table, const float* q_norm_w, const float* k_norm_w,
+                            float norm_eps, void* cache, float* weights, int capacity, int window,
+                            float softcap, float scale, void* workspace, size_t workspace_bytes,
+                            int32_t* status, void* stream);
+
+/*
+ * Eviction by accumulated attention weight, into another cache: of the n = cache_len[b]
+ * live slots of every (b, kv head), the last `recent` are kept and, of the others, those
+ * of greatest weight until there are `budget` (a tie goes to the lower slot; a NaN counts
+ * as greatest). Kept slots move to 0, 1, ... in slot order, with their weights:
+ *   cache_out   [B, Hkv, capacity_out] records, slots below len_out[b] written
+ *   weights_out [B, Hkv, capacity_out] written whole: kept weights, then zeros
+ *   index       device int32 [B, Hkv, budget]: the kept slots' numbers, then -1
+ *   len_out     device int32 [B]: min(n, budget)
+ * n <= budget keeps every slot. Attention does not mind the move (keys are stored
+ * rotated); later tokens go to slot start = len_out with pos still counting positions.
+ * 0 <= recent <= budget <= capacity_out; cache_len[b] in [0, max_cache_len] (else
+ * ATTN_DEV_LENGTH, and the row is skipped). The outputs must not overlap the inputs;
+ * no ring. B * Hkv <= 65535.
+ */
+int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* cache_len,
+                      int32_t max_cache_len, int budget, int recent, void* cache_out,
+                      float* weights_out, int32_t* index, int32_t* len_out, int B, int Hkv, int D,
+                      int capacity, int capacity_out, int32_t* status, void* stream);
 
 /*
  * gqa_attn_decode without a caller workspace, for callers that cannot
