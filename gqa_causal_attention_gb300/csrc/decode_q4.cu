@@ -15,12 +15,13 @@
 // operand is unpacked in registers and used once: staging it in shared memory for
 // tcgen05 would cost more shared-memory traffic than the copy of the codes itself.)
 //
-// Why no shift or conversion per code: a nibble u = c + 8 masked out of its 16-bit
-// half is the fp16 subnormal u * 2^-24, or 16 u * 2^-24 for the odd nibbles, whose
-// factor 16 goes into q (1 / 16) and into the output dims. Keys leave the offset 8 in:
-// sum q (u - 8) = sum q u - 8 sum q, and the last term is the accumulator's start
-// value. Values subtract it (one packed subtraction): their sum runs over thousands
-// of keys, and 8 sum p, kept apart, would swamp it.
+// A pair of codes becomes a packed fp16 pair in two instructions: a nibble u = c + 8
+// masked out of its 16-bit half and put under the exponent of 1024 is 1024 + u, or
+// 1024 + 16 u for the odd nibbles, and a packed subtraction leaves c or 16 c; the 16
+// goes into q (1 / 16) and into the output dims. (The masked nibble alone is the fp16
+// subnormal u * 2^-24 and would do for a key without the subtraction, but the tensor
+// core aligns its products by the operands' exponent fields: ten bits of the sum were
+// lost, and outputs were off by 2.5e-6 instead of 3e-7.)
 //
 // Each warp owns whole 32-key tiles and a ring of bulk copies of its own; nothing in
 // the loop waits for another warp. Products accumulate over one tile only (two
@@ -72,6 +73,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   const float2 f = __half22float2(h);
   hi = as_u32(h);
   lo = as_u32(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+// The nibbles at bits 4 ODD of w's two halves as packed fp16 c (ODD = 0) or 16 c (1).
+template <int ODD>
+__device__ __forceinline__ uint32_t codes(uint32_t w) {
+  const uint32_t u = (w & (ODD ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+  return as_u32(__hsub2(as_half2(u), as_half2(ODD ? 0x64806480u : 0x64086408u)));
 }
 
 // N 32-bit words from shared memory, aligned to their largest power-of-two divisor.
@@ -134,7 +142,6 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   constexpr int D = 32 * M, REC = q4::record_bytes(M), TILE_BYTES = kTile * REC, VW = (M + 1) / 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][kStages];
-  __shared__ float start_of[M][kHeads];      // -8 * 2^-24 sum of q over a group
   __shared__ float q_factor[kHeads];
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
   __shared__ int abort_flag;
@@ -194,37 +201,28 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
     top = __reduce_max_sync(0xffffffffu, top);
     int ex = static_cast<int>(top >> 23) - 127 - 12;          // 2^12 <= |x| 2^-ex < 2^13
-    ex = max(-120, min(ex, 100));
+    ex = max(-120, ex);
     if (top >= 0x7f800000u) ex = 0;                           // inf or NaN: its head becomes NaN
     const float f = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-    float sum = 0.f;
     uint32_t hi[4], lo[4];                   // pairs (2 st + odd): dims e and e + 4
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float w = e & 1 ? f * 0.0625f : f;
       split2(x[e] * w, x[e + 4] * w, hi[e], lo[e]);
-      const float2 fh = __half22float2(as_half2(hi[e])), fl = __half22float2(as_half2(lo[e]));
-      sum += ((fh.x + fl.x) + (fh.y + fl.y)) * (e & 1 ? 16.f : 1.f);
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     if (there) {
 #pragma unroll
       for (int st = 0; st < 2; ++st)         // thread (r = h, c = a) of step (g, st)
         *reinterpret_cast<uint4*>(frag + ((2 * g + st) * 32 + 4 * h + a) * 4) =
             make_uint4(hi[2 * st], lo[2 * st], hi[2 * st + 1], lo[2 * st + 1]);
-      if (a == 0) start_of[g][h] = sum * -0x1p-21f;           // -8 * 2^-24
     }
-    // scores come out as (sum) * 2^(24 + ex); times the softmax scale, in log2 units
+    // scores come out times 2^-ex; undo it, times the softmax scale, in log2 units
     if (lane == 0)
-      q_factor[h] = __uint_as_float(static_cast<uint32_t>(127 + 24 + ex) << 23) * j.scale *
+      q_factor[h] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * j.scale *
                     (j.softcap > 0.f ? 1.f : kLog2e);
   }
   __syncthreads();
 
-  float c_start[M];
-#pragma unroll
-  for (int g = 0; g < M; ++g) c_start[g] = start_of[g][r];
   const float qf = q_factor[r];
   const uint4* afrag = reinterpret_cast<const uint4*>(frag) + lane;
   float* score_row = nullptr;
@@ -269,10 +267,10 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
         const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          float d[4] = {c_start[g], c_start[g], 0.f, 0.f};
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
           const uint32_t w = kw[t][g], w8 = w >> 8;
-          mma(d, a0, w & 0x000f000fu, w & 0x00f000f0u);
-          mma(d, a1, w8 & 0x000f000fu, w8 & 0x00f000f0u);
+          mma(d, a0, codes<0>(w), codes<1>(w));
+          mma(d, a1, codes<0>(w8), codes<1>(w8));
           s[2 * t] = fmaf(unit_scale(sc[2 * t][g / 2], g & 1), d[0] + d[2], s[2 * t]);
           s[2 * t + 1] = fmaf(unit_scale(sc[2 * t + 1][g / 2], g & 1), d[1] + d[3], s[2 * t + 1]);
         }
@@ -384,13 +382,13 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float d[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t mask = q & 1 ? 0x00f000f0u : 0x000f000fu;
-        const __half2 off = as_half2(q & 1 ? 0x00800080u : 0x00080008u);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t b0 = (q & 2 ? v[k][0] >> 8 : v[k][0]) & mask;
-          const uint32_t b1 = (q & 2 ? v[k][1] >> 8 : v[k][1]) & mask;
-          mma(d, a[k], as_u32(__hsub2(as_half2(b0), off)), as_u32(__hsub2(as_half2(b1), off)));
+          const uint32_t w0 = q & 2 ? v[k][0] >> 8 : v[k][0], w1 = q & 2 ? v[k][1] >> 8 : v[k][1];
+          if (q & 1)
+            mma(d, a[k], codes<1>(w0), codes<1>(w1));
+          else
+            mma(d, a[k], codes<0>(w0), codes<0>(w1));
         }
         o[g][q][0] += d[0] + d[2];
         o[g][q][1] += d[1] + d[3];
@@ -421,7 +419,7 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   float m_all = sm_m[0][r];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) m_all = fmaxf(m_all, sm_m[w][r]);
-  const float mine_f = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_all) * 0x1p24f;
+  const float mine_f = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_all);
   float* ex = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int g = 0; g < M; ++g)
