@@ -11,9 +11,14 @@
 // read, twice what the CUDA cores could keep up with; unpacking comes on top. The
 // codes are small integers, exact in fp16, so m16n8k16 products of fp16 pairs are
 // exact, and q and p, split into a high and a low fp16 part (22 bits), keep fp32's
-// accuracy. The 16 rows of the A operand are the 8 heads' high and low parts. (The
-// operand is unpacked in registers and used once: staging it in shared memory for
-// tcgen05 would cost more shared-memory traffic than the copy of the codes itself.)
+// accuracy. (The codes are unpacked in registers and used once: staging them in shared
+// memory for tcgen05 would cost more shared-memory traffic than the copy itself.)
+//
+// Keys (then value dims) are the 16 rows of the A operand; the 8 columns of B are the
+// high and low parts of 4 query heads, so up to 4 heads need one product and up to 8
+// two, with the unpacking shared. A thread holds both parts of a head's score side by
+// side: their sum needs no exchange, and one 8 x 8 transpose (movmatrix) turns 8 keys'
+// packed weights into the next product's B operand.
 //
 // A pair of codes becomes a packed fp16 pair in two instructions: a nibble u = c + 8
 // masked out of its 16-bit half and put under the exponent of 1024 is 1024 + u, or
@@ -45,8 +50,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 32;                    // keys per tile
 constexpr int kWarps = 4;
-constexpr int kStages = 3;
-constexpr int kHeads = 8;                    // query heads per block
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -55,13 +58,20 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // D += A B, A 16 x 16 (row), B 16 x 8 (column), fp16 in, fp32 out.
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit elements (lane: row lane / 4, columns 2 (lane % 4), + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -80,6 +90,14 @@ template <int ODD>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
   const uint32_t u = (w & (ODD ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
   return as_u32(__hsub2(as_half2(u), as_half2(ODD ? 0x64806480u : 0x64086408u)));
+}
+
+// x >= 0 below 2^16 as (high, low) packed fp16: the top eleven bits and the rest, which
+// is exact in fp32. (Below 2^-14 the high part keeps fewer bits: an error of 2^-25, of
+// weights whose largest is near 2^14.)
+__device__ __forceinline__ uint32_t split1(float x) {
+  const float h = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+  return as_u32(__floats2half2_rn(h, x - h));
 }
 
 // N 32-bit words from shared memory, aligned to their largest power-of-two divisor.
@@ -122,8 +140,11 @@ __device__ __forceinline__ float unit_scale(uint32_t w, int odd) {     // bf16 h
   return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
 }
 
-constexpr size_t split_smem(int M) {
-  return static_cast<size_t>(kWarps) * kStages * kTile * q4::record_bytes(M) + 1024 * M;
+__host__ __device__ constexpr int stages(int M) { return M <= 4 ? 3 : 2; }
+
+// Rings of all warps, then the queries' B fragments.
+constexpr size_t split_smem(int M, int NT) {
+  return static_cast<size_t>(kWarps) * stages(M) * kTile * q4::record_bytes(M) + 512 * M * NT;
 }
 
 // Live slots of row b (0: the row is invalid).
@@ -136,10 +157,11 @@ __device__ __forceinline__ int live_slots(const DecodeQ4Job& j, int b, bool lead
   return j.window > 0 ? min(n, j.window) : n;
 }
 
-// One block: up to 8 query heads of one kv head over the slots [split chunk, + chunk).
-template <int M, bool WEIGHTS>
+// One block: up to 4 NT query heads of one kv head over the slots [split chunk, + chunk).
+template <int M, int NT, bool WEIGHTS>
 __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(DecodeQ4Job j) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), TILE_BYTES = kTile * REC, VW = (M + 1) / 2;
+  constexpr int kHeads = 4 * NT, kStages = stages(M);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ float q_factor[kHeads];
@@ -179,10 +201,12 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   }
   if (threadIdx.x == 0) abort_flag = 0;
 
-  // Queries as A fragments: a warp per head, lane g * 4 + a holds dims 32 g + 8 a .. + 7
+  // Queries as B fragments: a warp per head, lane g * 4 + a holds dims 32 g + 8 a .. + 7
   // (the dims of key word (a, g)). Scaled by a power of two so that the head's largest
-  // element lies in [2^12, 2^13): both fp16 parts are then normal over 22 bits.
-  uint32_t* frag = reinterpret_cast<uint32_t*>(smem + kWarps * kStages * TILE_BYTES);
+  // element lies in [2^12, 2^13): both fp16 parts are then normal over 22 bits. Product
+  // step (g, st) takes from thread (n, a) the pairs of dims 2 st, 2 st + 4 and 2 st + 1,
+  // 2 st + 5 of the word; column n = 2 h is head h's high part, 2 h + 1 its low part.
+  uint2* frag = reinterpret_cast<uint2*>(smem + kWarps * kStages * TILE_BYTES);
   for (int h = warp; h < kHeads; h += kWarps) {
     float x[8];
 #pragma unroll
@@ -200,11 +224,10 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
     top = __reduce_max_sync(0xffffffffu, top);
-    int ex = static_cast<int>(top >> 23) - 127 - 12;          // 2^12 <= |x| 2^-ex < 2^13
-    ex = max(-120, ex);
+    int ex = max(-120, static_cast<int>(top >> 23) - 127 - 12);   // 2^12 <= |x| 2^-ex < 2^13
     if (top >= 0x7f800000u) ex = 0;                           // inf or NaN: its head becomes NaN
     const float f = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-    uint32_t hi[4], lo[4];                   // pairs (2 st + odd): dims e and e + 4
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float w = e & 1 ? f * 0.0625f : f;
@@ -212,9 +235,11 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
     }
     if (there) {
 #pragma unroll
-      for (int st = 0; st < 2; ++st)         // thread (r = h, c = a) of step (g, st)
-        *reinterpret_cast<uint4*>(frag + ((2 * g + st) * 32 + 4 * h + a) * 4) =
-            make_uint4(hi[2 * st], lo[2 * st], hi[2 * st + 1], lo[2 * st + 1]);
+      for (int st = 0; st < 2; ++st) {
+        uint2* to = frag + (((h >> 2) * M + g) * 2 + st) * 32 + 8 * (h & 3) + a;
+        to[0] = make_uint2(hi[2 * st], hi[2 * st + 1]);
+        to[4] = make_uint2(lo[2 * st], lo[2 * st + 1]);
+      }
     }
     // scores come out times 2^-ex; undo it, times the softmax scale, in log2 units
     if (lane == 0)
@@ -223,19 +248,30 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   }
   __syncthreads();
 
-  const float qf = q_factor[r];
-  const uint4* afrag = reinterpret_cast<const uint4*>(frag) + lane;
-  float* score_row = nullptr;
-  if (WEIGHTS && g0 + r < G)
-    score_row = j.scores + (static_cast<long>(b) * j.H + hkv * G + g0 + r) * j.pitch;
+  const uint2* bfrag = frag + lane;
+  float qf[NT];
+  float* score_row[NT];                      // this thread's heads: c and, of 8, c + 4
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int h = 4 * t + c;
+    qf[t] = q_factor[h];
+    score_row[t] = WEIGHTS && g0 + h < G
+                       ? j.scores + (static_cast<long>(b) * j.H + hkv * G + g0 + h) * j.pitch
+                       : nullptr;
+  }
 
-  float m_run = -INFINITY, l_run = 0.f;
+  float m_run[NT], l_run[NT];
   int e_run = -60 - 14;                      // exponent of the reference beside the maximum
-  float o[M][4][2];
+  float o[NT][M][4];                         // head 4 t + c, dims 32 g + 4 r + (0 .. 3)
 #pragma unroll
-  for (int g = 0; g < M; ++g)
+  for (int t = 0; t < NT; ++t) {
+    m_run[t] = -INFINITY;
+    l_run[t] = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) o[g][q][0] = o[g][q][1] = 0.f;
+    for (int g = 0; g < M; ++g)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[t][g][q] = 0.f;
+  }
 
   int i = 0;
   for (; i < mine; ++i) {
@@ -245,49 +281,71 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
     const uint8_t* tile = ring + st * TILE_BYTES;
     const int kb = first_key(i), valid = min(kTile, k1 - kb);
 
-    // Scores. Thread (r, c) gets head r's of keys 8 t + 2 c and 8 t + 2 c + 1, t = 0 .. 3.
-    // Their scales, M of the key and M of the value, come in one load where the registers
-    // allow (M <= 4; odd M, whose halves share a word), else the value's later.
+    // Scores of keys r, r + 8, r + 16, r + 24 (x = 0 .. 3). Their scales, M of the key and
+    // M of the value, come in one load where the registers allow (M <= 4; odd M, whose
+    // halves share a word), else the value's later.
     constexpr bool kBoth = M <= 4 || M % 2 == 1;
     constexpr int SW = kBoth ? M : M / 2;
-    float s[8];
-    uint32_t sc[8][SW];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      s[x] = 0.f;
-      load_words<SW>(tile + (8 * (x >> 1) + 2 * c + (x & 1)) * REC + 32 * M, sc[x]);
-    }
+    float s[NT][4];
+    uint32_t sc[4][SW];
     {
       uint32_t kw[4][M];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) load_words<M>(tile + (8 * t + r) * REC + 4 * M * c, kw[t]);
+      for (int x = 0; x < 4; ++x) {
+        load_words<M>(tile + (8 * x + r) * REC + 4 * M * c, kw[x]);
+        load_words<SW>(tile + (8 * x + r) * REC + 32 * M, sc[x]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t][x] = 0.f;
+      }
 #pragma unroll
       for (int g = 0; g < M; ++g) {
-        const uint4 f0 = afrag[64 * g], f1 = afrag[64 * g + 32];
-        const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
+        uint2 f[NT][2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t w = kw[t][g], w8 = w >> 8;
-          mma(d, a0, codes<0>(w), codes<1>(w));
-          mma(d, a1, codes<0>(w8), codes<1>(w8));
-          s[2 * t] = fmaf(unit_scale(sc[2 * t][g / 2], g & 1), d[0] + d[2], s[2 * t]);
-          s[2 * t + 1] = fmaf(unit_scale(sc[2 * t + 1][g / 2], g & 1), d[1] + d[3], s[2 * t + 1]);
+        for (int t = 0; t < NT; ++t) {
+          f[t][0] = bfrag[((t * M + g) * 2) * 32];
+          f[t][1] = bfrag[((t * M + g) * 2 + 1) * 32];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {        // keys 16 k .. 16 k + 15
+          float d[NT][4];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[t][e] = 0.f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t w0 = q ? kw[2 * k][g] >> 8 : kw[2 * k][g];
+            const uint32_t w1 = q ? kw[2 * k + 1][g] >> 8 : kw[2 * k + 1][g];
+            const uint32_t a0 = codes<0>(w0), a1 = codes<0>(w1), a2 = codes<1>(w0), a3 = codes<1>(w1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma(d[t], a0, a1, a2, a3, f[t][q].x, f[t][q].y);
+          }
+          const float s0 = unit_scale(sc[2 * k][g / 2], g & 1);
+          const float s1 = unit_scale(sc[2 * k + 1][g / 2], g & 1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            s[t][2 * k] = fmaf(s0, d[t][0] + d[t][1], s[t][2 * k]);
+            s[t][2 * k + 1] = fmaf(s1, d[t][2] + d[t][3], s[t][2 * k + 1]);
+          }
         }
       }
     }
 #pragma unroll
-    for (int x = 0; x < 8; ++x) s[x] *= qf;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[t][x] *= qf[t];
     if (j.softcap > 0.f) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s[x] = tanhf(s[x] / j.softcap) * (j.softcap * kLog2e);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[t][x] = tanhf(s[t][x] / j.softcap) * (j.softcap * kLog2e);
     }
     // The value scales, apart from the keys'.
-    uint32_t vs[8][VW];
+    uint32_t vs[4][VW];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+    for (int x = 0; x < 4; ++x) {
       if constexpr (!kBoth) {
-        load_words<VW>(tile + (8 * (x >> 1) + 2 * c + (x & 1)) * REC + 34 * M, vs[x]);
+        load_words<VW>(tile + (8 * x + r) * REC + 34 * M, vs[x]);
       } else {
 #pragma unroll
         for (int w = 0; w < VW; ++w)
@@ -298,38 +356,35 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
     }
     if (valid < kTile) {                     // slots past the live ones: whatever was there
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        if (8 * (x >> 1) + 2 * c + (x & 1) >= valid) {
-          s[x] = -INFINITY;
+      for (int x = 0; x < 4; ++x) {
+        if (8 * x + r >= valid) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t][x] = -INFINITY;
 #pragma unroll
           for (int w = 0; w < VW; ++w) vs[x][w] = 0;
         }
       }
     }
-    if (WEIGHTS && score_row) {
+    if (WEIGHTS) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int k = 8 * t + 2 * c;
-        if (k < valid) score_row[kb + k] = s[2 * t];
-        if (k + 1 < valid) score_row[kb + k + 1] = s[2 * t + 1];
-      }
+      for (int t = 0; t < NT; ++t)
+        if (score_row[t]) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (8 * x + r < valid) score_row[t][kb + 8 * x + r] = s[t][x];
+        }
     }
-    // Reference: running maximum and running exponent of the value scales.
-    float mx = s[0];
+    // Reference: each head's running maximum and the running exponent of the value scales.
     uint32_t top = 0;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      mx = fmaxf(mx, s[x]);
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
       for (int w = 0; w < VW; ++w) top = __vmaxu2(top, vs[x][w]);
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
     if (top >= 0x7f80u) {                    // a NaN group: the others keep their range
       top = 0;
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           const uint32_t lo = vs[x][w] & 0xffffu, hi = vs[x][w] >> 16;
@@ -337,61 +392,79 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
         }
       top = __reduce_max_sync(0xffffffffu, top);
     }
-    const float m_new = fmaxf(m_run, mx);
     const int e_new = max(e_run, static_cast<int>(top >> 7) - 127 - 14);
-    if (__any_sync(0xffffffffu, m_new > m_run) || e_new != e_run) {
-      const float corr = m_new == -INFINITY
-                             ? 1.f
-                             : ex2((m_run - m_new) + static_cast<float>(e_run - e_new));
-      l_run *= corr;
+    float m_new[NT];
+    bool moved = e_new != e_run;
 #pragma unroll
-      for (int g = 0; g < M; ++g)
+    for (int t = 0; t < NT; ++t) {
+      float mx = fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      m_new[t] = fmaxf(m_run[t], mx);
+      moved |= m_new[t] > m_run[t];
+    }
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          o[g][q][0] *= corr;
-          o[g][q][1] *= corr;
-        }
-      m_run = m_new;
+      for (int t = 0; t < NT; ++t) {
+        const float corr = m_new[t] == -INFINITY
+                               ? 1.f
+                               : ex2((m_run[t] - m_new[t]) + static_cast<float>(e_run - e_new));
+        l_run[t] *= corr;
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[t][g][q] *= corr;
+        m_run[t] = m_new[t];
+      }
       e_run = e_new;
     }
-    const float ref = (m_run == -INFINITY ? 0.f : m_run) + static_cast<float>(e_run);
-    float p[8];
+    float p[NT][4];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      p[x] = ex2(s[x] - ref);
-      l_run += p[x];
+    for (int t = 0; t < NT; ++t) {
+      const float ref = (m_run[t] == -INFINITY ? 0.f : m_run[t]) + static_cast<float>(e_run);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        p[t][x] = ex2(s[t][x] - ref);
+        l_run[t] += p[t][x];
+      }
     }
 
-    // P V. Keys of the two 16-key steps: 16 k + 2 c, + 1, + 8, + 9.
+    // P V, 16 dims x 16 keys a product: thread (r, c) unpacks dims 32 g + 4 r + (0 .. 3) of
+    // keys 16 k + 2 c, + 1, + 8, + 9.
     uint32_t vw[8][VW];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
       load_units<M>(tile + (8 * (x >> 1) + 2 * c + (x & 1)) * REC + 16 * M + 2 * M * r, vw[x]);
 #pragma unroll
     for (int g = 0; g < M; ++g) {
-      uint32_t a[2][4], v[2][2];
+      uint32_t w[4], pb[NT][4];              // per 8 keys: value codes of key pairs, weights
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int x = 0; x < 4; ++x) {
+        w[x] = __byte_perm(vw[2 * x][g / 2], vw[2 * x + 1][g / 2], g & 1 ? 0x7632 : 0x5410);
+        const float sv = unit_scale(vs[x][g / 2], g & 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int x = 4 * k + 2 * h;
-          split2(p[x] * unit_scale(vs[x][g / 2], g & 1),
-                 p[x + 1] * unit_scale(vs[x + 1][g / 2], g & 1), a[k][2 * h], a[k][2 * h + 1]);
-          v[k][h] = __byte_perm(vw[x][g / 2], vw[x + 1][g / 2], g & 1 ? 0x7632 : 0x5410);
-        }
+        for (int t = 0; t < NT; ++t) pb[t][x] = transpose8(split1(p[t][x] * sv));
+      }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int q = 0; q < 2; ++q) {          // dims 4 r + 2 q (rows 0 .. 7) and + 2 q + 1
+        float d[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[t][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t w0 = q & 2 ? v[k][0] >> 8 : v[k][0], w1 = q & 2 ? v[k][1] >> 8 : v[k][1];
-          if (q & 1)
-            mma(d, a[k], codes<1>(w0), codes<1>(w1));
-          else
-            mma(d, a[k], codes<0>(w0), codes<0>(w1));
+          const uint32_t w0 = q ? w[2 * k] >> 8 : w[2 * k], w1 = q ? w[2 * k + 1] >> 8 : w[2 * k + 1];
+          const uint32_t a0 = codes<0>(w0), a1 = codes<1>(w0), a2 = codes<0>(w1), a3 = codes<1>(w1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma(d[t], a0, a1, a2, a3, pb[t][2 * k], pb[t][2 * k + 1]);
         }
-        o[g][q][0] += d[0] + d[2];
-        o[g][q][1] += d[1] + d[3];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          o[t][g][2 * q] += d[t][0] + d[t][1];
+          o[t][g][2 * q + 1] += d[t][2] + d[t][3];
+        }
       }
     }
     __syncwarp();                            // every lane is done with the stage
@@ -408,26 +481,30 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   }
 
   // The warps' sums, brought to one reference, meet in the (now idle) rings.
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-  const float m_ref = m_run + static_cast<float>(e_run);
-  if (c == 0) {
-    sm_m[warp][r] = m_ref;
-    sm_l[warp][r] = l_run;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l_run[t] += __shfl_xor_sync(0xffffffffu, l_run[t], off);
+    m_run[t] += static_cast<float>(e_run);
+    if (r == 0) {
+      sm_m[warp][4 * t + c] = m_run[t];
+      sm_l[warp][4 * t + c] = l_run[t];
+    }
   }
   __syncthreads();
-  float m_all = sm_m[0][r];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) m_all = fmaxf(m_all, sm_m[w][r]);
-  const float mine_f = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_all);
   float* ex = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int g = 0; g < M; ++g)
+  for (int t = 0; t < NT; ++t) {
+    const int h = 4 * t + c;
+    float m_all = sm_m[0][h];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      *reinterpret_cast<float4*>(ex + r * D + 32 * g + 8 * c + 4 * u) =
-          make_float4(o[g][0][u] * mine_f, o[g][1][u] * (mine_f * 0.0625f), o[g][2][u] * mine_f,
-                      o[g][3][u] * (mine_f * 0.0625f));
+    for (int w = 1; w < kWarps; ++w) m_all = fmaxf(m_all, sm_m[w][h]);
+    const float f = m_run[t] == -INFINITY ? 0.f : ex2(m_run[t] - m_all), fo = f * 0.0625f;
+#pragma unroll
+    for (int g = 0; g < M; ++g)
+      *reinterpret_cast<float4*>(ex + h * D + 32 * g + 4 * r) =
+          make_float4(o[t][g][0] * f, o[t][g][1] * fo, o[t][g][2] * f, o[t][g][3] * fo);
+  }
   __syncthreads();
   if (abort_flag) return;
   const bool single = nlive <= j.chunk;
@@ -523,24 +600,36 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   if (n < nlive) j.weights[bh * j.capacity + n] += acc;
 }
 
-template <int M, bool W>
+template <int M, int NT, bool W>
 cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   const cudaError_t e = allowed.get(
       [] {
-        return cudaFuncSetAttribute(decode_q4_kernel<M, W>,
+        return cudaFuncSetAttribute(decode_q4_kernel<M, NT, W>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(split_smem(M)));
+                                    static_cast<int>(split_smem(M, NT)));
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  decode_q4_kernel<M, W><<<grid, 32 * kWarps, split_smem(M), stream>>>(j);
+  decode_q4_kernel<M, NT, W><<<grid, 32 * kWarps, split_smem(M, NT), stream>>>(j);
   return cudaGetLastError();
 }
 
+// Query heads per block: 4 or 8.
+int head_tiles(int H, int Hkv) { return H / Hkv <= 4 ? 1 : 2; }
+long units_of(int B, int H, int Hkv) {
+  const int per = 4 * head_tiles(H, Hkv);
+  return static_cast<long>(B) * Hkv * ((H / Hkv + per - 1) / per);
+}
+
 template <int M>
-cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, cudaStream_t stream) {
-  return j.weights ? launch_split<M, true>(j, grid, stream) : launch_split<M, false>(j, grid, stream);
+cudaError_t launch_split(const DecodeQ4Job& j, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(units_of(j.B, j.H, j.Hkv)) * j.nsplit;
+  if (head_tiles(j.H, j.Hkv) == 1)
+    return j.weights ? launch_split<M, 1, true>(j, grid, stream)
+                     : launch_split<M, 1, false>(j, grid, stream);
+  return j.weights ? launch_split<M, 2, true>(j, grid, stream)
+                   : launch_split<M, 2, false>(j, grid, stream);
 }
 
 int eff_len(int max_cache_len, int window) {
@@ -550,7 +639,7 @@ int eff_len(int max_cache_len, int window) {
 // The most splits of any length up to this one: it does not shrink as the length grows.
 int split_bound(int B, int H, int Hkv, int max_cache_len, int window) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
-  const long units = static_cast<long>(B) * Hkv * ((H / Hkv + kHeads - 1) / kHeads);
+  const long units = units_of(B, H, Hkv);
   constexpr int resident = 152 * 3;          // blocks on the GPU at once
   const long want = units >= resident ? (4 * resident + units - 1) / units
                                       : (units < 1 ? 1 : resident / units);
@@ -604,19 +693,16 @@ void decode_q4_workspace(DecodeQ4Job* j, void* workspace) {
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream) {
-  const int G = j.H / j.Hkv;
-  const unsigned units = static_cast<unsigned>(j.B) * j.Hkv * ((G + kHeads - 1) / kHeads);
-  const unsigned grid = units * j.nsplit;
   cudaError_t e;
   switch (j.D / 32) {
-    case 1: e = launch_split<1>(j, grid, stream); break;
-    case 2: e = launch_split<2>(j, grid, stream); break;
-    case 3: e = launch_split<3>(j, grid, stream); break;
-    case 4: e = launch_split<4>(j, grid, stream); break;
-    case 5: e = launch_split<5>(j, grid, stream); break;
-    case 6: e = launch_split<6>(j, grid, stream); break;
-    case 7: e = launch_split<7>(j, grid, stream); break;
-    default: e = launch_split<8>(j, grid, stream); break;
+    case 1: e = launch_split<1>(j, stream); break;
+    case 2: e = launch_split<2>(j, stream); break;
+    case 3: e = launch_split<3>(j, stream); break;
+    case 4: e = launch_split<4>(j, stream); break;
+    case 5: e = launch_split<5>(j, stream); break;
+    case 6: e = launch_split<6>(j, stream); break;
+    case 7: e = launch_split<7>(j, stream); break;
+    default: e = launch_split<8>(j, stream); break;
   }
   if (e != cudaSuccess || (j.nsplit == 1 && !j.weights)) return e;
   const unsigned rows = j.nsplit > 1 ? static_cast<unsigned>(j.B) * j.H : 0;
