@@ -88,7 +88,10 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // The nibbles at bits 4 ODD of w's two halves as packed fp16 c (ODD = 0) or 16 c (1).
 template <int ODD>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
-  const uint32_t u = (w & (ODD ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+  uint32_t u;                                // (w & mask) | 0x6400 in one instruction
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+      : "=r"(u)
+      : "r"(w), "n"(ODD ? 0x00f000f0 : 0x000f000f), "r"(0x64006400u));
   return as_u32(__hsub2(as_half2(u), as_half2(ODD ? 0x64806480u : 0x64086408u)));
 }
 
