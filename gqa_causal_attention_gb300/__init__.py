@@ -13,6 +13,8 @@ PyTorch provides device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import threading
 
 import torch
@@ -86,6 +88,7 @@ class RopeParams(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_ext = None
 
 
 def library_path() -> str:
@@ -807,56 +810,30 @@ def kv_q4_record_bytes(D: int) -> int:
     return int(load().kv_q4_record_bytes(int(D)))
 
 
-def _on_device(fn: str, dtype, *tensors) -> None:
-    """Each tensor (None: left out) has this dtype, is contiguous and lies on the current
-    device, on whose stream the call is enqueued."""
-    dev = -1
-    for t in tensors:
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{fn}: expected {dtype}, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: expected CUDA tensors")
-        if dev < 0:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{fn}: tensors must lie on the current CUDA device")
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: tensors must be contiguous")
+def _native():
+    """The extension that checks and passes the tensors of the calls below, bound to the
+    library's entry points."""
+    global _ext
+    lib = load()
+    with _lock:
+        if _ext is None:
+            path = _build.build_ext()
+            loader = importlib.machinery.ExtensionFileLoader("_gqa_binding", path)
+            ext = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_gqa_binding", path, loader=loader))
+            loader.exec_module(ext)
+            ext.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+                "kv_cache_append_q4", "kv_cache_read_q4", "gqa_attn_decode_q4",
+                "gqa_attn_decode_step_q4", "kv_cache_evict_q4", "kv_q4_record_bytes")))
+            _ext = ext
+        return _ext
 
 
-def _q4_cache(fn: str, cache, B: int, Hkv: int, D: int) -> int:
-    """Checks a 4-bit cache's shape and returns its capacity."""
-    if cache.dim() != 4 or tuple(cache.shape[:2]) != (B, Hkv) or \
-            cache.shape[3] != kv_q4_record_bytes(D):
-        raise ValueError(f"{fn}: cache must be [B, Hkv, capacity, kv_q4_record_bytes(D)], got "
-                         f"{tuple(cache.shape)}")
-    return cache.shape[2]
-
-
-def _q4_rope(fn: str, D: int, params, table, *norms) -> None:
-    """A table of attn_rope_table_bytes for the parameters, norm weights of D."""
-    if params is not None and table is not None and \
-            table.numel() * 4 < attn_rope_table_bytes(params, D):
-        raise ValueError(f"{fn}: table is smaller than attn_rope_table_bytes")
-    for w in norms:
-        if w is not None and w.numel() != D:
-            raise ValueError(f"{fn}: norm weights must have head_dim elements")
-
-
-def _q4_rows(fn: str, B: int, *rows) -> None:
-    for t in rows:
-        if t is not None and t.numel() != B:
-            raise ValueError(f"{fn}: start, pos and lengths hold one value per batch row")
-
-
-def _q4_workspace(size: int, workspace, like):
-    if workspace is None:
-        return torch.empty(max(16, size), dtype=torch.uint8, device=like.device)
-    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    return workspace
+def _q4_workspace(size: int, like, stream):
+    ws = torch.empty(max(16, size), dtype=torch.uint8, device=like.device)
+    if stream is not None:       # taken on the current stream, used on this one
+        ws.record_stream(stream)
+    return ws
 
 
 def kv_cache_append_q4(k, v, cache, start, max_start: int, params: RopeParams = None, table=None,
@@ -866,38 +843,18 @@ def kv_cache_append_q4(k, v, cache, start, max_start: int, params: RopeParams = 
     records (cache: uint8 [B, Hkv, capacity, kv_q4_record_bytes(D)]) of slots start[b] + l.
     k_out: fp32 tensor for the rotated keys (k itself: in place), or None. pos: rotary
     positions where they are not the slots (bounded by max_pos), or None."""
-    fn = "kv_cache_append_q4"
-    _on_device(fn, torch.float32, k, v, table, k_norm_w, k_out)
-    _on_device(fn, torch.int32, start, pos, status)
-    _on_device(fn, torch.uint8, cache)
-    B, Hkv, L, D = k.shape
-    cap = _q4_cache(fn, cache, B, Hkv, D)
-    if v.shape != k.shape or (k_out is not None and k_out.shape != k.shape):
-        raise ValueError(f"{fn}: inconsistent shapes")
-    _q4_rows(fn, B, start, pos)
-    _q4_rope(fn, D, params, table, k_norm_w)
-    rc = load().kv_cache_append_q4(_ptr(k), _ptr(v), _ptr(k_out), B, Hkv, L, D, _ptr(start),
-                                   int(max_start), _ptr(pos), int(max_pos), _rp(params),
-                                   _ptr(table), _ptr(k_norm_w), float(norm_eps), _ptr(cache), cap,
-                                   int(window), _ptr(status), _stream(stream))
-    _check(fn, rc)
+    rc = (_ext or _native()).append(k, v, cache, start, max_start, params, table, k_norm_w,
+                                    norm_eps, k_out, pos, max_pos, window, status, stream)
+    if rc:
+        raise AttnError("kv_cache_append_q4", rc)
 
 
 def kv_cache_read_q4(cache, k, v, start, max_start: int, window: int = 0, status=None,
                      stream=None) -> None:
     """k, v [B, Hkv, L, D] (fp32) = what the 4-bit records of slots start[b] + l stand for."""
-    fn = "kv_cache_read_q4"
-    _on_device(fn, torch.float32, k, v)
-    _on_device(fn, torch.int32, start, status)
-    _on_device(fn, torch.uint8, cache)
-    B, Hkv, L, D = k.shape
-    cap = _q4_cache(fn, cache, B, Hkv, D)
-    if v.shape != k.shape:
-        raise ValueError(f"{fn}: inconsistent shapes")
-    _q4_rows(fn, B, start)
-    rc = load().kv_cache_read_q4(_ptr(cache), cap, int(window), _ptr(k), _ptr(v), B, Hkv, L, D,
-                                 _ptr(start), int(max_start), _ptr(status), _stream(stream))
-    _check(fn, rc)
+    rc = (_ext or _native()).read(cache, k, v, start, max_start, window, status, stream)
+    if rc:
+        raise AttnError("kv_cache_read_q4", rc)
 
 
 def gqa_attn_decode_q4_workspace_size(B: int, H: int, Hkv: int, D: int, max_cache_len: int,
@@ -913,29 +870,14 @@ def gqa_attn_decode_q4(q, cache, cache_len, max_cache_len: int, out, weights=Non
     or None): each live slot's softmax weights, summed over the kv head's query heads, are
     added to it. workspace: gqa_attn_decode_q4_workspace_size bytes, or None to take one from
     torch's caching allocator for this call."""
-    fn = "gqa_attn_decode_q4"
-    _on_device(fn, torch.float32, q, out, weights)
-    _on_device(fn, torch.int32, cache_len, status)
-    _on_device(fn, torch.uint8, cache)
-    B, H, one, D = q.shape
-    Hkv = cache.shape[1]
-    cap = _q4_cache(fn, cache, B, Hkv, D)
-    if one != 1 or out.shape != q.shape or \
-            (weights is not None and tuple(weights.shape) != (B, Hkv, cap)):
-        raise ValueError(f"{fn}: inconsistent shapes")
-    _q4_rows(fn, B, cache_len)
     if workspace is None:
-        size = gqa_attn_decode_q4_workspace_size(B, H, Hkv, D, max_cache_len, window,
-                                                 weights is not None)
-        workspace = _q4_workspace(size, None, q)
-    else:
-        workspace = _q4_workspace(0, workspace, q)
-    rc = load().gqa_attn_decode_q4(_ptr(q), _ptr(cache), _ptr(cache_len), int(max_cache_len),
-                                   _ptr(out), _ptr(weights), B, H, Hkv, D, cap, int(window),
-                                   float(softcap), float(scale), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(status),
-                                   _stream(stream))
-    _check(fn, rc)
+        B, H, _, D = q.shape
+        workspace = _q4_workspace(gqa_attn_decode_q4_workspace_size(
+            B, H, cache.shape[1], D, max_cache_len, window, weights is not None), q, stream)
+    rc = (_ext or _native()).decode(q, cache, cache_len, max_cache_len, out, weights, window,
+                                    softcap, scale, workspace, status, stream)
+    if rc:
+        raise AttnError("gqa_attn_decode_q4", rc)
 
 
 def gqa_attn_decode_step_q4_workspace_size(B: int, H: int, Hkv: int, D: int, max_start: int,
@@ -953,34 +895,15 @@ def gqa_attn_decode_step_q4(q, k, v, out, cache, start, max_start: int, params: 
     [B, Hkv, 1, D], read only) enters slot start[b], rotated to position pos[b] (None:
     start[b]), and out = its attention over the start[b] + 1 live slots. weights as for
     gqa_attn_decode_q4; workspace: gqa_attn_decode_step_q4_workspace_size bytes, or None."""
-    fn = "gqa_attn_decode_step_q4"
-    _on_device(fn, torch.float32, q, k, v, out, table, q_norm_w, k_norm_w, weights)
-    _on_device(fn, torch.int32, start, pos, status)
-    _on_device(fn, torch.uint8, cache)
-    B, H, one, D = q.shape
-    Hkv = cache.shape[1]
-    cap = _q4_cache(fn, cache, B, Hkv, D)
-    if one != 1 or out.shape != q.shape or tuple(k.shape) != (B, Hkv, 1, D) or \
-            v.shape != k.shape or \
-            (weights is not None and tuple(weights.shape) != (B, Hkv, cap)):
-        raise ValueError(f"{fn}: inconsistent shapes")
-    _q4_rows(fn, B, start, pos)
-    _q4_rope(fn, D, params, table, q_norm_w, k_norm_w)
     if workspace is None:
-        size = gqa_attn_decode_step_q4_workspace_size(B, H, Hkv, D, max_start, window,
-                                                      weights is not None)
-        workspace = _q4_workspace(size, None, q)
-    else:
-        workspace = _q4_workspace(0, workspace, q)
-    rc = load().gqa_attn_decode_step_q4(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, H, Hkv, D,
-                                        _ptr(start), int(max_start), _ptr(pos), int(max_pos),
-                                        _rp(params), _ptr(table), _ptr(q_norm_w), _ptr(k_norm_w),
-                                        float(norm_eps), _ptr(cache), _ptr(weights), cap,
-                                        int(window), float(softcap), float(scale),
-                                        _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(),
-                                        _ptr(status), _stream(stream))
-    _check(fn, rc)
+        B, H, _, D = q.shape
+        workspace = _q4_workspace(gqa_attn_decode_step_q4_workspace_size(
+            B, H, cache.shape[1], D, max_start, window, weights is not None), q, stream)
+    rc = (_ext or _native()).step(q, k, v, out, cache, start, max_start, params, table, q_norm_w,
+                                  k_norm_w, norm_eps, pos, max_pos, weights, window, softcap,
+                                  scale, workspace, status, stream)
+    if rc:
+        raise AttnError("gqa_attn_decode_step_q4", rc)
 
 
 def kv_cache_evict_q4(cache, weights, cache_len, max_cache_len: int, budget: int, recent: int,
@@ -989,23 +912,7 @@ def kv_cache_evict_q4(cache, weights, cache_len, max_cache_len: int, budget: int
     up to `budget`, compacted in slot order into cache_out (another 4-bit cache) and
     weights_out [B, Hkv, capacity_out]; index [B, Hkv, budget] gets the kept slots' numbers
     (then -1), len_out [B] the new lengths (both int32)."""
-    fn = "kv_cache_evict_q4"
-    _on_device(fn, torch.float32, weights, weights_out)
-    _on_device(fn, torch.int32, cache_len, index, len_out, status)
-    _on_device(fn, torch.uint8, cache, cache_out)
-    if cache.dim() != 4 or cache_out.dim() != 4:
-        raise ValueError(f"{fn}: caches must have 4 dims")
-    B, Hkv, cap, rec = cache.shape
-    cap_out = cache_out.shape[2]
-    D = next((d for d in range(32, 257, 32) if kv_q4_record_bytes(d) == rec), 0)
-    if D == 0 or tuple(cache_out.shape) != (B, Hkv, cap_out, rec) or \
-            tuple(weights.shape) != (B, Hkv, cap) or \
-            tuple(weights_out.shape) != (B, Hkv, cap_out) or \
-            tuple(index.shape) != (B, Hkv, int(budget)):
-        raise ValueError(f"{fn}: inconsistent shapes")
-    _q4_rows(fn, B, cache_len, len_out)
-    rc = load().kv_cache_evict_q4(_ptr(cache), _ptr(weights), _ptr(cache_len), int(max_cache_len),
-                                  int(budget), int(recent), _ptr(cache_out), _ptr(weights_out),
-                                  _ptr(index), _ptr(len_out), B, Hkv, D, cap, cap_out,
-                                  _ptr(status), _stream(stream))
-    _check(fn, rc)
+    rc = (_ext or _native()).evict(cache, weights, cache_len, max_cache_len, budget, recent,
+                                   cache_out, weights_out, index, len_out, status, stream)
+    if rc:
+        raise AttnError("kv_cache_evict_q4", rc)

@@ -1,9 +1,12 @@
-"""Compile libgqa_attn.so in-tree with nvcc for sm_103a.
+"""Compile libgqa_attn.so in-tree with nvcc for sm_103a, and the binding's extension.
 
 The sources under ``csrc/`` are compiled in parallel, one object each, and
 linked into ``_build/libgqa_attn.so`` next to this file. The CUDA runtime is
 linked statically, so the library loads on a machine without a GPU driver
 (the driver API is reached at run time through cudaGetDriverEntryPoint).
+
+``csrc/binding.cpp`` becomes ``_build/_gqa_binding.so``, a Python extension that only
+checks torch tensors and calls into the library (it links against torch, not against it).
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgqa_attn.so")
+EXT_SRC = os.path.join(CSRC, "binding.cpp")
+EXT = os.path.join(BUILD, "_gqa_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
@@ -45,9 +51,42 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def ext_up_to_date() -> bool:
+    if not os.path.exists(EXT):
+        return False
+    t = os.path.getmtime(EXT)
+    return all(os.path.getmtime(p) <= t for p in [EXT_SRC] + glob.glob(
+        os.path.join(INCLUDE, "*.h")))
+
+
+def build_ext(force: bool = False) -> str:
+    """Build the binding's extension if it is older than its source; return its path."""
+    if not force and ext_up_to_date():
+        return EXT
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = EXT + f".tmp{os.getpid()}"
+    lib = os.path.join(root, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", EXT_SRC, "-o", tmp,
+           "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Build the library if any source is newer than it; return its path."""
+    """Build the library and the extension if any source is newer; return the library's path."""
     if not force and up_to_date():
+        build_ext()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
@@ -62,7 +101,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return r.stdout + r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+        ext = ex.submit(build_ext, force)
         logs = list(ex.map(compile_one, zip(srcs, objs)))
+        ext.result()
     if verbose:
         for s, lg in zip(srcs, logs):
             if lg.strip():

@@ -366,6 +366,7 @@ struct AppendQ4Job {
   int max_positions, capacity, window;
   int32_t* status;
   const int32_t* skip = nullptr;
+  int l0 = 0;               // first token of a head that is looked at (set by the launcher)
 };
 cudaError_t launch_append_q4(const AppendQ4Job& j, cudaStream_t stream);
 

@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_q4.cuh"
+#include "tc_ptx.cuh"
 
 namespace gqa {
 
@@ -36,85 +37,104 @@ cudaError_t with_groups(int m, F f) {
   }
 }
 
-// A lane's quads of a raw row with their rotary partners, angles and norm weights,
-// then y = RoPE(RMSNorm(x)) in fp32 and its error bound. Every lane of the warp calls it.
+// A lane's quads of the raw row x through RMSNorm (nw) and RoPE (tab: the row's angles), in
+// fp32, and a bound of their error. Every lane of the warp calls it.
 template <int M, int NC>
-__device__ __forceinline__ void rotated_quads(const float* x, const float2* tab, int R,
-                                              const float* nw, float eps, int lane,
-                                              q4::Quad (&q)[NC]) {
-  using q4::Quad;
+__device__ __forceinline__ void rotate_quads(const float* x, const float2* tab, int R,
+                                             const float* nw, float eps, int lane,
+                                             float (&y)[NC][4], float (&err)[NC]) {
   constexpr int D = 32 * M;
   const int half = R / 2;
-  float ss = 0.f;
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    Quad& u = q[k];
-    const int d0 = 4 * (lane + 32 * k);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      u.own[e] = u.oth[e] = u.s[e] = 0.f;
-      u.c[e] = u.wo[e] = u.wt[e] = 1.f;
-    }
-    if (d0 >= D) continue;
-    const float4 t = *reinterpret_cast<const float4*>(x + d0);
-    u.own[0] = t.x; u.own[1] = t.y; u.own[2] = t.z; u.own[3] = t.w;
-    if (nw) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(nw + d0));
-      u.wo[0] = w.x; u.wo[1] = w.y; u.wo[2] = w.z; u.wo[3] = w.w;
-    }
-    if (half % 4 == 0) {                     // the quad lies within one half, so do its partners
-      if (d0 < R) {
-        const bool low = d0 < half;
-        const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
-        const float4 o = *reinterpret_cast<const float4*>(x + p);
-        u.oth[0] = o.x; u.oth[1] = o.y; u.oth[2] = o.z; u.oth[3] = o.w;
-        const float4* a = reinterpret_cast<const float4*>(tab + i);
-        const float4 a0 = __ldg(a), a1 = __ldg(a + 1);
-        u.c[0] = a0.x; u.c[1] = a0.z; u.c[2] = a1.x; u.c[3] = a1.z;
-        u.s[0] = a0.y; u.s[1] = a0.w; u.s[2] = a1.y; u.s[3] = a1.w;
-        if (low) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) u.s[e] = -u.s[e];
-        }
-        if (nw) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(nw + p));
-          u.wt[0] = w.x; u.wt[1] = w.y; u.wt[2] = w.z; u.wt[3] = w.w;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = d0 + e;
-        if (d < R) {
-          const bool low = d < half;
-          const int i = low ? d : d - half, p = low ? d + half : i;
-          u.oth[e] = x[p];
-          const float2 a = __ldg(tab + i);
-          u.c[e] = a.x;
-          u.s[e] = low ? -a.y : a.y;
-          if (nw) u.wt[e] = __ldg(nw + p);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ss = fmaf(u.own[e], u.own[e], ss);
-  }
   float inv = 1.f;
-  if (nw) inv = 1.0f / sqrtf(warp_sum(ss) / static_cast<float>(D) + eps);
+  if (nw) {
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int d0 = 4 * (lane + 32 * k);
+      if (d0 < D) {
+        const float4 t = *reinterpret_cast<const float4*>(x + d0);
+        ss = fmaf(t.x, t.x, fmaf(t.y, t.y, fmaf(t.z, t.z, fmaf(t.w, t.w, ss))));
+      }
+    }
+    inv = 1.0f / sqrtf(warp_sum(ss) / static_cast<float>(D) + eps);
+  }
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    Quad& u = q[k];
+    const int d0 = 4 * (lane + 32 * k);
+    // y = a c + b s, b the rotary partner; the error is below sixteen roundings of 2^-24 of
+    // either term: at most nine in the sum of squares, halved by the root, and one each in
+    // the quotient, the root, its reciprocal, the two products, the rotation's product and
+    // its sum
+    float a[4], b[4], c[4], s[4], mag = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float a = nw ? u.own[e] * inv * u.wo[e] : u.own[e];
-      const float b = nw ? u.oth[e] * inv * u.wt[e] : u.oth[e];
-      const float ac = a * u.c[e], bs = b * u.s[e];
-      u.y[e] = fmaf(a, u.c[e], bs);
-      // fewer than sixteen roundings of 2^-24 of either term: at most nine in the row's
-      // sum of squares, halved by the root, and one each in the quotient, the root, its
-      // reciprocal, the two products, the rotation's product and its sum
-      u.err[e] = (fabsf(ac) + fabsf(bs)) * 0x1p-20f;
+      a[e] = b[e] = s[e] = 0.f;
+      c[e] = 1.f;
     }
+    if (d0 < D) {
+      const float4 t = *reinterpret_cast<const float4*>(x + d0);
+      a[0] = t.x; a[1] = t.y; a[2] = t.z; a[3] = t.w;
+      if (nw) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(nw + d0));
+        a[0] = a[0] * inv * w.x; a[1] = a[1] * inv * w.y;
+        a[2] = a[2] * inv * w.z; a[3] = a[3] * inv * w.w;
+      }
+      if (half % 4 == 0) {                   // the quad lies within one half, so do its partners
+        if (d0 < R) {
+          const bool low = d0 < half;
+          const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
+          const float4 o = *reinterpret_cast<const float4*>(x + p);
+          b[0] = o.x; b[1] = o.y; b[2] = o.z; b[3] = o.w;
+          const float4* ang = reinterpret_cast<const float4*>(tab + i);
+          const float4 a0 = __ldg(ang), a1 = __ldg(ang + 1);
+          c[0] = a0.x; c[1] = a0.z; c[2] = a1.x; c[3] = a1.z;
+          s[0] = a0.y; s[1] = a0.w; s[2] = a1.y; s[3] = a1.w;
+          if (nw) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(nw + p));
+            b[0] = b[0] * inv * w.x; b[1] = b[1] * inv * w.y;
+            b[2] = b[2] * inv * w.z; b[3] = b[3] * inv * w.w;
+          }
+          if (low) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = -s[e];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = d0 + e;
+          if (d < R) {
+            const bool low = d < half;
+            const int i = low ? d : d - half, p = low ? d + half : i;
+            b[e] = nw ? x[p] * inv * __ldg(nw + p) : x[p];
+            const float2 t2 = __ldg(tab + i);
+            c[e] = t2.x;
+            s[e] = low ? -t2.y : t2.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float bs = b[e] * s[e];
+      y[k][e] = fmaf(a[e], c[e], bs);
+      mag = fmaxf(mag, fabsf(a[e] * c[e]) + fabsf(bs));
+    }
+    err[k] = mag * 0x1p-20f;
+  }
+}
+
+// A lane's quads of a row as they are.
+template <int M, int NC>
+__device__ __forceinline__ void plain_quads(const float* x, int lane, float (&y)[NC][4],
+                                            float (&err)[NC]) {
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int d0 = 4 * (lane + 32 * k);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d0 < 32 * M) t = *reinterpret_cast<const float4*>(x + d0);
+    y[k][0] = t.x; y[k][1] = t.y; y[k][2] = t.z; y[k][3] = t.w;
+    err[k] = 0.f;
   }
 }
 
@@ -137,75 +157,126 @@ __device__ __forceinline__ RowAt row_at(long row, long rows, int Hkv, int L) {
   return r;
 }
 
-// One row of k and v by one warp: key normed and rotated, both quantised and stored.
+// Where row (bh, l) of an append goes: its record, or nullptr where it is not stored; ok:
+// whether the row's positions are valid (reported once per batch row if not).
+struct Target {
+  bool ok;
+  uint8_t* rec;
+  long angle;               // row of the angle table
+};
 template <int M, bool ROT>
-__device__ __forceinline__ void append_row(const AppendQ4Job& j, long row, long rows, int lane) {
-  using namespace q4;
-  constexpr int D = 32 * M, NC = quads_per_lane(M);
-  const RowAt at = row_at(row, rows, j.Hkv, j.L);
+__device__ __forceinline__ Target append_target(const AppendQ4Job& j, const RowAt& at, int lane) {
   const int s0 = j.start[at.b], p0 = j.pos ? j.pos[at.b] : s0;
-  const bool first = at.l == 0 && at.bh % j.Hkv == 0 && lane == 0;     // one report per batch row
+  const bool first = at.l == j.l0 && at.bh % j.Hkv == 0 && lane == 0;
+  Target t{false, nullptr, static_cast<long>(p0) + at.l};
   if (s0 < 0 || p0 < 0 || (ROT && static_cast<long>(p0) + j.L > j.max_positions)) {
     if (first) report(j.status, ATTN_DEV_POSITION);
-    return;
+    return t;
   }
   if (j.window == 0 && static_cast<long>(s0) + j.L > j.capacity) {
     if (first) report(j.status, ATTN_DEV_CAPACITY);
-    return;
+    return t;
   }
-  const bool store = j.window == 0 || at.l >= j.L - j.window;
-  if (!store && !j.k_out) return;
-  const float* x = j.k + row * D;
-  Quad kq[NC], vq[NC];
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int d0 = 4 * (lane + 32 * k);
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (store && d0 < D) t = *reinterpret_cast<const float4*>(j.v + row * D + d0);
-    vq[k].own[0] = vq[k].y[0] = t.x; vq[k].own[1] = vq[k].y[1] = t.y;
-    vq[k].own[2] = vq[k].y[2] = t.z; vq[k].own[3] = vq[k].y[3] = t.w;
+  t.ok = true;
+  if (j.window == 0 || at.l >= j.L - j.window) {
+    const long p = static_cast<long>(s0) + at.l;
+    t.rec = j.cache + (at.bh * j.capacity + (j.window > 0 ? p % j.window : p)) *
+                          q4::record_bytes(M);
   }
-  if (ROT) {
-    rotated_quads<M>(x, j.table + static_cast<long>(p0 + at.l) * (j.R / 2), j.R, j.norm_w,
-                     j.norm_eps, lane, kq);
-  } else {
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int d0 = 4 * (lane + 32 * k);
-      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (d0 < D) t = *reinterpret_cast<const float4*>(x + d0);
-      kq[k].own[0] = kq[k].y[0] = t.x; kq[k].own[1] = kq[k].y[1] = t.y;
-      kq[k].own[2] = kq[k].y[2] = t.z; kq[k].own[3] = kq[k].y[3] = t.w;
-    }
+  return t;
+}
+
+// One row by one warp: x, v the raw rows (any memory); the record goes to rec (any memory)
+// unless it is nullptr, the rotated key to k_out unless that is.
+template <int M, bool ROT>
+__device__ __forceinline__ void append_row(const AppendQ4Job& j, const float* x, const float* v,
+                                           long angle, uint8_t* rec, float* k_out, int lane) {
+  using namespace q4;
+  constexpr int D = 32 * M, NC = quads_per_lane(M);
+  const float2* tab = ROT ? j.table + angle * (j.R / 2) : nullptr;
+  const float* nw = ROT ? j.norm_w : nullptr;
+  float y[NC][4], err[NC];
+  Coded q[NC];
+  if (ROT)
+    rotate_quads<M>(x, tab, j.R, nw, j.norm_eps, lane, y, err);
+  else
+    plain_quads<M>(x, lane, y, err);
+  if (rec) {
+    if (!quantise_fast(y, err, q)) quantise_exact<NC>(x, tab, j.R, nw, j.norm_eps, D, lane, q);
+    store_part<M>(rec, 0, q, lane);
   }
-  if (j.k_out) {
+  if (k_out) {
     __syncwarp();                            // in place: every lane has read its partners
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int d0 = 4 * (lane + 32 * k);
       if (d0 < D)
-        *reinterpret_cast<float4*>(j.k_out + row * D + d0) =
-            make_float4(kq[k].y[0], kq[k].y[1], kq[k].y[2], kq[k].y[3]);
+        *reinterpret_cast<float4*>(k_out + d0) = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
     }
   }
-  if (!store) return;
-  const long p = static_cast<long>(s0) + at.l;
-  const long slot = j.window > 0 ? p % j.window : p;
-  uint8_t* rec = j.cache + (at.bh * j.capacity + slot) * record_bytes(M);
-  Coded kc[NC], vc[NC];
-  quantise_row<NC, !ROT>(kq, ROT && j.norm_w != nullptr, D, j.norm_eps, kc);
-  quantise_row<NC, true>(vq, false, D, 0.f, vc);
-  store_part<M>(rec, 0, kc, lane);
-  store_part<M>(rec, 1, vc, lane);
+  if (rec) {
+    plain_quads<M>(v, lane, y, err);
+    if (!quantise_fast(y, err, q)) quantise_exact<NC>(v, nullptr, 0, nullptr, 0.f, D, lane, q);
+    store_part<M>(rec, 1, q, lane);
+  }
 }
 
+// Rows of k and v through shared memory: a block bulk-copies `tr` consecutive rows of each
+// (rows are contiguous whatever L is), its warps quantise them row by row into records in
+// shared memory, and the records leave in 16-byte pieces. The bytes in flight are then
+// bounded by shared memory, not by registers: a warp per row straight from memory, with the
+// values, partners and angles in registers, ran at 1.9 TB/s.
+// Rows come in segments of seg_rows (the whole tensor, or, of a chunk longer than its ring,
+// the last rows of each head), seg_tiles blocks each.
 template <int M, bool ROT>
-__global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j) {
+__global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j, int tr, long seg_rows,
+                                                        int seg_tiles) {
+  constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full;
+  __shared__ int abort_flag;
+  __shared__ uint8_t* to[32];
   if (gated_off(j.skip)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long seg = blockIdx.x / seg_tiles;
+  const long in_seg = static_cast<long>(blockIdx.x % seg_tiles) * tr;
+  const int n = static_cast<int>(min(static_cast<long>(tr), seg_rows - in_seg));
+  // a segment's first row: heads are j.L rows apart, of which the last seg_rows count
+  const long row0 = seg * j.L + j.l0 + in_seg;
+  float* xk = reinterpret_cast<float*>(smem);
+  float* xv = xk + tr * D;
+  uint8_t* recs = smem + 2 * tr * D * 4;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    tc::mbar_init(&full, 1);
+    tc::fence_mbar_init();
+    const uint32_t bytes = static_cast<uint32_t>(n) * D * 4;
+    tc::mbar_arrive_expect_tx(&full, 2 * bytes);
+    tc::bulk_load(xk, j.k + row0 * D, bytes, &full);
+    tc::bulk_load(xv, j.v + row0 * D, bytes, &full);
+  }
+  __syncthreads();
   const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
-  const long step = static_cast<long>(gridDim.x) * 8;
-  for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < rows; row += step)
-    append_row<M, ROT>(j, row, rows, threadIdx.x & 31);
+  if (!tc::mbar_wait(&full, 0, &abort_flag)) abort_flag = 1;
+  __syncthreads();
+  if (abort_flag) {                          // the copies never came
+    if (threadIdx.x == 0) report(j.status, ATTN_DEV_TIMEOUT);
+    return;
+  }
+  for (int i = warp; i < n; i += 8) {
+    const RowAt at = row_at(row0 + i, rows, j.Hkv, j.L);
+    const Target t = append_target<M, ROT>(j, at, lane);
+    if (lane == 0) to[i] = t.rec;
+    if (t.ok && (t.rec || j.k_out))
+      append_row<M, ROT>(j, xk + i * D, xv + i * D, t.angle, t.rec ? recs + i * REC : nullptr,
+                         j.k_out ? j.k_out + (row0 + i) * D : nullptr, lane);
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < n * P; p += 256) {
+    const int i = p / P;
+    if (to[i])
+      reinterpret_cast<uint4*>(to[i])[p - i * P] = reinterpret_cast<const uint4*>(recs)[p];
+  }
 }
 
 // Records back to fp32: a warp per row, each lane four dims of key and value.
@@ -266,7 +337,10 @@ __global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
   for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < qrows + kvrows;
        row += step) {
     if (row >= qrows) {
-      append_row<M, true>(a, row - qrows, kvrows, lane);
+      const RowAt at = row_at(row - qrows, kvrows, a.Hkv, 1);
+      const Target t = append_target<M, true>(a, at, lane);
+      if (t.ok)
+        append_row<M, true>(a, a.k + at.bh * D, a.v + at.bh * D, t.angle, t.rec, nullptr, lane);
       continue;
     }
     const int b = static_cast<int>(row / j.H);
@@ -275,15 +349,15 @@ __global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
                     (a.window > 0 || s0 < a.capacity);
     if (row % j.H == 0 && lane == 0) j.cache_len[b] = ok ? s0 + 1 : 0;
     if (!ok) continue;                       // the row's key rows report it
-    q4::Quad q[NC];
-    rotated_quads<M>(j.q + row * D, a.table + static_cast<long>(p0) * (a.R / 2), a.R, j.q_norm_w,
-                     a.norm_eps, lane, q);
+    float y[NC][4], err[NC];
+    rotate_quads<M>(j.q + row * D, a.table + static_cast<long>(p0) * (a.R / 2), a.R, j.q_norm_w,
+                    a.norm_eps, lane, y, err);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int d0 = 4 * (lane + 32 * k);
       if (d0 < D)
         *reinterpret_cast<float4*>(j.qrot + row * D + d0) =
-            make_float4(q[k].y[0], q[k].y[1], q[k].y[2], q[k].y[3]);
+            make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
     }
   }
 }
@@ -469,15 +543,44 @@ unsigned row_blocks(long rows) {
 
 }  // namespace
 
-cudaError_t launch_append_q4(const AppendQ4Job& j, cudaStream_t stream) {
-  const unsigned grid = row_blocks(static_cast<long>(j.B) * j.Hkv * j.L);
+namespace {
+template <int M, bool ROT>
+cudaError_t launch_append(const AppendQ4Job& j, int tr, long seg_rows, int seg_tiles, unsigned grid,
+                          cudaStream_t stream) {
+  constexpr int kMaxRows = M <= 4 ? 32 : 16;
+  static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
+  const cudaError_t e = allowed.get(
+      [] {
+        return cudaFuncSetAttribute(append_q4_kernel<M, ROT>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMaxRows * (256 * M + q4::record_bytes(M)));
+      },
+      cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
+  if (e != cudaSuccess) return e;
+  append_q4_kernel<M, ROT><<<grid, 256, tr * (256 * M + q4::record_bytes(M)), stream>>>(
+      j, tr, seg_rows, seg_tiles);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_append_q4(const AppendQ4Job& job, cudaStream_t stream) {
+  AppendQ4Job j = job;
+  const long heads = static_cast<long>(j.B) * j.Hkv;
+  // The rows that leave anything: all, or of a chunk longer than its ring the last ones.
+  const bool cut = !j.k_out && j.window > 0 && j.L > j.window;
+  const int used = cut ? j.window : j.L;
+  j.l0 = j.L - used;
+  const long segs = cut ? heads : 1, seg_rows = cut ? used : heads * j.L;
+  // Rows per block: 32 (16 wide ones: 36 KB), fewer while that leaves SMs without a block.
+  int tr = j.D <= 128 ? 32 : 16;
+  while (tr > 8 && (segs * seg_rows + tr - 1) / tr < 2 * 152) tr /= 2;
+  const long tiles = (seg_rows + tr - 1) / tr;
+  if (tiles * segs > 0x7fffffffL) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(tiles * segs);
   return with_groups(j.D / 32, [&](auto g) {
     constexpr int M = decltype(g)::value;
-    if (j.table)
-      append_q4_kernel<M, true><<<grid, 256, 0, stream>>>(j);
-    else
-      append_q4_kernel<M, false><<<grid, 256, 0, stream>>>(j);
-    return cudaGetLastError();
+    return j.table ? launch_append<M, true>(j, tr, seg_rows, static_cast<int>(tiles), grid, stream)
+                   : launch_append<M, false>(j, tr, seg_rows, static_cast<int>(tiles), grid, stream);
   });
 }
 

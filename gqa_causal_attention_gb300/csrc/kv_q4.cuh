@@ -48,49 +48,32 @@ __device__ __forceinline__ uint32_t bf16_bits_of(double x) {
   return static_cast<uint32_t>(r - (896ull << 7));
 }
 
-// Four neighbouring dims of one row around RMSNorm and RoPE:
-//   y[e] = a[e] * c[e] + b[e] * s[e],  a = own * inv * wo,  b = oth * inv * wt
-// with own the dims' raw values, oth their rotary partners', inv the row's 1 / rms
-// (1, and weights unused, without a norm). y is fp32, off by at most err.
-struct Quad {
-  float own[4], oth[4], c[4], s[4], wo[4], wt[4];
-  float y[4], err[4];
-};
-
-// What four dims become: 16 bits of codes, and their group's scale (the same on the
-// group's 8 lanes).
+// What four neighbouring dims become: 16 bits of codes, and their group's scale (the same
+// on the group's 8 lanes).
 struct Coded {
   uint32_t codes, scale;
 };
 
-// Quantises the warp's row of D dims: lane l holds quads l + 32 k (k < NC) of its D / 4
-// (zeros where there is none); a group is 8 aligned lanes. Codes and scales are those
-// of the exact y (of own when PLAIN: no norm and no rotation): the scale is
-// bf16(max|y| / 7), the code rint(y / scale), both rounded once, ties to even. fp32
-// decides wherever it is further from a rounding border than its error; otherwise the
-// warp works the row out again in fp64, whose rate is a thirtieth of fp32's here, so
-// that all rows in fp64 would cost several times the memory traffic. At D = 128 that
-// is under one row in a hundred with RoPE. Every lane of the warp must call it.
-template <int NC, bool PLAIN>
-__device__ __forceinline__ void quantise_row(const Quad (&q)[NC], bool norm, int D, float eps,
-                                             Coded (&out)[NC]) {
+// Quantises a row held as quads y[k] (dims 4 (lane + 32 k) .. + 3; zeros where there are
+// none), each off from the exact values by at most err[k]; a group is 8 aligned lanes. The
+// scale is bf16(max|y| / 7), the code rint(y / scale), ties to even. Returns whether every
+// rounding was further from its border than the error (warp-uniform): if not, the row has
+// to be done again by quantise_exact. Every lane of the warp must call it.
+template <int NC>
+__device__ __forceinline__ bool quantise_fast(const float (&y)[NC][4], const float (&err)[NC],
+                                              Coded (&out)[NC]) {
   bool unsure = false;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    const Quad& u = q[k];
-    uint32_t top = 0, far = 0;
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      top = max(top, __float_as_uint(u.y[e]) & 0x7fffffffu);     // NaN above inf above the rest
-      if (!PLAIN) far = max(far, __float_as_uint(u.err[e]));
-    }
-    top = group_max_u(top);
-    if (!PLAIN) far = group_max_u(far);
+    for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(y[k][e]) & 0x7fffffffu);
+    top = group_max_u(top);                               // NaN above inf above the rest
+    const uint32_t far = group_max_u(__float_as_uint(err[k]));
+    out[k].codes = 0x8888u;
     if (max(top, far) >= 0x7f800000u) {
-      out[k].codes = 0x8888u;
       out[k].scale = kNanScale;
     } else if ((top | far) == 0) {
-      out[k].codes = 0x8888u;
       out[k].scale = 0;
     } else {
       const float ferr = __uint_as_float(far);
@@ -100,61 +83,72 @@ __device__ __forceinline__ void quantise_row(const Quad (&q)[NC], bool norm, int
       unsure |= a7 < 0x1p-120f || fabsf(a7 - mid) <= ferr * 0.15f + a7 * 0x1p-23f;
       const uint32_t sc = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
       const float rs = 1.0f / bf16_to_float(sc);
+      // t is off by err / scale and by two roundings of 2^-24 of at most 7.04
+      const float near = 0.5f - fmaf(err[k], rs, 0x1p-20f);
       uint32_t codes = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // t is off by err / scale and by two roundings of 2^-24 of at most 7.04
-        const float t = u.y[e] * rs, c = rintf(t);
-        unsure |= 0.5f - fabsf(t - c) <= (PLAIN ? 0x1p-20f : fmaf(u.err[e], rs, 0x1p-20f));
+        const float t = y[k][e] * rs, c = rintf(t);
+        unsure |= fabsf(t - c) >= near;
         codes |= (static_cast<uint32_t>(static_cast<int>(c) + 8) & 15u) << (4 * e);
       }
       out[k].codes = codes;
       out[k].scale = sc;
     }
   }
-  if (!__any_sync(0xffffffffu, unsure)) return;
+  return !__any_sync(0xffffffffu, unsure);
+}
 
+// The same for the raw row x of D dims in fp64: y = RoPE(RMSNorm(x)) with the row's (cos,
+// sin) table tab (NULL: no rotation) and norm weights nw (NULL: none). fp64 runs at a
+// thirtieth of fp32's rate here, so all rows this way would cost several times the memory
+// traffic; about one row in a hundred comes here (D = 128, RoPE), one in a thousand without
+// rotation.
+template <int NC>
+__device__ __noinline__ void quantise_exact(const float* x, const float2* tab, int R,
+                                            const float* nw, float eps, int D, int lane,
+                                            Coded (&out)[NC]) {
   double inv = 1.0;
-  if (!PLAIN && norm) {
+  if (nw) {
     double ss = 0.0;
-#pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss += static_cast<double>(q[k].own[e]) * q[k].own[e];
+    for (int d = lane; d < D; d += 32) ss += static_cast<double>(x[d]) * x[d];
     inv = 1.0 / sqrt(warp_sum_d(ss) / D + static_cast<double>(eps));
   }
+  auto at = [&](int d) {
+    const double v = x[d];
+    return nw ? v * inv * nw[d] : v;
+  };
+  const int half = R / 2;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    const Quad& u = q[k];
     double y[4], amax = 0.0;
-#pragma unroll
+    bool bad = false;
     for (int e = 0; e < 4; ++e) {
-      if (PLAIN) {
-        y[e] = u.own[e];
-      } else {
-        double a = u.own[e], b = u.oth[e];
-        if (norm) {
-          a = a * inv * u.wo[e];
-          b = b * inv * u.wt[e];
+      const int d = 4 * (lane + 32 * k) + e;
+      y[e] = 0.0;
+      if (d < D) {
+        if (tab && d < R) {
+          const int i = d < half ? d : d - half;
+          const double a = at(i), b = at(i + half), c = tab[i].x, s = tab[i].y;
+          y[e] = d < half ? a * c - b * s : b * c + a * s;
+        } else {
+          y[e] = at(d);
         }
-        y[e] = a * u.c[e] + b * u.s[e];
       }
+      bad |= !isfinite(y[e]);
       amax = fmax(amax, fabs(y[e]));
     }
-#pragma unroll
     for (int o = 1; o <= 4; o <<= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (out[k].scale != kNanScale) {
-      const uint32_t sc = amax > 0.0 ? bf16_bits_of(amax / 7.0) : 0u;
-      const double s = bf16_to_float(sc);
-      uint32_t codes = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = sc ? max(-7, min(7, __double2int_rn(y[e] / s))) : 0;
-        codes |= static_cast<uint32_t>(c + 8) << (4 * e);
-      }
-      out[k].codes = codes;
-      out[k].scale = sc;
+    bad = group_max_u(bad ? 1u : 0u) != 0;
+    const uint32_t sc = bad ? kNanScale : (amax > 0.0 ? bf16_bits_of(amax / 7.0) : 0u);
+    const double s = bf16_to_float(sc);
+    uint32_t codes = 0;
+    for (int e = 0; e < 4; ++e) {
+      const int c = sc == 0 || bad ? 0 : max(-7, min(7, __double2int_rn(y[e] / s)));
+      codes |= static_cast<uint32_t>(c + 8) << (4 * e);
     }
+    out[k].codes = codes;
+    out[k].scale = sc;
   }
 }
 
