@@ -37,104 +37,116 @@ cudaError_t with_groups(int m, F f) {
   }
 }
 
-// A lane's quads of the raw row x through RMSNorm (nw) and RoPE (tab: the row's angles), in
-// fp32, and a bound of their error. Every lane of the warp calls it.
+// A lane's angles of a row: (cos, +-sin) of its quads' dims, the sign that of the partner's
+// term; (1, 0) past the rotary dims.
 template <int M, int NC>
-__device__ __forceinline__ void rotate_quads(const float* x, const float2* tab, int R,
-                                             const float* nw, float eps, int lane,
-                                             float (&y)[NC][4], float (&err)[NC]) {
-  constexpr int D = 32 * M;
+__device__ __forceinline__ void load_angles(const float2* tab, int R, int lane,
+                                            float (&c)[NC][4], float (&s)[NC][4]) {
   const int half = R / 2;
-  float inv = 1.f;
-  if (nw) {
-    float ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int d0 = 4 * (lane + 32 * k);
-      if (d0 < D) {
-        const float4 t = *reinterpret_cast<const float4*>(x + d0);
-        ss = fmaf(t.x, t.x, fmaf(t.y, t.y, fmaf(t.z, t.z, fmaf(t.w, t.w, ss))));
+  for (int k = 0; k < NC; ++k) {
+    const int d0 = 4 * (lane + 32 * k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[k][e] = 1.f;
+      s[k][e] = 0.f;
+    }
+    if (d0 >= R) continue;
+    if (half % 4 == 0) {                     // the quad lies within one half
+      const bool low = d0 < half;
+      const float4* ang = reinterpret_cast<const float4*>(tab + (low ? d0 : d0 - half));
+      const float4 a0 = __ldg(ang), a1 = __ldg(ang + 1);
+      const float sign = low ? -1.f : 1.f;
+      c[k][0] = a0.x; c[k][1] = a0.z; c[k][2] = a1.x; c[k][3] = a1.z;
+      s[k][0] = a0.y * sign; s[k][1] = a0.w * sign; s[k][2] = a1.y * sign; s[k][3] = a1.w * sign;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = d0 + e;
+        if (d < R) {
+          const float2 a = __ldg(tab + (d < half ? d : d - half));
+          c[k][e] = a.x;
+          s[k][e] = d < half ? -a.y : a.y;
+        }
       }
     }
+  }
+}
+
+// A lane's quads of the raw row x through RMSNorm (nw) and RoPE (angles c, s), in fp32, and
+// a bound of their error. Every lane of the warp calls it.
+template <int M, int NC>
+__device__ __forceinline__ void rotate_quads(const float* x, const float (&c)[NC][4],
+                                             const float (&s)[NC][4], int R, const float* nw,
+                                             float eps, int lane, float (&y)[NC][4],
+                                             float (&err)[NC]) {
+  constexpr int D = 32 * M;
+  const int half = R / 2;
+  float a[NC][4];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int d0 = 4 * (lane + 32 * k);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d0 < D) t = *reinterpret_cast<const float4*>(x + d0);
+    a[k][0] = t.x; a[k][1] = t.y; a[k][2] = t.z; a[k][3] = t.w;
+    ss = fmaf(t.x, t.x, fmaf(t.y, t.y, fmaf(t.z, t.z, fmaf(t.w, t.w, ss))));
+  }
+  // y = a c + b s, b the rotary partner. Without a norm its error is below four roundings of
+  // 2^-24 of the larger of a and b (the products' and the sum's); with one, below sixteen of
+  // either: at most nine in the sum of squares, halved by the root, and one each in the
+  // quotient, the root, its reciprocal and two products come on top.
+  float inv = 1.f, unit = 0x1p-22f;
+  if (nw) {
     inv = 1.0f / sqrtf(warp_sum(ss) / static_cast<float>(D) + eps);
+    unit = 0x1p-19f;
   }
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     const int d0 = 4 * (lane + 32 * k);
-    // y = a c + b s, b the rotary partner; the error is below sixteen roundings of 2^-24 of
-    // either term: at most nine in the sum of squares, halved by the root, and one each in
-    // the quotient, the root, its reciprocal, the two products, the rotation's product and
-    // its sum
-    float a[4], b[4], c[4], s[4], mag = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      a[e] = b[e] = s[e] = 0.f;
-      c[e] = 1.f;
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (nw && d0 < D) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(nw + d0));
+      a[k][0] = a[k][0] * inv * w.x; a[k][1] = a[k][1] * inv * w.y;
+      a[k][2] = a[k][2] * inv * w.z; a[k][3] = a[k][3] * inv * w.w;
     }
-    if (d0 < D) {
-      const float4 t = *reinterpret_cast<const float4*>(x + d0);
-      a[0] = t.x; a[1] = t.y; a[2] = t.z; a[3] = t.w;
-      if (nw) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(nw + d0));
-        a[0] = a[0] * inv * w.x; a[1] = a[1] * inv * w.y;
-        a[2] = a[2] * inv * w.z; a[3] = a[3] * inv * w.w;
-      }
-      if (half % 4 == 0) {                   // the quad lies within one half, so do its partners
-        if (d0 < R) {
-          const bool low = d0 < half;
-          const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
-          const float4 o = *reinterpret_cast<const float4*>(x + p);
-          b[0] = o.x; b[1] = o.y; b[2] = o.z; b[3] = o.w;
-          const float4* ang = reinterpret_cast<const float4*>(tab + i);
-          const float4 a0 = __ldg(ang), a1 = __ldg(ang + 1);
-          c[0] = a0.x; c[1] = a0.z; c[2] = a1.x; c[3] = a1.z;
-          s[0] = a0.y; s[1] = a0.w; s[2] = a1.y; s[3] = a1.w;
-          if (nw) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(nw + p));
-            b[0] = b[0] * inv * w.x; b[1] = b[1] * inv * w.y;
-            b[2] = b[2] * inv * w.z; b[3] = b[3] * inv * w.w;
-          }
-          if (low) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = -s[e];
-          }
+    if (d0 < R) {
+      if (half % 4 == 0) {
+        const int p = d0 < half ? d0 + half : d0 - half;
+        const float4 o = *reinterpret_cast<const float4*>(x + p);
+        b[0] = o.x; b[1] = o.y; b[2] = o.z; b[3] = o.w;
+        if (nw) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(nw + p));
+          b[0] = b[0] * inv * w.x; b[1] = b[1] * inv * w.y;
+          b[2] = b[2] * inv * w.z; b[3] = b[3] * inv * w.w;
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int d = d0 + e;
-          if (d < R) {
-            const bool low = d < half;
-            const int i = low ? d : d - half, p = low ? d + half : i;
-            b[e] = nw ? x[p] * inv * __ldg(nw + p) : x[p];
-            const float2 t2 = __ldg(tab + i);
-            c[e] = t2.x;
-            s[e] = low ? -t2.y : t2.y;
-          }
+          const int d = d0 + e, p = d < half ? d + half : d - half;
+          if (d < R) b[e] = nw ? x[p] * inv * __ldg(nw + p) : x[p];
         }
       }
     }
+    float mag = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float bs = b[e] * s[e];
-      y[k][e] = fmaf(a[e], c[e], bs);
-      mag = fmaxf(mag, fabsf(a[e] * c[e]) + fabsf(bs));
+      y[k][e] = fmaf(a[k][e], c[k][e], b[e] * s[k][e]);
+      mag = fmaxf(mag, fmaxf(fabsf(a[k][e]), fabsf(b[e])));
     }
-    err[k] = mag * 0x1p-20f;
+    err[k] = mag * unit;
   }
 }
 
 // A lane's quads of a row as they are.
 template <int M, int NC>
-__device__ __forceinline__ void plain_quads(const float* x, int lane, float (&y)[NC][4],
-                                            float (&err)[NC]) {
+__device__ __forceinline__ void plain_quads(const float* x, int lane, float (&y)[NC][4]) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     const int d0 = 4 * (lane + 32 * k);
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
     if (d0 < 32 * M) t = *reinterpret_cast<const float4*>(x + d0);
     y[k][0] = t.x; y[k][1] = t.y; y[k][2] = t.z; y[k][3] = t.w;
-    err[k] = 0.f;
   }
 }
 
@@ -158,16 +170,16 @@ __device__ __forceinline__ RowAt row_at(long row, long rows, int Hkv, int L) {
 }
 
 // Where row (bh, l) of an append goes: its record, or nullptr where it is not stored; ok:
-// whether the row's positions are valid (reported once per batch row if not).
+// whether the row's positions are valid (one thread reports a batch row that is not).
 struct Target {
   bool ok;
   uint8_t* rec;
   long angle;               // row of the angle table
 };
 template <int M, bool ROT>
-__device__ __forceinline__ Target append_target(const AppendQ4Job& j, const RowAt& at, int lane) {
+__device__ __forceinline__ Target append_target(const AppendQ4Job& j, const RowAt& at, bool one) {
   const int s0 = j.start[at.b], p0 = j.pos ? j.pos[at.b] : s0;
-  const bool first = at.l == j.l0 && at.bh % j.Hkv == 0 && lane == 0;
+  const bool first = one && at.l == j.l0 && at.bh % j.Hkv == 0;
   Target t{false, nullptr, static_cast<long>(p0) + at.l};
   if (s0 < 0 || p0 < 0 || (ROT && static_cast<long>(p0) + j.L > j.max_positions)) {
     if (first) report(j.status, ATTN_DEV_POSITION);
@@ -195,14 +207,22 @@ __device__ __forceinline__ void append_row(const AppendQ4Job& j, const float* x,
   constexpr int D = 32 * M, NC = quads_per_lane(M);
   const float2* tab = ROT ? j.table + angle * (j.R / 2) : nullptr;
   const float* nw = ROT ? j.norm_w : nullptr;
-  float y[NC][4], err[NC];
+  float y[NC][4], err[NC], c[NC][4], s[NC][4];
   Coded q[NC];
-  if (ROT)
-    rotate_quads<M>(x, tab, j.R, nw, j.norm_eps, lane, y, err);
-  else
-    plain_quads<M>(x, lane, y, err);
+  if (ROT) load_angles<M>(tab, j.R, lane, c, s);           // on their way while v is done
   if (rec) {
-    if (!quantise_fast(y, err, q)) quantise_exact<NC>(x, tab, j.R, nw, j.norm_eps, D, lane, q);
+    plain_quads<M>(v, lane, y);
+    if (!quantise_fast<NC, true>(y, err, q))
+      quantise_exact<NC>(v, nullptr, 0, nullptr, 0.f, D, lane, q);
+    store_part<M>(rec, 1, q, lane);
+  }
+  if (ROT)
+    rotate_quads<M>(x, c, s, j.R, nw, j.norm_eps, lane, y, err);
+  else
+    plain_quads<M>(x, lane, y);
+  if (rec) {
+    if (!quantise_fast<NC, !ROT>(y, err, q))
+      quantise_exact<NC>(x, tab, j.R, nw, j.norm_eps, D, lane, q);
     store_part<M>(rec, 0, q, lane);
   }
   if (k_out) {
@@ -214,28 +234,22 @@ __device__ __forceinline__ void append_row(const AppendQ4Job& j, const float* x,
         *reinterpret_cast<float4*>(k_out + d0) = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
     }
   }
-  if (rec) {
-    plain_quads<M>(v, lane, y, err);
-    if (!quantise_fast(y, err, q)) quantise_exact<NC>(v, nullptr, 0, nullptr, 0.f, D, lane, q);
-    store_part<M>(rec, 1, q, lane);
-  }
 }
 
 // Rows of k and v through shared memory: a block bulk-copies `tr` consecutive rows of each
 // (rows are contiguous whatever L is), its warps quantise them row by row into records in
 // shared memory, and the records leave in 16-byte pieces. The bytes in flight are then
-// bounded by shared memory, not by registers: a warp per row straight from memory, with the
-// values, partners and angles in registers, ran at 1.9 TB/s.
-// Rows come in segments of seg_rows (the whole tensor, or, of a chunk longer than its ring,
-// the last rows of each head), seg_tiles blocks each.
+// bounded by shared memory, not by registers. Rows come in segments of seg_rows (the whole
+// tensor, or, of a chunk longer than its ring, the last rows of each head), seg_tiles blocks
+// each.
 template <int M, bool ROT>
-__global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j, int tr, long seg_rows,
+__global__ void __launch_bounds__(256, M <= 4 ? 3 : 2) append_q4_kernel(AppendQ4Job j, int tr, long seg_rows,
                                                         int seg_tiles) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full;
   __shared__ int abort_flag;
-  __shared__ uint8_t* to[32];
+  __shared__ Target to[32];
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long seg = blockIdx.x / seg_tiles;
@@ -255,8 +269,10 @@ __global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j, int tr, l
     tc::bulk_load(xk, j.k + row0 * D, bytes, &full);
     tc::bulk_load(xv, j.v + row0 * D, bytes, &full);
   }
+  if (warp == 1 && lane < n)                 // meanwhile: where the rows go
+    to[lane] = append_target<M, ROT>(
+        j, row_at(row0 + lane, static_cast<long>(j.B) * j.Hkv * j.L, j.Hkv, j.L), true);
   __syncthreads();
-  const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
   if (!tc::mbar_wait(&full, 0, &abort_flag)) abort_flag = 1;
   __syncthreads();
   if (abort_flag) {                          // the copies never came
@@ -264,9 +280,7 @@ __global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j, int tr, l
     return;
   }
   for (int i = warp; i < n; i += 8) {
-    const RowAt at = row_at(row0 + i, rows, j.Hkv, j.L);
-    const Target t = append_target<M, ROT>(j, at, lane);
-    if (lane == 0) to[i] = t.rec;
+    const Target t = to[i];
     if (t.ok && (t.rec || j.k_out))
       append_row<M, ROT>(j, xk + i * D, xv + i * D, t.angle, t.rec ? recs + i * REC : nullptr,
                          j.k_out ? j.k_out + (row0 + i) * D : nullptr, lane);
@@ -274,34 +288,49 @@ __global__ void __launch_bounds__(256) append_q4_kernel(AppendQ4Job j, int tr, l
   __syncthreads();
   for (int p = threadIdx.x; p < n * P; p += 256) {
     const int i = p / P;
-    if (to[i])
-      reinterpret_cast<uint4*>(to[i])[p - i * P] = reinterpret_cast<const uint4*>(recs)[p];
+    if (to[i].rec)
+      reinterpret_cast<uint4*>(to[i].rec)[p - i * P] = reinterpret_cast<const uint4*>(recs)[p];
   }
 }
 
-// Records back to fp32: a warp per row, each lane four dims of key and value.
+// Records back to fp32: a block brings `tr` rows' records to shared memory in 16-byte
+// pieces, then a warp per row writes four dims of key and value per lane.
 template <int M>
-__global__ void __launch_bounds__(256) read_q4_kernel(ReadQ4Job j) {
+__global__ void __launch_bounds__(256) read_q4_kernel(ReadQ4Job j, int tr) {
+  constexpr int D = 32 * M, NC = quads_per_lane(M), REC = q4::record_bytes(M), P = REC / 16;
+  __shared__ __align__(16) uint8_t recs[32 * REC];
+  __shared__ const uint8_t* from[32];
   if (gated_off(j.skip)) return;
-  constexpr int D = 32 * M, NC = quads_per_lane(M);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
-  const long step = static_cast<long>(gridDim.x) * 8;
-  for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < rows; row += step) {
-    const RowAt at = row_at(row, rows, j.Hkv, j.L);
+  const long row0 = static_cast<long>(blockIdx.x) * tr;
+  const int n = static_cast<int>(min(static_cast<long>(tr), rows - row0));
+  if (threadIdx.x < n) {
+    const RowAt at = row_at(row0 + threadIdx.x, rows, j.Hkv, j.L);
     const int s0 = j.start[at.b];
-    const bool first = at.l == 0 && at.bh % j.Hkv == 0 && lane == 0;
+    const bool first = at.l == 0 && at.bh % j.Hkv == 0;
+    const uint8_t* src = nullptr;
     if (s0 < 0) {
       if (first) report(j.status, ATTN_DEV_POSITION);
-      continue;
-    }
-    if (j.window == 0 && static_cast<long>(s0) + j.L > j.capacity) {
+    } else if (j.window == 0 && static_cast<long>(s0) + j.L > j.capacity) {
       if (first) report(j.status, ATTN_DEV_CAPACITY);
-      continue;
+    } else {
+      const long p = static_cast<long>(s0) + at.l;
+      src = j.cache + (at.bh * j.capacity + (j.window > 0 ? p % j.window : p)) * REC;
     }
-    const long p = static_cast<long>(s0) + at.l;
-    const long slot = j.window > 0 ? p % j.window : p;
-    const uint8_t* rec = j.cache + (at.bh * j.capacity + slot) * q4::record_bytes(M);
+    from[threadIdx.x] = src;
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < n * P; p += 256) {
+    const int i = p / P;
+    if (from[i])
+      reinterpret_cast<uint4*>(recs)[p] = reinterpret_cast<const uint4*>(from[i])[p - i * P];
+  }
+  __syncthreads();
+  for (int i = warp; i < n; i += 8) {
+    if (!from[i]) continue;
+    const uint8_t* rec = recs + i * REC;
+    const long row = row0 + i;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int ch = lane + 32 * k;
@@ -313,11 +342,11 @@ __global__ void __launch_bounds__(256) read_q4_kernel(ReadQ4Job j) {
         const uint32_t c = *reinterpret_cast<const uint16_t*>(rec + off);
         const float s = q4::bf16_to_float(
             *reinterpret_cast<const uint16_t*>(rec + (32 + 2 * part) * M + 2 * g));
-        float4 y;
-        y.x = static_cast<float>(static_cast<int>(c & 15u) - 8) * s;
-        y.y = static_cast<float>(static_cast<int>((c >> 4) & 15u) - 8) * s;
-        y.z = static_cast<float>(static_cast<int>((c >> 8) & 15u) - 8) * s;
-        y.w = static_cast<float>(static_cast<int>(c >> 12) - 8) * s;
+        // 2^23 + u, less 2^23 + 8
+        auto value = [&](uint32_t u) {
+          return (__uint_as_float(0x4b000000u | (u & 15u)) - 8388616.0f) * s;
+        };
+        const float4 y = make_float4(value(c), value(c >> 4), value(c >> 8), value(c >> 12));
         *reinterpret_cast<float4*>((part ? j.v : j.k) + row * D + 4 * ch) = y;
       }
     }
@@ -338,7 +367,7 @@ __global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
        row += step) {
     if (row >= qrows) {
       const RowAt at = row_at(row - qrows, kvrows, a.Hkv, 1);
-      const Target t = append_target<M, true>(a, at, lane);
+      const Target t = append_target<M, true>(a, at, lane == 0);
       if (t.ok)
         append_row<M, true>(a, a.k + at.bh * D, a.v + at.bh * D, t.angle, t.rec, nullptr, lane);
       continue;
@@ -349,9 +378,9 @@ __global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
                     (a.window > 0 || s0 < a.capacity);
     if (row % j.H == 0 && lane == 0) j.cache_len[b] = ok ? s0 + 1 : 0;
     if (!ok) continue;                       // the row's key rows report it
-    float y[NC][4], err[NC];
-    rotate_quads<M>(j.q + row * D, a.table + static_cast<long>(p0) * (a.R / 2), a.R, j.q_norm_w,
-                    a.norm_eps, lane, y, err);
+    float y[NC][4], err[NC], c[NC][4], s[NC][4];
+    load_angles<M>(a.table + static_cast<long>(p0) * (a.R / 2), a.R, lane, c, s);
+    rotate_quads<M>(j.q + row * D, c, s, a.R, j.q_norm_w, a.norm_eps, lane, y, err);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int d0 = 4 * (lane + 32 * k);
@@ -585,9 +614,13 @@ cudaError_t launch_append_q4(const AppendQ4Job& job, cudaStream_t stream) {
 }
 
 cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream) {
-  const unsigned grid = row_blocks(static_cast<long>(j.B) * j.Hkv * j.L);
+  const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
+  int tr = 32;
+  while (tr > 8 && (rows + tr - 1) / tr < 4 * 152) tr /= 2;
+  const long blocks = (rows + tr - 1) / tr;
+  if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
   return with_groups(j.D / 32, [&](auto g) {
-    read_q4_kernel<decltype(g)::value><<<grid, 256, 0, stream>>>(j);
+    read_q4_kernel<decltype(g)::value><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(j, tr);
     return cudaGetLastError();
   });
 }

@@ -54,12 +54,17 @@ struct Coded {
   uint32_t codes, scale;
 };
 
+// t in (-2^21, 2^21) to the nearest integer, ties to even, as the sum's low bits: the float
+// 1.5 * 2^23 + 8 + t is rounded at its unit place. Its low four bits are then t's code + 8.
+constexpr float kRound = 12582920.0f;
+
 // Quantises a row held as quads y[k] (dims 4 (lane + 32 k) .. + 3; zeros where there are
 // none), each off from the exact values by at most err[k]; a group is 8 aligned lanes. The
 // scale is bf16(max|y| / 7), the code rint(y / scale), ties to even. Returns whether every
 // rounding was further from its border than the error (warp-uniform): if not, the row has
-// to be done again by quantise_exact. Every lane of the warp must call it.
-template <int NC>
+// to be done again by quantise_exact. EXACT: y is the row itself, err is not read. Every
+// lane of the warp must call it. About six instructions a value.
+template <int NC, bool EXACT>
 __device__ __forceinline__ bool quantise_fast(const float (&y)[NC][4], const float (&err)[NC],
                                               Coded (&out)[NC]) {
   bool unsure = false;
@@ -69,32 +74,35 @@ __device__ __forceinline__ bool quantise_fast(const float (&y)[NC][4], const flo
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(y[k][e]) & 0x7fffffffu);
     top = group_max_u(top);                               // NaN above inf above the rest
-    const uint32_t far = group_max_u(__float_as_uint(err[k]));
-    out[k].codes = 0x8888u;
-    if (max(top, far) >= 0x7f800000u) {
-      out[k].scale = kNanScale;
-    } else if ((top | far) == 0) {
-      out[k].scale = 0;
-    } else {
-      const float ferr = __uint_as_float(far);
-      const float a7 = __uint_as_float(top) / 7.0f;
-      const uint32_t bits = __float_as_uint(a7);
-      const float mid = __uint_as_float((bits & 0xffff0000u) | 0x8000u);
-      unsure |= a7 < 0x1p-120f || fabsf(a7 - mid) <= ferr * 0.15f + a7 * 0x1p-23f;
-      const uint32_t sc = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
-      const float rs = 1.0f / bf16_to_float(sc);
-      // t is off by err / scale and by two roundings of 2^-24 of at most 7.04
-      const float near = 0.5f - fmaf(err[k], rs, 0x1p-20f);
-      uint32_t codes = 0;
+    const uint32_t far = EXACT ? 0u : group_max_u(__float_as_uint(err[k]));
+    const float amax = __uint_as_float(top), ferr = __uint_as_float(far);
+    // amax / 7 to two roundings; far from a bf16 border that settles the scale
+    const float a7 = amax * (1.0f / 7.0f);
+    const uint32_t bits = __float_as_uint(a7);
+    const float mid = __uint_as_float((bits & 0xffff0000u) | 0x8000u);
+    const uint32_t sc = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
+    float rs;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(bf16_to_float(sc)));
+    // t = y / scale is off by err / scale, by 2^-23 of at most 7.04 in rs and by its rounding
+    const float near = 0.5f - (EXACT ? 0x1p-19f : fmaf(err[k], rs, 0x1p-19f));
+    uint32_t b[4];
+    float off = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float t = y[k][e] * rs, c = rintf(t);
-        unsure |= fabsf(t - c) >= near;
-        codes |= (static_cast<uint32_t>(static_cast<int>(c) + 8) & 15u) << (4 * e);
-      }
-      out[k].codes = codes;
-      out[k].scale = sc;
+    for (int e = 0; e < 4; ++e) {
+      const float t = y[k][e] * rs, u = t + kRound;
+      b[e] = __float_as_uint(u);
+      off = fmaxf(off, fabsf(t - (u - kRound)));
     }
+    // the four floats' high bits cancel below bit 16
+    out[k].codes = b[0] + 16u * b[1] + 256u * b[2] + 4096u * b[3];
+    out[k].scale = sc;
+    bool doubt = a7 < 0x1p-120f || fabsf(a7 - mid) <= fmaf(ferr, 0.15f, a7 * 0x1p-22f) || off >= near;
+    if (max(top, far) >= 0x7f800000u || (top | far) == 0) {   // inf or NaN; all zero
+      out[k].codes = 0x8888u;
+      out[k].scale = (top | far) == 0 ? 0u : kNanScale;
+      doubt = false;
+    }
+    unsure |= doubt;
   }
   return !__any_sync(0xffffffffu, unsure);
 }
@@ -102,8 +110,7 @@ __device__ __forceinline__ bool quantise_fast(const float (&y)[NC][4], const flo
 // The same for the raw row x of D dims in fp64: y = RoPE(RMSNorm(x)) with the row's (cos,
 // sin) table tab (NULL: no rotation) and norm weights nw (NULL: none). fp64 runs at a
 // thirtieth of fp32's rate here, so all rows this way would cost several times the memory
-// traffic; about one row in a hundred comes here (D = 128, RoPE), one in a thousand without
-// rotation.
+// traffic; a few rows in a thousand come here.
 template <int NC>
 __device__ __noinline__ void quantise_exact(const float* x, const float2* tab, int R,
                                             const float* nw, float eps, int D, int lane,
