@@ -150,6 +150,10 @@ __device__ __forceinline__ void plain_quads(const float* x, int lane, float (&y)
   }
 }
 
+// Blocks of the row passes: four warps and up to sixteen rows, so that several are in
+// flight on an SM in different stages.
+constexpr int kRowThreads = 128, kMaxRows = 16;
+
 struct RowAt {
   long bh;      // b * Hkv + hkv
   int b, l;
@@ -199,31 +203,42 @@ __device__ __forceinline__ Target append_target(const AppendQ4Job& j, const RowA
 }
 
 // One row by one warp: x, v the raw rows (any memory); the record goes to rec (any memory)
-// unless it is nullptr, the rotated key to k_out unless that is.
+// unless it is nullptr, the rotated key to k_out unless that is. Groups whose rounding fp32
+// cannot settle are noted in later[0 .. 3] (their lanes, key then value) for a second pass,
+// or with later == nullptr done at once.
 template <int M, bool ROT>
 __device__ __forceinline__ void append_row(const AppendQ4Job& j, const float* x, const float* v,
-                                           long angle, uint8_t* rec, float* k_out, int lane) {
+                                           long angle, uint8_t* rec, float* k_out, int lane,
+                                           uint32_t* later) {
   using namespace q4;
   constexpr int D = 32 * M, NC = quads_per_lane(M);
   const float2* tab = ROT ? j.table + angle * (j.R / 2) : nullptr;
   const float* nw = ROT ? j.norm_w : nullptr;
   float y[NC][4], err[NC], c[NC][4], s[NC][4];
-  Coded q[NC];
+  uint32_t q[NC], doubt[NC];
+  auto settle = [&](int part) {
+    const uint2 d = make_uint2(doubt[0], NC > 1 ? doubt[NC - 1] : 0u);
+    store_part<M>(rec, part, q, lane);
+    if (later) {
+      if (lane == 0) *reinterpret_cast<uint2*>(later + 2 * part) = d;
+    } else if (d.x | d.y) {
+      quantise_exact<M>(part ? v : x, part ? nullptr : tab, j.R, part ? nullptr : nw, j.norm_eps,
+                        lane, d, rec, part);
+    }
+  };
   if (ROT) load_angles<M>(tab, j.R, lane, c, s);           // on their way while v is done
   if (rec) {
     plain_quads<M>(v, lane, y);
-    if (!quantise_fast<NC, true>(y, err, q))
-      quantise_exact<NC>(v, nullptr, 0, nullptr, 0.f, D, lane, q);
-    store_part<M>(rec, 1, q, lane);
+    quantise_fast<NC, true>(y, err, q, doubt);
+    settle(1);
   }
   if (ROT)
     rotate_quads<M>(x, c, s, j.R, nw, j.norm_eps, lane, y, err);
   else
     plain_quads<M>(x, lane, y);
   if (rec) {
-    if (!quantise_fast<NC, !ROT>(y, err, q))
-      quantise_exact<NC>(x, tab, j.R, nw, j.norm_eps, D, lane, q);
-    store_part<M>(rec, 0, q, lane);
+    quantise_fast<NC, !ROT>(y, err, q, doubt);
+    settle(0);
   }
   if (k_out) {
     __syncwarp();                            // in place: every lane has read its partners
@@ -243,13 +258,14 @@ __device__ __forceinline__ void append_row(const AppendQ4Job& j, const float* x,
 // tensor, or, of a chunk longer than its ring, the last rows of each head), seg_tiles blocks
 // each.
 template <int M, bool ROT>
-__global__ void __launch_bounds__(256, M <= 4 ? 3 : 2) append_q4_kernel(AppendQ4Job j, int tr, long seg_rows,
+__global__ void __launch_bounds__(kRowThreads, M <= 4 ? 6 : 4) append_q4_kernel(AppendQ4Job j, int tr, long seg_rows,
                                                         int seg_tiles) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full;
   __shared__ int abort_flag;
-  __shared__ Target to[32];
+  __shared__ Target to[kMaxRows];
+  __shared__ __align__(8) uint32_t later[kMaxRows][4];
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long seg = blockIdx.x / seg_tiles;
@@ -279,14 +295,30 @@ __global__ void __launch_bounds__(256, M <= 4 ? 3 : 2) append_q4_kernel(AppendQ4
     if (threadIdx.x == 0) report(j.status, ATTN_DEV_TIMEOUT);
     return;
   }
-  for (int i = warp; i < n; i += 8) {
+  for (int i = warp; i < n; i += kRowThreads / 32) {
     const Target t = to[i];
     if (t.ok && (t.rec || j.k_out))
       append_row<M, ROT>(j, xk + i * D, xv + i * D, t.angle, t.rec ? recs + i * REC : nullptr,
-                         j.k_out ? j.k_out + (row0 + i) * D : nullptr, lane);
+                         j.k_out ? j.k_out + (row0 + i) * D : nullptr, lane, later[i]);
+  }
+  // Second pass, rarely anything: kept out of the loop above, whose registers a call there
+  // would have cost (and 6 us at 4 x 2048 tokens). A row's second
+  // pass is its own warp's.
+  __syncwarp();
+  for (int i = warp; i < n; i += kRowThreads / 32) {
+    if (!to[i].rec) continue;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      const uint2 d = *reinterpret_cast<const uint2*>(&later[i][2 * part]);
+      if (!(d.x | d.y)) continue;
+      const bool rot = ROT && part == 0;
+      q4::quantise_exact<M>((part ? xv : xk) + i * D,
+                            rot ? j.table + to[i].angle * (j.R / 2) : nullptr, j.R,
+                            rot ? j.norm_w : nullptr, j.norm_eps, lane, d, recs + i * REC, part);
+    }
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < n * P; p += 256) {
+  for (int p = threadIdx.x; p < n * P; p += kRowThreads) {
     const int i = p / P;
     if (to[i].rec)
       reinterpret_cast<uint4*>(to[i].rec)[p - i * P] = reinterpret_cast<const uint4*>(recs)[p];
@@ -296,10 +328,10 @@ __global__ void __launch_bounds__(256, M <= 4 ? 3 : 2) append_q4_kernel(AppendQ4
 // Records back to fp32: a block brings `tr` rows' records to shared memory in 16-byte
 // pieces, then a warp per row writes four dims of key and value per lane.
 template <int M>
-__global__ void __launch_bounds__(256) read_q4_kernel(ReadQ4Job j, int tr) {
+__global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int tr) {
   constexpr int D = 32 * M, NC = quads_per_lane(M), REC = q4::record_bytes(M), P = REC / 16;
-  __shared__ __align__(16) uint8_t recs[32 * REC];
-  __shared__ const uint8_t* from[32];
+  __shared__ __align__(16) uint8_t recs[kMaxRows * REC];
+  __shared__ const uint8_t* from[kMaxRows];
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
@@ -321,13 +353,13 @@ __global__ void __launch_bounds__(256) read_q4_kernel(ReadQ4Job j, int tr) {
     from[threadIdx.x] = src;
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < n * P; p += 256) {
+  for (int p = threadIdx.x; p < n * P; p += kRowThreads) {
     const int i = p / P;
     if (from[i])
       reinterpret_cast<uint4*>(recs)[p] = reinterpret_cast<const uint4*>(from[i])[p - i * P];
   }
   __syncthreads();
-  for (int i = warp; i < n; i += 8) {
+  for (int i = warp; i < n; i += kRowThreads / 32) {
     if (!from[i]) continue;
     const uint8_t* rec = recs + i * REC;
     const long row = row0 + i;
@@ -369,7 +401,8 @@ __global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
       const RowAt at = row_at(row - qrows, kvrows, a.Hkv, 1);
       const Target t = append_target<M, true>(a, at, lane == 0);
       if (t.ok)
-        append_row<M, true>(a, a.k + at.bh * D, a.v + at.bh * D, t.angle, t.rec, nullptr, lane);
+        append_row<M, true>(a, a.k + at.bh * D, a.v + at.bh * D, t.angle, t.rec, nullptr, lane,
+                            nullptr);
       continue;
     }
     const int b = static_cast<int>(row / j.H);
@@ -576,7 +609,6 @@ namespace {
 template <int M, bool ROT>
 cudaError_t launch_append(const AppendQ4Job& j, int tr, long seg_rows, int seg_tiles, unsigned grid,
                           cudaStream_t stream) {
-  constexpr int kMaxRows = M <= 4 ? 32 : 16;
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   const cudaError_t e = allowed.get(
       [] {
@@ -586,7 +618,7 @@ cudaError_t launch_append(const AppendQ4Job& j, int tr, long seg_rows, int seg_t
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  append_q4_kernel<M, ROT><<<grid, 256, tr * (256 * M + q4::record_bytes(M)), stream>>>(
+  append_q4_kernel<M, ROT><<<grid, kRowThreads, tr * (256 * M + q4::record_bytes(M)), stream>>>(
       j, tr, seg_rows, seg_tiles);
   return cudaGetLastError();
 }
@@ -600,9 +632,9 @@ cudaError_t launch_append_q4(const AppendQ4Job& job, cudaStream_t stream) {
   const int used = cut ? j.window : j.L;
   j.l0 = j.L - used;
   const long segs = cut ? heads : 1, seg_rows = cut ? used : heads * j.L;
-  // Rows per block: 32 (16 wide ones: 36 KB), fewer while that leaves SMs without a block.
-  int tr = j.D <= 128 ? 32 : 16;
-  while (tr > 8 && (segs * seg_rows + tr - 1) / tr < 2 * 152) tr /= 2;
+  // Rows per block: 16 (8 wide ones: 18 KB), fewer while that leaves SMs without a block.
+  int tr = j.D <= 128 ? 16 : 8;
+  while (tr > 4 && (segs * seg_rows + tr - 1) / tr < 2 * 152) tr /= 2;
   const long tiles = (seg_rows + tr - 1) / tr;
   if (tiles * segs > 0x7fffffffL) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(tiles * segs);
@@ -615,12 +647,12 @@ cudaError_t launch_append_q4(const AppendQ4Job& job, cudaStream_t stream) {
 
 cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream) {
   const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
-  int tr = 32;
-  while (tr > 8 && (rows + tr - 1) / tr < 4 * 152) tr /= 2;
+  int tr = kMaxRows;
+  while (tr > 4 && (rows + tr - 1) / tr < 4 * 152) tr /= 2;
   const long blocks = (rows + tr - 1) / tr;
   if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
   return with_groups(j.D / 32, [&](auto g) {
-    read_q4_kernel<decltype(g)::value><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(j, tr);
+    read_q4_kernel<decltype(g)::value><<<static_cast<unsigned>(blocks), kRowThreads, 0, stream>>>(j, tr);
     return cudaGetLastError();
   });
 }

@@ -39,20 +39,8 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
-// x > 0 (finite) rounded once to bf16, ties to even; below 2^-126 to the subnormal grid.
-__device__ __forceinline__ uint32_t bf16_bits_of(double x) {
-  if (x < 0x1p-126) return static_cast<uint32_t>(__double2int_rn(x * 0x1p133));
-  const unsigned long long b = __double_as_longlong(x);
-  // 45 of the 52 stored bits go; the exponent is rebased from 1023 to 127
-  const unsigned long long r = (b + ((1ull << 44) - 1) + ((b >> 45) & 1ull)) >> 45;
-  return static_cast<uint32_t>(r - (896ull << 7));
-}
-
-// What four neighbouring dims become: 16 bits of codes, and their group's scale (the same
-// on the group's 8 lanes).
-struct Coded {
-  uint32_t codes, scale;
-};
+// Four neighbouring dims quantised: their codes in the low 16 bits, their group's scale (the
+// same on the group's 8 lanes) in the high ones.
 
 // t in (-2^21, 2^21) to the nearest integer, ties to even, as the sum's low bits: the float
 // 1.5 * 2^23 + 8 + t is rounded at its unit place. Its low four bits are then t's code + 8.
@@ -60,14 +48,13 @@ constexpr float kRound = 12582920.0f;
 
 // Quantises a row held as quads y[k] (dims 4 (lane + 32 k) .. + 3; zeros where there are
 // none), each off from the exact values by at most err[k]; a group is 8 aligned lanes. The
-// scale is bf16(max|y| / 7), the code rint(y / scale), ties to even. Returns whether every
-// rounding was further from its border than the error (warp-uniform): if not, the row has
-// to be done again by quantise_exact. EXACT: y is the row itself, err is not read. Every
-// lane of the warp must call it. About six instructions a value.
+// scale is bf16(max|y| / 7), the code rint(y / scale), ties to even. doubt[k] gets the lanes
+// (warp-uniform) whose roundings were not further from their borders than the error: their
+// groups have to be done again by quantise_exact. EXACT: y is the row itself, err is not
+// read. Every lane of the warp must call it. About six instructions a value.
 template <int NC, bool EXACT>
-__device__ __forceinline__ bool quantise_fast(const float (&y)[NC][4], const float (&err)[NC],
-                                              Coded (&out)[NC]) {
-  bool unsure = false;
+__device__ __forceinline__ void quantise_fast(const float (&y)[NC][4], const float (&err)[NC],
+                                              uint32_t (&out)[NC], uint32_t (&doubt)[NC]) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     uint32_t top = 0;
@@ -94,89 +81,102 @@ __device__ __forceinline__ bool quantise_fast(const float (&y)[NC][4], const flo
       off = fmaxf(off, fabsf(t - (u - kRound)));
     }
     // the four floats' high bits cancel below bit 16
-    out[k].codes = b[0] + 16u * b[1] + 256u * b[2] + 4096u * b[3];
-    out[k].scale = sc;
-    bool doubt = a7 < 0x1p-120f || fabsf(a7 - mid) <= fmaf(ferr, 0.15f, a7 * 0x1p-22f) || off >= near;
+    out[k] = ((b[0] + 16u * b[1] + 256u * b[2] + 4096u * b[3]) & 0xffffu) | sc << 16;
+    bool unsure = a7 < 0x1p-120f || fabsf(a7 - mid) <= fmaf(ferr, 0.15f, a7 * 0x1p-22f) || off >= near;
     if (max(top, far) >= 0x7f800000u || (top | far) == 0) {   // inf or NaN; all zero
-      out[k].codes = 0x8888u;
-      out[k].scale = (top | far) == 0 ? 0u : kNanScale;
-      doubt = false;
+      out[k] = 0x8888u | ((top | far) == 0 ? 0u : kNanScale << 16);
+      unsure = false;
     }
-    unsure |= doubt;
-  }
-  return !__any_sync(0xffffffffu, unsure);
-}
-
-// The same for the raw row x of D dims in fp64: y = RoPE(RMSNorm(x)) with the row's (cos,
-// sin) table tab (NULL: no rotation) and norm weights nw (NULL: none). fp64 runs at a
-// thirtieth of fp32's rate here, so all rows this way would cost several times the memory
-// traffic; a few rows in a thousand come here.
-template <int NC>
-__device__ __noinline__ void quantise_exact(const float* x, const float2* tab, int R,
-                                            const float* nw, float eps, int D, int lane,
-                                            Coded (&out)[NC]) {
-  double inv = 1.0;
-  if (nw) {
-    double ss = 0.0;
-    for (int d = lane; d < D; d += 32) ss += static_cast<double>(x[d]) * x[d];
-    inv = 1.0 / sqrt(warp_sum_d(ss) / D + static_cast<double>(eps));
-  }
-  auto at = [&](int d) {
-    const double v = x[d];
-    return nw ? v * inv * nw[d] : v;
-  };
-  const int half = R / 2;
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    double y[4], amax = 0.0;
-    bool bad = false;
-    for (int e = 0; e < 4; ++e) {
-      const int d = 4 * (lane + 32 * k) + e;
-      y[e] = 0.0;
-      if (d < D) {
-        if (tab && d < R) {
-          const int i = d < half ? d : d - half;
-          const double a = at(i), b = at(i + half), c = tab[i].x, s = tab[i].y;
-          y[e] = d < half ? a * c - b * s : b * c + a * s;
-        } else {
-          y[e] = at(d);
-        }
-      }
-      bad |= !isfinite(y[e]);
-      amax = fmax(amax, fabs(y[e]));
-    }
-    for (int o = 1; o <= 4; o <<= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    bad = group_max_u(bad ? 1u : 0u) != 0;
-    const uint32_t sc = bad ? kNanScale : (amax > 0.0 ? bf16_bits_of(amax / 7.0) : 0u);
-    const double s = bf16_to_float(sc);
-    uint32_t codes = 0;
-    for (int e = 0; e < 4; ++e) {
-      const int c = sc == 0 || bad ? 0 : max(-7, min(7, __double2int_rn(y[e] / s)));
-      codes |= static_cast<uint32_t>(c + 8) << (4 * e);
-    }
-    out[k].codes = codes;
-    out[k].scale = sc;
+    doubt[k] = __ballot_sync(0xffffffffu, unsure);
   }
 }
 
-// Stores lane `lane`'s quads of a row into the record at rec: the key part (part = 0)
-// or the value part (part = 1).
+// Quad e of group g into the key part (part = 0) or value part (1) of the record at rec.
+template <int M>
+__device__ __forceinline__ void store_quad(uint8_t* rec, int part, uint32_t q, int g, int e) {
+  const int at = part ? 16 * M + 2 * (e * M + g) : 4 * ((e >> 1) * M + g) + 2 * (e & 1);
+  *reinterpret_cast<uint16_t*>(rec + at) = static_cast<uint16_t>(q);
+  if (e == 0)
+    *reinterpret_cast<uint16_t*>(rec + (32 + 2 * part) * M + 2 * g) = static_cast<uint16_t>(q >> 16);
+}
+
+// A lane's quads of a row.
 template <int M, int NC>
-__device__ __forceinline__ void store_part(uint8_t* rec, int part, const Coded (&q)[NC], int lane) {
+__device__ __forceinline__ void store_part(uint8_t* rec, int part, const uint32_t (&q)[NC], int lane) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     const int ch = lane + 32 * k;
-    if (ch >= 8 * M) continue;
-    const int g = ch >> 3, e = ch & 7;                  // group, quad within it
-    const int at = part ? 16 * M + 2 * (e * M + g) : 4 * ((e >> 1) * M + g) + 2 * (e & 1);
-    *reinterpret_cast<uint16_t*>(rec + at) = static_cast<uint16_t>(q[k].codes);
-    if (e == 0)
-      *reinterpret_cast<uint16_t*>(rec + (32 + 2 * part) * M + 2 * g) =
-          static_cast<uint16_t>(q[k].scale);
+    if (ch < 8 * M) store_quad<M>(rec, part, q[k], ch >> 3, ch & 7);
   }
   if (part == 1) {                                      // zero padding
     constexpr int pad = (record_bytes(M) - 36 * M) / 2;
     if (pad > 0 && lane < pad) *reinterpret_cast<uint16_t*>(rec + 36 * M + 2 * lane) = 0;
+  }
+}
+
+// 1 / rms of a row in fp64.
+template <int = 0>
+__device__ __noinline__ double exact_inv_rms(const float* x, float eps, int D, int lane) {
+  double ss = 0.0;
+#pragma unroll 1
+  for (int d = lane; d < D; d += 32) ss = fma(static_cast<double>(x[d]), static_cast<double>(x[d]), ss);
+  return 1.0 / sqrt(warp_sum_d(ss) / D + static_cast<double>(eps));
+}
+
+// The doubtful groups (doubt: quantise_fast's lanes, of quads 0 .. 31 and 32 .. 63) of the raw
+// row x again, in fp64, into part `part` of the record at rec: y = RoPE(RMSNorm(x)) with the
+// row's (cos, sin) table tab (NULL: no rotation) and norm weights nw (NULL: none), a group at
+// a time, one dim per lane. No quotient is formed: fp32 proposes the scale and the codes, and
+// exact products with the borders next to them decide. A few rows in a thousand come here
+// (with a norm about one in a hundred); kept short, since its instructions are not in the
+// cache then (unrolled over a row, the first use on an SM took 3 us).
+template <int M>
+__device__ __noinline__ void quantise_exact(const float* x, const float2* tab, int R,
+                                            const float* nw, float eps, int lane, uint2 doubt,
+                                            uint8_t* rec, int part) {
+  constexpr int D = 32 * M;
+  const double inv = nw ? exact_inv_rms<>(x, eps, D, lane) : 1.0;
+  const int half = R / 2;
+#pragma unroll 1
+  for (int g = 0; g < M; ++g) {
+    if (!((g < 4 ? doubt.x : doubt.y) >> (8 * (g & 3)) & 0xffu)) continue;
+    const int d = 32 * g + lane;
+    double y = x[d];
+    if (nw) y = y * inv * nw[d];
+    if (tab && d < R) {
+      const int i = d < half ? d : d - half, p = d < half ? d + half : i;
+      const float2 t = tab[i];
+      double b = x[p];
+      if (nw) b = b * inv * nw[p];
+      y = fma(y, static_cast<double>(t.x), b * (d < half ? -t.y : t.y));
+    }
+    double amax = fabs(y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // the scale's two borders, half a unit from the proposed one
+    const uint32_t bits = __float_as_uint(static_cast<float>(amax) * (1.0f / 7.0f));
+    uint32_t sc = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
+    const double above = 7.0 * __uint_as_float((sc << 16) | 0x8000u);
+    const double below = sc ? 7.0 * __uint_as_float(((sc - 1u) << 16) | 0x8000u) : -1.0;
+    if (amax > above || (amax == above && (sc & 1u)))
+      ++sc;
+    else if (amax < below || (amax == below && (sc & 1u)))
+      --sc;
+    // the code; tiny scales are lifted out of the subnormals for the proposal
+    const double s = bf16_to_float(sc), lift = sc < 0x0800u ? 0x1p100 : 1.0;
+    int c = sc ? __float2int_rn(static_cast<float>(y * lift) / static_cast<float>(s * lift)) : 0;
+    const double rest = fma(static_cast<double>(-c), s, y), border = 0.5 * s;
+    if (rest > border || (rest == border && (c & 1)))
+      ++c;
+    else if (rest < -border || (rest == -border && (c & 1)))
+      --c;
+    c = sc ? max(-7, min(7, c)) : 0;
+    // back to quads: lane l of the group's eight takes dims 4 (l % 8) .. + 3
+    uint32_t codes = static_cast<uint32_t>(c + 8) << (4 * (lane & 3));
+    codes |= __shfl_xor_sync(0xffffffffu, codes, 1);
+    codes |= __shfl_xor_sync(0xffffffffu, codes, 2);
+    codes = __shfl_sync(0xffffffffu, codes, 4 * (lane & 7));
+    if (lane >> 3 == (g & 3)) store_quad<M>(rec, part, codes | sc << 16, g, lane & 7);
   }
 }
 
