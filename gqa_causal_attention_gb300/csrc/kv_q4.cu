@@ -15,8 +15,6 @@ namespace gqa {
 
 namespace {
 
-__host__ __device__ constexpr int quads_per_lane(int M) { return (8 * M + 31) / 32; }
-
 // Calls f(std::integral_constant-like tag) for the runtime group count m = D / 32.
 template <int M>
 struct Groups {
@@ -37,117 +35,103 @@ cudaError_t with_groups(int m, F f) {
   }
 }
 
-// A lane's angles of a row: (cos, +-sin) of its quads' dims, the sign that of the partner's
-// term; (1, 0) past the rotary dims.
-template <int M, int NC>
-__device__ __forceinline__ void load_angles(const float2* tab, int R, int lane,
-                                            float (&c)[NC][4], float (&s)[NC][4]) {
+// How a row's rotation is read: not at all, in quads (half the rotary dims a multiple of
+// four: a quad lies within one half, and so do its partners), or dim by dim.
+enum { kNoRope = 0, kRopeQuads = 1, kRopeDims = 2 };
+
+__device__ __forceinline__ void load4(const float* p, float* r) {
+  const float4 t = *reinterpret_cast<const float4*>(p);
+  r[0] = t.x; r[1] = t.y; r[2] = t.z; r[3] = t.w;
+}
+
+// A lane's quads of the raw row x.
+template <int M>
+__device__ __forceinline__ void store_row(float* x, const q4::Lanes<M>& at, const float (&y)[8]) {
+  *reinterpret_cast<float4*>(x + at.dim(0)) = make_float4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<float4*>(x + at.dim(1)) = make_float4(y[4], y[5], y[6], y[7]);
+}
+template <int M>
+__device__ __forceinline__ void load_row(const float* x, const q4::Lanes<M>& at, float (&y)[8]) {
+  if (at.in) {
+    load4(x + at.dim(0), y);
+    load4(x + at.dim(1), y + 4);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  }
+}
+
+// A lane's quads of the raw row x through RMSNorm (nw) and RoPE (tab: the row's angles;
+// x and tab in any memory), in fp32, and a bound of their error. Every lane of the warp
+// calls it.
+template <int M, int ROPE>
+__device__ __forceinline__ float rotate_row(const float* x, const float2* tab, int R,
+                                            const float* nw, float eps, const q4::Lanes<M>& at,
+                                            int lane, float (&y)[8]) {
   const int half = R / 2;
+  float c[8], s[8], b[8], w[8];
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int d0 = 4 * (lane + 32 * k);
+  for (int e = 0; e < 8; ++e) {
+    c[e] = w[e] = 1.f;
+    s[e] = b[e] = 0.f;
+  }
+  // y = a c + b s, b the rotary partner
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[k][e] = 1.f;
-      s[k][e] = 0.f;
-    }
-    if (d0 >= R) continue;
-    if (half % 4 == 0) {                     // the quad lies within one half
+  for (int q = 0; q < 8; q += 4) {
+    const int d0 = at.dim(q / 4);
+    if (!at.in || d0 >= R) continue;
+    if (ROPE == kRopeQuads) {
       const bool low = d0 < half;
-      const float4* ang = reinterpret_cast<const float4*>(tab + (low ? d0 : d0 - half));
-      const float4 a0 = __ldg(ang), a1 = __ldg(ang + 1);
+      const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
       const float sign = low ? -1.f : 1.f;
-      c[k][0] = a0.x; c[k][1] = a0.z; c[k][2] = a1.x; c[k][3] = a1.z;
-      s[k][0] = a0.y * sign; s[k][1] = a0.w * sign; s[k][2] = a1.y * sign; s[k][3] = a1.w * sign;
+      const float4* ang = reinterpret_cast<const float4*>(tab + i);
+      const float4 a0 = ang[0], a1 = ang[1];
+      load4(x + p, b + q);
+      c[q] = a0.x; c[q + 1] = a0.z; c[q + 2] = a1.x; c[q + 3] = a1.z;
+      s[q] = a0.y * sign; s[q + 1] = a0.w * sign; s[q + 2] = a1.y * sign; s[q + 3] = a1.w * sign;
+      if (nw) load4(nw + p, w + q);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = d0 + e;
-        if (d < R) {
-          const float2 a = __ldg(tab + (d < half ? d : d - half));
-          c[k][e] = a.x;
-          s[k][e] = d < half ? -a.y : a.y;
-        }
+      for (int e = q; e < q + 4; ++e) {
+        const int d = d0 + e - q;
+        if (d >= R) continue;
+        const bool low = d < half;
+        const int i = low ? d : d - half, p = low ? d + half : i;
+        const float2 a = tab[i];
+        b[e] = x[p];
+        c[e] = a.x;
+        s[e] = low ? -a.y : a.y;
+        if (nw) w[e] = nw[p];
       }
     }
   }
-}
-
-// A lane's quads of the raw row x through RMSNorm (nw) and RoPE (angles c, s), in fp32, and
-// a bound of their error. Every lane of the warp calls it.
-template <int M, int NC>
-__device__ __forceinline__ void rotate_quads(const float* x, const float (&c)[NC][4],
-                                             const float (&s)[NC][4], int R, const float* nw,
-                                             float eps, int lane, float (&y)[NC][4],
-                                             float (&err)[NC]) {
-  constexpr int D = 32 * M;
-  const int half = R / 2;
-  float a[NC][4];
-  float ss = 0.f;
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int d0 = 4 * (lane + 32 * k);
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d0 < D) t = *reinterpret_cast<const float4*>(x + d0);
-    a[k][0] = t.x; a[k][1] = t.y; a[k][2] = t.z; a[k][3] = t.w;
-    ss = fmaf(t.x, t.x, fmaf(t.y, t.y, fmaf(t.z, t.z, fmaf(t.w, t.w, ss))));
-  }
-  // y = a c + b s, b the rotary partner. Without a norm its error is below four roundings of
-  // 2^-24 of the larger of a and b (the products' and the sum's); with one, below sixteen of
-  // either: at most nine in the sum of squares, halved by the root, and one each in the
-  // quotient, the root, its reciprocal and two products come on top.
-  float inv = 1.f, unit = 0x1p-22f;
+  load_row<M>(x, at, y);
+  // Without a norm y's error is below four roundings of 2^-24 of the larger of a and b (the
+  // products' and the sum's); with one, below sixteen of either: at most nine in the sum of
+  // squares, halved by the root, and one each in the quotient, the root, its reciprocal and
+  // two products come on top.
+  float unit = 0x1p-22f;
   if (nw) {
-    inv = 1.0f / sqrtf(warp_sum(ss) / static_cast<float>(D) + eps);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+    const float inv = 1.0f / sqrtf(q4::row_sum<M>(ss, lane) / static_cast<float>(32 * M) + eps);
     unit = 0x1p-19f;
-  }
+    float wo[8];
+    load_row<M>(nw, at, wo);
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int d0 = 4 * (lane + 32 * k);
-    float b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (nw && d0 < D) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(nw + d0));
-      a[k][0] = a[k][0] * inv * w.x; a[k][1] = a[k][1] * inv * w.y;
-      a[k][2] = a[k][2] * inv * w.z; a[k][3] = a[k][3] * inv * w.w;
+    for (int e = 0; e < 8; ++e) {
+      y[e] = y[e] * inv * wo[e];
+      b[e] = b[e] * inv * w[e];
     }
-    if (d0 < R) {
-      if (half % 4 == 0) {
-        const int p = d0 < half ? d0 + half : d0 - half;
-        const float4 o = *reinterpret_cast<const float4*>(x + p);
-        b[0] = o.x; b[1] = o.y; b[2] = o.z; b[3] = o.w;
-        if (nw) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(nw + p));
-          b[0] = b[0] * inv * w.x; b[1] = b[1] * inv * w.y;
-          b[2] = b[2] * inv * w.z; b[3] = b[3] * inv * w.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int d = d0 + e, p = d < half ? d + half : d - half;
-          if (d < R) b[e] = nw ? x[p] * inv * __ldg(nw + p) : x[p];
-        }
-      }
-    }
-    float mag = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[k][e] = fmaf(a[k][e], c[k][e], b[e] * s[k][e]);
-      mag = fmaxf(mag, fmaxf(fabsf(a[k][e]), fabsf(b[e])));
-    }
-    err[k] = mag * unit;
   }
-}
-
-// A lane's quads of a row as they are.
-template <int M, int NC>
-__device__ __forceinline__ void plain_quads(const float* x, int lane, float (&y)[NC][4]) {
+  float mag = 0.f;
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int d0 = 4 * (lane + 32 * k);
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d0 < 32 * M) t = *reinterpret_cast<const float4*>(x + d0);
-    y[k][0] = t.x; y[k][1] = t.y; y[k][2] = t.z; y[k][3] = t.w;
+  for (int e = 0; e < 8; ++e) {
+    mag = fmaxf(mag, fmaxf(fabsf(y[e]), fabsf(b[e])));
+    y[e] = fmaf(y[e], c[e], b[e] * s[e]);
   }
+  return mag * unit;
 }
 
 // Blocks of the row passes: four warps and up to sixteen rows, so that several are in
@@ -202,70 +186,56 @@ __device__ __forceinline__ Target append_target(const AppendQ4Job& j, const RowA
   return t;
 }
 
-// One row by one warp: x, v the raw rows (any memory); the record goes to rec (any memory)
-// unless it is nullptr, the rotated key to k_out unless that is. Groups whose rounding fp32
-// cannot settle are noted in later[0 .. 3] (their lanes, key then value) for a second pass,
-// or with later == nullptr done at once.
-template <int M, bool ROT>
-__device__ __forceinline__ void append_row(const AppendQ4Job& j, const float* x, const float* v,
-                                           long angle, uint8_t* rec, float* k_out, int lane,
-                                           uint32_t* later) {
+// A warp's rows, side by side: each lane's own row x, v (raw) and angles tab in any memory;
+// its record goes to rec (any memory) unless that is nullptr, the rotated key to k_out
+// unless that is. Every lane of the warp calls it; those without a row pass on = false and
+// any row's pointers. Groups whose rounding fp32 cannot settle come back as their lanes:
+// (key, value).
+template <int M, int ROPE>
+__device__ __forceinline__ uint2 append_rows(const AppendQ4Job& j, const float* x, const float* v,
+                                             const float2* tab, uint8_t* rec, float* k_out,
+                                             const q4::Lanes<M>& at, int lane, bool on) {
   using namespace q4;
-  constexpr int D = 32 * M, NC = quads_per_lane(M);
-  const float2* tab = ROT ? j.table + angle * (j.R / 2) : nullptr;
-  const float* nw = ROT ? j.norm_w : nullptr;
-  float y[NC][4], err[NC], c[NC][4], s[NC][4];
-  uint32_t q[NC], doubt[NC];
-  auto settle = [&](int part) {
-    const uint2 d = make_uint2(doubt[0], NC > 1 ? doubt[NC - 1] : 0u);
-    store_part<M>(rec, part, q, lane);
-    if (later) {
-      if (lane == 0) *reinterpret_cast<uint2*>(later + 2 * part) = d;
-    } else if (d.x | d.y) {
-      quantise_exact<M>(part ? v : x, part ? nullptr : tab, j.R, part ? nullptr : nw, j.norm_eps,
-                        lane, d, rec, part);
-    }
-  };
-  if (ROT) load_angles<M>(tab, j.R, lane, c, s);           // on their way while v is done
-  if (rec) {
-    plain_quads<M>(v, lane, y);
-    quantise_fast<NC, true>(y, err, q, doubt);
-    settle(1);
+  float y[8];
+  uint32_t codes, scale;
+  bool doubt;
+  uint2 r;
+  load_row<M>(v, at, y);
+  doubt = quantise_fast<true>(y, 0.f, codes, scale);
+  if (on && rec) {
+    store_codes<M>(rec, 1, codes, scale, at);
+    constexpr int pad = (record_bytes(M) - 36 * M) / 4;   // zero padding
+    if (pad > 0 && at.l < pad) *reinterpret_cast<uint32_t*>(rec + 36 * M + 4 * at.l) = 0;
   }
-  if (ROT)
-    rotate_quads<M>(x, c, s, j.R, nw, j.norm_eps, lane, y, err);
-  else
-    plain_quads<M>(x, lane, y);
-  if (rec) {
-    quantise_fast<NC, !ROT>(y, err, q, doubt);
-    settle(0);
+  r.y = __ballot_sync(0xffffffffu, doubt && on && rec);
+  if (ROPE != kNoRope) {
+    const float err = rotate_row<M, ROPE>(x, tab, j.R, j.norm_w, j.norm_eps, at, lane, y);
+    doubt = quantise_fast<false>(y, err, codes, scale);
+  } else {
+    load_row<M>(x, at, y);
+    doubt = quantise_fast<true>(y, 0.f, codes, scale);
   }
-  if (k_out) {
-    __syncwarp();                            // in place: every lane has read its partners
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int d0 = 4 * (lane + 32 * k);
-      if (d0 < D)
-        *reinterpret_cast<float4*>(k_out + d0) = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
-    }
-  }
+  if (on && rec) store_codes<M>(rec, 0, codes, scale, at);
+  r.x = __ballot_sync(0xffffffffu, doubt && on && rec);   // also: every lane has read its partners
+  if (on && k_out) store_row<M>(k_out, at, y);
+  return r;
 }
 
 // Rows of k and v through shared memory: a block bulk-copies `tr` consecutive rows of each
-// (rows are contiguous whatever L is), its warps quantise them row by row into records in
-// shared memory, and the records leave in 16-byte pieces. The bytes in flight are then
-// bounded by shared memory, not by registers. Rows come in segments of seg_rows (the whole
-// tensor, or, of a chunk longer than its ring, the last rows of each head), seg_tiles blocks
-// each.
-template <int M, bool ROT>
-__global__ void __launch_bounds__(kRowThreads, M <= 4 ? 6 : 4) append_q4_kernel(AppendQ4Job j, int tr, long seg_rows,
-                                                        int seg_tiles) {
+// (rows are contiguous whatever L is), its warps quantise them into records in shared memory,
+// and the records leave in 16-byte pieces. The bytes in flight are then bounded by shared
+// memory, not by registers. Rows come in segments of seg_rows (the whole tensor, or, of a
+// chunk longer than its ring, the last rows of each head), seg_tiles blocks each.
+template <int M, int ROPE>
+__global__ void __launch_bounds__(kRowThreads, 6) append_q4_kernel(AppendQ4Job j, int tr,
+                                                                   long seg_rows, int seg_tiles) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16;
+  constexpr int RW = q4::Lanes<M>::kRows, kWarps = kRowThreads / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full;
   __shared__ int abort_flag;
   __shared__ Target to[kMaxRows];
-  __shared__ __align__(8) uint32_t later[kMaxRows][4];
+  __shared__ uint2 later[kMaxRows];
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long seg = blockIdx.x / seg_tiles;
@@ -286,7 +256,7 @@ __global__ void __launch_bounds__(kRowThreads, M <= 4 ? 6 : 4) append_q4_kernel(
     tc::bulk_load(xv, j.v + row0 * D, bytes, &full);
   }
   if (warp == 1 && lane < n)                 // meanwhile: where the rows go
-    to[lane] = append_target<M, ROT>(
+    to[lane] = append_target<M, ROPE != kNoRope>(
         j, row_at(row0 + lane, static_cast<long>(j.B) * j.Hkv * j.L, j.Hkv, j.L), true);
   __syncthreads();
   if (!tc::mbar_wait(&full, 0, &abort_flag)) abort_flag = 1;
@@ -295,26 +265,34 @@ __global__ void __launch_bounds__(kRowThreads, M <= 4 ? 6 : 4) append_q4_kernel(
     if (threadIdx.x == 0) report(j.status, ATTN_DEV_TIMEOUT);
     return;
   }
-  for (int i = warp; i < n; i += kRowThreads / 32) {
+  const q4::Lanes<M> at(lane);
+  for (int i0 = warp * RW; i0 < n; i0 += kWarps * RW) {
+    const int i = min(i0 + at.row, n - 1);   // lanes past the last row follow it
     const Target t = to[i];
-    if (t.ok && (t.rec || j.k_out))
-      append_row<M, ROT>(j, xk + i * D, xv + i * D, t.angle, t.rec ? recs + i * REC : nullptr,
-                         j.k_out ? j.k_out + (row0 + i) * D : nullptr, lane, later[i]);
+    const bool on = at.in && i0 + at.row < n && t.ok;
+    const uint2 d = append_rows<M, ROPE>(
+        j, xk + i * D, xv + i * D, ROPE != kNoRope && t.ok ? j.table + t.angle * (j.R / 2) : j.table,
+        t.rec ? recs + i * REC : nullptr, j.k_out ? j.k_out + (row0 + i) * D : nullptr, at, lane, on);
+    if (at.in && at.l == 0 && i0 + at.row < n) {
+      const int sh = at.row * 4 * M;
+      const uint32_t mask = M == 8 ? 0xffffffffu : (1u << (4 * M & 31)) - 1u;
+      later[i] = make_uint2(d.x >> sh & mask, d.y >> sh & mask);
+    }
   }
   // Second pass, rarely anything: kept out of the loop above, whose registers a call there
-  // would have cost (and 6 us at 4 x 2048 tokens). A row's second
-  // pass is its own warp's.
+  // would have cost. A row's second pass is its own warp's.
   __syncwarp();
-  for (int i = warp; i < n; i += kRowThreads / 32) {
-    if (!to[i].rec) continue;
 #pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-      const uint2 d = *reinterpret_cast<const uint2*>(&later[i][2 * part]);
-      if (!(d.x | d.y)) continue;
-      const bool rot = ROT && part == 0;
-      q4::quantise_exact<M>((part ? xv : xk) + i * D,
-                            rot ? j.table + to[i].angle * (j.R / 2) : nullptr, j.R,
-                            rot ? j.norm_w : nullptr, j.norm_eps, lane, d, recs + i * REC, part);
+  for (int i0 = warp * RW; i0 < n; i0 += kWarps * RW) {
+#pragma unroll 1
+    for (int i = i0; i < min(i0 + RW, n); ++i) {
+      const uint2 d = later[i];
+      const bool rot = ROPE != kNoRope;
+      if (d.x)
+        q4::quantise_exact<M>(xk + i * D, rot ? j.table + to[i].angle * (j.R / 2) : nullptr, j.R,
+                              rot ? j.norm_w : nullptr, j.norm_eps, lane, d.x, recs + i * REC, 0);
+      if (d.y)
+        q4::quantise_exact<M>(xv + i * D, nullptr, 0, nullptr, 0.f, lane, d.y, recs + i * REC, 1);
     }
   }
   __syncthreads();
@@ -326,10 +304,10 @@ __global__ void __launch_bounds__(kRowThreads, M <= 4 ? 6 : 4) append_q4_kernel(
 }
 
 // Records back to fp32: a block brings `tr` rows' records to shared memory in 16-byte
-// pieces, then a warp per row writes four dims of key and value per lane.
+// pieces, then its warps write eight dims of key and value per lane.
 template <int M>
 __global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int tr) {
-  constexpr int D = 32 * M, NC = quads_per_lane(M), REC = q4::record_bytes(M), P = REC / 16;
+  constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16, RW = q4::Lanes<M>::kRows;
   __shared__ __align__(16) uint8_t recs[kMaxRows * REC];
   __shared__ const uint8_t* from[kMaxRows];
   if (gated_off(j.skip)) return;
@@ -359,69 +337,62 @@ __global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int t
       reinterpret_cast<uint4*>(recs)[p] = reinterpret_cast<const uint4*>(from[i])[p - i * P];
   }
   __syncthreads();
-  for (int i = warp; i < n; i += kRowThreads / 32) {
-    if (!from[i]) continue;
+  const q4::Lanes<M> at(lane);
+  for (int i0 = warp * RW; i0 < n; i0 += kRowThreads / 32 * RW) {
+    const int i = i0 + at.row;
+    if (!at.in || i >= n || !from[i]) continue;
     const uint8_t* rec = recs + i * REC;
-    const long row = row0 + i;
+    const uint16_t* sc = reinterpret_cast<const uint16_t*>(rec + 32 * M);
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int ch = lane + 32 * k;
-      if (ch >= 8 * M) continue;
-      const int g = ch >> 3, e = ch & 7;
+    for (int part = 0; part < 2; ++part) {
+      const float s = q4::bf16_to_float(sc[part * M + at.g]);
+      float y[8];
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const int off = part ? 16 * M + 2 * (e * M + g) : 4 * ((e >> 1) * M + g) + 2 * (e & 1);
-        const uint32_t c = *reinterpret_cast<const uint16_t*>(rec + off);
-        const float s = q4::bf16_to_float(
-            *reinterpret_cast<const uint16_t*>(rec + (32 + 2 * part) * M + 2 * g));
-        // 2^23 + u, less 2^23 + 8
-        auto value = [&](uint32_t u) {
-          return (__uint_as_float(0x4b000000u | (u & 15u)) - 8388616.0f) * s;
-        };
-        const float4 y = make_float4(value(c), value(c >> 4), value(c >> 8), value(c >> 12));
-        *reinterpret_cast<float4*>((part ? j.v : j.k) + row * D + 4 * ch) = y;
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t u =
+            *reinterpret_cast<const uint16_t*>(rec + q4::quad_at<M>(part, at.g, at.quad(q)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)          // 2^23 + code + 8, less 2^23 + 8
+          y[4 * q + e] = (__uint_as_float(0x4b000000u | (u >> (4 * e) & 15u)) - 8388616.0f) * s;
       }
+      store_row<M>((part ? j.v : j.k) + (row0 + i) * D, at, y);
     }
   }
 }
 
-// A step's first pass: a warp per row, the q rows (normed, rotated, fp32) first, then
-// the k and v rows.
-template <int M>
-__global__ void __launch_bounds__(256) prep_q4_kernel(PrepQ4Job j) {
+// A step's first pass, a warp per row (its first 4 M lanes): the q rows (normed, rotated,
+// fp32) first, then the k and v rows.
+template <int M, int ROPE>
+__global__ void __launch_bounds__(128) prep_q4_kernel(PrepQ4Job j) {
   if (gated_off(j.kv.skip)) return;
-  constexpr int D = 32 * M, NC = quads_per_lane(M);
+  constexpr int D = 32 * M;
   const AppendQ4Job& a = j.kv;
   const int lane = threadIdx.x & 31;
+  q4::Lanes<M> at(lane);
+  at.in = at.in && at.row == 0;
   const long qrows = static_cast<long>(a.B) * j.H, kvrows = static_cast<long>(a.B) * a.Hkv;
-  const long step = static_cast<long>(gridDim.x) * 8;
-  for (long row = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32; row < qrows + kvrows;
-       row += step) {
-    if (row >= qrows) {
-      const RowAt at = row_at(row - qrows, kvrows, a.Hkv, 1);
-      const Target t = append_target<M, true>(a, at, lane == 0);
-      if (t.ok)
-        append_row<M, true>(a, a.k + at.bh * D, a.v + at.bh * D, t.angle, t.rec, nullptr, lane,
-                            nullptr);
-      continue;
-    }
-    const int b = static_cast<int>(row / j.H);
-    const int s0 = a.start[b], p0 = a.pos ? a.pos[b] : s0;
-    const bool ok = s0 >= 0 && p0 >= 0 && p0 < a.max_positions &&
-                    (a.window > 0 || s0 < a.capacity);
-    if (row % j.H == 0 && lane == 0) j.cache_len[b] = ok ? s0 + 1 : 0;
-    if (!ok) continue;                       // the row's key rows report it
-    float y[NC][4], err[NC], c[NC][4], s[NC][4];
-    load_angles<M>(a.table + static_cast<long>(p0) * (a.R / 2), a.R, lane, c, s);
-    rotate_quads<M>(j.q + row * D, c, s, a.R, j.q_norm_w, a.norm_eps, lane, y, err);
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int d0 = 4 * (lane + 32 * k);
-      if (d0 < D)
-        *reinterpret_cast<float4*>(j.qrot + row * D + d0) =
-            make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
-    }
+  const long row = static_cast<long>(blockIdx.x) * 4 + threadIdx.x / 32;
+  if (row >= qrows + kvrows) return;
+  if (row >= qrows) {
+    const RowAt r = row_at(row - qrows, kvrows, a.Hkv, 1);
+    const Target t = append_target<M, true>(a, r, lane == 0);
+    if (!t.ok) return;
+    const float *x = a.k + r.bh * D, *v = a.v + r.bh * D;
+    const float2* tab = a.table + t.angle * (a.R / 2);
+    const uint2 d = append_rows<M, ROPE>(a, x, v, tab, t.rec, nullptr, at, lane, at.in);
+    if (d.x) q4::quantise_exact<M>(x, tab, a.R, a.norm_w, a.norm_eps, lane, d.x, t.rec, 0);
+    if (d.y) q4::quantise_exact<M>(v, nullptr, 0, nullptr, 0.f, lane, d.y, t.rec, 1);
+    return;
   }
+  const int b = static_cast<int>(row / j.H);
+  const int s0 = a.start[b], p0 = a.pos ? a.pos[b] : s0;
+  const bool ok = s0 >= 0 && p0 >= 0 && p0 < a.max_positions && (a.window > 0 || s0 < a.capacity);
+  if (row % j.H == 0 && lane == 0) j.cache_len[b] = ok ? s0 + 1 : 0;
+  if (!ok) return;                           // the row's key rows report it
+  float y[8];
+  rotate_row<M, ROPE>(j.q + row * D, a.table + static_cast<long>(p0) * (a.R / 2), a.R, j.q_norm_w,
+                      a.norm_eps, at, lane, y);
+  if (at.in) store_row<M>(j.qrot + row * D, at, y);
 }
 
 // ---------------------------------------------------------------- eviction
@@ -598,27 +569,22 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j) {
   }
 }
 
-unsigned row_blocks(long rows) {
-  const long blocks = (rows + 7) / 8;
-  return static_cast<unsigned>(blocks < 152L * 64 ? blocks : 152L * 64);
-}
-
 }  // namespace
 
 namespace {
-template <int M, bool ROT>
+template <int M, int ROPE>
 cudaError_t launch_append(const AppendQ4Job& j, int tr, long seg_rows, int seg_tiles, unsigned grid,
                           cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   const cudaError_t e = allowed.get(
       [] {
-        return cudaFuncSetAttribute(append_q4_kernel<M, ROT>,
+        return cudaFuncSetAttribute(append_q4_kernel<M, ROPE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kMaxRows * (256 * M + q4::record_bytes(M)));
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  append_q4_kernel<M, ROT><<<grid, kRowThreads, tr * (256 * M + q4::record_bytes(M)), stream>>>(
+  append_q4_kernel<M, ROPE><<<grid, kRowThreads, tr * (256 * M + q4::record_bytes(M)), stream>>>(
       j, tr, seg_rows, seg_tiles);
   return cudaGetLastError();
 }
@@ -640,8 +606,10 @@ cudaError_t launch_append_q4(const AppendQ4Job& job, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(tiles * segs);
   return with_groups(j.D / 32, [&](auto g) {
     constexpr int M = decltype(g)::value;
-    return j.table ? launch_append<M, true>(j, tr, seg_rows, static_cast<int>(tiles), grid, stream)
-                   : launch_append<M, false>(j, tr, seg_rows, static_cast<int>(tiles), grid, stream);
+    const int t = static_cast<int>(tiles);
+    if (!j.table) return launch_append<M, kNoRope>(j, tr, seg_rows, t, grid, stream);
+    return j.R % 8 == 0 ? launch_append<M, kRopeQuads>(j, tr, seg_rows, t, grid, stream)
+                        : launch_append<M, kRopeDims>(j, tr, seg_rows, t, grid, stream);
   });
 }
 
@@ -658,9 +626,14 @@ cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream) {
 }
 
 cudaError_t launch_prep_q4(const PrepQ4Job& j, cudaStream_t stream) {
-  const unsigned grid = row_blocks(static_cast<long>(j.kv.B) * (j.H + j.kv.Hkv));
+  const long rows = static_cast<long>(j.kv.B) * (j.H + j.kv.Hkv);
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
   return with_groups(j.kv.D / 32, [&](auto g) {
-    prep_q4_kernel<decltype(g)::value><<<grid, 256, 0, stream>>>(j);
+    constexpr int M = decltype(g)::value;
+    if (j.kv.R % 8 == 0)
+      prep_q4_kernel<M, kRopeQuads><<<grid, 128, 0, stream>>>(j);
+    else
+      prep_q4_kernel<M, kRopeDims><<<grid, 128, 0, stream>>>(j);
     return cudaGetLastError();
   });
 }

@@ -27,10 +27,47 @@ constexpr uint32_t kNanScale = 0x7fc0u;   // a group that held an inf or NaN: re
 
 __device__ __forceinline__ float bf16_to_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-__device__ __forceinline__ uint32_t group_max_u(uint32_t v) {      // over 8 aligned lanes
+// A warp's rows: four lanes a group, two quads of dims each, 4 M lanes a row, so one to eight
+// rows side by side. Lane a of group g holds quads a and a + 4 of the group's eight, in odd
+// groups the other way round: eight lanes' 16-byte accesses then meet all banks, and the
+// lanes of a group always touch 64 bytes in a row.
+template <int M>
+struct Lanes {
+  static constexpr int kRows = 32 / (4 * M);              // rows of a warp
+  int row, l, g, q0;                                      // l: lane of the row
+  bool in;                                                // whether the lane has a row
+  __device__ __forceinline__ explicit Lanes(int lane) {
+    row = lane / (4 * M);
+    in = row < kRows;
+    l = lane - row * 4 * M;
+    g = l >> 2;
+    q0 = (l & 3) + 4 * (g & 1);
+  }
+  __device__ __forceinline__ int quad(int i) const { return i ? q0 ^ 4 : q0; }
+  __device__ __forceinline__ int dim(int i) const { return 32 * g + 4 * quad(i); }
+};
+
+__device__ __forceinline__ uint32_t group_max_u(uint32_t v) {      // over 4 aligned lanes
   v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
-  return max(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  return max(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+// Sum over a row's 4 M lanes.
+template <int M>
+__device__ __forceinline__ float row_sum(float v, int lane) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  if constexpr ((M & (M - 1)) == 0) {
+#pragma unroll
+    for (int o = 4; o < 4 * M; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  } else {
+    const int base = lane - lane % (4 * M);
+    float t = 0.f;
+#pragma unroll
+    for (int g = 0; g < M; ++g) t += __shfl_sync(0xffffffffu, v, min(base + 4 * g, 31));
+    return t;
+  }
 }
 
 __device__ __forceinline__ double warp_sum_d(double v) {
@@ -39,79 +76,70 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
-// Four neighbouring dims quantised: their codes in the low 16 bits, their group's scale (the
-// same on the group's 8 lanes) in the high ones.
-
 // t in (-2^21, 2^21) to the nearest integer, ties to even, as the sum's low bits: the float
 // 1.5 * 2^23 + 8 + t is rounded at its unit place. Its low four bits are then t's code + 8.
 constexpr float kRound = 12582920.0f;
 
-// Quantises a row held as quads y[k] (dims 4 (lane + 32 k) .. + 3; zeros where there are
-// none), each off from the exact values by at most err[k]; a group is 8 aligned lanes. The
-// scale is bf16(max|y| / 7), the code rint(y / scale), ties to even. doubt[k] gets the lanes
-// (warp-uniform) whose roundings were not further from their borders than the error: their
-// groups have to be done again by quantise_exact. EXACT: y is the row itself, err is not
-// read. Every lane of the warp must call it. About six instructions a value.
-template <int NC, bool EXACT>
-__device__ __forceinline__ void quantise_fast(const float (&y)[NC][4], const float (&err)[NC],
-                                              uint32_t (&out)[NC], uint32_t (&doubt)[NC]) {
+// Quantises a lane's two quads y, four lanes a group, each value off from the
+// exact one by at most err: the scale is bf16(max|y| / 7), the code rint(y / scale), ties to
+// even. Returns whether a rounding was not further from its border than the error: the
+// group has to be done again by quantise_exact. EXACT: y is exact, err is not read. Every
+// lane of the warp must call it. About six instructions a value.
+template <bool EXACT>
+__device__ __forceinline__ bool quantise_fast(const float (&y)[8], float err, uint32_t& codes,
+                                              uint32_t& scale) {
+  float big = 0.f;                           // a NaN stays one, and its bits are above inf's
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    uint32_t top = 0;
+  for (int e = 0; e < 8; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(big) : "f"(fabsf(y[e])));
+  const uint32_t top = group_max_u(__float_as_uint(big));
+  const uint32_t far = EXACT ? 0u : group_max_u(__float_as_uint(err));
+  const float amax = __uint_as_float(top), ferr = __uint_as_float(far);
+  // amax / 7 to two roundings; far from a bf16 border that settles the scale
+  const float a7 = amax * (1.0f / 7.0f);
+  const uint32_t bits = __float_as_uint(a7);
+  const float mid = __uint_as_float((bits & 0xffff0000u) | 0x8000u);
+  scale = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
+  float rs;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(bf16_to_float(scale)));
+  // t = y / scale is off by err / scale, by 2^-23 of at most 7.04 in rs and by its rounding
+  const float near = 0.5f - (EXACT ? 0x1p-19f : fmaf(err, rs, 0x1p-19f));
+  uint32_t b[8];
+  float off = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(y[k][e]) & 0x7fffffffu);
-    top = group_max_u(top);                               // NaN above inf above the rest
-    const uint32_t far = EXACT ? 0u : group_max_u(__float_as_uint(err[k]));
-    const float amax = __uint_as_float(top), ferr = __uint_as_float(far);
-    // amax / 7 to two roundings; far from a bf16 border that settles the scale
-    const float a7 = amax * (1.0f / 7.0f);
-    const uint32_t bits = __float_as_uint(a7);
-    const float mid = __uint_as_float((bits & 0xffff0000u) | 0x8000u);
-    const uint32_t sc = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
-    float rs;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(bf16_to_float(sc)));
-    // t = y / scale is off by err / scale, by 2^-23 of at most 7.04 in rs and by its rounding
-    const float near = 0.5f - (EXACT ? 0x1p-19f : fmaf(err[k], rs, 0x1p-19f));
-    uint32_t b[4];
-    float off = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float t = y[k][e] * rs, u = t + kRound;
-      b[e] = __float_as_uint(u);
-      off = fmaxf(off, fabsf(t - (u - kRound)));
-    }
-    // the four floats' high bits cancel below bit 16
-    out[k] = ((b[0] + 16u * b[1] + 256u * b[2] + 4096u * b[3]) & 0xffffu) | sc << 16;
-    bool unsure = a7 < 0x1p-120f || fabsf(a7 - mid) <= fmaf(ferr, 0.15f, a7 * 0x1p-22f) || off >= near;
-    if (max(top, far) >= 0x7f800000u || (top | far) == 0) {   // inf or NaN; all zero
-      out[k] = 0x8888u | ((top | far) == 0 ? 0u : kNanScale << 16);
-      unsure = false;
-    }
-    doubt[k] = __ballot_sync(0xffffffffu, unsure);
+  for (int e = 0; e < 8; ++e) {
+    const float t = y[e] * rs, u = t + kRound;
+    b[e] = __float_as_uint(u);
+    off = fmaxf(off, fabsf(t - (u - kRound)));
   }
+  // four codes a sum: the floats' high bits cancel below bit 16
+  const uint32_t lo = b[0] + 16u * b[1] + 256u * b[2] + 4096u * b[3];
+  const uint32_t hi = b[4] + 16u * b[5] + 256u * b[6] + 4096u * b[7];
+  codes = __byte_perm(lo, hi, 0x5410);
+  const bool special = max(top, far) >= 0x7f800000u || (top | far) == 0;   // inf, NaN; zeros
+  if (special) {
+    codes = 0x88888888u;
+    scale = (top | far) == 0 ? 0u : kNanScale;
+  }
+  return !special && (a7 < 0x1p-120f || fabsf(a7 - mid) <= fmaf(ferr, 0.15f, a7 * 0x1p-22f) ||
+                      off >= near);
 }
 
-// Quad e of group g into the key part (part = 0) or value part (1) of the record at rec.
+// Quad q of group g at 16 bits of codes, in the key part (part = 0) or the value part (1) of
+// a record.
 template <int M>
-__device__ __forceinline__ void store_quad(uint8_t* rec, int part, uint32_t q, int g, int e) {
-  const int at = part ? 16 * M + 2 * (e * M + g) : 4 * ((e >> 1) * M + g) + 2 * (e & 1);
-  *reinterpret_cast<uint16_t*>(rec + at) = static_cast<uint16_t>(q);
-  if (e == 0)
-    *reinterpret_cast<uint16_t*>(rec + (32 + 2 * part) * M + 2 * g) = static_cast<uint16_t>(q >> 16);
+__device__ __forceinline__ int quad_at(int part, int g, int q) {
+  return part ? 16 * M + 2 * (q * M + g) : 4 * ((q >> 1) * M + g) + 2 * (q & 1);
 }
 
-// A lane's quads of a row.
-template <int M, int NC>
-__device__ __forceinline__ void store_part(uint8_t* rec, int part, const uint32_t (&q)[NC], int lane) {
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int ch = lane + 32 * k;
-    if (ch < 8 * M) store_quad<M>(rec, part, q[k], ch >> 3, ch & 7);
-  }
-  if (part == 1) {                                      // zero padding
-    constexpr int pad = (record_bytes(M) - 36 * M) / 2;
-    if (pad > 0 && lane < pad) *reinterpret_cast<uint16_t*>(rec + 36 * M + 2 * lane) = 0;
-  }
+// A lane's codes (its quads' in the low and high half) and its group's scale into a record.
+template <int M>
+__device__ __forceinline__ void store_codes(uint8_t* rec, int part, uint32_t codes, uint32_t scale,
+                                            const Lanes<M>& at) {
+  *reinterpret_cast<uint16_t*>(rec + quad_at<M>(part, at.g, at.quad(0))) = static_cast<uint16_t>(codes);
+  *reinterpret_cast<uint16_t*>(rec + quad_at<M>(part, at.g, at.quad(1))) =
+      static_cast<uint16_t>(codes >> 16);
+  if ((at.l & 3) == 0)
+    *reinterpret_cast<uint16_t*>(rec + (32 + 2 * part) * M + 2 * at.g) = static_cast<uint16_t>(scale);
 }
 
 // 1 / rms of a row in fp64.
@@ -123,23 +151,23 @@ __device__ __noinline__ double exact_inv_rms(const float* x, float eps, int D, i
   return 1.0 / sqrt(warp_sum_d(ss) / D + static_cast<double>(eps));
 }
 
-// The doubtful groups (doubt: quantise_fast's lanes, of quads 0 .. 31 and 32 .. 63) of the raw
-// row x again, in fp64, into part `part` of the record at rec: y = RoPE(RMSNorm(x)) with the
-// row's (cos, sin) table tab (NULL: no rotation) and norm weights nw (NULL: none), a group at
-// a time, one dim per lane. No quotient is formed: fp32 proposes the scale and the codes, and
-// exact products with the borders next to them decide. A few rows in a thousand come here
-// (with a norm about one in a hundred); kept short, since its instructions are not in the
-// cache then (unrolled over a row, the first use on an SM took 3 us).
+// The doubtful groups of the raw row x (doubt: four bits a group, any set) again, in fp64,
+// into part `part` of the record at rec: y = RoPE(RMSNorm(x)) with the row's (cos, sin)
+// table tab (NULL: no rotation) and norm weights nw (NULL: none), a group at a time, one dim
+// per lane. No quotient is formed: fp32 proposes the scale and the codes, and exact products
+// with the borders next to them decide. A few rows in a thousand come here (with a norm
+// about one in a hundred); kept short, since its instructions are not in the cache then
+// (unrolled over a row, the first use on an SM took 3 us).
 template <int M>
 __device__ __noinline__ void quantise_exact(const float* x, const float2* tab, int R,
-                                            const float* nw, float eps, int lane, uint2 doubt,
+                                            const float* nw, float eps, int lane, uint32_t doubt,
                                             uint8_t* rec, int part) {
   constexpr int D = 32 * M;
   const double inv = nw ? exact_inv_rms<>(x, eps, D, lane) : 1.0;
   const int half = R / 2;
 #pragma unroll 1
   for (int g = 0; g < M; ++g) {
-    if (!((g < 4 ? doubt.x : doubt.y) >> (8 * (g & 3)) & 0xffu)) continue;
+    if (!(doubt >> (4 * g) & 15u)) continue;
     const int d = 32 * g + lane;
     double y = x[d];
     if (nw) y = y * inv * nw[d];
@@ -171,12 +199,14 @@ __device__ __noinline__ void quantise_exact(const float* x, const float2* tab, i
     else if (rest < -border || (rest == -border && (c & 1)))
       --c;
     c = sc ? max(-7, min(7, c)) : 0;
-    // back to quads: lane l of the group's eight takes dims 4 (l % 8) .. + 3
+    // four lanes' codes make a quad
     uint32_t codes = static_cast<uint32_t>(c + 8) << (4 * (lane & 3));
     codes |= __shfl_xor_sync(0xffffffffu, codes, 1);
     codes |= __shfl_xor_sync(0xffffffffu, codes, 2);
-    codes = __shfl_sync(0xffffffffu, codes, 4 * (lane & 7));
-    if (lane >> 3 == (g & 3)) store_quad<M>(rec, part, codes | sc << 16, g, lane & 7);
+    if ((lane & 3) == 0)
+      *reinterpret_cast<uint16_t*>(rec + quad_at<M>(part, g, lane >> 2)) = static_cast<uint16_t>(codes);
+    if (lane == 0)
+      *reinterpret_cast<uint16_t*>(rec + (32 + 2 * part) * M + 2 * g) = static_cast<uint16_t>(sc);
   }
 }
 
