@@ -51,6 +51,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 32;                    // keys per tile
 constexpr int kWarps = 4;
 
+// A kernel launched dependent on the one before it waits here for that one's
+// end and its writes; the one before says early that the next may be set up.
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_may_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -143,11 +150,17 @@ __device__ __forceinline__ float unit_scale(uint32_t w, int odd) {     // bf16 h
   return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
 }
 
-__host__ __device__ constexpr int stages(int M) { return M <= 4 ? 3 : 2; }
+constexpr int kStages = 2;
+
+// Blocks an SM holds: what the registers leave (116 at D = 128 with one column tile, 162
+// with two).
+__host__ __device__ constexpr int resident_blocks(int M, int NT) {
+  return M > 4 ? 2 : (NT == 1 ? 4 : 3);
+}
 
 // Rings of all warps, then the queries' B fragments.
 constexpr size_t split_smem(int M, int NT) {
-  return static_cast<size_t>(kWarps) * stages(M) * kTile * q4::record_bytes(M) + 512 * M * NT;
+  return static_cast<size_t>(kWarps) * kStages * kTile * q4::record_bytes(M) + 512 * M * NT;
 }
 
 // Live slots of row b (0: the row is invalid).
@@ -162,9 +175,9 @@ __device__ __forceinline__ int live_slots(const DecodeQ4Job& j, int b, bool lead
 
 // One block: up to 4 NT query heads of one kv head over the slots [split chunk, + chunk).
 template <int M, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(DecodeQ4Job j) {
+__global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4_kernel(DecodeQ4Job j) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), TILE_BYTES = kTile * REC, VW = (M + 1) / 2;
-  constexpr int kHeads = 4 * NT, kStages = stages(M);
+  constexpr int kHeads = 4 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ float q_factor[kHeads];
@@ -182,6 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   const int b = static_cast<int>(bh / j.Hkv), hkv = static_cast<int>(bh - static_cast<long>(b) * j.Hkv);
   const int nlive = live_slots(j, b, threadIdx.x == 0 && split == 0 && g0 == 0 && hkv == 0);
   const int k0 = split * j.chunk;
+  dependents_may_launch();
   if (k0 >= nlive) return;
   const int k1 = min(k0 + j.chunk, nlive);
   const int tiles = (k1 - k0 + kTile - 1) / kTile;
@@ -539,43 +553,70 @@ __global__ void __launch_bounds__(32 * kWarps, M <= 4 ? 3 : 2) decode_q4_kernel(
   }
 }
 
-// Maximum reference and sum of one query row over its ns splits, by one warp.
-__device__ __forceinline__ float2 row_ml(const float* ml, int ns, int lane) {
-  float m = -INFINITY;
-  for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[2 * s]);
-  m = warp_max(m);
-  float l = 0.f;
-  if (m != -INFINITY)
-    for (int s = lane; s < ns; s += 32) l = fmaf(ex2(ml[2 * s] - m), ml[2 * s + 1], l);
-  return make_float2(m, warp_sum(l));
-}
+constexpr int kMaxSplits = 152 * 4;          // of one row: no more than blocks on the GPU at once
 
-// Blocks [0, rows): one query row's splits merged. Blocks after: with weights, 256
-// slots of one kv head get the sum over its query heads of 2^(score - reference) / sum
-// (one thread per slot, heads in order, so the result does not depend on timing).
+// Blocks [0, rows): one query row's splits merged, a split per warp at a time. Blocks after:
+// with weights, 256 slots of one kv head get the sum over its query heads of
+// 2^(score - reference) / sum (one thread per slot, heads in order, so the result does not
+// depend on timing). Launched dependent on the split kernel: its blocks are in place before
+// that one ends.
 __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, unsigned rows,
                                                                unsigned slot_blocks) {
+  __shared__ float factor[kMaxSplits];
+  __shared__ float red[8];
+  __shared__ __align__(16) float acc[8][kMaxHeadDim];
   __shared__ float2 sh[8];
+  dependent_wait();
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* ml = j.partial + static_cast<long>(j.B) * j.H * j.nsplit * j.D;
+  const float2* ml = reinterpret_cast<const float2*>(j.partial + static_cast<long>(j.B) * j.H * j.nsplit * j.D);
   if (blockIdx.x < rows) {
-    const int b = static_cast<int>(blockIdx.x / j.H);
-    const int nlive = live_slots(j, b, false);
+    const long row = blockIdx.x;
+    const int nlive = live_slots(j, static_cast<int>(row / j.H), false);
     if (nlive <= j.chunk) return;            // finished by its one split, or invalid
     const int ns = (nlive + j.chunk - 1) / j.chunk;
-    const long row = blockIdx.x;
-    const float* rml = ml + 2 * row * j.nsplit;
-    const float2 t = row_ml(rml, ns, lane);
-    const float* part = j.partial + row * j.nsplit * j.D;
-    const int d = threadIdx.x;
-    if (d >= j.D) return;
-    float y = 0.f;
-    for (int s = 0; s < ns; ++s) {
-      const float m = rml[2 * s];
-      if (m != -INFINITY) y = fmaf(ex2(m - t.x), part[static_cast<long>(s) * j.D + d], y);
+    ml += row * j.nsplit;
+    float m = -INFINITY;
+    for (int s = threadIdx.x; s < ns; s += 256) m = fmaxf(m, ml[s].x);
+    m = warp_max(m);
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+    float l = 0.f;
+    for (int s = threadIdx.x; s < ns; s += 256) {
+      const float2 t = ml[s];
+      const float f = t.x == -INFINITY ? 0.f : ex2(t.x - m);
+      factor[s] = f;
+      l = fmaf(f, t.y, l);
     }
-    j.out[row * j.D + d] = y / t.y;
+    l = warp_sum(l);
+    __syncthreads();
+    if (lane == 0) red[warp] = l;
+    const float* part = j.partial + row * j.nsplit * j.D;
+    for (int d = 4 * lane; d < j.D; d += 128) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int s = warp; s < ns; s += 8) {
+        const float f = factor[s];
+        const float4 t = *reinterpret_cast<const float4*>(part + static_cast<long>(s) * j.D + d);
+        if (f != 0.f) {                      // 0: a split whose scores were all -inf
+          y.x = fmaf(f, t.x, y.x); y.y = fmaf(f, t.y, y.y);
+          y.z = fmaf(f, t.z, y.z); y.w = fmaf(f, t.w, y.w);
+        }
+      }
+      *reinterpret_cast<float4*>(&acc[warp][d]) = y;
+    }
+    __syncthreads();
+    if (threadIdx.x >= j.D) return;
+    float y = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      y += acc[w][threadIdx.x];
+      l += red[w];
+    }
+    j.out[row * j.D + threadIdx.x] = y / l;
     return;
   }
   const unsigned blk = blockIdx.x - rows;
@@ -587,20 +628,34 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   const int ns = (nlive + j.chunk - 1) / j.chunk;
   const int G = j.H / j.Hkv;
   const long row0 = static_cast<long>(b) * j.H + hkv * G;
-  float acc = 0.f;
+  float* w = j.weights + bh * j.capacity + n;
+  float sum = 0.f;
   for (int g0 = 0; g0 < G; g0 += 8) {
     const int heads = min(8, G - g0);
+    float s[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      s[h] = h < heads && n < nlive ? j.scores[(row0 + g0 + h) * j.pitch + n] : 0.f;
     if (warp < heads) {
-      const float2 t = row_ml(ml + 2 * (row0 + g0 + warp) * j.nsplit, ns, lane);
-      if (lane == 0) sh[warp] = make_float2(t.x, 1.0f / t.y);
+      const float2* r = ml + (row0 + g0 + warp) * j.nsplit;
+      float m = -INFINITY, l = 0.f;
+      for (int i = lane; i < ns; i += 32) {
+        const float2 t = r[i];
+        const float top = fmaxf(m, t.x);
+        if (top != -INFINITY) l = l * ex2(m - top) + ex2(t.x - top) * t.y;
+        m = top;
+      }
+      const float top = warp_max(m);
+      l = warp_sum(m == -INFINITY ? 0.f : l * ex2(m - top));
+      if (lane == 0) sh[warp] = make_float2(top, 1.0f / l);
     }
     __syncthreads();
-    if (n < nlive)
-      for (int h = 0; h < heads; ++h)
-        acc = fmaf(ex2(j.scores[(row0 + g0 + h) * j.pitch + n] - sh[h].x), sh[h].y, acc);
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < heads) sum = fmaf(ex2(s[h] - sh[h].x), sh[h].y, sum);
     __syncthreads();
   }
-  if (n < nlive) j.weights[bh * j.capacity + n] += acc;
+  if (n < nlive) *w += sum;
 }
 
 template <int M, int NT, bool W>
@@ -639,15 +694,43 @@ int eff_len(int max_cache_len, int window) {
   return window > 0 && window < max_cache_len ? window : max_cache_len;
 }
 
+// Splits a row may get, whatever its length. With few rows: one wave of blocks, as many as
+// fit, if that loads the SMs evenly (one row of 131072 slots with 8 kv heads and 8 query
+// heads each, 3 blocks an SM: 57 splits 46.8 us, 38 48.1, 76 63.8, for a second wave goes to
+// whichever SMs end first). Otherwise 10 to 20 blocks an SM, which even out rows of
+// different lengths, and of those the count that leaves the busiest SM the least extra (64
+// rows of up to 8192 slots with 8 kv heads: 1 split 86.4 us, 2 84.0, 4 76.4, 8 77.5, 16 85.2).
+int most_splits(int B, int H, int Hkv) {
+  constexpr int kSms = 152;
+  const long units = units_of(B, H, Hkv);
+  if (units < 1) return 1;
+  const long resident = kSms * resident_blocks(4, head_tiles(H, Hkv));
+  if (units <= resident) {
+    const long n = resident / units, blocks = n * units;
+    if (20 * blocks >= 19 * kSms * ((blocks + kSms - 1) / kSms)) return static_cast<int>(n);
+  }
+  long best = 1;
+  double least = 1e30;
+  for (long n = 1; n == 1 || n * units <= 20 * kSms; ++n) {
+    if (n * units < 10 * kSms && (n + 1) * units <= 20 * kSms) continue;
+    const double per = static_cast<double>(n * units) / kSms;
+    const double extra = ((n * units + kSms - 1) / kSms) / per * (1.0 + 0.004 * per);
+    if (extra < least) {
+      least = extra;
+      best = n;
+    }
+  }
+  return static_cast<int>(best);
+}
+
 // The most splits of any length up to this one: it does not shrink as the length grows.
+// Up to 16 tiles stay in one block: the second launch costs what the split saves.
 int split_bound(int B, int H, int Hkv, int max_cache_len, int window) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
-  const long units = units_of(B, H, Hkv);
-  constexpr int resident = 152 * 3;          // blocks on the GPU at once
-  const long want = units >= resident ? (4 * resident + units - 1) / units
-                                      : (units < 1 ? 1 : resident / units);
-  const long most = (tiles + kWarps - 1) / kWarps;            // a tile for every warp
-  return static_cast<int>(want < most ? want : most);
+  if (tiles <= 4 * kWarps) return 1;
+  const int most = (tiles + kWarps - 1) / kWarps;             // a tile for every warp
+  const int want = most_splits(B, H, Hkv);
+  return want < most ? want : most;
 }
 
 }  // namespace
@@ -710,9 +793,16 @@ cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream) {
   if (e != cudaSuccess || (j.nsplit == 1 && !j.weights)) return e;
   const unsigned rows = j.nsplit > 1 ? static_cast<unsigned>(j.B) * j.H : 0;
   const unsigned per = j.weights ? (eff_len(j.max_cache_len, j.window) - 1) / 256 + 1 : 0;
-  decode_q4_finish_kernel<<<rows + static_cast<unsigned>(j.B) * j.Hkv * per, 256, 0, stream>>>(
-      j, rows, per ? per : 1);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(rows + static_cast<unsigned>(j.B) * j.Hkv * per);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_q4_finish_kernel, j, rows, per ? per : 1u);
 }
 
 }  // namespace gqa
