@@ -51,13 +51,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 32;                    // keys per tile
 constexpr int kWarps = 4;
 
-// A kernel launched dependent on the one before it waits here for that one's
-// end and its writes; the one before says early that the next may be set up.
-__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dependents_may_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -183,6 +176,8 @@ __global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4
   __shared__ float q_factor[kHeads];
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
   __shared__ int abort_flag;
+  dependents_may_launch();
+  dependent_wait();                          // a step's first pass
   if (gated_off(j.skip)) return;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -195,7 +190,6 @@ __global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4
   const int b = static_cast<int>(bh / j.Hkv), hkv = static_cast<int>(bh - static_cast<long>(b) * j.Hkv);
   const int nlive = live_slots(j, b, threadIdx.x == 0 && split == 0 && g0 == 0 && hkv == 0);
   const int k0 = split * j.chunk;
-  dependents_may_launch();
   if (k0 >= nlive) return;
   const int k1 = min(k0 + j.chunk, nlive);
   const int tiles = (k1 - k0 + kTile - 1) / kTile;
@@ -659,7 +653,7 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
 }
 
 template <int M, int NT, bool W>
-cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, bool after_prep, cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   const cudaError_t e = allowed.get(
       [] {
@@ -669,6 +663,8 @@ cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, cudaStream_t strea
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
+  if (after_prep)
+    return launch_dependent(decode_q4_kernel<M, NT, W>, grid, 32 * kWarps, split_smem(M, NT), stream, j);
   decode_q4_kernel<M, NT, W><<<grid, 32 * kWarps, split_smem(M, NT), stream>>>(j);
   return cudaGetLastError();
 }
@@ -681,13 +677,13 @@ long units_of(int B, int H, int Hkv) {
 }
 
 template <int M>
-cudaError_t launch_split(const DecodeQ4Job& j, cudaStream_t stream) {
+cudaError_t launch_split(const DecodeQ4Job& j, bool after_prep, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(units_of(j.B, j.H, j.Hkv)) * j.nsplit;
   if (head_tiles(j.H, j.Hkv) == 1)
-    return j.weights ? launch_split<M, 1, true>(j, grid, stream)
-                     : launch_split<M, 1, false>(j, grid, stream);
-  return j.weights ? launch_split<M, 2, true>(j, grid, stream)
-                   : launch_split<M, 2, false>(j, grid, stream);
+    return j.weights ? launch_split<M, 1, true>(j, grid, after_prep, stream)
+                     : launch_split<M, 1, false>(j, grid, after_prep, stream);
+  return j.weights ? launch_split<M, 2, true>(j, grid, after_prep, stream)
+                   : launch_split<M, 2, false>(j, grid, after_prep, stream);
 }
 
 int eff_len(int max_cache_len, int window) {
@@ -778,31 +774,23 @@ void decode_q4_workspace(DecodeQ4Job* j, void* workspace) {
   j->pitch = y.pitch;
 }
 
-cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream) {
+cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream, bool after_prep) {
   cudaError_t e;
   switch (j.D / 32) {
-    case 1: e = launch_split<1>(j, stream); break;
-    case 2: e = launch_split<2>(j, stream); break;
-    case 3: e = launch_split<3>(j, stream); break;
-    case 4: e = launch_split<4>(j, stream); break;
-    case 5: e = launch_split<5>(j, stream); break;
-    case 6: e = launch_split<6>(j, stream); break;
-    case 7: e = launch_split<7>(j, stream); break;
-    default: e = launch_split<8>(j, stream); break;
+    case 1: e = launch_split<1>(j, after_prep, stream); break;
+    case 2: e = launch_split<2>(j, after_prep, stream); break;
+    case 3: e = launch_split<3>(j, after_prep, stream); break;
+    case 4: e = launch_split<4>(j, after_prep, stream); break;
+    case 5: e = launch_split<5>(j, after_prep, stream); break;
+    case 6: e = launch_split<6>(j, after_prep, stream); break;
+    case 7: e = launch_split<7>(j, after_prep, stream); break;
+    default: e = launch_split<8>(j, after_prep, stream); break;
   }
   if (e != cudaSuccess || (j.nsplit == 1 && !j.weights)) return e;
   const unsigned rows = j.nsplit > 1 ? static_cast<unsigned>(j.B) * j.H : 0;
   const unsigned per = j.weights ? (eff_len(j.max_cache_len, j.window) - 1) / 256 + 1 : 0;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(rows + static_cast<unsigned>(j.B) * j.Hkv * per);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_q4_finish_kernel, j, rows, per ? per : 1u);
+  return launch_dependent(decode_q4_finish_kernel, rows + static_cast<unsigned>(j.B) * j.Hkv * per,
+                          256, 0, stream, j, rows, per ? per : 1u);
 }
 
 }  // namespace gqa

@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int t
 // fp32) first, then the k and v rows.
 template <int M, int ROPE>
 __global__ void __launch_bounds__(128) prep_q4_kernel(PrepQ4Job j) {
+  dependents_may_launch();
   if (gated_off(j.kv.skip)) return;
   constexpr int D = 32 * M;
   const AppendQ4Job& a = j.kv;
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   __shared__ uint32_t hist[2048];
   __shared__ uint32_t wsum[32];
   __shared__ uint32_t found_bin, found_left;
+  dependents_may_launch();
   if (gated_off(j.skip)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long bh = blockIdx.x;
@@ -539,10 +541,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
 
 // The kept records, 16 bytes a thread.
 template <int M>
-__global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j) {
+__global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j, unsigned per_head) {
+  dependent_wait();
   if (gated_off(j.skip)) return;
   constexpr int P = q4::record_bytes(M) / 16, U = 4;
-  const long bh = blockIdx.y;
+  const long bh = blockIdx.x / per_head;
   const int b = static_cast<int>(bh / j.Hkv);
   const int n = j.cache_len[b];
   if (n < 0 || n > j.max_cache_len || n > j.capacity) return;
@@ -550,8 +553,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j) {
   const uint4* src = reinterpret_cast<const uint4*>(j.cache) + bh * j.capacity * P;
   uint4* dst = reinterpret_cast<uint4*>(j.cache_out) + bh * j.capacity_out * P;
   const int32_t* index = j.index + bh * j.budget;
-  for (long i0 = static_cast<long>(blockIdx.x) * 256 * U + threadIdx.x; i0 < pieces;
-       i0 += static_cast<long>(gridDim.x) * 256 * U) {
+  for (long i0 = static_cast<long>(blockIdx.x % per_head) * 256 * U + threadIdx.x; i0 < pieces;
+       i0 += static_cast<long>(per_head) * 256 * U) {
     uint4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -656,11 +659,10 @@ cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream) {
     const long pieces = static_cast<long>(j.max_cache_len < j.budget ? j.max_cache_len : j.budget) *
                         (q4::record_bytes(M) / 16);
     if (pieces == 0) return cudaSuccess;
-    long blocks = (pieces + 1023) / 1024;
-    if (blocks > 65536) blocks = 65536;
-    // heads on the y axis: the host check keeps B * Hkv <= 65535
-    evict_move_kernel<M><<<dim3(static_cast<unsigned>(blocks), heads), 256, 0, stream>>>(j);
-    return cudaGetLastError();
+    // heads <= 65535 (host check)
+    const long per = (pieces + 1023) / 1024, most = 0x7fffffffL / heads;
+    const unsigned per_head = static_cast<unsigned>(per < most ? per : most);
+    return launch_dependent(evict_move_kernel<M>, heads * per_head, 256, 0, stream, j, per_head);
   });
 }
 
