@@ -406,22 +406,48 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-constexpr int kSelThreads = 1024;
 constexpr int kSelItems = 4;                 // slots per thread and compaction tile
 constexpr int kSelKeys = 40960;              // keys held in shared memory at most (160 KB)
 
-// One block per (row, head): the need-th largest of the old slots' keys by three radix
-// passes (11, 11, 10 bits from the top), then one ordered pass that writes the kept
-// slots' numbers and weights. The keys are read once from memory where they fit in
-// shared memory, else again from L2 in each pass.
+// Inclusive sum over a selection block; total: of all. Two barriers; wsum [32].
+template <int kSelThreads>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto scan = [&](uint32_t x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  v = scan(v);
+  if (lane == 31) wsum[warp] = v;
+  __syncthreads();
+  const uint32_t w = lane < kSelThreads / 32 ? wsum[lane] : 0u, upto = scan(w);
+  total = __shfl_sync(0xffffffffu, upto, 31);
+  v += __shfl_sync(0xffffffffu, upto - w, warp);
+  __syncthreads();
+  return v;
+}
+
+// One block per (row, head): the need-th largest of the old slots' keys, then one ordered
+// pass that writes the kept slots' numbers and weights. The largest by its top eleven bits
+// (a histogram of them, summed from the top); then among the few keys that share those,
+// gathered, bit by bit; where they are more than a thread each, by histograms of the next
+// eleven and ten bits. The keys are read once from memory where they fit in shared memory,
+// else again from L2 in each pass. Latency counts here: it is one block's chain of barriers.
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held) {
+  constexpr int kSelBins = 2048 / kSelThreads;
   extern __shared__ uint32_t keys[];
   __shared__ uint32_t hist[2048];
+  __shared__ uint32_t few[kSelThreads];
   __shared__ uint32_t wsum[32];
-  __shared__ uint32_t found_bin, found_left;
+  __shared__ uint32_t found_bin, found_left, found_count, gathered;
   dependents_may_launch();
   if (gated_off(j.skip)) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const long bh = blockIdx.x;
   const int b = static_cast<int>(bh / j.Hkv);
   const int n = j.cache_len[b];
@@ -445,10 +471,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   }
   const int old = n - j.recent;              // recent <= budget < n
   const bool in_smem = old <= held;
-  if (in_smem) {
-    for (int i = tid; i < old; i += kSelThreads) keys[i] = weight_key(w[i]);
-    __syncthreads();
-  }
   auto key_of = [&](int i) { return in_smem ? keys[i] : weight_key(w[i]); };
 
   // Threshold: keys above T are kept, and the first `left` of those equal to it.
@@ -460,34 +482,63 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const int bits = pass == 2 ? 10 : 11;
       const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
-      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kSelBins; ++i) hist[tid + i * kSelThreads] = 0;
+      if (tid == 0) gathered = 0;
       __syncthreads();
       for (int i = tid; i < old; i += kSelThreads) {
-        const uint32_t k = key_of(i);
+        uint32_t k;
+        if (pass == 0) {
+          k = weight_key(w[i]);
+          if (in_smem) keys[i] = k;
+        } else {
+          k = key_of(i);
+        }
         if ((k & above) == (T & above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      // bins from the top: thread t holds bins 2047 - 2 t and 2046 - 2 t
-      const uint32_t h0 = hist[2047 - 2 * tid], h1 = hist[2046 - 2 * tid];
-      uint32_t incl = h0 + h1;
+      // bins from the top: thread t holds kSelBins of them, from 2047 - kSelBins t down
+      uint32_t h[kSelBins], mine = 0, total;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) wsum[warp] = incl;
-      __syncthreads();
-      uint32_t base = 0;
-      for (int i = 0; i < warp; ++i) base += wsum[i];
-      const uint32_t end = base + incl, begin = end - h0 - h1;
-      if (begin < left && end >= left) {      // exactly one thread
-        const bool second = begin + h0 < left;
-        found_bin = second ? 2046 - 2 * tid : 2047 - 2 * tid;
-        found_left = left - begin - (second ? h0 : 0);
+      for (int i = 0; i < kSelBins; ++i) mine += h[i] = hist[2047 - kSelBins * tid - i];
+      uint32_t at = block_scan<kSelThreads>(mine, wsum, total) - mine;
+      if (at < left && at + mine >= left) {   // exactly one thread
+#pragma unroll
+        for (int i = 0; i < kSelBins; ++i) {
+          if (at < left && at + h[i] >= left) {
+            found_bin = 2047 - kSelBins * tid - i;
+            found_left = left - at;
+            found_count = h[i];
+          }
+          at += h[i];
+        }
       }
       __syncthreads();
       T |= found_bin << shift;
       left = found_left;
+      const uint32_t count = found_count;
+      if (pass == 0 && count <= kSelThreads) {
+        for (int i = tid; i < old; i += kSelThreads) {
+          const uint32_t k = key_of(i);
+          if (k >> 21 == T >> 21) few[atomicAdd(&gathered, 1u)] = k;
+        }
+        __syncthreads();
+        const uint32_t k = tid < count ? few[tid] : 0u;
+        bool in = tid < count;
+#pragma unroll 1
+        for (int bit = 20; bit >= 0; --bit) {
+          const bool set = k >> bit & 1u;
+          const uint32_t c = __syncthreads_count(in && set);
+          if (c >= left) {
+            T |= 1u << bit;
+            in = in && set;
+          } else {
+            left -= c;
+            in = in && !set;
+          }
+        }
+        break;
+      }
     }
   }
   // Ordered pass. Kept before a slot: those above T, and at most `left` equal to it.
@@ -495,33 +546,24 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   for (int t0 = 0; t0 < n; t0 += kSelThreads * kSelItems) {
     const int i0 = t0 + tid * kSelItems;
     uint32_t up = 0, eq = 0;                  // bit e: slot i0 + e
+    float wv[kSelItems];
+#pragma unroll
+    for (int e = 0; e < kSelItems; ++e) wv[e] = i0 + e < n ? w[i0 + e] : 0.f;
 #pragma unroll
     for (int e = 0; e < kSelItems; ++e) {
       const int i = i0 + e;
       if (i >= old) {
         if (i < n) up |= 1u << e;
       } else if (any_old) {
-        const uint32_t k = key_of(i);
+        const uint32_t k = weight_key(wv[e]);
         if (k > T) up |= 1u << e;
         if (k == T) eq |= 1u << e;
       }
     }
     // counts of both in one word: at most 4096 each
     const uint32_t own = __popc(up) | static_cast<uint32_t>(__popc(eq)) << 16;
-    uint32_t incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    __syncthreads();                          // wsum of the tile before is read
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - own, total = 0;
-    for (int i = 0; i < 32; ++i) {
-      if (i < warp) before += wsum[i];
-      total += wsum[i];
-    }
+    uint32_t total;
+    const uint32_t before = block_scan<kSelThreads>(own, wsum, total) - own;
     uint32_t nup = base_up + (before & 0xffffu), neq = base_eq + (before >> 16);
 #pragma unroll
     for (int e = 0; e < kSelItems; ++e) {
@@ -529,7 +571,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
       if (is_up || (is_eq && neq < left)) {
         const uint32_t at = nup + min(neq, left);
         index[at] = i0 + e;
-        wo[at] = w[i0 + e];
+        wo[at] = wv[e];
       }
       nup += is_up;
       neq += is_eq;
@@ -641,19 +683,31 @@ cudaError_t launch_prep_q4(const PrepQ4Job& j, cudaStream_t stream) {
   });
 }
 
-cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream) {
+namespace {
+template <int T>
+cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   const cudaError_t e = allowed.get(
       [] {
-        return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSelKeys * 4);
+        return cudaFuncSetAttribute(evict_select_kernel<T>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
   const int held = j.max_cache_len < kSelKeys ? j.max_cache_len : kSelKeys;
+  evict_select_kernel<T><<<heads, T, held * 4, stream>>>(j, held);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream) {
   const unsigned heads = static_cast<unsigned>(j.B) * j.Hkv;
-  evict_select_kernel<<<heads, kSelThreads, held * 4, stream>>>(j, held);
-  if (const cudaError_t l = cudaGetLastError(); l != cudaSuccess) return l;
+  // Short heads are chains of barriers, cheaper among 16 warps than among 32 (8 heads of 1100
+  // slots: 8.8 us with the move, 10.0 with 32 warps); long ones are work on the keys (128 heads
+  // of up to 8192: 42.4 and 41.4).
+  const cudaError_t e = j.max_cache_len <= 4096 ? launch_select<512>(j, heads, stream)
+                                                : launch_select<1024>(j, heads, stream);
+  if (e != cudaSuccess) return e;
   return with_groups(j.D / 32, [&](auto g) {
     constexpr int M = decltype(g)::value;
     const long pieces = static_cast<long>(j.max_cache_len < j.budget ? j.max_cache_len : j.budget) *
