@@ -152,8 +152,8 @@ __host__ __device__ constexpr int resident_blocks(int M, int NT) {
 }
 
 // Rings of all warps, then the queries' B fragments.
-constexpr size_t split_smem(int M, int NT) {
-  return static_cast<size_t>(kWarps) * kStages * kTile * q4::record_bytes(M) + 512 * M * NT;
+constexpr size_t split_smem(int M, int NT, int NW) {
+  return static_cast<size_t>(NW) * kStages * kTile * q4::record_bytes(M) + 512 * M * NT;
 }
 
 // Live slots of row b (0: the row is invalid).
@@ -167,14 +167,16 @@ __device__ __forceinline__ int live_slots(const DecodeQ4Job& j, int b, bool lead
 }
 
 // One block: up to 4 NT query heads of one kv head over the slots [split chunk, + chunk).
-template <int M, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4_kernel(DecodeQ4Job j) {
+// NW warps share its tiles.
+template <int M, int NT, bool WEIGHTS, int NW>
+__global__ void __launch_bounds__(32 * NW, NW > kWarps ? 1 : resident_blocks(M, NT))
+decode_q4_kernel(DecodeQ4Job j) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), TILE_BYTES = kTile * REC, VW = (M + 1) / 2;
   constexpr int kHeads = 4 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ uint64_t full[NW][kStages];
   __shared__ float q_factor[kHeads];
-  __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+  __shared__ float sm_m[NW][kHeads], sm_l[NW][kHeads];
   __shared__ int abort_flag;
   dependents_may_launch();
   dependent_wait();                          // a step's first pass
@@ -193,11 +195,11 @@ __global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4
   if (k0 >= nlive) return;
   const int k1 = min(k0 + j.chunk, nlive);
   const int tiles = (k1 - k0 + kTile - 1) / kTile;
-  const int mine = tiles > warp ? (tiles - 1 - warp) / kWarps + 1 : 0;
+  const int mine = tiles > warp ? (tiles - 1 - warp) / NW + 1 : 0;
 
   uint8_t* ring = smem + warp * kStages * TILE_BYTES;
   const uint8_t* records = j.cache + bh * j.capacity * REC;
-  auto first_key = [&](int i) { return k0 + (i * kWarps + warp) * kTile; };
+  auto first_key = [&](int i) { return k0 + (i * NW + warp) * kTile; };
   auto issue = [&](int i) {                  // lane 0: tile i of this warp
     const int s = i % kStages, kb = first_key(i);
     const uint32_t bytes = static_cast<uint32_t>(min(kTile, k1 - kb)) * REC;
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4
   // element lies in [2^12, 2^13): both fp16 parts are then normal over 22 bits. Product
   // step (g, st) takes from thread (n, a) the pairs of dims 2 st, 2 st + 4 and 2 st + 1,
   // 2 st + 5 of the word; column n = 2 h is head h's high part, 2 h + 1 its low part.
-  uint2* frag = reinterpret_cast<uint2*>(smem + kWarps * kStages * TILE_BYTES);
-  for (int h = warp; h < kHeads; h += kWarps) {
+  uint2* frag = reinterpret_cast<uint2*>(smem + NW * kStages * TILE_BYTES);
+  for (int h = warp; h < kHeads; h += NW) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = 0.f;
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4
     const int h = 4 * t + c;
     float m_all = sm_m[0][h];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) m_all = fmaxf(m_all, sm_m[w][h]);
+    for (int w = 1; w < NW; ++w) m_all = fmaxf(m_all, sm_m[w][h]);
     const float f = m_run[t] == -INFINITY ? 0.f : ex2(m_run[t] - m_all), fo = f * 0.0625f;
 #pragma unroll
     for (int g = 0; g < M; ++g)
@@ -522,14 +524,14 @@ __global__ void __launch_bounds__(32 * kWarps, resident_blocks(M, NT)) decode_q4
   const long hrow0 = static_cast<long>(b) * j.H + hkv * G + g0;
   const int heads = min(kHeads, G - g0);
   float* ml = j.partial + static_cast<long>(j.B) * j.H * j.nsplit * D;
-  for (int t = threadIdx.x; t < heads * (D / 4); t += 32 * kWarps) {
+  for (int t = threadIdx.x; t < heads * (D / 4); t += 32 * NW) {
     const int h = t / (D / 4), d = 4 * (t - h * (D / 4));
     float M_ = sm_m[0][h], L = 0.f;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) M_ = fmaxf(M_, sm_m[w][h]);
+    for (int w = 1; w < NW; ++w) M_ = fmaxf(M_, sm_m[w][h]);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < NW; ++w) {
       if (sm_m[w][h] != -INFINITY) L = fmaf(ex2(sm_m[w][h] - M_), sm_l[w][h], L);
       const float4 z = *reinterpret_cast<const float4*>(smem + w * kStages * TILE_BYTES +
                                                         (h * D + d) * 4);
@@ -652,20 +654,20 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   if (n < nlive) *w += sum;
 }
 
-template <int M, int NT, bool W>
+template <int M, int NT, bool W, int NW>
 cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, bool after_prep, cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
+  constexpr size_t smem = split_smem(M, NT, NW);
+  auto kernel = decode_q4_kernel<M, NT, W, NW>;
   const cudaError_t e = allowed.get(
-      [] {
-        return cudaFuncSetAttribute(decode_q4_kernel<M, NT, W>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(split_smem(M, NT)));
+      [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(smem));
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  if (after_prep)
-    return launch_dependent(decode_q4_kernel<M, NT, W>, grid, 32 * kWarps, split_smem(M, NT), stream, j);
-  decode_q4_kernel<M, NT, W><<<grid, 32 * kWarps, split_smem(M, NT), stream>>>(j);
+  if (after_prep) return launch_dependent(kernel, grid, 32 * NW, smem, stream, j);
+  kernel<<<grid, 32 * NW, smem, stream>>>(j);
   return cudaGetLastError();
 }
 
@@ -676,14 +678,28 @@ long units_of(int B, int H, int Hkv) {
   return static_cast<long>(B) * Hkv * ((H / Hkv + per - 1) / per);
 }
 
+// Short rows of few heads: one tile a warp, sixteen warps where the registers allow (the
+// one block's rounds are the kernel's time: one row of 500 slots, 8 kv heads of 4 query
+// heads, 6.1 us with 4 warps).
+constexpr int kShortTiles = 16;
+
+template <int M, int NT>
+cudaError_t launch_split(const DecodeQ4Job& j, bool after_prep, cudaStream_t stream) {
+  const long units = units_of(j.B, j.H, j.Hkv);
+  const unsigned grid = static_cast<unsigned>(units) * j.nsplit;
+  constexpr int kBig = M <= 4 && NT == 1 ? 16 : 8;
+  const bool big = j.nsplit == 1 && j.chunk > kWarps * kTile && units <= 152;
+  if (j.weights)
+    return big ? launch_split<M, NT, true, kBig>(j, grid, after_prep, stream)
+               : launch_split<M, NT, true, kWarps>(j, grid, after_prep, stream);
+  return big ? launch_split<M, NT, false, kBig>(j, grid, after_prep, stream)
+             : launch_split<M, NT, false, kWarps>(j, grid, after_prep, stream);
+}
+
 template <int M>
 cudaError_t launch_split(const DecodeQ4Job& j, bool after_prep, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(units_of(j.B, j.H, j.Hkv)) * j.nsplit;
-  if (head_tiles(j.H, j.Hkv) == 1)
-    return j.weights ? launch_split<M, 1, true>(j, grid, after_prep, stream)
-                     : launch_split<M, 1, false>(j, grid, after_prep, stream);
-  return j.weights ? launch_split<M, 2, true>(j, grid, after_prep, stream)
-                   : launch_split<M, 2, false>(j, grid, after_prep, stream);
+  return head_tiles(j.H, j.Hkv) == 1 ? launch_split<M, 1>(j, after_prep, stream)
+                                     : launch_split<M, 2>(j, after_prep, stream);
 }
 
 int eff_len(int max_cache_len, int window) {
@@ -723,7 +739,7 @@ int most_splits(int B, int H, int Hkv) {
 // Up to 16 tiles stay in one block: the second launch costs what the split saves.
 int split_bound(int B, int H, int Hkv, int max_cache_len, int window) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
-  if (tiles <= 4 * kWarps) return 1;
+  if (tiles <= kShortTiles) return 1;
   const int most = (tiles + kWarps - 1) / kWarps;             // a tile for every warp
   const int want = most_splits(B, H, Hkv);
   return want < most ? want : most;
