@@ -14,11 +14,11 @@
 // accuracy. (The codes are unpacked in registers and used once: staging them in shared
 // memory for tcgen05 would cost more shared-memory traffic than the copy itself.)
 //
-// Keys (then value dims) are the 16 rows of the A operand; the 8 columns of B are the
-// high and low parts of 4 query heads, so up to 4 heads need one product and up to 8
-// two, with the unpacking shared. A thread holds both parts of a head's score side by
-// side: their sum needs no exchange, and one 8 x 8 transpose (movmatrix) turns 8 keys'
-// packed weights into the next product's B operand.
+// Keys (then value dims) are the 16 rows of the A operand. With up to 4 query heads (NT =
+// 1) the 8 columns of B are their high and low parts, side by side in a thread, which sums
+// them. With up to 8 (NT = 2) the columns are the heads, and a second product with the low
+// parts adds to the first one's sums. Either way one 8 x 8 transpose (movmatrix) turns 8
+// keys' packed weights into the next product's B operand.
 //
 // A pair of codes becomes a packed fp16 pair in two instructions: a nibble u = c + 8
 // masked out of its 16-bit half and put under the exponent of 1024 is 1024 + u, or
@@ -95,12 +95,10 @@ __device__ __forceinline__ uint32_t codes(uint32_t w) {
   return as_u32(__hsub2(as_half2(u), as_half2(ODD ? 0x64806480u : 0x64086408u)));
 }
 
-// x >= 0 below 2^16 as (high, low) packed fp16: the top eleven bits and the rest, which
-// is exact in fp32. (Below 2^-14 the high part keeps fewer bits: an error of 2^-25, of
-// weights whose largest is near 2^14.)
-__device__ __forceinline__ uint32_t split1(float x) {
-  const float h = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
-  return as_u32(__floats2half2_rn(h, x - h));
+// The top eleven bits of x >= 0 below 2^16: exact in fp16, as is the rest in fp32. (Below
+// 2^-14 fp16 keeps fewer bits: an error of 2^-25, of weights whose largest is near 2^14.)
+__device__ __forceinline__ float high_part(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
 }
 
 // N 32-bit words from shared memory, aligned to their largest power-of-two divisor.
@@ -218,7 +216,8 @@ decode_q4_kernel(DecodeQ4Job j) {
   // (the dims of key word (a, g)). Scaled by a power of two so that the head's largest
   // element lies in [2^12, 2^13): both fp16 parts are then normal over 22 bits. Product
   // step (g, st) takes from thread (n, a) the pairs of dims 2 st, 2 st + 4 and 2 st + 1,
-  // 2 st + 5 of the word; column n = 2 h is head h's high part, 2 h + 1 its low part.
+  // 2 st + 5 of the word. Column n = 2 h is head h's high part and 2 h + 1 its low part (NT
+  // = 1), or n = h in two fragments, high and low.
   uint2* frag = reinterpret_cast<uint2*>(smem + NW * kStages * TILE_BYTES);
   for (int h = warp; h < kHeads; h += NW) {
     float x[8];
@@ -249,9 +248,9 @@ decode_q4_kernel(DecodeQ4Job j) {
     if (there) {
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        uint2* to = frag + (((h >> 2) * M + g) * 2 + st) * 32 + 8 * (h & 3) + a;
+        uint2* to = frag + (2 * g + st) * 32 + (NT == 1 ? 8 : 4) * h + a;
         to[0] = make_uint2(hi[2 * st], hi[2 * st + 1]);
-        to[4] = make_uint2(lo[2 * st], lo[2 * st + 1]);
+        to[NT == 1 ? 4 : 64 * M] = make_uint2(lo[2 * st], lo[2 * st + 1]);
       }
     }
     // scores come out times 2^-ex; undo it, times the softmax scale, in log2 units
@@ -263,10 +262,11 @@ decode_q4_kernel(DecodeQ4Job j) {
 
   const uint2* bfrag = frag + lane;
   float qf[NT];
-  float* score_row[NT];                      // this thread's heads: c and, of 8, c + 4
+  auto head = [&](int t) { return NT * c + t; };           // this thread's heads
+  float* score_row[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int h = 4 * t + c;
+    const int h = head(t);
     qf[t] = q_factor[h];
     score_row[t] = WEIGHTS && g0 + h < G
                        ? j.scores + (static_cast<long>(b) * j.H + hkv * G + g0 + h) * j.pitch
@@ -275,7 +275,7 @@ decode_q4_kernel(DecodeQ4Job j) {
 
   float m_run[NT], l_run[NT];
   int e_run = -60 - 14;                      // exponent of the reference beside the maximum
-  float o[NT][M][4];                         // head 4 t + c, dims 32 g + 4 r + (0 .. 3)
+  float o[NT][M][4];                         // head(t), dims 32 g + 4 r + (0 .. 3)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     m_run[t] = -INFINITY;
@@ -312,7 +312,7 @@ decode_q4_kernel(DecodeQ4Job j) {
       }
 #pragma unroll
       for (int g = 0; g < M; ++g) {
-        uint2 f[NT][2];
+        uint2 f[NT][2];                      // NT = 2: high parts, low parts
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           f[t][0] = bfrag[((t * M + g) * 2) * 32];
@@ -320,25 +320,26 @@ decode_q4_kernel(DecodeQ4Job j) {
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {        // keys 16 k .. 16 k + 15
-          float d[NT][4];
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[t][e] = 0.f;
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint32_t w0 = q ? kw[2 * k][g] >> 8 : kw[2 * k][g];
             const uint32_t w1 = q ? kw[2 * k + 1][g] >> 8 : kw[2 * k + 1][g];
             const uint32_t a0 = codes<0>(w0), a1 = codes<0>(w1), a2 = codes<1>(w0), a3 = codes<1>(w1);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma(d[t], a0, a1, a2, a3, f[t][q].x, f[t][q].y);
+            for (int t = 0; t < NT; ++t) mma(d, a0, a1, a2, a3, f[t][q].x, f[t][q].y);
           }
           const float s0 = unit_scale(sc[2 * k][g / 2], g & 1);
           const float s1 = unit_scale(sc[2 * k + 1][g / 2], g & 1);
+          if (NT == 1) {
+            s[0][2 * k] = fmaf(s0, d[0] + d[1], s[0][2 * k]);
+            s[0][2 * k + 1] = fmaf(s1, d[2] + d[3], s[0][2 * k + 1]);
+          } else {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            s[t][2 * k] = fmaf(s0, d[t][0] + d[t][1], s[t][2 * k]);
-            s[t][2 * k + 1] = fmaf(s1, d[t][2] + d[t][3], s[t][2 * k + 1]);
+            for (int t = 0; t < NT; ++t) {
+              s[t][2 * k] = fmaf(s0, d[t], s[t][2 * k]);
+              s[t][2 * k + 1] = fmaf(s1, d[2 + t], s[t][2 * k + 1]);
+            }
           }
         }
       }
@@ -456,27 +457,34 @@ decode_q4_kernel(DecodeQ4Job j) {
       for (int x = 0; x < 4; ++x) {
         w[x] = __byte_perm(vw[2 * x][g / 2], vw[2 * x + 1][g / 2], g & 1 ? 0x7632 : 0x5410);
         const float sv = unit_scale(vs[x][g / 2], g & 1);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) pb[t][x] = transpose8(split1(p[t][x] * sv));
+        if (NT == 1) {
+          const float y = p[0][x] * sv, h = high_part(y);
+          pb[0][x] = transpose8(as_u32(__floats2half2_rn(h, y - h)));
+        } else {
+          const float y0 = p[0][x] * sv, y1 = p[NT - 1][x] * sv, h0 = high_part(y0), h1 = high_part(y1);
+          pb[0][x] = transpose8(as_u32(__floats2half2_rn(h0, h1)));
+          pb[NT - 1][x] = transpose8(as_u32(__floats2half2_rn(y0 - h0, y1 - h1)));
+        }
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {          // dims 4 r + 2 q (rows 0 .. 7) and + 2 q + 1
-        float d[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[t][e] = 0.f;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t w0 = q ? w[2 * k] >> 8 : w[2 * k], w1 = q ? w[2 * k + 1] >> 8 : w[2 * k + 1];
           const uint32_t a0 = codes<0>(w0), a1 = codes<1>(w0), a2 = codes<0>(w1), a3 = codes<1>(w1);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma(d[t], a0, a1, a2, a3, pb[t][2 * k], pb[t][2 * k + 1]);
+          for (int t = 0; t < NT; ++t) mma(d, a0, a1, a2, a3, pb[t][2 * k], pb[t][2 * k + 1]);
         }
+        if (NT == 1) {
+          o[0][g][2 * q] += d[0] + d[1];
+          o[0][g][2 * q + 1] += d[2] + d[3];
+        } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][g][2 * q] += d[t][0] + d[t][1];
-          o[t][g][2 * q + 1] += d[t][2] + d[t][3];
+          for (int t = 0; t < NT; ++t) {
+            o[t][g][2 * q] += d[t];
+            o[t][g][2 * q + 1] += d[2 + t];
+          }
         }
       }
     }
@@ -500,15 +508,15 @@ decode_q4_kernel(DecodeQ4Job j) {
     for (int off = 4; off < 32; off <<= 1) l_run[t] += __shfl_xor_sync(0xffffffffu, l_run[t], off);
     m_run[t] += static_cast<float>(e_run);
     if (r == 0) {
-      sm_m[warp][4 * t + c] = m_run[t];
-      sm_l[warp][4 * t + c] = l_run[t];
+      sm_m[warp][head(t)] = m_run[t];
+      sm_l[warp][head(t)] = l_run[t];
     }
   }
   __syncthreads();
   float* ex = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int h = 4 * t + c;
+    const int h = head(t);
     float m_all = sm_m[0][h];
 #pragma unroll
     for (int w = 1; w < NW; ++w) m_all = fmaxf(m_all, sm_m[w][h]);
