@@ -1353,7 +1353,7 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
   j.q = p.qrot; j.cache = p.kv.cache; j.cache_len = p.cache_len;
   j.max_cache_len = max_start + 1; j.out = out; j.weights = weights; j.status = status;
   gqa::decode_q4_workspace(&j, ws + lay.part);
-  return cuda_status(gqa::launch_decode_q4(j, s, true));
+  return cuda_status(gqa::launch_decode_q4(j, s));
 }
 
 int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* cache_len,

@@ -19,16 +19,17 @@ __device__ __forceinline__ bool gated_off(const int32_t* skip) {
   return skip && (*reinterpret_cast<const volatile int32_t*>(skip) & ATTN_DEV_NONFINITE);
 }
 
-// A kernel launched dependent on the one before it (launch_dependent) waits here for that
-// one's end and its writes; the one before says with the second call that the next may be
-// set up meanwhile. Both do nothing in a kernel launched the ordinary way.
+// A kernel launched by launch_dependent may start while the one enqueued before it still
+// runs, whatever that one is: it must call dependent_wait before its first access to global
+// memory, which returns when everything before has ended and its writes are visible. With
+// dependents_may_launch a kernel lets the next one be placed already when all of its own
+// blocks have started. (Every kernel of the 4-bit cache does both: they are short, and
+// between two of them the launch otherwise costs about 2 us.)
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependents_may_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Launches a kernel that waits (dependent_wait) for the one enqueued before it: its blocks
-// are placed while that one still runs.
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
                              cudaStream_t stream, A... args) {

@@ -177,7 +177,7 @@ decode_q4_kernel(DecodeQ4Job j) {
   __shared__ float sm_m[NW][kHeads], sm_l[NW][kHeads];
   __shared__ int abort_flag;
   dependents_may_launch();
-  dependent_wait();                          // a step's first pass
+  dependent_wait();
   if (gated_off(j.skip)) return;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -562,14 +562,14 @@ constexpr int kMaxSplits = 152 * 4;          // of one row: no more than blocks 
 // Blocks [0, rows): one query row's splits merged, a split per warp at a time. Blocks after:
 // with weights, 256 slots of one kv head get the sum over its query heads of
 // 2^(score - reference) / sum (one thread per slot, heads in order, so the result does not
-// depend on timing). Launched dependent on the split kernel: its blocks are in place before
-// that one ends.
+// depend on timing).
 __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, unsigned rows,
                                                                unsigned slot_blocks) {
   __shared__ float factor[kMaxSplits];
   __shared__ float red[8];
   __shared__ __align__(16) float acc[8][kMaxHeadDim];
   __shared__ float2 sh[8];
+  dependents_may_launch();
   dependent_wait();
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
 }
 
 template <int M, int NT, bool W, int NW>
-cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, bool after_prep, cudaStream_t stream) {
+cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   constexpr size_t smem = split_smem(M, NT, NW);
   auto kernel = decode_q4_kernel<M, NT, W, NW>;
@@ -674,9 +674,7 @@ cudaError_t launch_split(const DecodeQ4Job& j, unsigned grid, bool after_prep, c
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  if (after_prep) return launch_dependent(kernel, grid, 32 * NW, smem, stream, j);
-  kernel<<<grid, 32 * NW, smem, stream>>>(j);
-  return cudaGetLastError();
+  return launch_dependent(kernel, grid, 32 * NW, smem, stream, j);
 }
 
 // Query heads per block: 4 or 8.
@@ -692,22 +690,22 @@ long units_of(int B, int H, int Hkv) {
 constexpr int kShortTiles = 16;
 
 template <int M, int NT>
-cudaError_t launch_split(const DecodeQ4Job& j, bool after_prep, cudaStream_t stream) {
+cudaError_t launch_split(const DecodeQ4Job& j, cudaStream_t stream) {
   const long units = units_of(j.B, j.H, j.Hkv);
   const unsigned grid = static_cast<unsigned>(units) * j.nsplit;
   constexpr int kBig = M <= 4 && NT == 1 ? 16 : 8;
   const bool big = j.nsplit == 1 && j.chunk > kWarps * kTile && units <= 152;
   if (j.weights)
-    return big ? launch_split<M, NT, true, kBig>(j, grid, after_prep, stream)
-               : launch_split<M, NT, true, kWarps>(j, grid, after_prep, stream);
-  return big ? launch_split<M, NT, false, kBig>(j, grid, after_prep, stream)
-             : launch_split<M, NT, false, kWarps>(j, grid, after_prep, stream);
+    return big ? launch_split<M, NT, true, kBig>(j, grid, stream)
+               : launch_split<M, NT, true, kWarps>(j, grid, stream);
+  return big ? launch_split<M, NT, false, kBig>(j, grid, stream)
+             : launch_split<M, NT, false, kWarps>(j, grid, stream);
 }
 
 template <int M>
-cudaError_t launch_split(const DecodeQ4Job& j, bool after_prep, cudaStream_t stream) {
-  return head_tiles(j.H, j.Hkv) == 1 ? launch_split<M, 1>(j, after_prep, stream)
-                                     : launch_split<M, 2>(j, after_prep, stream);
+cudaError_t launch_split(const DecodeQ4Job& j, cudaStream_t stream) {
+  return head_tiles(j.H, j.Hkv) == 1 ? launch_split<M, 1>(j, stream)
+                                     : launch_split<M, 2>(j, stream);
 }
 
 int eff_len(int max_cache_len, int window) {
@@ -798,17 +796,17 @@ void decode_q4_workspace(DecodeQ4Job* j, void* workspace) {
   j->pitch = y.pitch;
 }
 
-cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream, bool after_prep) {
+cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream) {
   cudaError_t e;
   switch (j.D / 32) {
-    case 1: e = launch_split<1>(j, after_prep, stream); break;
-    case 2: e = launch_split<2>(j, after_prep, stream); break;
-    case 3: e = launch_split<3>(j, after_prep, stream); break;
-    case 4: e = launch_split<4>(j, after_prep, stream); break;
-    case 5: e = launch_split<5>(j, after_prep, stream); break;
-    case 6: e = launch_split<6>(j, after_prep, stream); break;
-    case 7: e = launch_split<7>(j, after_prep, stream); break;
-    default: e = launch_split<8>(j, after_prep, stream); break;
+    case 1: e = launch_split<1>(j, stream); break;
+    case 2: e = launch_split<2>(j, stream); break;
+    case 3: e = launch_split<3>(j, stream); break;
+    case 4: e = launch_split<4>(j, stream); break;
+    case 5: e = launch_split<5>(j, stream); break;
+    case 6: e = launch_split<6>(j, stream); break;
+    case 7: e = launch_split<7>(j, stream); break;
+    default: e = launch_split<8>(j, stream); break;
   }
   if (e != cudaSuccess || (j.nsplit == 1 && !j.weights)) return e;
   const unsigned rows = j.nsplit > 1 ? static_cast<unsigned>(j.B) * j.H : 0;

@@ -419,8 +419,7 @@ void decode_q4_plan(int B, int H, int Hkv, int max_cache_len, int window, int* n
 size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights,
                        bool bound);
 void decode_q4_workspace(DecodeQ4Job* j, void* workspace);   // plan and pointers into it
-// after_prep: launch_prep_q4 was enqueued just before.
-cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream, bool after_prep = false);
+cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream);
 
 // A decode step's first pass: the rows' q normed and rotated, their k and v appended.
 struct PrepQ4Job {

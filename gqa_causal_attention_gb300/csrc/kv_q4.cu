@@ -236,6 +236,8 @@ __global__ void __launch_bounds__(kRowThreads, 6) append_q4_kernel(AppendQ4Job j
   __shared__ int abort_flag;
   __shared__ Target to[kMaxRows];
   __shared__ uint2 later[kMaxRows];
+  dependents_may_launch();
+  dependent_wait();
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long seg = blockIdx.x / seg_tiles;
@@ -310,6 +312,8 @@ __global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int t
   constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16, RW = q4::Lanes<M>::kRows;
   __shared__ __align__(16) uint8_t recs[kMaxRows * REC];
   __shared__ const uint8_t* from[kMaxRows];
+  dependents_may_launch();
+  dependent_wait();
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long rows = static_cast<long>(j.B) * j.Hkv * j.L;
@@ -365,6 +369,7 @@ __global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int t
 template <int M, int ROPE>
 __global__ void __launch_bounds__(128) prep_q4_kernel(PrepQ4Job j) {
   dependents_may_launch();
+  dependent_wait();
   if (gated_off(j.kv.skip)) return;
   constexpr int D = 32 * M;
   const AppendQ4Job& a = j.kv;
@@ -446,6 +451,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   __shared__ uint32_t wsum[32];
   __shared__ uint32_t found_bin, found_left, found_count, gathered;
   dependents_may_launch();
+  dependent_wait();
   if (gated_off(j.skip)) return;
   const int tid = threadIdx.x;
   const long bh = blockIdx.x;
@@ -584,6 +590,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
 // The kept records, 16 bytes a thread.
 template <int M>
 __global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j, unsigned per_head) {
+  dependents_may_launch();
   dependent_wait();
   if (gated_off(j.skip)) return;
   constexpr int P = q4::record_bytes(M) / 16, U = 4;
@@ -629,9 +636,8 @@ cudaError_t launch_append(const AppendQ4Job& j, int tr, long seg_rows, int seg_t
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  append_q4_kernel<M, ROPE><<<grid, kRowThreads, tr * (256 * M + q4::record_bytes(M)), stream>>>(
-      j, tr, seg_rows, seg_tiles);
-  return cudaGetLastError();
+  return launch_dependent(append_q4_kernel<M, ROPE>, grid, kRowThreads,
+                          tr * (256 * M + q4::record_bytes(M)), stream, j, tr, seg_rows, seg_tiles);
 }
 }  // namespace
 
@@ -665,8 +671,8 @@ cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream) {
   const long blocks = (rows + tr - 1) / tr;
   if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
   return with_groups(j.D / 32, [&](auto g) {
-    read_q4_kernel<decltype(g)::value><<<static_cast<unsigned>(blocks), kRowThreads, 0, stream>>>(j, tr);
-    return cudaGetLastError();
+    return launch_dependent(read_q4_kernel<decltype(g)::value>, static_cast<unsigned>(blocks),
+                            kRowThreads, 0, stream, j, tr);
   });
 }
 
@@ -675,11 +681,8 @@ cudaError_t launch_prep_q4(const PrepQ4Job& j, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
   return with_groups(j.kv.D / 32, [&](auto g) {
     constexpr int M = decltype(g)::value;
-    if (j.kv.R % 8 == 0)
-      prep_q4_kernel<M, kRopeQuads><<<grid, 128, 0, stream>>>(j);
-    else
-      prep_q4_kernel<M, kRopeDims><<<grid, 128, 0, stream>>>(j);
-    return cudaGetLastError();
+    return j.kv.R % 8 == 0 ? launch_dependent(prep_q4_kernel<M, kRopeQuads>, grid, 128, 0, stream, j)
+                           : launch_dependent(prep_q4_kernel<M, kRopeDims>, grid, 128, 0, stream, j);
   });
 }
 
@@ -695,8 +698,7 @@ cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, cudaStream_t stre
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
   const int held = j.max_cache_len < kSelKeys ? j.max_cache_len : kSelKeys;
-  evict_select_kernel<T><<<heads, T, held * 4, stream>>>(j, held);
-  return cudaGetLastError();
+  return launch_dependent(evict_select_kernel<T>, heads, T, held * 4, stream, j, held);
 }
 }  // namespace
 
