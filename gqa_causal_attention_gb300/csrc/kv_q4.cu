@@ -36,29 +36,27 @@ cudaError_t with_groups(int m, F f) {
 }
 
 // How a row's rotation is read: not at all, in quads (half the rotary dims a multiple of
-// four: a quad lies within one half, and so do its partners), or dim by dim.
-enum { kNoRope = 0, kRopeQuads = 1, kRopeDims = 2 };
+// four: a quad lies within one half, and so do its partners), in quads with every dim
+// rotary, or dim by dim.
+enum { kNoRope = 0, kRopeQuads = 1, kRopeDims = 2, kRopeAll = 3 };
+int rope_kind(int R, int D) { return R % 8 ? kRopeDims : (R == D ? kRopeAll : kRopeQuads); }
 
 __device__ __forceinline__ void load4(const float* p, float* r) {
   const float4 t = *reinterpret_cast<const float4*>(p);
   r[0] = t.x; r[1] = t.y; r[2] = t.z; r[3] = t.w;
 }
 
-// A lane's quads of the raw row x.
+// A lane's quads of a row. (Lanes without a row of their own have dims of a row too: they
+// read along, and what they make of it is dropped.)
+template <int M>
+__device__ __forceinline__ void load_row(const float* x, const q4::Lanes<M>& at, float (&y)[8]) {
+  load4(x + at.dim(0), y);
+  load4(x + at.dim(1), y + 4);
+}
 template <int M>
 __device__ __forceinline__ void store_row(float* x, const q4::Lanes<M>& at, const float (&y)[8]) {
   *reinterpret_cast<float4*>(x + at.dim(0)) = make_float4(y[0], y[1], y[2], y[3]);
   *reinterpret_cast<float4*>(x + at.dim(1)) = make_float4(y[4], y[5], y[6], y[7]);
-}
-template <int M>
-__device__ __forceinline__ void load_row(const float* x, const q4::Lanes<M>& at, float (&y)[8]) {
-  if (at.in) {
-    load4(x + at.dim(0), y);
-    load4(x + at.dim(1), y + 4);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.f;
-  }
 }
 
 // A lane's quads of the raw row x through RMSNorm (nw) and RoPE (tab: the row's angles;
@@ -68,19 +66,21 @@ template <int M, int ROPE>
 __device__ __forceinline__ float rotate_row(const float* x, const float2* tab, int R,
                                             const float* nw, float eps, const q4::Lanes<M>& at,
                                             int lane, float (&y)[8]) {
-  const int half = R / 2;
+  const int half = ROPE == kRopeAll ? 16 * M : R / 2;
   float c[8], s[8], b[8], w[8];
+  if (ROPE != kRopeAll) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = w[e] = 1.f;
-    s[e] = b[e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      c[e] = w[e] = 1.f;
+      s[e] = b[e] = 0.f;
+    }
   }
   // y = a c + b s, b the rotary partner
 #pragma unroll
   for (int q = 0; q < 8; q += 4) {
     const int d0 = at.dim(q / 4);
-    if (!at.in || d0 >= R) continue;
-    if (ROPE == kRopeQuads) {
+    if (ROPE != kRopeAll && d0 >= R) continue;
+    if (ROPE != kRopeDims) {
       const bool low = d0 < half;
       const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
       const float sign = low ? -1.f : 1.f;
@@ -659,8 +659,11 @@ cudaError_t launch_append_q4(const AppendQ4Job& job, cudaStream_t stream) {
     constexpr int M = decltype(g)::value;
     const int t = static_cast<int>(tiles);
     if (!j.table) return launch_append<M, kNoRope>(j, tr, seg_rows, t, grid, stream);
-    return j.R % 8 == 0 ? launch_append<M, kRopeQuads>(j, tr, seg_rows, t, grid, stream)
-                        : launch_append<M, kRopeDims>(j, tr, seg_rows, t, grid, stream);
+    switch (rope_kind(j.R, j.D)) {
+      case kRopeAll: return launch_append<M, kRopeAll>(j, tr, seg_rows, t, grid, stream);
+      case kRopeQuads: return launch_append<M, kRopeQuads>(j, tr, seg_rows, t, grid, stream);
+      default: return launch_append<M, kRopeDims>(j, tr, seg_rows, t, grid, stream);
+    }
   });
 }
 
