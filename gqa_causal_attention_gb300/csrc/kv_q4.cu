@@ -227,7 +227,7 @@ __device__ __forceinline__ uint2 append_rows(const AppendQ4Job& j, const float* 
 // memory, not by registers. Rows come in segments of seg_rows (the whole tensor, or, of a
 // chunk longer than its ring, the last rows of each head), seg_tiles blocks each.
 template <int M, int ROPE>
-__global__ void __launch_bounds__(kRowThreads, 6) append_q4_kernel(AppendQ4Job j, int tr,
+__global__ void __launch_bounds__(kRowThreads, 7) append_q4_kernel(AppendQ4Job j, int tr,
                                                                    long seg_rows, int seg_tiles) {
   constexpr int D = 32 * M, REC = q4::record_bytes(M), P = REC / 16;
   constexpr int RW = q4::Lanes<M>::kRows, kWarps = kRowThreads / 32;
