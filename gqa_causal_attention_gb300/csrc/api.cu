@@ -1282,20 +1282,18 @@ int gqa_attn_decode_q4(const float* q, const void* cache, const int32_t* cache_l
   j.q = q; j.cache = static_cast<const uint8_t*>(cache); j.cache_len = cache_len;
   j.max_cache_len = max_cache_len; j.out = out; j.weights = weights; j.status = status;
   gqa::decode_q4_workspace(&j, workspace);
-  return cuda_status(gqa::launch_decode_q4(j, s));
+  return cuda_status(gqa::launch_decode_q4(j, gqa::StepQ4Args{}, s));
 }
 
 namespace {
-// Workspace of gqa_attn_decode_step_q4: rotated q [B, H, D] | cache lengths [B] | the
-// decode's.
+// Workspace of gqa_attn_decode_step_q4: cache lengths [B] | the decode's.
 struct StepQ4Layout {
-  size_t cl, part, total;
+  size_t part, total;
 };
 StepQ4Layout step_q4_layout(int B, int H, int Hkv, int D, int len, int window, bool weights,
                             bool bound) {
   StepQ4Layout y{};
-  y.cl = round256((size_t)B * H * D * sizeof(float));
-  y.part = y.cl + round256((size_t)B * sizeof(int32_t));
+  y.part = round256((size_t)B * sizeof(int32_t));
   y.total = y.part + round256(gqa::decode_q4_bytes(B, H, Hkv, D, len, window, weights, bound));
   return y;
 }
@@ -1323,7 +1321,7 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
   if (!rope_params_ok(rp, D)) return ATTN_ERR_PARAM;
   if (B == 0) return ATTN_OK;
   if (!q || !k || !v || !out || !start || !table || !cache) return ATTN_ERR_NULL;
-  gqa::PrepQ4Job p{};
+  gqa::StepQ4Args p{};
   if (const int rc = q4_append_check(rp, table, k_norm_w, norm_eps, D, 1, max_start, pos, max_pos,
                                      capacity, window, &p.kv))
     return rc;
@@ -1347,13 +1345,11 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
   if (const int rc = fin.gate(status, s, &j.skip)) return rc;
   p.kv.k = k; p.kv.v = v; p.kv.cache = static_cast<uint8_t*>(cache);
   p.kv.B = B; p.kv.Hkv = Hkv; p.kv.start = start; p.kv.status = status; p.kv.skip = j.skip;
-  p.q = q; p.qrot = reinterpret_cast<float*>(ws); p.q_norm_w = q_norm_w;
-  p.cache_len = reinterpret_cast<int32_t*>(ws + lay.cl); p.H = H;
-  if (const cudaError_t e = gqa::launch_prep_q4(p, s); e != cudaSuccess) return cuda_status(e);
-  j.q = p.qrot; j.cache = p.kv.cache; j.cache_len = p.cache_len;
+  p.q_norm_w = q_norm_w; p.cache_len = reinterpret_cast<int32_t*>(ws);
+  j.q = q; j.cache = p.kv.cache; j.cache_len = p.cache_len;
   j.max_cache_len = max_start + 1; j.out = out; j.weights = weights; j.status = status;
   gqa::decode_q4_workspace(&j, ws + lay.part);
-  return cuda_status(gqa::launch_decode_q4(j, s));
+  return cuda_status(gqa::launch_decode_q4(j, p, s));
 }
 
 int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* cache_len,

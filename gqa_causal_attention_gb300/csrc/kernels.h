@@ -419,17 +419,20 @@ void decode_q4_plan(int B, int H, int Hkv, int max_cache_len, int window, int* n
 size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights,
                        bool bound);
 void decode_q4_workspace(DecodeQ4Job* j, void* workspace);   // plan and pointers into it
-cudaError_t launch_decode_q4(const DecodeQ4Job& j, cudaStream_t stream);
 
-// A decode step's first pass: the rows' q normed and rotated, their k and v appended.
-struct PrepQ4Job {
-  AppendQ4Job kv;           // L = 1
-  const float* q;           // [B, H, D] raw
-  float* qrot;              // [B, H, D]
+// A whole decode step (kv.k != nullptr): j.q is the raw q, normed and rotated by the blocks
+// that use it; the warp whose tile holds the new token's slot appends it first (kv: L = 1,
+// no k_out); cache_len[b] = start[b] + 1 is written for the second pass, 0 for a row that is
+// skipped (DecodeQ4Job::cache_len points to it).
+struct StepQ4Args {
+  AppendQ4Job kv;
   const float* q_norm_w;
-  int32_t* cache_len;       // [B] out: start + 1, 0 for a row that is skipped
-  int H;
+  int32_t* cache_len;       // [B]
 };
-cudaError_t launch_prep_q4(const PrepQ4Job& j, cudaStream_t stream);
+cudaError_t launch_decode_q4(const DecodeQ4Job& j, const StepQ4Args& step, cudaStream_t stream);
+// Its split kernel, for head dims up to 128 and above.
+cudaError_t launch_decode_q4_narrow(const DecodeQ4Job& j, const StepQ4Args& step, cudaStream_t stream);
+cudaError_t launch_decode_q4_wide(const DecodeQ4Job& j, const StepQ4Args& step, cudaStream_t stream);
+
 
 }  // namespace gqa
