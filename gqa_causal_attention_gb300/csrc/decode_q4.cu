@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   const int G = j.H / j.Hkv;
   const long row0 = static_cast<long>(b) * j.H + hkv * G;
   float* w = j.weights + bh * j.capacity + n;
+  const float before = n < nlive ? *w : 0.f;
   float sum = 0.f;
   for (int g0 = 0; g0 < G; g0 += 8) {
     const int heads = min(8, G - g0);
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
       if (h < heads) sum = fmaf(ex2(s[h] - sh[h].x), sh[h].y, sum);
     __syncthreads();
   }
-  if (n < nlive) *w += sum;
+  if (n < nlive) *w = before + sum;
 }
 
 int eff_len(int max_cache_len, int window) {

@@ -240,6 +240,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+constexpr int kFew = 256;                    // keys sharing the threshold's top bits, at most
 constexpr int kSelItems = 4;                 // slots per thread and compaction tile
 constexpr int kSelKeys = 40960;              // keys held in shared memory at most (160 KB)
 
@@ -268,15 +269,15 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum, uint3
 // One block per (row, head): the need-th largest of the old slots' keys, then one ordered
 // pass that writes the kept slots' numbers and weights. The largest by its top eleven bits
 // (a histogram of them, summed from the top); then among the few keys that share those,
-// gathered, bit by bit; where they are more than a thread each, by histograms of the next
-// eleven and ten bits. The keys are read once from memory where they fit in shared memory,
+// gathered, by counting for each how many are larger; where they are not few, by histograms
+// of the next eleven and ten bits. The keys are read once from memory where they fit in shared memory,
 // else again from L2 in each pass. Latency counts here: it is one block's chain of barriers.
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held) {
   constexpr int kSelBins = 2048 / kSelThreads;
   extern __shared__ uint32_t keys[];
   __shared__ uint32_t hist[2048];
-  __shared__ uint32_t few[kSelThreads];
+  __shared__ __align__(16) uint32_t few[kFew];
   __shared__ uint32_t wsum[32];
   __shared__ uint32_t found_bin, found_left, found_count, gathered;
   dependents_may_launch();
@@ -352,26 +353,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
       T |= found_bin << shift;
       left = found_left;
       const uint32_t count = found_count;
-      if (pass == 0 && count <= kSelThreads) {
+      if (pass == 0 && count <= kFew) {
         for (int i = tid; i < old; i += kSelThreads) {
           const uint32_t k = key_of(i);
           if (k >> 21 == T >> 21) few[atomicAdd(&gathered, 1u)] = k;
         }
+        if (tid >= static_cast<int>(count) && tid < kFew) few[tid] = 0;    // below every old key
         __syncthreads();
-        const uint32_t k = tid < count ? few[tid] : 0u;
-        bool in = tid < count;
-#pragma unroll 1
-        for (int bit = 20; bit >= 0; --bit) {
-          const bool set = k >> bit & 1u;
-          const uint32_t c = __syncthreads_count(in && set);
-          if (c >= left) {
-            T |= 1u << bit;
-            in = in && set;
-          } else {
-            left -= c;
-            in = in && !set;
+        if (tid < static_cast<int>(count)) {
+          const uint32_t k = few[tid];
+          uint32_t more = 0, same = 0;
+          for (uint32_t i = 0; i < count; i += 4) {
+            const uint4 f = *reinterpret_cast<const uint4*>(few + i);
+            more += (f.x > k) + (f.y > k) + (f.z > k) + (f.w > k);
+            same += (f.x == k) + (f.y == k) + (f.z == k) + (f.w == k);
+          }
+          if (more < left && more + same >= left) {       // threads that agree on the key
+            found_bin = k;
+            found_left = left - more;
           }
         }
+        __syncthreads();
+        T = found_bin;
+        left = found_left;
         break;
       }
     }
