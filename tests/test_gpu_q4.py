@@ -665,3 +665,133 @@ def test_finite_check_covers_the_q4_calls():
             g.gqa_attn_decode_q4(q, cache, i32([8]), n, out)
     finally:
         g.attn_set_check_finite(prev)
+
+
+# ---------------------------------------------------------------- calls and shapes
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    """A step with weights (or in a ring), then a decode over the same cache, at drawn shapes."""
+    gen = torch.Generator().manual_seed(seed)
+    pick = lambda *xs: xs[int(torch.randint(len(xs), (1,), generator=gen))]  # noqa: E731
+    D, G, Hkv, B = pick(32, 64, 96, 128, 160, 192, 224, 256), pick(1, 2, 3, 4, 5, 8, 9, 16), pick(1, 2, 3), pick(1, 2, 5)
+    H, R = G * Hkv, pick(D, D // 2, 2, D - 2)
+    cap = pick(1, 33, 130, 513, 2049)
+    ring = seed % 3 == 0
+    window, norm, softcap = cap if ring else 0, seed % 2 == 0, pick(0.0, 20.0)
+    cache, kc, vc = filled(seed, B, Hkv, cap, D)
+    hi = 3000 if ring else cap
+    start = torch.randint(0, hi, (B,), generator=gen).tolist()
+    pos = torch.randint(0, 4000, (B,), generator=gen).tolist()
+    rp, table, tab = table_of(4000, R, D)
+    q, k, v = (syn.normal(seed + 100, n, (B, h, 1, D)) for n, h in (("q", H), ("k", Hkv), ("v", Hkv)))
+    qn, kn = (syn.norm_weight(seed, n, D) if norm else None for n in ("qn", "kn"))
+    cu = lambda t: None if t is None else t.to(dev())  # noqa: E731
+    live = [min(s + 1, cap) for s in start]
+    for b in range(B):
+        cache[b, :, live[b]:] = 255
+    out, st = torch.full((B, H, 1, D), math.nan, device=dev()), status()
+    w = None if ring else torch.zeros(B, Hkv, cap, device=dev())
+    g.gqa_attn_decode_step_q4(cu(q), cu(k), cu(v), out, cache, i32(start), max(start), rp, table,
+                              cu(qn), cu(kn), pos=i32(pos), max_pos=max(pos), weights=w,
+                              window=window, softcap=softcap, status=st)
+    y, qr = ref.rotate(k, pos, tab, kn), ref.rotate(q, pos, tab, qn)
+    for b in range(B):
+        slot = start[b] % cap
+        kc[b, :, slot], vc[b, :, slot] = ref.stands_for(y)[b, :, 0], ref.stands_for(v)[b, :, 0]
+    want, ww, S = ref.decode(qr, kc, vc, live, softcap)
+    tol = 2e-6 * (1 + S / math.log(2))
+    assert value(st) == 0
+    close(out, want, tol * float(vc.abs().max()))
+    if w is not None:
+        close(w, ww, tol * G + tol)
+    got = torch.empty_like(out)
+    g.gqa_attn_decode_q4(qr.float().to(dev()), cache, i32([s + 1 for s in start]), max(start) + 1, got,
+                         window=window, softcap=softcap, status=st)
+    assert value(st) == 0
+    close(got, want, tol * float(vc.abs().max()))
+
+
+def test_workspace_of_a_longer_length_serves_a_shorter_one():
+    B, H, Hkv, D, cap = 3, 16, 2, 64, 4000
+    cache, k, v = filled(4, B, Hkv, cap, D)
+    q = syn.normal(4, "q", (B, H, 1, D))
+    ws = torch.empty(g.gqa_attn_decode_q4_workspace_size(B, H, Hkv, D, cap, 0, True), dtype=torch.uint8, device=dev())
+    for n in (1, 32, 513, 700, 2048, 4000):
+        out, st = torch.empty(B, H, 1, D, device=dev()), status()
+        w = torch.zeros(B, Hkv, cap, device=dev())
+        ws.fill_(255)
+        g.gqa_attn_decode_q4(q.to(dev()), cache, i32([n, max(1, n // 2), 1]), n, out, weights=w, workspace=ws, status=st)
+        assert value(st) == 0
+        want, ww, S = ref.decode(q, k, v, [n, max(1, n // 2), 1])
+        close(out, want, 2e-6 * (1 + S / math.log(2)) * float(v.abs().max()))
+        close(w, ww, 2e-6 * (1 + S / math.log(2)) * 9)
+
+
+def test_binding_refuses_what_does_not_fit():
+    B, H, Hkv, D, cap = 2, 4, 2, 64, 16
+    d = dev()
+    cache = torch.zeros(B, Hkv, cap, 80, dtype=torch.uint8, device=d)
+    q, out = torch.zeros(B, H, 1, D, device=d), torch.zeros(B, H, 1, D, device=d)
+    k = torch.zeros(B, Hkv, 1, D, device=d)
+    cl, w = i32([1, 1]), torch.zeros(B, Hkv, cap, device=d)
+    rp, table, _ = table_of(32, D, D)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=d)
+    dec = lambda **x: g.gqa_attn_decode_q4(**{**dict(q=q, cache=cache, cache_len=cl, max_cache_len=4, out=out, workspace=ws), **x})  # noqa: E731
+    app = lambda **x: g.kv_cache_append_q4(**{**dict(k=k, v=k, cache=cache, start=cl, max_start=1), **x})  # noqa: E731
+    dec(), app()
+    for bad in (dict(q=q.half()), dict(cache=cache.view(torch.int8)), dict(cache_len=cl.long()), dict(status=torch.zeros(1, device=d)),
+                dict(q=None), dict(max_cache_len="4")):
+        with pytest.raises(TypeError):
+            dec(**bad)
+    for bad in (dict(q=q.cpu()), dict(q=q[:, :2]), dict(out=out[..., :32]), dict(cache=cache[:1]), dict(cache=cache[..., :72]),
+                dict(cache_len=i32([1])), dict(weights=w[:, :, :8]), dict(workspace=ws.cpu()), dict(workspace=ws[::2]),
+                dict(q=torch.zeros(B, H, 2, D, device=d), out=torch.zeros(B, H, 2, D, device=d)),
+                dict(status=torch.zeros(0, dtype=torch.int32, device=d))):
+        with pytest.raises(ValueError):
+            dec(**bad)
+    for bad in (dict(v=k[:, :1]), dict(k_out=torch.zeros(B, Hkv, 2, D, device=d)), dict(pos=i32([1])),
+                dict(params=rp, table=table[:10]), dict(params=rp, table=table, k_norm_w=torch.ones(32, device=d)),
+                dict(k=k.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            app(**bad)
+    with pytest.raises(g.AttnError):
+        dec(workspace=ws[:0], max_cache_len=17)
+    with pytest.raises(g.AttnError):
+        app(max_start=16)
+    with pytest.raises(TypeError):
+        app(params=b"no", table=table)
+
+
+def test_empty_batches_are_no_ops():
+    d, e = dev(), lambda *s: torch.zeros(*s, device=dev())  # noqa: E731
+    cache = torch.zeros(0, 2, 8, 80, dtype=torch.uint8, device=d)
+    none = torch.zeros(0, dtype=torch.int32, device=d)
+    g.kv_cache_append_q4(e(0, 2, 3, 64), e(0, 2, 3, 64), cache, none, 0)
+    g.kv_cache_read_q4(cache, e(0, 2, 3, 64), e(0, 2, 3, 64), none, 0)
+    g.gqa_attn_decode_q4(e(0, 4, 1, 64), cache, none, 1, e(0, 4, 1, 64), workspace=e(4))
+    g.kv_cache_evict_q4(cache, e(0, 2, 8), none, 8, 4, 1, cache.clone(), e(0, 2, 8),
+                        torch.zeros(0, 2, 4, dtype=torch.int32, device=d), none.clone())
+    full = torch.full((1, 2, 8, 80), 7, dtype=torch.uint8, device=d)
+    g.kv_cache_append_q4(e(1, 2, 0, 64), e(1, 2, 0, 64), full, i32([8]), 8)
+    torch.cuda.synchronize()
+    assert bool((full == 7).all())
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Every call takes a stream; without a workspace, one is kept alive until it has passed."""
+    B, H, Hkv, D, cap, n = 2, 8, 2, 128, 3000, 2900
+    cache, k, v = filled(21, B, Hkv, cap, D)
+    q = syn.normal(1, "q", (B, H, 1, D)).to(dev())
+    want = torch.empty_like(q)
+    g.gqa_attn_decode_q4(q, cache, i32([n, n]), n, want)
+    cl = i32([n, n])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = [torch.zeros_like(q) for _ in range(20)]
+    torch.cuda.synchronize()
+    for o in outs:
+        g.gqa_attn_decode_q4(q, cache, cl, n, o, stream=s)
+        torch.empty(1 << 22, dtype=torch.uint8, device=dev()).fill_(255)   # would reuse a freed workspace
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
