@@ -9,7 +9,42 @@ namespace {
 
 constexpr int kMaxSplits = 152 * 4;          // of one row: no more than blocks on the GPU at once
 
-// Blocks [0, rows): one query row's splits merged, a split per warp at a time. Blocks after:
+constexpr int kFewSplits = 8;
+
+// One query row's few splits by one warp: every load is on its way before the first factor is
+// known, and no barrier is met.
+__device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml, long row, int lane) {
+  const int nlive = live_slots(j, j.cache_len[row / j.H], false);
+  if (nlive <= j.chunk) return;              // finished by its one split, or invalid
+  const int ns = (nlive + j.chunk - 1) / j.chunk;
+  const float* part = j.partial + row * j.nsplit * j.D;
+  const float2 t = lane < ns ? ml[row * j.nsplit + lane] : make_float2(-INFINITY, 0.f);
+  for (int d0 = 0; d0 < j.D; d0 += 128) {
+    const int d = d0 + 4 * lane;
+    float4 p[kFewSplits];
+#pragma unroll
+    for (int s = 0; s < kFewSplits; ++s)
+      if (s < ns && d < j.D)
+        p[s] = *reinterpret_cast<const float4*>(part + static_cast<long>(s) * j.D + d);
+    const float m = warp_max(t.x), f = t.x == -INFINITY ? 0.f : ex2(t.x - m);
+    const float inv = 1.0f / warp_sum(f * t.y);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kFewSplits; ++s) {
+      const float fs = __shfl_sync(0xffffffffu, f, s);
+      if (s < ns && fs != 0.f) {             // 0: a split whose scores were all -inf
+        y.x = fmaf(fs, p[s].x, y.x); y.y = fmaf(fs, p[s].y, y.y);
+        y.z = fmaf(fs, p[s].z, y.z); y.w = fmaf(fs, p[s].w, y.w);
+      }
+    }
+    if (d < j.D)
+      *reinterpret_cast<float4*>(j.out + row * j.D + d) =
+          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  }
+}
+
+// Blocks [0, rows): one query row's splits merged, a split per warp at a time; with few
+// splits eight rows, one a warp. Blocks after:
 // with weights, 256 slots of one kv head get the sum over its query heads of
 // 2^(score - reference) / sum (one thread per slot, heads in order, so the result does not
 // depend on timing).
@@ -25,6 +60,11 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float2* ml = reinterpret_cast<const float2*>(j.partial + static_cast<long>(j.B) * j.H * j.nsplit * j.D);
   if (blockIdx.x < rows) {
+    if (j.nsplit <= kFewSplits) {
+      const long r = static_cast<long>(blockIdx.x) * 8 + warp;
+      if (r < static_cast<long>(j.B) * j.H) merge_few(j, ml, r, lane);
+      return;
+    }
     const long row = blockIdx.x;
     const int nlive = live_slots(j, j.cache_len[row / j.H], false);
     if (nlive <= j.chunk) return;            // finished by its one split, or invalid
@@ -205,7 +245,8 @@ cudaError_t launch_decode_q4(const DecodeQ4Job& j, const StepQ4Args& st, cudaStr
   const cudaError_t e = j.D <= 128 ? launch_decode_q4_narrow(j, st, stream)
                                    : launch_decode_q4_wide(j, st, stream);
   if (e != cudaSuccess || (j.nsplit == 1 && !j.weights)) return e;
-  const unsigned rows = j.nsplit > 1 ? static_cast<unsigned>(j.B) * j.H : 0;
+  const unsigned heads = static_cast<unsigned>(j.B) * j.H;
+  const unsigned rows = j.nsplit == 1 ? 0 : (j.nsplit <= kFewSplits ? (heads + 7) / 8 : heads);
   const unsigned per = j.weights ? (eff_len(j.max_cache_len, j.window) - 1) / 256 + 1 : 0;
   return launch_dependent(decode_q4_finish_kernel, rows + static_cast<unsigned>(j.B) * j.Hkv * per,
                           256, 0, stream, j, rows, per ? per : 1u);
