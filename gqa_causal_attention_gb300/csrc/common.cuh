@@ -22,9 +22,9 @@ __device__ __forceinline__ bool gated_off(const int32_t* skip) {
 // A kernel launched by launch_dependent may start while the one enqueued before it still
 // runs, whatever that one is: it must call dependent_wait before its first access to global
 // memory, which returns when everything before has ended and its writes are visible. With
-// dependents_may_launch a kernel lets the next one be placed already when all of its own
-// blocks have started. (Every kernel of the 4-bit cache does both: they are short, and
-// between two of them the launch otherwise costs about 2 us.)
+// dependents_may_launch a kernel lets the next one be placed once all of its own blocks have
+// got there. (Every kernel of the 4-bit cache waits this way: they are short, and between
+// two of them the launch otherwise costs about 2 us.)
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependents_may_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -54,7 +54,6 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   __shared__ float red[8];
   __shared__ __align__(16) float acc[8][kMaxHeadDim];
   __shared__ float2 sh[8];
-  dependents_may_launch();
   dependent_wait();
   if (gated_off(j.skip)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

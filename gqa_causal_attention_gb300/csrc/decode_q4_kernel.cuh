@@ -225,7 +225,6 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   __shared__ float q_factor[kHeads];
   __shared__ float sm_m[NW][kHeads], sm_l[NW][kHeads];
   __shared__ int abort_flag;
-  dependents_may_launch();
   dependent_wait();
   if (gated_off(j.skip)) return;
 
@@ -573,6 +572,10 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
     report(j.status, ATTN_DEV_TIMEOUT);
   }
 
+  // Only now: blocks of the next kernel placed earlier would take the free places of the SMs
+  // that got fewer of these, and spread unevenly themselves (one row of 131072 slots, 19
+  // splits, repeated: 92 us instead of 60).
+  dependents_may_launch();
   // The warps' sums, brought to one reference, meet in the (now idle) rings.
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
