@@ -1238,7 +1238,7 @@ size_t gqa_attn_decode_q4_workspace_size(int B, int H, int Hkv, int D, int max_c
   if (B < 1 || !q4_dims_ok(B, H, Hkv, 1, D) || !q4_grid_ok(B, H) || max_cache_len < 1 ||
       window < 0)
     return 0;
-  return gqa::decode_q4_bytes(B, H, Hkv, D, max_cache_len, window, with_weights != 0, true);
+  return gqa::decode_q4_bytes(B, H, Hkv, D, max_cache_len, window, with_weights != 0);
 }
 
 namespace {
@@ -1268,8 +1268,8 @@ int gqa_attn_decode_q4(const float* q, const void* cache, const int32_t* cache_l
   if (window == 0 && max_cache_len > capacity) return ATTN_ERR_CAPACITY;
   if (!q || !cache || !cache_len || !out) return ATTN_ERR_NULL;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return ATTN_ERR_ALIGN;
-  const size_t need =
-      gqa::decode_q4_bytes(B, H, Hkv, D, max_cache_len, window, weights != nullptr, false);
+  j.max_cache_len = max_cache_len; j.weights = weights;
+  const size_t need = gqa::decode_q4_prepare(&j);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
@@ -1280,23 +1280,14 @@ int gqa_attn_decode_q4(const float* q, const void* cache, const int32_t* cache_l
   fin.add_q4(cache, B, Hkv, capacity, D, gqa::kFiniteCache, cache_len, window, 0);
   if (const int rc = fin.gate(status, s, &j.skip)) return rc;
   j.q = q; j.cache = static_cast<const uint8_t*>(cache); j.cache_len = cache_len;
-  j.max_cache_len = max_cache_len; j.out = out; j.weights = weights; j.status = status;
+  j.out = out; j.status = status;
   gqa::decode_q4_workspace(&j, workspace);
   return cuda_status(gqa::launch_decode_q4(j, gqa::StepQ4Args{}, s));
 }
 
 namespace {
-// Workspace of gqa_attn_decode_step_q4: cache lengths [B] | the decode's.
-struct StepQ4Layout {
-  size_t part, total;
-};
-StepQ4Layout step_q4_layout(int B, int H, int Hkv, int D, int len, int window, bool weights,
-                            bool bound) {
-  StepQ4Layout y{};
-  y.part = round256((size_t)B * sizeof(int32_t));
-  y.total = y.part + round256(gqa::decode_q4_bytes(B, H, Hkv, D, len, window, weights, bound));
-  return y;
-}
+// Workspace of gqa_attn_decode_step_q4: cache lengths [B], then the decode's.
+size_t step_q4_part(int B) { return round256((size_t)B * sizeof(int32_t)); }
 }  // namespace
 
 size_t gqa_attn_decode_step_q4_workspace_size(int B, int H, int Hkv, int D, int32_t max_start,
@@ -1304,7 +1295,8 @@ size_t gqa_attn_decode_step_q4_workspace_size(int B, int H, int Hkv, int D, int3
   if (B < 1 || !q4_dims_ok(B, H, Hkv, 1, D) || !q4_grid_ok(B, H) || max_start < 0 ||
       max_start == 0x7fffffff || window < 0)
     return 0;
-  return step_q4_layout(B, H, Hkv, D, max_start + 1, window, with_weights != 0, true).total;
+  return step_q4_part(B) +
+         round256(gqa::decode_q4_bytes(B, H, Hkv, D, max_start + 1, window, with_weights != 0));
 }
 
 int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, float* out, int B,
@@ -1329,9 +1321,9 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
       !aligned16(cache) || (q_norm_w && !aligned16(q_norm_w)) ||
       (k_norm_w && !aligned16(k_norm_w)))
     return ATTN_ERR_ALIGN;
-  const StepQ4Layout lay =
-      step_q4_layout(B, H, Hkv, D, max_start + 1, window, weights != nullptr, false);
-  if (!workspace || workspace_bytes < lay.total) return ATTN_ERR_WORKSPACE;
+  j.max_cache_len = max_start + 1; j.weights = weights;
+  const size_t part = step_q4_part(B);
+  if (!workspace || workspace_bytes < part + gqa::decode_q4_prepare(&j)) return ATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1347,8 +1339,8 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
   p.kv.B = B; p.kv.Hkv = Hkv; p.kv.start = start; p.kv.status = status; p.kv.skip = j.skip;
   p.q_norm_w = q_norm_w; p.cache_len = reinterpret_cast<int32_t*>(ws);
   j.q = q; j.cache = p.kv.cache; j.cache_len = p.cache_len;
-  j.max_cache_len = max_start + 1; j.out = out; j.weights = weights; j.status = status;
-  gqa::decode_q4_workspace(&j, ws + lay.part);
+  j.out = out; j.status = status;
+  gqa::decode_q4_workspace(&j, ws + part);
   return cuda_status(gqa::launch_decode_q4(j, p, s));
 }
 

@@ -7,7 +7,8 @@ namespace gqa {
 
 namespace {
 
-constexpr int kMaxSplits = 152 * 4;          // of one row: no more than blocks on the GPU at once
+constexpr int kSms = 152;
+constexpr int kMaxSplits = 8 * kSms;           // of one row: no more than blocks on the GPU at once
 
 constexpr int kFewSplits = 8;
 
@@ -156,54 +157,62 @@ int eff_len(int max_cache_len, int window) {
   return window > 0 && window < max_cache_len ? window : max_cache_len;
 }
 
-// Splits a row may get, whatever its length. With few rows: one wave of blocks, as many as
-// fit, if that loads the SMs evenly (one row of 131072 slots with 8 kv heads and 8 query
-// heads each, 3 blocks an SM: 57 splits 46.8 us, 38 48.1, 76 63.8, for a second wave goes to
-// whichever SMs end first). Otherwise 10 to 20 blocks an SM, which even out rows of
-// different lengths, and of those the count that leaves the busiest SM the least extra (64
-// rows of up to 8192 slots with 8 kv heads: 1 split 86.4 us, 2 84.0, 4 76.4, 8 77.5, 16 85.2).
-int most_splits(int B, int H, int Hkv) {
-  constexpr int kSms = 152;
+// The most splits a plan takes: one wave of blocks, or up to twenty blocks an SM in at most
+// twenty splits.
+int most_splits(int B, int H, int Hkv, int D) {
   const long units = units_of(B, H, Hkv);
   if (units < 1) return 1;
-  const long resident = kSms * resident_blocks(4, head_tiles(H, Hkv));
-  if (units <= resident) {
-    const long n = resident / units, blocks = n * units;
-    if (20 * blocks >= 19 * kSms * ((blocks + kSms - 1) / kSms)) return static_cast<int>(n);
-  }
-  long best = 1;
-  double least = 1e30;
-  for (long n = 1; n == 1 || n * units <= 20 * kSms; ++n) {
-    if (n * units < 10 * kSms && (n + 1) * units <= 20 * kSms) continue;
-    const double per = static_cast<double>(n * units) / kSms;
-    const double extra = ((n * units + kSms - 1) / kSms) / per * (1.0 + 0.004 * per);
-    if (extra < least) {
-      least = extra;
-      best = n;
-    }
-  }
-  return static_cast<int>(best);
+  const long resident = kSms * resident_blocks(D / 32, head_tiles(H, Hkv));
+  long n = resident / units, many = 20 * kSms / units;
+  if (many > 20) many = 20;
+  if (n < many) n = many;
+  return static_cast<int>(n < 1 ? 1 : n);
 }
 
 // The most splits of any length up to this one: it does not shrink as the length grows.
 // Up to 16 tiles stay in one block: the second launch costs what the split saves.
-int split_bound(int B, int H, int Hkv, int max_cache_len, int window) {
+int split_bound(int B, int H, int Hkv, int D, int max_cache_len, int window) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
   if (tiles <= kShortTiles) return 1;
   const int most = (tiles + kWarps - 1) / kWarps;             // a tile for every warp
-  const int want = most_splits(B, H, Hkv);
+  const int want = most_splits(B, H, Hkv, D);
   return want < most ? want : most;
 }
 
 }  // namespace
 
-void decode_q4_plan(int B, int H, int Hkv, int max_cache_len, int window, int* nsplit,
+// The split count whose time, in tiles of one SM at full load, comes out least:
+//   k (per + 6) / r   k blocks on the busiest SM, each of `per` tiles (whole rounds of its
+//                     warps) and a start and an end worth 6; r: what one block alone (0.65)
+//                     or two (0.93) reach of an SM's rate
+//   x 1.25            for a last wave that is not full: its blocks go to whichever SMs end first
+//   + 6 or 12         the second launch, with few splits or many.
+// Measured (us): one row of 131072 slots, 8 kv heads of 8: 38 splits 48.1, 57 46.8, 76 60.7;
+// 8 rows of up to 4000: 2 21.8, 4 18.8, 7 17.6, 14 25.3; 64 rows of 512..8192, 8 kv heads of
+// 4: 1 89.3, 2 82.5, 4 72.8, 8 73.8, 16 90.9; 8 rows of 4096, D = 256, 8 kv heads of 2: 2 27.3,
+// 4 23.8, 6 31.8, 8 27.1.
+void decode_q4_plan(int B, int H, int Hkv, int D, int max_cache_len, int window, int* nsplit,
                     int* chunk) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
-  const int n = split_bound(B, H, Hkv, max_cache_len, window);
-  const int per = (tiles + n - 1) / n;
-  *chunk = per * kTile;
-  *nsplit = (tiles + per - 1) / per;
+  const int bound = split_bound(B, H, Hkv, D, max_cache_len, window);
+  const long units = units_of(B, H, Hkv);
+  const int resident = resident_blocks(D / 32, head_tiles(H, Hkv));
+  double least = 1e30;
+  int best = tiles;
+  for (int n = 1, per = tiles; n <= bound; n = per > 1 ? (tiles + per - 2) / (per - 1) : bound + 1) {
+    per = (tiles + n - 1) / n;               // the next n is the first with fewer tiles a block
+    const long k = (units * n + kSms - 1) / kSms;
+    const double rate = k == 1 ? 0.65 : (k == 2 ? 0.93 : 1.0);
+    const double wave = k > resident && k < 2 * resident ? 1.25 : 1.0;
+    const double time = k * ((per + kWarps - 1) / kWarps * kWarps + 6) / rate * wave +
+                        (n == 1 ? 0 : (n <= kFewSplits ? 6 : 12));
+    if (time < least) {
+      least = time;
+      best = per;
+    }
+  }
+  *chunk = best * kTile;
+  *nsplit = (tiles + best - 1) / best;
 }
 
 namespace {
@@ -223,21 +232,24 @@ Layout layout(int B, int H, int D, int nsplit, int eff, bool weights) {
 }
 }  // namespace
 
-size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights,
-                       bool bound) {
-  int nsplit, chunk;
-  decode_q4_plan(B, H, Hkv, max_cache_len, window, &nsplit, &chunk);
-  if (bound) nsplit = split_bound(B, H, Hkv, max_cache_len, window);
-  return layout(B, H, D, nsplit, eff_len(max_cache_len, window), weights).total;
+size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights) {
+  return layout(B, H, D, split_bound(B, H, Hkv, D, max_cache_len, window),
+                eff_len(max_cache_len, window), weights).total;
+}
+
+size_t decode_q4_prepare(DecodeQ4Job* j) {
+  decode_q4_plan(j->B, j->H, j->Hkv, j->D, j->max_cache_len, j->window, &j->nsplit, &j->chunk);
+  const Layout y = layout(j->B, j->H, j->D, j->nsplit, eff_len(j->max_cache_len, j->window),
+                          j->weights != nullptr);
+  j->pitch = y.pitch;
+  j->scores_at = y.scores;
+  return y.total;
 }
 
 void decode_q4_workspace(DecodeQ4Job* j, void* workspace) {
-  decode_q4_plan(j->B, j->H, j->Hkv, j->max_cache_len, j->window, &j->nsplit, &j->chunk);
-  const Layout y = layout(j->B, j->H, j->D, j->nsplit, eff_len(j->max_cache_len, j->window),
-                          j->weights != nullptr);
   j->partial = static_cast<float*>(workspace);
-  j->scores = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + y.scores) : nullptr;
-  j->pitch = y.pitch;
+  j->scores = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + j->scores_at)
+                        : nullptr;
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Job& j, const StepQ4Args& st, cudaStream_t stream) {

@@ -145,10 +145,12 @@ __device__ __forceinline__ float unit_scale(uint32_t w, int odd) {     // bf16 h
 
 constexpr int kStages = 2;
 
-// Blocks an SM holds: what the registers leave (116 at D = 128 with one column tile, 162
-// with two).
+// Blocks an SM holds: what registers (117 a thread at D = 128 with NT = 1, 163 with 2) and,
+// from D = 192, shared memory leave. Twenty warps an SM instead of sixteen were no faster at
+// D = 128.
 __host__ __device__ constexpr int resident_blocks(int M, int NT) {
-  return M > 4 ? 2 : (NT == 1 ? 4 : 3);
+  constexpr int blocks[2][8] = {{8, 6, 5, 4, 4, 3, 3, 2}, {5, 4, 3, 3, 3, 2, 2, 2}};
+  return blocks[NT - 1][M - 1];
 }
 
 // Rings of all warps, then the queries' B fragments.

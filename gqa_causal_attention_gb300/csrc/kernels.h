@@ -410,15 +410,16 @@ struct DecodeQ4Job {
   float* partial;           // [B * H * nsplit, D] outputs, then (m, l) pairs
   float* scores;            // weights only: [B * H, pitch] scores in log2 units
   int nsplit, chunk, pitch;
+  size_t scores_at;
   int32_t* status;
   const int32_t* skip = nullptr;
 };
-void decode_q4_plan(int B, int H, int Hkv, int max_cache_len, int window, int* nsplit, int* chunk);
-// Workspace of a decode: its partials (for exactly this length, or the most for any
-// length up to it) and, with weights, its scores.
-size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights,
-                       bool bound);
-void decode_q4_workspace(DecodeQ4Job* j, void* workspace);   // plan and pointers into it
+// Workspace that serves every length up to this one.
+size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights);
+// Plans j (sizes, max_cache_len and weights set): splits and pitch; returns the workspace
+// bytes it takes. Then its pointers into a workspace.
+size_t decode_q4_prepare(DecodeQ4Job* j);
+void decode_q4_workspace(DecodeQ4Job* j, void* workspace);
 
 // A whole decode step (kv.k != nullptr): j.q is the raw q, normed and rotated by the blocks
 // that use it; the warp whose tile holds the new token's slot appends it first (kv: L = 1,
