@@ -45,10 +45,10 @@ __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml
 }
 
 // Blocks [0, rows): one query row's splits merged, a split per warp at a time; with few
-// splits eight rows, one a warp. Blocks after:
-// with weights, 256 slots of one kv head get the sum over its query heads of
-// 2^(score - reference) / sum (one thread per slot, heads in order, so the result does not
-// depend on timing).
+// splits eight rows, one a warp. Blocks after: with weights, 256 slots of one kv head get the
+// sum over its query heads of 2^(score - reference) / sum (one thread per slot, heads in
+// order, so the result does not depend on timing). A few us, bound by its chain of loads:
+// merging 64 splits one after the other in a thread took 19 us, a warp per split 5.
 __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, unsigned rows,
                                                                unsigned slot_blocks) {
   __shared__ float factor[kMaxSplits];

@@ -26,12 +26,17 @@
 // goes into q (1 / 16) and into the output dims. (The masked nibble alone is the fp16
 // subnormal u * 2^-24 and would do for a key without the subtraction, but the tensor
 // core aligns its products by the operands' exponent fields: ten bits of the sum were
-// lost, and outputs were off by 2.5e-6 instead of 3e-7.)
+// lost, and outputs were off by 2.5e-6 instead of 1.1e-7.)
 //
 // Each warp owns whole 32-key tiles and a ring of bulk copies of its own; nothing in
 // the loop waits for another warp. Products accumulate over one tile only (two
-// m16n8k16 steps) and are then added to the fp32 sums with rounding to nearest: the
-// tensor core truncates its sums, which over a long cache would drift.
+// m16n8k16 steps) and are then added to the fp32 sums: those round to nearest, the tensor
+// core's do not, and over a long cache that would drift.
+//
+// What bounds it: issue. A 32-key tile at D = 128 takes 658 instructions of a warp (304 of them
+// unpack), 2.7 a cycle and SM, with the memory at 60 % of its peak: 32 rows of 8192 slots, 32
+// heads over 8, 302 MB in 62 us, 4.9 TB/s. With 8 heads a kv head 864 a tile, 2.4 a cycle from
+// twelve warps an SM: one row of 131072 slots, 151 MB in 45 us.
 //
 // The reference of p is the running row maximum minus 14 plus the running exponent of
 // the value scales, so that p * sv peaks near 2^14 whatever the values' magnitude and
