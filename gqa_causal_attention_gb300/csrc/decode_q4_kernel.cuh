@@ -206,6 +206,35 @@ __device__ __forceinline__ void rotate_query(const float* row, const float2* tab
   }
   if (d0 >= D) return;
   const int half = R / 2;
+  if (half % 8 == 0) {                       // the eight dims lie within one half
+    float b[8], w[8], cs[16];
+    const bool rotary = d0 < R, low = d0 < half;
+    const int i = low ? d0 : d0 - half, p = low ? d0 + half : i;
+    if (rotary) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) load4(reinterpret_cast<const float*>(tab + i) + 4 * q, cs + 4 * q);
+      load4(row + p, b);
+      load4(row + p + 4, b + 4);
+    }
+    if (nw) {
+      load4(nw + d0, w);
+      load4(nw + d0 + 4, w + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+      if (rotary) {
+        load4(nw + p, w);
+        load4(nw + p + 4, w + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = b[e] * inv * w[e];
+      }
+    }
+    if (rotary) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = fmaf(x[e], cs[2 * e], (low ? -b[e] : b[e]) * cs[2 * e + 1]);
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int d = d0 + e;
