@@ -294,19 +294,24 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
                   &full[warp][s]);
   };
   if (step && row.slot >= k0 && row.slot < k1 && (row.slot - k0) / kTile % NW == warp) {
-    // This warp's tiles hold the new token's slot: it goes there first. (Every block of the
-    // kv head's query heads writes the same bytes.) The fence orders the writes before this
-    // warp's bulk copies.
+    // This warp's tiles hold the new token's slot: it goes there first. With more than 8 heads
+    // a kv head several blocks do this, so the record is finished in the (still idle) ring and
+    // only its final bytes, the same in each, reach the cache. The fence orders the writes
+    // there and the reads here before this warp's bulk copies.
     q4::Lanes<M> at(lane);
     at.in = at.in && at.row == 0;
     const float *x = st.kv.k + bh * D, *v = st.kv.v + bh * D;
     const float2* tab = st.kv.table + static_cast<long>(row.pos) * (st.kv.R / 2);
-    uint8_t* rec = st.kv.cache + (bh * j.capacity + row.slot) * REC;
-    const uint2 d = append_rows<M, kRopeDims>(st.kv, x, v, tab, rec, nullptr, at, lane, at.in);
+    const uint2 d = append_rows<M, kRopeDims>(st.kv, x, v, tab, ring, nullptr, at, lane, at.in);
+    __syncwarp();
     if (d.x)
-      q4::quantise_exact<M>(x, tab, st.kv.R, st.kv.norm_w, st.kv.norm_eps, lane, d.x, rec, 0);
-    if (d.y) q4::quantise_exact<M>(v, nullptr, 0, nullptr, 0.f, lane, d.y, rec, 1);
-    asm volatile("fence.proxy.async.global;" ::: "memory");
+      q4::quantise_exact<M>(x, tab, st.kv.R, st.kv.norm_w, st.kv.norm_eps, lane, d.x, ring, 0);
+    if (d.y) q4::quantise_exact<M>(v, nullptr, 0, nullptr, 0.f, lane, d.y, ring, 1);
+    __syncwarp();
+    if (lane < REC / 16)
+      reinterpret_cast<uint4*>(st.kv.cache + (bh * j.capacity + row.slot) * REC)[lane] =
+          reinterpret_cast<const uint4*>(ring)[lane];
+    asm volatile("fence.proxy.async;" ::: "memory");
     __syncwarp();
   }
   if (lane == 0) {
