@@ -33,7 +33,7 @@ __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml
 #pragma unroll
     for (int s = 0; s < kFewSplits; ++s) {
       const float fs = __shfl_sync(0xffffffffu, f, s);
-      if (s < ns && fs != 0.f) {             // 0: a split whose scores were all -inf
+      if (s < ns) {                          // a factor of 0 still passes on a NaN
         y.x = fmaf(fs, p[s].x, y.x); y.y = fmaf(fs, p[s].y, y.y);
         y.z = fmaf(fs, p[s].z, y.z); y.w = fmaf(fs, p[s].w, y.w);
       }
@@ -94,10 +94,8 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
       for (int s = warp; s < ns; s += 8) {
         const float f = factor[s];
         const float4 t = *reinterpret_cast<const float4*>(part + static_cast<long>(s) * j.D + d);
-        if (f != 0.f) {                      // 0: a split whose scores were all -inf
-          y.x = fmaf(f, t.x, y.x); y.y = fmaf(f, t.y, y.y);
-          y.z = fmaf(f, t.z, y.z); y.w = fmaf(f, t.w, y.w);
-        }
+        y.x = fmaf(f, t.x, y.x); y.y = fmaf(f, t.y, y.y);
+        y.z = fmaf(f, t.z, y.z); y.w = fmaf(f, t.w, y.w);
       }
       *reinterpret_cast<float4*>(&acc[warp][d]) = y;
     }

@@ -623,6 +623,8 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) l_run[t] += __shfl_xor_sync(0xffffffffu, l_run[t], off);
     m_run[t] += static_cast<float>(e_run);
+    // Scores that were all NaN have no maximum; any one keeps their sum in the merge.
+    if (m_run[t] == -INFINITY && l_run[t] != l_run[t]) m_run[t] = 0.f;
     if (r == 0) {
       sm_m[warp][head(t)] = m_run[t];
       sm_l[warp][head(t)] = l_run[t];

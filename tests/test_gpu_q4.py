@@ -315,6 +315,32 @@ def test_decode_nan_stays_where_it_is():
     assert err <= 2e-6 * (1 + S / math.log(2)) * float(v.nan_to_num(0.0).abs().max())
 
 
+@pytest.mark.parametrize("B,H,n", [(1, 2, 20000), (40, 4, 4000), (1, 2, 300)])
+def test_decode_nan_of_a_whole_split_is_not_lost(B, H, n):
+    """Half the keys of one kv head NaN, so whole splits (and whole warps' shares) have no score
+    at all; in the other kv head a NaN value whose softmax weight is 2^-200 or so: fp32 holds it
+    as 0, and 0 times NaN is NaN all the same. Row 1 (if there is one) holds no NaN."""
+    Hkv, D = 2, 64
+    k, v = syn.normal(1, "k", (1, Hkv, n, D)), syn.normal(1, "v", (1, Hkv, n, D))
+    q = syn.normal(2, "q", (1, H, 1, D))
+    k[0, 1, -1] = 60 * q[0, -1, 0]           # the key that outweighs every other by far
+    k, v = k.repeat(B, 1, 1, 1), v.repeat(B, 1, 1, 1)
+    k[0, 0, n // 2:, 0] = math.nan
+    v[0, 1, 3, 40] = math.nan
+    cache = torch.zeros(B, Hkv, n, ref.record_bytes(D), dtype=torch.uint8, device=dev())
+    g.kv_cache_append_q4(k.to(dev()), v.to(dev()), cache, i32([0] * B), 0)
+    q = q.repeat(B, 1, 1, 1).to(dev())
+    out, w, st = torch.empty_like(q), torch.zeros(B, Hkv, n, device=dev()), status()
+    bad = torch.zeros(B, H, 1, D, dtype=torch.bool)
+    bad[0, :H // 2] = True
+    bad[0, H // 2:, :, 32:] = True
+    for weights in (None, w):
+        g.gqa_attn_decode_q4(q, cache, i32([n] * B), n, out, weights=weights, status=st)
+        assert value(st) == 0
+        assert torch.equal(out.isnan().cpu(), bad)
+    assert bool(w[0, 0].isnan().all()) and not bool(w[0, 1].isnan().any() or w[1:].isnan().any())
+
+
 def test_decode_skips_bad_rows_and_leaves_their_output():
     B, H, Hkv, D, cap = 4, 4, 2, 64, 600
     cache, k, v = filled(9, B, Hkv, cap, D)
