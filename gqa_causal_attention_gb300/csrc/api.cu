@@ -1156,6 +1156,11 @@ bool q4_dims_ok(int B, int Hx, int Hkv, int L, int D) {
 // The number of blocks of a launch is bounded by 2^31 - 1: rows and heads stay far below.
 bool q4_grid_ok(int B, int H) { return static_cast<int64_t>(B) * H <= (1 << 20); }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 // Host checks that an append and a decode step share; fills the job's cache part.
 int q4_append_check(const attn_rope_params* rp, const float* table, const float* k_norm_w,
                     float norm_eps, int D, int L, int32_t max_start, const int32_t* pos,
@@ -1200,6 +1205,9 @@ int kv_cache_append_q4(const float* k, const float* v, float* k_out, int B, int 
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || (k_out && !aligned16(k_out)) ||
       (table && !aligned16(table)) || (k_norm_w && !aligned16(k_norm_w)))
     return ATTN_ERR_ALIGN;
+  const size_t in = (size_t)B * Hkv * L * D * sizeof(float);
+  if (k_out && ((k_out != k && overlap(k_out, in, k, in)) || overlap(k_out, in, v, in)))
+    return ATTN_ERR_PARAM;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Finite fin;
   fin.add(k, B, Hkv, L, D);
@@ -1356,8 +1364,16 @@ int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* ca
   if (max_cache_len > capacity || budget > capacity_out) return ATTN_ERR_CAPACITY;
   if (!cache || !weights || !cache_len || !cache_out || !weights_out || !index || !len_out)
     return ATTN_ERR_NULL;
-  if (cache == cache_out || weights == weights_out || cache_len == len_out) return ATTN_ERR_PARAM;
   if (!aligned16(cache) || !aligned16(cache_out)) return ATTN_ERR_ALIGN;
+  const size_t heads = (size_t)B * Hkv, rec = gqa::q4::record_bytes(D / 32);
+  const struct { const void* p; size_t n; } in[] = {{cache, heads * capacity * rec},
+      {weights, heads * capacity * sizeof(float)}, {cache_len, B * sizeof(int32_t)}},
+      to[] = {{cache_out, heads * capacity_out * rec},
+      {weights_out, heads * capacity_out * sizeof(float)},
+      {index, heads * budget * sizeof(int32_t)}, {len_out, B * sizeof(int32_t)}};
+  for (const auto& a : in)
+    for (const auto& b : to)
+      if (overlap(a.p, a.n, b.p, b.n)) return ATTN_ERR_PARAM;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   gqa::EvictQ4Job j{};
   Finite fin;

@@ -40,7 +40,8 @@
 //
 // The reference of p is the running row maximum minus 14 plus the running exponent of
 // the value scales, so that p * sv peaks near 2^14 whatever the values' magnitude and
-// both fp16 parts keep their bits down to 2^-24.
+// both fp16 parts keep their bits down to 2^-24. (p itself is dropped below 2^-126, which is
+// 2^(-126 + e) of the largest for values near 2^(e + 17): nothing below values of 1e30.)
 #pragma once
 
 #include <cuda_fp16.h>

@@ -80,9 +80,9 @@ __device__ __forceinline__ float rotate_row(const float* x, const float2* tab, i
   }
   load_row<M>(x, at, y);
   // Without a norm y's error is below four roundings of 2^-24 of the larger of a and b (the
-  // products' and the sum's); with one, below sixteen of either: at most nine in the sum of
-  // squares, halved by the root, and one each in the quotient, the root, its reciprocal and
-  // two products come on top.
+  // product's and the sum's). With one a and b are off by thirteen themselves: at most sixteen
+  // in the sum of squares and two in the quotient and eps, halved by the root, and one each
+  // in the root, its reciprocal and two products; times sqrt(2) and with the former, below 32.
   float unit = 0x1p-22f;
   if (nw) {
     float ss = 0.f;

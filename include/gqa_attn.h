@@ -534,10 +534,12 @@ size_t kv_q4_record_bytes(int D);   /* 36 m rounded up to 16; 0 for an invalid D
 
 /*
  * Cache append, as kv_cache_append, into 4-bit records: for each row b, kv head, token l
- *   y = RoPE(RMSNorm(k[b,hkv,l,:]))   (norm if k_norm_w; both only if rp)
+ *   y = RoPE(RMSNorm(k[b,hkv,l,:]))   (norm if k_norm_w, its sum of squares in fp32 as in
+ *                                      the other calls; both only if rp)
  *   record at slot(start[b] + l)  <-  y and v[b,hkv,l,:], quantised as above
  *   k_out[b,hkv,l,:] <- y in fp32     (k_out NULL: not wanted; k_out == k: in place)
- * k and v [B, Hkv, L, D] are only read, unless k_out is k. slot(p) = p without a window
+ * k and v [B, Hkv, L, D] are only read, unless k_out is k (one that overlaps k or v in
+ * another way: ATTN_ERR_PARAM). slot(p) = p without a window
  * (capacity > every p), p mod window with one (capacity == window; of a longer chunk
  * only its last window positions are stored).
  *   start    device int32 [B], slot positions; max_start bounds them (host)
@@ -616,8 +618,8 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
  * n <= budget keeps every slot. Attention does not mind the move (keys are stored
  * rotated); later tokens go to slot start = len_out with pos still counting positions.
  * 0 <= recent <= budget <= capacity_out; cache_len[b] in [0, max_cache_len] (else
- * ATTN_DEV_LENGTH, and the row is skipped). The outputs must not overlap the inputs;
- * no ring. B * Hkv <= 65535.
+ * ATTN_DEV_LENGTH, and the row is skipped). An output that overlaps an input:
+ * ATTN_ERR_PARAM; no ring. B * Hkv <= 65535.
  */
 int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* cache_len,
                       int32_t max_cache_len, int budget, int recent, void* cache_out,

@@ -44,6 +44,9 @@ def test_reference_scale_rounding():
     assert ref.round_bf16(x).tolist() == want
 
 
+Q = ctypes.c_void_p(64 << 20)
+
+
 def append(k=P, v=P, k_out=None, B=2, Hkv=2, L=3, D=64, start=P, max_start=0, pos=None, max_pos=0,
            params=None, table=None, norm=None, eps=1e-6, cache=P, cap=16, window=0):
     return g.load().kv_cache_append_q4(k, v, k_out, B, Hkv, L, D, start, max_start, pos, max_pos,
@@ -64,6 +67,9 @@ def append(k=P, v=P, k_out=None, B=2, Hkv=2, L=3, D=64, start=P, max_start=0, po
     (CAPACITY, dict(max_start=14)), (CAPACITY, dict(L=17)),
     (ALIGN, dict(k=ODD)), (ALIGN, dict(v=ODD)), (ALIGN, dict(cache=ODD)), (ALIGN, dict(k_out=ODD)),
     (ALIGN, dict(params=rp(), table=ODD)), (ALIGN, dict(params=rp(), table=P, norm=ODD)),
+    # k_out one row into k, v itself, or ending inside v
+    (PARAM, dict(v=Q, k_out=ctypes.c_void_p((1 << 20) + 256))), (PARAM, dict(v=Q, k_out=Q)),
+    (PARAM, dict(v=Q, k_out=ctypes.c_void_p((64 << 20) - 256))),
 ])
 def test_append_refusals(want, kw):
     assert append(**kw) == want
@@ -123,7 +129,11 @@ def test_step_refusals(want, kw):
         None) == want
 
 
-P2, P3, P4 = (ctypes.c_void_p(i << 20) for i in (2, 3, 4))
+def at(mib, offset=0):
+    return ctypes.c_void_p((mib << 20) + offset)
+
+
+P2, P3, P4 = at(2), at(3), at(4)
 
 
 @no_device
@@ -133,6 +143,9 @@ P2, P3, P4 = (ctypes.c_void_p(i << 20) for i in (2, 3, 4))
     (CAPACITY, dict(cap_out=7)), (NULL, dict(cache=None)), (NULL, dict(w=None)), (NULL, dict(cl=None)),
     (NULL, dict(out=None)), (NULL, dict(w_out=None)), (NULL, dict(index=None)),
     (NULL, dict(len_out=None)), (PARAM, dict(out=P)), (PARAM, dict(w_out=P2)), (PARAM, dict(len_out=P3)),
+    # outputs that begin or end inside an input (3200 bytes of records, 160 of weights)
+    (PARAM, dict(out=at(1, 3184))), (PARAM, dict(out=at(1, -16))), (PARAM, dict(w_out=at(2, 156))),
+    (PARAM, dict(index=at(2, -4))), (PARAM, dict(len_out=at(1, 0))), (PARAM, dict(index=at(3, 0))),
     (ALIGN, dict(cache=ODD)), (ALIGN, dict(out=ODD)),
 ])
 def test_evict_refusals(want, kw):
