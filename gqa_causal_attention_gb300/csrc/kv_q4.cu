@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kRowThreads, 7) append_q4_kernel(AppendQ4Job j
     return;
   }
   const q4::Lanes<M> at(lane);
+  uint32_t doubts = 0;
   for (int i0 = warp * RW; i0 < n; i0 += kWarps * RW) {
     const int i = min(i0 + at.row, n - 1);   // lanes past the last row follow it
     const Target t = to[i];
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kRowThreads, 7) append_q4_kernel(AppendQ4Job j
     const uint2 d = append_rows<M, ROPE>(
         j, xk + i * D, xv + i * D, ROPE != kNoRope && t.ok ? j.table + t.angle * (j.R / 2) : j.table,
         t.rec ? recs + i * REC : nullptr, j.k_out ? j.k_out + (row0 + i) * D : nullptr, at, lane, on);
+    doubts |= d.x | d.y;
     if (at.in && at.l == 0 && i0 + at.row < n) {
       const int sh = at.row * 4 * M;
       const uint32_t mask = M == 8 ? 0xffffffffu : (1u << (4 * M & 31)) - 1u;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kRowThreads, 7) append_q4_kernel(AppendQ4Job j
   // would have cost. A row's second pass is its own warp's.
   __syncwarp();
 #pragma unroll 1
-  for (int i0 = warp * RW; i0 < n; i0 += kWarps * RW) {
+  for (int i0 = doubts ? warp * RW : n; i0 < n; i0 += kWarps * RW) {
 #pragma unroll 1
     for (int i = i0; i < min(i0 + RW, n); ++i) {
       const uint2 d = later[i];

@@ -81,35 +81,38 @@ __device__ __forceinline__ double warp_sum_d(double v) {
 constexpr float kRound = 12582920.0f;
 
 // Quantises a lane's two quads y, four lanes a group, each value off from the
-// exact one by at most err: the scale is bf16(max|y| / 7), the code rint(y / scale), ties to
-// even. Returns whether a rounding was not further from its border than the error: the
-// group has to be done again by quantise_exact. EXACT: y is exact, err is not read. Every
-// lane of the warp must call it. About six instructions a value.
+// exact one by at most err and rel times the group's largest: the scale is bf16(max|y| / 7),
+// the code rint(y / scale), ties to even. Returns whether a rounding was not further from its
+// border than the error: the group has to be done again by quantise_exact. Both distances
+// from a border, max|y| - 7 (middle of two scales) and y - code * scale, are exact in fp32, so
+// of exact values only ties and some borders' nearest neighbours are in doubt. EXACT: y is
+// exact, err and rel are not read. Every lane of the warp must call it. About six
+// instructions a value.
 template <bool EXACT>
-__device__ __forceinline__ bool quantise_fast(const float (&y)[8], float err, uint32_t& codes,
-                                              uint32_t& scale) {
+__device__ __forceinline__ bool quantise_fast(const float (&y)[8], float err, float rel,
+                                              uint32_t& codes, uint32_t& scale) {
   float big = 0.f;                           // a NaN stays one, and its bits are above inf's
 #pragma unroll
   for (int e = 0; e < 8; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(big) : "f"(fabsf(y[e])));
   const uint32_t top = group_max_u(__float_as_uint(big));
   const uint32_t far = EXACT ? 0u : group_max_u(__float_as_uint(err));
-  const float amax = __uint_as_float(top), ferr = __uint_as_float(far);
-  // amax / 7 to two roundings; far from a bf16 border that settles the scale
+  const float amax = __uint_as_float(top);
+  const float ferr = EXACT ? 0.f : fmaf(amax, rel, __uint_as_float(far));
+  // amax / 7 to two roundings lies between two scales (or on one); their middle decides
   const float a7 = amax * (1.0f / 7.0f);
   const uint32_t bits = __float_as_uint(a7);
-  const float mid = __uint_as_float((bits & 0xffff0000u) | 0x8000u);
-  scale = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
+  const float past = fmaf(-7.f, __uint_as_float((bits & 0xffff0000u) | 0x8000u), amax);
+  scale = (bits >> 16) + (past > 0.f);
+  const float s = bf16_to_float(scale), near = fmaf(0.5f, s, -ferr);
   float rs;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(bf16_to_float(scale)));
-  // t = y / scale is off by err / scale, by 2^-23 of at most 7.04 in rs and by its rounding
-  const float near = 0.5f - (EXACT ? 0x1p-19f : fmaf(err, rs, 0x1p-19f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
   uint32_t b[8];
   float off = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = y[e] * rs, u = t + kRound;
+    const float u = fmaf(y[e], rs, kRound);
     b[e] = __float_as_uint(u);
-    off = fmaxf(off, fabsf(t - (u - kRound)));
+    off = fmaxf(off, fabsf(fmaf(kRound - u, s, y[e])));
   }
   // four codes a sum: the floats' high bits cancel below bit 16
   const uint32_t lo = b[0] + 16u * b[1] + 256u * b[2] + 4096u * b[3];
@@ -120,8 +123,7 @@ __device__ __forceinline__ bool quantise_fast(const float (&y)[8], float err, ui
     codes = 0x88888888u;
     scale = (top | far) == 0 ? 0u : kNanScale;
   }
-  return !special && (a7 < 0x1p-120f || fabsf(a7 - mid) <= fmaf(ferr, 0.15f, a7 * 0x1p-22f) ||
-                      off >= near);
+  return !special && (a7 < 0x1p-120f || fabsf(past) <= ferr || off >= near);
 }
 
 // Quad q of group g at 16 bits of codes, in the key part (part = 0) or the value part (1) of
@@ -148,16 +150,16 @@ __device__ __noinline__ double exact_inv_rms(const float* x, float eps, int D, i
   double ss = 0.0;
 #pragma unroll 1
   for (int d = lane; d < D; d += 32) ss = fma(static_cast<double>(x[d]), static_cast<double>(x[d]), ss);
-  return 1.0 / sqrt(warp_sum_d(ss) / D + static_cast<double>(eps));
+  return rsqrt(warp_sum_d(ss) / D + static_cast<double>(eps));
 }
 
 // The doubtful groups of the raw row x (doubt: four bits a group, any set) again, in fp64,
 // into part `part` of the record at rec: y = RoPE(RMSNorm(x)) with the row's (cos, sin)
 // table tab (NULL: no rotation) and norm weights nw (NULL: none), a group at a time, one dim
 // per lane. No quotient is formed: fp32 proposes the scale and the codes, and exact products
-// with the borders next to them decide. A few rows in a thousand come here (with a norm
-// about one in a hundred); kept short, since its instructions are not in the cache then
-// (unrolled over a row, the first use on an SM took 3 us).
+// with the borders next to them decide. At D = 128 one row in 2500 comes here, with a norm one
+// in 300 (with D = 256 twice as many); kept short, since its instructions are not in the cache
+// then: about 3 us a use, which 64 rows of one token still see.
 template <int M>
 __device__ __noinline__ void quantise_exact(const float* x, const float2* tab, int R,
                                             const float* nw, float eps, int lane, uint32_t doubt,
@@ -178,21 +180,23 @@ __device__ __noinline__ void quantise_exact(const float* x, const float2* tab, i
       if (nw) b = b * inv * nw[p];
       y = fma(y, static_cast<double>(t.x), b * (d < half ? -t.y : t.y));
     }
-    double amax = fabs(y);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // the scale's two borders, half a unit from the proposed one
+    // the largest: of |y| as 64 bits, the upper half first
+    const double ay = fabs(y);
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(__double2hiint(ay)));
+    const uint32_t lo = __reduce_max_sync(
+        0xffffffffu, __double2hiint(ay) == static_cast<int>(hi) ? static_cast<uint32_t>(__double2loint(ay)) : 0u);
+    const double amax = __hiloint2double(static_cast<int>(hi), static_cast<int>(lo));
+    // a seventh of it lies between two scales (or on one), whose middle decides
     const uint32_t bits = __float_as_uint(static_cast<float>(amax) * (1.0f / 7.0f));
-    uint32_t sc = (bits + 0x7fffu + ((bits >> 16) & 1u)) >> 16;
-    const double above = 7.0 * __uint_as_float((sc << 16) | 0x8000u);
-    const double below = sc ? 7.0 * __uint_as_float(((sc - 1u) << 16) | 0x8000u) : -1.0;
-    if (amax > above || (amax == above && (sc & 1u)))
-      ++sc;
-    else if (amax < below || (amax == below && (sc & 1u)))
-      --sc;
+    uint32_t sc = bits >> 16;
+    const double past = fma(-7.0, static_cast<double>(__uint_as_float((bits & 0xffff0000u) | 0x8000u)), amax);
+    if (past > 0.0 || (past == 0.0 && (sc & 1u))) ++sc;
     // the code; tiny scales are lifted out of the subnormals for the proposal
-    const double s = bf16_to_float(sc), lift = sc < 0x0800u ? 0x1p100 : 1.0;
-    int c = sc ? __float2int_rn(static_cast<float>(y * lift) / static_cast<float>(s * lift)) : 0;
+    const double s = bf16_to_float(sc);
+    const float lift = sc < 0x0800u ? 0x1p100f : 1.0f;
+    float rs;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(bf16_to_float(sc) * lift));
+    int c = sc ? __float2int_rn(static_cast<float>(y * lift) * rs) : 0;
     const double rest = fma(static_cast<double>(-c), s, y), border = 0.5 * s;
     if (rest > border || (rest == border && (c & 1)))
       ++c;

@@ -32,9 +32,15 @@ __device__ __forceinline__ void store_row(float* x, const q4::Lanes<M>& at, cons
   *reinterpret_cast<float4*>(x + at.dim(1)) = make_float4(y[4], y[5], y[6], y[7]);
 }
 
+// The part of rotate_row's error that goes with the values themselves: with a norm the
+// common factor's 9 roundings (at most 12 in the sum of squares, one each in the quotient and
+// the sum with eps, halved by the root; one each in the root and its reciprocal), without one
+// what quantise_fast rounds in its own bounds.
+__device__ __forceinline__ float row_error(const float* nw) { return nw ? 0x1.28p-21f : 0x1p-26f; }
+
 // A lane's quads of the raw row x through RMSNorm (nw) and RoPE (tab: the row's angles;
-// x and tab in any memory), in fp32, and a bound of their error. Every lane of the warp
-// calls it.
+// x and tab in any memory), in fp32, and a bound of their error (with row_error's). Every
+// lane of the warp calls it.
 template <int M, int ROPE>
 __device__ __forceinline__ float rotate_row(const float* x, const float2* tab, int R,
                                             const float* nw, float eps, const q4::Lanes<M>& at,
@@ -79,17 +85,16 @@ __device__ __forceinline__ float rotate_row(const float* x, const float2* tab, i
     }
   }
   load_row<M>(x, at, y);
-  // Without a norm y's error is below four roundings of 2^-24 of the larger of a and b (the
-  // product's and the sum's). With one a and b are off by thirteen themselves: at most sixteen
-  // in the sum of squares and two in the quotient and eps, halved by the root, and one each
-  // in the root, its reciprocal and two products; times sqrt(2) and with the former, below 32.
-  float unit = 0x1p-22f;
+  // Errors in roundings of 2^-24, |(a, b)| <= sqrt(2) of the larger: 1 of b s and 1 of y, 2.42 of
+  // the larger. With a norm also two each in a and b, 5.25 in all, and the common factor's.
+  float unit = 0x1.4p-23f;                   // 2.5
   if (nw) {
-    float ss = 0.f;
+    float ss[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-    const float inv = 1.0f / sqrtf(q4::row_sum<M>(ss, lane) / static_cast<float>(32 * M) + eps);
-    unit = 0x1p-19f;
+    for (int e = 0; e < 4; ++e) ss[e] = fmaf(y[2 * e], y[2 * e], y[2 * e + 1] * y[2 * e + 1]);
+    const float sum = q4::row_sum<M>((ss[0] + ss[1]) + (ss[2] + ss[3]), lane);
+    const float inv = 1.0f / sqrtf(sum / static_cast<float>(32 * M) + eps);
+    unit = 0x1.6p-22f;                       // 5.5
     float wo[8];
     load_row<M>(nw, at, wo);
 #pragma unroll
@@ -122,7 +127,7 @@ __device__ __forceinline__ uint2 append_rows(const AppendQ4Job& j, const float* 
   bool doubt;
   uint2 r;
   load_row<M>(v, at, y);
-  doubt = quantise_fast<true>(y, 0.f, codes, scale);
+  doubt = quantise_fast<true>(y, 0.f, 0.f, codes, scale);
   if (on && rec) {
     store_codes<M>(rec, 1, codes, scale, at);
     constexpr int pad = (record_bytes(M) - 36 * M) / 4;   // zero padding
@@ -131,10 +136,10 @@ __device__ __forceinline__ uint2 append_rows(const AppendQ4Job& j, const float* 
   r.y = __ballot_sync(0xffffffffu, doubt && on && rec);
   if (ROPE != kNoRope) {
     const float err = rotate_row<M, ROPE>(x, tab, j.R, j.norm_w, j.norm_eps, at, lane, y);
-    doubt = quantise_fast<false>(y, err, codes, scale);
+    doubt = quantise_fast<false>(y, err, row_error(j.norm_w), codes, scale);
   } else {
     load_row<M>(x, at, y);
-    doubt = quantise_fast<true>(y, 0.f, codes, scale);
+    doubt = quantise_fast<true>(y, 0.f, 0.f, codes, scale);
   }
   if (on && rec) store_codes<M>(rec, 0, codes, scale, at);
   r.x = __ballot_sync(0xffffffffu, doubt && on && rec);   // also: every lane has read its partners

@@ -153,6 +153,33 @@ def test_append_on_borders_and_at_extremes(D):
     assert torch.equal(cache.cpu(), ref.pack(k, v))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "spread", "decimals"])
+@pytest.mark.parametrize("D,R,norm", [(64, 64, False), (96, 20, True), (128, 128, True), (256, 256, True)])
+def test_append_of_many_rows(D, R, norm, kind):
+    """Enough rows that hundreds of groups have a value or a scale next to a rounding border;
+    values of 8 bits, of widely spread magnitude per dim, and of few decimals."""
+    B, Hkv, L = 2, 2, 4000
+    k, v = syn.normal(D, "k", (B, Hkv, L, D)), syn.normal(D, "v", (B, Hkv, L, D))
+    if kind == "bf16":
+        k, v = k.bfloat16().float(), v.bfloat16().float()
+    elif kind == "spread":
+        m = torch.exp2(torch.arange(D) * 5 % 23 - 11.0)
+        k, v = k * m, v * m
+    else:
+        k, v = (k * 10).round() / 10, (v * 10).round() / 10
+    kn = syn.norm_weight(D, "kn", D) if norm else None
+    rp, table, tab = table_of(4100, R, D)
+    cache, st = torch.zeros(B, Hkv, L, ref.record_bytes(D), dtype=torch.uint8, device=dev()), status()
+    kd, vd = k.to(dev()), v.to(dev())
+    g.kv_cache_append_q4(kd, vd, cache, i32([0, 0]), 0, rp, table,
+                         None if kn is None else kn.to(dev()), 1e-6, pos=i32([0, 100]),
+                         max_pos=100, status=st)
+    g.kv_cache_read_q4(cache, kd, vd, i32([0, 0]), 0, status=st)
+    assert value(st) == 0
+    assert torch.equal(kd.cpu().double(), ref.stands_for(ref.rotate(k, [0, 100], tab, kn)))
+    assert torch.equal(vd.cpu().double(), ref.stands_for(v))
+
+
 def test_append_cancelling_rotation():
     """A whole group of rotated values that all but cancel: fp32 alone could not tell them."""
     D, L = 64, 40
