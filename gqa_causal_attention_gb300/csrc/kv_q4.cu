@@ -273,17 +273,18 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum, uint3
 }
 
 // One block per (row, head): the need-th largest of the old slots' keys, then one ordered
-// pass that writes the kept slots' numbers and weights. The largest by its top eleven bits
-// (a histogram of them, summed from the top); then among the few keys that share those,
-// gathered, by counting for each how many are larger; where they are not few, by histograms
-// of the next eleven and ten bits. The keys are read once from memory where they fit in shared memory,
+// pass that writes the kept slots' numbers and weights. The largest by its top 11 or 13 bits
+// (sign, exponent and two or four bits more: a histogram of them, summed from the top); then
+// among the few keys that share those, gathered, by counting for each how many are larger;
+// where they are not few, by histograms of the next bits first. The keys are read once from memory where they fit in shared memory,
 // else again from L2 in each pass. Latency counts here: it is one block's chain of barriers
 // and 45 instructions a key and warp (128 heads of up to 8192 slots: 13.5 us; 8 of 1100: 5).
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held) {
-  constexpr int kSelBins = 2048 / kSelThreads;
+  constexpr int kTopBits = kSelThreads == 1024 ? 13 : 11, kBins = 1 << kTopBits;
+  constexpr int kPer = kBins / kSelThreads;
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[2048];
+  __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) uint32_t few[kFew];
   __shared__ uint32_t wsum[32];
   __shared__ uint32_t found_bin, found_left, found_count, gathered;
@@ -322,11 +323,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   if (any_old) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const int bits = pass == 2 ? 10 : 11;
+      const int shift = pass == 0 ? 32 - kTopBits : (pass == 1 ? 22 - kTopBits : 0);
+      const int bits = pass == 0 ? kTopBits : (pass == 1 ? 10 : 22 - kTopBits);
       const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
 #pragma unroll
-      for (int i = 0; i < kSelBins; ++i) hist[tid + i * kSelThreads] = 0;
+      for (int i = 0; i < kPer / 4; ++i)
+        reinterpret_cast<uint4*>(hist)[tid + i * kSelThreads] = make_uint4(0, 0, 0, 0);
       if (tid == 0) gathered = 0;
       __syncthreads();
       for (int i = tid; i < old; i += kSelThreads) {
@@ -340,16 +342,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
         if ((k & above) == (T & above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      // bins from the top: thread t holds kSelBins of them, from 2047 - kSelBins t down
-      uint32_t h[kSelBins], mine = 0, total;
+      // bins from the top: thread t holds kPer of them, from kBins - 1 - kPer t down
+      uint32_t h[kPer], mine = 0, total;
 #pragma unroll
-      for (int i = 0; i < kSelBins; ++i) mine += h[i] = hist[2047 - kSelBins * tid - i];
+      for (int i = 0; i < kPer; i += 4) {
+        const uint4 q = reinterpret_cast<const uint4*>(hist)[(kBins - kPer * tid - i) / 4 - 1];
+        h[i] = q.w; h[i + 1] = q.z; h[i + 2] = q.y; h[i + 3] = q.x;
+        mine += q.x + q.y + q.z + q.w;
+      }
       uint32_t at = block_scan<kSelThreads>(mine, wsum, total) - mine;
       if (at < left && at + mine >= left) {   // exactly one thread
 #pragma unroll
-        for (int i = 0; i < kSelBins; ++i) {
+        for (int i = 0; i < kPer; ++i) {
           if (at < left && at + h[i] >= left) {
-            found_bin = 2047 - kSelBins * tid - i;
+            found_bin = kBins - 1 - kPer * tid - i;
             found_left = left - at;
             found_count = h[i];
           }
@@ -360,10 +366,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
       T |= found_bin << shift;
       left = found_left;
       const uint32_t count = found_count;
-      if (pass == 0 && count <= kFew) {
+      if (shift > 0 && count <= kFew) {
         for (int i = tid; i < old; i += kSelThreads) {
           const uint32_t k = key_of(i);
-          if (k >> 21 == T >> 21) few[atomicAdd(&gathered, 1u)] = k;
+          if (k >> shift == T >> shift) few[atomicAdd(&gathered, 1u)] = k;
         }
         if (tid >= static_cast<int>(count) && tid < kFew) few[tid] = 0;    // below every old key
         __syncthreads();
