@@ -1360,7 +1360,7 @@ int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* ca
       recent > budget || (int64_t)B * Hkv > 65535)
     return ATTN_ERR_SHAPE;
   if (B == 0) return ATTN_OK;
-  if (max_cache_len < 0) return ATTN_ERR_SHAPE;
+  if (max_cache_len < 0 || max_cache_len > (1 << 30)) return ATTN_ERR_SHAPE;
   if (max_cache_len > capacity || budget > capacity_out) return ATTN_ERR_CAPACITY;
   if (!cache || !weights || !cache_len || !cache_out || !weights_out || !index || !len_out)
     return ATTN_ERR_NULL;

@@ -238,52 +238,48 @@ __global__ void __launch_bounds__(kRowThreads) read_q4_kernel(ReadQ4Job j, int t
 
 // ---------------------------------------------------------------- eviction
 
-// Order of weights as unsigned keys: larger weight, larger key; -0 and +0 alike; NaN
-// above everything (a slot whose weight is unknown is kept).
+// Order of weights as unsigned keys, never 0: larger weight, larger key; -0 and +0 alike; NaN
+// above everything (a slot whose weight is unknown is kept). The sum makes +0 of -0 and
+// 0x7fffffff of every NaN.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(w == 0.f ? 0.f : w);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  float c;
+  asm("add.f32 %0, %1, 0f00000000;" : "=f"(c) : "f"(w));
+  const uint32_t b = __float_as_uint(c);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 constexpr int kFew = 256;                    // keys sharing the threshold's top bits, at most
-constexpr int kSelItems = 4;                 // slots per thread and compaction tile
+constexpr int kSelItems = 8;                 // slots per thread and compaction tile
 constexpr int kSelKeys = 40960;              // keys held in shared memory at most (160 KB)
 
-// Inclusive sum over a selection block; total: of all. Two barriers; wsum [32].
+// What the warps before this one counted (own: one value a warp), and all. wsum [32].
 template <int kSelThreads>
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum, uint32_t& total) {
+__device__ __forceinline__ uint32_t warps_before(uint32_t own, uint32_t* wsum, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto scan = [&](uint32_t x) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  };
-  v = scan(v);
-  if (lane == 31) wsum[warp] = v;
+  if (lane == 0) wsum[warp] = own;
   __syncthreads();
-  const uint32_t w = lane < kSelThreads / 32 ? wsum[lane] : 0u, upto = scan(w);
-  total = __shfl_sync(0xffffffffu, upto, 31);
-  v += __shfl_sync(0xffffffffu, upto - w, warp);
-  __syncthreads();
-  return v;
+  const uint32_t w = lane < kSelThreads / 32 ? wsum[lane] : 0u;
+  total = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
 }
 
 // One block per (row, head): the need-th largest of the old slots' keys, then one ordered
 // pass that writes the kept slots' numbers and weights. The largest by its top 11 or 13 bits
 // (sign, exponent and two or four bits more: a histogram of them, summed from the top); then
 // among the few keys that share those, gathered, by counting for each how many are larger;
-// where they are not few, by histograms of the next bits first. The keys are read once from memory where they fit in shared memory,
-// else again from L2 in each pass. Latency counts here: it is one block's chain of barriers
-// and 45 instructions a key and warp (128 heads of up to 8192 slots: 13.5 us; 8 of 1100: 5).
+// where they are not few, by histograms of the next bits first. The weights are read once
+// where their keys fit in shared memory, the first of them before the length is known, else
+// again from L2 in each pass. Bound by one block's issue and its chain of barriers: every
+// instruction counts 16 or 32 times a pass (128 heads of up to 8192 slots: 8 us; 8 of 1100: 4.5).
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held) {
   constexpr int kTopBits = kSelThreads == 1024 ? 13 : 11, kBins = 1 << kTopBits;
-  constexpr int kPer = kBins / kSelThreads;
-  extern __shared__ uint32_t keys[];
+  constexpr int kPer = kBins / kSelThreads, kTileSlots = kSelThreads * kSelItems;
+  constexpr int kShare = kSelThreads / kFew;     // threads that count for one of the few keys
+  extern __shared__ __align__(16) uint32_t keys[];         // of the old slots, if they fit
   __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) uint32_t few[kFew];
   __shared__ uint32_t wsum[32];
@@ -291,67 +287,86 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   dependents_may_launch();
   dependent_wait();
   if (gated_off(j.skip)) return;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long bh = blockIdx.x;
   const int b = static_cast<int>(bh / j.Hkv);
+  const float* w = j.weights + bh * j.capacity;
+  float ahead[kSelItems];
+#pragma unroll
+  for (int e = 0; e < kSelItems; ++e) {
+    const int i = tid + e * kSelThreads;
+    ahead[e] = i < j.max_cache_len ? w[i] : 0.f;           // <= capacity
+  }
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i)
+      reinterpret_cast<uint4*>(hist)[tid + i * kSelThreads] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) gathered = 0;
+    __syncthreads();
+  };
+  clear();
   const int n = j.cache_len[b];
   if (n < 0 || n > j.max_cache_len || n > j.capacity) {
     if (tid == 0 && bh % j.Hkv == 0) report(j.status, ATTN_DEV_LENGTH);
     return;
   }
-  const float* w = j.weights + bh * j.capacity;
   float* wo = j.weights_out + bh * j.capacity_out;
   int32_t* index = j.index + bh * j.budget;
   const int kept = min(n, j.budget);
   if (tid == 0 && bh % j.Hkv == 0) j.len_out[b] = kept;
   for (long i = kept + tid; i < j.capacity_out; i += kSelThreads) wo[i] = 0.f;
   for (int i = kept + tid; i < j.budget; i += kSelThreads) index[i] = -1;
-  if (n <= j.budget) {
-    for (int i = tid; i < n; i += kSelThreads) {
-      index[i] = i;
-      wo[i] = w[i];
-    }
-    return;
+  // What is kept whatever its weight: all, or the recent slots, behind the others.
+  const int old = n <= j.budget ? 0 : n - j.recent, need = n <= j.budget ? 0 : j.budget - j.recent;
+  for (int i = old + tid; i < n; i += kSelThreads) {
+    index[need + i - old] = i;
+    wo[need + i - old] = w[i];
   }
-  const int old = n - j.recent;              // recent <= budget < n
+  if (need == 0) return;                     // n <= budget, or only recent slots are kept
+
+  // Keys of whole tiles, 0 behind the last; their histogram.
   const bool in_smem = old <= held;
-  auto key_of = [&](int i) { return in_smem ? keys[i] : weight_key(w[i]); };
+  for (int i0 = 0; i0 < old; i0 += kTileSlots) {
+#pragma unroll
+    for (int e = 0; e < kSelItems; ++e) {
+      const int i = i0 + tid + e * kSelThreads;
+      if (i0 > 0) ahead[e] = i < old ? w[i] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kSelItems; ++e) {
+      const int i = i0 + tid + e * kSelThreads;
+      const uint32_t k = i < old ? weight_key(ahead[e]) : 0u;
+      if (in_smem) keys[i] = k;
+      if (i < old) atomicAdd(&hist[k >> (32 - kTopBits)], 1u);
+    }
+  }
+  __syncthreads();
+  auto key_of = [&](int i) { return in_smem ? keys[i] : (i < old ? weight_key(w[i]) : 0u); };
 
   // Threshold: keys above T are kept, and the first `left` of those equal to it.
-  uint32_t T = 0, left = static_cast<uint32_t>(j.budget - j.recent);
-  const bool any_old = left > 0;
-  if (any_old) {
+  uint32_t T = 0, left = static_cast<uint32_t>(need);
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 32 - kTopBits : (pass == 1 ? 22 - kTopBits : 0);
-      const int bits = pass == 0 ? kTopBits : (pass == 1 ? 10 : 22 - kTopBits);
-      const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+  for (int shift = 32 - kTopBits;;) {
+    // bins from the top: thread t holds kPer of them, from kBins - 1 - kPer t down
+    uint32_t h[kPer], mine = 0, total;
 #pragma unroll
-      for (int i = 0; i < kPer / 4; ++i)
-        reinterpret_cast<uint4*>(hist)[tid + i * kSelThreads] = make_uint4(0, 0, 0, 0);
-      if (tid == 0) gathered = 0;
-      __syncthreads();
-      for (int i = tid; i < old; i += kSelThreads) {
-        uint32_t k;
-        if (pass == 0) {
-          k = weight_key(w[i]);
-          if (in_smem) keys[i] = k;
-        } else {
-          k = key_of(i);
-        }
-        if ((k & above) == (T & above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-      }
-      __syncthreads();
-      // bins from the top: thread t holds kPer of them, from kBins - 1 - kPer t down
-      uint32_t h[kPer], mine = 0, total;
+    for (int i = 0; i < kPer; i += 4) {
+      const uint4 q = reinterpret_cast<const uint4*>(hist)[(kBins - kPer * tid - i) / 4 - 1];
+      h[i] = q.w; h[i + 1] = q.z; h[i + 2] = q.y; h[i + 3] = q.x;
+      mine += q.x + q.y + q.z + q.w;
+    }
+    // only the warp that holds the bin scans its own
+    const uint32_t own = __reduce_add_sync(0xffffffffu, mine);
+    uint32_t at = warps_before<kSelThreads>(own, wsum, total);
+    if (at < left && at + own >= left) {
+      uint32_t upto = mine;
 #pragma unroll
-      for (int i = 0; i < kPer; i += 4) {
-        const uint4 q = reinterpret_cast<const uint4*>(hist)[(kBins - kPer * tid - i) / 4 - 1];
-        h[i] = q.w; h[i + 1] = q.z; h[i + 2] = q.y; h[i + 3] = q.x;
-        mine += q.x + q.y + q.z + q.w;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
-      uint32_t at = block_scan<kSelThreads>(mine, wsum, total) - mine;
-      if (at < left && at + mine >= left) {   // exactly one thread
+      at += upto - mine;
+      if (at < left && at + mine >= left) {   // one thread
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           if (at < left && at + h[i] >= left) {
@@ -362,74 +377,84 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
           at += h[i];
         }
       }
+    }
+    __syncthreads();
+    T |= found_bin << shift;
+    left = found_left;
+    const int count = static_cast<int>(found_count);
+    if (shift == 0) break;
+    if (count > kFew) {                      // the next ten bits (at most) of those
+      const int next = shift > 10 ? shift - 10 : 0;
+      clear();
+      for (int i = tid; i < old; i += kSelThreads) {
+        const uint32_t k = key_of(i);
+        if (k >> shift == T >> shift)
+          atomicAdd(&hist[(k >> next) & ((1u << (shift - next)) - 1)], 1u);
+      }
       __syncthreads();
-      T |= found_bin << shift;
-      left = found_left;
-      const uint32_t count = found_count;
-      if (shift > 0 && count <= kFew) {
-        for (int i = tid; i < old; i += kSelThreads) {
-          const uint32_t k = key_of(i);
-          if (k >> shift == T >> shift) few[atomicAdd(&gathered, 1u)] = k;
-        }
-        if (tid >= static_cast<int>(count) && tid < kFew) few[tid] = 0;    // below every old key
-        __syncthreads();
-        if (tid < static_cast<int>(count)) {
-          const uint32_t k = few[tid];
-          uint32_t more = 0, same = 0;
-          for (uint32_t i = 0; i < count; i += 4) {
-            const uint4 f = *reinterpret_cast<const uint4*>(few + i);
-            more += (f.x > k) + (f.y > k) + (f.z > k) + (f.w > k);
-            same += (f.x == k) + (f.y == k) + (f.z == k) + (f.w == k);
-          }
-          if (more < left && more + same >= left) {       // threads that agree on the key
-            found_bin = k;
-            found_left = left - more;
-          }
-        }
-        __syncthreads();
-        T = found_bin;
-        left = found_left;
-        break;
+      shift = next;
+      continue;
+    }
+    for (int i = tid; i < old; i += kSelThreads) {
+      const uint32_t k = key_of(i);
+      if (k >> shift == T >> shift) few[atomicAdd(&gathered, 1u)] = k;
+    }
+    if (tid >= count && tid < (count + 3) / 4 * 4) few[tid] = 0;           // below every key
+    __syncthreads();
+    if (warp * (32 / kShare) < count) {
+      const int mine_at = tid / kShare;
+      const uint32_t k = mine_at < count ? few[mine_at] : 0u;
+      uint32_t more = 0, same = 0;
+      for (int i = 4 * (tid % kShare); i < count; i += 4 * kShare) {
+        const uint4 f = *reinterpret_cast<const uint4*>(few + i);
+        more += (f.x > k) + (f.y > k) + (f.z > k) + (f.w > k);
+        same += (f.x == k) + (f.y == k) + (f.z == k) + (f.w == k);
+      }
+#pragma unroll
+      for (int o = 1; o < kShare; o <<= 1) {
+        more += __shfl_xor_sync(0xffffffffu, more, o);
+        same += __shfl_xor_sync(0xffffffffu, same, o);
+      }
+      if (mine_at < count && more < left && more + same >= left) {
+        found_bin = k;                       // threads that agree on the key
+        found_left = left - more;
       }
     }
+    __syncthreads();
+    T = found_bin;
+    left = found_left;
+    break;
   }
-  // Ordered pass. Kept before a slot: those above T, and at most `left` equal to it.
+
+  // Ordered pass. Kept before a slot: those above T, and at most `left` equal to it. A warp's
+  // slots are consecutive, 32 at a time, so its writes are too.
   uint32_t base_up = 0, base_eq = 0;
-  for (int t0 = 0; t0 < n; t0 += kSelThreads * kSelItems) {
-    const int i0 = t0 + tid * kSelItems;
-    uint32_t up = 0, eq = 0;                  // bit e: slot i0 + e
-    float wv[kSelItems];
-#pragma unroll
-    for (int e = 0; e < kSelItems; ++e) wv[e] = i0 + e < n ? w[i0 + e] : 0.f;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int t0 = 0; t0 < old; t0 += kTileSlots) {
+    const int i0 = t0 + warp * 32 * kSelItems + lane;
+    uint32_t k[kSelItems], up[kSelItems], eq[kSelItems], own = 0, total;   // own: eq in the upper half
 #pragma unroll
     for (int e = 0; e < kSelItems; ++e) {
-      const int i = i0 + e;
-      if (i >= old) {
-        if (i < n) up |= 1u << e;
-      } else if (any_old) {
-        const uint32_t k = weight_key(wv[e]);
-        if (k > T) up |= 1u << e;
-        if (k == T) eq |= 1u << e;
-      }
+      k[e] = key_of(i0 + 32 * e);
+      up[e] = __ballot_sync(0xffffffffu, k[e] > T);
+      eq[e] = __ballot_sync(0xffffffffu, k[e] == T);
+      own += __popc(up[e]) + (__popc(eq[e]) << 16);        // at most 8192 of each a block
     }
-    // counts of both in one word: at most 4096 each
-    const uint32_t own = __popc(up) | static_cast<uint32_t>(__popc(eq)) << 16;
-    uint32_t total;
-    const uint32_t before = block_scan<kSelThreads>(own, wsum, total) - own;
+    const uint32_t before = warps_before<kSelThreads>(own, wsum, total);
     uint32_t nup = base_up + (before & 0xffffu), neq = base_eq + (before >> 16);
 #pragma unroll
     for (int e = 0; e < kSelItems; ++e) {
-      const bool is_up = up >> e & 1u, is_eq = eq >> e & 1u;
-      if (is_up || (is_eq && neq < left)) {
-        const uint32_t at = nup + min(neq, left);
-        index[at] = i0 + e;
-        wo[at] = wv[e];
+      const uint32_t u = nup + __popc(up[e] & below), q = neq + __popc(eq[e] & below);
+      if (k[e] > T || (k[e] == T && q < left)) {
+        index[u + min(q, left)] = i0 + 32 * e;
+        wo[u + min(q, left)] = key_weight(k[e]);
       }
-      nup += is_up;
-      neq += is_eq;
+      nup += __popc(up[e]);
+      neq += __popc(eq[e]);
     }
     base_up += total & 0xffffu;
     base_eq += total >> 16;
+    __syncthreads();
   }
 }
 
@@ -537,7 +562,9 @@ cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, cudaStream_t stre
       },
       cudaErrorInvalidDevice, [](const cudaError_t& v) { return v == cudaSuccess; });
   if (e != cudaSuccess) return e;
-  const int held = j.max_cache_len < kSelKeys ? j.max_cache_len : kSelKeys;
+  constexpr int tile = T * kSelItems;        // whole tiles are held
+  static_assert(kSelKeys % tile == 0, "");
+  const int held = j.max_cache_len < kSelKeys ? (j.max_cache_len + tile - 1) / tile * tile : kSelKeys;
   return launch_dependent(evict_select_kernel<T>, heads, T, held * 4, stream, j, held);
 }
 }  // namespace
@@ -545,8 +572,8 @@ cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, cudaStream_t stre
 cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream) {
   const unsigned heads = static_cast<unsigned>(j.B) * j.Hkv;
   // Short heads are chains of barriers, cheaper among 16 warps than among 32 (8 heads of 1100
-  // slots: 8.8 us with the move, 10.0 with 32 warps); long ones are work on the keys (128 heads
-  // of up to 8192: 42.4 and 41.4).
+  // slots: 7.3 us with the move, 8.8 with 32 warps); long ones are work on the keys (128 heads
+  // of up to 8192: 38.5 and 35.2).
   const cudaError_t e = j.max_cache_len <= 4096 ? launch_select<512>(j, heads, stream)
                                                 : launch_select<1024>(j, heads, stream);
   if (e != cudaSuccess) return e;

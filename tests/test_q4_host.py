@@ -139,7 +139,7 @@ P2, P3, P4 = at(2), at(3), at(4)
 @no_device
 @pytest.mark.parametrize("want,kw", [
     (SHAPE, dict(D=8)), (SHAPE, dict(budget=0)), (SHAPE, dict(recent=-1)), (SHAPE, dict(recent=9)),
-    (SHAPE, dict(n=-1)), (SHAPE, dict(B=70000, Hkv=1)), (OK, dict(B=0)), (CAPACITY, dict(n=21)),
+    (SHAPE, dict(n=-1)), (SHAPE, dict(n=(1 << 30) + 1, cap=1 << 30)), (SHAPE, dict(B=70000, Hkv=1)), (OK, dict(B=0)), (CAPACITY, dict(n=21)),
     (CAPACITY, dict(cap_out=7)), (NULL, dict(cache=None)), (NULL, dict(w=None)), (NULL, dict(cl=None)),
     (NULL, dict(out=None)), (NULL, dict(w_out=None)), (NULL, dict(index=None)),
     (NULL, dict(len_out=None)), (PARAM, dict(out=P)), (PARAM, dict(w_out=P2)), (PARAM, dict(len_out=P3)),
