@@ -11,6 +11,10 @@ constexpr int kSms = 152;
 constexpr int kMaxSplits = 8 * kSms;           // of one row: no more than blocks on the GPU at once
 
 constexpr int kFewSplits = 8;
+// Slots whose weights one block adds up: the rows' sums, which every block needs, then weigh
+// little (8 rows of up to 4000 slots, 64 heads over 8, with weights: 256 24.6 us, 512 22.7,
+// 1024 21.1, 2048 21.7).
+constexpr int kSlots = 1024;
 
 // One query row's few splits by one warp: every load is on its way before the first factor is
 // known, and no barrier is met.
@@ -45,8 +49,8 @@ __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml
 }
 
 // Blocks [0, rows): one query row's splits merged, a split per warp at a time; with few
-// splits eight rows, one a warp. Blocks after: with weights, 256 slots of one kv head get the
-// sum over its query heads of 2^(score - reference) / sum (one thread per slot, heads in
+// splits eight rows, one a warp. Blocks after: with weights, kSlots slots of one kv head get
+// the sum over its query heads of 2^(score - reference) / sum (one thread for each, heads in
 // order, so the result does not depend on timing). A few us, bound by its chain of loads:
 // merging 64 splits one after the other in a thread took 19 us, a warp per split 5.
 __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, unsigned rows,
@@ -115,20 +119,27 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   const long bh = blk / slot_blocks;
   const int b = static_cast<int>(bh / j.Hkv), hkv = static_cast<int>(bh - static_cast<long>(b) * j.Hkv);
   const int nlive = live_slots(j, j.cache_len[b], false);
-  const int n = static_cast<int>(blk % slot_blocks) * 256 + threadIdx.x;
-  if (static_cast<int>(blk % slot_blocks) * 256 >= nlive) return;
+  const int n0 = static_cast<int>(blk % slot_blocks) * kSlots + threadIdx.x;
+  if (n0 - static_cast<int>(threadIdx.x) >= nlive) return;
   const int ns = (nlive + j.chunk - 1) / j.chunk;
   const int G = j.H / j.Hkv;
   const long row0 = static_cast<long>(b) * j.H + hkv * G;
-  float* w = j.weights + bh * j.capacity + n;
-  const float before = n < nlive ? *w : 0.f;
-  float sum = 0.f;
+  float* w = j.weights + bh * j.capacity + n0;
+  float before[kSlots / 256], sum[kSlots / 256];
+#pragma unroll
+  for (int u = 0; u < kSlots / 256; ++u) {
+    before[u] = n0 + 256 * u < nlive ? w[256 * u] : 0.f;
+    sum[u] = 0.f;
+  }
   for (int g0 = 0; g0 < G; g0 += 8) {
     const int heads = min(8, G - g0);
-    float s[8];
+    float s[kSlots / 256][8];
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
-      s[h] = h < heads && n < nlive ? j.scores[(row0 + g0 + h) * j.pitch + n] : 0.f;
+    for (int u = 0; u < kSlots / 256; ++u)
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        s[u][h] = h < heads && n0 + 256 * u < nlive
+                      ? j.scores[(row0 + g0 + h) * j.pitch + n0 + 256 * u] : 0.f;
     if (warp < heads) {
       const float2* r = ml + (row0 + g0 + warp) * j.nsplit;
       float m = -INFINITY, l = 0.f;
@@ -145,10 +156,15 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 8; ++h)
-      if (h < heads) sum = fmaf(ex2(s[h] - sh[h].x), sh[h].y, sum);
+      if (h < heads) {
+#pragma unroll
+        for (int u = 0; u < kSlots / 256; ++u) sum[u] = fmaf(ex2(s[u][h] - sh[h].x), sh[h].y, sum[u]);
+      }
     __syncthreads();
   }
-  if (n < nlive) *w = before + sum;
+#pragma unroll
+  for (int u = 0; u < kSlots / 256; ++u)
+    if (n0 + 256 * u < nlive) w[256 * u] = before[u] + sum[u];
 }
 
 int eff_len(int max_cache_len, int window) {
@@ -168,10 +184,11 @@ int most_splits(int B, int H, int Hkv, int D) {
 }
 
 // The most splits of any length up to this one: it does not shrink as the length grows.
-// Up to 16 tiles stay in one block: the second launch costs what the split saves.
-int split_bound(int B, int H, int Hkv, int D, int max_cache_len, int window) {
+// Up to 16 tiles stay in one block: the second launch costs what the split saves. With
+// weights it comes anyway (one row of 500 slots: 8.3 us in one block, 6.2 in four splits).
+int split_bound(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
-  if (tiles <= kShortTiles) return 1;
+  if (tiles <= kShortTiles && !weights) return 1;
   const int most = (tiles + kWarps - 1) / kWarps;             // a tile for every warp
   const int want = most_splits(B, H, Hkv, D);
   return want < most ? want : most;
@@ -189,10 +206,10 @@ int split_bound(int B, int H, int Hkv, int D, int max_cache_len, int window) {
 // 8 rows of up to 4000: 2 21.8, 4 18.8, 7 17.6, 14 25.3; 64 rows of 512..8192, 8 kv heads of
 // 4: 1 89.3, 2 82.5, 4 72.8, 8 73.8, 16 90.9; 8 rows of 4096, D = 256, 8 kv heads of 2: 2 27.3,
 // 4 23.8, 6 31.8, 8 27.1.
-void decode_q4_plan(int B, int H, int Hkv, int D, int max_cache_len, int window, int* nsplit,
-                    int* chunk) {
+void decode_q4_plan(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights,
+                    int* nsplit, int* chunk) {
   const int tiles = (eff_len(max_cache_len, window) - 1) / kTile + 1;
-  const int bound = split_bound(B, H, Hkv, D, max_cache_len, window);
+  const int bound = split_bound(B, H, Hkv, D, max_cache_len, window, weights);
   const long units = units_of(B, H, Hkv);
   const int resident = resident_blocks(D / 32, head_tiles(H, Hkv));
   double least = 1e30;
@@ -203,7 +220,7 @@ void decode_q4_plan(int B, int H, int Hkv, int D, int max_cache_len, int window,
     const double rate = k == 1 ? 0.65 : (k == 2 ? 0.93 : 1.0);
     const double wave = k > resident && k < 2 * resident ? 1.25 : 1.0;
     const double time = k * ((per + kWarps - 1) / kWarps * kWarps + 6) / rate * wave +
-                        (n == 1 ? 0 : (n <= kFewSplits ? 6 : 12));
+                        (n == 1 && !weights ? 0 : (n <= kFewSplits ? 6 : 12));
     if (time < least) {
       least = time;
       best = per;
@@ -231,12 +248,13 @@ Layout layout(int B, int H, int D, int nsplit, int eff, bool weights) {
 }  // namespace
 
 size_t decode_q4_bytes(int B, int H, int Hkv, int D, int max_cache_len, int window, bool weights) {
-  return layout(B, H, D, split_bound(B, H, Hkv, D, max_cache_len, window),
+  return layout(B, H, D, split_bound(B, H, Hkv, D, max_cache_len, window, weights),
                 eff_len(max_cache_len, window), weights).total;
 }
 
 size_t decode_q4_prepare(DecodeQ4Job* j) {
-  decode_q4_plan(j->B, j->H, j->Hkv, j->D, j->max_cache_len, j->window, &j->nsplit, &j->chunk);
+  decode_q4_plan(j->B, j->H, j->Hkv, j->D, j->max_cache_len, j->window, j->weights != nullptr,
+                 &j->nsplit, &j->chunk);
   const Layout y = layout(j->B, j->H, j->D, j->nsplit, eff_len(j->max_cache_len, j->window),
                           j->weights != nullptr);
   j->pitch = y.pitch;
@@ -256,7 +274,7 @@ cudaError_t launch_decode_q4(const DecodeQ4Job& j, const StepQ4Args& st, cudaStr
   if (e != cudaSuccess || (j.nsplit == 1 && !j.weights)) return e;
   const unsigned heads = static_cast<unsigned>(j.B) * j.H;
   const unsigned rows = j.nsplit == 1 ? 0 : (j.nsplit <= kFewSplits ? (heads + 7) / 8 : heads);
-  const unsigned per = j.weights ? (eff_len(j.max_cache_len, j.window) - 1) / 256 + 1 : 0;
+  const unsigned per = j.weights ? (eff_len(j.max_cache_len, j.window) - 1) / kSlots + 1 : 0;
   return launch_dependent(decode_q4_finish_kernel, rows + static_cast<unsigned>(j.B) * j.Hkv * per,
                           256, 0, stream, j, rows, per ? per : 1u);
 }
