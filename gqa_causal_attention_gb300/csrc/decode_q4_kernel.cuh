@@ -274,6 +274,17 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   const long bh = unit / ngroups;
   const int b = static_cast<int>(bh / j.Hkv), hkv = static_cast<int>(bh - static_cast<long>(b) * j.Hkv);
   const bool lead = threadIdx.x == 0 && split == 0 && g0 == 0 && hkv == 0;   // one a batch row
+  // A warp's first query head is on its way while the row's length comes.
+  const float* queries = j.q + (static_cast<long>(b) * j.H + hkv * G + g0) * D;
+  float4 q0 = make_float4(0.f, 0.f, 0.f, 0.f), q1 = q0;
+  auto load_query = [&](int h) {
+    if (lane < 4 * M && h < min(kHeads, G - g0)) {
+      const float4* src = reinterpret_cast<const float4*>(queries + h * D + 8 * lane);
+      q0 = __ldg(src);
+      q1 = __ldg(src + 1);
+    }
+  };
+  load_query(warp);
   const bool step = st.kv.k != nullptr;
   StepRow row{};
   if (step) row = step_row(st, b, lead);
@@ -330,20 +341,15 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   // = 1), or n = h in two fragments, high and low.
   uint2* frag = reinterpret_cast<uint2*>(smem + NW * kStages * TILE_BYTES);
   for (int h = warp; h < kHeads; h += NW) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    const bool there = lane < 4 * M;
-    const float* qrow = j.q + (static_cast<long>(b) * j.H + hkv * G + min(g0 + h, G - 1)) * D;
-    const int g = lane >> 2, a = lane & 3;
-    if (there && g0 + h < G) {
-      const float4* src = reinterpret_cast<const float4*>(qrow + 8 * lane);
-      const float4 t0 = __ldg(src), t1 = __ldg(src + 1);
-      x[0] = t0.x; x[1] = t0.y; x[2] = t0.z; x[3] = t0.w;
-      x[4] = t1.x; x[5] = t1.y; x[6] = t1.z; x[7] = t1.w;
+    if (h > warp) {
+      q0 = q1 = make_float4(0.f, 0.f, 0.f, 0.f);
+      load_query(h);
     }
+    float x[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    const bool there = lane < 4 * M;
+    const int g = lane >> 2, a = lane & 3;
     if (step)
-      rotate_query(qrow, st.kv.table + static_cast<long>(row.pos) * (st.kv.R / 2), st.kv.R,
+      rotate_query(queries + h * D, st.kv.table + static_cast<long>(row.pos) * (st.kv.R / 2), st.kv.R,
                    st.q_norm_w, st.kv.norm_eps, D, g0 + h < G ? 8 * lane : D, x);
     uint32_t top = 0;
 #pragma unroll
