@@ -266,16 +266,19 @@ __device__ __forceinline__ uint32_t warps_before(uint32_t own, uint32_t* wsum, u
   return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
 }
 
-// One block per (row, head): the need-th largest of the old slots' keys, then one ordered
-// pass that writes the kept slots' numbers and weights. The largest by its top 11 or 13 bits
-// (sign, exponent and two or four bits more: a histogram of them, summed from the top); then
-// among the few keys that share those, gathered, by counting for each how many are larger;
-// where they are not few, by histograms of the next bits first. The weights are read once
-// where their keys fit in shared memory, the first of them before the length is known, else
-// again from L2 in each pass. Bound by one block's issue and its chain of barriers: every
-// instruction counts 16 or 32 times a pass (128 heads of up to 8192 slots: 8 us; 8 of 1100: 4.5).
+// `parts` blocks per (row, head), each for a share of the kept slots: the need-th largest of
+// the old slots' keys, then one ordered pass that writes the kept slots' numbers and weights.
+// The largest by its top 11 or 13 bits (sign, exponent and two or four bits more: a histogram
+// of them, summed from the top); then among the few keys that share those, gathered, by
+// counting for each how many are larger; where they are not few, by histograms of the next
+// bits first. The weights are read once where their keys fit in shared memory, the first of
+// them before the length is known, else again from L2 in each pass. Bound by one block's issue
+// and its chain of barriers: every instruction counts 16 or 32 times a pass (128 heads of up
+// to 8192 slots: 8 us).
+// With several parts, where the heads alone would leave SMs idle, every block finds the whole
+// threshold for itself, writes its share and moves its records too: no second launch.
 template <int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held) {
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j, int held, int parts) {
   constexpr int kTopBits = kSelThreads == 1024 ? 13 : 11, kBins = 1 << kTopBits;
   constexpr int kPer = kBins / kSelThreads, kTileSlots = kSelThreads * kSelItems;
   constexpr int kShare = kSelThreads / kFew;     // threads that count for one of the few keys
@@ -288,8 +291,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   dependent_wait();
   if (gated_off(j.skip)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long bh = blockIdx.x;
-  const int b = static_cast<int>(bh / j.Hkv);
+  const int head = blockIdx.x / parts, part = blockIdx.x - head * parts;
+  const long bh = head;
+  const int b = head / j.Hkv;
+  const bool lead = tid == 0 && part == 0 && head % j.Hkv == 0;            // one a batch row
   const float* w = j.weights + bh * j.capacity;
   float ahead[kSelItems];
 #pragma unroll
@@ -307,26 +312,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   clear();
   const int n = j.cache_len[b];
   if (n < 0 || n > j.max_cache_len || n > j.capacity) {
-    if (tid == 0 && bh % j.Hkv == 0) report(j.status, ATTN_DEV_LENGTH);
+    if (lead) report(j.status, ATTN_DEV_LENGTH);
     return;
   }
   float* wo = j.weights_out + bh * j.capacity_out;
   int32_t* index = j.index + bh * j.budget;
   const int kept = min(n, j.budget);
-  if (tid == 0 && bh % j.Hkv == 0) j.len_out[b] = kept;
-  for (long i = kept + tid; i < j.capacity_out; i += kSelThreads) wo[i] = 0.f;
-  for (int i = kept + tid; i < j.budget; i += kSelThreads) index[i] = -1;
-  // What is kept whatever its weight: all, or the recent slots, behind the others.
-  const int old = n <= j.budget ? 0 : n - j.recent, need = n <= j.budget ? 0 : j.budget - j.recent;
-  for (int i = old + tid; i < n; i += kSelThreads) {
-    index[need + i - old] = i;
-    wo[need + i - old] = w[i];
+  if (lead) j.len_out[b] = kept;
+  if (part == parts - 1) {
+    for (long i = kept + tid; i < j.capacity_out; i += kSelThreads) wo[i] = 0.f;
+    for (int i = kept + tid; i < j.budget; i += kSelThreads) index[i] = -1;
   }
-  if (need == 0) return;                     // n <= budget, or only recent slots are kept
+  // Kept whatever its weight: all, or the recent slots, behind the others (`need` old ones).
+  const int old = n <= j.budget ? 0 : n - j.recent, need = n <= j.budget ? 0 : j.budget - j.recent;
 
   // Keys of whole tiles, 0 behind the last; their histogram.
   const bool in_smem = old <= held;
-  for (int i0 = 0; i0 < old; i0 += kTileSlots) {
+  for (int i0 = 0; need > 0 && i0 < old; i0 += kTileSlots) {
 #pragma unroll
     for (int e = 0; e < kSelItems; ++e) {
       const int i = i0 + tid + e * kSelThreads;
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
   // Threshold: keys above T are kept, and the first `left` of those equal to it.
   uint32_t T = 0, left = static_cast<uint32_t>(need);
 #pragma unroll 1
-  for (int shift = 32 - kTopBits;;) {
+  for (int shift = 32 - kTopBits; need > 0;) {
     // bins from the top: thread t holds kPer of them, from kBins - 1 - kPer t down
     uint32_t h[kPer], mine = 0, total;
 #pragma unroll
@@ -426,11 +428,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
     break;
   }
 
+  // This block's share of the kept slots; their numbers take the histogram's place.
+  const int share = (j.budget + parts - 1) / parts, lo = part * share, hi = min(lo + share, kept);
+  auto keep = [&](int at, int slot, float weight) {
+    if (at < lo || at >= hi) return;
+    index[at] = slot;
+    wo[at] = weight;
+    if (parts > 1) hist[at - lo] = static_cast<uint32_t>(slot);
+  };
+  for (int i = old + tid; i < n; i += kSelThreads) keep(need + i - old, i, w[i]);
+
   // Ordered pass. Kept before a slot: those above T, and at most `left` equal to it. A warp's
   // slots are consecutive, 32 at a time, so its writes are too.
   uint32_t base_up = 0, base_eq = 0;
   const uint32_t below = (1u << lane) - 1u;
-  for (int t0 = 0; t0 < old; t0 += kTileSlots) {
+  for (int t0 = 0; need > 0 && t0 < old; t0 += kTileSlots) {
     const int i0 = t0 + warp * 32 * kSelItems + lane;
     uint32_t k[kSelItems], up[kSelItems], eq[kSelItems], own = 0, total;   // own: eq in the upper half
 #pragma unroll
@@ -445,16 +457,34 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
 #pragma unroll
     for (int e = 0; e < kSelItems; ++e) {
       const uint32_t u = nup + __popc(up[e] & below), q = neq + __popc(eq[e] & below);
-      if (k[e] > T || (k[e] == T && q < left)) {
-        index[u + min(q, left)] = i0 + 32 * e;
-        wo[u + min(q, left)] = key_weight(k[e]);
-      }
+      if (k[e] > T || (k[e] == T && q < left))
+        keep(static_cast<int>(u + min(q, left)), i0 + 32 * e, key_weight(k[e]));
       nup += __popc(up[e]);
       neq += __popc(eq[e]);
     }
     base_up += total & 0xffffu;
     base_eq += total >> 16;
     __syncthreads();
+  }
+  if (parts == 1) return;                    // the records are moved by the next kernel
+  __syncthreads();
+  const int P = q4::record_bytes(j.D / 32) / 16, pieces = max(hi - lo, 0) * P;
+  const uint4* src = reinterpret_cast<const uint4*>(j.cache) + bh * j.capacity * P;
+  uint4* dst = reinterpret_cast<uint4*>(j.cache_out) + (bh * j.capacity_out + lo) * P;
+  constexpr int U = 4;
+  for (int i0 = tid; i0 < pieces; i0 += kSelThreads * U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + kSelThreads * u;
+      if (i < pieces) {
+        const int r = i / P;
+        v[u] = src[static_cast<long>(hist[r]) * P + (i - r * P)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + kSelThreads * u < pieces) dst[i0 + kSelThreads * u] = v[u];
   }
 }
 
@@ -553,7 +583,7 @@ cudaError_t launch_read_q4(const ReadQ4Job& j, cudaStream_t stream) {
 
 namespace {
 template <int T>
-cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, cudaStream_t stream) {
+cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, int parts, cudaStream_t stream) {
   static PerContext<cudaError_t> allowed;    // the shared-memory size is per context
   const cudaError_t e = allowed.get(
       [] {
@@ -565,18 +595,25 @@ cudaError_t launch_select(const EvictQ4Job& j, unsigned heads, cudaStream_t stre
   constexpr int tile = T * kSelItems;        // whole tiles are held
   static_assert(kSelKeys % tile == 0, "");
   const int held = j.max_cache_len < kSelKeys ? (j.max_cache_len + tile - 1) / tile * tile : kSelKeys;
-  return launch_dependent(evict_select_kernel<T>, heads, T, held * 4, stream, j, held);
+  return launch_dependent(evict_select_kernel<T>, heads * parts, T, held * 4, stream, j, held, parts);
 }
 }  // namespace
 
 cudaError_t launch_evict_q4(const EvictQ4Job& j, cudaStream_t stream) {
   const unsigned heads = static_cast<unsigned>(j.B) * j.Hkv;
   // Short heads are chains of barriers, cheaper among 16 warps than among 32 (8 heads of 1100
-  // slots: 7.3 us with the move, 8.8 with 32 warps); long ones are work on the keys (128 heads
-  // of up to 8192: 38.5 and 35.2).
-  const cudaError_t e = j.max_cache_len <= 4096 ? launch_select<512>(j, heads, stream)
-                                                : launch_select<1024>(j, heads, stream);
-  if (e != cudaSuccess) return e;
+  // slots: 7.3 us with the move as a second kernel, 8.8 with 32 warps); long ones are work on
+  // the keys (128 heads of up to 8192: 38.5 and 35.2).
+  const bool short_heads = j.max_cache_len <= 4096;
+  // Heads that leave most SMs idle get several blocks, which move the records too (8 heads of
+  // 1100 slots 6.7 us instead of 7.3, 16 of 8192 9.3 instead of 12.1, 32 of 4000 10.4 instead
+  // of 11.3; with two blocks a head it was 64 of 4000 16.3 instead of 15.5).
+  int parts = heads > 38 ? 1 : static_cast<int>(152 / heads);
+  if (parts > 16) parts = 16;
+  if ((j.budget + parts - 1) / parts > (short_heads ? 2048 : 8192)) parts = 1;
+  const cudaError_t e = short_heads ? launch_select<512>(j, heads, parts, stream)
+                                    : launch_select<1024>(j, heads, parts, stream);
+  if (e != cudaSuccess || parts > 1) return e;
   return with_groups(j.D / 32, [&](auto g) {
     constexpr int M = decltype(g)::value;
     const long pieces = static_cast<long>(j.max_cache_len < j.budget ? j.max_cache_len : j.budget) *

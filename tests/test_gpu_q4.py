@@ -510,6 +510,9 @@ EVICT = [
     (1, 1, 256, (9000,), 9001, 8190, 4000, 8200),
     (1, 1, 32, (50000,), 50000, 20001, 3, 20001),    # more keys than shared memory holds
     (2, 2, 160, (64, 65), 70, 1, 0, 1),
+    # many heads: selected and moved by two kernels
+    (21, 2, 32, tuple(90 + 17 * i for i in range(21)), 430, 100, 20, 101),
+    (13, 3, 64, tuple(5000 - 230 * i for i in range(13)), 5003, 2500, 300, 2500),
 ]
 
 
