@@ -512,7 +512,9 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j, unsigned 
       const long i = i0 + 256 * u;
       if (i < pieces) {
         const uint32_t r = static_cast<uint32_t>(i / P);
-        v[u] = src[static_cast<long>(index[r]) * P + (i - static_cast<long>(r) * P)];
+        // (in bounds even if the length has changed since the selection)
+        const uint32_t slot = min(static_cast<uint32_t>(index[r]), static_cast<uint32_t>(j.capacity - 1));
+        v[u] = src[static_cast<long>(slot) * P + (i - static_cast<long>(r) * P)];
       }
     }
 #pragma unroll
