@@ -563,7 +563,71 @@ def test_evict_skips_bad_rows():
         assert bool((out[b] == 9).all()) and bool((w_out[b] == 9.0).all()) and bool((index[b] == 9).all())
 
 
+def test_evict_of_many_heads_skips_bad_rows():
+    """As above where the selection and the move are two kernels."""
+    B, Hkv, D, cap = 12, 4, 32, 50
+    cache, _, _ = filled(1, B, Hkv, cap, D)
+    out = torch.full((B, Hkv, 8, 48), 9, dtype=torch.uint8, device=dev())
+    w, w_out = torch.rand(B, Hkv, cap, device=dev()), torch.full((B, Hkv, 8), 9.0, device=dev())
+    index = torch.full((B, Hkv, 8), 9, dtype=torch.int32, device=dev())
+    lens = [51, 50, -1, 0, 7, 8, 9, 2 ** 31 - 1, 20, 30, 40, -2 ** 31]
+    n_out, st = i32([9] * B), status()
+    g.kv_cache_evict_q4(cache, w, i32(lens), 50, 8, 2, out, w_out, index, n_out, status=st)
+    assert value(st) == g.DEV_LENGTH
+    for b, n in enumerate(lens):
+        if not 0 <= n <= 50:
+            assert int(n_out[b]) == 9 and bool((out[b] == 9).all())
+            assert bool((w_out[b] == 9.0).all()) and bool((index[b] == 9).all())
+            continue
+        assert int(n_out[b]) == min(n, 8)
+        for h in range(Hkv):
+            keep = ref.evict(w[b, h].cpu(), n, 8, 2)
+            assert index[b, h].tolist() == keep + [-1] * (8 - len(keep))
+            assert torch.equal(out[b, h, :len(keep)], cache[b, h, keep])
+            assert bool((out[b, h, len(keep):] == 9).all()) and bool((w_out[b, h, len(keep):] == 0).all())
+
+
 # ---------------------------------------------------------------- together
+
+def test_captured_chunk_replays():
+    """Append, read back and decode captured once, replayed on new contents and positions."""
+    B, H, Hkv, D, L, cap = 2, 12, 2, 96, 37, 300
+    rp, table, tab = table_of(512, D, D)
+    k, v = (torch.randn(B, Hkv, L, D, device=dev()) for _ in range(2))
+    q, ko, kr, vr = torch.randn(B, H, 1, D, device=dev()), *(torch.empty_like(k) for _ in range(3))
+    cache = torch.zeros(B, Hkv, cap, ref.record_bytes(D), dtype=torch.uint8, device=dev())
+    start, lens, st, out = i32([0, 0]), i32([L, L]), status(), torch.empty_like(q)
+    ws = torch.empty(g.gqa_attn_decode_q4_workspace_size(B, H, Hkv, D, cap), dtype=torch.uint8,
+                     device=dev())
+
+    def chunk():
+        g.kv_cache_append_q4(k, v, cache, start, cap - L, rp, table, k_out=ko, status=st)
+        g.kv_cache_read_q4(cache, kr, vr, start, cap - L, status=st)
+        g.gqa_attn_decode_q4(q, cache, lens, cap, out, workspace=ws, status=st)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        chunk()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        chunk()
+    kc, vc = (torch.zeros(B, Hkv, cap, D, dtype=torch.float64) for _ in range(2))
+    for i in range(4):
+        at = [i * L, i * L]
+        x = [syn.normal(30 + i, m, t.shape) for m, t in (("k", k), ("v", v), ("q", q))]
+        for t, y in zip((k, v, q, start, lens), x + [i32(at), i32([a + L for a in at])]):
+            t.copy_(y)
+        graph.replay()
+        assert value(st) == 0
+        y = ref.rotate(x[0], at, tab)
+        kc[:, :, i * L:(i + 1) * L], vc[:, :, i * L:(i + 1) * L] = ref.stands_for(y), ref.stands_for(x[1])
+        assert torch.equal(kr.cpu().double(), ref.stands_for(y))
+        assert torch.equal(vr.cpu().double(), ref.stands_for(x[1]))
+        want, _, S = ref.decode(x[2], kc, vc, [a + L for a in at])
+        close(out, want, 2e-6 * (1 + S / math.log(2)) * float(vc.abs().max()))
+
 
 def test_serving_run_with_eviction():
     """A prompt enters a 4-bit cache and is attended; a second prompt chunk continues it (read
