@@ -94,7 +94,8 @@ __device__ __forceinline__ Target append_target(const AppendQ4Job& j, const RowA
 // chunk longer than its ring, the last rows of each head), seg_tiles blocks each.
 // 4 x 2048 tokens, 8 heads, D = 128, RoPE, rotated keys kept (111 MB): 25 us, 4.4 TB/s; bound
 // by issue (225 instructions for a row's 256 values, 2.4 of 4 a cycle). Sixteen rows and seven
-// blocks an SM: with 32 rows in 256 threads 8 % slower, eight rows 6 %.
+// blocks an SM: with 32 rows in 256 threads 8 % slower, eight rows 6 %; six blocks 2 % slower,
+// eight the same.
 template <int M, int ROPE>
 __global__ void __launch_bounds__(kRowThreads, 7) append_q4_kernel(AppendQ4Job j, int tr,
                                                                    long seg_rows, int seg_tiles) {
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
 }
 
 // The kept records, 16 bytes a thread, four in flight: 128 heads' 4096 of 8192 records of 144
-// bytes (151 MB) in 27 us, 5.6 TB/s.
+// bytes (151 MB) in 27 us, 5.6 TB/s (two in flight 2.3 us more, eight 3.2; streaming loads and
+// stores the same).
 template <int M>
 __global__ void __launch_bounds__(256) evict_move_kernel(EvictQ4Job j, unsigned per_head) {
   dependents_may_launch();
