@@ -226,6 +226,17 @@ def _i32(name: str, t):
         raise TypeError(f"{name} must be a contiguous CUDA int32 tensor")
 
 
+def _workspace(nbytes: int, like, stream):
+    """Scratch for one call on `stream` (None: the current one). It is taken on that stream, so
+    that whatever used or will use the block is ordered with the call: a block of the current
+    stream's pool may still be written by a kernel queued there for a tensor freed since."""
+    nbytes = max(16, nbytes)
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def _check(fn: str, rc: int):
     if rc != 0:
         raise AttnError(fn, rc)
@@ -829,13 +840,6 @@ def _native():
         return _ext
 
 
-def _q4_workspace(size: int, like, stream):
-    ws = torch.empty(max(16, size), dtype=torch.uint8, device=like.device)
-    if stream is not None:       # taken on the current stream, used on this one
-        ws.record_stream(stream)
-    return ws
-
-
 def kv_cache_append_q4(k, v, cache, start, max_start: int, params: RopeParams = None, table=None,
                        k_norm_w=None, norm_eps: float = 1e-6, k_out=None, pos=None,
                        max_pos: int = 0, window: int = 0, status=None, stream=None) -> None:
@@ -872,7 +876,7 @@ def gqa_attn_decode_q4(q, cache, cache_len, max_cache_len: int, out, weights=Non
     torch's caching allocator for this call."""
     if workspace is None:
         B, H, _, D = q.shape
-        workspace = _q4_workspace(gqa_attn_decode_q4_workspace_size(
+        workspace = _workspace(gqa_attn_decode_q4_workspace_size(
             B, H, cache.shape[1], D, max_cache_len, window, weights is not None), q, stream)
     rc = (_ext or _native()).decode(q, cache, cache_len, max_cache_len, out, weights, window,
                                     softcap, scale, workspace, status, stream)
@@ -897,7 +901,7 @@ def gqa_attn_decode_step_q4(q, k, v, out, cache, start, max_start: int, params: 
     gqa_attn_decode_q4; workspace: gqa_attn_decode_step_q4_workspace_size bytes, or None."""
     if workspace is None:
         B, H, _, D = q.shape
-        workspace = _q4_workspace(gqa_attn_decode_step_q4_workspace_size(
+        workspace = _workspace(gqa_attn_decode_step_q4_workspace_size(
             B, H, cache.shape[1], D, max_start, window, weights is not None), q, stream)
     rc = (_ext or _native()).step(q, k, v, out, cache, start, max_start, params, table, q_norm_w,
                                   k_norm_w, norm_eps, pos, max_pos, weights, window, softcap,

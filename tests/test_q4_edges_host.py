@@ -1,0 +1,49 @@
+"""The 4-bit KV cache on the host, next to test_q4_host: where a call's workspace comes from."""
+import contextlib
+
+import pytest
+import torch
+
+import gqa_causal_attention_gb300 as g
+
+
+class Taken(Exception):
+    pass
+
+
+@pytest.fixture
+def pool(monkeypatch):
+    """Torch's allocator stopped at the binding's first request, which is raised as
+    Taken(stream, bytes); streams are names."""
+    current = ["current"]
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    def empty(n, dtype=torch.float32, device=None):
+        raise Taken(current[-1], int(n) * torch.tensor([], dtype=dtype).element_size())
+
+    t = {name: torch.zeros(shape) for name, shape in (
+        ("q", (2, 16, 1, 64)), ("k", (2, 2, 1, 64)), ("cache", (2, 2, 3000, 80)))}
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", empty)
+    return t
+
+
+@pytest.mark.parametrize("stream", [None, "other"])
+@pytest.mark.parametrize("weights", [None, True])
+def test_a_workspace_is_taken_on_the_stream_that_uses_it(pool, stream, weights):
+    q, k, cache = pool["q"], pool["k"], pool["cache"]
+    calls = [
+        (lambda: g.gqa_attn_decode_q4(q, cache, None, 2999, q, weights=weights, stream=stream),
+         g.gqa_attn_decode_q4_workspace_size(2, 16, 2, 64, 2999, 0, bool(weights))),
+        (lambda: g.gqa_attn_decode_step_q4(q, k, k, q, cache, None, 2999, None, None,
+                                           weights=weights, stream=stream),
+         g.gqa_attn_decode_step_q4_workspace_size(2, 16, 2, 64, 2999, 0, bool(weights)))]
+    for call, size in calls:
+        with pytest.raises(Taken) as e:
+            call()
+        assert e.value.args == (stream or "current", size)
