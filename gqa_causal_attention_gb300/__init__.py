@@ -281,11 +281,12 @@ def attn_rope_table_init(params: RopeParams, D: int, table: torch.Tensor, stream
 
 
 def rope_table(params: RopeParams, D: int, device="cuda", stream=None) -> torch.Tensor:
-    """Allocate (with torch) and fill the cos/sin table for ``params``."""
+    """Allocate (with torch) and fill the cos/sin table for ``params``, both on `stream`."""
     n = attn_rope_table_bytes(params, D)
     if n == 0:
         raise AttnError("attn_rope_table_bytes", -7)
-    t = torch.empty(n // 4, dtype=torch.float32, device=device)
+    with torch.cuda.stream(stream):          # None: the current one
+        t = torch.empty(n // 4, dtype=torch.float32, device=device)
     attn_rope_table_init(params, D, t, stream)
     return t
 
@@ -339,7 +340,7 @@ def gqa_attn_prefill(q, k, v, out, window: int = 0, softcap: float = 0.0, scale:
         raise ValueError("gqa_attn_prefill: inconsistent shapes")
     if workspace is None:
         n = gqa_attn_prefill_workspace_size(B, Hkv, L, D)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -371,7 +372,7 @@ def gqa_attn_prefill_rope(q, k, v, out, start, max_start: int, params: RopeParam
         raise ValueError("gqa_attn_prefill_rope: inconsistent shapes")
     if workspace is None:
         n = gqa_attn_prefill_rope_workspace_size(B, H, Hkv, L, D, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -410,7 +411,7 @@ def gqa_attn_prefill_ragged(q, k, v, out, lengths, params: RopeParams = None, ta
         raise ValueError("gqa_attn_prefill_ragged: lengths must hold B values")
     if workspace is None:
         n = gqa_attn_prefill_ragged_workspace_size(B, H, Hkv, L, D, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -463,7 +464,7 @@ def gqa_attn_prefill_rope_vt(q, k, vt, out, start, max_start: int, params: RopeP
                          "B * Hkv * D * gqa_attn_vt_pitch(L) elements")
     if workspace is None:
         n = gqa_attn_prefill_rope_vt_workspace_size(B, H, L, D, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -511,7 +512,7 @@ def gqa_attn_prefill_from_host(q_host, k_host, v_host, out_host, q, k, v, out, k
     cap = int(k_cache.shape[2])
     if workspace is None:
         n = gqa_attn_prefill_from_host_workspace_size(B, H, Hkv, L, D, cap, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -550,7 +551,7 @@ def gqa_attn_prefill_cached(q, k, v, k_cache, v_cache, out, start, max_start: in
         raise ValueError("gqa_attn_prefill_cached: inconsistent shapes")
     if workspace is None:
         n = gqa_attn_prefill_cached_workspace_size(B, H, Hkv, L, D, max_start, window, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -671,7 +672,7 @@ def gqa_attn_prefill_step(q, k, v, out, k_cache, v_cache, params: RopeParams, ta
         raise ValueError("gqa_attn_prefill_step: inconsistent shapes")
     if workspace is None:
         n = gqa_attn_prefill_step_workspace_size(B, H, Hkv, L, D, window, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -718,7 +719,7 @@ def gqa_attn_decode_step(q, k, v, out, pos, max_pos: int, k_cache, v_cache, para
         raise ValueError("gqa_attn_decode_step: inconsistent shapes")
     if workspace is None:
         n = gqa_attn_decode_step_workspace_size(B, H, Hkv, D, max_pos, window)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=q.device)
+        workspace = _workspace(n, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
@@ -784,7 +785,7 @@ def gqa_block_forward(x, out, weights: dict, n_heads: int, n_kv_heads: int,
         setattr(w, field, t.data_ptr())
     if workspace is None:
         n = gqa_block_forward_workspace_size(B, L, H, Hkv, D, IT, params)
-        workspace = torch.empty(max(4, n // 4), dtype=torch.float32, device=x.device)
+        workspace = _workspace(n, x, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     wbytes = workspace.numel() * workspace.element_size()
