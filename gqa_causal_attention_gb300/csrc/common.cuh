@@ -21,7 +21,8 @@ __device__ __forceinline__ bool gated_off(const int32_t* skip) {
 
 // A kernel launched by launch_dependent may start while the one enqueued before it still
 // runs, whatever that one is: it must call dependent_wait before its first access to global
-// memory, which returns when everything before has ended and its writes are visible. With
+// memory, which returns when everything before has ended and its writes are visible. What it
+// reads may thus be written while it is already resident: no read-only loads (__ldg). With
 // dependents_may_launch a kernel lets the next one be placed once all of its own blocks have
 // got there. (Every kernel of the 4-bit cache waits this way: they are short, and between
 // two of them the launch otherwise costs about 2 us.)

@@ -243,7 +243,7 @@ __device__ __forceinline__ void rotate_query(const float* row, const float2* tab
     if (d < R) {
       const int i = d < half ? d : d - half, p = d < half ? d + half : i;
       const float b = nw ? row[p] * inv * nw[p] : row[p];
-      const float2 t = __ldg(tab + i);
+      const float2 t = tab[i];
       a = d < half ? fmaf(a, t.x, -b * t.y) : fmaf(a, t.x, b * t.y);
     }
     x[e] = a;
@@ -280,8 +280,8 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   auto load_query = [&](int h) {
     if (lane < 4 * M && h < min(kHeads, G - g0)) {
       const float4* src = reinterpret_cast<const float4*>(queries + h * D + 8 * lane);
-      q0 = __ldg(src);
-      q1 = __ldg(src + 1);
+      q0 = src[0];
+      q1 = src[1];
     }
   };
   load_query(warp);

@@ -1,5 +1,9 @@
-"""The 4-bit KV cache on the host, next to test_q4_host: where a call's workspace comes from."""
+"""The 4-bit KV cache on the host, next to test_q4_host: where a call's workspace comes from,
+and how its kernels read."""
 import contextlib
+import glob
+import os
+import re
 
 import pytest
 import torch
@@ -47,3 +51,15 @@ def test_a_workspace_is_taken_on_the_stream_that_uses_it(pool, stream, weights):
         with pytest.raises(Taken) as e:
             call()
         assert e.value.args == (stream or "current", size)
+
+
+def test_kernels_that_start_early_read_by_plain_loads():
+    """A kernel launched by launch_dependent is resident while the ones before it still write:
+    the read-only path (__ldg, ld.global.nc) wants data that nothing writes in that time."""
+    csrc = os.path.join(os.path.dirname(g.__file__), "csrc")
+    seen = 0
+    for path in glob.glob(os.path.join(csrc, "*q4*")):
+        code = re.sub(r"//[^\n]*", "", open(path).read())
+        seen += "dependent_wait()" in code
+        assert not re.search(r"__ldg|\.nc\b|__restrict__", code), path
+    assert seen >= 3
