@@ -31,8 +31,9 @@ __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml
     for (int s = 0; s < kFewSplits; ++s)
       if (s < ns && d < j.D)
         p[s] = *reinterpret_cast<const float4*>(part + static_cast<long>(s) * j.D + d);
-    const float m = warp_max(t.x), f = t.x == -INFINITY ? 0.f : ex2(t.x - m);
-    const float inv = 1.0f / warp_sum(f * t.y);
+    const float m = warp_max(t.x);
+    float f = t.x == -INFINITY ? 0.f : ex2(t.x - m) * t.y;
+    f *= 1.0f / warp_sum(f);                 // a split's share of the row
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int s = 0; s < kFewSplits; ++s) {
@@ -43,8 +44,7 @@ __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml
       }
     }
     if (d < j.D)
-      *reinterpret_cast<float4*>(j.out + row * j.D + d) =
-          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      *reinterpret_cast<float4*>(j.out + row * j.D + d) = y;
   }
 }
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml
 __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, unsigned rows,
                                                                unsigned slot_blocks) {
   __shared__ float factor[kMaxSplits];
-  __shared__ float red[8];
+  __shared__ float red[8], sums[8];
   __shared__ __align__(16) float acc[8][kMaxHeadDim];
   __shared__ float2 sh[8];
   dependent_wait();
@@ -84,19 +84,23 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
     float l = 0.f;
     for (int s = threadIdx.x; s < ns; s += 256) {
       const float2 t = ml[s];
-      const float f = t.x == -INFINITY ? 0.f : ex2(t.x - m);
+      const float f = t.x == -INFINITY ? 0.f : ex2(t.x - m) * t.y;
       factor[s] = f;
-      l = fmaf(f, t.y, l);
+      l += f;
     }
     l = warp_sum(l);
+    if (lane == 0) sums[warp] = l;
     __syncthreads();
-    if (lane == 0) red[warp] = l;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) l += sums[w];
+    const float inv = 1.0f / l;
     const float* part = j.partial + row * j.nsplit * j.D;
     for (int d = 4 * lane; d < j.D; d += 128) {
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int s = warp; s < ns; s += 8) {
-        const float f = factor[s];
+        const float f = factor[s] * inv;     // a split's share of the row
         const float4 t = *reinterpret_cast<const float4*>(part + static_cast<long>(s) * j.D + d);
         y.x = fmaf(f, t.x, y.x); y.y = fmaf(f, t.y, y.y);
         y.z = fmaf(f, t.z, y.z); y.w = fmaf(f, t.w, y.w);
@@ -106,13 +110,9 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
     __syncthreads();
     if (threadIdx.x >= j.D) return;
     float y = 0.f;
-    l = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      y += acc[w][threadIdx.x];
-      l += red[w];
-    }
-    j.out[row * j.D + threadIdx.x] = y / l;
+    for (int w = 0; w < 8; ++w) y += acc[w][threadIdx.x];
+    j.out[row * j.D + threadIdx.x] = y;
     return;
   }
   const unsigned blk = blockIdx.x - rows;

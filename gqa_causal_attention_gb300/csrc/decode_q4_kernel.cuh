@@ -38,10 +38,12 @@
 // heads over 8, 302 MB in 62 us, 4.9 TB/s. With 8 heads a kv head 864 a tile, 2.4 a cycle from
 // twelve warps an SM: one row of 131072 slots, 151 MB in 45 us.
 //
-// The reference of p is the running row maximum minus 14 plus the running exponent of
-// the value scales, so that p * sv peaks near 2^14 whatever the values' magnitude and
-// both fp16 parts keep their bits down to 2^-24. (p itself is dropped below 2^-126, which is
-// 2^(-126 + e) of the largest for values near 2^(e + 17): nothing below values of 1e30.)
+// p and its sum are relative to the running row maximum. For the products p is multiplied by
+// 2^-e (exact), e the running exponent of the warp's value scales less 14, so that p * sv peaks
+// near 2^14 and both fp16 parts keep their bits down to 2^-24: 22 bits of every weighted value
+// within 2^16 of the largest scale the warp has met, fewer below. The output's sums stay in
+// units of 2^e until they are normalised, so they neither overflow nor vanish: e reaches down to
+// -127, where scales below 2^-126 (values below 1e-37) begin to lose bits.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -101,6 +103,11 @@ __device__ __forceinline__ uint32_t codes(uint32_t w) {
       : "=r"(u)
       : "r"(w), "n"(ODD ? 0x00f000f0 : 0x000f000f), "r"(0x64006400u));
   return as_u32(__hsub2(as_half2(u), as_half2(ODD ? 0x64806480u : 0x64086408u)));
+}
+
+// 2^n, n <= 127: 0 below fp32's subnormals' first binary order.
+__device__ __forceinline__ float pow2(int n) {
+  return __uint_as_float(n >= -126 ? static_cast<uint32_t>(127 + n) << 23 : (n == -127 ? 0x400000u : 0u));
 }
 
 // The top eleven bits of x >= 0 below 2^16: exact in fp16, as is the rest in fp32. (Below
@@ -261,6 +268,7 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   __shared__ uint64_t full[NW][kStages];
   __shared__ float q_factor[kHeads];
   __shared__ float sm_m[NW][kHeads], sm_l[NW][kHeads];
+  __shared__ int sm_e[NW];
   __shared__ int abort_flag;
   dependent_wait();
   if (gated_off(j.skip)) return;
@@ -393,7 +401,7 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   }
 
   float m_run[NT], l_run[NT];
-  int e_run = -60 - 14;                      // exponent of the reference beside the maximum
+  int e_run = -127;                          // o's unit is 2^e_run
   float o[NT][M][4];                         // head(t), dims 32 g + 4 r + (0 .. 3)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -538,12 +546,12 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
       moved |= m_new[t] > m_run[t];
     }
     if (__any_sync(0xffffffffu, moved)) {
+      const float coarser = pow2(e_run - e_new);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float corr = m_new[t] == -INFINITY
-                               ? 1.f
-                               : ex2((m_run[t] - m_new[t]) + static_cast<float>(e_run - e_new));
+        float corr = m_new[t] == -INFINITY ? 1.f : ex2(m_run[t] - m_new[t]);
         l_run[t] *= corr;
+        corr *= coarser;
 #pragma unroll
         for (int g = 0; g < M; ++g)
 #pragma unroll
@@ -553,13 +561,15 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
       e_run = e_new;
     }
     float p[NT][4];
+    const float lift = pow2(-e_run);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float ref = (m_run[t] == -INFINITY ? 0.f : m_run[t]) + static_cast<float>(e_run);
+      const float ref = m_run[t] == -INFINITY ? 0.f : m_run[t];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         p[t][x] = ex2(s[t][x] - ref);
         l_run[t] += p[t][x];
+        p[t][x] *= lift;
       }
     }
 
@@ -629,7 +639,6 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) l_run[t] += __shfl_xor_sync(0xffffffffu, l_run[t], off);
-    m_run[t] += static_cast<float>(e_run);
     // Scores that were all NaN have no maximum; any one keeps their sum in the merge.
     if (m_run[t] == -INFINITY && l_run[t] != l_run[t]) m_run[t] = 0.f;
     if (r == 0) {
@@ -637,7 +646,10 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
       sm_l[warp][head(t)] = l_run[t];
     }
   }
+  if (lane == 0) sm_e[warp] = e_run;
   __syncthreads();
+  const int e_all = __reduce_max_sync(0xffffffffu, sm_e[lane % NW]);
+  const float coarser = pow2(e_run - e_all);
   float* ex = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -645,7 +657,7 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
     float m_all = sm_m[0][h];
 #pragma unroll
     for (int w = 1; w < NW; ++w) m_all = fmaxf(m_all, sm_m[w][h]);
-    const float f = m_run[t] == -INFINITY ? 0.f : ex2(m_run[t] - m_all), fo = f * 0.0625f;
+    const float f = (m_run[t] == -INFINITY ? 0.f : ex2(m_run[t] - m_all)) * coarser, fo = f * 0.0625f;
 #pragma unroll
     for (int g = 0; g < M; ++g)
       *reinterpret_cast<float4*>(ex + h * D + 32 * g + 4 * r) =
@@ -670,13 +682,12 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
                                                         (h * D + d) * 4);
       y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
     }
-    if (single) {
-      const float inv = 1.0f / L;
-      *reinterpret_cast<float4*>(j.out + (hrow0 + h) * D + d) =
-          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    } else {
-      *reinterpret_cast<float4*>(j.partial + ((hrow0 + h) * j.nsplit + split) * D + d) = y;
-    }
+    // Out of the unit only when normalised, a split's part by its own sum: a mean of values.
+    // (A split without any weight counts for nothing; a row without any has no softmax.)
+    const float inv = L == 0.f && !single ? 0.f : 1.0f / L, back = pow2(e_all);
+    float* to = single ? j.out + (hrow0 + h) * D : j.partial + ((hrow0 + h) * j.nsplit + split) * D;
+    *reinterpret_cast<float4*>(to + d) =
+        make_float4(y.x * inv * back, y.y * inv * back, y.z * inv * back, y.w * inv * back);
     if ((WEIGHTS || !single) && d == 0)
       *reinterpret_cast<float2*>(ml + 2 * ((hrow0 + h) * j.nsplit + split)) = make_float2(M_, L);
   }

@@ -407,7 +407,7 @@ struct DecodeQ4Job {
   float* weights;           // [B, Hkv, capacity] or nullptr: += each slot's softmax weights
   int B, H, Hkv, D, capacity, window;
   float softcap, scale;
-  float* partial;           // [B * H * nsplit, D] outputs, then (m, l) pairs
+  float* partial;           // [B * H * nsplit, D] outputs of a split's slots alone, then (m, l)
   float* scores;            // weights only: [B * H, pitch] scores in log2 units
   int nsplit, chunk, pitch;
   size_t scores_at;

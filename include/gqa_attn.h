@@ -568,8 +568,9 @@ int kv_cache_read_q4(const void* cache, int capacity, int window, float* k, floa
 /*
  * gqa_attn_decode over a 4-bit cache: same q, out, cache_len, window, softcap and scale,
  * with the keys and values the records stand for. Products and sums keep fp32's
- * accuracy (the queries and softmax weights are split in two fp16 parts, the codes are
- * exact).
+ * accuracy (the queries and softmax weights are split in two fp16 parts of 22 bits, the
+ * codes are exact) for values from 1e-37 to fp32's largest; of a value group whose scale
+ * is 2^(16 + n) below the largest that the same warp reads, 22 - n bits remain.
  *   weights   device fp32 [B, Hkv, capacity] or NULL. weights[b,hkv,n] += the sum over
  *             the kv head's query heads of slot n's softmax weight, for every live slot;
  *             others are left alone. What kv_cache_evict_q4 ranks slots by. Not with a

@@ -1,0 +1,68 @@
+"""The 4-bit KV cache at the ends of its ranges: values of any magnitude, weights held to their
+own size. Reference: q4_ref, in 64 bits.
+
+Outputs here are held to their own weighted sums, A = sum p |v|, at scores of S <= 1/2 (log2
+units): a score is off by at most 12 * 2^-23 of its terms' magnitudes (as in test_gpu_q4),
+which are under 1/2, so p by 12 * 2^-23 / 2 * ln 2 + 2^-22 (the exponential) = 7.4e-7, numerator
+and denominator each; p times a scale is split into 22 bits, 2^-23; sums of at most 10 tiles a
+warp, 16 warps and 10 splits, each step 2^-24 of A, 2.2e-6. Together 3.9e-6 A; 4e-6 A is the
+bound."""
+import math
+
+import pytest
+import torch
+
+import gqa_causal_attention_gb300 as g
+import q4_ref as ref
+from gqa_causal_attention_gb300 import synthetic as syn
+
+from gpu_util import dev
+from test_gpu_q4 import filled, i32, status, value
+
+pytestmark = pytest.mark.gpu
+
+
+def quiet(seed, B, H, Hkv, D, n, vmul):
+    """A cache whose scores stay within 1/2, its values (normal) times vmul: (q, cache, k, v)."""
+    cache, k, v = filled(seed, B, Hkv, n, D, (0.03, vmul))
+    q = syn.normal(seed + 1, "q", (B, H, 1, D)).clamp(-2, 2)
+    return q, cache, k, v
+
+
+def held(q, cache, k, v, lens):
+    """Decode with and without weights against the reference, each within 4e-6 of its own size."""
+    B, H, _, D = q.shape
+    Hkv, n = k.shape[1:3]
+    want, ww, S = ref.decode(q, k, v, lens)
+    size, _, _ = ref.decode(q, k, v.abs(), lens)
+    assert S <= 0.5 / math.log2(math.e)
+    for weights in (None, torch.zeros(B, Hkv, n, device=dev())):
+        out, st = torch.full((B, H, 1, D), math.nan, device=dev()), status()
+        g.gqa_attn_decode_q4(q.to(dev()), cache, i32(lens), n, out, weights=weights, status=st)
+        assert value(st) == 0
+        # fp32's own last bit, below 2^-126
+        err = ((out.cpu().double() - want).abs() - 2.0 ** -149) / size.clamp(min=1e-300)
+        assert bool(out.isfinite().all()) and float(err.max()) <= 4e-6, float(err.max())
+        if weights is not None:
+            err = (weights.cpu().double() - ww).abs() - 4e-6 * ww      # 0 behind the live slots
+            assert float(err.max()) <= 0, float(err.max())
+
+
+@pytest.mark.parametrize("D,G,n", [(64, 4, 333), (128, 8, 300), (256, 2, 200)])
+@pytest.mark.parametrize("vmag", [1e-37, 1e-35, 1e-30, 1e-27, 1e-25, 1.0, 1e20, 1e30, 1e36, 4e37])
+def test_decode_keeps_fp32_accuracy_of_values_of_any_magnitude(vmag, D, G, n):
+    held(*quiet(D, 1, 2 * G, 2, D, n, vmag), [n])
+
+
+@pytest.mark.parametrize("one_sign", [False, True])
+@pytest.mark.parametrize("early,late", [(0.0, 1e25), (1e25, 0.0), (1e-30, 1e25), (1e-35, 1e35), (1e35, 1e-35)])
+@pytest.mark.parametrize("n", [300, 3000])
+def test_decode_of_values_that_change_magnitude(n, early, late, one_sign):
+    """Slots of one magnitude, then of another, up to 2^232 apart: those of the smaller values
+    keep their share of the softmax. With one sign the values' sum is past fp32's largest number."""
+    vmul = torch.full((1, 1, n, 1), early)
+    vmul[:, :, n // 2:] = late
+    if one_sign:
+        vmul = vmul * torch.where(syn.normal(n, "v", (2, 2, n, 64)) < 0, -1.0, 1.0)
+    q, cache, k, v = quiet(n, 2, 8, 2, 64, n, vmul)
+    held(q, cache, k, v, [n, n - 1])
