@@ -622,11 +622,8 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   }
   if (i < mine && lane == 0) {
     // A wait ran out: let the copies already issued land, then report.
-    for (int u = i; u < min(mine, i + kStages); ++u) {
-      const uint64_t t0 = tc::globaltimer();
-      while (!tc::mbar_try_wait(&full[warp][u % kStages], (u / kStages) & 1))
-        if (tc::globaltimer() - t0 > tc::kWaitLimitNs) break;
-    }
+    for (int u = i; u < min(mine, i + kStages); ++u)
+      tc::mbar_drain(&full[warp][u % kStages], (u / kStages) & 1);
     report(j.status, ATTN_DEV_TIMEOUT);
   }
 

@@ -133,8 +133,11 @@ __global__ void __launch_bounds__(kRowThreads, 7) append_q4_kernel(AppendQ4Job j
   __syncthreads();
   if (!tc::mbar_wait(&full, 0, &abort_flag)) abort_flag = 1;
   __syncthreads();
-  if (abort_flag) {                          // the copies never came
-    if (threadIdx.x == 0) report(j.status, ATTN_DEV_TIMEOUT);
+  if (abort_flag) {                          // the copies are late
+    if (threadIdx.x == 0) {
+      tc::mbar_drain(&full, 0);
+      report(j.status, ATTN_DEV_TIMEOUT);
+    }
     return;
   }
   const q4::Lanes<M> at(lane);

@@ -1,5 +1,6 @@
 """The 4-bit KV cache on the host, next to test_q4_host: where a call's workspace comes from,
-and how its kernels read."""
+and
+how its kernels read and give up."""
 import contextlib
 import glob
 import os
@@ -63,3 +64,16 @@ def test_kernels_that_start_early_read_by_plain_loads():
         seen += "dependent_wait()" in code
         assert not re.search(r"__ldg|\.nc\b|__restrict__", code), path
     assert seen >= 3
+
+
+def test_a_block_that_gives_up_lets_its_copies_land():
+    """Where a wait for bulk copies into shared memory runs out, the block drains them before it
+    reports and ends. (A copy that never comes cannot be made on the host; read in the source.)"""
+    csrc = os.path.join(os.path.dirname(g.__file__), "csrc")
+    seen = 0
+    for path in glob.glob(os.path.join(csrc, "*q4*")):
+        code = open(path).read()
+        for m in re.finditer(r"report\([^;]*ATTN_DEV_TIMEOUT\)", code):
+            seen += 1
+            assert "mbar_drain(" in code[max(0, m.start() - 300):m.start()], path
+    assert seen == 2
