@@ -101,7 +101,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     with _lock:
         if _lib is not None:
             return _lib
-        path = _build.build() if build_if_missing else _build.LIB
+        path = _build.build_lib() if build_if_missing else _build.LIB
         lib = ctypes.CDLL(path)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         rp = ctypes.POINTER(RopeParams)

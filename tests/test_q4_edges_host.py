@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import gqa_causal_attention_gb300 as g
+from gqa_causal_attention_gb300 import _build
 
 
 class Taken(Exception):
@@ -77,3 +78,26 @@ def test_a_block_that_gives_up_lets_its_copies_land():
             seen += 1
             assert "mbar_drain(" in code[max(0, m.start() - 300):m.start()], path
     assert seen == 2
+
+
+def test_the_library_loads_where_the_extension_cannot_be_built(monkeypatch):
+    """Calls that never touch the 4-bit cache need neither torch's headers nor a compiler."""
+    def none(*a, **kw):
+        raise RuntimeError("no compiler")
+
+    g.load()
+    monkeypatch.setattr(_build, "build_ext", none)
+    monkeypatch.setattr(_build.subprocess, "run", none)
+    monkeypatch.setattr(g, "_lib", None)
+    monkeypatch.setattr(g, "_ext", None)
+    assert g.load() is g.load()
+    assert g.attn_version() and g.gqa_attn_decode_workspace_size(1, 8, 2, 64, 500) > 0
+    with pytest.raises(RuntimeError, match="no compiler"):
+        g.kv_cache_read_q4(None, None, None, None, 0)
+
+
+def test_an_extension_of_another_torch_is_not_taken(monkeypatch):
+    path = _build.build_ext()
+    assert _build.ext_up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not _build.ext_up_to_date() and _build.ext_path() != path
