@@ -21,7 +21,7 @@ constexpr int kSlots = 1024;
 __device__ __forceinline__ void merge_few(const DecodeQ4Job& j, const float2* ml, long row, int lane) {
   const int nlive = live_slots(j, j.cache_len[row / j.H], false);
   if (nlive <= j.chunk) return;              // finished by its one split, or invalid
-  const int ns = (nlive + j.chunk - 1) / j.chunk;
+  const int ns = (nlive - 1) / j.chunk + 1;
   const float* part = j.partial + row * j.nsplit * j.D;
   const float2 t = lane < ns ? ml[row * j.nsplit + lane] : make_float2(-INFINITY, 0.f);
   for (int d0 = 0; d0 < j.D; d0 += 128) {
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
     const long row = blockIdx.x;
     const int nlive = live_slots(j, j.cache_len[row / j.H], false);
     if (nlive <= j.chunk) return;            // finished by its one split, or invalid
-    const int ns = (nlive + j.chunk - 1) / j.chunk;
+    const int ns = (nlive - 1) / j.chunk + 1;
     ml += row * j.nsplit;
     float m = -INFINITY;
     for (int s = threadIdx.x; s < ns; s += 256) m = fmaxf(m, ml[s].x);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) decode_q4_finish_kernel(DecodeQ4Job j, un
   const int nlive = live_slots(j, j.cache_len[b], false);
   const int n0 = static_cast<int>(blk % slot_blocks) * kSlots + threadIdx.x;
   if (n0 - static_cast<int>(threadIdx.x) >= nlive) return;
-  const int ns = (nlive + j.chunk - 1) / j.chunk;
+  const int ns = (nlive - 1) / j.chunk + 1;
   const int G = j.H / j.Hkv;
   const long row0 = static_cast<long>(b) * j.H + hkv * G;
   float* w = j.weights + bh * j.capacity + n0;
@@ -183,6 +183,9 @@ int most_splits(int B, int H, int Hkv, int D) {
   return static_cast<int>(n < 1 ? 1 : n);
 }
 
+// Two splits where one would hold more slots than an int counts in whole tiles.
+int least_splits(int tiles) { return tiles > (1 << 30) / kTile ? 2 : 1; }
+
 // The most splits of any length up to this one: it does not shrink as the length grows.
 // Up to 16 tiles stay in one block: the second launch costs what the split saves. With
 // weights it comes anyway (one row of 500 slots: 8.3 us in one block, 6.2 in four splits).
@@ -191,7 +194,7 @@ int split_bound(int B, int H, int Hkv, int D, int max_cache_len, int window, boo
   if (tiles <= kShortTiles && !weights) return 1;
   const int most = (tiles + kWarps - 1) / kWarps;             // a tile for every warp
   const int want = most_splits(B, H, Hkv, D);
-  return want < most ? want : most;
+  return want < least_splits(tiles) ? least_splits(tiles) : (want < most ? want : most);
 }
 
 }  // namespace
@@ -214,7 +217,8 @@ void decode_q4_plan(int B, int H, int Hkv, int D, int max_cache_len, int window,
   const int resident = resident_blocks(D / 32, head_tiles(H, Hkv));
   double least = 1e30;
   int best = tiles;
-  for (int n = 1, per = tiles; n <= bound; n = per > 1 ? (tiles + per - 2) / (per - 1) : bound + 1) {
+  for (int n = least_splits(tiles), per = tiles; n <= bound;
+       n = per > 1 ? (tiles + per - 2) / (per - 1) : bound + 1) {
     per = (tiles + n - 1) / n;               // the next n is the first with fewer tiles a block
     const long k = (units * n + kSms - 1) / kSms;
     const double rate = k == 1 ? 0.65 : (k == 2 ? 0.93 : 1.0);
@@ -233,14 +237,14 @@ void decode_q4_plan(int B, int H, int Hkv, int D, int max_cache_len, int window,
 namespace {
 struct Layout {
   size_t scores, total;
-  int pitch;
+  long pitch;
 };
 Layout layout(int B, int H, int D, int nsplit, int eff, bool weights) {
   Layout y{};
   const size_t rows = static_cast<size_t>(B) * H;
   size_t p = nsplit > 1 || weights ? rows * nsplit * (D + 2) * sizeof(float) : 0;
   y.scores = p = (p + 255) / 256 * 256;
-  y.pitch = (eff + 3) / 4 * 4;
+  y.pitch = (eff + 3L) / 4 * 4;
   if (weights) p += rows * y.pitch * sizeof(float);
   y.total = p;
   return y;

@@ -299,7 +299,7 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
   const int nlive = live_slots(j, step ? row.n : j.cache_len[b], lead);
   const int k0 = split * j.chunk;
   if (k0 >= nlive) return;
-  const int k1 = min(k0 + j.chunk, nlive);
+  const int k1 = k0 + min(j.chunk, nlive - k0);
   const int tiles = (k1 - k0 + kTile - 1) / kTile;
   const int mine = tiles > warp ? (tiles - 1 - warp) / NW + 1 : 0;
 

@@ -409,7 +409,8 @@ struct DecodeQ4Job {
   float softcap, scale;
   float* partial;           // [B * H * nsplit, D] outputs of a split's slots alone, then (m, l)
   float* scores;            // weights only: [B * H, pitch] scores in log2 units
-  int nsplit, chunk, pitch;
+  int nsplit, chunk;
+  long pitch;
   size_t scores_at;
   int32_t* status;
   const int32_t* skip = nullptr;

@@ -101,3 +101,12 @@ def test_an_extension_of_another_torch_is_not_taken(monkeypatch):
     assert _build.ext_up_to_date()
     monkeypatch.setattr(torch, "__version__", "0.0.1")
     assert not _build.ext_up_to_date() and _build.ext_path() != path
+
+
+@pytest.mark.parametrize("B,H,Hkv,D", [(1, 8, 8, 128), (1, 1, 1, 32), (1, 1 << 17, 1, 32), (3, 24, 2, 96)])
+def test_workspace_sizes_up_to_the_longest_caches(B, H, Hkv, D):
+    last = 0
+    for n in [(1 << i) + d for i in range(20, 31) for d in (0, 1)] + [2 ** 31 - d for d in range(70, 0, -1)]:
+        size = g.gqa_attn_decode_q4_workspace_size(B, H, Hkv, D, n, 0, True)
+        assert 4 * B * H * n <= size and last <= size < 2 ** 52
+        last = size
