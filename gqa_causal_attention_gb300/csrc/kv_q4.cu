@@ -403,7 +403,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
     }
     for (int i = tid; i < old; i += kSelThreads) {
       const uint32_t k = key_of(i);
-      if (k >> shift == T >> shift) few[atomicAdd(&gathered, 1u)] = k;
+      if (k >> shift == T >> shift) {        // (in bounds even if a weight has changed since)
+        const uint32_t at = atomicAdd(&gathered, 1u);
+        if (at < kFew) few[at] = k;
+      }
     }
     if (tid >= count && tid < (count + 3) / 4 * 4) few[tid] = 0;           // below every key
     __syncthreads();
@@ -482,8 +485,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictQ4Job j,
     for (int u = 0; u < U; ++u) {
       const int i = i0 + kSelThreads * u;
       if (i < pieces) {
-        const int r = i / P;
-        v[u] = src[static_cast<long>(hist[r]) * P + (i - r * P)];
+        const int r = i / P;                 // (and here)
+        const uint32_t slot = min(hist[r], static_cast<uint32_t>(j.capacity - 1));
+        v[u] = src[static_cast<long>(slot) * P + (i - r * P)];
       }
     }
 #pragma unroll

@@ -620,7 +620,9 @@ int gqa_attn_decode_step_q4(const float* q, const float* k, const float* v, floa
  * rotated); later tokens go to slot start = len_out with pos still counting positions.
  * 0 <= recent <= budget <= capacity_out; cache_len[b] in [0, max_cache_len] (else
  * ATTN_DEV_LENGTH, and the row is skipped), max_cache_len <= 2^30. An output that overlaps
- * an input: ATTN_ERR_PARAM; no ring. B * Hkv <= 65535.
+ * an input: ATTN_ERR_PARAM; no ring. B * Hkv <= 65535. (Weights or lengths that another
+ * stream changes during the call make the result meaningless, but nothing is read or written
+ * out of bounds.)
  */
 int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* cache_len,
                       int32_t max_cache_len, int budget, int recent, void* cache_out,

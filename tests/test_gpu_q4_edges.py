@@ -66,3 +66,38 @@ def test_decode_of_values_that_change_magnitude(n, early, late, one_sign):
         vmul = vmul * torch.where(syn.normal(n, "v", (2, 2, n, 64)) < 0, -1.0, 1.0)
     q, cache, k, v = quiet(n, 2, 8, 2, 64, n, vmul)
     held(q, cache, k, v, [n, n - 1])
+
+
+def sorted_keep(w, n, budget, recent):
+    """The kept slots of one head's n live ones, in order (no NaN among the weights)."""
+    old = n - recent
+    first = torch.sort(w[:old], descending=True, stable=True).indices[:budget - recent]
+    return torch.cat([first.sort().values, torch.arange(old, n, device=w.device)])
+
+
+@pytest.mark.parametrize("B,cap,n,budget,recent", [
+    (64, 65536, 65000, 300, 10),             # 512 heads: two kernels, keys reread from memory
+    (1, 4200000, 4199999, 4100000, 1000),    # 8 heads, several blocks each if the shares fit
+    (1, 4200000, 4100001, 70000, 0),
+])
+def test_evict_far_into_large_caches(B, cap, n, budget, recent):
+    """Records past 2^32 bytes from the start of the cache, and of the output where it is as large."""
+    Hkv, D, cap_out = 8, 128, cap
+    d = dev()
+    cache = torch.full((B, Hkv, cap, 144), 255, dtype=torch.uint8, device=d)
+    cache[B - 1].random_(0, 256)
+    w = torch.rand(B, Hkv, cap, device=d).mul_(1 << 12).floor_()      # ties throughout
+    out = torch.full((B, Hkv, cap_out, 144), 9, dtype=torch.uint8, device=d)
+    w_out = torch.full((B, Hkv, cap_out), math.nan, device=d)
+    index = torch.empty(B, Hkv, budget, dtype=torch.int32, device=d)
+    n_out, st = i32([-7] * B), status()
+    g.kv_cache_evict_q4(cache, w, i32([0] * (B - 1) + [n]), cap, budget, recent, out, w_out, index,
+                        n_out, status=st)
+    assert value(st) == 0 and n_out.tolist() == [0] * (B - 1) + [budget]
+    assert bool((index[:-1] == -1).all()) and bool((w_out[:-1] == 0).all())
+    for h in (0, 3, Hkv - 1):
+        keep = sorted_keep(w[B - 1, h], n, budget, recent)
+        assert torch.equal(index[B - 1, h].long(), keep)
+        assert torch.equal(w_out[B - 1, h, :budget], w[B - 1, h, keep])
+        assert torch.equal(out[B - 1, h, :budget], cache[B - 1, h, keep])
+        assert bool((w_out[B - 1, h, budget:] == 0).all()) and bool((out[B - 1, h, budget:] == 9).all())
