@@ -17,7 +17,7 @@ import q4_ref as ref
 from gqa_causal_attention_gb300 import synthetic as syn
 
 from gpu_util import dev
-from test_gpu_q4 import filled, i32, status, value
+from test_gpu_q4 import filled, i32, status, table_of, value
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,38 @@ def test_evict_far_into_large_caches(B, cap, n, budget, recent):
         assert torch.equal(w_out[B - 1, h, :budget], w[B - 1, h, keep])
         assert torch.equal(out[B - 1, h, :budget], cache[B - 1, h, keep])
         assert bool((w_out[B - 1, h, budget:] == 0).all()) and bool((out[B - 1, h, budget:] == 9).all())
+
+
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("B,H,Hkv,D,lens,softcap", [
+    (1, 8, 1, 128, (20000,), 0.0), (2, 32, 8, 128, (700, 129), 0.0), (1, 32, 2, 64, (5000,), 30.0),
+    (3, 4, 4, 96, (1, 33, 500), 0.0), (1, 10, 1, 256, (3001,), 0.0),
+])
+def test_weights_are_held_to_their_own_size(B, H, Hkv, D, lens, softcap, step):
+    """Eviction ranks slots by these, so each is held to the outputs' bound (test_gpu_q4) times
+    itself, however small; and every kv head's new weights sum to its query heads. (That sum
+    differs by the exponentials' 2^-22, taken once for the sums and once for the weights, their
+    arguments' rounding, 2^-20 ln 2 below 2^5, and the sums' own: under 3e-6 of it.)"""
+    n, G = max(lens), H // Hkv
+    cache, k, v = filled(H + D, B, Hkv, n, D)
+    q = syn.normal(D, "q", (B, H, 1, D))
+    out, st = torch.empty(B, H, 1, D, device=dev()), status()
+    w = torch.zeros(B, Hkv, n, device=dev())
+    if step:                                 # the last slot enters again, at position 0
+        rp, table, _ = table_of(16, D, D)
+        at = [x - 1 for x in lens]
+        new = [syn.normal(7, name, (B, Hkv, 1, D)) for name in ("k", "v")]
+        g.gqa_attn_decode_step_q4(q.to(dev()), new[0].to(dev()), new[1].to(dev()), out, cache,
+                                  i32(at), n - 1, rp, table, pos=i32([0] * B), weights=w,
+                                  softcap=softcap, status=st)
+        for b in range(B):
+            k[b, :, at[b]], v[b, :, at[b]] = (ref.stands_for(x)[b, :, 0] for x in new)
+    else:
+        g.gqa_attn_decode_q4(q.to(dev()), cache, i32(lens), n, out, weights=w, softcap=softcap,
+                             status=st)
+    assert value(st) == 0
+    _, ww, S = ref.decode(q, k, v, lens, softcap)
+    got = w.cpu().double()
+    err = (got - ww).abs() - 2e-6 * (1 + S / math.log(2)) * ww
+    assert float(err.max()) <= 2.0 ** -126
+    assert float((got.sum(-1) / G - 1).abs().max()) <= 1e-5
