@@ -136,3 +136,13 @@ def test_weights_are_held_to_their_own_size(B, H, Hkv, D, lens, softcap, step):
     err = (got - ww).abs() - 2e-6 * (1 + S / math.log(2)) * ww
     assert float(err.max()) <= 2.0 ** -126
     assert float((got.sum(-1) / G - 1).abs().max()) <= 1e-5
+
+
+@pytest.mark.parametrize("kmag,qmag", [(2e31, 5e-33), (1e20, 1e-21), (1e-10, 1e9), (1e-36, 1e35)])
+def test_decode_keeps_fp32_accuracy_of_keys_of_any_magnitude(kmag, qmag):
+    """Keys up to 1e32 in magnitude, queries to match (scores within 1/2)."""
+    B, H, Hkv, D, n = 1, 8, 2, 64, 333
+    cache, k, v = filled(8, B, Hkv, n, D, (kmag, 1.0))
+    q = syn.normal(9, "q", (B, H, 1, D)).clamp(-2, 2) * (0.3 * qmag)
+    assert float(k.abs().max()) <= 1e32
+    held(q, cache, k, v, [n])

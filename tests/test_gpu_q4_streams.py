@@ -126,3 +126,28 @@ def test_captured_branches_that_join():
         k2, v2 = torch.cat([k[:, :, :n], a, b], 2), torch.cat([v[:, :, :n], b, a], 2)
         want, _, S = ref.decode(qs[0], k2, v2, [n + 2] * 2)
         assert (out[2].cpu().double() - want).abs().max() <= 2e-6 * (1 + 1.45 * S) * v2.abs().max()
+
+
+def test_captured_calls_on_branches_take_workspaces_of_their_own():
+    """Decodes without a workspace on two branches of a captured stream, several on each."""
+    B, H, Hkv, D, n = 2, 8, 2, 64, 3000
+    cache, k, v = filled(5, B, Hkv, n, D)
+    q = torch.stack([syn.normal(i, "q", (B, H, 1, D)) for i in range(6)]).to(dev())
+    want, out = torch.empty_like(q), torch.zeros_like(q)
+    length = i32([n, n - 5])
+    for i in range(6):
+        g.gqa_attn_decode_q4(q[i], cache, length, n, want[i])
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        for i in range(6):
+            g.gqa_attn_decode_q4(q[i], cache, length, n, out[i], stream=side if i % 2 else None)
+        main.wait_stream(side)
+    for _ in range(5):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
