@@ -561,7 +561,7 @@ decode_q4_kernel(DecodeQ4Job j, StepQ4Args st) {
       e_run = e_new;
     }
     float p[NT][4];
-    const float lift = pow2(-e_run);
+    const float lift = __uint_as_float(static_cast<uint32_t>(127 - e_run) << 23);   // 2^-e_run
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const float ref = m_run[t] == -INFINITY ? 0.f : m_run[t];
