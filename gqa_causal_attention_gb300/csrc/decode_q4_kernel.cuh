@@ -33,10 +33,14 @@
 // m16n8k16 steps) and are then added to the fp32 sums: those round to nearest, the tensor
 // core's do not, and over a long cache that would drift.
 //
-// What bounds it: issue. A 32-key tile at D = 128 takes 658 instructions of a warp (304 of them
-// unpack), 2.7 a cycle and SM, with the memory at 60 % of its peak: 32 rows of 8192 slots, 32
-// heads over 8, 302 MB in 62 us, 4.9 TB/s. With 8 heads a kv head 864 a tile, 2.4 a cycle from
-// twelve warps an SM: one row of 131072 slots, 151 MB in 45 us.
+// What bounds it: no one unit. A 32-key tile at D = 128 takes 707 instructions of a warp, starts
+// and ends among them (304 unpack); 32 rows of 8192 slots, 32 heads over 8 (302 MB, 4.7 TB/s):
+// 2.8 of 4 instructions a cycle, ALU pipe at 58 %, memory at 59 %, tensor pipe at 25 %. The sixteen
+// warps an SM that the registers leave wait for the ALU pipe and for their own results in turn, and
+// 1280 blocks are two waves and a little. With 8 heads a kv head, twelve warps an SM, 881
+// instructions a tile, 2.4 a cycle: one row of 131072 slots, 151 MB in 46 us, 3.3 TB/s. With few
+// or ragged rows the blocks' uneven shares come on top: a row takes the same chunk whatever its
+// length, so the last block of a short row has little, and some SMs hold two blocks, others one.
 //
 // p and its sum are relative to the running row maximum. For the products p is multiplied by
 // 2^-e (exact), e the running exponent of the warp's value scales less 14, so that p * sv peaks
@@ -158,7 +162,7 @@ __device__ __forceinline__ float unit_scale(uint32_t w, int odd) {     // bf16 h
 
 constexpr int kStages = 2;
 
-// Blocks an SM holds: what registers (117 a thread at D = 128 with NT = 1, 163 with 2) and,
+// Blocks an SM holds: what registers (124 a thread at D = 128 with NT = 1, 163 with 2) and,
 // from D = 192, shared memory leave. Twenty warps an SM instead of sixteen were no faster at
 // D = 128.
 __host__ __device__ constexpr int resident_blocks(int M, int NT) {

@@ -535,7 +535,8 @@ size_t kv_q4_record_bytes(int D);   /* 36 m rounded up to 16; 0 for an invalid D
 /*
  * Cache append, as kv_cache_append, into 4-bit records: for each row b, kv head, token l
  *   y = RoPE(RMSNorm(k[b,hkv,l,:]))   (norm if k_norm_w, its sum of squares in fp32 as in
- *                                      the other calls; both only if rp)
+ *                                      the other calls, so not for rows whose squares leave
+ *                                      fp32's normal numbers; both only if rp)
  *   record at slot(start[b] + l)  <-  y and v[b,hkv,l,:], quantised as above
  *   k_out[b,hkv,l,:] <- y in fp32     (k_out NULL: not wanted; k_out == k: in place)
  * k and v [B, Hkv, L, D] are only read, unless k_out is k (one that overlaps k or v in
@@ -569,8 +570,9 @@ int kv_cache_read_q4(const void* cache, int capacity, int window, float* k, floa
  * gqa_attn_decode over a 4-bit cache: same q, out, cache_len, window, softcap and scale,
  * with the keys and values the records stand for. Products and sums keep fp32's
  * accuracy (the queries and softmax weights are split in two fp16 parts of 22 bits, the
- * codes are exact) for values from 1e-37 to fp32's largest; of a value group whose scale
- * is 2^(16 + n) below the largest that the same warp reads, 22 - n bits remain.
+ * codes are exact) for values from 1e-37 to fp32's largest and keys up to 1e32, past which
+ * scores may overflow whatever q is; of a value group whose scale is 2^(16 + n) below the
+ * largest that the same warp reads, 22 - n bits remain.
  *   weights   device fp32 [B, Hkv, capacity] or NULL. weights[b,hkv,n] += the sum over
  *             the kv head's query heads of slot n's softmax weight, for every live slot;
  *             others are left alone. What kv_cache_evict_q4 ranks slots by. Not with a
