@@ -39,12 +39,30 @@ __all__ = [
     "kv_q4_record_bytes", "kv_cache_append_q4", "kv_cache_read_q4", "kv_cache_evict_q4",
     "gqa_attn_decode_q4", "gqa_attn_decode_q4_workspace_size",
     "gqa_attn_decode_step_q4", "gqa_attn_decode_step_q4_workspace_size",
+    "kv_cache_append_paged", "gqa_attn_decode_paged", "gqa_attn_decode_paged_workspace_size",
+    "gqa_attn_decode_shared", "gqa_attn_decode_shared_workspace_size", "gqa_attn_prefill_packed",
     "attn_selftest_wait_timeout",
     "attn_status_string", "attn_version", "attn_last_cuda_error", "rope_table", "ROPE_SCALING",
-    "DEV_POSITION", "DEV_CAPACITY", "DEV_LENGTH", "DEV_TIMEOUT",
+    "DEV_POSITION", "DEV_CAPACITY", "DEV_LENGTH", "DEV_TIMEOUT", "DEV_PAGE",
 ]
 
 DEV_POSITION, DEV_CAPACITY, DEV_LENGTH, DEV_TIMEOUT, DEV_NONFINITE = 1, 2, 4, 8, 16
+DEV_PAGE = 32
+TYPE_FP16, TYPE_BF16 = 1, 2
+
+
+class Rows(ctypes.Structure):
+    """Mirror of ``attn_rows``."""
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class PagedKv(ctypes.Structure):
+    """Mirror of ``attn_paged_kv``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
 ROPE_SCALING = {None: 0, "none": 0, "linear": 1, "llama3": 2}
 
 
@@ -106,6 +124,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         rp = ctypes.POINTER(RopeParams)
         f = ctypes.c_float
+        rows, kv = ctypes.POINTER(Rows), ctypes.POINTER(PagedKv)
         sig = {
             "attn_rope_table_bytes": (sz, [rp, i32]),
             "attn_rope_table_init": (i32, [rp, i32, vp, sz, vp]),
@@ -178,6 +197,20 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                               f, vp, vp, i32, i32, f, f, vp, sz, vp, vp]),
             "kv_cache_evict_q4": (i32, [vp, vp, vp, ctypes.c_int32, i32, i32, vp, vp, vp, vp,
                                         i32, i32, i32, i32, i32, vp, vp]),
+            "kv_cache_append_paged": (i32, [i32, rows, rows, rows, rows, rows, i32, i32, i32, i32,
+                                            i32, vp, vp, ctypes.c_int32, rp, vp, vp, vp, f, kv,
+                                            vp, i32, vp, vp]),
+            "gqa_attn_decode_paged_workspace_size": (sz, [i32, i32, i32, i32, ctypes.c_int32,
+                                                          i32]),
+            "gqa_attn_decode_paged": (i32, [i32, rows, kv, vp, i32, vp, ctypes.c_int32, rows, i32,
+                                            i32, i32, i32, i32, f, f, vp, sz, vp, vp]),
+            "gqa_attn_decode_shared_workspace_size": (sz, [i32, i32, i32, i32, ctypes.c_int32,
+                                                           ctypes.c_int32]),
+            "gqa_attn_decode_shared": (i32, [i32, rows, kv, vp, i32, ctypes.c_int32, vp, i32, vp,
+                                             ctypes.c_int32, rows, i32, i32, i32, i32, f, f, vp,
+                                             sz, vp, vp]),
+            "gqa_attn_prefill_packed": (i32, [i32, rows, rows, rows, vp, ctypes.c_int32, rows,
+                                              i32, i32, i32, i32, i32, i32, f, f, vp, vp]),
             "attn_selftest_wait_timeout": (i32, [vp, vp]),
             "attn_status_string": (ctypes.c_char_p, [i32]),
             "attn_version": (ctypes.c_char_p, []),
@@ -836,7 +869,9 @@ def _native():
             loader.exec_module(ext)
             ext.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
                 "kv_cache_append_q4", "kv_cache_read_q4", "gqa_attn_decode_q4",
-                "gqa_attn_decode_step_q4", "kv_cache_evict_q4", "kv_q4_record_bytes")))
+                "gqa_attn_decode_step_q4", "kv_cache_evict_q4", "kv_q4_record_bytes",
+                "kv_cache_append_paged", "gqa_attn_decode_paged", "gqa_attn_decode_shared",
+                "gqa_attn_prefill_packed")))
             _ext = ext
         return _ext
 
@@ -921,3 +956,83 @@ def kv_cache_evict_q4(cache, weights, cache_len, max_cache_len: int, budget: int
                                    cache_out, weights_out, index, len_out, status, stream)
     if rc:
         raise AttnError("kv_cache_evict_q4", rc)
+
+
+# ---------------------------------------------------------------- 16-bit paged serving
+
+def kv_cache_append_paged(k, v, k_cache, v_cache, block_table, start, max_pos: int,
+                          params: RopeParams = None, table=None, k_norm_w=None,
+                          norm_eps: float = 1e-6, cu_seqlens=None, q=None, q_out=None,
+                          q_norm_w=None, k_out=None, status=None, stream=None) -> None:
+    """Packed tokens into a paged cache: k, v [T, Hkv, D] (fp16 or bf16; k through RMSNorm and
+    RoPE, with params) into the pages of k_cache, v_cache [pages, Hkv, page, D] that block_table
+    (int32 [B, pages of a row]) names, sequence b's tokens (rows cu_seqlens[b] ..
+    cu_seqlens[b + 1]; None: one token each) at positions start[b] on, none above max_pos.
+    q, q_out [T, H, D]: queries rotated on the way, or None. k_out [T, Hkv, D]: the rotated keys
+    too, or None. q_out may be q and k_out may be k."""
+    rc = (_ext or _native()).append_paged(k, v, k_cache, v_cache, block_table, start, max_pos,
+                                          params, table, k_norm_w, norm_eps, cu_seqlens, q, q_out,
+                                          q_norm_w, k_out, status, stream)
+    if rc:
+        raise AttnError("kv_cache_append_paged", rc)
+
+
+def gqa_attn_decode_paged_workspace_size(B: int, H: int, Hkv: int, D: int, max_cache_len: int,
+                                         window: int = 0) -> int:
+    return int(load().gqa_attn_decode_paged_workspace_size(B, H, Hkv, D, int(max_cache_len),
+                                                           int(window)))
+
+
+def gqa_attn_decode_paged(q, k_cache, v_cache, block_table, cache_len, max_cache_len: int, out,
+                          window: int = 0, softcap: float = 0.0, scale: float = 0.0,
+                          workspace=None, status=None, stream=None) -> None:
+    """out [B, H, D] = attention of one rotated query per row (q [B, H, D], fp16 or bf16) over its
+    cache_len[b] positions (at most max_cache_len; 0 gives zeros) in the pages of k_cache,
+    v_cache [pages, Hkv, page, D] that block_table [B, pages of a row] names. workspace:
+    gqa_attn_decode_paged_workspace_size bytes, or None to take one from torch's caching
+    allocator for this call."""
+    if workspace is None:
+        B, H, D = q.shape
+        workspace = _workspace(gqa_attn_decode_paged_workspace_size(
+            B, H, k_cache.shape[1], D, max_cache_len, window), q, stream)
+    rc = (_ext or _native()).decode_paged(q, k_cache, v_cache, block_table, cache_len,
+                                          max_cache_len, out, window, softcap, scale, workspace,
+                                          status, stream)
+    if rc:
+        raise AttnError("gqa_attn_decode_paged", rc)
+
+
+def gqa_attn_decode_shared_workspace_size(B: int, H: int, Hkv: int, D: int, prefix_len: int,
+                                          max_cache_len: int) -> int:
+    return int(load().gqa_attn_decode_shared_workspace_size(B, H, Hkv, D, int(prefix_len),
+                                                            int(max_cache_len)))
+
+
+def gqa_attn_decode_shared(q, k_cache, v_cache, prefix_table, prefix_len: int, block_table,
+                           cache_len, max_cache_len: int, out, softcap: float = 0.0,
+                           scale: float = 0.0, workspace=None, status=None, stream=None) -> None:
+    """gqa_attn_decode_paged for rows that all begin with the prefix_len positions in the pages of
+    prefix_table (int32 [pages]), followed by cache_len[b] of their own in the pages of
+    block_table; the prefix is read once for all rows. workspace:
+    gqa_attn_decode_shared_workspace_size bytes, or None."""
+    if workspace is None:
+        B, H, D = q.shape
+        workspace = _workspace(gqa_attn_decode_shared_workspace_size(
+            B, H, k_cache.shape[1], D, prefix_len, max_cache_len), q, stream)
+    rc = (_ext or _native()).decode_shared(q, k_cache, v_cache, prefix_table, prefix_len,
+                                           block_table, cache_len, max_cache_len, out, softcap,
+                                           scale, workspace, status, stream)
+    if rc:
+        raise AttnError("gqa_attn_decode_shared", rc)
+
+
+def gqa_attn_prefill_packed(q, k, v, cu_seqlens, max_len: int, out, window: int = 0,
+                            softcap: float = 0.0, scale: float = 0.0, status=None,
+                            stream=None) -> None:
+    """out [T, H, D] = causal (or windowed) attention of packed prompts: sequence b is rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] (int32 [B + 1], lengths at most max_len) of q [T, H, D] and
+    k, v [T, Hkv, D] (fp16 or bf16, rotated). Rows of no sequence are left alone."""
+    rc = (_ext or _native()).prefill_packed(q, k, v, cu_seqlens, max_len, out, window, softcap,
+                                            scale, status, stream)
+    if rc:
+        raise AttnError("gqa_attn_prefill_packed", rc)

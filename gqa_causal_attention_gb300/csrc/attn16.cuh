@@ -1,0 +1,636 @@
+// Attention on the tensor cores in 16 bits ("Core Layers -- Deep Reference", "Flash Attention",
+// "MHA and GQA"): the whole prompts of a packed batch, causal or windowed; and the part of a
+// batch's single-token attention that falls on a prefix all rows share.
+//
+//   S = Q K^T,  P = 2^(c cap(S) - m),  O = sum P V,  l = sum P,  out = O / l
+//
+// over blocks of 128 keys with a running reference m per query row; products of 16-bit operands
+// with fp32 accumulation, softmax and sums in fp32, P rounded once to 16 bits for the second
+// product (half a step of the type, the size of the output's own rounding).
+//
+// How, on GB300:
+//  * A tile is 128 rows: TQ = 128 / G tokens x the G query heads of one kv head, which share
+//    every key, value and almost all of the mask. A block works on two tiles at once (tokens
+//    t0 .. t0 + TQ - 1 and the TQ after): while one tile's softmax runs, the tensor core does
+//    the other's products, and both read each K and V block once.
+//  * TMA brings Q tiles (boxes of 64 dims x G heads x TQ tokens), K and V blocks (128 keys; from
+//    pages, box by page) through one ring of stages in the 128-byte swizzle. V is the
+//    MN-major operand of the second product as it lies: no transposition.
+//  * Tensor memory: S0 | S1 (128 fp32 columns each), O0 | O1. P overwrites S's first half in
+//    16 bits and is the A operand of O += P V.
+//  * One thread issues all products, in the order P V (tile 0), next S (tile 0), P V (tile 1),
+//    next S (tile 1): the tensor pipe runs them in that order, so S may be written over the
+//    P before it without a wait.
+//  * Softmax: a thread per row, 4 warps per tile, S read in halves of 64 columns. The reference is
+//    the row's first maximum and stands until a half's sum shows that some weight exceeded
+//    2^8 (then the half is redone against a new maximum and O rescaled): no maximum is
+//    taken in the common case.
+//  * Values behind the last key (another sequence's, an unused slot's) are zeroed in shared memory:
+//    whatever lies there, NaNs included, has no part in the result.
+//  * Every wait is bounded; one that runs out raises ATTN_DEV_TIMEOUT and the block winds down.
+#pragma once
+
+#include "paged.cuh"
+#include "prefill_common.cuh"
+
+namespace gqa {
+namespace attn16 {
+
+using prefill::drain_wait;
+using prefill::kRescaleLog2;
+using prefill::kSmemLimit;
+using prefill::kTmemCols;
+
+constexpr int kBK = 128;                       // keys per block
+constexpr int kRows = 128;                     // query rows per tile
+
+struct Args {
+  int T, B, max_len;                           // packed prompts
+  const int32_t* cu;
+  const int32_t* prefix_table;                 // shared prefix
+  int prefix_len, pages, page_shift;
+  int H, Hkv, D, G, TQ;
+  int units, splits, split_keys;               // shared: row pairs, splits of the key blocks
+  int window, softcap_on;
+  float c_score, c_cap_in, c_cap_out;          // log2 units
+  void* out;
+  int64_t o_token, o_head;
+  float* part_o;
+  float2* part_ml;
+  int32_t* status;
+  const int32_t* skip;
+};
+
+template <class T_, int DP_, bool SHARED_>
+struct Cfg {
+  using T = T_;
+  static constexpr int DP = DP_;               // head dim padded to whole 64-dim chunks
+  static constexpr bool SHARED = SHARED_;
+  static constexpr bool BF16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+  static constexpr int kChunks = DP / 64;
+  static constexpr int kChunk = 128 * 128;     // 128 rows x 64 dims (128 bytes)
+  static constexpr int kTileBytes = kChunks * kChunk;   // a Q tile, a K block or a V block
+  static constexpr int kNSraw = (kSmemLimit - 2048 - 2 * kTileBytes) / kTileBytes;
+  static constexpr int NS = kNSraw > 8 ? 8 : kNSraw;
+  static constexpr int kSmem = (NS + 2) * kTileBytes + 2048;
+  static constexpr int kSCol = 0, kOCol = 256;
+  // fp16 has few small numbers and P's range is [0, 2^(8 + kBias)]: shifted up, weights down
+  // to 2^-21 of the largest keep all their bits.
+  static constexpr float kBias = BF16 ? 0.f : 7.f;
+};
+constexpr int kThreads = 320;                  // 2 x 4 softmax warps, producer, products
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2];
+  uint64_t p_ready[2][2];                      // [tile][half]
+  uint64_t o_half[2], o_done[2];
+  uint64_t v_fixed;                            // the last block's V is zeroed behind the last key
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  struct {
+    int hk, row0, q0, ntok, kbase, nk, jlo, jhi, nt, la, part;
+  } unit;
+};
+using Unit = decltype(Bars::unit);
+
+// Tile t's key blocks: [lo, hi] in steps of la, from the first that is its own.
+__device__ __forceinline__ bool active(const Args& a, const Unit& u, int t, int j, bool shared) {
+  if (shared) return u.la == 2 ? ((j - u.jlo) & 1) == t : t < u.nt;
+  if (t >= u.nt) return false;
+  const int first = u.q0 + t * a.TQ, last = min(first + a.TQ, u.q0 + u.ntok) - 1;
+  if (j * kBK > last) return false;
+  return !(a.window > 0 && (j + 1) * kBK <= first - a.window + 1);
+}
+
+// ---------------------------------------------------------------- producer (one warp)
+template <class C>
+__device__ void producer(const Args& a, const Unit& u, const CUtensorMap* tq, const CUtensorMap* tk,
+                         const CUtensorMap* tv, uint8_t* sq, uint8_t* skv, Bars* bars, int lane) {
+  volatile int* abort = &bars->abort;
+  int stage = 0;
+  uint32_t phase = 0, loaded = 0;              // loads so far
+  if (lane == 0) {
+    const int tiles = u.la == 2 ? 1 : u.nt;
+    tc::mbar_arrive_expect_tx(&bars->q_full, tiles * C::kChunks * 128 * a.G * a.TQ);
+    for (int t = 0; t < tiles; ++t)
+      for (int c = 0; c < C::kChunks; ++c)
+        tc::tma_load_3d(sq + t * C::kTileBytes + c * C::kChunk, tq, &bars->q_full, 64 * c,
+                        u.hk * a.G, u.row0 + t * a.TQ);
+  }
+  // The last block holds fewer than 128 keys: its V is zeroed behind them.
+  const int last_keys = u.nk - u.jhi * kBK;
+  auto load = [&](bool is_v, int j) -> bool {
+    bool ok = true;
+    uint64_t* full = &bars->kv_full[stage];
+    uint8_t* dst = skv + stage * C::kTileBytes;
+    int rows = kBK, id = 0;
+    const int page = 1 << a.page_shift, box = min(page, kBK);
+    if (C::SHARED) {
+      // one lane per page of the block
+      const int n = min(kBK, u.nk - j * kBK), boxes = (n + box - 1) / box;
+      if (lane < boxes) {
+        id = a.prefix_table[(static_cast<int64_t>(j) * kBK + lane * box) >> a.page_shift];
+        if (id < 0 || id >= a.pages) {
+          report(a.status, ATTN_DEV_PAGE);
+          id = -1;
+        }
+      }
+      rows = boxes * box;
+    }
+    if (lane == 0) ok = tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1u, abort);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    const CUtensorMap* map = is_v ? tv : tk;
+    if (C::SHARED) {
+      // A page that does not exist is read as page 0 (the result is without meaning).
+      if (lane == 0) tc::mbar_arrive_expect_tx(full, C::kChunks * 128 * rows);
+      __syncwarp();
+      if (lane < rows / box) {
+        const int at = (j * kBK + lane * box) & (page - 1);
+        for (int c = 0; c < C::kChunks; ++c)
+          tc::tma_load_4d(dst + c * C::kChunk + lane * box * 128, map, full, 64 * c, at, u.hk,
+                          max(id, 0));
+      }
+    } else if (lane == 0) {
+      tc::mbar_arrive_expect_tx(full, C::kTileBytes);
+      for (int c = 0; c < C::kChunks; ++c)
+        tc::tma_load_3d(dst + c * C::kChunk, map, full, 64 * c, u.hk, u.kbase + j * kBK);
+    }
+    ++loaded;
+    if (is_v && j == u.jhi && last_keys < kBK) {
+      ok = tc::mbar_wait(full, phase, abort);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      for (int e = lane; e < (kBK - last_keys) * 8 * C::kChunks; e += 32) {
+        const int c = e / ((kBK - last_keys) * 8), r = e % ((kBK - last_keys) * 8);
+        *reinterpret_cast<uint4*>(dst + c * C::kChunk + last_keys * 128 + r * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->v_fixed);
+    }
+    if (++stage == C::NS) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    return true;
+  };
+  bool ok = true;
+  for (int e = 0; ok && e < u.la && u.jlo + e <= u.jhi; ++e) ok = load(false, u.jlo + e);
+  for (int j = u.jlo; ok && j <= u.jhi; ++j) {
+    ok = load(true, j);
+    if (ok && j + u.la <= u.jhi) ok = load(false, j + u.la);
+  }
+  // Every copy this block started lands before the block may exit.
+  if (lane == 0) {
+    drain_wait(&bars->q_full, 0);
+    for (uint32_t s = 0; s < C::NS && s < loaded; ++s) {
+      const uint32_t fill = (loaded - 1 - s) / C::NS;   // the last load into stage s
+      drain_wait(&bars->kv_full[s], fill & 1);
+    }
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------- products (one thread)
+template <class C>
+__device__ void products(const Args& a, const Unit& u, uint32_t tmem, uint8_t* sq, uint8_t* skv,
+                         Bars* bars) {
+  volatile int* abort = &bars->abort;
+  constexpr uint32_t id_s = tc::idesc_f16(kRows, kBK, C::BF16, false);
+  constexpr uint32_t id_o = tc::idesc_f16(kRows, C::DP, C::BF16, true);
+  const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sq), 16, 1024);
+  const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(skv), 16, 1024);
+  // V [keys][dims], dims contiguous: the next 64 dims are a chunk away, the next 8 keys 1024 bytes
+  const uint64_t vd = tc::sdesc_sw128(tc::smem_u32(skv), C::kChunk, 1024);
+  const int ksteps = (a.D + 15) / 16;
+  int stage = 0;
+  uint32_t phase = 0;
+  uint32_t done[2] = {0, 0};                   // blocks of each tile so far
+  auto take = [&](int& st) -> bool {
+    if (!tc::mbar_wait(&bars->kv_full[stage], phase, abort)) return false;
+    st = stage;
+    if (++stage == C::NS) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    return true;
+  };
+  auto scores = [&](int t, int st) {
+    const uint64_t q = qd + ((u.la == 2 ? 0 : t) * C::kTileBytes >> 4);
+    const uint64_t k = kd + (st * C::kTileBytes >> 4);
+    for (int s = 0; s < ksteps; ++s) {
+      const uint32_t off = ((s >> 2) * C::kChunk + (s & 3) * 32) >> 4;
+      tc::mma_f16_ss(tmem + C::kSCol + t * kBK, q + off, k + off, id_s, s > 0);
+    }
+    tc::mma_commit(&bars->s_full[t]);
+  };
+  auto run = [&]() -> bool {
+    if (!tc::mbar_wait(&bars->q_full, 0, abort)) return false;
+    tc::fence_after_sync();
+    for (int e = 0; e < u.la && u.jlo + e <= u.jhi; ++e) {
+      int st = 0;
+      if (!take(st)) return false;
+      tc::fence_after_sync();
+      for (int t = 0; t < 2; ++t)
+        if (active(a, u, t, u.jlo + e, C::SHARED)) scores(t, st);
+      tc::mma_commit(&bars->kv_empty[st]);
+    }
+    for (int j = u.jlo; j <= u.jhi; ++j) {
+      int vs = 0, ks = -1;
+      if (!take(vs)) return false;
+      if (j == u.jhi && u.nk - j * kBK < kBK && !tc::mbar_wait(&bars->v_fixed, 0, abort))
+        return false;
+      const bool next = j + u.la <= u.jhi;
+      for (int t = 0; t < 2; ++t) {
+        if (active(a, u, t, j, C::SHARED)) {
+          for (int h = 0; h < 2; ++h) {
+            if (!tc::mbar_wait(&bars->p_ready[t][h], done[t] & 1, abort)) return false;
+            tc::fence_after_sync();
+            for (int s = 4 * h; s < 4 * h + 4; ++s)
+              tc::mma_f16_ts(tmem + C::kOCol + t * C::DP, tmem + C::kSCol + t * kBK + 8 * s,
+                             vd + ((vs * C::kTileBytes + s * 2048) >> 4), id_o,
+                             (done[t] > 0 || s > 0) ? 1u : 0u);
+            if (h == 0) tc::mma_commit(&bars->o_half[t]);
+          }
+          tc::mma_commit(&bars->o_done[t]);
+          ++done[t];
+        }
+        if (next && active(a, u, t, j + u.la, C::SHARED)) {
+          if (ks < 0 && !take(ks)) return false;
+          tc::fence_after_sync();
+          scores(t, ks);
+        }
+      }
+      tc::mma_commit(&bars->kv_empty[vs]);
+      if (next) {
+        if (ks < 0 && !take(ks)) return false;
+        tc::mma_commit(&bars->kv_empty[ks]);
+      }
+    }
+    return true;
+  };
+  run();
+  tc::mma_commit(&bars->drain);                // nothing may still run when the block frees its TMEM
+  drain_wait(&bars->drain, 0);
+}
+
+// ---------------------------------------------------------------- softmax (4 warps a tile)
+template <class C>
+__device__ void softmax(const Args& a, const Unit& u, uint32_t tmem, Bars* bars, int t, int quarter,
+                        int lane) {
+  using T = typename C::T;
+  volatile int* abort = &bars->abort;
+  const int row = quarter * 32 + lane, tok = row / a.G, head = u.hk * a.G + row % a.G;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const int tile = C::SHARED && u.la == 2 ? 0 : t;
+  const int local = tile * a.TQ + tok;         // token of the unit
+  const bool live = tok < a.TQ && local < u.ntok;
+  const int qpos = u.q0 + local;
+  const float cs = a.softcap_on ? 1.0f : a.c_score;
+  constexpr float kLimit = C::BF16 ? 256.0f : 32768.0f;   // 2^(8 + kBias)
+  float m_ref = -INFINITY, l = 0.f;            // P = 2^(score - m_ref) with the bias inside m_ref
+  uint32_t n = 0;                              // blocks so far
+  bool ok = true;
+  for (int j = u.jlo; j <= u.jhi; ++j) {
+    if (!active(a, u, t, j, C::SHARED)) continue;
+    ok = tc::mbar_wait(&bars->s_full[t], n & 1, abort);
+    if (__any_sync(0xffffffffu, !ok)) {        // leave together: tcgen05.ld is warp-wide
+      ok = false;
+      break;
+    }
+    tc::fence_after_sync();
+    const uint32_t scol = lane_base + C::kSCol + t * kBK;
+    const int k0 = j * kBK;
+    const int hi = (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;        // visible: c <= hi
+    const int lo = !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : -1;   // and c >= lo
+    const bool edge = __any_sync(0xffffffffu, hi < kBK - 1 || lo > 0);
+#pragma unroll 1
+    for (int hh = 0; hh < 2; ++hh) {
+      float s[64];
+      uint32_t p[32];
+      float lsum = 0.f;
+      const bool fast = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
+#pragma unroll 1
+      for (int pass = fast ? 0 : 1; pass < 2; ++pass) {
+        tc::tmem_ld64(scol + 64 * hh, s);
+        if (a.softcap_on) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float e = tc::ex2(s[c] * a.c_cap_in);
+            s[c] = fmaf(-2.0f * a.c_cap_out, tc::rcp(e + 1.0f), a.c_cap_out);
+          }
+        }
+        if (edge) {
+          const int h2 = hi - 64 * hh, l2 = lo - 64 * hh;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c > h2 || c < l2 ? -INFINITY : s[c];
+        }
+        if (pass == 1) {
+          const float m_new = fmaxf(m_ref, fmaf(prefill::tq_max<64>(s), cs, -C::kBias));
+          const bool grow = m_ref != -INFINITY && m_new - m_ref > kRescaleLog2;
+          if (__any_sync(0xffffffffu, grow)) {
+            // once every product that wrote O is done
+            if (hh == 0 ? n > 0 : true)
+              ok = hh == 0 ? tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort)
+                           : tc::mbar_wait(&bars->o_half[t], n & 1, abort);
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const float f = grow ? tc::ex2(m_ref - m_new) : 1.0f;
+            if (n > 0 || hh > 0) {
+#pragma unroll 1
+              for (int c = 0; c < C::DP; c += 32) {
+                float o[32];
+                tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tc::tmem_st32(lane_base + C::kOCol + t * C::DP + c, o);
+              }
+            }
+            if (grow) {
+              l *= f;
+              m_ref = m_new;
+            }
+          }
+          if (m_ref == -INFINITY) m_ref = m_new;
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t c2 = tc::pack2(cs, cs), m2 = tc::pack2(-m_use, -m_use);
+        uint64_t acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = tc::pack2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float x0, x1;
+          tc::unpack2(tc::fma2(tc::pack2(s[c], s[c + 1]), c2, m2), x0, x1);
+          x0 = tc::ex2(x0);
+          x1 = tc::ex2(x1);
+          p[c / 2] = Pair<T>::pack(x0, x1);
+          acc[(c / 2) % 4] = tc::add2(acc[(c / 2) % 4], tc::pack2(x0, x1));
+        }
+        float a0, a1;
+        tc::unpack2(tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3])), a0, a1);
+        lsum = a0 + a1;
+        if (pass == 1 || !__any_sync(0xffffffffu, live && !(lsum <= kLimit))) break;
+      }
+      if (!ok) break;
+      l += lsum;
+      tc::tmem_st32(scol + 32 * hh, reinterpret_cast<const float*>(p));
+      tc::fence_before_sync();
+      tc::mbar_arrive(&bars->p_ready[t][hh]);
+    }
+    if (!ok) break;
+    ++n;
+  }
+  if (!ok) return;
+
+  if (n > 0) {
+    ok = tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort);
+    if (__any_sync(0xffffffffu, !ok || *abort)) return;
+    tc::fence_after_sync();
+  }
+  const bool any = n > 0 && m_ref != -INFINITY;
+  const float inv = any ? 1.0f / l : 0.f;
+  if constexpr (C::SHARED) {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.H;
+    const int part = u.la == 2 ? 2 * u.part + t : u.part;
+    if (u.la == 1 && t >= u.nt) return;
+    const int64_t at = part * rows + static_cast<int64_t>(u.row0 + local) * a.H + head;
+    if (live) a.part_ml[at] = make_float2(any ? m_ref : -INFINITY, any ? l : 0.f);
+#pragma unroll 1
+    for (int c = 0; c < C::DP; c += 32) {
+      float o[32];
+      if (n > 0) tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
+      float* dst = a.part_o + at * a.D + c;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        if (live && c + e < a.D)
+          *reinterpret_cast<float4*>(dst + e) =
+              any ? make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  } else {
+    if (t >= u.nt) return;
+    T* dst = static_cast<T*>(a.out) + (u.row0 + local) * a.o_token + head * a.o_head;
+#pragma unroll 1
+    for (int c = 0; c < C::DP; c += 32) {
+      float o[32];
+      tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        if (live && c + e < a.D) {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = o[e + i] * inv;
+          *reinterpret_cast<uint4*>(dst + c + e) = pack8<T>(x);
+        }
+    }
+  }
+}
+
+// The block's unit; false where it has none. Whole warp.
+template <class C>
+__device__ bool find_unit(const Args& a, unsigned x, Unit& u) {
+  u.hk = x % a.Hkv;
+  const int y = x / a.Hkv, tokens = 2 * a.TQ;
+  if (C::SHARED) {
+    const int pair = y / a.splits, blocks = (a.prefix_len + kBK - 1) / kBK;
+    u.part = y % a.splits;
+    u.row0 = pair * tokens;
+    u.q0 = 0;
+    u.ntok = min(tokens, a.B - u.row0);
+    u.kbase = 0;
+    u.nk = a.prefix_len;
+    u.jlo = static_cast<int>(static_cast<int64_t>(u.part) * blocks / a.splits);
+    u.jhi = static_cast<int>(static_cast<int64_t>(u.part + 1) * blocks / a.splits) - 1;
+    u.nt = u.ntok > a.TQ ? 2 : 1;
+    u.la = a.split_keys ? 2 : 1;
+    return true;
+  }
+  // Sequence b's tiles begin at slot cu[b] / tokens + b: never more than the next one's.
+  // Later slots first: the last tokens of a prompt have the most keys.
+  const int slot = a.units - 1 - y;
+  const int b = warp_find_last(a.B, slot, [&](int i) {
+    return static_cast<int64_t>(max(a.cu[i], 0) / tokens) + i;
+  });
+  if (b < 0) return false;
+  const SeqRows s = seq_rows(a.cu, b, a.T);
+  if (s.n < 0 || s.n > a.max_len) {
+    if (threadIdx.x % 32 == 0) report(a.status, ATTN_DEV_LENGTH);
+    return false;
+  }
+  u.q0 = (slot - (s.first / tokens + b)) * tokens;
+  if (u.q0 >= s.n) return false;
+  u.ntok = min(tokens, s.n - u.q0);
+  u.row0 = s.first + u.q0;
+  u.kbase = s.first;
+  u.nk = s.n;
+  u.nt = u.ntok > a.TQ ? 2 : 1;
+  u.la = 1;
+  u.part = 0;
+  u.jlo = a.window > 0 ? max(0, u.q0 - a.window + 1) / kBK : 0;
+  u.jhi = (u.q0 + u.ntok - 1) / kBK;
+  return true;
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  if (gated_off(a.skip)) return;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* skv = sq + 2 * C::kTileBytes;
+  Bars* bars = reinterpret_cast<Bars*>(skv + C::NS * C::kTileBytes);
+  static_assert(sizeof(Bars) <= 1024, "barriers fit behind the ring");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == 9) {
+    tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (warp == 8) {
+    Unit u{};
+    const bool any = find_unit<C>(a, blockIdx.x, u);
+    if (lane == 0) {
+      if (!any) u.nt = 0;
+      bars->unit = u;
+    }
+  }
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->q_full, 1);
+    for (int s = 0; s < C::NS; ++s) {
+      tc::mbar_init(&bars->kv_full[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(&bars->s_full[t], 1);
+      tc::mbar_init(&bars->p_ready[t][0], 128);
+      tc::mbar_init(&bars->p_ready[t][1], 128);
+      tc::mbar_init(&bars->o_half[t], 1);
+      tc::mbar_init(&bars->o_done[t], 1);
+    }
+    tc::mbar_init(&bars->v_fixed, 1);
+    tc::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    tc::fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  const Unit u = bars->unit;
+  if (u.nt > 0) {
+    if (warp == 8) {
+      producer<C>(a, u, &tm_q, &tm_k, &tm_v, sq, skv, bars, lane);
+    } else if (warp == 9) {
+      if (lane == 0) products<C>(a, u, tmem, sq, skv, bars);
+      __syncwarp();
+    } else {
+      softmax<C>(a, u, tmem, bars, warp / 4, warp % 4, lane);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && bars->abort) report(a.status, ATTN_DEV_TIMEOUT);
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- launch
+// [tokens, heads, D] rows: boxes of 64 dims x box_heads x box_tokens.
+inline bool map_rows(CUtensorMap* m, const RowsArg& r, bool bf16, int D, int heads, int T,
+                     int box_heads, int box_tokens) {
+  auto enc = prefill::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(r.head) * 2,
+                                 static_cast<cuuint64_t>(r.token) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, r.p,
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A pool [pages, Hkv, page, D]: boxes of 64 dims x min(page, 128) slots.
+inline bool map_pool(CUtensorMap* m, void* p, bool bf16, int D, int Hkv, const PagedKv& c) {
+  auto enc = prefill::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t page = 1ull << c.page_shift;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), page, static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, page * D * 2,
+                                 static_cast<cuuint64_t>(c.page_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page < kBK ? page : kBK), 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, p,
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
+  static PerContext<cudaError_t> attr;
+  const cudaError_t e = attr.get(
+      [] {
+        return cudaFuncSetAttribute(attn16_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::kSmem);
+      },
+      cudaErrorInvalidDevice, [](cudaError_t r) { return r == cudaSuccess; });
+  if (e != cudaSuccess) return e;
+  Args a{};
+  a.T = j.T; a.B = j.B; a.max_len = j.max_len; a.cu = j.cu;
+  a.prefix_table = j.prefix_table; a.prefix_len = j.prefix_len;
+  a.pages = j.cache.pages; a.page_shift = j.cache.page_shift;
+  a.H = j.H; a.Hkv = j.Hkv; a.D = j.D; a.G = j.H / j.Hkv; a.TQ = kRows / a.G;
+  a.window = j.window;
+  a.softcap_on = j.softcap > 0.f;
+  a.c_score = j.scale * kLog2e16;
+  a.c_cap_in = j.softcap > 0.f ? 2.0f * kLog2e16 * j.scale / j.softcap : 0.f;
+  a.c_cap_out = kLog2e16 * j.softcap;
+  a.out = j.out.p; a.o_token = j.out.token; a.o_head = j.out.head;
+  a.part_o = j.part_o; a.part_ml = j.part_ml;
+  a.status = j.status; a.skip = j.skip;
+  const int tokens = 2 * a.TQ;
+  unsigned grid;
+  CUtensorMap tq, tk, tv;
+  if (C::SHARED) {
+    a.split_keys = a.B <= a.TQ;
+    a.splits = shared_prefix_splits(a.B, a.H, a.Hkv, a.prefix_len) / (a.split_keys ? 2 : 1);
+    a.units = (a.B + tokens - 1) / tokens;
+    grid = static_cast<unsigned>(a.Hkv) * a.units * a.splits;
+    if (!map_rows(&tq, j.q, j.bf16, a.D, a.H, a.B, a.G, a.TQ) ||
+        !map_pool(&tk, j.cache.k, j.bf16, a.D, a.Hkv, j.cache) ||
+        !map_pool(&tv, j.cache.v, j.bf16, a.D, a.Hkv, j.cache))
+      return cudaErrorInvalidValue;
+  } else {
+    a.units = a.T / tokens + a.B;
+    grid = static_cast<unsigned>(a.Hkv) * a.units;
+    if (!map_rows(&tq, j.q, j.bf16, a.D, a.H, a.T, a.G, a.TQ) ||
+        !map_rows(&tk, j.k, j.bf16, a.D, a.Hkv, a.T, 1, kBK) ||
+        !map_rows(&tv, j.v, j.bf16, a.D, a.Hkv, a.T, 1, kBK))
+      return cudaErrorInvalidValue;
+  }
+  attn16_kernel<C><<<grid, kThreads, C::kSmem, stream>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_type(const Attn16Job& j, cudaStream_t stream) {
+  if (j.cu)
+    return j.D <= 64 ? launch<Cfg<T, 64, false>>(j, stream) : launch<Cfg<T, 128, false>>(j, stream);
+  return j.D <= 64 ? launch<Cfg<T, 64, true>>(j, stream) : launch<Cfg<T, 128, true>>(j, stream);
+}
+
+}  // namespace attn16
+}  // namespace gqa

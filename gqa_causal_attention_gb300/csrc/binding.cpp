@@ -1,5 +1,5 @@
-// Native marshalling for the per-token calls of the 4-bit cache: checks torch tensors and
-// hands their pointers to the C ABI. A decode step runs for a few microseconds; the same
+// Native marshalling for the calls of the 4-bit cache and of 16-bit paged serving: checks torch
+// tensors and hands their pointers to the C ABI. A decode step runs for a few microseconds; the same
 // checks written in Python took about as long again.
 //
 // Every function takes its arguments by position and returns the call's ATTN_* code, or
@@ -24,6 +24,10 @@ decltype(&gqa_attn_decode_q4) c_decode;
 decltype(&gqa_attn_decode_step_q4) c_step;
 decltype(&kv_cache_evict_q4) c_evict;
 decltype(&kv_q4_record_bytes) c_record;
+decltype(&kv_cache_append_paged) c_append_paged;
+decltype(&gqa_attn_decode_paged) c_decode_paged;
+decltype(&gqa_attn_decode_shared) c_decode_shared;
+decltype(&gqa_attn_prefill_packed) c_prefill_packed;
 
 // Raised inside a call; the Python error is set.
 struct Raise {};
@@ -293,14 +297,173 @@ PyObject* evict(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// Addresses of the C entry points: append, read, decode, step, evict, record bytes.
+// ---------------------------------------------------------------- 16-bit paged serving
+
+// A call's 16-bit tensors: one type, last dim contiguous, on the call's device.
+struct Args16 {
+  Args& a;
+  at::ScalarType type = at::ScalarType::Undefined;
+
+  const at::Tensor* tensor(int i, int dims, bool optional = false) {
+    PyObject* o = a.v[i];
+    if (o == Py_None) {
+      if (optional) return nullptr;
+      fail(PyExc_TypeError, a.fn, "a required tensor is None");
+    }
+    if (!THPVariable_Check(o)) fail(PyExc_TypeError, a.fn, "expected a tensor");
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (type == at::ScalarType::Undefined) type = t.scalar_type();
+    if ((type != at::kHalf && type != at::kBFloat16) || t.scalar_type() != type)
+      fail(PyExc_TypeError, a.fn, "expected torch.float16 or torch.bfloat16, one type for all");
+    if (!t.is_cuda()) fail(PyExc_ValueError, a.fn, "expected CUDA tensors");
+    if (a.device < 0) a.device = c10::cuda::current_device();
+    if (t.get_device() != a.device)
+      fail(PyExc_ValueError, a.fn, "tensors must lie on the current CUDA device");
+    a.check(t.dim() == dims, "a tensor has the wrong number of dims");
+    a.sizes(&t);
+    a.check(t.size(dims - 1) <= 1 || t.stride(dims - 1) == 1, "the last dim must be contiguous");
+    return &t;
+  }
+  int code() const { return type == at::kHalf ? ATTN_TYPE_FP16 : ATTN_TYPE_BF16; }
+};
+
+attn_rows rows16(const at::Tensor* t) {
+  if (!t) return attn_rows{nullptr, 0, 0};
+  return attn_rows{t->data_ptr(), t->stride(0), t->stride(1)};
+}
+
+// Pools [pages, Hkv, page, D]: pages apart as they like, contiguous within, k like v.
+attn_paged_kv pools16(Args& a, const at::Tensor* k, const at::Tensor* v, int64_t D) {
+  a.check(v->sizes() == k->sizes() && k->size(3) == D, "inconsistent shapes");
+  for (const at::Tensor* t : {k, v}) {
+    const int64_t page = k->size(2);
+    a.check((page <= 1 || t->stride(2) == D) && (k->size(1) <= 1 || t->stride(1) == page * D),
+            "a page of the cache must be contiguous");
+  }
+  a.check(k->size(0) <= 1 || k->stride(0) == v->stride(0), "k_cache and v_cache: one page stride");
+  return attn_paged_kv{k->data_ptr(), v->data_ptr(), k->stride(0),
+                       static_cast<int32_t>(k->size(0)), static_cast<int32_t>(k->size(2))};
+}
+
+const at::Tensor* table16(Args& a, int i, int64_t B) {
+  const at::Tensor* t = a.i32(i);
+  a.check(t->dim() == 2 && t->size(0) == B, "block_table must be [B, pages of a row]");
+  a.sizes(t);
+  return t;
+}
+
+// k, v, k_cache, v_cache, block_table, start, max_pos, params, table, k_norm_w, eps,
+// cu_seqlens, q, q_out, q_norm_w, k_out, status, stream
+PyObject* append_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run("kv_cache_append_paged", args, n, 18, [](Args& a) {
+    Args16 x{a};
+    const at::Tensor *k = x.tensor(0, 3), *v = x.tensor(1, 3), *kc = x.tensor(2, 4),
+                     *vc = x.tensor(3, 4), *start = a.i32(5);
+    attn_rope_params rp;
+    const bool rope = a.rope(7, &rp);
+    const at::Tensor *table = a.f32(8, true), *kn = a.f32(9, true), *cu = a.i32(11, true),
+                     *q = x.tensor(12, 3, true), *qo = x.tensor(13, 3, true),
+                     *qn = a.f32(14, true), *ko = x.tensor(15, 3, true), *status = a.i32(16, true);
+    const int64_t T = k->size(0), Hkv = k->size(1), D = k->size(2), B = start->numel();
+    const int64_t H = q ? q->size(1) : Hkv;
+    a.check(v->sizes() == k->sizes() && (!ko || ko->sizes() == k->sizes()) && kc->size(1) == Hkv &&
+                (!q || (q->size(0) == T && q->size(2) == D)) && (!q == !qo) &&
+                (!q || qo->sizes() == q->sizes()),
+            "inconsistent shapes");
+    a.check(!cu || cu->numel() == B + 1, "cu_seqlens holds one value more than start");
+    const at::Tensor* bt = table16(a, 4, B);
+    a.status(status);
+    a.table(rope ? &rp : nullptr, table, D);
+    a.norm(qn, D);
+    a.norm(kn, D);
+    const attn_rows rq = rows16(q), rqo = rows16(qo), rk = rows16(k), rko = rows16(ko),
+                    rv = rows16(v);
+    const attn_paged_kv cache = pools16(a, kc, vc, D);
+    return c_append_paged(x.code(), &rq, &rqo, &rk, &rko, &rv, T, B, H, Hkv, D, ptr<int32_t>(cu),
+                          ptr<int32_t>(start), a.whole(6), rope ? &rp : nullptr, ptr<float>(table),
+                          ptr<float>(qn), ptr<float>(kn), a.real(10), &cache, ptr<int32_t>(bt),
+                          bt->size(1), ptr<int32_t>(status), a.stream(17));
+  });
+}
+
+// q, k_cache, v_cache, block_table, cache_len, max_cache_len, out, window, softcap, scale,
+// workspace, status, stream
+PyObject* decode_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run("gqa_attn_decode_paged", args, n, 13, [](Args& a) {
+    Args16 x{a};
+    const at::Tensor *q = x.tensor(0, 3), *kc = x.tensor(1, 4), *vc = x.tensor(2, 4),
+                     *len = a.i32(4), *out = x.tensor(6, 3), *status = a.i32(11, true);
+    const int64_t B = q->size(0), H = q->size(1), D = q->size(2), Hkv = kc->size(1);
+    a.check(out->sizes() == q->sizes(), "inconsistent shapes");
+    const at::Tensor* bt = table16(a, 3, B);
+    a.rows(len, B);
+    a.status(status);
+    const attn_rows rq = rows16(q), ro = rows16(out);
+    const attn_paged_kv cache = pools16(a, kc, vc, D);
+    void* ws;
+    size_t bytes;
+    workspace(a, 10, &ws, &bytes);
+    return c_decode_paged(x.code(), &rq, &cache, ptr<int32_t>(bt), bt->size(1), ptr<int32_t>(len),
+                          a.whole(5), &ro, B, H, Hkv, D, a.whole(7), a.real(8), a.real(9), ws,
+                          bytes, ptr<int32_t>(status), a.stream(12));
+  });
+}
+
+// q, k_cache, v_cache, prefix_table, prefix_len, block_table, cache_len, max_cache_len, out,
+// softcap, scale, workspace, status, stream
+PyObject* decode_shared(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run("gqa_attn_decode_shared", args, n, 14, [](Args& a) {
+    Args16 x{a};
+    const at::Tensor *q = x.tensor(0, 3), *kc = x.tensor(1, 4), *vc = x.tensor(2, 4),
+                     *pt = a.i32(3), *len = a.i32(6), *out = x.tensor(8, 3),
+                     *status = a.i32(12, true);
+    const int64_t B = q->size(0), H = q->size(1), D = q->size(2), Hkv = kc->size(1);
+    a.check(out->sizes() == q->sizes() && pt->dim() == 1, "inconsistent shapes");
+    a.sizes(pt);
+    const at::Tensor* bt = table16(a, 5, B);
+    a.rows(len, B);
+    a.status(status);
+    const attn_rows rq = rows16(q), ro = rows16(out);
+    const attn_paged_kv cache = pools16(a, kc, vc, D);
+    void* ws;
+    size_t bytes;
+    workspace(a, 11, &ws, &bytes);
+    return c_decode_shared(x.code(), &rq, &cache, ptr<int32_t>(pt), pt->size(0), a.whole(4),
+                           ptr<int32_t>(bt), bt->size(1), ptr<int32_t>(len), a.whole(7), &ro, B, H,
+                           Hkv, D, a.real(9), a.real(10), ws, bytes, ptr<int32_t>(status),
+                           a.stream(13));
+  });
+}
+
+// q, k, v, cu_seqlens, max_len, out, window, softcap, scale, status, stream
+PyObject* prefill_packed(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run("gqa_attn_prefill_packed", args, n, 11, [](Args& a) {
+    Args16 x{a};
+    const at::Tensor *q = x.tensor(0, 3), *k = x.tensor(1, 3), *v = x.tensor(2, 3), *cu = a.i32(3),
+                     *out = x.tensor(5, 3), *status = a.i32(9, true);
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2), Hkv = k->size(1);
+    a.check(k->size(0) == T && k->size(2) == D && v->sizes() == k->sizes() &&
+                out->sizes() == q->sizes(),
+            "inconsistent shapes");
+    a.check(cu->numel() >= 1 && cu->numel() <= INT32_MAX, "cu_seqlens must hold B + 1 values");
+    a.status(status);
+    const attn_rows rq = rows16(q), rk = rows16(k), rv = rows16(v), ro = rows16(out);
+    return c_prefill_packed(x.code(), &rq, &rk, &rv, ptr<int32_t>(cu), a.whole(4), &ro, T,
+                            cu->numel() - 1, H, Hkv, D, a.whole(6), a.real(7), a.real(8),
+                            ptr<int32_t>(status), a.stream(10));
+  });
+}
+
+// Addresses of the C entry points: append, read, decode, step, evict, record bytes; paged
+// append, paged decode, shared decode, packed prefill.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* p[6];
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind: expected 6 addresses");
+  constexpr int kCalls = 10;
+  void* p[kCalls];
+  if (n != kCalls) {
+    PyErr_SetString(PyExc_TypeError, "bind: wrong number of addresses");
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < kCalls; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null address");
@@ -313,13 +476,20 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   c_step = reinterpret_cast<decltype(c_step)>(p[3]);
   c_evict = reinterpret_cast<decltype(c_evict)>(p[4]);
   c_record = reinterpret_cast<decltype(c_record)>(p[5]);
+  c_append_paged = reinterpret_cast<decltype(c_append_paged)>(p[6]);
+  c_decode_paged = reinterpret_cast<decltype(c_decode_paged)>(p[7]);
+  c_decode_shared = reinterpret_cast<decltype(c_decode_shared)>(p[8]);
+  c_prefill_packed = reinterpret_cast<decltype(c_prefill_packed)>(p[9]);
   Py_RETURN_NONE;
 }
 
-#define Q4_METHOD(name) \
+#define NATIVE_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {Q4_METHOD(append), Q4_METHOD(read),  Q4_METHOD(decode), Q4_METHOD(step),
-                         Q4_METHOD(evict),  Q4_METHOD(bind),  {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {NATIVE_METHOD(append), NATIVE_METHOD(read),  NATIVE_METHOD(decode), NATIVE_METHOD(step),
+                         NATIVE_METHOD(evict),  NATIVE_METHOD(bind),
+                         NATIVE_METHOD(append_paged), NATIVE_METHOD(decode_paged),
+                         NATIVE_METHOD(decode_shared), NATIVE_METHOD(prefill_packed),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gqa_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -113,7 +113,64 @@ __global__ void __launch_bounds__(256) finite_check_kernel(FiniteJob j) {
   if (threadIdx.x == 0 && bad_block) report(j.status, ATTN_DEV_NONFINITE);
 }
 
+__device__ __forceinline__ bool not_finite16(uint32_t x, uint32_t exp) {
+  return (x & exp) == exp || (x & exp << 16) == exp << 16;   // either half an inf or a NaN
+}
+
+// 16-bit rows and pages (a warp per head row, its lanes 16 bytes each).
+__global__ void __launch_bounds__(256) finite16_kernel(Finite16Job j) {
+  __shared__ int bad_block;
+  if (threadIdx.x == 0) bad_block = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const long nwarps = static_cast<long>(gridDim.x) * 8;
+  const long gwarp = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32;
+  const uint32_t exp = j.bf16 ? 0x7f80u : 0x7c00u;
+  bool bad = false;
+  auto row = [&](const void* p, int64_t at) {
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    for (int c = lane; c < j.D / 8; c += 32) {
+      const uint4 v = r[c];
+      bad |= not_finite16(v.x, exp) | not_finite16(v.y, exp) | not_finite16(v.z, exp) |
+             not_finite16(v.w, exp);
+    }
+  };
+  for (int ri = 0; ri < 3; ++ri) {
+    const RowsArg& r = j.rows[ri];
+    if (!r.p) continue;
+    const long lo = j.cu ? max(j.cu[0], 0) : 0, hi = j.cu ? min(j.cu[j.B], j.T) : j.T;
+    for (long x = gwarp; x < (hi - lo) * j.heads[ri]; x += nwarps)
+      row(r.p, (lo + x / j.heads[ri]) * r.token + x % j.heads[ri] * r.head);
+  }
+  for (int pi = 0; pi < 2; ++pi) {
+    const Finite16Pages& g = j.pages[pi];
+    for (int b = 0; b < g.B; ++b) {
+      const int len = g.len ? g.len[b] : g.fixed_len;
+      if (len < 0 || len > g.max_len) continue;
+      const int lo = g.window > 0 ? max(0, len - g.window) : 0;
+      for (long x = gwarp; x < static_cast<long>(len - lo) * j.Hkv; x += nwarps) {
+        const int pos = lo + static_cast<int>(x / j.Hkv), h = static_cast<int>(x % j.Hkv);
+        const int id = g.table[static_cast<int64_t>(b) * g.width + (pos >> j.cache.page_shift)];
+        if (id < 0 || id >= j.cache.pages) continue;
+        const int64_t at = id * j.cache.page_stride +
+                           ((static_cast<int64_t>(h) << j.cache.page_shift) +
+                            (pos & ((1 << j.cache.page_shift) - 1))) * j.D;
+        row(j.cache.k, at);
+        row(j.cache.v, at);
+      }
+    }
+  }
+  if (bad) bad_block = 1;
+  __syncthreads();
+  if (threadIdx.x == 0 && bad_block) report(j.status, ATTN_DEV_NONFINITE);
+}
+
 }  // namespace
+
+cudaError_t launch_finite16_check(const Finite16Job& j, cudaStream_t stream) {
+  finite16_kernel<<<152 * 4, 256, 0, stream>>>(j);
+  return cudaGetLastError();
+}
 
 int check_finite_enabled() {
   int v = g_check.load();

@@ -436,5 +436,109 @@ cudaError_t launch_decode_q4(const DecodeQ4Job& j, const StepQ4Args& step, cudaS
 cudaError_t launch_decode_q4_narrow(const DecodeQ4Job& j, const StepQ4Args& step, cudaStream_t stream);
 cudaError_t launch_decode_q4_wide(const DecodeQ4Job& j, const StepQ4Args& step, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 16-bit paged serving
+// Token-major rows of heads: x[t * token + h * head + d], strides in elements.
+struct RowsArg {
+  void* p = nullptr;
+  int64_t token = 0, head = 0;
+};
+// A paged cache: pools [pages, Hkv, 1 << page_shift, D], page_stride elements between pages.
+struct PagedKv {
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int pages, page_shift;
+};
+
+struct AppendPagedJob {
+  bool bf16;
+  RowsArg q, q_out, k, k_out, v;   // q.p == nullptr: keys and values only; k_out.p may be nullptr
+  int T, B, H, Hkv, D, R;          // R: rotary dims (table != nullptr)
+  const int32_t* cu;               // [B + 1], or nullptr: row t is the one token of sequence t
+  const int32_t* start;            // [B]
+  int max_pos;
+  const float2* table;             // nullptr: no rotation, no norm
+  const float* q_norm_w;
+  const float* k_norm_w;
+  float norm_eps;
+  PagedKv cache;
+  const int32_t* block_table;      // [B, width]
+  int width;
+  int32_t* status;
+  const int32_t* skip;
+};
+cudaError_t launch_append_paged(const AppendPagedJob& j, cudaStream_t stream);
+
+// The opt-in non-finite check of the 16-bit calls: up to three sets of rows (of the sequences
+// alone, with cu) and the live slots of up to two sets of pages.
+struct Finite16Pages {
+  const int32_t* table = nullptr;
+  const int32_t* len = nullptr;    // [B], or nullptr: fixed_len for the one row
+  int width = 0, B = 0, fixed_len = 0, max_len = 0, window = 0;
+};
+struct Finite16Job {
+  bool bf16;
+  int D, Hkv, T, B;
+  const int32_t* cu;
+  RowsArg rows[3];
+  int heads[3];
+  PagedKv cache;
+  Finite16Pages pages[2];
+  int32_t* status;
+};
+cudaError_t launch_finite16_check(const Finite16Job& j, cudaStream_t stream);
+
+// Partial results over a shared prefix: nsplit x [B * H] rows, each o / sum (fp32 [D]) with
+// (reference, sum) of its weights 2^(score - reference).
+struct PrefixParts {
+  const float* o = nullptr;
+  const float2* ml = nullptr;
+  int nsplit = 0;
+};
+
+struct DecodePagedJob {
+  bool bf16;
+  RowsArg q, out;
+  PagedKv cache;
+  const int32_t* block_table;
+  int width;
+  const int32_t* cache_len;        // [B]
+  int max_len;
+  int B, H, Hkv, D;
+  int window;
+  float softcap, scale;
+  PrefixParts prefix;
+  float* partial;                  // workspace
+  int blocks;                      // 0: one block per row and head group
+  int32_t* status;
+  const int32_t* skip;
+};
+// The blocks a call runs (0: one per row and head group) and the workspace it takes.
+int decode_paged_blocks(int B, int H, int Hkv, int max_len, int window);
+size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window);
+cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream);
+
+// Attention on the tensor cores in 16 bits: packed prompts (cu != nullptr), or B rows of one
+// token each over a shared prefix, whose partial results go to part_o, part_ml.
+struct Attn16Job {
+  bool bf16;
+  RowsArg q, k, v, out;            // k, v: packed prompts
+  PagedKv cache;                   // shared prefix
+  const int32_t* prefix_table;
+  int prefix_len;
+  const int32_t* cu;
+  int T, B, max_len;
+  int H, Hkv, D;
+  int window;
+  float softcap, scale;
+  float* part_o;
+  float2* part_ml;
+  int32_t* status;
+  const int32_t* skip;
+};
+// Splits of a shared prefix (the partial results per row).
+int shared_prefix_splits(int B, int H, int Hkv, int prefix_len);
+cudaError_t launch_attn16_bf16(const Attn16Job& j, cudaStream_t stream);
+cudaError_t launch_attn16_fp16(const Attn16Job& j, cudaStream_t stream);
 
 }  // namespace gqa

@@ -1,0 +1,98 @@
+// 16-bit tensors and the paged KV cache: what their kernels share.
+//
+// Rows of heads are token-major, x[token * token_stride + head * head_stride + d] (elements);
+// the pools are [pages, Hkv, page, D] with a stride of their own between pages. Position p of
+// row b lies in slot p % page of pool page block_table[b][p / page].
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gqa {
+
+constexpr float kLog2e16 = 1.4426950408889634f;
+
+template <class T>
+struct Rows {
+  T* p;
+  int64_t token, head;      // strides in elements
+  __device__ __forceinline__ T* at(int64_t t, int h) const { return p + t * token + h * head; }
+};
+template <class T>
+__host__ __device__ __forceinline__ Rows<T> rows_as(const RowsArg& r) {
+  return {static_cast<T*>(r.p), r.token, r.head};
+}
+
+// The eight 16-bit values of a 16-byte granule as floats, and back (rounded to nearest even).
+__device__ __forceinline__ float2 two(__nv_bfloat162 x) { return __bfloat1622float2(x); }
+__device__ __forceinline__ float2 two(__half2 x) { return __half22float2(x); }
+template <class T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+template <>
+struct Pair<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+template <class T>
+__device__ __forceinline__ float2 unpack(uint32_t x) {
+  return two(*reinterpret_cast<const typename Pair<T>::type*>(&x));
+}
+template <class T>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack<T>(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <class T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]),
+                    Pair<T>::pack(x[4], x[5]), Pair<T>::pack(x[6], x[7]));
+}
+
+// The largest b in [0, n) with key(b) <= x for nondecreasing keys (-1: none), found by the whole
+// warp, 32 keys at a time: two rounds of loads for up to 1024 keys.
+template <class F>
+__device__ __forceinline__ int warp_find_last(int n, int64_t x, F key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && key(lo + i) <= x;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    if (c == 0) return -1;                   // only ever in the first round
+    lo += (c - 1) * step;
+    if (step == 1) return lo;
+    n = min(step, n - (c - 1) * step);
+  }
+  return -1;
+}
+
+// Sequence b's rows [first, first + n) of T packed rows; n < 0 where cu_seqlens breaks a rule.
+struct SeqRows {
+  int first, n;
+};
+__device__ __forceinline__ SeqRows seq_rows(const int32_t* cu, int b, int T) {
+  const int a = cu[b], e = cu[b + 1];
+  return {a, a < 0 || e < a || e > T ? -1 : e - a};
+}
+
+}  // namespace gqa

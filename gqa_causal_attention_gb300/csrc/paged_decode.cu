@@ -1,0 +1,573 @@
+// Single-token attention over a paged 16-bit cache ("mojolearn.transformer", step; "Core Layers
+// -- Deep Reference", "MHA and GQA"):
+//
+//   out[b,h] = sum_n w_n v_n / sum_n w_n,   w_n = 2^(c cap(q . k_n) - m),   n in [max(0, len - W), len)
+//
+// one pass over keys and values with a running reference m, sums in fp32.
+//
+// * Memory bound: every key and value is read once for the (up to 8) query heads of a unit, 4 D
+//   bytes and 4 G D flops a position. Keys and values go from global memory straight into the
+//   operands of m16n8k16 products: a lane's 16-byte loads are made the operand's layout by
+//   taking the head dims (the products' inner or outer index) in an order of their own, and
+//   pairs of value rows by one byte permutation a register. No shared memory, no transposition.
+//     scores S[head, key] = Q K^T      A = 8 heads of Q (rows 8..15 zero), B = 16 bytes a key
+//     O[dim, head] += V^T P^T          A = value pairs, B = P as the scores' layout leaves it
+// * P is split in two 16-bit parts, so its rounding (2^-9 in bf16) does not add to the
+//   output's: a second product on a pipe that is a fifth used.
+// * The tiles (16 positions) of all rows and heads, counted from the lengths on the device, are
+//   dealt out to the blocks in equal shares, whatever the lengths; a block's share is one run
+//   of tiles, so at most its first and last unit are shared with other blocks and merged by a
+//   second kernel. Where units are many or short, one block does each unit and nothing is merged.
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace gqa {
+
+namespace {
+
+constexpr int kTile = 16;                     // positions per warp step (never across pages)
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSms = 152;
+constexpr int kResident = 2;                  // blocks per SM
+constexpr int kHeads = 8;                     // query heads of a unit
+constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
+constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps (8 bytes each)
+
+struct DecodeArgs {
+  const void* q;
+  void* out;
+  int64_t q_token, q_head, o_token, o_head;
+  const void* k;
+  const void* v;
+  int64_t page_stride, head_stride;
+  int pages, page_shift;
+  const int32_t* block_table;
+  int64_t width;
+  const int32_t* cache_len;
+  int max_len, B, H, Hkv, D, G, HT;           // HT: units per kv head
+  int window, softcap_on;
+  float c_score, c_cap_in, c_cap_out;         // log2 units
+  PrefixParts prefix;
+  float* part_o;                              // [blocks][2][8][D]
+  float2* part_ml;                            // [blocks][2][8]
+  int blocks;
+  int32_t* status;
+  const int32_t* skip;
+};
+
+// Row b's live positions [lo, n) and its tiles; n < 0 where the length breaks a rule.
+struct Span {
+  int lo, n, t0, nt;
+};
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
+  const int n = a.cache_len[b];
+  if (n < 0 || n > a.max_len) return {0, -1, 0, 0};
+  const int lo = a.window > 0 ? max(0, n - a.window) : 0;
+  return {lo, n, lo / kTile, n > 0 ? (n - 1) / kTile + 1 - lo / kTile : 0};
+}
+
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                        uint32_t a2, uint32_t a3, uint32_t b0,
+                                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                 uint32_t a2, uint32_t a3, uint32_t b0,
+                                                 uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Streamed once: 16 bytes past L1.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+template <int DP>
+struct __align__(16) Merge {                  // one block's warps, then its result
+  float m[kWarps][kHeads], l[kWarps][kHeads];
+  float o[kWarps][kHeads][DP + 4];
+};
+
+// What a merge writes: the unit's output row of head h, dims d .. d + 3 of o with total weight l.
+template <class T>
+__device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int head, int d, float4 o) {
+  T* p = static_cast<T*>(a.out) + b * a.o_token + head * a.o_head + d;
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(Pair<T>::pack(o.x, o.y), Pair<T>::pack(o.z, o.w));
+}
+
+// The row's own result (o / l, reference m, weight l) joined with its prefix parts.
+template <class T>
+__device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int head, int d, float4 o,
+                                           float m, float l) {
+  if (a.prefix.nsplit == 0) {
+    store_out<T>(a, b, head, d, o);
+    return;
+  }
+  const int64_t rows = static_cast<int64_t>(a.B) * a.H, row = static_cast<int64_t>(b) * a.H + head;
+  float top = m;
+  for (int s = 0; s < a.prefix.nsplit; ++s) top = fmaxf(top, a.prefix.ml[s * rows + row].x);
+  float f = l > 0.f ? tc::ex2(m - top) * l : 0.f, sum = f;
+  float4 y = make_float4(f * o.x, f * o.y, f * o.z, f * o.w);
+  for (int s = 0; s < a.prefix.nsplit; ++s) {
+    const float2 ml = a.prefix.ml[s * rows + row];
+    f = ml.y > 0.f ? tc::ex2(ml.x - top) * ml.y : 0.f;
+    const float4 p = *reinterpret_cast<const float4*>(a.prefix.o + (s * rows + row) * a.D + d);
+    sum += f;
+    y.x = fmaf(f, p.x, y.x); y.y = fmaf(f, p.y, y.y);
+    y.z = fmaf(f, p.z, y.z); y.w = fmaf(f, p.w, y.w);
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  store_out<T>(a, b, head, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+}
+
+// Tiles [t0, t1) of row b's span for kv head hk, query heads [h0, h0 + nh): the block's result
+// goes to the output when whole, else to partial slot `slot` of this block.
+template <class T, int DP>
+__device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h0, int nh,
+                        const Span& sp, int t0, int t1, int slot) {
+  constexpr int KC = DP / 32, VH = DP / 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const T* kbase = static_cast<const T*>(a.k) + hk * a.head_stride;
+  const T* vbase = static_cast<const T*>(a.v) + hk * a.head_stride;
+  const int32_t* table = a.block_table + b * a.width;
+  const int page_mask = (1 << a.page_shift) - 1;
+
+  uint4 qf[KC];
+#pragma unroll
+  for (int c = 0; c < KC; ++c) {
+    const int d = 32 * c + 8 * t;
+    qf[c] = g < nh && d < a.D
+                ? *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.q_token +
+                                                  (h0 + g) * a.q_head + d)
+                : make_uint4(0, 0, 0, 0);
+  }
+  float o[VH][4][4];
+#pragma unroll
+  for (int h = 0; h < VH; ++h)
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[h][m][e] = 0.f;
+  float m_ref = -INFINITY, l = 0.f;           // of head g (l: this lane's keys)
+
+  int ids = -1, ids_at = -1;                  // page of the warp's tile ids_at + 8 * lane
+  uint4 kf[2][KC], vf[VH][4];
+  int64_t off = -1;                           // of the tile whose loads are on their way
+  auto locate = [&](int tile) {               // element offset of the tile's first slot, < 0: none
+    if (ids_at < 0 || tile >= ids_at + 32 * kWarps) {
+      ids_at = tile;
+      const int mine = tile + kWarps * lane;
+      ids = mine < t1 ? table[(static_cast<int64_t>(sp.t0 + mine) * kTile) >> a.page_shift] : 0;
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, (tile - ids_at) / kWarps);
+    if (id < 0 || id >= a.pages) {
+      if (lane == 0) report(a.status, ATTN_DEV_PAGE);
+      off = -1;
+      return;
+    }
+    off = id * a.page_stride + static_cast<int64_t>(((sp.t0 + tile) * kTile) & page_mask) * a.D;
+  };
+  auto load_k = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const int d = 32 * c + 8 * t;
+        kf[i][c] = off >= 0 && d < a.D ? ld_stream(kbase + off + (8 * i + g) * a.D + d)
+                                       : make_uint4(0, 0, 0, 0);
+      }
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int h = 0; h < VH; ++h)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 64 * h + 8 * g, key = 2 * t + (r & 1) + 8 * (r >> 1);
+        vf[h][r] = off >= 0 && d < a.D ? ld_stream(vbase + off + key * a.D + d)
+                                       : make_uint4(0, 0, 0, 0);
+      }
+  };
+
+  int tile = t0 + warp;
+  if (tile < t1) {
+    locate(tile);
+    load_k();
+    load_v();
+  }
+  for (; tile < t1; tile += kWarps) {
+    const bool there = off >= 0;
+    float s[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        mma16816<T>(s[i], qf[c].x, 0u, qf[c].y, 0u, kf[i][c].x, kf[i][c].y);
+        mma16816<T>(s[i], qf[c].z, 0u, qf[c].w, 0u, kf[i][c].z, kf[i][c].w);
+      }
+    }
+    const bool more = tile + kWarps < t1;
+    if (more) {
+      locate(tile + kWarps);
+      load_k();
+    }
+    // scores of head g, keys k0 + {0, 1, 8, 9}
+    float x[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
+    const int k0 = (sp.t0 + tile) * kTile + 2 * t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (a.softcap_on) {
+        const float u = tc::ex2(x[e] * a.c_cap_in);
+        x[e] = fmaf(-2.0f * a.c_cap_out, tc::rcp(u + 1.0f), a.c_cap_out);
+      } else {
+        x[e] *= a.c_score;
+      }
+    }
+    const int tile0 = (sp.t0 + tile) * kTile;
+    if (tile0 < sp.lo || tile0 > sp.n - kTile || !there) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = k0 + (e & 1) + 8 * (e >> 1);
+        if (key < sp.lo || key >= sp.n || !there) {
+          x[e] = -INFINITY;
+          // an unused slot may hold anything, which a weight of 0 would still pass on
+#pragma unroll
+          for (int h = 0; h < VH; ++h) vf[h][e] = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    const float mine = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    const float ref = m_ref == -INFINITY ? -INFINITY : m_ref + kGrow;
+    if (__any_sync(0xffffffffu, mine > ref)) {
+      float top = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float m_new = top > ref ? fmaxf(top, m_ref) : m_ref;
+      const float f = m_new == -INFINITY ? 1.0f : tc::ex2(m_ref - m_new);
+      m_ref = m_new;
+      l *= f;
+      const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+      for (int h = 0; h < VH; ++h)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          o[h][m][0] *= f0; o[h][m][1] *= f1;
+          o[h][m][2] *= f0; o[h][m][3] *= f1;
+        }
+    }
+    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+    float p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      p[e] = tc::ex2(x[e] - m_use);
+      l += p[e];
+    }
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = Pair<T>::pack(p[2 * i], p[2 * i + 1]);
+      const float2 r = unpack<T>(hi[i]);
+      lo[i] = Pair<T>::pack(p[2 * i] - r.x, p[2 * i + 1] - r.y);
+    }
+#pragma unroll
+    for (int h = 0; h < VH; ++h) {
+      const uint32_t* v0 = &vf[h][0].x;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t sel = m & 1 ? 0x7632u : 0x5410u;
+        const int w = m / 2;
+        (void)v0;
+        auto word = [&](int r, int i) {
+          const uint4& q4 = vf[h][r];
+          return i == 0 ? q4.x : i == 1 ? q4.y : i == 2 ? q4.z : q4.w;
+        };
+        const uint32_t a0 = __byte_perm(word(0, w), word(1, w), sel);
+        const uint32_t a1 = __byte_perm(word(0, 2 + w), word(1, 2 + w), sel);
+        const uint32_t a2 = __byte_perm(word(2, w), word(3, w), sel);
+        const uint32_t a3 = __byte_perm(word(2, 2 + w), word(3, 2 + w), sel);
+        mma16816<T>(o[h][m], a0, a1, a2, a3, hi[0], hi[1]);
+        mma16816<T>(o[h][m], a0, a1, a2, a3, lo[0], lo[1]);
+      }
+    }
+    if (more) load_v();
+  }
+
+  // The block's warps: weights, then dims.
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  __syncthreads();                            // an earlier segment's sums have been read
+  if (t == 0) {
+    sh->m[warp][g] = m_ref;
+    sh->l[warp][g] = l;
+  }
+#pragma unroll
+  for (int h = 0; h < VH; ++h)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int d = 64 * h + 8 * g + m;
+      sh->o[warp][2 * t][d] = o[h][m][0];
+      sh->o[warp][2 * t + 1][d] = o[h][m][1];
+      sh->o[warp][2 * t][d + 4] = o[h][m][2];
+      sh->o[warp][2 * t + 1][d + 4] = o[h][m][3];
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < kHeads * DP / 4; e += kThreads) {
+    const int h = e / (DP / 4), d = 4 * (e % (DP / 4));
+    if (h >= nh || d >= a.D) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][h]);
+    float sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sh->m[w][h] == -INFINITY ? 0.f : tc::ex2(sh->m[w][h] - top);
+      const float4 p = *reinterpret_cast<const float4*>(&sh->o[w][h][d]);
+      sum = fmaf(f, sh->l[w][h], sum);
+      y.x = fmaf(f, p.x, y.x); y.y = fmaf(f, p.y, y.y);
+      y.z = fmaf(f, p.z, y.z); y.w = fmaf(f, p.w, y.w);
+    }
+    const float inv = top == -INFINITY ? 0.f : 1.0f / sum;
+    y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    if (slot < 0) {
+      finish_row<T>(a, b, h0 + h, d, y, top, sum);
+    } else {
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kHeads + h;
+      *reinterpret_cast<float4*>(a.part_o + at * a.D + d) = y;
+      if (d == 0) a.part_ml[at] = make_float2(top, sum);
+    }
+  }
+}
+
+// A row without positions of its own: zeros, or its prefix alone.
+template <class T>
+__device__ void empty_row(const DecodeArgs& a, int b) {
+  const int n4 = a.D / 4;
+  for (int e = threadIdx.x; e < a.H * n4; e += kThreads)
+    finish_row<T>(a, b, e / n4, 4 * (e % n4), make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
+}
+
+// One block per unit (row, kv head, group of up to 8 query heads).
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads, kResident) decode_paged_units_kernel(const DecodeArgs a) {
+  __shared__ Merge<DP> sh;
+  dependent_wait();
+  dependents_may_launch();
+  if (gated_off(a.skip)) return;
+  const int per_row = a.Hkv * a.HT;
+  const int b = blockIdx.x / per_row, u = blockIdx.x % per_row;
+  const Span sp = span_of(a, b);
+  if (sp.n < 0) {
+    if (threadIdx.x == 0) report(a.status, ATTN_DEV_LENGTH);
+    return;
+  }
+  if (sp.nt == 0) {
+    if (u == 0) empty_row<T>(a, b);
+    return;
+  }
+  const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
+  segment<T, DP>(a, &sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, 0, sp.nt, -1);
+}
+
+// prefix[b]: tiles of rows before b; returns their total. Whole block.
+__device__ long long scan_tiles(const DecodeArgs& a, long long* prefix, bool tell) {
+  __shared__ long long warp_sum_of[kWarps];
+  __shared__ long long carry;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) carry = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    long long n = 0;
+    if (b < a.B) {
+      const Span sp = span_of(a, b);
+      if (sp.n < 0 && tell) report(a.status, ATTN_DEV_LENGTH);
+      n = sp.nt;
+    }
+    long long s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    if (lane == 31) warp_sum_of[warp] = s;
+    __syncthreads();
+    long long before = carry;
+    for (int w = 0; w < warp; ++w) before += warp_sum_of[w];
+    if (b < a.B) prefix[b] = before + s - n;
+    __syncthreads();
+    if (threadIdx.x == kThreads - 1) carry = before + s;
+    __syncthreads();
+  }
+  return carry;
+}
+
+__device__ __forceinline__ int row_of(const DecodeArgs& a, const long long* prefix, long long x,
+                                      int per_row) {
+  int lo = 0, hi = a.B - 1;                   // the last row that begins at or before tile x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (prefix[mid] * per_row <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Block i takes tiles [i total / blocks, (i + 1) total / blocks) of the list of all rows' heads' tiles.
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads, kResident) decode_paged_share_kernel(const DecodeArgs a) {
+  __shared__ Merge<DP> sh;
+  extern __shared__ long long prefix[];
+  dependent_wait();
+  dependents_may_launch();
+  if (gated_off(a.skip)) return;
+  const int per_row = a.Hkv * a.HT;
+  const long long total = scan_tiles(a, prefix, blockIdx.x == 0) * per_row;
+  for (int b = blockIdx.x; b < a.B; b += a.blocks)
+    if (span_of(a, b).n == 0) empty_row<T>(a, b);
+  long long x = static_cast<long long>(blockIdx.x) * total / a.blocks;
+  const long long end = static_cast<long long>(blockIdx.x + 1) * total / a.blocks;
+  while (x < end) {
+    const int b = row_of(a, prefix, x, per_row);
+    const Span sp = span_of(a, b);
+    const long long in_row = x - prefix[b] * per_row;
+    const int u = static_cast<int>(in_row / sp.nt), t0 = static_cast<int>(in_row % sp.nt);
+    const int t1 = static_cast<int>(min(static_cast<long long>(sp.nt), t0 + (end - x)));
+    const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
+    // Slot 0: a unit begun by an earlier block (the share's first); slot 1: one begun here and
+    // continued by the next (its last).
+    const int slot = t0 > 0 ? 0 : (t1 < sp.nt ? 1 : -1);
+    segment<T, DP>(a, &sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, t0, t1, slot);
+    x += t1 - t0;
+  }
+}
+
+// Units that several blocks shared, one block each.
+template <class T>
+__global__ void __launch_bounds__(kThreads) decode_paged_merge_kernel(const DecodeArgs a) {
+  extern __shared__ long long prefix[];
+  dependent_wait();
+  dependents_may_launch();
+  if (gated_off(a.skip)) return;
+  const int per_row = a.Hkv * a.HT;
+  const long long total = scan_tiles(a, prefix, false) * per_row;
+  const int b = blockIdx.x / per_row, u = blockIdx.x % per_row;
+  const Span sp = span_of(a, b);
+  if (sp.n <= 0) return;
+  const long long x0 = prefix[b] * per_row + static_cast<long long>(u) * sp.nt;
+  const long long x1 = x0 + sp.nt - 1;
+  const int i0 = static_cast<int>(((x0 + 1) * a.blocks - 1) / total);   // blocks of its first
+  const int i1 = static_cast<int>(((x1 + 1) * a.blocks - 1) / total);   // and last tile
+  if (i0 == i1) return;                       // one block had it whole
+  const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
+  const int nh = min(kHeads, (hk + 1) * a.G - h0), n4 = a.D / 4;
+  for (int e = threadIdx.x; e < nh * n4; e += kThreads) {
+    const int h = e / n4, d = 4 * (e % n4);
+    auto at = [&](int i) { return (static_cast<int64_t>(i) * 2 + (i == i0)) * kHeads + h; };
+    float top = -INFINITY;
+    for (int i = i0; i <= i1; ++i) top = fmaxf(top, a.part_ml[at(i)].x);
+    float sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = i0; i <= i1; ++i) {
+      const float2 ml = a.part_ml[at(i)];
+      const float4 p = *reinterpret_cast<const float4*>(a.part_o + at(i) * a.D + d);
+      const float f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - top) * ml.y;
+      sum += f;
+      y.x = fmaf(f, p.x, y.x); y.y = fmaf(f, p.y, y.y);
+      y.z = fmaf(f, p.z, y.z); y.w = fmaf(f, p.w, y.w);
+    }
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    finish_row<T>(a, b, h0 + h, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv), top, sum);
+  }
+}
+
+template <class T, int DP>
+cudaError_t launch_dp(const DecodeArgs& a, cudaStream_t stream) {
+  const unsigned units = static_cast<unsigned>(a.B) * a.Hkv * a.HT;
+  if (a.blocks == 0)
+    return launch_dependent(decode_paged_units_kernel<T, DP>, units, kThreads, 0, stream, a);
+  const size_t smem = static_cast<size_t>(a.B) * sizeof(long long);
+  static PerContext<cudaError_t> attr;
+  cudaError_t e = attr.get(
+      [] {
+        const int most = kMaxScanRows * sizeof(long long);
+        const cudaError_t r = cudaFuncSetAttribute(decode_paged_share_kernel<T, DP>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        return r != cudaSuccess ? r
+                                : cudaFuncSetAttribute(decode_paged_merge_kernel<T>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      },
+      cudaErrorInvalidDevice, [](cudaError_t r) { return r == cudaSuccess; });
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(decode_paged_share_kernel<T, DP>, a.blocks, kThreads, smem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(decode_paged_merge_kernel<T>, units, kThreads, smem, stream, a);
+}
+
+int eff_len(int max_len, int window) { return window > 0 && window < max_len ? window : max_len; }
+
+}  // namespace
+
+// Blocks that share all tiles, or 0: one per unit, where none of them is long or there are many.
+int decode_paged_blocks(int B, int H, int Hkv, int max_len, int window) {
+  const int G = H / Hkv;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + kHeads - 1) / kHeads);
+  const int64_t tiles = (eff_len(max_len, window) + kTile - 1) / kTile + 1;
+  if (tiles <= 4 * kWarps || B > kMaxScanRows || units == 0) return 0;
+  const int64_t most = kSms * kResident, want = (units * tiles + kWarps - 1) / kWarps;
+  return static_cast<int>(want < most ? want : most);
+}
+
+// part_ml follows part_o; sized for every length up to max_len (more blocks never take less).
+size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window) {
+  const size_t blocks = decode_paged_blocks(B, H, Hkv, max_len, window);
+  return blocks * 2 * kHeads * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
+  DecodeArgs a{};
+  a.q = j.q.p; a.q_token = j.q.token; a.q_head = j.q.head;
+  a.out = j.out.p; a.o_token = j.out.token; a.o_head = j.out.head;
+  a.k = j.cache.k; a.v = j.cache.v;
+  a.page_stride = j.cache.page_stride;
+  a.head_stride = static_cast<int64_t>(j.D) << j.cache.page_shift;
+  a.pages = j.cache.pages; a.page_shift = j.cache.page_shift;
+  a.block_table = j.block_table; a.width = j.width;
+  a.cache_len = j.cache_len; a.max_len = j.max_len;
+  a.B = j.B; a.H = j.H; a.Hkv = j.Hkv; a.D = j.D;
+  a.G = j.H / j.Hkv; a.HT = (a.G + kHeads - 1) / kHeads;
+  a.window = j.window;
+  a.softcap_on = j.softcap > 0.f;
+  a.c_score = j.scale * kLog2e16;
+  a.c_cap_in = j.softcap > 0.f ? 2.0f * kLog2e16 * j.scale / j.softcap : 0.f;
+  a.c_cap_out = kLog2e16 * j.softcap;
+  a.prefix = j.prefix;
+  a.blocks = j.blocks;
+  a.part_o = j.partial;
+  a.part_ml = reinterpret_cast<float2*>(j.partial + static_cast<size_t>(j.blocks) * 2 * kHeads * j.D);
+  a.status = j.status; a.skip = j.skip;
+  if (j.D <= 64)
+    return j.bf16 ? launch_dp<__nv_bfloat16, 64>(a, stream) : launch_dp<__half, 64>(a, stream);
+  return j.bf16 ? launch_dp<__nv_bfloat16, 128>(a, stream) : launch_dp<__half, 128>(a, stream);
+}
+
+}  // namespace gqa

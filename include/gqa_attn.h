@@ -13,8 +13,9 @@
  * Conventions shared by every call
  * --------------------------------
  * - All tensors are fp32, contiguous, row-major, in DEVICE memory owned by the
- *   caller, except the host buffers of gqa_attn_prefill_from_host and the 4-bit
- *   records of the _q4 calls. No call
+ *   caller, except the host buffers of gqa_attn_prefill_from_host, the 4-bit
+ *   records of the _q4 calls and the 16-bit tensors of the _paged, _shared and
+ *   _packed calls (which say their layout themselves). No call
  *   allocates or frees device memory; the only device memory the library keeps
  *   is the fixed scratch array of gqa_attn_decode_static, and the only other
  *   state is the pair of copy streams per device of gqa_attn_prefill_from_host
@@ -67,6 +68,7 @@ extern "C" {
 #define ATTN_DEV_NONFINITE 16  /* the opt-in check found an inf or NaN input; the call
                                   (and every later checked call on this status word)
                                   computed nothing, see attn_set_check_finite */
+#define ATTN_DEV_PAGE      32  /* a block table entry outside [0, pages) was needed */
 
 /* RoPE frequency scaling ("mojolearn.transformer", rope_scaling). */
 #define ATTN_ROPE_SCALING_NONE   0
@@ -630,6 +632,126 @@ int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* ca
                       int32_t max_cache_len, int budget, int recent, void* cache_out,
                       float* weights_out, int32_t* index, int32_t* len_out, int B, int Hkv, int D,
                       int capacity, int capacity_out, int32_t* status, void* stream);
+
+/*
+ * Serving in 16 bits from a paged cache. The four calls below take bf16 or fp16 tensors
+ * (one type for all of a call's), prompts packed one after the other without padding, and
+ * a KV cache in pages that rows of any length share; sums, softmax and rotation are fp32,
+ * and each result is rounded once.
+ *
+ * Rows: queries, keys, values and outputs are [T, heads, D] with strides of their own in
+ * elements, x[t * token_stride + h * head_stride + d], so that they may be slices of one
+ * fused projection, or head-major. Strides are multiples of 8 and at least D (of an axis
+ * of one element they are not read), 16-byte aligned at the start (ATTN_ERR_ALIGN,
+ * ATTN_ERR_SHAPE); an output's rows may not overlap each other (ATTN_ERR_PARAM). Outputs
+ * must not overlap inputs, except where a call says so.
+ * D is a multiple of 8, 16 <= D <= 128; H / Hkv <= 128.
+ */
+#define ATTN_TYPE_FP16 1
+#define ATTN_TYPE_BF16 2
+typedef struct attn_rows {
+    void* p;
+    int64_t token_stride, head_stride;
+} attn_rows;
+
+/*
+ * A paged cache ("dew.nn.backbones.causal_transformer": a cache dense or paged): pools k
+ * and v of `pages` pages, [Hkv, page_size, D] each, page_stride elements from one to the
+ * next (a multiple of 8, at least Hkv * page_size * D). page_size is a power of two from 16
+ * to 1024. Position p of row b lies in slot p % page_size of page
+ *   block_table[b * table_width + p / page_size]        (device int32, [B, table_width]).
+ * Rows may share pages (a common beginning). Entries of pages that a call does not reach
+ * -- behind a row's last position, before its window -- are never read as pages and
+ * may hold anything; so may slots behind a row's last position, NaNs included. An entry
+ * that is needed and lies outside [0, pages) sets ATTN_DEV_PAGE; nothing is read or written
+ * through it, an append skips the token, and an attention's row is without meaning.
+ */
+typedef struct attn_paged_kv {
+    void* k;
+    void* v;
+    int64_t page_stride;
+    int32_t pages, page_size;
+} attn_paged_kv;
+
+/*
+ * Append packed tokens: token i of sequence b, row t = cu_seqlens[b] + i, at position
+ * p = start[b] + i:
+ *   q_out[t,h,:]  <- RoPE_p(RMSNorm(q[t,h,:]))   (norm with q_norm_w; both only if rp)
+ *   y = RoPE_p(RMSNorm(k[t,hkv,:])) -> its slot of the k pool (and k_out[t,hkv,:])
+ *   v[t,hkv,:] -> its slot of the v pool (exact copy)
+ *   q, q_out    NULL (or p NULL): no queries; q_out may be q
+ *   k_out       NULL (or p NULL): not wanted; may be k
+ *   cu_seqlens  device int32 [B + 1], nondecreasing, in [0, T]; rows before the first and
+ *               behind the last sequence are left alone. NULL: T == B, one token each
+ *   start       device int32 [B]: positions already in the cache
+ *   max_pos     host bound on every position written, below max_positions and the
+ *               table's table_width * page_size (ATTN_ERR_POSITION, ATTN_ERR_CAPACITY)
+ *   rp, table, norm weights (fp32) as for kv_cache_append
+ * A sequence with bad bounds (ATTN_DEV_LENGTH) or positions outside [0, max_pos]
+ * (ATTN_DEV_POSITION) is skipped. Two tokens for one slot leave either's.
+ */
+int kv_cache_append_paged(int type, const attn_rows* q, const attn_rows* q_out, const attn_rows* k,
+                          const attn_rows* k_out, const attn_rows* v, int T, int B, int H, int Hkv,
+                          int D, const int32_t* cu_seqlens, const int32_t* start, int32_t max_pos,
+                          const attn_rope_params* rp, const float* table, const float* q_norm_w,
+                          const float* k_norm_w, float norm_eps, const attn_paged_kv* cache,
+                          const int32_t* block_table, int table_width, int32_t* status,
+                          void* stream);
+
+/*
+ * Single-token attention over a paged cache: out[b,h,:] = the softmax of
+ * cap(scale * q[b,h,:] . k_n) over positions n of row b in
+ * [max(0, cache_len[b] - window), cache_len[b]) (window 0: all), applied to v_n. q already
+ * rotated, q and out [B, H, D] rows; scale, softcap as for gqa_attn_decode.
+ *   cache_len   device int32 [B], in [0, max_cache_len]; 0 (a batch place without a
+ *               request) gives +0.0. Outside: ATTN_DEV_LENGTH, the row is left untouched
+ *   max_cache_len  host bound, at most table_width * page_size (ATTN_ERR_CAPACITY)
+ *   workspace   gqa_attn_decode_paged_workspace_size bytes, 16-byte aligned (never
+ *               shrinking as max_cache_len grows; 0, and NULL allowed, where one pass
+ *               finishes). Calls that overlap on the GPU need workspaces of their own
+ * Results do not depend on timing. B * H <= 2^24.
+ */
+size_t gqa_attn_decode_paged_workspace_size(int B, int H, int Hkv, int D, int32_t max_cache_len,
+                                            int window);
+int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cache,
+                          const int32_t* block_table, int table_width, const int32_t* cache_len,
+                          int32_t max_cache_len, const attn_rows* out, int B, int H, int Hkv, int D,
+                          int window, float softcap, float scale, void* workspace,
+                          size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * The same for rows that all begin with one prefix (a system prompt, several samples of one
+ * prompt): row b's positions are the prefix's prefix_len >= 1, in the pages of prefix_table
+ * (device int32 [prefix_width]), then its own cache_len[b] >= 0 in the pages of its block
+ * table (position prefix_len + i of the row is slot i % page_size of entry
+ * i / page_size). The prefix is read once for all rows, as a matrix product. No window.
+ *   workspace   gqa_attn_decode_shared_workspace_size bytes, 16-byte aligned
+ * A cache_len[b] outside [0, max_cache_len] sets ATTN_DEV_LENGTH and the row is left
+ * untouched.
+ */
+size_t gqa_attn_decode_shared_workspace_size(int B, int H, int Hkv, int D, int32_t prefix_len,
+                                             int32_t max_cache_len);
+int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* cache,
+                           const int32_t* prefix_table, int prefix_width, int32_t prefix_len,
+                           const int32_t* block_table, int table_width, const int32_t* cache_len,
+                           int32_t max_cache_len, const attn_rows* out, int B, int H, int Hkv,
+                           int D, float softcap, float scale, void* workspace,
+                           size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Attention of whole prompts, packed: sequence b is rows [cu_seqlens[b], cu_seqlens[b+1])
+ * of q, k, v (rotated) and out, and token i of it sees its own sequence's tokens
+ * [max(0, i - window + 1), i] (window 0: all up to i).
+ *   cu_seqlens  device int32 [B + 1], nondecreasing, in [0, T]; empty sequences are allowed
+ *   max_len     host bound on every length
+ * A sequence with bad bounds or longer than max_len sets ATTN_DEV_LENGTH and is skipped;
+ * rows of no sequence are neither written nor have a part in any result, whatever they
+ * hold. (An inf or NaN in a sequence's own v may reach its earlier rows too.)
+ */
+int gqa_attn_prefill_packed(int type, const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                            const int32_t* cu_seqlens, int32_t max_len, const attn_rows* out, int T,
+                            int B, int H, int Hkv, int D, int window, float softcap, float scale,
+                            int32_t* status, void* stream);
 
 /*
  * gqa_attn_decode without a caller workspace, for callers that cannot
