@@ -18,11 +18,10 @@
 //    MN-major operand of the second product as it lies: no transposition.
 //  * Tensor memory: S0 | S1 (128 fp32 columns each), O0 | O1. P overwrites S's first half in
 //    16 bits and is the A operand of O += P V.
-//  * One thread issues all products, in the order P V (tile 0), next S (tile 0), P V (tile 1),
+//  * One warp issues all products, in the order P V (tile 0), next S (tile 0), P V (tile 1),
 //    next S (tile 1): the tensor pipe runs them in that order, so S may be written over the
 //    P before it without a wait.
-//  * Softmax: a thread per row, 4 warps per tile, S read in halves of 64 columns. The reference is
-//    the row's first maximum and stands until a half's sum shows that some weight exceeded
+//  * Softmax: a thread per row, 4 warps per tile. The reference is the row's first maximum and stands until a half's sum shows that some weight exceeded
 //    2^8 (then the half is redone against a new maximum and O rescaled): no maximum is
 //    taken in the common case.
 //  * Values behind the last key (another sequence's, an unused slot's) are zeroed in shared memory:
@@ -78,362 +77,55 @@ struct Cfg {
   // to 2^-21 of the largest keep all their bits.
   static constexpr float kBias = BF16 ? 0.f : 7.f;
 };
-constexpr int kThreads = 320;                  // 2 x 4 softmax warps, producer, products
+// 2 x 4 softmax warps; producer, products and two idle warps. The block starts with 168
+// registers a thread; a row's 128 scores take more, so the last four warps hand theirs on.
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "the block's registers");
 
 struct Bars {
-  uint64_t q_full;
+  uint4 answer;                                // of the launch control
+  uint64_t answered;
+  uint64_t unit_full[2], unit_empty[2];
+  uint64_t q_full, q_empty;
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2];
   uint64_t p_ready[2][2];                      // [tile][half]
-  uint64_t o_half[2], o_done[2];
+  uint64_t o_half[2], o_done[2], o_free[2];
   uint64_t v_fixed;                            // the last block's V is zeroed behind the last key
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
   struct {
-    int hk, row0, q0, ntok, kbase, nk, jlo, jhi, nt, la, part;
-  } unit;
+    int hk, row0, q0, ntok, kbase, nk, jlo, jhi, nt, la, part;   // nt 0: no more units
+  } unit[2];
 };
-using Unit = decltype(Bars::unit);
+using Unit = std::remove_extent<decltype(Bars::unit)>::type;
 
-// Tile t's key blocks: [lo, hi] in steps of la, from the first that is its own.
-__device__ __forceinline__ bool active(const Args& a, const Unit& u, int t, int j, bool shared) {
-  if (shared) return u.la == 2 ? ((j - u.jlo) & 1) == t : t < u.nt;
-  if (t >= u.nt) return false;
-  const int first = u.q0 + t * a.TQ, last = min(first + a.TQ, u.q0 + u.ntok) - 1;
-  if (j * kBK > last) return false;
-  return !(a.window > 0 && (j + 1) * kBK <= first - a.window + 1);
+// The block's r-th unit, read by a consumer (count of unit_empty: the products' thread and
+// one lane of each softmax warp).
+__device__ __forceinline__ bool next_unit(Bars* bars, uint32_t r, Unit& u) {
+  if (!tc::mbar_wait(&bars->unit_full[r & 1], (r >> 1) & 1, &bars->abort)) return false;
+  u = bars->unit[r & 1];
+  return u.nt > 0;
+}
+
+// Tile t's key blocks [lo, hi] of the unit's (la 2: every other one of them, from jlo + t).
+template <class C>
+__device__ __forceinline__ void tile_blocks(const Args& a, const Unit& u, int t, int& lo, int& hi) {
+  lo = u.jlo;
+  hi = u.jhi;
+  if (u.la == 1 && t >= u.nt) {
+    hi = lo - 1;
+  } else if (!C::SHARED) {
+    const int first = u.q0 + t * a.TQ, last = min(first + a.TQ, u.q0 + u.ntok) - 1;
+    lo = a.window > 0 ? max(0, first - a.window + 1) / kBK : 0;
+    hi = last / kBK;
+  }
 }
 
 // ---------------------------------------------------------------- producer (one warp)
-template <class C>
-__device__ void producer(const Args& a, const Unit& u, const CUtensorMap* tq, const CUtensorMap* tk,
-                         const CUtensorMap* tv, uint8_t* sq, uint8_t* skv, Bars* bars, int lane) {
-  volatile int* abort = &bars->abort;
-  int stage = 0;
-  uint32_t phase = 0, loaded = 0;              // loads so far
-  if (lane == 0) {
-    const int tiles = u.la == 2 ? 1 : u.nt;
-    tc::mbar_arrive_expect_tx(&bars->q_full, tiles * C::kChunks * 128 * a.G * a.TQ);
-    for (int t = 0; t < tiles; ++t)
-      for (int c = 0; c < C::kChunks; ++c)
-        tc::tma_load_3d(sq + t * C::kTileBytes + c * C::kChunk, tq, &bars->q_full, 64 * c,
-                        u.hk * a.G, u.row0 + t * a.TQ);
-  }
-  // The last block holds fewer than 128 keys: its V is zeroed behind them.
-  const int last_keys = u.nk - u.jhi * kBK;
-  auto load = [&](bool is_v, int j) -> bool {
-    bool ok = true;
-    uint64_t* full = &bars->kv_full[stage];
-    uint8_t* dst = skv + stage * C::kTileBytes;
-    int rows = kBK, id = 0;
-    const int page = 1 << a.page_shift, box = min(page, kBK);
-    if (C::SHARED) {
-      // one lane per page of the block
-      const int n = min(kBK, u.nk - j * kBK), boxes = (n + box - 1) / box;
-      if (lane < boxes) {
-        id = a.prefix_table[(static_cast<int64_t>(j) * kBK + lane * box) >> a.page_shift];
-        if (id < 0 || id >= a.pages) {
-          report(a.status, ATTN_DEV_PAGE);
-          id = -1;
-        }
-      }
-      rows = boxes * box;
-    }
-    if (lane == 0) ok = tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1u, abort);
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-    const CUtensorMap* map = is_v ? tv : tk;
-    if (C::SHARED) {
-      // A page that does not exist is read as page 0 (the result is without meaning).
-      if (lane == 0) tc::mbar_arrive_expect_tx(full, C::kChunks * 128 * rows);
-      __syncwarp();
-      if (lane < rows / box) {
-        const int at = (j * kBK + lane * box) & (page - 1);
-        for (int c = 0; c < C::kChunks; ++c)
-          tc::tma_load_4d(dst + c * C::kChunk + lane * box * 128, map, full, 64 * c, at, u.hk,
-                          max(id, 0));
-      }
-    } else if (lane == 0) {
-      tc::mbar_arrive_expect_tx(full, C::kTileBytes);
-      for (int c = 0; c < C::kChunks; ++c)
-        tc::tma_load_3d(dst + c * C::kChunk, map, full, 64 * c, u.hk, u.kbase + j * kBK);
-    }
-    ++loaded;
-    if (is_v && j == u.jhi && last_keys < kBK) {
-      ok = tc::mbar_wait(full, phase, abort);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      for (int e = lane; e < (kBK - last_keys) * 8 * C::kChunks; e += 32) {
-        const int c = e / ((kBK - last_keys) * 8), r = e % ((kBK - last_keys) * 8);
-        *reinterpret_cast<uint4*>(dst + c * C::kChunk + last_keys * 128 + r * 16) =
-            make_uint4(0, 0, 0, 0);
-      }
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->v_fixed);
-    }
-    if (++stage == C::NS) {
-      stage = 0;
-      phase ^= 1u;
-    }
-    return true;
-  };
-  bool ok = true;
-  for (int e = 0; ok && e < u.la && u.jlo + e <= u.jhi; ++e) ok = load(false, u.jlo + e);
-  for (int j = u.jlo; ok && j <= u.jhi; ++j) {
-    ok = load(true, j);
-    if (ok && j + u.la <= u.jhi) ok = load(false, j + u.la);
-  }
-  // Every copy this block started lands before the block may exit.
-  if (lane == 0) {
-    drain_wait(&bars->q_full, 0);
-    for (uint32_t s = 0; s < C::NS && s < loaded; ++s) {
-      const uint32_t fill = (loaded - 1 - s) / C::NS;   // the last load into stage s
-      drain_wait(&bars->kv_full[s], fill & 1);
-    }
-  }
-  __syncwarp();
-}
-
-// ---------------------------------------------------------------- products (one thread)
-template <class C>
-__device__ void products(const Args& a, const Unit& u, uint32_t tmem, uint8_t* sq, uint8_t* skv,
-                         Bars* bars) {
-  volatile int* abort = &bars->abort;
-  constexpr uint32_t id_s = tc::idesc_f16(kRows, kBK, C::BF16, false);
-  constexpr uint32_t id_o = tc::idesc_f16(kRows, C::DP, C::BF16, true);
-  const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sq), 16, 1024);
-  const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(skv), 16, 1024);
-  // V [keys][dims], dims contiguous: the next 64 dims are a chunk away, the next 8 keys 1024 bytes
-  const uint64_t vd = tc::sdesc_sw128(tc::smem_u32(skv), C::kChunk, 1024);
-  const int ksteps = (a.D + 15) / 16;
-  int stage = 0;
-  uint32_t phase = 0;
-  uint32_t done[2] = {0, 0};                   // blocks of each tile so far
-  auto take = [&](int& st) -> bool {
-    if (!tc::mbar_wait(&bars->kv_full[stage], phase, abort)) return false;
-    st = stage;
-    if (++stage == C::NS) {
-      stage = 0;
-      phase ^= 1u;
-    }
-    return true;
-  };
-  auto scores = [&](int t, int st) {
-    const uint64_t q = qd + ((u.la == 2 ? 0 : t) * C::kTileBytes >> 4);
-    const uint64_t k = kd + (st * C::kTileBytes >> 4);
-    for (int s = 0; s < ksteps; ++s) {
-      const uint32_t off = ((s >> 2) * C::kChunk + (s & 3) * 32) >> 4;
-      tc::mma_f16_ss(tmem + C::kSCol + t * kBK, q + off, k + off, id_s, s > 0);
-    }
-    tc::mma_commit(&bars->s_full[t]);
-  };
-  auto run = [&]() -> bool {
-    if (!tc::mbar_wait(&bars->q_full, 0, abort)) return false;
-    tc::fence_after_sync();
-    for (int e = 0; e < u.la && u.jlo + e <= u.jhi; ++e) {
-      int st = 0;
-      if (!take(st)) return false;
-      tc::fence_after_sync();
-      for (int t = 0; t < 2; ++t)
-        if (active(a, u, t, u.jlo + e, C::SHARED)) scores(t, st);
-      tc::mma_commit(&bars->kv_empty[st]);
-    }
-    for (int j = u.jlo; j <= u.jhi; ++j) {
-      int vs = 0, ks = -1;
-      if (!take(vs)) return false;
-      if (j == u.jhi && u.nk - j * kBK < kBK && !tc::mbar_wait(&bars->v_fixed, 0, abort))
-        return false;
-      const bool next = j + u.la <= u.jhi;
-      for (int t = 0; t < 2; ++t) {
-        if (active(a, u, t, j, C::SHARED)) {
-          for (int h = 0; h < 2; ++h) {
-            if (!tc::mbar_wait(&bars->p_ready[t][h], done[t] & 1, abort)) return false;
-            tc::fence_after_sync();
-            for (int s = 4 * h; s < 4 * h + 4; ++s)
-              tc::mma_f16_ts(tmem + C::kOCol + t * C::DP, tmem + C::kSCol + t * kBK + 8 * s,
-                             vd + ((vs * C::kTileBytes + s * 2048) >> 4), id_o,
-                             (done[t] > 0 || s > 0) ? 1u : 0u);
-            if (h == 0) tc::mma_commit(&bars->o_half[t]);
-          }
-          tc::mma_commit(&bars->o_done[t]);
-          ++done[t];
-        }
-        if (next && active(a, u, t, j + u.la, C::SHARED)) {
-          if (ks < 0 && !take(ks)) return false;
-          tc::fence_after_sync();
-          scores(t, ks);
-        }
-      }
-      tc::mma_commit(&bars->kv_empty[vs]);
-      if (next) {
-        if (ks < 0 && !take(ks)) return false;
-        tc::mma_commit(&bars->kv_empty[ks]);
-      }
-    }
-    return true;
-  };
-  run();
-  tc::mma_commit(&bars->drain);                // nothing may still run when the block frees its TMEM
-  drain_wait(&bars->drain, 0);
-}
-
-// ---------------------------------------------------------------- softmax (4 warps a tile)
-template <class C>
-__device__ void softmax(const Args& a, const Unit& u, uint32_t tmem, Bars* bars, int t, int quarter,
-                        int lane) {
-  using T = typename C::T;
-  volatile int* abort = &bars->abort;
-  const int row = quarter * 32 + lane, tok = row / a.G, head = u.hk * a.G + row % a.G;
-  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-  const int tile = C::SHARED && u.la == 2 ? 0 : t;
-  const int local = tile * a.TQ + tok;         // token of the unit
-  const bool live = tok < a.TQ && local < u.ntok;
-  const int qpos = u.q0 + local;
-  const float cs = a.softcap_on ? 1.0f : a.c_score;
-  constexpr float kLimit = C::BF16 ? 256.0f : 32768.0f;   // 2^(8 + kBias)
-  float m_ref = -INFINITY, l = 0.f;            // P = 2^(score - m_ref) with the bias inside m_ref
-  uint32_t n = 0;                              // blocks so far
-  bool ok = true;
-  for (int j = u.jlo; j <= u.jhi; ++j) {
-    if (!active(a, u, t, j, C::SHARED)) continue;
-    ok = tc::mbar_wait(&bars->s_full[t], n & 1, abort);
-    if (__any_sync(0xffffffffu, !ok)) {        // leave together: tcgen05.ld is warp-wide
-      ok = false;
-      break;
-    }
-    tc::fence_after_sync();
-    const uint32_t scol = lane_base + C::kSCol + t * kBK;
-    const int k0 = j * kBK;
-    const int hi = (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;        // visible: c <= hi
-    const int lo = !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : -1;   // and c >= lo
-    const bool edge = __any_sync(0xffffffffu, hi < kBK - 1 || lo > 0);
-#pragma unroll 1
-    for (int hh = 0; hh < 2; ++hh) {
-      float s[64];
-      uint32_t p[32];
-      float lsum = 0.f;
-      const bool fast = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
-#pragma unroll 1
-      for (int pass = fast ? 0 : 1; pass < 2; ++pass) {
-        tc::tmem_ld64(scol + 64 * hh, s);
-        if (a.softcap_on) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const float e = tc::ex2(s[c] * a.c_cap_in);
-            s[c] = fmaf(-2.0f * a.c_cap_out, tc::rcp(e + 1.0f), a.c_cap_out);
-          }
-        }
-        if (edge) {
-          const int h2 = hi - 64 * hh, l2 = lo - 64 * hh;
-#pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = c > h2 || c < l2 ? -INFINITY : s[c];
-        }
-        if (pass == 1) {
-          const float m_new = fmaxf(m_ref, fmaf(prefill::tq_max<64>(s), cs, -C::kBias));
-          const bool grow = m_ref != -INFINITY && m_new - m_ref > kRescaleLog2;
-          if (__any_sync(0xffffffffu, grow)) {
-            // once every product that wrote O is done
-            if (hh == 0 ? n > 0 : true)
-              ok = hh == 0 ? tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort)
-                           : tc::mbar_wait(&bars->o_half[t], n & 1, abort);
-            if (__any_sync(0xffffffffu, !ok)) {
-              ok = false;
-              break;
-            }
-            tc::fence_after_sync();
-            const float f = grow ? tc::ex2(m_ref - m_new) : 1.0f;
-            if (n > 0 || hh > 0) {
-#pragma unroll 1
-              for (int c = 0; c < C::DP; c += 32) {
-                float o[32];
-                tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tc::tmem_st32(lane_base + C::kOCol + t * C::DP + c, o);
-              }
-            }
-            if (grow) {
-              l *= f;
-              m_ref = m_new;
-            }
-          }
-          if (m_ref == -INFINITY) m_ref = m_new;
-        }
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t c2 = tc::pack2(cs, cs), m2 = tc::pack2(-m_use, -m_use);
-        uint64_t acc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = tc::pack2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float x0, x1;
-          tc::unpack2(tc::fma2(tc::pack2(s[c], s[c + 1]), c2, m2), x0, x1);
-          x0 = tc::ex2(x0);
-          x1 = tc::ex2(x1);
-          p[c / 2] = Pair<T>::pack(x0, x1);
-          acc[(c / 2) % 4] = tc::add2(acc[(c / 2) % 4], tc::pack2(x0, x1));
-        }
-        float a0, a1;
-        tc::unpack2(tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3])), a0, a1);
-        lsum = a0 + a1;
-        if (pass == 1 || !__any_sync(0xffffffffu, live && !(lsum <= kLimit))) break;
-      }
-      if (!ok) break;
-      l += lsum;
-      tc::tmem_st32(scol + 32 * hh, reinterpret_cast<const float*>(p));
-      tc::fence_before_sync();
-      tc::mbar_arrive(&bars->p_ready[t][hh]);
-    }
-    if (!ok) break;
-    ++n;
-  }
-  if (!ok) return;
-
-  if (n > 0) {
-    ok = tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort);
-    if (__any_sync(0xffffffffu, !ok || *abort)) return;
-    tc::fence_after_sync();
-  }
-  const bool any = n > 0 && m_ref != -INFINITY;
-  const float inv = any ? 1.0f / l : 0.f;
-  if constexpr (C::SHARED) {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.H;
-    const int part = u.la == 2 ? 2 * u.part + t : u.part;
-    if (u.la == 1 && t >= u.nt) return;
-    const int64_t at = part * rows + static_cast<int64_t>(u.row0 + local) * a.H + head;
-    if (live) a.part_ml[at] = make_float2(any ? m_ref : -INFINITY, any ? l : 0.f);
-#pragma unroll 1
-    for (int c = 0; c < C::DP; c += 32) {
-      float o[32];
-      if (n > 0) tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
-      float* dst = a.part_o + at * a.D + c;
-#pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        if (live && c + e < a.D)
-          *reinterpret_cast<float4*>(dst + e) =
-              any ? make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  } else {
-    if (t >= u.nt) return;
-    T* dst = static_cast<T*>(a.out) + (u.row0 + local) * a.o_token + head * a.o_head;
-#pragma unroll 1
-    for (int c = 0; c < C::DP; c += 32) {
-      float o[32];
-      tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
-#pragma unroll
-      for (int e = 0; e < 32; e += 8)
-        if (live && c + e < a.D) {
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = o[e + i] * inv;
-          *reinterpret_cast<uint4*>(dst + c + e) = pack8<T>(x);
-        }
-    }
-  }
-}
-
-// The block's unit; false where it has none. Whole warp.
+// Unit x of the grid; false where it is empty. Whole warp.
 template <class C>
 __device__ bool find_unit(const Args& a, unsigned x, Unit& u) {
   u.hk = x % a.Hkv;
@@ -478,10 +170,417 @@ __device__ bool find_unit(const Args& a, unsigned x, Unit& u) {
   return true;
 }
 
+// Finds the block's units, its own and then any that no block has begun (cancelled launches),
+// publishes each and loads it. The next one's search and loads run while the products are still
+// at this one's.
+template <class C>
+__device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                         const CUtensorMap* tv, uint8_t* sq, uint8_t* skv, Bars* bars, int lane) {
+  volatile int* abort = &bars->abort;
+  int stage = 0;
+  uint32_t phase = 0, loaded = 0;              // loads so far
+  uint32_t units = 0, asked = 0;
+  Unit u{};
+  // The last block of a sequence may hold fewer than 128 keys: its V is zeroed behind them.
+  auto load = [&](bool is_v, int j) -> bool {
+    bool ok = true;
+    uint64_t* full = &bars->kv_full[stage];
+    uint8_t* dst = skv + stage * C::kTileBytes;
+    int rows = kBK, id = 0;
+    const int page = 1 << a.page_shift, box = min(page, kBK);
+    if (C::SHARED) {
+      // one lane per page of the block
+      const int n = min(kBK, u.nk - j * kBK), boxes = (n + box - 1) / box;
+      if (lane < boxes) {
+        id = a.prefix_table[(static_cast<int64_t>(j) * kBK + lane * box) >> a.page_shift];
+        if (id < 0 || id >= a.pages) {
+          report(a.status, ATTN_DEV_PAGE);
+          id = -1;
+        }
+      }
+      rows = boxes * box;
+    }
+    if (lane == 0) ok = tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1u, abort);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    const CUtensorMap* map = is_v ? tv : tk;
+    if (C::SHARED) {
+      // A page that does not exist is read as page 0 (the result is without meaning).
+      if (lane == 0) tc::mbar_arrive_expect_tx(full, C::kChunks * 128 * rows);
+      __syncwarp();
+      if (lane < rows / box) {
+        const int at = (j * kBK + lane * box) & (page - 1);
+        for (int c = 0; c < C::kChunks; ++c)
+          tc::tma_load_4d(dst + c * C::kChunk + lane * box * 128, map, full, 64 * c, at, u.hk,
+                          max(id, 0));
+      }
+    } else if (lane == 0) {
+      tc::mbar_arrive_expect_tx(full, C::kTileBytes);
+      for (int c = 0; c < C::kChunks; ++c)
+        tc::tma_load_3d(dst + c * C::kChunk, map, full, 64 * c, u.hk, u.kbase + j * kBK);
+    }
+    ++loaded;
+    const int last_keys = u.nk - j * kBK;
+    if (is_v && last_keys < kBK) {
+      ok = tc::mbar_wait(full, phase, abort);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      for (int e = lane; e < (kBK - last_keys) * 8 * C::kChunks; e += 32) {
+        const int c = e / ((kBK - last_keys) * 8), r = e % ((kBK - last_keys) * 8);
+        *reinterpret_cast<uint4*>(dst + c * C::kChunk + last_keys * 128 + r * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->v_fixed);
+    }
+    if (++stage == C::NS) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    return true;
+  };
+  auto publish = [&]() -> bool {               // u, as the units-th
+    bool ok = true;
+    if (lane == 0) {
+      ok = tc::mbar_wait(&bars->unit_empty[units & 1], ((units >> 1) & 1) ^ 1u, abort);
+      if (ok) {
+        bars->unit[units & 1] = u;
+        tc::mbar_arrive(&bars->unit_full[units & 1]);
+      }
+    }
+    return __shfl_sync(0xffffffffu, ok, 0);
+  };
+  bool ok = true, answer_due = false;
+  int x = blockIdx.x;
+  while (ok) {
+    if (lane == 0) {                           // the next unit, asked for ahead
+      tc::fence_proxy_async();
+      tc::mbar_arrive_expect_tx(&bars->answered, 16);
+      tc::clc_request(&bars->answer, &bars->answered);
+    }
+    answer_due = true;
+    if (find_unit<C>(a, x, u)) {
+      if (!(ok = publish())) break;
+      const int tiles = u.la == 2 ? 1 : u.nt;
+      if (lane == 0) {
+        ok = tc::mbar_wait(&bars->q_empty, (units & 1) ^ 1u, abort);
+        if (ok) {
+          tc::mbar_arrive_expect_tx(&bars->q_full, tiles * C::kChunks * 128 * a.G * a.TQ);
+          for (int t = 0; t < tiles; ++t)
+            for (int c = 0; c < C::kChunks; ++c)
+              tc::tma_load_3d(sq + t * C::kTileBytes + c * C::kChunk, tq, &bars->q_full, 64 * c,
+                              u.hk * a.G, u.row0 + t * a.TQ);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      ++units;
+      for (int e = 0; ok && e < u.la && u.jlo + e <= u.jhi; ++e) ok = load(false, u.jlo + e);
+      for (int j = u.jlo; ok && j <= u.jhi; ++j) {
+        ok = load(true, j);
+        if (ok && j + u.la <= u.jhi) ok = load(false, j + u.la);
+      }
+      if (!ok) break;
+    }
+    ok = tc::mbar_wait(&bars->answered, asked & 1, abort);
+    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+    ++asked;
+    answer_due = false;
+    x = tc::clc_answer(&bars->answer);
+    __syncwarp();
+    if (x < 0) {
+      u.nt = 0;
+      publish();
+      break;
+    }
+  }
+  // Every copy this block started lands before the block may exit.
+  if (lane == 0) {
+    if (answer_due) drain_wait(&bars->answered, asked & 1);
+    if (units > 0) drain_wait(&bars->q_full, (units - 1) & 1);
+    for (uint32_t s = 0; s < C::NS && s < loaded; ++s) {
+      const uint32_t fill = (loaded - 1 - s) / C::NS;   // the last load into stage s
+      drain_wait(&bars->kv_full[s], fill & 1);
+    }
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------- products (one warp, one lane issues)
+// The tensor pipe takes a product every 64 cycles, so the warp that issues them has to be lean: it
+// stays converged with every operand the same in all lanes (uniform registers), its loops over
+// a block's products are unrolled, and where a wait runs out it goes on (on data that is then
+// without meaning, all of it this block's) to the block's end, where the warp leaves together.
+template <class C>
+__device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv, Bars* bars) {
+  volatile int* abort = &bars->abort;
+  constexpr uint32_t id_s = tc::idesc_f16(kRows, kBK, C::BF16, false);
+  constexpr uint32_t id_o = tc::idesc_f16(kRows, C::DP, C::BF16, true);
+  const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sq), 16, 1024);
+  const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(skv), 16, 1024);
+  // V [keys][dims], dims contiguous: the next 64 dims are a chunk away, the next 8 keys 1024 bytes
+  const uint64_t vd = tc::sdesc_sw128(tc::smem_u32(skv), C::kChunk, 1024);
+  uint32_t stage = 0, phase = 0, fixed = 0;
+  uint32_t done[2] = {0, 0}, outputs[2] = {0, 0};   // blocks, and units, of each tile so far
+  bool bad = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { bad |= !tc::mbar_wait(bar, parity, abort); };
+  auto take = [&]() -> uint32_t {
+    wait(&bars->kv_full[stage], phase);
+    const uint32_t st = stage;
+    if (++stage == C::NS) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    return st;
+  };
+  for (uint32_t r = 0;; ++r) {
+    Unit u;
+    if (!__all_sync(0xffffffffu, next_unit(bars, r, u))) break;
+    if (threadIdx.x % 32 == 0) tc::mbar_arrive(&bars->unit_empty[r & 1]);
+    const int la = __shfl_sync(0xffffffffu, u.la, 0), nk = __shfl_sync(0xffffffffu, u.nk, 0);
+    const int jlo = __shfl_sync(0xffffffffu, u.jlo, 0), jhi = __shfl_sync(0xffffffffu, u.jhi, 0);
+    int lo[2], hi[2];                          // each tile's blocks
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      int l = 0, h = 0;
+      tile_blocks<C>(a, u, t, l, h);
+      lo[t] = __shfl_sync(0xffffffffu, l, 0);
+      hi[t] = __shfl_sync(0xffffffffu, h, 0);
+    }
+    auto active = [&](int t, int j) { return j >= lo[t] && j <= hi[t] && (la == 1 || ((j - jlo) & 1) == t); };
+    auto scores = [&](int t, uint32_t st) {
+      const uint64_t q = qd + ((la == 2 ? 0 : t) * C::kTileBytes >> 4);
+      const uint64_t k = kd + (st * C::kTileBytes >> 4);
+#pragma unroll
+      for (int s = 0; s < C::DP / 16; ++s) {
+        const uint32_t off = ((s >> 2) * C::kChunk + (s & 3) * 32) >> 4;
+        tc::mma_f16_ss(tmem + C::kSCol + t * kBK, q + off, k + off, id_s, s > 0);
+      }
+      tc::mma_commit_warp(&bars->s_full[t]);
+    };
+    wait(&bars->q_full, r & 1);
+    for (int e = 0; e < la && jlo + e <= jhi; ++e) {
+      const uint32_t st = take();
+      tc::fence_after_sync();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (active(t, jlo + e)) scores(t, st);
+      tc::mma_commit_warp(&bars->kv_empty[st]);
+    }
+    if (jlo + la > jhi) tc::mma_commit_warp(&bars->q_empty);
+    for (int j = jlo; j <= jhi; ++j) {
+      const uint32_t vs = take();
+      const bool next = j + la <= jhi;
+      uint32_t ks = 0;
+      if (next) ks = take();
+      if (nk - j * kBK < kBK) wait(&bars->v_fixed, fixed++ & 1);
+      const uint64_t v = vd + (vs * C::kTileBytes >> 4);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (active(t, j)) {
+          const bool first = la == 2 ? j - jlo == t : j == lo[t];
+          if (first) {
+            if (outputs[t] > 0) wait(&bars->o_free[t], (outputs[t] - 1) & 1);
+            ++outputs[t];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wait(&bars->p_ready[t][h], done[t] & 1);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int s = 4 * h; s < 4 * h + 4; ++s)
+              tc::mma_f16_ts(tmem + C::kOCol + t * C::DP, tmem + C::kSCol + t * kBK + 8 * s,
+                             v + (s * 2048 >> 4), id_o, (!first || s > 0) ? 1u : 0u);
+            if (h == 0) tc::mma_commit_warp(&bars->o_half[t]);
+          }
+          tc::mma_commit_warp(&bars->o_done[t]);
+          ++done[t];
+        }
+        if (next && active(t, j + la)) scores(t, ks);
+      }
+      tc::mma_commit_warp(&bars->kv_empty[vs]);
+      if (next) tc::mma_commit_warp(&bars->kv_empty[ks]);
+      if (j + la == jhi) tc::mma_commit_warp(&bars->q_empty);   // the unit's last S
+      if (__any_sync(0xffffffffu, bad)) break;
+    }
+    if (__any_sync(0xffffffffu, bad)) break;
+  }
+  tc::mma_commit_warp(&bars->drain);           // nothing may still run when the block frees its TMEM
+  drain_wait(&bars->drain, 0);
+}
+
+// ---------------------------------------------------------------- softmax (4 warps a tile)
+template <class C>
+__device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, Bars* bars, int t, int quarter,
+                        int lane, uint32_t& n) {
+  using T = typename C::T;
+  volatile int* abort = &bars->abort;
+  const uint32_t n0 = n;                       // this tile's blocks before this unit
+  const int row = quarter * 32 + lane, tok = row / a.G, head = u.hk * a.G + row % a.G;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const int tile = C::SHARED && u.la == 2 ? 0 : t;
+  const int local = tile * a.TQ + tok;         // token of the unit
+  const bool live = tok < a.TQ && local < u.ntok;
+  const int qpos = u.q0 + local;
+  const float cs = a.softcap_on ? 1.0f : a.c_score;
+  constexpr float kLimit = C::BF16 ? 256.0f : 32768.0f;   // 2^(8 + kBias)
+  float m_ref = -INFINITY, l = 0.f;            // P = 2^(score - m_ref) with the bias inside m_ref
+  // The warp's rows' first and last visible keys are ordered as their tokens are.
+  const int tok0 = 32 * quarter / a.G, tok1 = min((32 * quarter + 31) / a.G, a.TQ - 1);
+  const int q_lo = u.q0 + tile * a.TQ + tok0, q_hi = u.q0 + tile * a.TQ + tok1;
+  int j_lo, j_hi;
+  tile_blocks<C>(a, u, t, j_lo, j_hi);
+  bool ok = true, started = false;             // started: every live row has a reference
+  for (int j = u.la == 2 ? j_lo + t : j_lo; j <= j_hi; j += u.la) {
+    ok = tc::mbar_wait(&bars->s_full[t], n & 1, abort);
+    if (__any_sync(0xffffffffu, !ok)) {        // leave together: tcgen05.ld is warp-wide
+      ok = false;
+      break;
+    }
+    tc::fence_after_sync();
+    const uint32_t scol = lane_base + C::kSCol + t * kBK;
+    float s[128];
+    tc::tmem_ld128(scol, s);
+    const int k0 = j * kBK;
+    if (a.softcap_on) {
+#pragma unroll
+      for (int c = 0; c < 128; ++c) {
+        const float e = tc::ex2(s[c] * a.c_cap_in);
+        s[c] = fmaf(-2.0f * a.c_cap_out, tc::rcp(e + 1.0f), a.c_cap_out);
+      }
+    }
+    // Blocks that the mask crosses: keys c <= hi and c >= lo are visible.
+    if (k0 + kBK > u.nk || (!C::SHARED && (k0 + kBK - 1 > q_lo ||
+                                           (a.window > 0 && k0 < q_hi - a.window + 1)))) {
+      const int hi = (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;
+      const int lo = !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : 0;
+#pragma unroll
+      for (int c = 0; c < 128; ++c) s[c] = c > hi || c < lo ? -INFINITY : s[c];
+    }
+    // P in two halves of 64 columns, each released to the products as soon as it is written.
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      uint32_t p[32];
+      float lsum;
+      bool slow = !started;
+#pragma unroll 1
+      while (true) {
+        if (slow) {                            // a new reference from this half's maximum
+          const float m_new = fmaxf(m_ref, fmaf(prefill::tq_max<64>(s + 64 * hh), cs, -C::kBias));
+          const bool grow = m_ref != -INFINITY && m_new - m_ref > kRescaleLog2;
+          if (__any_sync(0xffffffffu, grow)) {
+            if (n > n0 || hh > 0) {            // once every product that wrote O is done
+              ok = hh == 0 ? tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort)
+                           : tc::mbar_wait(&bars->o_half[t], n & 1, abort);
+              if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+              }
+              tc::fence_after_sync();
+              const float f = grow ? tc::ex2(m_ref - m_new) : 1.0f;
+#pragma unroll 1
+              for (int c = 0; c < C::DP; c += 16) {
+                float o[16];
+                tc::tmem_ld16(lane_base + C::kOCol + t * C::DP + c, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tc::tmem_st16(lane_base + C::kOCol + t * C::DP + c, o);
+              }
+              l *= f;
+            }
+            if (grow) m_ref = m_new;
+          }
+          if (m_ref == -INFINITY) m_ref = m_new;
+        }
+        // -inf only while every key so far was masked; then every score is -inf
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t c2 = tc::pack2(cs, cs), m2 = tc::pack2(-m_use, -m_use);
+        uint64_t acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = tc::pack2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float x0, x1;
+          tc::unpack2(tc::fma2(tc::pack2(s[64 * hh + c], s[64 * hh + c + 1]), c2, m2), x0, x1);
+          x0 = tc::ex2(x0);
+          x1 = tc::ex2(x1);
+          p[c / 2] = Pair<T>::pack(x0, x1);
+          acc[(c / 2) % 4] = tc::add2(acc[(c / 2) % 4], tc::pack2(x0, x1));
+        }
+        float a0, a1;
+        tc::unpack2(tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3])), a0, a1);
+        lsum = a0 + a1;
+        if (slow || !__any_sync(0xffffffffu, live && !(lsum <= kLimit))) break;
+        slow = true;
+      }
+      if (!ok) break;
+      l += lsum;
+      tc::tmem_st32(scol + 32 * hh, reinterpret_cast<const float*>(p));
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->p_ready[t][hh]);
+      if (!started && hh == 1) started = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
+    }
+    if (!ok) break;
+    ++n;
+  }
+  if (!ok) return false;
+
+  const bool has = n > n0;                     // the tile had blocks: its O waits to be read
+  if (has) {
+    ok = tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort);
+    if (__any_sync(0xffffffffu, !ok || *abort)) return false;
+    tc::fence_after_sync();
+  }
+  const bool any = has && m_ref != -INFINITY;
+  const float inv = any ? 1.0f / l : 0.f;
+  if constexpr (C::SHARED) {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.H;
+    const int part = u.la == 2 ? 2 * u.part + t : u.part;
+    if (u.la == 1 && t >= u.nt) return true;
+    const int64_t at = part * rows + static_cast<int64_t>(u.row0 + local) * a.H + head;
+    if (live) a.part_ml[at] = make_float2(any ? m_ref : -INFINITY, any ? l : 0.f);
+#pragma unroll 1
+    for (int c = 0; c < C::DP; c += 32) {
+      float o[32];
+      if (has) tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
+      float* dst = a.part_o + at * a.D + c;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        if (live && c + e < a.D)
+          *reinterpret_cast<float4*>(dst + e) =
+              any ? make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  } else {
+    if (t >= u.nt) return true;
+    T* dst = static_cast<T*>(a.out) + (u.row0 + local) * a.o_token + head * a.o_head;
+#pragma unroll 1
+    for (int c = 0; c < C::DP; c += 32) {
+      float o[32];
+      tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        if (live && c + e < a.D) {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = o[e + i] * inv;
+          *reinterpret_cast<uint4*>(dst + c + e) = pack8<T>(x);
+        }
+    }
+  }
+  if (has) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bars->o_free[t]);
+  }
+  return true;
+}
+
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     attn16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  dependent_wait();
   if (gated_off(a.skip)) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -489,31 +588,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* skv = sq + 2 * C::kTileBytes;
   Bars* bars = reinterpret_cast<Bars*>(skv + C::NS * C::kTileBytes);
   static_assert(sizeof(Bars) <= 1024, "barriers fit behind the ring");
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   if (warp == 9) {
     tc::tmem_alloc(&bars->tmem_base, kTmemCols);
     tc::tmem_relinquish();
   }
-  if (warp == 8) {
-    Unit u{};
-    const bool any = find_unit<C>(a, blockIdx.x, u);
-    if (lane == 0) {
-      if (!any) u.nt = 0;
-      bars->unit = u;
-    }
-  }
   if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->answered, 1);
     tc::mbar_init(&bars->q_full, 1);
+    tc::mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < C::NS; ++s) {
       tc::mbar_init(&bars->kv_full[s], 1);
       tc::mbar_init(&bars->kv_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(&bars->s_full[t], 1);
-      tc::mbar_init(&bars->p_ready[t][0], 128);
-      tc::mbar_init(&bars->p_ready[t][1], 128);
+      tc::mbar_init(&bars->p_ready[t][0], 4);
+      tc::mbar_init(&bars->p_ready[t][1], 4);
       tc::mbar_init(&bars->o_half[t], 1);
       tc::mbar_init(&bars->o_done[t], 1);
+      tc::mbar_init(&bars->o_free[t], 4);
+      tc::mbar_init(&bars->unit_full[t], 1);
+      tc::mbar_init(&bars->unit_empty[t], 9);
     }
     tc::mbar_init(&bars->v_fixed, 1);
     tc::mbar_init(&bars->drain, 1);
@@ -524,15 +620,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
-  const Unit u = bars->unit;
-  if (u.nt > 0) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
-      producer<C>(a, u, &tm_q, &tm_k, &tm_v, sq, skv, bars, lane);
+      producer<C>(a, &tm_q, &tm_k, &tm_v, sq, skv, bars, lane);
     } else if (warp == 9) {
-      if (lane == 0) products<C>(a, u, tmem, sq, skv, bars);
-      __syncwarp();
-    } else {
-      softmax<C>(a, u, tmem, bars, warp / 4, warp % 4, lane);
+      products<C>(a, tmem, sq, skv, bars);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    uint32_t n = 0;
+    for (uint32_t r = 0;; ++r) {
+      Unit u;
+      const bool any = next_unit(bars, r, u);
+      if (!__all_sync(0xffffffffu, any)) break;    // every lane has read it
+      if (lane == 0) tc::mbar_arrive(&bars->unit_empty[r & 1]);
+      if (!softmax<C>(a, u, tmem, bars, warp / 4, warp % 4, lane, n)) break;
     }
   }
   tc::fence_before_sync();
@@ -621,8 +724,7 @@ cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
         !map_rows(&tv, j.v, j.bf16, a.D, a.Hkv, a.T, 1, kBK))
       return cudaErrorInvalidValue;
   }
-  attn16_kernel<C><<<grid, kThreads, C::kSmem, stream>>>(tq, tk, tv, a);
-  return cudaGetLastError();
+  return launch_dependent(attn16_kernel<C>, grid, kThreads, C::kSmem, stream, tq, tk, tv, a);
 }
 
 template <class T>
