@@ -29,6 +29,9 @@
 //  * Every wait is bounded; one that runs out raises ATTN_DEV_TIMEOUT and the block winds down.
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "paged.cuh"
 #include "prefill_common.cuh"
 
@@ -49,7 +52,7 @@ struct Args {
   const int32_t* prefix_table;                 // shared prefix
   int prefix_len, pages, page_shift;
   int H, Hkv, D, G, TQ;
-  int units, splits, split_keys;               // shared: row pairs, splits of the key blocks
+  int units, splits, split_keys;               // shared: pairs of tiles, splits of the key blocks
   int window, softcap_on;
   float c_score, c_cap_in, c_cap_out;          // log2 units
   void* out;
@@ -84,8 +87,6 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "the block's registers");
 
 struct Bars {
-  uint4 answer;                                // of the launch control
-  uint64_t answered;
   uint64_t unit_full[2], unit_empty[2];
   uint64_t q_full, q_empty;
   uint64_t kv_full[8], kv_empty[8];
@@ -125,13 +126,38 @@ __device__ __forceinline__ void tile_blocks(const Args& a, const Unit& u, int t,
 }
 
 // ---------------------------------------------------------------- producer (one warp)
-// Unit x of the grid; false where it is empty. Whole warp.
+// The blocks walk one list of units, heaviest first, in snake order: unit x of round r for block c.
+__device__ __forceinline__ unsigned unit_at(unsigned c, unsigned r, unsigned blocks) {
+  return r * blocks + ((r & 1) ? blocks - 1 - c : c);
+}
+
+// Tiles (of 2 TQ tokens) of sequence b; 0 where its bounds break a rule.
+__device__ __forceinline__ int seq_tiles(const Args& a, int b, bool tell) {
+  const SeqRows s = seq_rows(a.cu, b, a.T);
+  if (s.n < 0 || s.n > a.max_len) {
+    if (tell) report(a.status, ATTN_DEV_LENGTH);
+    return 0;
+  }
+  return (s.n + 2 * a.TQ - 1) / (2 * a.TQ);
+}
+
+// Tiles of all sequences with index >= i (whole warp; cu_seqlens stays in L1).
+__device__ __forceinline__ int tiles_from(const Args& a, int i, bool tell) {
+  int n = 0;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += max(0, seq_tiles(a, b, tell) - i);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// Unit x of the list; false past its end. Whole warp. Packed prompts: tiles by their index within
+// their sequence, last first (a tile's keys grow with it), the kv heads of a tile side by
+// side. `top`: no tile of index top or above is left (kept from unit to unit).
 template <class C>
-__device__ bool find_unit(const Args& a, unsigned x, Unit& u) {
+__device__ bool find_unit(const Args& a, unsigned x, int& top, Unit& u) {
   u.hk = x % a.Hkv;
   const int y = x / a.Hkv, tokens = 2 * a.TQ;
   if (C::SHARED) {
     const int pair = y / a.splits, blocks = (a.prefix_len + kBK - 1) / kBK;
+    if (pair >= a.units) return false;
     u.part = y % a.splits;
     u.row0 = pair * tokens;
     u.q0 = 0;
@@ -144,20 +170,29 @@ __device__ bool find_unit(const Args& a, unsigned x, Unit& u) {
     u.la = a.split_keys ? 2 : 1;
     return true;
   }
-  // Sequence b's tiles begin at slot cu[b] / tokens + b: never more than the next one's.
-  // Later slots first: the last tokens of a prompt have the most keys.
-  const int slot = a.units - 1 - y;
-  const int b = warp_find_last(a.B, slot, [&](int i) {
-    return static_cast<int64_t>(max(a.cu[i], 0) / tokens) + i;
-  });
-  if (b < 0) return false;
-  const SeqRows s = seq_rows(a.cu, b, a.T);
-  if (s.n < 0 || s.n > a.max_len) {
-    if (threadIdx.x % 32 == 0) report(a.status, ATTN_DEV_LENGTH);
-    return false;
+  // The largest index i < top with more than y tiles of index >= i.
+  if (tiles_from(a, 0, false) <= y) return false;
+  int lo = 0, hi = top;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (tiles_from(a, mid, false) > y) lo = mid; else hi = mid;
   }
-  u.q0 = (slot - (s.first / tokens + b)) * tokens;
-  if (u.q0 >= s.n) return false;
+  top = lo + 1;
+  int k = y - tiles_from(a, lo + 1, false);    // among the sequences that have a tile lo
+  int b = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int mine = b0 + (threadIdx.x & 31);
+    const bool has = mine < a.B && seq_tiles(a, mine, false) > lo;
+    const uint32_t all = __ballot_sync(0xffffffffu, has);
+    if (k < __popc(all)) {                     // the lane with k others before it
+      const int before = __popc(all & ((1u << (threadIdx.x & 31)) - 1));
+      b = b0 + __ffs(__ballot_sync(0xffffffffu, has && before == k)) - 1;
+      break;
+    }
+    k -= __popc(all);
+  }
+  const SeqRows s = seq_rows(a.cu, b, a.T);
+  u.q0 = lo * tokens;
   u.ntok = min(tokens, s.n - u.q0);
   u.row0 = s.first + u.q0;
   u.kbase = s.first;
@@ -170,16 +205,15 @@ __device__ bool find_unit(const Args& a, unsigned x, Unit& u) {
   return true;
 }
 
-// Finds the block's units, its own and then any that no block has begun (cancelled launches),
-// publishes each and loads it. The next one's search and loads run while the products are still
-// at this one's.
+// Finds the block's units, publishes each and loads it. The next one's search and loads run while
+// the products are still at this one's.
 template <class C>
 __device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap* tk,
                          const CUtensorMap* tv, uint8_t* sq, uint8_t* skv, Bars* bars, int lane) {
   volatile int* abort = &bars->abort;
   int stage = 0;
   uint32_t phase = 0, loaded = 0;              // loads so far
-  uint32_t units = 0, asked = 0;
+  uint32_t units = 0;
   Unit u{};
   // The last block of a sequence may hold fewer than 128 keys: its V is zeroed behind them.
   auto load = [&](bool is_v, int j) -> bool {
@@ -249,53 +283,41 @@ __device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap
     }
     return __shfl_sync(0xffffffffu, ok, 0);
   };
-  bool ok = true, answer_due = false;
-  int x = blockIdx.x;
+  bool ok = true;
+  int top = 0x7fffffff;
+  if (!C::SHARED) {
+    int most = 0;
+    for (int b = lane; b < a.B; b += 32) most = max(most, seq_tiles(a, b, blockIdx.x == 0));
+    top = __reduce_max_sync(0xffffffffu, most);
+  }
   while (ok) {
-    if (lane == 0) {                           // the next unit, asked for ahead
-      tc::fence_proxy_async();
-      tc::mbar_arrive_expect_tx(&bars->answered, 16);
-      tc::clc_request(&bars->answer, &bars->answered);
-    }
-    answer_due = true;
-    if (find_unit<C>(a, x, u)) {
-      if (!(ok = publish())) break;
-      const int tiles = u.la == 2 ? 1 : u.nt;
-      if (lane == 0) {
-        ok = tc::mbar_wait(&bars->q_empty, (units & 1) ^ 1u, abort);
-        if (ok) {
-          tc::mbar_arrive_expect_tx(&bars->q_full, tiles * C::kChunks * 128 * a.G * a.TQ);
-          for (int t = 0; t < tiles; ++t)
-            for (int c = 0; c < C::kChunks; ++c)
-              tc::tma_load_3d(sq + t * C::kTileBytes + c * C::kChunk, tq, &bars->q_full, 64 * c,
-                              u.hk * a.G, u.row0 + t * a.TQ);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      ++units;
-      for (int e = 0; ok && e < u.la && u.jlo + e <= u.jhi; ++e) ok = load(false, u.jlo + e);
-      for (int j = u.jlo; ok && j <= u.jhi; ++j) {
-        ok = load(true, j);
-        if (ok && j + u.la <= u.jhi) ok = load(false, j + u.la);
-      }
-      if (!ok) break;
-    }
-    ok = tc::mbar_wait(&bars->answered, asked & 1, abort);
-    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-    ++asked;
-    answer_due = false;
-    x = tc::clc_answer(&bars->answer);
-    __syncwarp();
-    if (x < 0) {
+    if (!find_unit<C>(a, unit_at(blockIdx.x, units, gridDim.x), top, u)) {
       u.nt = 0;
       publish();
       break;
     }
+    if (!(ok = publish())) break;
+    if (lane == 0) {
+      const int tiles = u.la == 2 ? 1 : u.nt;
+      ok = tc::mbar_wait(&bars->q_empty, (units & 1) ^ 1u, abort);
+      if (ok) {
+        tc::mbar_arrive_expect_tx(&bars->q_full, tiles * C::kChunks * 128 * a.G * a.TQ);
+        for (int t = 0; t < tiles; ++t)
+          for (int c = 0; c < C::kChunks; ++c)
+            tc::tma_load_3d(sq + t * C::kTileBytes + c * C::kChunk, tq, &bars->q_full, 64 * c,
+                            u.hk * a.G, u.row0 + t * a.TQ);
+      }
+    }
+    if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+    ++units;
+    for (int e = 0; ok && e < u.la && u.jlo + e <= u.jhi; ++e) ok = load(false, u.jlo + e);
+    for (int j = u.jlo; ok && j <= u.jhi; ++j) {
+      ok = load(true, j);
+      if (ok && j + u.la <= u.jhi) ok = load(false, j + u.la);
+    }
   }
   // Every copy this block started lands before the block may exit.
   if (lane == 0) {
-    if (answer_due) drain_wait(&bars->answered, asked & 1);
     if (units > 0) drain_wait(&bars->q_full, (units - 1) & 1);
     for (uint32_t s = 0; s < C::NS && s < loaded; ++s) {
       const uint32_t fill = (loaded - 1 - s) / C::NS;   // the last load into stage s
@@ -594,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    tc::mbar_init(&bars->answered, 1);
     tc::mbar_init(&bars->q_full, 1);
     tc::mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < C::NS; ++s) {
@@ -705,26 +726,27 @@ cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
   a.part_o = j.part_o; a.part_ml = j.part_ml;
   a.status = j.status; a.skip = j.skip;
   const int tokens = 2 * a.TQ;
-  unsigned grid;
+  int64_t grid;                                // units at most: no more blocks than SMs
   CUtensorMap tq, tk, tv;
   if (C::SHARED) {
     a.split_keys = a.B <= a.TQ;
     a.splits = shared_prefix_splits(a.B, a.H, a.Hkv, a.prefix_len) / (a.split_keys ? 2 : 1);
     a.units = (a.B + tokens - 1) / tokens;
-    grid = static_cast<unsigned>(a.Hkv) * a.units * a.splits;
+    grid = static_cast<int64_t>(a.Hkv) * a.units * a.splits;
     if (!map_rows(&tq, j.q, j.bf16, a.D, a.H, a.B, a.G, a.TQ) ||
         !map_pool(&tk, j.cache.k, j.bf16, a.D, a.Hkv, j.cache) ||
         !map_pool(&tv, j.cache.v, j.bf16, a.D, a.Hkv, j.cache))
       return cudaErrorInvalidValue;
   } else {
-    a.units = a.T / tokens + a.B;
-    grid = static_cast<unsigned>(a.Hkv) * a.units;
+    const int64_t tiles = (static_cast<int64_t>(a.max_len) + tokens - 1) / tokens;
+    grid = static_cast<int64_t>(a.Hkv) * std::min<int64_t>(a.T / tokens + a.B, tiles * a.B);
     if (!map_rows(&tq, j.q, j.bf16, a.D, a.H, a.T, a.G, a.TQ) ||
         !map_rows(&tk, j.k, j.bf16, a.D, a.Hkv, a.T, 1, kBK) ||
         !map_rows(&tv, j.v, j.bf16, a.D, a.Hkv, a.T, 1, kBK))
       return cudaErrorInvalidValue;
   }
-  return launch_dependent(attn16_kernel<C>, grid, kThreads, C::kSmem, stream, tq, tk, tv, a);
+  grid = std::max<int64_t>(1, std::min<int64_t>(grid, prefill::sm_count()));
+  return launch_dependent(attn16_kernel<C>, static_cast<unsigned>(grid), kThreads, C::kSmem, stream, tq, tk, tv, a);
 }
 
 template <class T>

@@ -904,16 +904,6 @@ __global__ void __launch_bounds__(PCfg<DP>::kThreads, 1)
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    return 152;
-  }
-  return n;
-}
-
 template <int DP, bool ROPE, bool RAGGED>
 cudaError_t launch_tq(const AttnShape& s, cudaStream_t stream) {
   using C = PCfg<DP, RAGGED>;

@@ -192,32 +192,6 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// ---------------------------------------------------------------- cluster launch control
-// Ask for a block of this grid that has not started: its launch is cancelled and its index comes
-// back, as 16 bytes at `resp` counted on `bar`. After an answer without a block no more may be
-// asked for.
-__device__ __forceinline__ void clc_request(void* resp, uint64_t* bar) {
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
-      " [%0], [%1];" ::"r"(smem_u32(resp)),
-      "r"(smem_u32(bar))
-      : "memory");
-}
-
-// The answer: the block's index (x), or -1.
-__device__ __forceinline__ int clc_answer(const void* resp) {
-  uint32_t ok, x;
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b128 h;\n ld.shared.b128 h, [%2];\n"
-      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
-      " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
-      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
-      : "=r"(ok), "=r"(x)
-      : "r"(smem_u32(resp))
-      : "memory");
-  return ok ? static_cast<int>(x) : -1;
-}
-
 // ---------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
