@@ -18,14 +18,19 @@
 //    MN-major operand of the second product as it lies: no transposition.
 //  * Tensor memory: S0 | S1 (128 fp32 columns each), O0 | O1. P overwrites S's first half in
 //    16 bits and is the A operand of O += P V.
-//  * One warp issues all products, in the order P V (tile 0), next S (tile 0), P V (tile 1),
-//    next S (tile 1): the tensor pipe runs them in that order, so S may be written over the
-//    P before it without a wait.
-//  * Softmax: a thread per row, 4 warps per tile. The reference is the row's first maximum and stands until a half's sum shows that some weight exceeded
-//    2^8 (then the half is redone against a new maximum and O rescaled): no maximum is
-//    taken in the common case.
+//  * Each tile's products are issued by a warp of its own, P V before the next S: the tensor
+//    pipe runs a warp's products in order, so S may be written over the P before it without a
+//    wait. (One warp for both spent a third of its time on barriers that were long complete,
+//    about 150 cycles each, with the pipe running dry: 8192 tokens 394 us.)
+//  * Softmax: a thread per row, 4 warps per tile. The reference is the row's first maximum and
+//    stands until a block's weights sum to more than 2^15 (then the block is redone against a
+//    new maximum and O rescaled): no maximum is taken in the common case.
 //  * Values behind the last key (another sequence's, an unused slot's) are zeroed in shared memory:
 //    whatever lies there, NaNs included, has no part in the result.
+//  * Sixteen warps: softmax (2 x 4), loads, products (2), the list of units with the zeroing of V
+//    behind the last key, and four that bring finished rows out of tensor memory, so that the
+//    next unit's products and softmax run meanwhile. The blocks walk one list of units (a
+//    pair of tiles each), heaviest first.
 //  * Every wait is bounded; one that runs out raises ATTN_DEV_TIMEOUT and the block winds down.
 #pragma once
 
@@ -39,11 +44,11 @@ namespace gqa {
 namespace attn16 {
 
 using prefill::drain_wait;
-using prefill::kRescaleLog2;
 using prefill::kSmemLimit;
 using prefill::kTmemCols;
 
 constexpr int kBK = 128;                       // keys per block
+constexpr int kSums = 2 * 128 * 8;             // (sum, reference) of each row, behind the barriers
 constexpr int kRows = 128;                     // query rows per tile
 
 struct Args {
@@ -52,6 +57,8 @@ struct Args {
   const int32_t* prefix_table;                 // shared prefix
   int prefix_len, pages, page_shift;
   int H, Hkv, D, G, TQ;
+  uint64_t inv_tokens;                         // floor(2^64 / (2 TQ)) + 1: n / (2 TQ) by the product's high half
+  uint32_t inv_G;                              // floor(2^16 / G) + 1: row / G, row < 128
   int units, splits, split_keys;               // shared: pairs of tiles, splits of the key blocks
   int window, softcap_on;
   float c_score, c_cap_in, c_cap_out;          // log2 units
@@ -72,42 +79,47 @@ struct Cfg {
   static constexpr int kChunks = DP / 64;
   static constexpr int kChunk = 128 * 128;     // 128 rows x 64 dims (128 bytes)
   static constexpr int kTileBytes = kChunks * kChunk;   // a Q tile, a K block or a V block
-  static constexpr int kNSraw = (kSmemLimit - 2048 - 2 * kTileBytes) / kTileBytes;
+  static constexpr int kOut = 4 * 4096;        // 4 KB a warp: output rows on their way out
+  static constexpr int kNSraw = (kSmemLimit - 2048 - kSums - kOut - 2 * kTileBytes) / kTileBytes;
   static constexpr int NS = kNSraw > 8 ? 8 : kNSraw;
-  static constexpr int kSmem = (NS + 2) * kTileBytes + 2048;
+  static constexpr int kSmem = (NS + 2) * kTileBytes + kOut + kSums + 2048;
   static constexpr int kSCol = 0, kOCol = 256;
-  // fp16 has few small numbers and P's range is [0, 2^(8 + kBias)]: shifted up, weights down
-  // to 2^-21 of the largest keep all their bits.
+  // fp16 has few small numbers: with the first maximum's weight at 2^7, weights down to 2^-21 of
+  // it keep all their bits, and there is room for weights 2^8 times as large.
   static constexpr float kBias = BF16 ? 0.f : 7.f;
 };
-// 2 x 4 softmax warps; producer, products and two idle warps. The block starts with 168
-// registers a thread; a row's 128 scores take more, so the last four warps hand theirs on.
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "the block's registers");
+// Warps 0-7 softmax, 8 loads, 9 and 10 products, 11 units and V's tails, 12-15 output rows. The block starts
+// with 128 registers a thread; a row's 128 scores take more, so the last eight warps hand theirs on.
+constexpr int kThreads = 512;
+constexpr int kRegsSoftmax = 184, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "the block's registers");
+constexpr int kUnits = 4;                      // units ahead
+constexpr int kReaders = 15;                   // warps that read each unit
 
 struct Bars {
-  uint64_t unit_full[2], unit_empty[2];
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t q_full, q_empty;
   uint64_t kv_full[8], kv_empty[8];
+  uint64_t landed[8];                          // V that is zeroed behind the last key before it is full
   uint64_t s_full[2];
-  uint64_t p_ready[2][2];                      // [tile][half]
-  uint64_t o_half[2], o_done[2], o_free[2];
-  uint64_t v_fixed;                            // the last block's V is zeroed behind the last key
-  uint64_t drain;
+  uint64_t p_ready[2], o_done[2];
+  uint64_t turn[2];                            // the tiles' products of a block are issued in turn
+  uint64_t l_ready[2], o_final[2], o_free[2];  // once a unit
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
   struct {
     int hk, row0, q0, ntok, kbase, nk, jlo, jhi, nt, la, part;   // nt 0: no more units
-  } unit[2];
+  } unit[kUnits];
 };
 using Unit = std::remove_extent<decltype(Bars::unit)>::type;
 
-// The block's r-th unit, read by a consumer (count of unit_empty: the products' thread and
-// one lane of each softmax warp).
-__device__ __forceinline__ bool next_unit(Bars* bars, uint32_t r, Unit& u) {
-  if (!tc::mbar_wait(&bars->unit_full[r & 1], (r >> 1) & 1, &bars->abort)) return false;
-  u = bars->unit[r & 1];
+// The block's r-th unit, read by a whole warp; false: there is none (or a wait ran out).
+__device__ __forceinline__ bool next_unit(Bars* bars, uint32_t r, int lane, Unit& u) {
+  const bool ok = tc::mbar_wait_short(&bars->unit_full[r % kUnits], (r / kUnits) & 1, &bars->abort);
+  if (ok) u = bars->unit[r % kUnits];
+  if (!__all_sync(0xffffffffu, ok)) return false;              // every lane has read it
+  if (lane == 0) tc::mbar_arrive(&bars->unit_empty[r % kUnits]);
   return u.nt > 0;
 }
 
@@ -138,21 +150,22 @@ __device__ __forceinline__ int seq_tiles(const Args& a, int b, bool tell) {
     if (tell) report(a.status, ATTN_DEV_LENGTH);
     return 0;
   }
-  return (s.n + 2 * a.TQ - 1) / (2 * a.TQ);
+  return static_cast<int>(__umul64hi(s.n + 2 * a.TQ - 1, a.inv_tokens));
 }
 
 // Tiles of all sequences with index >= i (whole warp; cu_seqlens stays in L1).
-__device__ __forceinline__ int tiles_from(const Args& a, int i, bool tell) {
+__device__ __forceinline__ int tiles_from(const Args& a, int i) {
   int n = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += max(0, seq_tiles(a, b, tell) - i);
+#pragma unroll 1
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += max(0, seq_tiles(a, b, false) - i);
   return __reduce_add_sync(0xffffffffu, n);
 }
 
 // Unit x of the list; false past its end. Whole warp. Packed prompts: tiles by their index within
 // their sequence, last first (a tile's keys grow with it), the kv heads of a tile side by
-// side. `top`: no tile of index top or above is left (kept from unit to unit).
+// side. `past` tiles have an index of top or above (kept from unit to unit, which come in order).
 template <class C>
-__device__ bool find_unit(const Args& a, unsigned x, int& top, Unit& u) {
+__device__ bool find_unit(const Args& a, unsigned x, int& top, int& past, Unit& u) {
   u.hk = x % a.Hkv;
   const int y = x / a.Hkv, tokens = 2 * a.TQ;
   if (C::SHARED) {
@@ -170,16 +183,22 @@ __device__ bool find_unit(const Args& a, unsigned x, int& top, Unit& u) {
     u.la = a.split_keys ? 2 : 1;
     return true;
   }
-  // The largest index i < top with more than y tiles of index >= i.
-  if (tiles_from(a, 0, false) <= y) return false;
-  int lo = 0, hi = top;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (tiles_from(a, mid, false) > y) lo = mid; else hi = mid;
+  // The largest index lo < top with more than y tiles of index >= lo; then top = lo + 1.
+  int lo = -1;
+#pragma unroll 1
+  while (top - lo > 1) {
+    const int mid = (lo + top) / 2, n = tiles_from(a, mid);
+    if (n > y) {
+      lo = mid;
+    } else {
+      top = mid;
+      past = n;
+    }
   }
-  top = lo + 1;
-  int k = y - tiles_from(a, lo + 1, false);    // among the sequences that have a tile lo
+  if (lo < 0) return false;
+  int k = y - past;                            // among the sequences that have a tile lo
   int b = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int mine = b0 + (threadIdx.x & 31);
     const bool has = mine < a.B && seq_tiles(a, mine, false) > lo;
@@ -205,20 +224,75 @@ __device__ bool find_unit(const Args& a, unsigned x, int& top, Unit& u) {
   return true;
 }
 
-// Finds the block's units, publishes each and loads it. The next one's search and loads run while
-// the products are still at this one's.
+// ---------------------------------------------------------------- units, and V behind the last key (one warp)
+// The last block of a sequence may hold fewer than 128 keys: once its V has landed, the rows
+// behind them are zeroed, and only then is the stage full.
 template <class C>
-__device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap* tk,
-                         const CUtensorMap* tv, uint8_t* sq, uint8_t* skv, Bars* bars, int lane) {
+__device__ __forceinline__ bool zero_tail(const Unit& u, uint8_t* skv, Bars* bars, int lane,
+                                          uint32_t& loaded, uint32_t& fills) {
+  loaded += 2 * (u.jhi - u.jlo + 1);           // as the loads count them: the unit's last is its last V
+  const int keys = u.nk - u.jhi * kBK, stage = (loaded - 1) % C::NS;
+  if (keys >= kBK) return true;
+  const bool ok = tc::mbar_wait_short(&bars->landed[stage], fills >> stage & 1, &bars->abort);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  fills ^= 1u << stage;
+  uint8_t* v = skv + stage * C::kTileBytes;
+#pragma unroll 1
+  for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll 2
+    for (int e = 8 * keys + lane; e < 8 * kBK; e += 32)
+      *reinterpret_cast<uint4*>(v + c * C::kChunk + e * 16) = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(&bars->kv_full[stage]);
+  return true;
+}
+
+// Publishes the block's units; a unit's tail is done once the next one is published.
+template <class C>
+__device__ void scheduler(const Args& a, uint8_t* skv, Bars* bars, int lane) {
+  volatile int* abort = &bars->abort;
+  int top = 0, past = 0;
+  uint32_t loaded = 0, fills = 0;
+  if (!C::SHARED) {
+#pragma unroll 1
+    for (int b = lane; b < a.B; b += 32) top = max(top, seq_tiles(a, b, blockIdx.x == 0));
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  Unit before{};
+  for (uint32_t r = 0;; ++r) {
+    Unit u{};
+    const bool any = find_unit<C>(a, unit_at(blockIdx.x, r, gridDim.x), top, past, u);
+    if (!any) u.nt = 0;
+    bool ok = true;
+    if (lane == 0) {
+      ok = tc::mbar_wait_short(&bars->unit_empty[r % kUnits], ((r / kUnits) & 1) ^ 1u, abort);
+      if (ok) {
+        bars->unit[r % kUnits] = u;
+        tc::mbar_arrive(&bars->unit_full[r % kUnits]);
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok && r > 0) ok = zero_tail<C>(before, skv, bars, lane, loaded, fills);
+    if (!any || !ok) return;
+    before = u;
+  }
+}
+
+// ---------------------------------------------------------------- loads (one warp)
+// A unit's ring order: K of its first block (first la blocks), then V and the K that is la ahead.
+template <class C>
+__device__ void loads(const Args& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                      const CUtensorMap* tv, uint8_t* sq, uint8_t* skv, Bars* bars, int lane) {
   volatile int* abort = &bars->abort;
   int stage = 0;
-  uint32_t phase = 0, loaded = 0;              // loads so far
-  uint32_t units = 0;
+  uint32_t phase = 0, loaded = 0, units = 0;
+  uint32_t to_land = 0, fills = 0;             // stages whose last load lands apart; landings' parities
   Unit u{};
-  // The last block of a sequence may hold fewer than 128 keys: its V is zeroed behind them.
   auto load = [&](bool is_v, int j) -> bool {
     bool ok = true;
-    uint64_t* full = &bars->kv_full[stage];
+    const bool apart = is_v && u.nk - j * kBK < kBK;   // zeroed behind the last key, then full
+    uint64_t* full = apart ? &bars->landed[stage] : &bars->kv_full[stage];
     uint8_t* dst = skv + stage * C::kTileBytes;
     int rows = kBK, id = 0;
     const int page = 1 << a.page_shift, box = min(page, kBK);
@@ -234,7 +308,7 @@ __device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap
       }
       rows = boxes * box;
     }
-    if (lane == 0) ok = tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1u, abort);
+    if (lane == 0) ok = tc::mbar_wait_short(&bars->kv_empty[stage], phase ^ 1u, abort);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
     const CUtensorMap* map = is_v ? tv : tk;
     if (C::SHARED) {
@@ -243,28 +317,23 @@ __device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap
       __syncwarp();
       if (lane < rows / box) {
         const int at = (j * kBK + lane * box) & (page - 1);
+#pragma unroll 1
         for (int c = 0; c < C::kChunks; ++c)
           tc::tma_load_4d(dst + c * C::kChunk + lane * box * 128, map, full, 64 * c, at, u.hk,
                           max(id, 0));
       }
     } else if (lane == 0) {
       tc::mbar_arrive_expect_tx(full, C::kTileBytes);
+#pragma unroll 1
       for (int c = 0; c < C::kChunks; ++c)
         tc::tma_load_3d(dst + c * C::kChunk, map, full, 64 * c, u.hk, u.kbase + j * kBK);
     }
     ++loaded;
-    const int last_keys = u.nk - j * kBK;
-    if (is_v && last_keys < kBK) {
-      ok = tc::mbar_wait(full, phase, abort);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      for (int e = lane; e < (kBK - last_keys) * 8 * C::kChunks; e += 32) {
-        const int c = e / ((kBK - last_keys) * 8), r = e % ((kBK - last_keys) * 8);
-        *reinterpret_cast<uint4*>(dst + c * C::kChunk + last_keys * 128 + r * 16) =
-            make_uint4(0, 0, 0, 0);
-      }
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->v_fixed);
+    if (apart) {
+      fills ^= 1u << stage;
+      to_land |= 1u << stage;
+    } else {
+      to_land &= ~(1u << stage);
     }
     if (++stage == C::NS) {
       stage = 0;
@@ -272,37 +341,16 @@ __device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap
     }
     return true;
   };
-  auto publish = [&]() -> bool {               // u, as the units-th
-    bool ok = true;
-    if (lane == 0) {
-      ok = tc::mbar_wait(&bars->unit_empty[units & 1], ((units >> 1) & 1) ^ 1u, abort);
-      if (ok) {
-        bars->unit[units & 1] = u;
-        tc::mbar_arrive(&bars->unit_full[units & 1]);
-      }
-    }
-    return __shfl_sync(0xffffffffu, ok, 0);
-  };
   bool ok = true;
-  int top = 0x7fffffff;
-  if (!C::SHARED) {
-    int most = 0;
-    for (int b = lane; b < a.B; b += 32) most = max(most, seq_tiles(a, b, blockIdx.x == 0));
-    top = __reduce_max_sync(0xffffffffu, most);
-  }
-  while (ok) {
-    if (!find_unit<C>(a, unit_at(blockIdx.x, units, gridDim.x), top, u)) {
-      u.nt = 0;
-      publish();
-      break;
-    }
-    if (!(ok = publish())) break;
+  while (ok && next_unit(bars, units, lane, u)) {
     if (lane == 0) {
       const int tiles = u.la == 2 ? 1 : u.nt;
-      ok = tc::mbar_wait(&bars->q_empty, (units & 1) ^ 1u, abort);
+      ok = tc::mbar_wait_short(&bars->q_empty, (units & 1) ^ 1u, abort);
       if (ok) {
         tc::mbar_arrive_expect_tx(&bars->q_full, tiles * C::kChunks * 128 * a.G * a.TQ);
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t)
+#pragma unroll 1
           for (int c = 0; c < C::kChunks; ++c)
             tc::tma_load_3d(sq + t * C::kTileBytes + c * C::kChunk, tq, &bars->q_full, 64 * c,
                             u.hk * a.G, u.row0 + t * a.TQ);
@@ -310,30 +358,40 @@ __device__ void producer(const Args& a, const CUtensorMap* tq, const CUtensorMap
     }
     if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
     ++units;
-    for (int e = 0; ok && e < u.la && u.jlo + e <= u.jhi; ++e) ok = load(false, u.jlo + e);
-    for (int j = u.jlo; ok && j <= u.jhi; ++j) {
-      ok = load(true, j);
-      if (ok && j + u.la <= u.jhi) ok = load(false, j + u.la);
+    // K, V by turns: item i is K of block jlo + i for the first la, then V and K alternate
+    const int blocks = u.jhi - u.jlo + 1;
+#pragma unroll 1
+    for (int i = 0, nk = 0, nv = 0; ok && i < 2 * blocks; ++i) {
+      const bool is_k = nk < blocks && nk < nv + u.la;
+      ok = load(!is_k, u.jlo + (is_k ? nk++ : nv++));
     }
   }
   // Every copy this block started lands before the block may exit.
   if (lane == 0) {
     if (units > 0) drain_wait(&bars->q_full, (units - 1) & 1);
+#pragma unroll 1
     for (uint32_t s = 0; s < C::NS && s < loaded; ++s) {
       const uint32_t fill = (loaded - 1 - s) / C::NS;   // the last load into stage s
-      drain_wait(&bars->kv_full[s], fill & 1);
+      if (to_land >> s & 1)
+        drain_wait(&bars->landed[s], (fills >> s & 1) ^ 1u);
+      else
+        drain_wait(&bars->kv_full[s], fill & 1);
     }
   }
   __syncwarp();
 }
 
-// ---------------------------------------------------------------- products (one warp, one lane issues)
-// The tensor pipe takes a product every 64 cycles, so the warp that issues them has to be lean: it
-// stays converged with every operand the same in all lanes (uniform registers), its loops over
-// a block's products are unrolled, and where a wait runs out it goes on (on data that is then
-// without meaning, all of it this block's) to the block's end, where the warp leaves together.
+// ---------------------------------------------------------------- products (a warp per tile, one lane issues)
+// The tensor pipe takes a product every 64 cycles, so the warps that issue them have to be lean:
+// they stay converged with every operand the same in all lanes (uniform registers), the loops
+// over a block's products are unrolled, and where a wait runs out a warp goes on (on data that
+// is then without meaning, all of it this block's) to the block's end, where it leaves together.
+// Both warps walk the whole ring, whether a block is their tile's or not, and take turns: one
+// tile's softmax then runs while the other's products do (left to themselves the tiles fell
+// into step, 3500 cycles a block instead of 2800).
 template <class C>
-__device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv, Bars* bars) {
+__device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv, Bars* bars,
+                         const int t) {
   volatile int* abort = &bars->abort;
   constexpr uint32_t id_s = tc::idesc_f16(kRows, kBK, C::BF16, false);
   constexpr uint32_t id_o = tc::idesc_f16(kRows, C::DP, C::BF16, true);
@@ -341,10 +399,11 @@ __device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv
   const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(skv), 16, 1024);
   // V [keys][dims], dims contiguous: the next 64 dims are a chunk away, the next 8 keys 1024 bytes
   const uint64_t vd = tc::sdesc_sw128(tc::smem_u32(skv), C::kChunk, 1024);
-  uint32_t stage = 0, phase = 0, fixed = 0;
-  uint32_t done[2] = {0, 0}, outputs[2] = {0, 0};   // blocks, and units, of each tile so far
+  const uint32_t s_col = tmem + C::kSCol + t * kBK, o_col = tmem + C::kOCol + t * C::DP;
+  uint32_t stage = 0, phase = 0;
+  uint32_t done = 0, outputs = 0, turns = 0;   // the tile's blocks, units and turns so far
   bool bad = false;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { bad |= !tc::mbar_wait(bar, parity, abort); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { bad |= !tc::mbar_wait_short(bar, parity, abort); };
   auto take = [&]() -> uint32_t {
     wait(&bars->kv_full[stage], phase);
     const uint32_t st = stage;
@@ -356,26 +415,21 @@ __device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv
   };
   for (uint32_t r = 0;; ++r) {
     Unit u;
-    if (!__all_sync(0xffffffffu, next_unit(bars, r, u))) break;
-    if (threadIdx.x % 32 == 0) tc::mbar_arrive(&bars->unit_empty[r & 1]);
-    const int la = __shfl_sync(0xffffffffu, u.la, 0), nk = __shfl_sync(0xffffffffu, u.nk, 0);
+    if (!next_unit(bars, r, threadIdx.x % 32, u)) break;
+    const int la = __shfl_sync(0xffffffffu, u.la, 0);
     const int jlo = __shfl_sync(0xffffffffu, u.jlo, 0), jhi = __shfl_sync(0xffffffffu, u.jhi, 0);
-    int lo[2], hi[2];                          // each tile's blocks
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      int l = 0, h = 0;
-      tile_blocks<C>(a, u, t, l, h);
-      lo[t] = __shfl_sync(0xffffffffu, l, 0);
-      hi[t] = __shfl_sync(0xffffffffu, h, 0);
-    }
-    auto active = [&](int t, int j) { return j >= lo[t] && j <= hi[t] && (la == 1 || ((j - jlo) & 1) == t); };
-    auto scores = [&](int t, uint32_t st) {
-      const uint64_t q = qd + ((la == 2 ? 0 : t) * C::kTileBytes >> 4);
+    int lo = 0, hi = 0;                        // the tile's blocks
+    tile_blocks<C>(a, u, t, lo, hi);
+    lo = __shfl_sync(0xffffffffu, lo, 0);
+    hi = __shfl_sync(0xffffffffu, hi, 0);
+    auto active = [&](int j) { return j >= lo && j <= hi && (la == 1 || ((j - jlo) & 1) == t); };
+    const uint64_t q = qd + ((la == 2 ? 0 : t) * C::kTileBytes >> 4);
+    auto scores = [&](uint32_t st) {
       const uint64_t k = kd + (st * C::kTileBytes >> 4);
 #pragma unroll
       for (int s = 0; s < C::DP / 16; ++s) {
         const uint32_t off = ((s >> 2) * C::kChunk + (s & 3) * 32) >> 4;
-        tc::mma_f16_ss(tmem + C::kSCol + t * kBK, q + off, k + off, id_s, s > 0);
+        tc::mma_f16_ss(s_col, q + off, k + off, id_s, s > 0);
       }
       tc::mma_commit_warp(&bars->s_full[t]);
     };
@@ -383,219 +437,303 @@ __device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv
     for (int e = 0; e < la && jlo + e <= jhi; ++e) {
       const uint32_t st = take();
       tc::fence_after_sync();
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (active(t, jlo + e)) scores(t, st);
+      if (active(jlo + e)) scores(st);
       tc::mma_commit_warp(&bars->kv_empty[st]);
     }
     if (jlo + la > jhi) tc::mma_commit_warp(&bars->q_empty);
-    for (int j = jlo; j <= jhi; ++j) {
+    for (int j = jlo; j <= jhi; ++j, ++turns) {
       const uint32_t vs = take();
-      const bool next = j + la <= jhi;
+      const bool next = j + la <= jhi, mine = active(j), first = la == 2 ? j - jlo == t : j == lo;
       uint32_t ks = 0;
       if (next) ks = take();
-      if (nk - j * kBK < kBK) wait(&bars->v_fixed, fixed++ & 1);
-      const uint64_t v = vd + (vs * C::kTileBytes >> 4);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (active(t, j)) {
-          const bool first = la == 2 ? j - jlo == t : j == lo[t];
-          if (first) {
-            if (outputs[t] > 0) wait(&bars->o_free[t], (outputs[t] - 1) & 1);
-            ++outputs[t];
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wait(&bars->p_ready[t][h], done[t] & 1);
-            tc::fence_after_sync();
-#pragma unroll
-            for (int s = 4 * h; s < 4 * h + 4; ++s)
-              tc::mma_f16_ts(tmem + C::kOCol + t * C::DP, tmem + C::kSCol + t * kBK + 8 * s,
-                             v + (s * 2048 >> 4), id_o, (!first || s > 0) ? 1u : 0u);
-            if (h == 0) tc::mma_commit_warp(&bars->o_half[t]);
-          }
-          tc::mma_commit_warp(&bars->o_done[t]);
-          ++done[t];
+      if (mine) {
+        if (first) {
+          if (outputs > 0) wait(&bars->o_free[t], (outputs - 1) & 1);
+          ++outputs;
         }
-        if (next && active(t, j + la)) scores(t, ks);
+        wait(&bars->p_ready[t], done & 1);
+        ++done;
+      }
+      // In turn: tile 0's products of this block, then tile 1's, then tile 0's of the next.
+      if (t == 1 || turns > 0) wait(&bars->turn[t], (turns - 1 + t) & 1);
+      tc::fence_after_sync();
+      if (mine) {
+        const uint64_t v = vd + (vs * C::kTileBytes >> 4);
+        // (Leaving out the steps of 16 keys that no row of the tile sees, at a tile's last
+        // block, made these branches of and the whole kernel 9% slower.)
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          tc::mma_f16_ts(o_col, s_col + 8 * s, v + (s * 2048 >> 4), id_o,
+                         (!first || s > 0) ? 1u : 0u);
+        tc::mma_commit_warp(&bars->o_done[t]);
+        if (j + la > hi) tc::mma_commit_warp(&bars->o_final[t]);
       }
       tc::mma_commit_warp(&bars->kv_empty[vs]);
-      if (next) tc::mma_commit_warp(&bars->kv_empty[ks]);
+      if (next) {
+        if (active(j + la)) scores(ks);
+        tc::mma_commit_warp(&bars->kv_empty[ks]);
+      }
+      if (threadIdx.x % 32 == 0) tc::mbar_arrive(&bars->turn[1 - t]);
+      __syncwarp();
       if (j + la == jhi) tc::mma_commit_warp(&bars->q_empty);   // the unit's last S
       if (__any_sync(0xffffffffu, bad)) break;
     }
     if (__any_sync(0xffffffffu, bad)) break;
   }
-  tc::mma_commit_warp(&bars->drain);           // nothing may still run when the block frees its TMEM
-  drain_wait(&bars->drain, 0);
+  tc::mma_commit_warp(&bars->drain[t]);        // nothing may still run when the block frees its TMEM
+  drain_wait(&bars->drain[t], 0);
 }
 
 // ---------------------------------------------------------------- softmax (4 warps a tile)
+// 2^(s cs - m) of N scores, packed to 16 bits; returns their sum.
+template <class T, int N>
+__device__ __forceinline__ float exp_pack(const float* s, float cs, float m, uint32_t* p) {
+  const uint64_t c2 = tc::pack2(cs, cs), m2 = tc::pack2(-m, -m);
+  uint64_t acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = tc::pack2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    float x0, x1;
+    tc::unpack2(tc::fma2(tc::pack2(s[c], s[c + 1]), c2, m2), x0, x1);
+    x0 = tc::ex2(x0);
+    x1 = tc::ex2(x1);
+    p[c / 2] = Pair<T>::pack(x0, x1);
+    acc[(c / 2) % 4] = tc::add2(acc[(c / 2) % 4], tc::pack2(x0, x1));
+  }
+  float a0, a1;
+  tc::unpack2(tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3])), a0, a1);
+  return a0 + a1;
+}
+
+// The n lowest bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+}
+
+// Only a block's common path is unrolled; what is rare (masks, softcap, a new reference) works on
+// 32 columns at a time in rolled loops, on S in tensor memory: the roles' loops together have
+// to stay in the instruction caches (with all paths unrolled the kernel took 1.2 times as long).
 template <class C>
-__device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, Bars* bars, int t, int quarter,
-                        int lane, uint32_t& n) {
+__device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sums, Bars* bars, int t,
+                        int quarter, int lane, uint32_t& n, uint32_t& outputs) {
   using T = typename C::T;
   volatile int* abort = &bars->abort;
   const uint32_t n0 = n;                       // this tile's blocks before this unit
-  const int row = quarter * 32 + lane, tok = row / a.G, head = u.hk * a.G + row % a.G;
+  const int row = quarter * 32 + lane, tok = row * a.inv_G >> 16;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const int tile = C::SHARED && u.la == 2 ? 0 : t;
   const int local = tile * a.TQ + tok;         // token of the unit
   const bool live = tok < a.TQ && local < u.ntok;
   const int qpos = u.q0 + local;
   const float cs = a.softcap_on ? 1.0f : a.c_score;
-  constexpr float kLimit = C::BF16 ? 256.0f : 32768.0f;   // 2^(8 + kBias)
+  constexpr float kLimit = 32768.0f;           // no weight can then be past fp16's range
   float m_ref = -INFINITY, l = 0.f;            // P = 2^(score - m_ref) with the bias inside m_ref
   // The warp's rows' first and last visible keys are ordered as their tokens are.
-  const int tok0 = 32 * quarter / a.G, tok1 = min((32 * quarter + 31) / a.G, a.TQ - 1);
+  const int tok0 = 32 * quarter * a.inv_G >> 16;
+  const int tok1 = min(static_cast<int>((32 * quarter + 31) * a.inv_G >> 16), a.TQ - 1);
   const int q_lo = u.q0 + tile * a.TQ + tok0, q_hi = u.q0 + tile * a.TQ + tok1;
+  const int tile_keys = C::SHARED ? u.nk : u.q0 + min((t + 1) * a.TQ, u.ntok);
   int j_lo, j_hi;
   tile_blocks<C>(a, u, t, j_lo, j_hi);
   bool ok = true, started = false;             // started: every live row has a reference
+  const uint32_t scol = lane_base + C::kSCol + t * kBK;
   for (int j = u.la == 2 ? j_lo + t : j_lo; j <= j_hi; j += u.la) {
-    ok = tc::mbar_wait(&bars->s_full[t], n & 1, abort);
-    if (__any_sync(0xffffffffu, !ok)) {        // leave together: tcgen05.ld is warp-wide
-      ok = false;
-      break;
-    }
+    ok = tc::mbar_wait_short(&bars->s_full[t], n & 1, abort);
+    if (!__all_sync(0xffffffffu, ok)) return false;   // together: tcgen05.ld is warp-wide
     tc::fence_after_sync();
-    const uint32_t scol = lane_base + C::kSCol + t * kBK;
-    float s[128];
-    tc::tmem_ld128(scol, s);
     const int k0 = j * kBK;
-    if (a.softcap_on) {
-#pragma unroll
-      for (int c = 0; c < 128; ++c) {
-        const float e = tc::ex2(s[c] * a.c_cap_in);
-        s[c] = fmaf(-2.0f * a.c_cap_out, tc::rcp(e + 1.0f), a.c_cap_out);
-      }
-    }
     // Blocks that the mask crosses: keys c <= hi and c >= lo are visible.
-    if (k0 + kBK > u.nk || (!C::SHARED && (k0 + kBK - 1 > q_lo ||
-                                           (a.window > 0 && k0 < q_hi - a.window + 1)))) {
-      const int hi = (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;
-      const int lo = !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : 0;
-#pragma unroll
-      for (int c = 0; c < 128; ++c) s[c] = c > hi || c < lo ? -INFINITY : s[c];
-    }
-    // P in two halves of 64 columns, each released to the products as soon as it is written.
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      uint32_t p[32];
-      float lsum;
-      bool slow = !started;
+    const bool edge = k0 + kBK > u.nk ||
+                      (!C::SHARED && (k0 + kBK - 1 > q_lo ||
+                                      (a.window > 0 && k0 < q_hi - a.window + 1)));
+    // Chunks of 32 columns from `chunks` on hold no key of the tile.
+    const int chunks = min(4, (tile_keys - k0 + 31) / 32);
+    if (edge || a.softcap_on) {
+      const int hi = !edge ? kBK : (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;
+      const int lo = edge && !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : 0;
 #pragma unroll 1
-      while (true) {
-        if (slow) {                            // a new reference from this half's maximum
-          const float m_new = fmaxf(m_ref, fmaf(prefill::tq_max<64>(s + 64 * hh), cs, -C::kBias));
-          const bool grow = m_ref != -INFINITY && m_new - m_ref > kRescaleLog2;
-          if (__any_sync(0xffffffffu, grow)) {
-            if (n > n0 || hh > 0) {            // once every product that wrote O is done
-              ok = hh == 0 ? tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort)
-                           : tc::mbar_wait(&bars->o_half[t], n & 1, abort);
-              if (__any_sync(0xffffffffu, !ok)) {
-                ok = false;
-                break;
-              }
-              tc::fence_after_sync();
-              const float f = grow ? tc::ex2(m_ref - m_new) : 1.0f;
-#pragma unroll 1
-              for (int c = 0; c < C::DP; c += 16) {
-                float o[16];
-                tc::tmem_ld16(lane_base + C::kOCol + t * C::DP + c, o);
+      for (int i = 0; i < chunks; ++i) {
+        float x[32];
+        tc::tmem_ld32(scol + 32 * i, x);
+        if (a.softcap_on) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= f;
-                tc::tmem_st16(lane_base + C::kOCol + t * C::DP + c, o);
-              }
-              l *= f;
-            }
-            if (grow) m_ref = m_new;
+          for (int c = 0; c < 32; ++c) {
+            const float e = tc::ex2(x[c] * a.c_cap_in);
+            x[c] = fmaf(-2.0f * a.c_cap_out, tc::rcp(e + 1.0f), a.c_cap_out);
           }
-          if (m_ref == -INFINITY) m_ref = m_new;
         }
-        // -inf only while every key so far was masked; then every score is -inf
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t c2 = tc::pack2(cs, cs), m2 = tc::pack2(-m_use, -m_use);
-        uint64_t acc[4];
+        const uint32_t seen = bits_below(hi + 1 - 32 * i) & ~bits_below(lo - 32 * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = tc::pack2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float x0, x1;
-          tc::unpack2(tc::fma2(tc::pack2(s[64 * hh + c], s[64 * hh + c + 1]), c2, m2), x0, x1);
-          x0 = tc::ex2(x0);
-          x1 = tc::ex2(x1);
-          p[c / 2] = Pair<T>::pack(x0, x1);
-          acc[(c / 2) % 4] = tc::add2(acc[(c / 2) % 4], tc::pack2(x0, x1));
-        }
-        float a0, a1;
-        tc::unpack2(tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3])), a0, a1);
-        lsum = a0 + a1;
-        if (slow || !__any_sync(0xffffffffu, live && !(lsum <= kLimit))) break;
-        slow = true;
+        for (int c = 0; c < 32; ++c) x[c] = seen >> c & 1 ? x[c] : -INFINITY;
+        tc::tmem_st32(scol + 32 * i, x);
       }
-      if (!ok) break;
-      l += lsum;
-      tc::tmem_st32(scol + 32 * hh, reinterpret_cast<const float*>(p));
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->p_ready[t][hh]);
-      if (!started && hh == 1) started = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
     }
-    if (!ok) break;
-    ++n;
-  }
-  if (!ok) return false;
-
-  const bool has = n > n0;                     // the tile had blocks: its O waits to be read
-  if (has) {
-    ok = tc::mbar_wait(&bars->o_done[t], (n - 1) & 1, abort);
-    if (__any_sync(0xffffffffu, !ok || *abort)) return false;
-    tc::fence_after_sync();
-  }
-  const bool any = has && m_ref != -INFINITY;
-  const float inv = any ? 1.0f / l : 0.f;
-  if constexpr (C::SHARED) {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.H;
-    const int part = u.la == 2 ? 2 * u.part + t : u.part;
-    if (u.la == 1 && t >= u.nt) return true;
-    const int64_t at = part * rows + static_cast<int64_t>(u.row0 + local) * a.H + head;
-    if (live) a.part_ml[at] = make_float2(any ? m_ref : -INFINITY, any ? l : 0.f);
-#pragma unroll 1
-    for (int c = 0; c < C::DP; c += 32) {
-      float o[32];
-      if (has) tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
-      float* dst = a.part_o + at * a.D + c;
-#pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        if (live && c + e < a.D)
-          *reinterpret_cast<float4*>(dst + e) =
-              any ? make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    bool written = false;
+    if (started && chunks == 4) {
+      float x[128];
+      uint32_t p[64];
+      tc::tmem_ld128(scol, x);
+      float lsum = exp_pack<T, 64>(x, cs, m_ref, p);
+      lsum += exp_pack<T, 64>(x + 64, cs, m_ref, p + 32);
+      written = !__any_sync(0xffffffffu, live && !(lsum <= kLimit));
+      if (written) {
+        l += lsum;
+        tc::tmem_st64(scol, reinterpret_cast<const float*>(p));
+      }
     }
-  } else {
-    if (t >= u.nt) return true;
-    T* dst = static_cast<T*>(a.out) + (u.row0 + local) * a.o_token + head * a.o_head;
+    if (!written) {                            // a new reference from the block's maximum
+      float x[32], top = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < C::DP; c += 32) {
-      float o[32];
-      tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, o);
+      for (int i = 0; i < chunks; ++i) {
+        tc::tmem_ld32(scol + 32 * i, x);
+        top = fmaxf(top, prefill::tq_max<32>(x));
+      }
+      const float m_new = fmaxf(m_ref, fmaf(top, cs, -C::kBias));
+      const bool grow = m_ref != -INFINITY && m_new > m_ref;
+      if (n > n0 && __any_sync(0xffffffffu, grow)) {   // O once every product that wrote it is done
+        ok = tc::mbar_wait_short(&bars->o_done[t], (n - 1) & 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc::fence_after_sync();
+        const float f = grow ? tc::ex2(m_ref - m_new) : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < C::DP; c += 32) {
+          tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, x);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8)
-        if (live && c + e < a.D) {
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = o[e + i] * inv;
-          *reinterpret_cast<uint4*>(dst + c + e) = pack8<T>(x);
+          for (int e = 0; e < 32; ++e) x[e] *= f;
+          tc::tmem_st32(lane_base + C::kOCol + t * C::DP + c, x);
         }
+        l *= f;
+        if (grow) m_ref = m_new;
+      }
+      if (m_ref == -INFINITY) m_ref = m_new;
+      // -inf only while every key so far was masked; then every score is -inf
+      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {            // P's columns lie below those still to be read
+        uint32_t p[16];
+        if (i < chunks) {
+          tc::tmem_ld32(scol + 32 * i, x);
+          l += exp_pack<T, 32>(x, cs, m_use, p);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) p[c] = 0u;
+        }
+        tc::tmem_st16(scol + 16 * i, reinterpret_cast<const float*>(p));
+      }
+      if (!started) started = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
     }
-  }
-  if (has) {
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&bars->o_free[t]);
+    if (lane == 0) tc::mbar_arrive(&bars->p_ready[t]);
+    ++n;
   }
+  if (n == n0) return true;                    // the tile had no blocks
+  // The row's sum and reference for those who bring it out, once they have read the last.
+  if (outputs > 0) {
+    ok = tc::mbar_wait_short(&bars->o_free[t], (outputs - 1) & 1, abort);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+  }
+  ++outputs;
+  sums[t * 128 + row] = make_float2(l, m_ref);
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(&bars->l_ready[t]);
   return true;
+}
+
+// ---------------------------------------------------------------- output rows (4 warps)
+// O / l of a finished tile: 128 bytes of a row at a time through shared memory, so that 8 lanes
+// write them at once (a lane writing its own row touched 32 lines an instruction).
+template <class C>
+__device__ void outputs(const Args& a, uint32_t tmem, uint8_t* stage, const float2* sums, Bars* bars,
+                        int quarter, int lane) {
+  using T = typename C::T;
+  volatile int* abort = &bars->abort;
+  const int row = quarter * 32 + lane, tok = row * a.inv_G >> 16;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  uint4* s = reinterpret_cast<uint4*>(stage);
+  constexpr int kElem = C::SHARED ? 4 : 2;     // bytes of an output value
+  constexpr int kPer = 16 / kElem;             // values in 16 bytes
+  constexpr int kCols = 128 / kElem;           // columns in 128 bytes of a row
+  uint32_t done = 0;                           // bit t: parity of the tile's outputs
+  for (uint32_t r = 0;; ++r) {
+    Unit u;
+    if (!next_unit(bars, r, lane, u)) return;
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+      if (u.la == 1 && t >= u.nt) continue;
+      const bool has = u.la == 1 || u.jlo + t <= u.jhi;   // a split of one block: tile 1 has none
+      float2 ml = make_float2(0.f, -INFINITY);
+      if (has) {
+        bool ok = tc::mbar_wait_short(&bars->l_ready[t], done >> t & 1, abort);
+        ok = ok && tc::mbar_wait_short(&bars->o_final[t], done >> t & 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        done ^= 1u << t;
+        tc::fence_after_sync();
+        ml = sums[t * 128 + row];
+      }
+      const bool any = ml.y != -INFINITY;
+      const float inv = any ? 1.0f / ml.x : 0.f;
+      const int local = (u.la == 2 ? 0 : t * a.TQ) + tok, head = u.hk * a.G + row - tok * a.G;
+      const bool live = tok < a.TQ && local < u.ntok;
+      char* dst = nullptr;                     // the lane's row, where it is one
+      if constexpr (C::SHARED) {
+        const int part = u.la == 2 ? 2 * u.part + t : u.part;
+        const int64_t at = (static_cast<int64_t>(part) * a.B + u.row0 + local) * a.H + head;
+        if (live) {
+          a.part_ml[at] = make_float2(ml.y, any ? ml.x : 0.f);
+          dst = reinterpret_cast<char*>(a.part_o + at * a.D);
+        }
+      } else {
+        if (live)
+          dst = reinterpret_cast<char*>(static_cast<T*>(a.out) + (u.row0 + local) * a.o_token +
+                                        head * a.o_head);
+      }
+      char* rows[8];                           // where the lane's 16 bytes of 8 rows go
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        rows[i] = reinterpret_cast<char*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(dst), 4 * i + lane / 8));
+#pragma unroll 1
+      for (int c = 0; c < C::DP; c += kCols) {
+#pragma unroll 1
+        for (int h = 0; h < kCols; h += 16) {
+          float o[16];
+          if (has) {
+            tc::tmem_ld16(lane_base + C::kOCol + t * C::DP + c + h, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= inv;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16 / kPer; ++e) {
+            uint4 w;
+            if constexpr (C::SHARED)
+              w = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                             __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+            else
+              w = pack8<T>(*reinterpret_cast<float(*)[8]>(o + 8 * e));
+            s[lane * 8 + ((h / kPer + e) ^ (lane & 7))] = w;
+          }
+        }
+        __syncwarp();
+        if (has && c + kCols >= C::DP) {       // O may be written again
+          tc::fence_before_sync();
+          if (lane == 0) tc::mbar_arrive(&bars->o_free[t]);
+        }
+        const int e = lane & 7, byte = c * kElem + 16 * e;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int from = 4 * i + lane / 8;
+          const uint4 x = s[from * 8 + (e ^ (from & 7))];
+          if (rows[i] && byte < kElem * a.D) *reinterpret_cast<uint4*>(rows[i] + byte) = x;
+        }
+        __syncwarp();
+      }
+    }
+  }
 }
 
 template <class C>
@@ -608,7 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   uint8_t* skv = sq + 2 * C::kTileBytes;
-  Bars* bars = reinterpret_cast<Bars*>(skv + C::NS * C::kTileBytes);
+  uint8_t* sout = skv + C::NS * C::kTileBytes;
+  Bars* bars = reinterpret_cast<Bars*>(sout + C::kOut);
+  float2* sums = reinterpret_cast<float2*>(sout + C::kOut + 1024);
   static_assert(sizeof(Bars) <= 1024, "barriers fit behind the ring");
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   if (warp == 9) {
@@ -616,24 +756,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      tc::mbar_init(&bars->unit_full[i], 1);
+      tc::mbar_init(&bars->unit_empty[i], kReaders);
+    }
     tc::mbar_init(&bars->q_full, 1);
-    tc::mbar_init(&bars->q_empty, 1);
+    tc::mbar_init(&bars->q_empty, 2);
     for (int s = 0; s < C::NS; ++s) {
       tc::mbar_init(&bars->kv_full[s], 1);
-      tc::mbar_init(&bars->kv_empty[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 2);
+      tc::mbar_init(&bars->landed[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(&bars->s_full[t], 1);
-      tc::mbar_init(&bars->p_ready[t][0], 4);
-      tc::mbar_init(&bars->p_ready[t][1], 4);
-      tc::mbar_init(&bars->o_half[t], 1);
+      tc::mbar_init(&bars->p_ready[t], 4);
+      tc::mbar_init(&bars->turn[t], 1);
       tc::mbar_init(&bars->o_done[t], 1);
+      tc::mbar_init(&bars->l_ready[t], 4);
+      tc::mbar_init(&bars->o_final[t], 1);
       tc::mbar_init(&bars->o_free[t], 4);
-      tc::mbar_init(&bars->unit_full[t], 1);
-      tc::mbar_init(&bars->unit_empty[t], 9);
+      tc::mbar_init(&bars->drain[t], 1);
     }
-    tc::mbar_init(&bars->v_fixed, 1);
-    tc::mbar_init(&bars->drain, 1);
     bars->abort = 0;
     tc::fence_mbar_init();
   }
@@ -644,20 +787,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
-      producer<C>(a, &tm_q, &tm_k, &tm_v, sq, skv, bars, lane);
-    } else if (warp == 9) {
-      products<C>(a, tmem, sq, skv, bars);
+      loads<C>(a, &tm_q, &tm_k, &tm_v, sq, skv, bars, lane);
+    } else if (warp <= 10) {
+      products<C>(a, tmem, sq, skv, bars, warp - 9);
+    } else if (warp == 11) {
+      scheduler<C>(a, skv, bars, lane);
+    } else {
+      outputs<C>(a, tmem, sout + (warp - 12) * 4096, sums, bars, warp - 12, lane);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    uint32_t n = 0;
-    for (uint32_t r = 0;; ++r) {
-      Unit u;
-      const bool any = next_unit(bars, r, u);
-      if (!__all_sync(0xffffffffu, any)) break;    // every lane has read it
-      if (lane == 0) tc::mbar_arrive(&bars->unit_empty[r & 1]);
-      if (!softmax<C>(a, u, tmem, bars, warp / 4, warp % 4, lane, n)) break;
-    }
+    uint32_t n = 0, outs = 0;
+    Unit u;
+    for (uint32_t r = 0; next_unit(bars, r, lane, u); ++r)
+      if (!softmax<C>(a, u, tmem, sums, bars, warp / 4, warp % 4, lane, n, outs)) break;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -717,6 +860,8 @@ cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
   a.prefix_table = j.prefix_table; a.prefix_len = j.prefix_len;
   a.pages = j.cache.pages; a.page_shift = j.cache.page_shift;
   a.H = j.H; a.Hkv = j.Hkv; a.D = j.D; a.G = j.H / j.Hkv; a.TQ = kRows / a.G;
+  a.inv_tokens = ~0ull / (2 * a.TQ) + 1;
+  a.inv_G = 65536 / a.G + 1;
   a.window = j.window;
   a.softcap_on = j.softcap > 0.f;
   a.c_score = j.scale * kLog2e16;

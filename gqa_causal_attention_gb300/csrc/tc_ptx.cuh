@@ -87,6 +87,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same in the least code, for kernels whose many roles share the instruction caches.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity,
+                                                volatile int* abort) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
+}
+
 // After a wait that ran out: gives the copies already issued on this phase of `bar` as long
 // again to land. A block must not end before that: its shared memory may go to another block.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
