@@ -79,7 +79,7 @@ struct Cfg {
   static constexpr int kChunks = DP / 64;
   static constexpr int kChunk = 128 * 128;     // 128 rows x 64 dims (128 bytes)
   static constexpr int kTileBytes = kChunks * kChunk;   // a Q tile, a K block or a V block
-  static constexpr int kOut = 4 * 4096;        // 4 KB a warp: output rows on their way out
+  static constexpr int kOut = 16384;           // output rows on their way out (a share per warp)
   static constexpr int kNSraw = (kSmemLimit - 2048 - kSums - kOut - 2 * kTileBytes) / kTileBytes;
   static constexpr int NS = kNSraw > 8 ? 8 : kNSraw;
   static constexpr int kSmem = (NS + 2) * kTileBytes + kOut + kSums + 2048;
@@ -94,7 +94,6 @@ constexpr int kThreads = 512;
 constexpr int kRegsSoftmax = 184, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "the block's registers");
 constexpr int kUnits = 4;                      // units ahead
-constexpr int kReaders = 15;                   // warps that read each unit
 
 struct Bars {
   uint64_t unit_full[kUnits], unit_empty[kUnits];
@@ -506,6 +505,65 @@ __device__ __forceinline__ float exp_pack(const float* s, float cs, float m, uin
   return a0 + a1;
 }
 
+// A shared prefix: the softmax warps bring their rows out themselves (a block has one unit, as a rule,
+// and eight warps are faster than four): O / l in fp32, 64 bytes of a row at a time through
+// shared memory, with the row's reference and sum.
+template <class C>
+__device__ bool partial_rows(const Args& a, const Unit& u, uint32_t tmem, uint8_t* stage, Bars* bars,
+                             int t, int quarter, int lane, bool has, uint32_t n, float l, float m_ref) {
+  if (u.la == 1 && t >= u.nt) return true;
+  if (has) {
+    const bool ok = tc::mbar_wait_short(&bars->o_done[t], (n - 1) & 1, &bars->abort);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc::fence_after_sync();
+  }
+  const int row = quarter * 32 + lane, tok = row * a.inv_G >> 16;
+  const int local = (u.la == 2 ? 0 : t * a.TQ) + tok, head = u.hk * a.G + row - tok * a.G;
+  const int part = u.la == 2 ? 2 * u.part + t : u.part;
+  const int64_t at = (static_cast<int64_t>(part) * a.B + u.row0 + local) * a.H + head;
+  float* dst = nullptr;
+  if (tok < a.TQ && local < u.ntok) {
+    a.part_ml[at] = make_float2(m_ref, l);     // (-inf, 0) for a split without blocks
+    dst = a.part_o + at * a.D;
+  }
+  float* rows[4];                              // where the lane's 16 bytes of 4 rows go
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    rows[i] = reinterpret_cast<float*>(__shfl_sync(
+        0xffffffffu, reinterpret_cast<unsigned long long>(dst), 8 * i + lane / 4));
+  const float inv = has && m_ref != -INFINITY ? 1.0f / l : 0.f;
+  const uint32_t col = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + C::kOCol + t * C::DP;
+  float4* s = reinterpret_cast<float4*>(stage);
+#pragma unroll 1
+  for (int c = 0; c < C::DP; c += 16) {
+    float o[16];
+    if (has) {
+      tc::tmem_ld16(col + c, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s[lane * 4 + (e ^ (lane >> 1 & 3))] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv,
+                                                        o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+    __syncwarp();
+    const int e = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int from = 8 * i + lane / 4;
+      const float4 x = s[from * 4 + (e ^ (from >> 1 & 3))];
+      if (rows[i] && c + 4 * e < a.D) *reinterpret_cast<float4*>(rows[i] + c + 4 * e) = x;
+    }
+    __syncwarp();
+  }
+  if (has) {
+    tc::fence_before_sync();
+    if (lane == 0) tc::mbar_arrive(&bars->o_free[t]);
+  }
+  return true;
+}
+
 // The n lowest bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
@@ -515,8 +573,8 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 // 32 columns at a time in rolled loops, on S in tensor memory: the roles' loops together have
 // to stay in the instruction caches (with all paths unrolled the kernel took 1.2 times as long).
 template <class C>
-__device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sums, Bars* bars, int t,
-                        int quarter, int lane, uint32_t& n, uint32_t& outputs) {
+__device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sums, uint8_t* stage,
+                        Bars* bars, int t, int quarter, int lane, uint32_t& n, uint32_t& outputs) {
   using T = typename C::T;
   volatile int* abort = &bars->abort;
   const uint32_t n0 = n;                       // this tile's blocks before this unit
@@ -628,6 +686,8 @@ __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sum
     if (lane == 0) tc::mbar_arrive(&bars->p_ready[t]);
     ++n;
   }
+  if constexpr (C::SHARED)
+    return partial_rows<C>(a, u, tmem, stage, bars, t, quarter, lane, n > n0, n, l, m_ref);
   if (n == n0) return true;                    // the tile had no blocks
   // The row's sum and reference for those who bring it out, once they have read the last.
   if (outputs > 0) {
@@ -652,83 +712,52 @@ __device__ void outputs(const Args& a, uint32_t tmem, uint8_t* stage, const floa
   const int row = quarter * 32 + lane, tok = row * a.inv_G >> 16;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   uint4* s = reinterpret_cast<uint4*>(stage);
-  constexpr int kElem = C::SHARED ? 4 : 2;     // bytes of an output value
-  constexpr int kPer = 16 / kElem;             // values in 16 bytes
-  constexpr int kCols = 128 / kElem;           // columns in 128 bytes of a row
   uint32_t done = 0;                           // bit t: parity of the tile's outputs
   for (uint32_t r = 0;; ++r) {
     Unit u;
     if (!next_unit(bars, r, lane, u)) return;
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-      if (u.la == 1 && t >= u.nt) continue;
-      const bool has = u.la == 1 || u.jlo + t <= u.jhi;   // a split of one block: tile 1 has none
-      float2 ml = make_float2(0.f, -INFINITY);
-      if (has) {
-        bool ok = tc::mbar_wait_short(&bars->l_ready[t], done >> t & 1, abort);
-        ok = ok && tc::mbar_wait_short(&bars->o_final[t], done >> t & 1, abort);
-        if (!__all_sync(0xffffffffu, ok)) return;
-        done ^= 1u << t;
-        tc::fence_after_sync();
-        ml = sums[t * 128 + row];
-      }
-      const bool any = ml.y != -INFINITY;
-      const float inv = any ? 1.0f / ml.x : 0.f;
-      const int local = (u.la == 2 ? 0 : t * a.TQ) + tok, head = u.hk * a.G + row - tok * a.G;
-      const bool live = tok < a.TQ && local < u.ntok;
+    for (int t = 0; t < u.nt; ++t) {
+      bool ok = tc::mbar_wait_short(&bars->l_ready[t], done >> t & 1, abort);
+      ok = ok && tc::mbar_wait_short(&bars->o_final[t], done >> t & 1, abort);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      done ^= 1u << t;
+      tc::fence_after_sync();
+      const float inv = 1.0f / sums[t * 128 + row].x;   // every live row sees itself
+      const int local = t * a.TQ + tok, head = u.hk * a.G + row - tok * a.G;
       char* dst = nullptr;                     // the lane's row, where it is one
-      if constexpr (C::SHARED) {
-        const int part = u.la == 2 ? 2 * u.part + t : u.part;
-        const int64_t at = (static_cast<int64_t>(part) * a.B + u.row0 + local) * a.H + head;
-        if (live) {
-          a.part_ml[at] = make_float2(ml.y, any ? ml.x : 0.f);
-          dst = reinterpret_cast<char*>(a.part_o + at * a.D);
-        }
-      } else {
-        if (live)
-          dst = reinterpret_cast<char*>(static_cast<T*>(a.out) + (u.row0 + local) * a.o_token +
-                                        head * a.o_head);
-      }
+      if (tok < a.TQ && local < u.ntok)
+        dst = reinterpret_cast<char*>(static_cast<T*>(a.out) + (u.row0 + local) * a.o_token +
+                                      head * a.o_head);
       char* rows[8];                           // where the lane's 16 bytes of 8 rows go
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         rows[i] = reinterpret_cast<char*>(__shfl_sync(
             0xffffffffu, reinterpret_cast<unsigned long long>(dst), 4 * i + lane / 8));
 #pragma unroll 1
-      for (int c = 0; c < C::DP; c += kCols) {
+      for (int c = 0; c < C::DP; c += 64) {
 #pragma unroll 1
-        for (int h = 0; h < kCols; h += 16) {
+        for (int h = 0; h < 64; h += 16) {
           float o[16];
-          if (has) {
-            tc::tmem_ld16(lane_base + C::kOCol + t * C::DP + c + h, o);
+          tc::tmem_ld16(lane_base + C::kOCol + t * C::DP + c + h, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= inv;
-          } else {
+          for (int e = 0; e < 16; ++e) o[e] *= inv;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 16 / kPer; ++e) {
-            uint4 w;
-            if constexpr (C::SHARED)
-              w = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                             __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
-            else
-              w = pack8<T>(*reinterpret_cast<float(*)[8]>(o + 8 * e));
-            s[lane * 8 + ((h / kPer + e) ^ (lane & 7))] = w;
-          }
+          for (int e = 0; e < 2; ++e)
+            s[lane * 8 + ((h / 8 + e) ^ (lane & 7))] =
+                pack8<T>(*reinterpret_cast<float(*)[8]>(o + 8 * e));
         }
         __syncwarp();
-        if (has && c + kCols >= C::DP) {       // O may be written again
+        if (c + 64 >= C::DP) {                 // O may be written again
           tc::fence_before_sync();
           if (lane == 0) tc::mbar_arrive(&bars->o_free[t]);
         }
-        const int e = lane & 7, byte = c * kElem + 16 * e;
+        const int e = lane & 7;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int from = 4 * i + lane / 8;
           const uint4 x = s[from * 8 + (e ^ (from & 7))];
-          if (rows[i] && byte < kElem * a.D) *reinterpret_cast<uint4*>(rows[i] + byte) = x;
+          if (rows[i] && c + 8 * e < a.D) *reinterpret_cast<uint4*>(rows[i] + 2 * c + 16 * e) = x;
         }
         __syncwarp();
       }
@@ -758,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
       tc::mbar_init(&bars->unit_full[i], 1);
-      tc::mbar_init(&bars->unit_empty[i], kReaders);
+      tc::mbar_init(&bars->unit_empty[i], C::SHARED ? 11 : 15);   // warps that read it
     }
     tc::mbar_init(&bars->q_full, 1);
     tc::mbar_init(&bars->q_empty, 2);
@@ -793,14 +822,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 11) {
       scheduler<C>(a, skv, bars, lane);
     } else {
-      outputs<C>(a, tmem, sout + (warp - 12) * 4096, sums, bars, warp - 12, lane);
+      if (!C::SHARED) outputs<C>(a, tmem, sout + (warp - 12) * 4096, sums, bars, warp - 12, lane);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     uint32_t n = 0, outs = 0;
     Unit u;
     for (uint32_t r = 0; next_unit(bars, r, lane, u); ++r)
-      if (!softmax<C>(a, u, tmem, sums, bars, warp / 4, warp % 4, lane, n, outs)) break;
+      if (!softmax<C>(a, u, tmem, sums, sout + warp * 2048, bars, warp / 4, warp % 4, lane, n, outs))
+        break;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -874,8 +904,9 @@ cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
   int64_t grid;                                // units at most: no more blocks than SMs
   CUtensorMap tq, tk, tv;
   if (C::SHARED) {
-    a.split_keys = a.B <= a.TQ;
-    a.splits = shared_prefix_splits(a.B, a.H, a.Hkv, a.prefix_len) / (a.split_keys ? 2 : 1);
+    const PrefixPlan plan = shared_prefix_plan(a.B, a.H, a.Hkv, a.prefix_len);
+    a.split_keys = plan.split_keys;
+    a.splits = plan.splits;
     a.units = (a.B + tokens - 1) / tokens;
     grid = static_cast<int64_t>(a.Hkv) * a.units * a.splits;
     if (!map_rows(&tq, j.q, j.bf16, a.D, a.H, a.B, a.G, a.TQ) ||

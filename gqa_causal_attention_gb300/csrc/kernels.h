@@ -507,15 +507,22 @@ struct DecodePagedJob {
   int B, H, Hkv, D;
   int window;
   float softcap, scale;
-  PrefixParts prefix;
+  const int32_t* prefix_table;     // positions before each row's own, read from these pages
+  int prefix_len;                  // (0: none)
+  PrefixParts prefix;              // or their partial results; then the rows' own results go to
+  float* own_o;                    // own_o [B * H][D] and own_ml [B * H] before they are joined
+  float2* own_ml;
   float* partial;                  // workspace
-  int blocks;                      // 0: one block per row and head group
   int32_t* status;
   const int32_t* skip;
 };
-// The blocks a call runs (0: one per row and head group) and the workspace it takes.
-int decode_paged_blocks(int B, int H, int Hkv, int max_len, int window);
-size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window);
+// How a call is split (blocks 0: one block of `warps` warps per row and group of 8 query heads)
+// and the workspace it takes.
+struct DecodePagedPlan {
+  int blocks, warps;
+};
+DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int max_len, int window, int prefix_len);
+size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window, int prefix_len);
 cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream);
 
 // Attention on the tensor cores in 16 bits: packed prompts (cu != nullptr), or B rows of one
@@ -536,8 +543,14 @@ struct Attn16Job {
   int32_t* status;
   const int32_t* skip;
 };
-// Splits of a shared prefix (the partial results per row).
-int shared_prefix_splits(int B, int H, int Hkv, int prefix_len);
+// Splits of a shared prefix (the partial results per row); split_keys: a block's two halves take
+// every other key block of one tile of rows.
+struct PrefixPlan {
+  int splits;                      // of the key blocks
+  bool split_keys;
+  int parts() const { return split_keys ? 2 * splits : splits; }
+};
+PrefixPlan shared_prefix_plan(int B, int H, int Hkv, int prefix_len);
 cudaError_t launch_attn16_bf16(const Attn16Job& j, cudaStream_t stream);
 cudaError_t launch_attn16_fp16(const Attn16Job& j, cudaStream_t stream);
 

@@ -77,18 +77,28 @@ bool rope_ok(const attn_rope_params* rp, int D) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace of a shared-prefix call: partial outputs, their weights, then the decode's own.
+// Workspace of a shared-prefix call: the prefix's partial outputs and their weights, the rows' own,
+// then the decode's. `parts` 0: the prefix is read with each row's own positions, which costs
+// less than the two kernels more where all rows together read at most kRereadBytes of it, mostly
+// from L2.
+constexpr int64_t kRereadBytes = 64 << 20;
 struct SharedLayout {
-  size_t ml, own, total;
-  int splits;
+  size_t ml, own_o, own_ml, decode, total;
+  int parts;
 };
 SharedLayout shared_layout(int B, int H, int Hkv, int D, int prefix_len, int max_len) {
   SharedLayout y{};
-  y.splits = gqa::shared_prefix_splits(B, H, Hkv, prefix_len);
-  const size_t rows = static_cast<size_t>(B) * H * y.splits;
-  y.ml = align256(rows * D * sizeof(float));
-  y.own = y.ml + align256(rows * 2 * sizeof(float));
-  y.total = y.own + gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0);
+  if (static_cast<int64_t>(B) * prefix_len * Hkv * D * 4 <= kRereadBytes) {
+    y.total = gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, prefix_len);
+    return y;
+  }
+  y.parts = gqa::shared_prefix_plan(B, H, Hkv, prefix_len).parts();
+  const size_t rows = static_cast<size_t>(B) * H;
+  y.ml = align256(rows * y.parts * D * sizeof(float));
+  y.own_o = y.ml + align256(rows * y.parts * 2 * sizeof(float));
+  y.own_ml = y.own_o + align256(rows * D * sizeof(float));
+  y.decode = y.own_ml + align256(rows * 2 * sizeof(float));
+  y.total = y.decode + gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, 0);
   return y;
 }
 
@@ -127,7 +137,6 @@ int decode_checks(const DecodeCall& c, gqa::DecodePagedJob* j) {
   j->window = c.window;
   j->softcap = c.softcap;
   j->scale = scale_of(c.scale, c.D);
-  j->blocks = gqa::decode_paged_blocks(c.B, c.H, c.Hkv, c.max_cache_len, c.window);
   return ATTN_OK;
 }
 
@@ -201,7 +210,7 @@ int kv_cache_append_paged(int type, const attn_rows* q, const attn_rows* q_out, 
 size_t gqa_attn_decode_paged_workspace_size(int B, int H, int Hkv, int D, int32_t max_cache_len,
                                             int window) {
   if (!heads_ok(H, Hkv, D) || B < 1 || max_cache_len < 0 || window < 0) return 0;
-  return gqa::decode_paged_bytes(B, H, Hkv, D, max_cache_len, window);
+  return gqa::decode_paged_bytes(B, H, Hkv, D, max_cache_len, window, 0);
 }
 
 int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cache,
@@ -214,7 +223,7 @@ int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cac
                      B, H, Hkv, D, window, softcap, scale};
   if (int rc = decode_checks(c, &j)) return rc;
   if (B == 0) return ATTN_OK;
-  const size_t need = gqa::decode_paged_bytes(B, H, Hkv, D, max_cache_len, window);
+  const size_t need = gqa::decode_paged_bytes(B, H, Hkv, D, max_cache_len, window, 0);
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   if (need && !aligned16(workspace)) return ATTN_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -247,14 +256,21 @@ int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* ca
   if (prefix_len > (static_cast<int64_t>(prefix_width) << j.cache.page_shift))
     return ATTN_ERR_CAPACITY;
   const SharedLayout y = shared_layout(B, H, Hkv, D, prefix_len, max_cache_len);
-  if (!workspace || workspace_bytes < y.total) return ATTN_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+  if (y.total && (!workspace || workspace_bytes < y.total)) return ATTN_ERR_WORKSPACE;
+  if (y.total && !aligned16(workspace)) return ATTN_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(workspace);
   gqa::Finite16Job f = finite_job(j);
   gqa::Finite16Pages& p = f.pages[1];
   p.table = prefix_table; p.width = prefix_width; p.B = 1; p.fixed_len = p.max_len = prefix_len;
   if (int rc = finite_gate(&f, nullptr, nullptr, D, status, s, &j.skip)) return rc;
+  j.status = status;
+  if (y.parts == 0) {
+    j.prefix_table = prefix_table;
+    j.prefix_len = prefix_len;
+    j.partial = reinterpret_cast<float*>(w);
+    return gqa::record_cuda_error(gqa::launch_decode_paged(j, s));
+  }
   gqa::Attn16Job a{};
   a.bf16 = j.bf16;
   a.q = j.q;
@@ -270,9 +286,10 @@ int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* ca
     return rc;
   j.prefix.o = a.part_o;
   j.prefix.ml = a.part_ml;
-  j.prefix.nsplit = y.splits;
-  j.partial = reinterpret_cast<float*>(w + y.own);
-  j.status = status;
+  j.prefix.nsplit = y.parts;
+  j.own_o = reinterpret_cast<float*>(w + y.own_o);
+  j.own_ml = reinterpret_cast<float2*>(w + y.own_ml);
+  j.partial = reinterpret_cast<float*>(w + y.decode);
   return gqa::record_cuda_error(gqa::launch_decode_paged(j, s));
 }
 

@@ -16,8 +16,11 @@
 //   output's: a second product on a pipe that is a fifth used.
 // * The tiles (16 positions) of all rows and heads, counted from the lengths on the device, are
 //   dealt out to the blocks in equal shares, whatever the lengths; a block's share is one run
-//   of tiles, so at most its first and last unit are shared with other blocks and merged by a
-//   second kernel. Where units are many or short, one block does each unit and nothing is merged.
+//   of tiles, so at most its first and last unit are shared with other blocks and joined by a
+//   second kernel, a warp per row and head. Where rows are short, one block does each unit
+//   and nothing is left to join (one row of 500 slots: 12.2 us shared out, see decode_paged_plan).
+// * With a prefix that all rows share, either its partial results (from the tensor cores) are joined
+//   here too, or, where it is read a few times only, its tiles come before the row's own.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -26,13 +29,13 @@ namespace gqa {
 namespace {
 
 constexpr int kTile = 16;                     // positions per warp step (never across pages)
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 152;
-constexpr int kResident = 2;                  // blocks per SM
+constexpr int kShareWarps = 8;                // a block that takes a share; two of them per SM
+constexpr int kResident = 2;
+constexpr int kWideWarps = 16;                // a block alone on its SM
 constexpr int kHeads = 8;                     // query heads of a unit
 constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
-constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps (8 bytes each)
+constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps
 
 struct DecodeArgs {
   const void* q;
@@ -48,7 +51,11 @@ struct DecodeArgs {
   int max_len, B, H, Hkv, D, G, HT;           // HT: units per kv head
   int window, softcap_on;
   float c_score, c_cap_in, c_cap_out;         // log2 units
-  PrefixParts prefix;
+  const int32_t* prefix_table;                // prefix read here, before the row's own positions
+  int prefix_len;
+  PrefixParts prefix;                         // or its partial results
+  float* own_o;                               // with those: the rows' own results, [B * H][D]
+  float2* own_ml;                             // and [B * H] (reference, sum)
   float* part_o;                              // [blocks][2][8][D]
   float2* part_ml;                            // [blocks][2][8]
   int blocks;
@@ -56,15 +63,17 @@ struct DecodeArgs {
   const int32_t* skip;
 };
 
-// Row b's live positions [lo, n) and its tiles; n < 0 where the length breaks a rule.
+// Row b's live positions [lo, n) of its own and its tiles: pt of the prefix, then its own from
+// tile t0 on; n < 0 where the length breaks a rule.
 struct Span {
-  int lo, n, t0, nt;
+  int lo, n, t0, pt, nt;
 };
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
   const int n = a.cache_len[b];
-  if (n < 0 || n > a.max_len) return {0, -1, 0, 0};
+  if (n < 0 || n > a.max_len) return {0, -1, 0, 0, 0};
   const int lo = a.window > 0 ? max(0, n - a.window) : 0;
-  return {lo, n, lo / kTile, n > 0 ? (n - 1) / kTile + 1 - lo / kTile : 0};
+  const int pt = (a.prefix_len + kTile - 1) / kTile;
+  return {lo, n, lo / kTile, pt, pt + (n > 0 ? (n - 1) / kTile + 1 - lo / kTile : 0)};
 }
 
 template <class T>
@@ -99,13 +108,13 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return v;
 }
 
-template <int DP>
+template <int W, int DP>
 struct __align__(16) Merge {                  // one block's warps, then its result
-  float m[kWarps][kHeads], l[kWarps][kHeads];
-  float o[kWarps][kHeads][DP + 4];
+  float o[W][kHeads][DP + 4];
+  float m[W][kHeads], l[W][kHeads];
 };
 
-// What a merge writes: the unit's output row of head h, dims d .. d + 3 of o with total weight l.
+// Output row of query head `head`, dims d .. d + 3.
 template <class T>
 __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int head, int d, float4 o) {
   T* p = static_cast<T*>(a.out) + b * a.o_token + head * a.o_head + d;
@@ -113,35 +122,11 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int head, 
       make_uint2(Pair<T>::pack(o.x, o.y), Pair<T>::pack(o.z, o.w));
 }
 
-// The row's own result (o / l, reference m, weight l) joined with its prefix parts.
-template <class T>
-__device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int head, int d, float4 o,
-                                           float m, float l) {
-  if (a.prefix.nsplit == 0) {
-    store_out<T>(a, b, head, d, o);
-    return;
-  }
-  const int64_t rows = static_cast<int64_t>(a.B) * a.H, row = static_cast<int64_t>(b) * a.H + head;
-  float top = m;
-  for (int s = 0; s < a.prefix.nsplit; ++s) top = fmaxf(top, a.prefix.ml[s * rows + row].x);
-  float f = l > 0.f ? tc::ex2(m - top) * l : 0.f, sum = f;
-  float4 y = make_float4(f * o.x, f * o.y, f * o.z, f * o.w);
-  for (int s = 0; s < a.prefix.nsplit; ++s) {
-    const float2 ml = a.prefix.ml[s * rows + row];
-    f = ml.y > 0.f ? tc::ex2(ml.x - top) * ml.y : 0.f;
-    const float4 p = *reinterpret_cast<const float4*>(a.prefix.o + (s * rows + row) * a.D + d);
-    sum += f;
-    y.x = fmaf(f, p.x, y.x); y.y = fmaf(f, p.y, y.y);
-    y.z = fmaf(f, p.z, y.z); y.w = fmaf(f, p.w, y.w);
-  }
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-  store_out<T>(a, b, head, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-}
-
 // Tiles [t0, t1) of row b's span for kv head hk, query heads [h0, h0 + nh): the block's result
-// goes to the output when whole, else to partial slot `slot` of this block.
-template <class T, int DP>
-__device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h0, int nh,
+// goes to the output when whole (slot < 0), or to where it is joined with the prefix, else to
+// partial slot `slot` of this block.
+template <class T, int W, int DP>
+__device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, int h0, int nh,
                         const Span& sp, int t0, int t1, int slot) {
   constexpr int KC = DP / 32, VH = DP / 64;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -169,22 +154,26 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
       for (int e = 0; e < 4; ++e) o[h][m][e] = 0.f;
   float m_ref = -INFINITY, l = 0.f;           // of head g (l: this lane's keys)
 
-  int ids = -1, ids_at = -1;                  // page of the warp's tile ids_at + 8 * lane
+  int ids = -1, ids_at = -1;                  // page of the warp's tile ids_at + W * lane
   uint4 kf[2][KC], vf[VH][4];
   int64_t off = -1;                           // of the tile whose loads are on their way
+  // The first position of a tile in its table, the prefix's or the row's own.
+  auto first_pos = [&](int tile) { return (tile < sp.pt ? tile : sp.t0 + tile - sp.pt) * kTile; };
   auto locate = [&](int tile) {               // element offset of the tile's first slot, < 0: none
-    if (ids_at < 0 || tile >= ids_at + 32 * kWarps) {
+    if (ids_at < 0 || tile >= ids_at + 32 * W) {
       ids_at = tile;
-      const int mine = tile + kWarps * lane;
-      ids = mine < t1 ? table[(static_cast<int64_t>(sp.t0 + mine) * kTile) >> a.page_shift] : 0;
+      const int mine = tile + W * lane;
+      ids = 0;
+      if (mine < t1)
+        ids = (mine < sp.pt ? a.prefix_table : table)[first_pos(mine) >> a.page_shift];
     }
-    const int id = __shfl_sync(0xffffffffu, ids, (tile - ids_at) / kWarps);
+    const int id = __shfl_sync(0xffffffffu, ids, (tile - ids_at) / W);
     if (id < 0 || id >= a.pages) {
       if (lane == 0) report(a.status, ATTN_DEV_PAGE);
       off = -1;
       return;
     }
-    off = id * a.page_stride + static_cast<int64_t>(((sp.t0 + tile) * kTile) & page_mask) * a.D;
+    off = id * a.page_stride + static_cast<int64_t>(first_pos(tile) & page_mask) * a.D;
   };
   auto load_k = [&]() {
 #pragma unroll
@@ -213,7 +202,7 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
     load_k();
     load_v();
   }
-  for (; tile < t1; tile += kWarps) {
+  for (; tile < t1; tile += W) {
     const bool there = off >= 0;
     float s[2][4];
 #pragma unroll
@@ -226,14 +215,13 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
         mma16816<T>(s[i], qf[c].z, 0u, qf[c].w, 0u, kf[i][c].z, kf[i][c].w);
       }
     }
-    const bool more = tile + kWarps < t1;
+    const bool more = tile + W < t1;
     if (more) {
-      locate(tile + kWarps);
+      locate(tile + W);
       load_k();
     }
     // scores of head g, keys k0 + {0, 1, 8, 9}
     float x[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
-    const int k0 = (sp.t0 + tile) * kTile + 2 * t;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (a.softcap_on) {
@@ -243,12 +231,13 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
         x[e] *= a.c_score;
       }
     }
-    const int tile0 = (sp.t0 + tile) * kTile;
-    if (tile0 < sp.lo || tile0 > sp.n - kTile || !there) {
+    const int tile0 = first_pos(tile), lo = tile < sp.pt ? 0 : sp.lo;
+    const int end = tile < sp.pt ? a.prefix_len : sp.n;
+    if (tile0 < lo || tile0 > end - kTile || !there) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = k0 + (e & 1) + 8 * (e >> 1);
-        if (key < sp.lo || key >= sp.n || !there) {
+        const int key = tile0 + 2 * t + (e & 1) + 8 * (e >> 1);
+        if (key < lo || key >= end || !there) {
           x[e] = -INFINITY;
           // an unused slot may hold anything, which a weight of 0 would still pass on
 #pragma unroll
@@ -281,21 +270,19 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
       p[e] = tc::ex2(x[e] - m_use);
       l += p[e];
     }
-    uint32_t hi[2], lo[2];
+    uint32_t hi[2], rest[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       hi[i] = Pair<T>::pack(p[2 * i], p[2 * i + 1]);
       const float2 r = unpack<T>(hi[i]);
-      lo[i] = Pair<T>::pack(p[2 * i] - r.x, p[2 * i + 1] - r.y);
+      rest[i] = Pair<T>::pack(p[2 * i] - r.x, p[2 * i + 1] - r.y);
     }
 #pragma unroll
     for (int h = 0; h < VH; ++h) {
-      const uint32_t* v0 = &vf[h][0].x;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const uint32_t sel = m & 1 ? 0x7632u : 0x5410u;
         const int w = m / 2;
-        (void)v0;
         auto word = [&](int r, int i) {
           const uint4& q4 = vf[h][r];
           return i == 0 ? q4.x : i == 1 ? q4.y : i == 2 ? q4.z : q4.w;
@@ -305,7 +292,7 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
         const uint32_t a2 = __byte_perm(word(2, w), word(3, w), sel);
         const uint32_t a3 = __byte_perm(word(2, 2 + w), word(3, 2 + w), sel);
         mma16816<T>(o[h][m], a0, a1, a2, a3, hi[0], hi[1]);
-        mma16816<T>(o[h][m], a0, a1, a2, a3, lo[0], lo[1]);
+        mma16816<T>(o[h][m], a0, a1, a2, a3, rest[0], rest[1]);
       }
     }
     if (more) load_v();
@@ -330,16 +317,16 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
       sh->o[warp][2 * t + 1][d + 4] = o[h][m][3];
     }
   __syncthreads();
-  for (int e = threadIdx.x; e < kHeads * DP / 4; e += kThreads) {
+  for (int e = threadIdx.x; e < kHeads * DP / 4; e += 32 * W) {
     const int h = e / (DP / 4), d = 4 * (e % (DP / 4));
     if (h >= nh || d >= a.D) continue;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh->m[w][h]);
+    for (int w = 0; w < W; ++w) top = fmaxf(top, sh->m[w][h]);
     float sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = sh->m[w][h] == -INFINITY ? 0.f : tc::ex2(sh->m[w][h] - top);
       const float4 p = *reinterpret_cast<const float4*>(&sh->o[w][h][d]);
       sum = fmaf(f, sh->l[w][h], sum);
@@ -348,32 +335,34 @@ __device__ void segment(const DecodeArgs& a, Merge<DP>* sh, int b, int hk, int h
     }
     const float inv = top == -INFINITY ? 0.f : 1.0f / sum;
     y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    if (slot < 0) {
-      finish_row<T>(a, b, h0 + h, d, y, top, sum);
-    } else {
-      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kHeads + h;
-      *reinterpret_cast<float4*>(a.part_o + at * a.D + d) = y;
-      if (d == 0) a.part_ml[at] = make_float2(top, sum);
+    if (slot < 0 && !a.own_o) {
+      store_out<T>(a, b, h0 + h, d, y);
+      continue;
     }
+    const int64_t at = slot < 0 ? static_cast<int64_t>(b) * a.H + h0 + h
+                                : (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kHeads + h;
+    *reinterpret_cast<float4*>((slot < 0 ? a.own_o : a.part_o) + at * a.D + d) = y;
+    if (d == 0) (slot < 0 ? a.own_ml : a.part_ml)[at] = make_float2(top, sum);
   }
 }
 
-// A row without positions of its own: zeros, or its prefix alone.
+// A row without any position: zeros (unless it is joined with a prefix later).
 template <class T>
-__device__ void empty_row(const DecodeArgs& a, int b) {
+__device__ __noinline__ void empty_row(const DecodeArgs& a, int b) {
+  if (a.own_o) return;
   const int n4 = a.D / 4;
-  for (int e = threadIdx.x; e < a.H * n4; e += kThreads)
-    finish_row<T>(a, b, e / n4, 4 * (e % n4), make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
+  for (int e = threadIdx.x; e < a.H * n4; e += blockDim.x)
+    store_out<T>(a, b, e / n4, 4 * (e % n4), make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
 // One block per unit (row, kv head, group of up to 8 query heads).
-template <class T, int DP>
-__global__ void __launch_bounds__(kThreads, kResident) decode_paged_units_kernel(const DecodeArgs a) {
-  __shared__ Merge<DP> sh;
+template <class T, int W, int DP>
+__global__ void __launch_bounds__(32 * W, 16 / W) decode_paged_units_kernel(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   dependent_wait();
   dependents_may_launch();
   if (gated_off(a.skip)) return;
-  const int per_row = a.Hkv * a.HT;
+  const unsigned per_row = a.Hkv * a.HT;
   const int b = blockIdx.x / per_row, u = blockIdx.x % per_row;
   const Span sp = span_of(a, b);
   if (sp.n < 0) {
@@ -385,161 +374,220 @@ __global__ void __launch_bounds__(kThreads, kResident) decode_paged_units_kernel
     return;
   }
   const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
-  segment<T, DP>(a, &sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, 0, sp.nt, -1);
+  segment<T, W, DP>(a, reinterpret_cast<Merge<W, DP>*>(smem), b, hk, h0,
+                    min(kHeads, (hk + 1) * a.G - h0), sp, 0, sp.nt, -1);
 }
 
-// prefix[b]: tiles of rows before b; returns their total. Whole block.
-__device__ long long scan_tiles(const DecodeArgs& a, long long* prefix, bool tell) {
-  __shared__ long long warp_sum_of[kWarps];
-  __shared__ long long carry;
+// prefix[b]: tiles of rows before b; returns their total. Whole block of W warps. (The tiles of all
+// rows and heads of a cache that fits the GPU are fewer than 2^32: one takes 512 bytes at least.)
+template <int W>
+__device__ unsigned scan_tiles(const DecodeArgs& a, unsigned* prefix, bool tell) {
+  __shared__ unsigned warp_sum_of[W];
+  __shared__ unsigned carry;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) carry = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+  unsigned before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.B; b0 += 32 * W) {
     const int b = b0 + threadIdx.x;
-    long long n = 0;
+    unsigned n = 0;
     if (b < a.B) {
       const Span sp = span_of(a, b);
       if (sp.n < 0 && tell) report(a.status, ATTN_DEV_LENGTH);
       n = sp.nt;
     }
-    long long s = n;
+    unsigned s = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, s, o);
+      const unsigned x = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += x;
     }
     if (lane == 31) warp_sum_of[warp] = s;
     __syncthreads();
-    long long before = carry;
     for (int w = 0; w < warp; ++w) before += warp_sum_of[w];
     if (b < a.B) prefix[b] = before + s - n;
+    if (threadIdx.x == 32 * W - 1) carry = before + s;
     __syncthreads();
-    if (threadIdx.x == kThreads - 1) carry = before + s;
-    __syncthreads();
+    before = carry;
   }
-  return carry;
+  return before;
 }
 
-__device__ __forceinline__ int row_of(const DecodeArgs& a, const long long* prefix, long long x,
-                                      int per_row) {
-  int lo = 0, hi = a.B - 1;                   // the last row that begins at or before tile x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (prefix[mid] * per_row <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+// Block i's share of `total` tiles begins at share_begin(i): the first total % blocks blocks have
+// one more than the others.
+__device__ __forceinline__ unsigned share_begin(unsigned total, unsigned blocks, unsigned i) {
+  const unsigned q = total / blocks, r = total - q * blocks;
+  return i * q + min(i, r);
+}
+__device__ __forceinline__ unsigned share_of(unsigned total, unsigned blocks, unsigned x) {
+  const unsigned q = total / blocks, r = total - q * blocks, big = r * (q + 1);
+  return x < big ? x / (q + 1) : r + (x - big) / q;   // q > 0 where x >= big
 }
 
-// Block i takes tiles [i total / blocks, (i + 1) total / blocks) of the list of all rows' heads' tiles.
 template <class T, int DP>
-__global__ void __launch_bounds__(kThreads, kResident) decode_paged_share_kernel(const DecodeArgs a) {
-  __shared__ Merge<DP> sh;
-  extern __shared__ long long prefix[];
+__global__ void __launch_bounds__(32 * kShareWarps, kResident)
+    decode_paged_share_kernel(const DecodeArgs a) {
+  using M = Merge<kShareWarps, DP>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  M* sh = reinterpret_cast<M*>(smem);
+  unsigned* prefix = reinterpret_cast<unsigned*>(smem + sizeof(M));
   dependent_wait();
   dependents_may_launch();
   if (gated_off(a.skip)) return;
-  const int per_row = a.Hkv * a.HT;
-  const long long total = scan_tiles(a, prefix, blockIdx.x == 0) * per_row;
-  for (int b = blockIdx.x; b < a.B; b += a.blocks)
-    if (span_of(a, b).n == 0) empty_row<T>(a, b);
-  long long x = static_cast<long long>(blockIdx.x) * total / a.blocks;
-  const long long end = static_cast<long long>(blockIdx.x + 1) * total / a.blocks;
-  while (x < end) {
-    const int b = row_of(a, prefix, x, per_row);
+  const unsigned per_row = a.Hkv * a.HT;
+  const unsigned total = scan_tiles<kShareWarps>(a, prefix, blockIdx.x == 0) * per_row;
+  for (int b = blockIdx.x; b < a.B; b += a.blocks) {
     const Span sp = span_of(a, b);
-    const long long in_row = x - prefix[b] * per_row;
-    const int u = static_cast<int>(in_row / sp.nt), t0 = static_cast<int>(in_row % sp.nt);
-    const int t1 = static_cast<int>(min(static_cast<long long>(sp.nt), t0 + (end - x)));
+    if (sp.n == 0 && sp.nt == 0) empty_row<T>(a, b);
+  }
+  unsigned x = share_begin(total, a.blocks, blockIdx.x);
+  const unsigned end = share_begin(total, a.blocks, blockIdx.x + 1);
+#pragma unroll 1
+  while (x < end) {
+    int b = 0, past = a.B;                    // the last row that begins at or before tile x
+    while (past - b > 1) {
+      const int mid = (b + past) / 2;
+      if (prefix[mid] * per_row <= x) b = mid; else past = mid;
+    }
+    const Span sp = span_of(a, b);
+    const unsigned in_row = x - prefix[b] * per_row, u = in_row / sp.nt;
+    const int t0 = in_row - u * sp.nt, t1 = min(static_cast<unsigned>(sp.nt), t0 + (end - x));
     const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
     // Slot 0: a unit begun by an earlier block (the share's first); slot 1: one begun here and
     // continued by the next (its last).
     const int slot = t0 > 0 ? 0 : (t1 < sp.nt ? 1 : -1);
-    segment<T, DP>(a, &sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, t0, t1, slot);
+    segment<T, kShareWarps, DP>(a, sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, t0, t1, slot);
     x += t1 - t0;
   }
 }
 
-// Units that several blocks shared, one block each.
+// Joins a row's results, a warp per row and query head: the shares of the blocks that had its unit
+// (nothing to do where one block finished it), and the prefix's parts.
 template <class T>
-__global__ void __launch_bounds__(kThreads) decode_paged_merge_kernel(const DecodeArgs a) {
-  extern __shared__ long long prefix[];
+__global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  unsigned* prefix = reinterpret_cast<unsigned*>(smem);
   dependent_wait();
   dependents_may_launch();
   if (gated_off(a.skip)) return;
-  const int per_row = a.Hkv * a.HT;
-  const long long total = scan_tiles(a, prefix, false) * per_row;
-  const int b = blockIdx.x / per_row, u = blockIdx.x % per_row;
+  const int lane = threadIdx.x & 31;
+  const unsigned per_row = a.Hkv * a.HT;
+  const unsigned total = a.blocks ? scan_tiles<8>(a, prefix, false) * per_row : 0;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  if (row >= static_cast<int64_t>(a.B) * a.H) return;
+  const int b = row / a.H, head = row - static_cast<int64_t>(b) * a.H;
   const Span sp = span_of(a, b);
-  if (sp.n <= 0) return;
-  const long long x0 = prefix[b] * per_row + static_cast<long long>(u) * sp.nt;
-  const long long x1 = x0 + sp.nt - 1;
-  const int i0 = static_cast<int>(((x0 + 1) * a.blocks - 1) / total);   // blocks of its first
-  const int i1 = static_cast<int>(((x1 + 1) * a.blocks - 1) / total);   // and last tile
-  if (i0 == i1) return;                       // one block had it whole
-  const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
-  const int nh = min(kHeads, (hk + 1) * a.G - h0), n4 = a.D / 4;
-  for (int e = threadIdx.x; e < nh * n4; e += kThreads) {
-    const int h = e / n4, d = 4 * (e % n4);
-    auto at = [&](int i) { return (static_cast<int64_t>(i) * 2 + (i == i0)) * kHeads + h; };
-    float top = -INFINITY;
-    for (int i = i0; i <= i1; ++i) top = fmaxf(top, a.part_ml[at(i)].x);
-    float sum = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = i0; i <= i1; ++i) {
-      const float2 ml = a.part_ml[at(i)];
-      const float4 p = *reinterpret_cast<const float4*>(a.part_o + at(i) * a.D + d);
-      const float f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - top) * ml.y;
-      sum += f;
-      y.x = fmaf(f, p.x, y.x); y.y = fmaf(f, p.y, y.y);
-      y.z = fmaf(f, p.z, y.z); y.w = fmaf(f, p.w, y.w);
-    }
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-    finish_row<T>(a, b, h0 + h, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv), top, sum);
+  if (sp.n < 0) return;
+  const int hk = head / a.G, g = head - hk * a.G, h = g % kHeads;
+  unsigned i0 = 0, own = sp.nt > 0 ? 1 : 0;   // first block, and how many had the unit
+  if (a.blocks && sp.nt > 0) {
+    const unsigned x0 = prefix[b] * per_row + (hk * a.HT + g / kHeads) * sp.nt;
+    i0 = share_of(total, a.blocks, x0);
+    own = share_of(total, a.blocks, x0 + sp.nt - 1) - i0 + 1;
   }
+  if (own <= 1 && a.prefix.nsplit == 0) return;
+  const unsigned parts = own + a.prefix.nsplit;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.H;
+  auto ml_of = [&](unsigned i) -> float2 {
+    if (i >= own) return a.prefix.ml[(i - own) * rows + row];
+    if (own == 1) return a.own_ml[row];
+    return a.part_ml[(static_cast<int64_t>(i0 + i) * 2 + (i == 0)) * kHeads + h];
+  };
+  auto o_of = [&](unsigned i) -> const float* {
+    if (i >= own) return a.prefix.o + ((i - own) * rows + row) * a.D;
+    if (own == 1) return a.own_o + row * a.D;
+    return a.part_o + ((static_cast<int64_t>(i0 + i) * 2 + (i == 0)) * kHeads + h) * a.D;
+  };
+  float top = -INFINITY;
+  for (unsigned i = lane; i < parts; i += 32) top = fmaxf(top, ml_of(i).x);
+  top = warp_max(top);
+  float sum = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int d = 4 * lane;
+#pragma unroll 1
+  for (unsigned s0 = 0; s0 < parts; s0 += 32) {
+    const unsigned n = min(32u, parts - s0);
+    float f = 0.f;
+    if (lane < n) {
+      const float2 ml = ml_of(s0 + lane);
+      f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - top) * ml.y;
+    }
+    sum += warp_sum(f);
+#pragma unroll 8
+    for (unsigned i = 0; i < n; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      if (d < a.D) {
+        const float4 p = *reinterpret_cast<const float4*>(o_of(s0 + i) + d);
+        y.x = fmaf(fi, p.x, y.x); y.y = fmaf(fi, p.y, y.y);
+        y.z = fmaf(fi, p.z, y.z); y.w = fmaf(fi, p.w, y.w);
+      }
+    }
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
+  if (d < a.D)
+    store_out<T>(a, b, head, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+}
+
+// Shared memory past 48 KB is an attribute of the kernel in each device's context.
+template <auto* Kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static PerContext<cudaError_t> attr;
+  return attr.get(
+      [=] {
+        return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(bytes));
+      },
+      cudaErrorInvalidDevice, [](cudaError_t r) { return r == cudaSuccess; });
+}
+
+template <class T, int W, int DP>
+cudaError_t launch_units(const DecodeArgs& a, unsigned units, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(Merge<W, DP>);
+  const cudaError_t e = allow_smem<decode_paged_units_kernel<T, W, DP>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(decode_paged_units_kernel<T, W, DP>, units, 32 * W, smem, stream, a);
 }
 
 template <class T, int DP>
-cudaError_t launch_dp(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_dp(const DecodeArgs& a, int warps, cudaStream_t stream) {
   const unsigned units = static_cast<unsigned>(a.B) * a.Hkv * a.HT;
-  if (a.blocks == 0)
-    return launch_dependent(decode_paged_units_kernel<T, DP>, units, kThreads, 0, stream, a);
-  const size_t smem = static_cast<size_t>(a.B) * sizeof(long long);
-  static PerContext<cudaError_t> attr;
-  cudaError_t e = attr.get(
-      [] {
-        const int most = kMaxScanRows * sizeof(long long);
-        const cudaError_t r = cudaFuncSetAttribute(decode_paged_share_kernel<T, DP>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        return r != cudaSuccess ? r
-                                : cudaFuncSetAttribute(decode_paged_merge_kernel<T>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-      },
-      cudaErrorInvalidDevice, [](cudaError_t r) { return r == cudaSuccess; });
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(decode_paged_share_kernel<T, DP>, a.blocks, kThreads, smem, stream, a);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(decode_paged_merge_kernel<T>, units, kThreads, smem, stream, a);
+  cudaError_t e;
+  size_t scan = 0;
+  if (a.blocks == 0) {
+    e = warps == kWideWarps ? launch_units<T, kWideWarps, DP>(a, units, stream)
+                            : launch_units<T, kShareWarps, DP>(a, units, stream);
+  } else {
+    using M = Merge<kShareWarps, DP>;
+    scan = static_cast<size_t>(a.B) * sizeof(unsigned);
+    e = allow_smem<decode_paged_share_kernel<T, DP>>(sizeof(M) + kMaxScanRows * sizeof(unsigned));
+    if (e == cudaSuccess)
+      e = launch_dependent(decode_paged_share_kernel<T, DP>, a.blocks, 32 * kShareWarps,
+                           sizeof(M) + scan, stream, a);
+  }
+  if (e != cudaSuccess || (a.blocks == 0 && a.prefix.nsplit == 0)) return e;
+  return launch_dependent(decode_paged_join_kernel<T>,
+                          static_cast<unsigned>((static_cast<int64_t>(a.B) * a.H + 7) / 8), 256,
+                          scan, stream, a);
 }
-
-int eff_len(int max_len, int window) { return window > 0 && window < max_len ? window : max_len; }
 
 }  // namespace
 
-// Blocks that share all tiles, or 0: one per unit, where none of them is long or there are many.
-int decode_paged_blocks(int B, int H, int Hkv, int max_len, int window) {
+// One block per unit where no row has more than 4 tiles a warp -- 8 warps (512 slots), or 16 (1024)
+// where every unit can have an SM to itself --, else blocks that share all tiles.
+DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int max_len, int window, int prefix_len) {
   const int G = H / Hkv;
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + kHeads - 1) / kHeads);
-  const int64_t tiles = (eff_len(max_len, window) + kTile - 1) / kTile + 1;
-  if (tiles <= 4 * kWarps || B > kMaxScanRows || units == 0) return 0;
-  const int64_t most = kSms * kResident, want = (units * tiles + kWarps - 1) / kWarps;
-  return static_cast<int>(want < most ? want : most);
+  const int64_t own = window > 0 && window < max_len ? window + kTile - 1 : max_len;
+  const int64_t tiles = (own + kTile - 1) / kTile + (prefix_len + kTile - 1) / kTile;
+  if (tiles <= 4 * kWideWarps && units <= kSms)
+    return {0, tiles <= kShareWarps ? kShareWarps : kWideWarps};
+  if (tiles <= 4 * kShareWarps || B > kMaxScanRows) return {0, kShareWarps};
+  const int64_t most = kSms * kResident, want = (units * tiles + kShareWarps - 1) / kShareWarps;
+  return {static_cast<int>(want < most ? want : most), kShareWarps};
 }
 
-// part_ml follows part_o; sized for every length up to max_len (more blocks never take less).
-size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window) {
-  const size_t blocks = decode_paged_blocks(B, H, Hkv, max_len, window);
+// The partial results of the blocks' shares (part_ml follows part_o). Never shrinks as max_len grows.
+size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window, int prefix_len) {
+  const size_t blocks = decode_paged_plan(B, H, Hkv, max_len, window, prefix_len).blocks;
   return blocks * 2 * kHeads * (D + 2) * sizeof(float);
 }
 
@@ -560,14 +608,22 @@ cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
   a.c_score = j.scale * kLog2e16;
   a.c_cap_in = j.softcap > 0.f ? 2.0f * kLog2e16 * j.scale / j.softcap : 0.f;
   a.c_cap_out = kLog2e16 * j.softcap;
+  a.prefix_table = j.prefix_table;
+  a.prefix_len = j.prefix_len;
   a.prefix = j.prefix;
-  a.blocks = j.blocks;
+  a.own_o = j.own_o;
+  a.own_ml = j.own_ml;
+  const DecodePagedPlan plan =
+      decode_paged_plan(j.B, j.H, j.Hkv, j.max_len, j.window, j.prefix_len);
+  a.blocks = plan.blocks;
   a.part_o = j.partial;
-  a.part_ml = reinterpret_cast<float2*>(j.partial + static_cast<size_t>(j.blocks) * 2 * kHeads * j.D);
+  a.part_ml = reinterpret_cast<float2*>(j.partial + static_cast<size_t>(a.blocks) * 2 * kHeads * j.D);
   a.status = j.status; a.skip = j.skip;
   if (j.D <= 64)
-    return j.bf16 ? launch_dp<__nv_bfloat16, 64>(a, stream) : launch_dp<__half, 64>(a, stream);
-  return j.bf16 ? launch_dp<__nv_bfloat16, 128>(a, stream) : launch_dp<__half, 128>(a, stream);
+    return j.bf16 ? launch_dp<__nv_bfloat16, 64>(a, plan.warps, stream)
+                  : launch_dp<__half, 64>(a, plan.warps, stream);
+  return j.bf16 ? launch_dp<__nv_bfloat16, 128>(a, plan.warps, stream)
+                : launch_dp<__half, 128>(a, plan.warps, stream);
 }
 
 }  // namespace gqa
