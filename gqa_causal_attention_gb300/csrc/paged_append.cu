@@ -15,14 +15,20 @@ namespace gqa {
 namespace {
 
 enum { kPlain = 0, kShuffle = 1, kAnyDims = 2 };   // how the rotary partner is reached
-constexpr int kPasses = 4;
+// 9500 tokens of 32 + 2 x 8 heads of 128, norms: 2 passes a group and all of a token's 12 groups in
+// one warp 65 us; 6 groups 71, 1 group 114; 4 passes (more registers, fewer warps) 74, 12 passes 118.
+constexpr int kPasses = 2;
+constexpr int kGroups = 12;
+constexpr int64_t kManyWarps = 152 * 24;
 
 // A head row of D values is held by LPH lanes (a power of two >= D / 8), 16 bytes each, so a warp
-// takes 32 / LPH heads in a pass and kPasses passes of one token: their loads are all on
-// their way before the token's place in the cache is known. With half the rotary dims a
-// multiple of 8 (kShuffle) the partner dims are another lane's whole granule.
+// takes 32 / LPH heads in a pass. It does `groups` groups of kPasses passes of one token; a
+// group's loads are on their way before the group before it is worked on, the first before the
+// token's place in the cache is known. The token's angles, times the norm's weights, stay in
+// registers for all its queries, then all its keys. With half the rotary dims a multiple of 8 (kShuffle) the partner dims are another lane's whole granule.
 template <class T, int LPH, int ROPE>
-__global__ void __launch_bounds__(256) append_paged_kernel(const AppendPagedJob j, unsigned warps) {
+__global__ void __launch_bounds__(256, 3) append_paged_kernel(const AppendPagedJob j, unsigned warps,
+                                                           int warps_per_token, int groups) {
   dependent_wait();
   dependents_may_launch();
   if (gated_off(j.skip)) return;
@@ -31,21 +37,23 @@ __global__ void __launch_bounds__(256) append_paged_kernel(const AppendPagedJob 
   constexpr int HPW = 32 / LPH;
   const int lane = threadIdx.x & 31;
   const int nq = j.q.p ? j.H : 0, heads = nq + 2 * j.Hkv;
-  const int per_token = (heads + HPW * kPasses - 1) / (HPW * kPasses);
-  const int t = w / per_token, h0 = (w % per_token) * HPW * kPasses + lane / LPH;
+  const int t = w / warps_per_token;
+  int h0 = (w % warps_per_token) * groups * HPW * kPasses + lane / LPH;
   const int d0 = 8 * (lane % LPH);
   const bool in_row = d0 < j.D;
+  const float inv_D = 1.0f / static_cast<float>(j.D);
   const Rows<T> q = rows_as<T>(j.q), k = rows_as<T>(j.k), v = rows_as<T>(j.v);
-
-  uint4 raw[kPasses];
+  auto row_of = [&](int h) -> const T* {
+    return h < nq ? q.at(t, h) : (h < nq + j.Hkv ? k.at(t, h - nq) : v.at(t, h - nq - j.Hkv));
+  };
+  uint4 raw[kPasses], ahead[kPasses];
+  auto load = [&](uint4 (&to)[kPasses], int h) {
 #pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int h = h0 + u * HPW;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (!in_row || h >= heads) continue;
-    const T* src = h < nq ? q.at(t, h) : (h < nq + j.Hkv ? k.at(t, h - nq) : v.at(t, h - nq - j.Hkv));
-    raw[u] = *reinterpret_cast<const uint4*>(src + d0);
-  }
+    for (int u = 0; u < kPasses; ++u, h += HPW)
+      to[u] = in_row && h < heads ? *reinterpret_cast<const uint4*>(row_of(h) + d0)
+                                  : make_uint4(0, 0, 0, 0);
+  };
+  load(raw, h0);
 
   // The token's sequence, position and page.
   int b = t, i = 0, n = 1;
@@ -68,6 +76,51 @@ __global__ void __launch_bounds__(256) append_paged_kernel(const AppendPagedJob 
   }
   const int pos = static_cast<int>(first) + i;
   const int page = j.block_table[static_cast<int64_t>(b) * j.width + (pos >> j.cache.page_shift)];
+  const int half = j.R / 2, hl = half / 8;   // hl: lanes of half the rotary dims
+  const int from = (lane & ~(LPH - 1)) + ((lane % LPH) < hl ? lane % LPH + hl : lane % LPH - hl);
+  // Factors of a rotated row's own and partner dims, with the norm's weights in them (the common
+  // 1 / rms comes after): y = x own + x' other, of the kind (query or key) at hand.
+  float own[8], other[8];
+  int kind = -1;
+  auto factors = [&](const float* nw) {
+    const float2* row = j.table + static_cast<int64_t>(pos) * half;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      own[e] = 1.f;
+      other[e] = 0.f;
+    }
+    if (!in_row) return;
+    if (d0 < j.R) {
+      if (ROPE == kShuffle) {
+        const float4* r4 = reinterpret_cast<const float4*>(row + (d0 < half ? d0 : d0 - half));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 c = r4[e];
+          own[2 * e] = c.x; own[2 * e + 1] = c.z;
+          other[2 * e] = c.y; other[2 * e + 1] = c.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = d0 + e;
+          if (d < j.R) {
+            const float2 c = row[d < half ? d : d - half];
+            own[e] = c.x;
+            other[e] = c.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = d0 + e;
+      if (d < half) other[e] = -other[e];    // the first half's partner enters with a minus
+      if (nw) {
+        own[e] *= nw[d];
+        if (d < j.R) other[e] *= nw[d < half ? d + half : d - half];
+      }
+    }
+  };
   if (page < 0 || page >= j.cache.pages) {
     if (lane == 0) report(j.status, ATTN_DEV_PAGE);
     return;
@@ -77,118 +130,89 @@ __global__ void __launch_bounds__(256) append_paged_kernel(const AppendPagedJob 
   T* kc = static_cast<T*>(j.cache.k) + page * j.cache.page_stride + slot * j.D + d0;
   T* vc = static_cast<T*>(j.cache.v) + page * j.cache.page_stride + slot * j.D + d0;
 
-  const int half = j.R / 2;
-  float cs[8], sn[8];
-  if (ROPE != kPlain) {
-    const float2* row = j.table + static_cast<int64_t>(pos) * half;
+#pragma unroll 1
+  for (int g = 0; g < groups; ++g, h0 += HPW * kPasses) {
+    if (g + 1 < groups) load(ahead, h0 + HPW * kPasses);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e] = 1.f;
-      sn[e] = 0.f;
-    }
-    if (in_row && d0 < j.R) {
-      if (ROPE == kShuffle) {
-        const float4* r4 = reinterpret_cast<const float4*>(row + (d0 < half ? d0 : d0 - half));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 c = r4[e];
-          cs[2 * e] = c.x; cs[2 * e + 1] = c.z;
-          sn[2 * e] = c.y; sn[2 * e + 1] = c.w;
+    for (int u = 0; u < kPasses; ++u) {
+      const int h = h0 + u * HPW;
+      const bool is_q = h < nq, is_v = h >= nq + j.Hkv, live = in_row && h < heads;
+      uint4 y = raw[u];
+      if (ROPE != kPlain) {
+        const float* nw = is_q ? j.q_norm_w : j.k_norm_w;
+        if (!is_v && kind != is_q) {         // at most twice a warp and lane
+          factors(nw);
+          kind = is_q;
         }
+        float x[8], p[8];
+        unpack8<T>(raw[u], x);
+        float inv = 1.f;
+        if (j.q_norm_w || j.k_norm_w) {      // sums over the row's lanes (all lanes take part)
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+          for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (nw) inv = rsqrtf(fmaf(ss, inv_D, j.norm_eps));   // within 2 ulp of fp32
+        }
+        if (ROPE == kShuffle) {
+          const uint4 o = make_uint4(__shfl_sync(0xffffffffu, raw[u].x, from & 31),
+                                     __shfl_sync(0xffffffffu, raw[u].y, from & 31),
+                                     __shfl_sync(0xffffffffu, raw[u].z, from & 31),
+                                     __shfl_sync(0xffffffffu, raw[u].w, from & 31));
+          unpack8<T>(o, p);
+        } else {                             // partner dims one by one from the raw row
+          const T* src = is_q ? q.at(t, h) : k.at(t, min(h - nq, j.Hkv - 1));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int d = d0 + e;
+            p[e] = 0.f;
+            if (live && !is_v && d < j.R) p[e] = static_cast<float>(src[d < half ? d + half : d - half]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // past the rotary dims: no partner (its lane's value may be anything)
+          const float r = fmaf(x[e], own[e], d0 + e < j.R ? p[e] * other[e] : 0.f);
+          x[e] = r * inv;
+        }
+        if (!is_v) y = pack8<T>(x);
+        __syncwarp();                        // in place: every lane has read its partners
+      }
+      if (!live) continue;
+      if (is_q) {
+        *reinterpret_cast<uint4*>(rows_as<T>(j.q_out).at(t, h) + d0) = y;
+      } else if (!is_v) {
+        const int hk = h - nq;
+        *reinterpret_cast<uint4*>(kc + hk * head_stride) = y;
+        if (j.k_out.p) *reinterpret_cast<uint4*>(rows_as<T>(j.k_out).at(t, hk) + d0) = y;
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = d0 + e;
-          if (d < j.R) {
-            const float2 c = row[d < half ? d : d - half];
-            cs[e] = c.x;
-            sn[e] = c.y;
-          }
-        }
+        *reinterpret_cast<uint4*>(vc + (h - nq - j.Hkv) * head_stride) = y;
       }
-      // y = x c + partner s: the first half's partner enters with a minus
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (d0 + e < half) sn[e] = -sn[e];
     }
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) raw[u] = ahead[u];
   }
+}
 
-#pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int h = h0 + u * HPW;
-    const bool is_q = h < nq, is_v = h >= nq + j.Hkv, live = in_row && h < heads;
-    uint4 y = raw[u];
-    if (ROPE != kPlain) {
-      float x[8], p[8];
-      unpack8<T>(raw[u], x);
-      const float* nw = is_v ? nullptr : (is_q ? j.q_norm_w : j.k_norm_w);
-      float inv = 1.f;
-      if (j.q_norm_w || j.k_norm_w) {        // sums over the row's lanes (all lanes take part)
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        inv = 1.0f / sqrtf(ss / static_cast<float>(j.D) + j.norm_eps);
-      }
-      if (ROPE == kAnyDims) {                // partner dims one by one from the raw row
-        const T* src = is_q ? q.at(t, h) : k.at(t, min(h - nq, j.Hkv - 1));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = d0 + e;
-          p[e] = 0.f;
-          if (live && !is_v && d < j.R) {
-            const int pd = d < half ? d + half : d - half;
-            p[e] = static_cast<float>(src[pd]);
-            if (nw) p[e] *= inv * nw[pd];
-          }
-        }
-      }
-      if (nw && live) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv * nw[d0 + e];
-      }
-      if (ROPE == kShuffle) {
-        const int hl = half / 8;             // lanes of half the rotary dims
-        const int from = (lane & ~(LPH - 1)) + ((lane % LPH) < hl ? (lane % LPH) + hl
-                                                                  : (lane % LPH) - hl);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], from & 31);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = d0 + e < j.R ? fmaf(x[e], cs[e], p[e] * sn[e]) : x[e];
-      if (!is_v) y = pack8<T>(x);
-      __syncwarp();                          // in place: every lane has read its partners
-    }
-    if (!live) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(rows_as<T>(j.q_out).at(t, h) + d0) = y;
-    } else if (!is_v) {
-      const int hk = h - nq;
-      *reinterpret_cast<uint4*>(kc + hk * head_stride) = y;
-      if (j.k_out.p) *reinterpret_cast<uint4*>(rows_as<T>(j.k_out).at(t, hk) + d0) = y;
-    } else {
-      *reinterpret_cast<uint4*>(vc + (h - nq - j.Hkv) * head_stride) = y;
-    }
-  }
+template <class T, int LPH, int ROPE>
+cudaError_t launch_rope(const AppendPagedJob& j, cudaStream_t stream) {
+  const int heads = (j.q.p ? j.H : 0) + 2 * j.Hkv, per = 32 / LPH * kPasses;
+  const int all = (heads + per - 1) / per;   // groups of a token
+  // Few tokens: a warp for each group. Many: kGroups groups a warp, which share its search and angles.
+  int groups = 1;
+  if (static_cast<int64_t>(j.T) * all > kManyWarps) groups = all < kGroups ? all : kGroups;
+  const int per_token = (all + groups - 1) / groups;
+  const unsigned warps = static_cast<unsigned>(j.T) * per_token;
+  return launch_dependent(append_paged_kernel<T, LPH, ROPE>, (warps + 7) / 8, 256, 0, stream, j,
+                          warps, per_token, groups);
 }
 
 template <class T, int LPH>
 cudaError_t launch_lph(const AppendPagedJob& j, cudaStream_t stream) {
-  const int heads = (j.q.p ? j.H : 0) + 2 * j.Hkv;
-  const int per_warp = 32 / LPH * kPasses;
-  const unsigned warps = static_cast<unsigned>(j.T) * ((heads + per_warp - 1) / per_warp);
-  const unsigned grid = (warps + 7) / 8;
-  const int rope = !j.table ? kPlain : (j.R % 16 == 0 ? kShuffle : kAnyDims);
-  switch (rope) {
-    case kPlain:
-      return launch_dependent(append_paged_kernel<T, LPH, kPlain>, grid, 256, 0, stream, j, warps);
-    case kShuffle:
-      return launch_dependent(append_paged_kernel<T, LPH, kShuffle>, grid, 256, 0, stream, j, warps);
-    default:
-      return launch_dependent(append_paged_kernel<T, LPH, kAnyDims>, grid, 256, 0, stream, j, warps);
-  }
+  if (!j.table) return launch_rope<T, LPH, kPlain>(j, stream);
+  return j.R % 16 == 0 ? launch_rope<T, LPH, kShuffle>(j, stream)
+                       : launch_rope<T, LPH, kAnyDims>(j, stream);
 }
 
 template <class T>
