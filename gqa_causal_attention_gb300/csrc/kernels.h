@@ -521,7 +521,8 @@ struct DecodePagedJob {
 struct DecodePagedPlan {
   int blocks, warps;
 };
-DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int max_len, int window, int prefix_len);
+DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int D, int max_len, int window,
+                                  int prefix_len);
 size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window, int prefix_len);
 cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream);
 
