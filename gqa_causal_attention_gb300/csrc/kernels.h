@@ -509,9 +509,7 @@ struct DecodePagedJob {
   float softcap, scale;
   const int32_t* prefix_table;     // positions before each row's own, read from these pages
   int prefix_len;                  // (0: none)
-  PrefixParts prefix;              // or their partial results; then the rows' own results go to
-  float* own_o;                    // own_o [B * H][D] and own_ml [B * H] before they are joined
-  float2* own_ml;
+  PrefixParts prefix;              // or their partial results
   float* partial;                  // workspace
   int32_t* status;
   const int32_t* skip;

@@ -77,13 +77,13 @@ bool rope_ok(const attn_rope_params* rp, int D) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace of a shared-prefix call: the prefix's partial outputs and their weights, the rows' own,
-// then the decode's. `parts` 0: the prefix is read with each row's own positions, which costs
-// less than the two kernels more where all rows together read at most kRereadBytes of it, mostly
+// Workspace of a shared-prefix call: the prefix's partial outputs and their weights, then the
+// decode's. `parts` 0: the prefix is read with each row's own positions, which costs
+// less than a kernel more where all rows together read at most kRereadBytes of it, mostly
 // from L2.
 constexpr int64_t kRereadBytes = 64 << 20;
 struct SharedLayout {
-  size_t ml, own_o, own_ml, decode, total;
+  size_t ml, decode, total;
   int parts;
 };
 SharedLayout shared_layout(int B, int H, int Hkv, int D, int prefix_len, int max_len) {
@@ -95,9 +95,7 @@ SharedLayout shared_layout(int B, int H, int Hkv, int D, int prefix_len, int max
   y.parts = gqa::shared_prefix_plan(B, H, Hkv, prefix_len).parts();
   const size_t rows = static_cast<size_t>(B) * H;
   y.ml = align256(rows * y.parts * D * sizeof(float));
-  y.own_o = y.ml + align256(rows * y.parts * 2 * sizeof(float));
-  y.own_ml = y.own_o + align256(rows * D * sizeof(float));
-  y.decode = y.own_ml + align256(rows * 2 * sizeof(float));
+  y.decode = y.ml + align256(rows * y.parts * 2 * sizeof(float));
   y.total = y.decode + gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, 0);
   return y;
 }
@@ -287,8 +285,6 @@ int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* ca
   j.prefix.o = a.part_o;
   j.prefix.ml = a.part_ml;
   j.prefix.nsplit = y.parts;
-  j.own_o = reinterpret_cast<float*>(w + y.own_o);
-  j.own_ml = reinterpret_cast<float2*>(w + y.own_ml);
   j.partial = reinterpret_cast<float*>(w + y.decode);
   return gqa::record_cuda_error(gqa::launch_decode_paged(j, s));
 }

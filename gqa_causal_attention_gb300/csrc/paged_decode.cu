@@ -32,6 +32,7 @@ constexpr int kSms = 152;
 constexpr int kShareWarps = 8;                // a block that takes a share; two of them per SM
 constexpr int kResident = 2;
 constexpr int kWideWarps = 16;                // a block alone on its SM
+constexpr int kSlimWarps = 4;                 // four of them per SM
 constexpr int kHeads = 8;                     // query heads of a unit
 constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
 constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps
@@ -53,8 +54,6 @@ struct DecodeArgs {
   const int32_t* prefix_table;                // prefix read here, before the row's own positions
   int prefix_len;
   PrefixParts prefix;                         // or its partial results
-  float* own_o;                               // with those: the rows' own results, [B * H][D]
-  float2* own_ml;                             // and [B * H] (reference, sum)
   float* part_o;                              // [blocks][2][8][D]
   float2* part_ml;                            // [blocks][2][8]
   int blocks;
@@ -128,10 +127,73 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int head, 
       make_uint2(Pair<T>::pack(o.x, o.y), Pair<T>::pack(o.z, o.w));
 }
 
+// Adds `count` parts -- part(i, ml, o) says where the i-th's (reference, sum) and o / sum lie -- to a
+// row's y = sum of weights x values, its reference `top` and sum. Whole warp, dims d .. d + 3 a lane.
+// 32 parts at a time, a lane each; then their rows, eight loads on their way at once (one after
+// the other 38 parts took 20 us).
+template <class F>
+__device__ __forceinline__ void add_parts(F part, unsigned count, int d, int D, float4& y, float& top,
+                                          float& sum) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (unsigned s0 = 0; s0 < count; s0 += 32) {
+    const unsigned n = min(32u, count - s0);
+    const float2* ml;
+    const float* o;
+    part(s0 + min(static_cast<unsigned>(lane), n - 1), ml, o);
+    const float2 mine = lane < n ? *ml : make_float2(-INFINITY, 0.f);
+    const float before = top;
+    top = fmaxf(top, warp_max(mine.x));
+    const float f = mine.y == 0.f ? 0.f : tc::ex2(mine.x - top) * mine.y;
+    if (before != top && before != -INFINITY) {
+      const float r = tc::ex2(before - top);
+      sum *= r;
+      y.x *= r; y.y *= r; y.z *= r; y.w *= r;
+    }
+    sum += warp_sum(f);
+#pragma unroll 1
+    for (unsigned i = 0; i < n; i += 8) {
+      float4 p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float* from = reinterpret_cast<const float*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(o), min(i + e, n - 1)));
+        p[e] = d < D ? *reinterpret_cast<const float4*>(from + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float fi = __shfl_sync(0xffffffffu, f, min(i + e, 31u));
+        if (i + e < n) {
+          y.x = fmaf(fi, p[e].x, y.x); y.y = fmaf(fi, p[e].y, y.y);
+          y.z = fmaf(fi, p[e].z, y.z); y.w = fmaf(fi, p[e].w, y.w);
+        }
+      }
+    }
+  }
+}
+
+// The prefix's parts (PRE) of row b, query head `head`, and the row's output. (A kernel without
+// them is one of its own: their code costs the others registers, 5% of the time.)
+template <class T, bool PRE>
+__device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int head, int d, float4 y,
+                                           float top, float sum) {
+  const int64_t row = static_cast<int64_t>(b) * a.H + head, rows = static_cast<int64_t>(a.B) * a.H;
+  if (PRE)
+    add_parts(
+        [&](unsigned i, const float2*& ml, const float*& o) {
+          ml = a.prefix.ml + i * rows + row;
+          o = a.prefix.o + (i * rows + row) * a.D;
+        },
+        a.prefix.nsplit, d, a.D, y, top, sum);
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;      // (a NaN stays one)
+  if (d < a.D)
+    store_out<T>(a, b, head, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+}
+
 // Tiles [t0, t1) of row b's span for kv head hk, query heads [h0, h0 + nh): the block's result
-// goes to the output when whole (slot < 0), or to where it is joined with the prefix, else to
-// partial slot `slot` of this block.
-template <class T, int W, int DP>
+// goes, with the prefix's parts, to the output when whole (slot < 0), else to partial slot `slot`
+// of this block.
+template <class T, int W, int DP, bool PRE>
 __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, int h0, int nh,
                         const Span& sp, int t0, int t1, int slot) {
   constexpr int KC = DP / 32, VH = DP / 64;
@@ -325,46 +387,44 @@ __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, in
       sh->o[warp][2 * t + 1][d + 4] = o[h][m][3];
     }
   __syncthreads();
-  for (int e = threadIdx.x; e < kHeads * DP / 4; e += 32 * W) {
-    const int h = e / (DP / 4), d = 4 * (e % (DP / 4));
-    if (h >= nh || d >= a.D) continue;
-    float top = -INFINITY;
+  const int d = 4 * lane;
+#pragma unroll 1
+  for (int h = warp; h < nh; h += W) {
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) top = fmaxf(top, sh->m[w][h]);
-    float sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float f = sh->m[w][h] == -INFINITY ? 0.f : tc::ex2(sh->m[w][h] - top);
-      const float4 p = *reinterpret_cast<const float4*>(&sh->o[w][h][d]);
+      const float4 p = d < DP ? *reinterpret_cast<const float4*>(&sh->o[w][h][d])
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
       sum = fmaf(f, sh->l[w][h], sum);
       y.x = fmaf(f, p.x, y.x); y.y = fmaf(f, p.y, y.y);
       y.z = fmaf(f, p.z, y.z); y.w = fmaf(f, p.w, y.w);
     }
-    const float inv = top == -INFINITY ? 0.f : 1.0f / sum;
-    y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    if (slot < 0 && !a.own_o) {
-      store_out<T>(a, b, h0 + h, d, y);
+    if (slot < 0) {
+      finish_row<T, PRE>(a, b, h0 + h, d, y, top, sum);
       continue;
     }
-    const int64_t at = slot < 0 ? static_cast<int64_t>(b) * a.H + h0 + h
-                                : (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kHeads + h;
-    *reinterpret_cast<float4*>((slot < 0 ? a.own_o : a.part_o) + at * a.D + d) = y;
-    if (d == 0) (slot < 0 ? a.own_ml : a.part_ml)[at] = make_float2(top, sum);
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kHeads + h;
+    const float inv = top == -INFINITY ? 0.f : 1.0f / sum;
+    if (d < a.D)
+      *reinterpret_cast<float4*>(a.part_o + at * a.D + d) =
+          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    if (lane == 0) a.part_ml[at] = make_float2(top, sum);
   }
 }
 
-// A row without any position: zeros (unless it is joined with a prefix later).
-template <class T>
+// A row without any position of its own: zeros, or its prefix alone.
+template <class T, bool PRE>
 __device__ __noinline__ void empty_row(const DecodeArgs& a, int b) {
-  if (a.own_o) return;
-  const int n4 = a.D / 4;
-  for (int e = threadIdx.x; e < a.H * n4; e += blockDim.x)
-    store_out<T>(a, b, e / n4, 4 * (e % n4), make_float4(0.f, 0.f, 0.f, 0.f));
+  for (int head = threadIdx.x / 32; head < a.H; head += blockDim.x / 32)
+    finish_row<T, PRE>(a, b, head, 4 * (threadIdx.x & 31), make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
 }
 
 // One block per unit (row, kv head, group of up to 8 query heads).
-template <class T, int W, int DP>
+template <class T, int W, int DP, bool PRE>
 __global__ void __launch_bounds__(32 * W, 16 / W) decode_paged_units_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   dependent_wait();
@@ -378,11 +438,11 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_paged_units_kernel(cons
     return;
   }
   if (sp.nt == 0) {
-    if (u == 0) empty_row<T>(a, b);
+    if (u == 0) empty_row<T, PRE>(a, b);
     return;
   }
   const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
-  segment<T, W, DP>(a, reinterpret_cast<Merge<W, DP>*>(smem), b, hk, h0,
+  segment<T, W, DP, PRE>(a, reinterpret_cast<Merge<W, DP>*>(smem), b, hk, h0,
                     min(kHeads, (hk + 1) * a.G - h0), sp, 0, sp.nt, -1);
 }
 
@@ -431,7 +491,7 @@ __device__ __forceinline__ unsigned share_of(unsigned total, unsigned blocks, un
   return x < big ? x / (q + 1) : r + (x - big) / q;   // q > 0 where x >= big
 }
 
-template <class T, int DP>
+template <class T, int DP, bool PRE>
 __global__ void __launch_bounds__(32 * kShareWarps, kResident)
     decode_paged_share_kernel(const DecodeArgs a) {
   using M = Merge<kShareWarps, DP>;
@@ -445,7 +505,7 @@ __global__ void __launch_bounds__(32 * kShareWarps, kResident)
   const unsigned total = scan_tiles<kShareWarps>(a, prefix, blockIdx.x == 0) * per_row;
   for (int b = blockIdx.x; b < a.B; b += a.blocks) {
     const Span sp = span_of(a, b);
-    if (sp.n == 0 && sp.nt == 0) empty_row<T>(a, b);
+    if (sp.n == 0 && sp.nt == 0) empty_row<T, PRE>(a, b);
   }
   unsigned x = share_begin(total, a.blocks, blockIdx.x);
   const unsigned end = share_begin(total, a.blocks, blockIdx.x + 1);
@@ -463,14 +523,14 @@ __global__ void __launch_bounds__(32 * kShareWarps, kResident)
     // Slot 0: a unit begun by an earlier block (the share's first); slot 1: one begun here and
     // continued by the next (its last).
     const int slot = t0 > 0 ? 0 : (t1 < sp.nt ? 1 : -1);
-    segment<T, kShareWarps, DP>(a, sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, t0, t1, slot);
+    segment<T, kShareWarps, DP, PRE>(a, sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, t0, t1, slot);
     x += t1 - t0;
   }
 }
 
-// Joins the results of a row and query head: the shares of the blocks that had its unit (nothing to
-// do where one block finished it), and the prefix's parts. W warps each, taking every W-th part.
-template <class T, int W>
+// Joins the shares of a row and query head that several blocks had (nothing to do where one block
+// finished it), and the prefix's parts. W warps each, taking every W-th share.
+template <class T, int W, bool PRE>
 __global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float4 rest_y[8][32];
@@ -481,7 +541,7 @@ __global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs
   if (gated_off(a.skip)) return;
   const int lane = threadIdx.x & 31;
   const unsigned per_row = a.Hkv * a.HT;
-  const unsigned total = a.blocks ? scan_tiles<8>(a, prefix, false) * per_row : 0;
+  const unsigned total = scan_tiles<8>(a, prefix, false) * per_row;
   const int warp = threadIdx.x / 32, w = warp % W;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (8 / W) + warp / W;
   if (row >= static_cast<int64_t>(a.B) * a.H) return;   // with W = 8 all of a block or none
@@ -489,81 +549,32 @@ __global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs
   const Span sp = span_of(a, b);
   if (sp.n < 0) return;
   const int hk = head / a.G, g = head - hk * a.G, h = g % kHeads;
-  unsigned i0 = 0, own = sp.nt > 0 ? 1 : 0;   // first block, and how many had the unit
-  if (a.blocks && sp.nt > 0) {
+  unsigned i0 = 0, own = 0;                   // first block, and how many had the unit
+  if (sp.nt > 0) {
     const unsigned x0 = prefix[b] * per_row + (hk * a.HT + g / kHeads) * sp.nt;
     i0 = share_of(total, a.blocks, x0);
     own = share_of(total, a.blocks, x0 + sp.nt - 1) - i0 + 1;
   }
-  if (own <= 1 && a.prefix.nsplit == 0) return;
-  const unsigned parts = own + a.prefix.nsplit;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.H;
-  // Part i's place: the row's shares (or its one result), then the prefix's splits.
-  auto part = [&](unsigned i, const float2*& ml, const float*& o) {
-    int64_t at = row;
-    const float *base = a.own_o;
-    const float2 *base_ml = a.own_ml;
-    if (i >= own) {
-      base = a.prefix.o;
-      base_ml = a.prefix.ml;
-      at += (i - own) * rows;
-    } else if (own > 1) {
-      base = a.part_o;
-      base_ml = a.part_ml;
-      at = (static_cast<int64_t>(i0 + i) * 2 + (i == 0)) * kHeads + h;
-    }
-    o = base + at * a.D;
-    ml = base_ml + at;
-  };
+  if (own <= 1) return;                       // one block had it whole, or there is none
   const int d = 4 * lane;
   float top = -INFINITY, sum = 0.f;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  // 32 parts at a time, a lane each; then their rows, eight loads on their way at once (one after
-  // the other 38 parts took 20 us).
-  const unsigned todo = w < parts ? (parts - w + W - 1) / W : 0;
-#pragma unroll 1
-  for (unsigned s0 = 0; s0 < todo; s0 += 32) {
-    const unsigned n = min(32u, todo - s0);
-    const float2* ml;
-    const float* o;
-    part(w + W * (s0 + min(static_cast<unsigned>(lane), n - 1)), ml, o);
-    const float2 mine = lane < n ? *ml : make_float2(-INFINITY, 0.f);
-    const float before = top;
-    top = fmaxf(top, warp_max(mine.x));
-    const float f = mine.y == 0.f ? 0.f : tc::ex2(mine.x - top) * mine.y;
-    if (before != top && before != -INFINITY) {
-      const float r = tc::ex2(before - top);
-      sum *= r;
-      y.x *= r; y.y *= r; y.z *= r; y.w *= r;
-    }
-    sum += warp_sum(f);
-#pragma unroll 1
-    for (unsigned i = 0; i < n; i += 8) {
-      float4 p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float* from = reinterpret_cast<const float*>(__shfl_sync(
-            0xffffffffu, reinterpret_cast<unsigned long long>(o), min(i + e, n - 1)));
-        p[e] = d < a.D ? *reinterpret_cast<const float4*>(from + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float fi = __shfl_sync(0xffffffffu, f, min(i + e, 31u));
-        if (i + e < n) {
-          y.x = fmaf(fi, p[e].x, y.x); y.y = fmaf(fi, p[e].y, y.y);
-          y.z = fmaf(fi, p[e].z, y.z); y.w = fmaf(fi, p[e].w, y.w);
-        }
-      }
-    }
-  }
+  add_parts(
+      [&](unsigned i, const float2*& ml, const float*& o) {
+        const unsigned p = w + W * i;
+        const int64_t at = (static_cast<int64_t>(i0 + p) * 2 + (p == 0)) * kHeads + h;
+        ml = a.part_ml + at;
+        o = a.part_o + at * a.D;
+      },
+      w < own ? (own - w + W - 1) / W : 0, d, a.D, y, top, sum);
   if (W > 1) {
     rest_y[warp][lane] = y;
     if (lane == 0) rest_ml[warp] = make_float2(top, sum);
     __syncthreads();
     if (w > 0) return;
     const float2 ml = lane < W ? rest_ml[lane] : make_float2(-INFINITY, 0.f);
-    const float all = warp_max(ml.x);
-    const float f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - all);
+    top = warp_max(ml.x);
+    const float f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - top);
     sum = warp_sum(f * ml.y);
     y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -574,9 +585,7 @@ __global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs
       y.z = fmaf(fi, p.z, y.z); y.w = fmaf(fi, p.w, y.w);
     }
   }
-  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
-  if (d < a.D)
-    store_out<T>(a, b, head, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+  finish_row<T, PRE>(a, b, head, d, y, top, sum);
 }
 
 // Shared memory past 48 KB is an attribute of the kernel in each device's context.
@@ -591,45 +600,57 @@ cudaError_t allow_smem(size_t bytes) {
       cudaErrorInvalidDevice, [](cudaError_t r) { return r == cudaSuccess; });
 }
 
-template <class T, int W, int DP>
+template <class T, int W, int DP, bool PRE>
 cudaError_t launch_units(const DecodeArgs& a, unsigned units, cudaStream_t stream) {
   constexpr size_t smem = sizeof(Merge<W, DP>);
-  const cudaError_t e = allow_smem<decode_paged_units_kernel<T, W, DP>>(smem);
+  const cudaError_t e = allow_smem<decode_paged_units_kernel<T, W, DP, PRE>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_paged_units_kernel<T, W, DP>, units, 32 * W, smem, stream, a);
+  return launch_dependent(decode_paged_units_kernel<T, W, DP, PRE>, units, 32 * W, smem, stream, a);
 }
 
-template <class T, int DP>
+template <class T, int DP, bool PRE>
 cudaError_t launch_dp(const DecodeArgs& a, int warps, cudaStream_t stream) {
   const unsigned units = static_cast<unsigned>(a.B) * a.Hkv * a.HT;
   cudaError_t e;
   size_t scan = 0;
   if (a.blocks == 0) {
-    e = warps == kWideWarps ? launch_units<T, kWideWarps, DP>(a, units, stream)
-                            : launch_units<T, kShareWarps, DP>(a, units, stream);
+    e = warps == kWideWarps   ? launch_units<T, kWideWarps, DP, PRE>(a, units, stream)
+        : warps == kSlimWarps ? launch_units<T, kSlimWarps, DP, PRE>(a, units, stream)
+                              : launch_units<T, kShareWarps, DP, PRE>(a, units, stream);
   } else {
     using M = Merge<kShareWarps, DP>;
     scan = static_cast<size_t>(a.B) * sizeof(unsigned);
-    e = allow_smem<decode_paged_share_kernel<T, DP>>(sizeof(M) + kMaxScanRows * sizeof(unsigned));
+    e = allow_smem<decode_paged_share_kernel<T, DP, PRE>>(sizeof(M) + kMaxScanRows * sizeof(unsigned));
     if (e == cudaSuccess)
-      e = launch_dependent(decode_paged_share_kernel<T, DP>, a.blocks, 32 * kShareWarps,
+      e = launch_dependent(decode_paged_share_kernel<T, DP, PRE>, a.blocks, 32 * kShareWarps,
                            sizeof(M) + scan, stream, a);
   }
-  if (e != cudaSuccess || (a.blocks == 0 && a.prefix.nsplit == 0)) return e;
-  // A unit's shares, about: past a dozen parts a row gets a block of its own.
+  if (e != cudaSuccess || a.blocks == 0) return e;
+  // A unit's shares, about: past a dozen a row gets a block of its own.
   const int64_t rows = static_cast<int64_t>(a.B) * a.H;
-  const bool wide = a.blocks / units + a.prefix.nsplit > 12;
-  return wide ? launch_dependent(decode_paged_join_kernel<T, 8>, static_cast<unsigned>(rows), 256,
+  const bool wide = a.blocks / units > 12;
+  return wide ? launch_dependent(decode_paged_join_kernel<T, 8, PRE>, static_cast<unsigned>(rows), 256,
                                  scan, stream, a)
-              : launch_dependent(decode_paged_join_kernel<T, 1>,
+              : launch_dependent(decode_paged_join_kernel<T, 1, PRE>,
                                  static_cast<unsigned>((rows + 7) / 8), 256, scan, stream, a);
 }
 
 }  // namespace
 
+namespace {
+template <class T>
+cudaError_t launch_type(const DecodeArgs& a, int warps, cudaStream_t stream) {
+  if (a.D <= 64)
+    return a.prefix.nsplit ? launch_dp<T, 64, true>(a, warps, stream)
+                           : launch_dp<T, 64, false>(a, warps, stream);
+  return a.prefix.nsplit ? launch_dp<T, 128, true>(a, warps, stream)
+                         : launch_dp<T, 128, false>(a, warps, stream);
+}
+}  // namespace
+
 // One block per unit where no row has more than 4 tiles a warp (8 of up to 64 dims) -- 8 warps (512
 // slots), or 16 (1024) where every unit can have an SM to itself --, else blocks that share all
-// tiles. Measured, one row, 8 kv heads of 4, us with 16 warps a unit and shared out: 500 slots
+// tiles. Units that would not all be resident with 8 warps take 4. Measured, one row, 8 kv heads of 4, us with 16 warps a unit and shared out: 500 slots
 // 8.3, 9.7; 1000 12.1, 12.6; 2000 20, 14; 8000 68, 21.
 DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int D, int max_len, int window,
                                   int prefix_len) {
@@ -640,7 +661,8 @@ DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int D, int max_len, int
   const int per_warp = D <= 64 ? 8 : 4;
   if (tiles <= per_warp * kWideWarps && units <= kSms)
     return {0, tiles <= kShareWarps ? kShareWarps : kWideWarps};
-  if (tiles <= per_warp * kShareWarps || B > kMaxScanRows) return {0, kShareWarps};
+  if (tiles <= per_warp * kShareWarps || B > kMaxScanRows)
+    return {0, units > kSms * kResident ? kSlimWarps : kShareWarps};
   const int64_t most = kSms * kResident, want = (units * tiles + kShareWarps - 1) / kShareWarps;
   return {static_cast<int>(want < most ? want : most), kShareWarps};
 }
@@ -671,19 +693,14 @@ cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
   a.prefix_table = j.prefix_table;
   a.prefix_len = j.prefix_len;
   a.prefix = j.prefix;
-  a.own_o = j.own_o;
-  a.own_ml = j.own_ml;
   const DecodePagedPlan plan =
       decode_paged_plan(j.B, j.H, j.Hkv, j.D, j.max_len, j.window, j.prefix_len);
   a.blocks = plan.blocks;
   a.part_o = j.partial;
   a.part_ml = reinterpret_cast<float2*>(j.partial + static_cast<size_t>(a.blocks) * 2 * kHeads * j.D);
   a.status = j.status; a.skip = j.skip;
-  if (j.D <= 64)
-    return j.bf16 ? launch_dp<__nv_bfloat16, 64>(a, plan.warps, stream)
-                  : launch_dp<__half, 64>(a, plan.warps, stream);
-  return j.bf16 ? launch_dp<__nv_bfloat16, 128>(a, plan.warps, stream)
-                : launch_dp<__half, 128>(a, plan.warps, stream);
+  return j.bf16 ? launch_type<__nv_bfloat16>(a, plan.warps, stream)
+                : launch_type<__half>(a, plan.warps, stream);
 }
 
 }  // namespace gqa
