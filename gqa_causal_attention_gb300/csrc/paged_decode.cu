@@ -6,10 +6,13 @@
 // one pass over keys and values with a running reference m, sums in fp32.
 //
 // * Memory bound: every key and value is read once for the (up to 8) query heads of a unit, 4 D
-//   bytes and 4 G D flops a position. Keys and values go from global memory straight into the
-//   operands of m16n8k16 products: a lane's 16-byte loads are made the operand's layout by
-//   taking the head dims (the products' inner or outer index) in an order of their own, and
-//   pairs of value rows by one byte permutation a register. No shared memory, no transposition.
+//   bytes and 4 G D flops a position. Each warp has a ring of tiles (16 positions, their keys and
+//   values) of its own in shared memory, filled by TMA three tiles ahead, so that 190 KB are on
+//   their way to an SM at a time whatever its warps do (loads into registers, half as much:
+//   64 rows of 512..8192 slots 197 us). In the 128-byte swizzle, with the tile's rows taken in an
+//   order that keeps eight lanes on eight banks, a lane's 16 bytes are operands of m16n8k16
+//   products as they lie: the products' inner and outer dims are taken in an order of their own,
+//   and pairs of value rows made by one byte permutation a register.
 //     scores S[key, head] = K Q^T      A = 16 keys, B = 8 heads of Q
 //     O[dim, head] += V^T P^T          A = value pairs, B = P, its 8 x 8 blocks transposed by movmatrix
 // * P is split in two 16-bit parts, so its rounding (2^-8 in bf16) does not add to the output's.
@@ -20,8 +23,10 @@
 //   and nothing is left to join (one row of 500 slots: 12.2 us shared out, see decode_paged_plan).
 // * With a prefix that all rows share, either its partial results (from the tensor cores) are joined
 //   here too, or, where it is read a few times only, its tiles come before the row's own.
+#include <type_traits>
+
 #include "paged.cuh"
-#include "tc_ptx.cuh"
+#include "prefill_common.cuh"
 
 namespace gqa {
 
@@ -29,10 +34,12 @@ namespace {
 
 constexpr int kTile = 16;                     // positions per warp step (never across pages)
 constexpr int kSms = 152;
-constexpr int kShareWarps = 8;                // a block that takes a share; two of them per SM
+constexpr int kRing = 3;                       // tiles on their way per warp
+// Warps of a block that takes a share, or one of many units (two such blocks per SM), and of a
+// block alone on its SM: 96 and 192 KB of rings.
+__host__ __device__ constexpr int warps_of(int D) { return D <= 64 ? 8 : 4; }
+__host__ __device__ constexpr int wide_warps_of(int D) { return 2 * warps_of(D); }
 constexpr int kResident = 2;
-constexpr int kWideWarps = 16;                // a block alone on its SM
-constexpr int kSlimWarps = 4;                 // four of them per SM
 constexpr int kHeads = 8;                     // query heads of a unit
 constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
 constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps
@@ -105,18 +112,29 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Streamed once: 16 bytes past L1.
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
 template <int W, int DP>
 struct __align__(16) Merge {                  // one block's warps, then its result
   float o[W][kHeads][DP + 4];
   float m[W][kHeads], l[W][kHeads];
+};
+
+// A block's shared memory: rings, which the merge takes over once their tiles are done.
+template <int W, int DP>
+struct Smem {
+  static constexpr int kBox = kTile * 128;    // 16 positions x 64 dims
+  static constexpr int kStage = 2 * (DP / 64) * kBox;   // keys, then values
+  union {
+    uint8_t ring[W][kRing][kStage];
+    Merge<W, DP> merge;
+  };
+  uint64_t full[W][kRing];
+  int abort;
+  static_assert(sizeof(Merge<W, DP>) <= W * kRing * kStage, "the merge fits in the rings");
+};
+
+// A warp's ring: tiles asked for and taken so far (stage = count % kRing, parity of its turns).
+struct Ring {
+  uint32_t asked = 0, taken = 0;
 };
 
 // Output row of query head `head`, dims d .. d + 3.
@@ -194,15 +212,49 @@ __device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int head,
 // goes, with the prefix's parts, to the output when whole (slot < 0), else to partial slot `slot`
 // of this block.
 template <class T, int W, int DP, bool PRE>
-__device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, int h0, int nh,
-                        const Span& sp, int t0, int t1, int slot) {
-  constexpr int KC = DP / 32, VH = DP / 64;
+__device__ void segment(const DecodeArgs& a, const CUtensorMap* tk, const CUtensorMap* tv,
+                        Smem<W, DP>* sm, Ring& ring, int b, int hk, int h0, int nh, const Span& sp,
+                        int t0, int t1, int slot) {
+  constexpr int KC = DP / 32, VH = DP / 64, kBox = Smem<W, DP>::kBox;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const T* kbase = static_cast<const T*>(a.k) + hk * a.head_stride;
-  const T* vbase = static_cast<const T*>(a.v) + hk * a.head_stride;
   const int32_t* table = a.block_table + b * a.width;
   const int page_mask = (1 << a.page_shift) - 1;
+  volatile int* abort = &sm->abort;
+
+  int ids = -1, ids_at = -1;                  // page of the warp's tile ids_at + W * lane
+  uint32_t bad = 0;                           // stages whose tile has no page
+  // The first position of a tile in its table, the prefix's or the row's own.
+  auto first_pos = [&](int tile) { return (tile < sp.pt ? tile : sp.t0 + tile - sp.pt) * kTile; };
+  auto ask = [&](int tile) {
+    if (ids_at < 0 || tile >= ids_at + 32 * W) {
+      ids_at = tile;
+      const int mine = tile + W * lane;
+      ids = 0;
+      if (mine < t1)
+        ids = (mine < sp.pt ? a.prefix_table : table)[first_pos(mine) >> a.page_shift];
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, (tile - ids_at) / W);
+    const uint32_t st = ring.asked % kRing;
+    const bool there = id >= 0 && id < a.pages;
+    bad = there ? bad & ~(1u << st) : bad | 1u << st;
+    if (lane == 0) {
+      if (!there) report(a.status, ATTN_DEV_PAGE);   // page 0 is read and not used
+      uint64_t* full = &sm->full[warp][st];
+      uint8_t* dst = sm->ring[warp][st];
+      const int at = first_pos(tile) & page_mask, page = there ? id : 0;
+      tc::mbar_arrive_expect_tx(full, 2 * VH * kBox);
+#pragma unroll
+      for (int h = 0; h < VH; ++h) {
+        tc::tma_load_4d(dst + h * kBox, tk, full, 64 * h, at, hk, page);
+        tc::tma_load_4d(dst + (VH + h) * kBox, tv, full, 64 * h, at, hk, page);
+      }
+    }
+    ++ring.asked;
+  };
+  int next = t0 + warp;                       // the next tile to ask for
+  if (!__any_sync(0xffffffffu, *abort))
+    for (int i = 0; i < kRing && next < t1; ++i, next += W) ask(next);
 
   uint4 qf[KC];
 #pragma unroll
@@ -222,67 +274,35 @@ __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, in
       for (int e = 0; e < 4; ++e) o[h][m][e] = 0.f;
   float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // heads 2 t, 2 t + 1 (l: this lane's keys)
 
-  int ids = -1, ids_at = -1;                  // page of the warp's tile ids_at + W * lane
-  uint4 kf[2][KC], vf[VH][4];
-  int64_t off = -1;                           // of the tile whose loads are on their way
-  // The first position of a tile in its table, the prefix's or the row's own.
-  auto first_pos = [&](int tile) { return (tile < sp.pt ? tile : sp.t0 + tile - sp.pt) * kTile; };
-  auto locate = [&](int tile) {               // element offset of the tile's first slot, < 0: none
-    if (ids_at < 0 || tile >= ids_at + 32 * W) {
-      ids_at = tile;
-      const int mine = tile + W * lane;
-      ids = 0;
-      if (mine < t1)
-        ids = (mine < sp.pt ? a.prefix_table : table)[first_pos(mine) >> a.page_shift];
-    }
-    const int id = __shfl_sync(0xffffffffu, ids, (tile - ids_at) / W);
-    if (id < 0 || id >= a.pages) {
-      if (lane == 0) report(a.status, ATTN_DEV_PAGE);
-      off = -1;
-      return;
-    }
-    off = id * a.page_stride + static_cast<int64_t>(first_pos(tile) & page_mask) * a.D;
-  };
-  auto load_k = [&]() {
+  // The products' key g is the tile's row g ^ 4 (g & 1) (and 8 more): rows of neighbouring g are then
+  // four apart in the swizzle, and a quarter warp's reads of keys or values meet no bank twice.
+  const int row_k = g ^ (g & 1) << 2;
+  auto swizzled = [](int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); };
+#pragma unroll 1
+  for (int tile = t0 + warp; tile < t1; tile += W) {
+    const uint32_t st = ring.taken % kRing;
+    if (ring.taken == ring.asked) break;      // a wait ran out before
+    const bool ok = tc::mbar_wait_short(&sm->full[warp][st], ring.taken / kRing & 1, abort);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    ++ring.taken;
+    const uint8_t* base = sm->ring[warp][st];
+    const bool there = !(bad >> st & 1);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};        // keys of rows g, g, g + 8, g + 8, heads 2 t, 2 t + 1
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const int d = 32 * c + 8 * t;
-        kf[i][c] = off >= 0 && d < a.D ? ld_stream(kbase + off + (8 * i + g) * a.D + d)
-                                       : make_uint4(0, 0, 0, 0);
-      }
-  };
-  auto load_v = [&]() {
+    for (int c = 0; c < KC; ++c) {
+      const uint8_t* at = base + (c / 2) * kBox;
+      const uint4 k0 = *reinterpret_cast<const uint4*>(at + swizzled(row_k, (c & 1) * 4 + t));
+      const uint4 k1 = *reinterpret_cast<const uint4*>(at + swizzled(row_k + 8, (c & 1) * 4 + t));
+      mma16816<T>(x, k0.x, k1.x, k0.y, k1.y, qf[c].x, qf[c].y);
+      mma16816<T>(x, k0.z, k1.z, k0.w, k1.w, qf[c].z, qf[c].w);
+    }
+    uint4 vf[VH][4];
+    const int row_v[4] = {2 * t, (2 * t + 1) ^ 4, 2 * t + 8, ((2 * t + 1) ^ 4) + 8};
 #pragma unroll
     for (int h = 0; h < VH; ++h)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = 64 * h + 8 * g, key = 2 * t + (r & 1) + 8 * (r >> 1);
-        vf[h][r] = off >= 0 && d < a.D ? ld_stream(vbase + off + key * a.D + d)
-                                       : make_uint4(0, 0, 0, 0);
-      }
-  };
-
-  int tile = t0 + warp;
-  if (tile < t1) {
-    locate(tile);
-    load_k();
-    load_v();
-  }
-  for (; tile < t1; tile += W) {
-    const bool there = off >= 0;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};        // keys g, g, g + 8, g + 8 of heads 2 t, 2 t + 1
-#pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      mma16816<T>(x, kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qf[c].x, qf[c].y);
-      mma16816<T>(x, kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qf[c].z, qf[c].w);
-    }
-    const bool more = tile + W < t1;
-    if (more) {
-      locate(tile + W);
-      load_k();
-    }
+      for (int r = 0; r < 4; ++r)
+        vf[h][r] = *reinterpret_cast<const uint4*>(base + (VH + h) * kBox + swizzled(row_v[r], g));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (a.softcap_on) {
@@ -297,7 +317,7 @@ __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, in
     if (tile0 < lo || tile0 > end - kTile || !there) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = tile0 + g + 8 * (e >> 1), mine = tile0 + 2 * t + (e & 1) + 8 * (e >> 1);
+        const int key = tile0 + row_k + 8 * (e >> 1), mine = tile0 + row_v[e];
         if (key < lo || key >= end || !there) x[e] = -INFINITY;
         // an unused slot may hold anything, which a weight of 0 would still pass on
         if (mine < lo || mine >= end || !there) {
@@ -305,6 +325,11 @@ __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, in
           for (int h = 0; h < VH; ++h) vf[h][e] = make_uint4(0, 0, 0, 0);
         }
       }
+    }
+    __syncwarp();                             // the stage has been read
+    if (next < t1) {
+      ask(next);
+      next += W;
     }
     const float ref0 = m_ref[0] + kGrow, ref1 = m_ref[1] + kGrow;   // -inf stays -inf
     const float max0 = fmaxf(x[0], x[2]), max1 = fmaxf(x[1], x[3]);
@@ -360,15 +385,21 @@ __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, in
         mma16816<T>(o[h][m], a0, a1, a2, a3, rest[0], rest[1]);
       }
     }
-    if (more) load_v();
   }
+  // After a wait that ran out: copies still on their way land before the rings are used again.
+  if (ring.taken != ring.asked) {
+    for (; ring.taken != ring.asked; ++ring.taken)
+      tc::mbar_drain(&sm->full[warp][ring.taken % kRing], ring.taken / kRing & 1);
+    if (lane == 0) report(a.status, ATTN_DEV_TIMEOUT);
+  }
+  Merge<W, DP>* sh = &sm->merge;
 
   // The block's warps: weights, then dims.
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-  __syncthreads();                            // an earlier segment's sums have been read
+  __syncthreads();                            // every warp is done with its ring
   if (g == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -416,6 +447,15 @@ __device__ void segment(const DecodeArgs& a, Merge<W, DP>* sh, int b, int hk, in
   }
 }
 
+// The rings' barriers; whole block.
+template <int W, int DP>
+__device__ __forceinline__ void init_rings(Smem<W, DP>* sm) {
+  if (threadIdx.x < W * kRing) tc::mbar_init(&sm->full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x == 0) sm->abort = 0;
+  tc::fence_mbar_init();
+  __syncthreads();
+}
+
 // A row without any position of its own: zeros, or its prefix alone.
 template <class T, bool PRE>
 __device__ __noinline__ void empty_row(const DecodeArgs& a, int b) {
@@ -423,10 +463,23 @@ __device__ __noinline__ void empty_row(const DecodeArgs& a, int b) {
     finish_row<T, PRE>(a, b, head, 4 * (threadIdx.x & 31), make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
 }
 
+template <class S>
+__device__ __forceinline__ S* aligned_smem(uint8_t* raw) {   // 1024 bytes: the swizzle's period
+  return reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
 // One block per unit (row, kv head, group of up to 8 query heads).
 template <class T, int W, int DP, bool PRE>
-__global__ void __launch_bounds__(32 * W, 16 / W) decode_paged_units_kernel(const DecodeArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? kResident : 1)
+    decode_paged_units_kernel(const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ CUtensorMap tv, const DecodeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  auto* sm = aligned_smem<Smem<W, DP>>(smem_raw);
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch(&tk);
+    tc::tma_prefetch(&tv);
+  }
+  init_rings(sm);
   dependent_wait();
   dependents_may_launch();
   if (gated_off(a.skip)) return;
@@ -442,8 +495,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_paged_units_kernel(cons
     return;
   }
   const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
-  segment<T, W, DP, PRE>(a, reinterpret_cast<Merge<W, DP>*>(smem), b, hk, h0,
-                    min(kHeads, (hk + 1) * a.G - h0), sp, 0, sp.nt, -1);
+  Ring ring;
+  segment<T, W, DP, PRE>(a, &tk, &tv, sm, ring, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, 0,
+                         sp.nt, -1);
 }
 
 // prefix[b]: tiles of rows before b; returns their total. Whole block of W warps. (The tiles of all
@@ -492,21 +546,28 @@ __device__ __forceinline__ unsigned share_of(unsigned total, unsigned blocks, un
 }
 
 template <class T, int DP, bool PRE>
-__global__ void __launch_bounds__(32 * kShareWarps, kResident)
-    decode_paged_share_kernel(const DecodeArgs a) {
-  using M = Merge<kShareWarps, DP>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  M* sh = reinterpret_cast<M*>(smem);
-  unsigned* prefix = reinterpret_cast<unsigned*>(smem + sizeof(M));
+__global__ void __launch_bounds__(32 * warps_of(DP), kResident)
+    decode_paged_share_kernel(const __grid_constant__ CUtensorMap tk,
+                              const __grid_constant__ CUtensorMap tv, const DecodeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr int W = warps_of(DP);
+  auto* sm = aligned_smem<Smem<W, DP>>(smem_raw);
+  unsigned* prefix = reinterpret_cast<unsigned*>(sm + 1);
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch(&tk);
+    tc::tma_prefetch(&tv);
+  }
+  init_rings(sm);
   dependent_wait();
   dependents_may_launch();
   if (gated_off(a.skip)) return;
   const unsigned per_row = a.Hkv * a.HT;
-  const unsigned total = scan_tiles<kShareWarps>(a, prefix, blockIdx.x == 0) * per_row;
+  const unsigned total = scan_tiles<W>(a, prefix, blockIdx.x == 0) * per_row;
   for (int b = blockIdx.x; b < a.B; b += a.blocks) {
     const Span sp = span_of(a, b);
     if (sp.n == 0 && sp.nt == 0) empty_row<T, PRE>(a, b);
   }
+  Ring ring;
   unsigned x = share_begin(total, a.blocks, blockIdx.x);
   const unsigned end = share_begin(total, a.blocks, blockIdx.x + 1);
 #pragma unroll 1
@@ -523,8 +584,11 @@ __global__ void __launch_bounds__(32 * kShareWarps, kResident)
     // Slot 0: a unit begun by an earlier block (the share's first); slot 1: one begun here and
     // continued by the next (its last).
     const int slot = t0 > 0 ? 0 : (t1 < sp.nt ? 1 : -1);
-    segment<T, kShareWarps, DP, PRE>(a, sh, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, t0, t1, slot);
+    segment<T, W, DP, PRE>(a, &tk, &tv, sm, ring, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp,
+                           t0, t1, slot);
     x += t1 - t0;
+    tc::fence_proxy_async();                  // the merge's writes come before the next tiles
+    __syncthreads();
   }
 }
 
@@ -600,30 +664,52 @@ cudaError_t allow_smem(size_t bytes) {
       cudaErrorInvalidDevice, [](cudaError_t r) { return r == cudaSuccess; });
 }
 
+// A pool [pages, Hkv, page, D]: boxes of 64 dims x one tile.
+bool map_tiles(CUtensorMap* m, const void* p, bool bf16, const DecodeArgs& a) {
+  auto enc = prefill::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t page = 1ull << a.page_shift;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), page, static_cast<cuuint64_t>(a.Hkv),
+                              static_cast<cuuint64_t>(a.pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.D) * 2, page * a.D * 2,
+                                 static_cast<cuuint64_t>(a.page_stride) * 2};
+  const cuuint32_t box[4] = {64, kTile, 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class T, int W, int DP, bool PRE>
-cudaError_t launch_units(const DecodeArgs& a, unsigned units, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(Merge<W, DP>);
+cudaError_t launch_units(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                         unsigned units, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(Smem<W, DP>) + 1024;
   const cudaError_t e = allow_smem<decode_paged_units_kernel<T, W, DP, PRE>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_paged_units_kernel<T, W, DP, PRE>, units, 32 * W, smem, stream, a);
+  return launch_dependent(decode_paged_units_kernel<T, W, DP, PRE>, units, 32 * W, smem, stream, tk,
+                          tv, a);
 }
 
 template <class T, int DP, bool PRE>
 cudaError_t launch_dp(const DecodeArgs& a, int warps, cudaStream_t stream) {
+  constexpr bool kBf16 = !std::is_same<T, __half>::value;
+  CUtensorMap tk, tv;
+  if (!map_tiles(&tk, a.k, kBf16, a) || !map_tiles(&tv, a.v, kBf16, a)) return cudaErrorInvalidValue;
   const unsigned units = static_cast<unsigned>(a.B) * a.Hkv * a.HT;
   cudaError_t e;
   size_t scan = 0;
   if (a.blocks == 0) {
-    e = warps == kWideWarps   ? launch_units<T, kWideWarps, DP, PRE>(a, units, stream)
-        : warps == kSlimWarps ? launch_units<T, kSlimWarps, DP, PRE>(a, units, stream)
-                              : launch_units<T, kShareWarps, DP, PRE>(a, units, stream);
+    e = warps == wide_warps_of(DP)
+            ? launch_units<T, wide_warps_of(DP), DP, PRE>(a, tk, tv, units, stream)
+            : launch_units<T, warps_of(DP), DP, PRE>(a, tk, tv, units, stream);
   } else {
-    using M = Merge<kShareWarps, DP>;
+    constexpr int W = warps_of(DP);
+    constexpr size_t smem = sizeof(Smem<W, DP>) + 1024;
     scan = static_cast<size_t>(a.B) * sizeof(unsigned);
-    e = allow_smem<decode_paged_share_kernel<T, DP, PRE>>(sizeof(M) + kMaxScanRows * sizeof(unsigned));
+    e = allow_smem<decode_paged_share_kernel<T, DP, PRE>>(smem + kMaxScanRows * sizeof(unsigned));
     if (e == cudaSuccess)
-      e = launch_dependent(decode_paged_share_kernel<T, DP, PRE>, a.blocks, 32 * kShareWarps,
-                           sizeof(M) + scan, stream, a);
+      e = launch_dependent(decode_paged_share_kernel<T, DP, PRE>, a.blocks, 32 * W, smem + scan,
+                           stream, tk, tv, a);
   }
   if (e != cudaSuccess || a.blocks == 0) return e;
   // A unit's shares, about: past a dozen a row gets a block of its own.
@@ -648,23 +734,20 @@ cudaError_t launch_type(const DecodeArgs& a, int warps, cudaStream_t stream) {
 }
 }  // namespace
 
-// One block per unit where no row has more than 4 tiles a warp (8 of up to 64 dims) -- 8 warps (512
-// slots), or 16 (1024) where every unit can have an SM to itself --, else blocks that share all
-// tiles. Units that would not all be resident with 8 warps take 4. Measured, one row, 8 kv heads of 4, us with 16 warps a unit and shared out: 500 slots
-// 8.3, 9.7; 1000 12.1, 12.6; 2000 20, 14; 8000 68, 21.
+// One block per unit where no row has more than 8 tiles a warp, the block alone on its SM where all
+// units can be; else blocks that share all tiles. Measured, one row, 8 kv heads of 4 heads of 128,
+// us with a wide block a unit and shared out: 500 slots 6.8, 9.7; 1000 10.3, 11; 2000 17, 11.1.
 DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int D, int max_len, int window,
                                   int prefix_len) {
   const int G = H / Hkv;
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + kHeads - 1) / kHeads);
   const int64_t own = window > 0 && window < max_len ? window + kTile - 1 : max_len;
   const int64_t tiles = (own + kTile - 1) / kTile + (prefix_len + kTile - 1) / kTile;
-  const int per_warp = D <= 64 ? 8 : 4;
-  if (tiles <= per_warp * kWideWarps && units <= kSms)
-    return {0, tiles <= kShareWarps ? kShareWarps : kWideWarps};
-  if (tiles <= per_warp * kShareWarps || B > kMaxScanRows)
-    return {0, units > kSms * kResident ? kSlimWarps : kShareWarps};
-  const int64_t most = kSms * kResident, want = (units * tiles + kShareWarps - 1) / kShareWarps;
-  return {static_cast<int>(want < most ? want : most), kShareWarps};
+  const int warps = warps_of(D), wide = wide_warps_of(D);
+  if (tiles <= 8 * wide && units <= kSms) return {0, wide};
+  if (tiles <= 8 * warps || B > kMaxScanRows) return {0, warps};
+  const int64_t most = kSms * kResident, want = (units * tiles + warps - 1) / warps;
+  return {static_cast<int>(want < most ? want : most), warps};
 }
 
 // The partial results of the blocks' shares (part_ml follows part_o). Never shrinks as max_len grows.
