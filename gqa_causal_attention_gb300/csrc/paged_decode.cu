@@ -7,7 +7,7 @@
 //
 // * Memory bound: every key and value is read once for the (up to 8) query heads of a unit, 4 D
 //   bytes and 4 G D flops a position. Each warp has a ring of tiles (16 positions, their keys and
-//   values) of its own in shared memory, filled by TMA three tiles ahead, so that 190 KB are on
+//   values) of its own in shared memory, filled by TMA two or three tiles ahead, so that 190 KB are on
 //   their way to an SM at a time whatever its warps do (loads into registers, half as much:
 //   64 rows of 512..8192 slots 197 us). In the 128-byte swizzle, with the tile's rows taken in an
 //   order that keeps eight lanes on eight banks, a lane's 16 bytes are operands of m16n8k16
@@ -34,12 +34,16 @@ namespace {
 
 constexpr int kTile = 16;                     // positions per warp step (never across pages)
 constexpr int kSms = 152;
-constexpr int kRing = 3;                       // tiles on their way per warp
-// Warps of a block that takes a share, or one of many units (two such blocks per SM), and of a
-// block alone on its SM: 96 and 192 KB of rings.
+// Warps of a block that takes a share, or one of many units, how many such blocks an SM holds, and
+// those of a block alone on its SM; tiles on their way per warp: about 192 KB an SM. (8 rows of
+// 32768 slots, 8 kv heads of 8 heads of 128: two blocks of 4 warps, three tiles 171.5 us, three and
+// two 165. Heads of 64, where a tile is half as long: 15.7 and 18 for 23 rows of 1..5000.)
 __host__ __device__ constexpr int warps_of(int D) { return D <= 64 ? 8 : 4; }
 __host__ __device__ constexpr int wide_warps_of(int D) { return 2 * warps_of(D); }
-constexpr int kResident = 2;
+__host__ __device__ constexpr int resident_of(int D) { return D <= 64 ? 2 : 3; }
+__host__ __device__ constexpr int ring_of(int W, int D) {
+  return W == warps_of(D) && D > 64 ? 2 : 3;
+}
 constexpr int kHeads = 8;                     // query heads of a unit
 constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
 constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps
@@ -121,6 +125,7 @@ struct __align__(16) Merge {                  // one block's warps, then its res
 // A block's shared memory: rings, which the merge takes over once their tiles are done.
 template <int W, int DP>
 struct Smem {
+  static constexpr int kRing = ring_of(W, DP);
   static constexpr int kBox = kTile * 128;    // 16 positions x 64 dims
   static constexpr int kStage = 2 * (DP / 64) * kBox;   // keys, then values
   union {
@@ -132,7 +137,7 @@ struct Smem {
   static_assert(sizeof(Merge<W, DP>) <= W * kRing * kStage, "the merge fits in the rings");
 };
 
-// A warp's ring: tiles asked for and taken so far (stage = count % kRing, parity of its turns).
+// A warp's ring: tiles asked for and taken so far (stage: count % kRing, parity: of its turns).
 struct Ring {
   uint32_t asked = 0, taken = 0;
 };
@@ -215,7 +220,7 @@ template <class T, int W, int DP, bool PRE>
 __device__ void segment(const DecodeArgs& a, const CUtensorMap* tk, const CUtensorMap* tv,
                         Smem<W, DP>* sm, Ring& ring, int b, int hk, int h0, int nh, const Span& sp,
                         int t0, int t1, int slot) {
-  constexpr int KC = DP / 32, VH = DP / 64, kBox = Smem<W, DP>::kBox;
+  constexpr int KC = DP / 32, VH = DP / 64, kBox = Smem<W, DP>::kBox, kRing = Smem<W, DP>::kRing;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int32_t* table = a.block_table + b * a.width;
@@ -450,7 +455,7 @@ __device__ void segment(const DecodeArgs& a, const CUtensorMap* tk, const CUtens
 // The rings' barriers; whole block.
 template <int W, int DP>
 __device__ __forceinline__ void init_rings(Smem<W, DP>* sm) {
-  if (threadIdx.x < W * kRing) tc::mbar_init(&sm->full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x < W * Smem<W, DP>::kRing) tc::mbar_init(&sm->full[0][0] + threadIdx.x, 1);
   if (threadIdx.x == 0) sm->abort = 0;
   tc::fence_mbar_init();
   __syncthreads();
@@ -470,7 +475,7 @@ __device__ __forceinline__ S* aligned_smem(uint8_t* raw) {   // 1024 bytes: the 
 
 // One block per unit (row, kv head, group of up to 8 query heads).
 template <class T, int W, int DP, bool PRE>
-__global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? kResident : 1)
+__global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? resident_of(DP) : 1)
     decode_paged_units_kernel(const __grid_constant__ CUtensorMap tk,
                               const __grid_constant__ CUtensorMap tv, const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -546,7 +551,7 @@ __device__ __forceinline__ unsigned share_of(unsigned total, unsigned blocks, un
 }
 
 template <class T, int DP, bool PRE>
-__global__ void __launch_bounds__(32 * warps_of(DP), kResident)
+__global__ void __launch_bounds__(32 * warps_of(DP), resident_of(DP))
     decode_paged_share_kernel(const __grid_constant__ CUtensorMap tk,
                               const __grid_constant__ CUtensorMap tv, const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -746,7 +751,7 @@ DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int D, int max_len, int
   const int warps = warps_of(D), wide = wide_warps_of(D);
   if (tiles <= 8 * wide && units <= kSms) return {0, wide};
   if (tiles <= 8 * warps || B > kMaxScanRows) return {0, warps};
-  const int64_t most = kSms * kResident, want = (units * tiles + warps - 1) / warps;
+  const int64_t most = kSms * resident_of(D), want = (units * tiles + warps - 1) / warps;
   return {static_cast<int>(want < most ? want : most), warps};
 }
 
