@@ -601,9 +601,9 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
 }
 
-// Only a block's common path is unrolled; what is rare (masks, softcap, a new reference) works on
-// 32 columns at a time in rolled loops, on S in tensor memory: the roles' loops together have
-// to stay in the instruction caches (with all paths unrolled the kernel took 1.2 times as long).
+// Only a block's common path and its mask are unrolled; what is rarer (softcap, a block done again)
+// works on 32 columns at a time in rolled loops, on S in tensor memory: the roles' loops together
+// have to stay in the instruction caches (with all paths unrolled the kernel took 1.2 times as long).
 template <class C>
 __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sums, uint8_t* stage,
                         Bars* bars, int t, int quarter, int lane, uint32_t& n, uint32_t& outputs) {
@@ -637,41 +637,50 @@ __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sum
     const bool edge = k0 + kBK > u.nk ||
                       (!C::SHARED && (k0 + kBK - 1 > q_lo ||
                                       (a.window > 0 && k0 < q_hi - a.window + 1)));
-    // Chunks of 32 columns from `chunks` on hold no key of the tile.
-    const int chunks = min(4, (tile_keys - k0 + 31) / 32);
-    if (edge || a.softcap_on) {
-      const int hi = !edge ? kBK : (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;
-      const int lo = edge && !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : 0;
+    const int hi = !edge ? kBK : (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;
+    const int lo = edge && !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : 0;
+    auto seen = [&](int c0) { return bits_below(hi + 1 - c0) & ~bits_below(lo - c0); };   // of 32 columns
+    if (a.softcap_on) {                        // in place, in tensor memory, where the tile has keys
+      const int chunks = min(4, (tile_keys - k0 + 31) / 32);
 #pragma unroll 1
       for (int i = 0; i < chunks; ++i) {
         float x[32];
         tc::tmem_ld32(scol + 32 * i, x);
-        if (a.softcap_on) soft_cap(a, x, live);
-        const uint32_t seen = bits_below(hi + 1 - 32 * i) & ~bits_below(lo - 32 * i);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = seen >> c & 1 ? x[c] : -INFINITY;
+        soft_cap(a, x, live);
         tc::tmem_st32(scol + 32 * i, x);
       }
     }
-    bool written = false;
-    if (started && chunks == 4) {
-      float x[128];
-      uint32_t p[64];
-      tc::tmem_ld128(scol, x);
-      float lsum = exp_pack<T, 64>(x, cs, m_ref, p);
-      lsum += exp_pack<T, 64>(x + 64, cs, m_ref, p + 32);
-      written = !__any_sync(0xffffffffu, live && !(lsum <= kLimit));
-      if (written) {
-        l += lsum;
-        tc::tmem_st64(scol, reinterpret_cast<const float*>(p));
+    float x[128];
+    uint32_t p[64];
+    tc::tmem_ld128(scol, x);
+    if (edge) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t m = seen(32 * w);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[32 * w + c] = m >> c & 1 ? x[32 * w + c] : -INFINITY;
       }
     }
-    if (!written) {                            // a new reference from the block's maximum
-      float x[32], top = -INFINITY;
+    if (!started) {                            // rows without a reference take the block's maximum
+      const float top = prefill::tq_max<128>(x);
+      if (m_ref == -INFINITY) m_ref = fmaf(top, cs, -C::kBias);
+      started = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
+    }
+    // -inf only while every key so far was masked; then every score is -inf
+    float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+    float lsum = exp_pack<T, 64>(x, cs, m_use, p);
+    lsum += exp_pack<T, 64>(x + 64, cs, m_use, p + 32);
+    if (!__any_sync(0xffffffffu, live && !(lsum <= kLimit))) {
+      l += lsum;
+      tc::tmem_st64(scol, reinterpret_cast<const float*>(p));
+    } else {                                   // a new reference, and all of it again
+      float y[32], top = -INFINITY;
 #pragma unroll 1
-      for (int i = 0; i < chunks; ++i) {
-        tc::tmem_ld32(scol + 32 * i, x);
-        top = fmaxf(top, prefill::tq_max<32>(x));
+      for (int i = 0; i < 4; ++i) {
+        tc::tmem_ld32(scol + 32 * i, y);
+        const uint32_t m = seen(32 * i);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) top = m >> c & 1 ? fmaxf(top, y[c]) : top;
       }
       const float m_new = fmaxf(m_ref, fmaf(top, cs, -C::kBias));
       const bool grow = m_ref != -INFINITY && m_new > m_ref;
@@ -682,30 +691,25 @@ __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sum
         const float f = grow ? tc::ex2(m_ref - m_new) : 1.0f;
 #pragma unroll 1
         for (int c = 0; c < C::DP; c += 32) {
-          tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, x);
+          tc::tmem_ld32(lane_base + C::kOCol + t * C::DP + c, y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] *= f;
-          tc::tmem_st32(lane_base + C::kOCol + t * C::DP + c, x);
+          for (int e = 0; e < 32; ++e) y[e] *= f;
+          tc::tmem_st32(lane_base + C::kOCol + t * C::DP + c, y);
         }
         l *= f;
-        if (grow) m_ref = m_new;
       }
-      if (m_ref == -INFINITY) m_ref = m_new;
-      // -inf only while every key so far was masked; then every score is -inf
-      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+      if (grow) m_ref = m_new;
+      m_use = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {            // P's columns lie below those still to be read
-        uint32_t p[16];
-        if (i < chunks) {
-          tc::tmem_ld32(scol + 32 * i, x);
-          l += exp_pack<T, 32>(x, cs, m_use, p);
-        } else {
+        uint32_t q[16];
+        tc::tmem_ld32(scol + 32 * i, y);
+        const uint32_t m = seen(32 * i);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) p[c] = 0u;
-        }
-        tc::tmem_st16(scol + 16 * i, reinterpret_cast<const float*>(p));
+        for (int c = 0; c < 32; ++c) y[c] = m >> c & 1 ? y[c] : -INFINITY;
+        l += exp_pack<T, 32>(y, cs, m_use, q);
+        tc::tmem_st16(scol + 16 * i, reinterpret_cast<const float*>(q));
       }
-      if (!started) started = !__any_sync(0xffffffffu, live && m_ref == -INFINITY);
     }
     tc::fence_before_sync();
     __syncwarp();
