@@ -403,7 +403,10 @@ __device__ void products(const Args& a, uint32_t tmem, uint8_t* sq, uint8_t* skv
   uint32_t stage = 0, phase = 0;
   uint32_t done = 0, outputs = 0, turns = 0;   // the tile's blocks, units and turns so far
   bool bad = false;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { bad |= !tc::mbar_wait_short(bar, parity, abort); };
+  // Most of these are complete by now: asked first without leave to sleep (8192 tokens 369 -> 351 us).
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!tc::mbar_try_wait(bar, parity)) bad |= !tc::mbar_wait_short(bar, parity, abort);
+  };
   auto take = [&]() -> uint32_t {
     wait(&bars->kv_full[stage], phase);
     const uint32_t st = stage;
@@ -629,7 +632,8 @@ __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sum
   bool ok = true, started = false;             // started: every live row has a reference
   const uint32_t scol = lane_base + C::kSCol + t * kBK;
   for (int j = u.la == 2 ? j_lo + t : j_lo; j <= j_hi; j += u.la) {
-    ok = tc::mbar_wait_short(&bars->s_full[t], n & 1, abort);
+    ok = tc::mbar_try_wait(&bars->s_full[t], n & 1) ||
+         tc::mbar_wait_short(&bars->s_full[t], n & 1, abort);
     if (!__all_sync(0xffffffffu, ok)) return false;   // together: tcgen05.ld is warp-wide
     tc::fence_after_sync();
     const int k0 = j * kBK;
