@@ -321,7 +321,8 @@ def _own(s):
     kept = s["kept"]
     if c["op"] == "append":
         g.kv_cache_append_paged(s["k"], s["v"], s["k_cache"], s["v_cache"], s["block_table"],
-                                s["start"], s["max_pos"], kept["rp"], s["table"], s["k_norm"],
+                                s["start"], max(0, s["max_pos"] - 1), kept["rp"], s["table"],
+                                s["k_norm"],
                                 EPS, cu_seqlens=s["cu"], q=s["q"], q_out=s["q_out"],
                                 q_norm_w=s["q_norm"], k_out=s["k_out"], status=s["status"])
     elif c["op"] == "decode":
