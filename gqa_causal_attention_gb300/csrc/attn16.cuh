@@ -35,6 +35,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -935,8 +936,11 @@ cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
     const double c = static_cast<double>(j.scale) / j.softcap, z = c * c;
     const double series[5] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315, 62.0 / 2835};
     double power = static_cast<double>(j.scale) * 1.4426950408889634;
-    for (int i = 0; i < 5; ++i, power *= z) a.cap_series[i] = static_cast<float>(series[i] * power);
     a.cap_limit = static_cast<float>(0.4 / c);
+    for (int i = 0; i < 5; ++i, power *= z) {
+      a.cap_series[i] = static_cast<float>(series[i] * power);
+      if (!std::isfinite(a.cap_series[i])) a.cap_limit = -1.f;   // a cap of next to nothing: no series
+    }
   }
   a.out = j.out.p; a.o_token = j.out.token; a.o_head = j.out.head;
   a.part_o = j.part_o; a.part_ml = j.part_ml;

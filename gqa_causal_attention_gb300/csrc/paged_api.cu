@@ -26,7 +26,7 @@ int rows_of(const attn_rows* r, int T, int heads, int D, bool apart, RowsArg* ou
   if (!r || !r->p) return ATTN_ERR_NULL;
   if (!aligned16(r->p)) return ATTN_ERR_ALIGN;
   const int64_t head = heads > 1 ? r->head_stride : D;
-  const int64_t token = T > 1 ? r->token_stride : (head > D ? head : D) * heads;
+  const int64_t token = T > 1 ? r->token_stride : D;
   if (token % 8 || head % 8) return ATTN_ERR_ALIGN;
   if (token < D || head < D || token > kMaxStride || head > kMaxStride) return ATTN_ERR_SHAPE;
   if (apart && token < (heads - 1) * head + D && head < (T - 1) * token + D) return ATTN_ERR_PARAM;
@@ -81,14 +81,14 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // decode's. `parts` 0: the prefix is read with each row's own positions, which costs
 // less than a kernel more where all rows together read at most kRereadBytes of it, mostly
 // from L2.
-constexpr int64_t kRereadBytes = 64 << 20;
+constexpr double kRereadBytes = 64 << 20;
 struct SharedLayout {
   size_t ml, decode, total;
   int parts;
 };
 SharedLayout shared_layout(int B, int H, int Hkv, int D, int prefix_len, int max_len) {
   SharedLayout y{};
-  if (static_cast<int64_t>(B) * prefix_len * Hkv * D * 4 <= kRereadBytes) {
+  if (4.0 * B * prefix_len * Hkv * D <= kRereadBytes) {
     y.total = gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, prefix_len);
     return y;
   }

@@ -505,8 +505,7 @@ __global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? resident_of(DP) : 
                          sp.nt, -1);
 }
 
-// prefix[b]: tiles of rows before b; returns their total. Whole block of W warps. (The tiles of all
-// rows and heads of a cache that fits the GPU are fewer than 2^32: one takes 512 bytes at least.)
+// prefix[b]: tiles of rows before b; returns their total. Whole block of W warps.
 template <int W>
 __device__ unsigned scan_tiles(const DecodeArgs& a, unsigned* prefix, bool tell) {
   __shared__ unsigned warp_sum_of[W];
@@ -783,7 +782,9 @@ cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
   a.prefix = j.prefix;
   const DecodePagedPlan plan =
       decode_paged_plan(j.B, j.H, j.Hkv, j.D, j.max_len, j.window, j.prefix_len);
-  a.blocks = plan.blocks;
+  // Shares are counted in 32 bits: rows that share pages could have more tiles than that.
+  const int64_t most = (static_cast<int64_t>(j.max_len) + j.prefix_len) / kTile + 2;
+  a.blocks = static_cast<int64_t>(j.B) * j.Hkv * a.HT * most < (int64_t(1) << 32) ? plan.blocks : 0;
   a.part_o = j.partial;
   a.part_ml = reinterpret_cast<float2*>(j.partial + static_cast<size_t>(a.blocks) * 2 * kHeads * j.D);
   a.status = j.status; a.skip = j.skip;

@@ -686,7 +686,8 @@ typedef struct attn_paged_kv {
  *   start       device int32 [B]: positions already in the cache
  *   max_pos     host bound on every position written, below max_positions and the
  *               table's table_width * page_size (ATTN_ERR_POSITION, ATTN_ERR_CAPACITY)
- *   rp, table, norm weights (fp32) as for kv_cache_append
+ *   rp, table, norm weights (fp32) as for kv_cache_append (the norm's sum of squares in
+ *               fp32, so not for rows whose squares leave fp32's normal numbers)
  * A sequence with bad bounds (ATTN_DEV_LENGTH) or positions outside [0, max_pos]
  * (ATTN_DEV_POSITION) is skipped. Two tokens for one slot leave either's.
  */
@@ -746,7 +747,7 @@ int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* ca
  *   max_len     host bound on every length
  * A sequence with bad bounds or longer than max_len sets ATTN_DEV_LENGTH and is skipped;
  * rows of no sequence are neither written nor have a part in any result, whatever they
- * hold. (An inf or NaN in a sequence's own v may reach its earlier rows too.)
+ * hold. (An inf or NaN in a sequence's own v may reach rows of it that do not see it.)
  */
 int gqa_attn_prefill_packed(int type, const attn_rows* q, const attn_rows* k, const attn_rows* v,
                             const int32_t* cu_seqlens, int32_t max_len, const attn_rows* out, int T,

@@ -346,3 +346,58 @@ def test_prefill_bad_sequences():
     assert st == g.DEV_LENGTH and torch.equal(out[:100], good[:100]) and not (out[150:] == 7.0).all()
     out, st = run([0, 100], 0)
     assert st == g.DEV_LENGTH and (out == 7.0).all()
+
+
+# ---------------------------------------------------------------- corners
+
+def test_caps_of_next_to_nothing_and_scores_past_the_cap():
+    prefill(BF, 4, 2, 64, [200], softcap=1e-30)
+    prefill(FP, 4, 2, 64, [200, 150], softcap=2.0, scale=3.0)
+    decode(FP, 4, 2, 64, 16, [200, 1500], softcap=1e-30)
+    decode(BF, 4, 2, 64, 16, [200, 1500], softcap=2.0, scale=3.0)
+
+
+def test_one_row_of_a_wider_tensor():
+    """Axes of one element: their strides are not read."""
+    gn, t, H, D = gen(23), BF, 4, 64
+    wide = normal(gn, (9, H, 5, D), t)
+    q = wide[4:5, :, 2]                          # [1, H, D], heads 5 D apart
+    k, v = (normal(gn, (1, 1, D), t).expand(1, 1, D) for _ in range(2))
+    out = torch.empty(1, H, D, dtype=t, device=dev())
+    g.gqa_attn_prefill_packed(q, k, v, i32([0, 1]), 1, out)
+    assert torch.equal(out, v.expand(1, H, D).contiguous())
+    c = Cache(gn, 3, 1, 16, D, t)
+    table = c.table([1])
+    g.kv_cache_append_paged(k, v, c.k, c.v, table, i32([0]), 0, q=q, q_out=out)
+    assert torch.equal(out, q.contiguous())
+    g.gqa_attn_decode_paged(q, c.k, c.v, table, i32([1]), 1, out)
+    assert torch.equal(out, v.expand(1, H, D).contiguous())
+
+
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them():
+    """A NaN in one row's cache or query, or in one sequence, leaves every other row as it was."""
+    gn, t = gen(29), FP
+    lens = [100, 3000, 2000]
+    c = Cache(gn, 400, 2, 16, 64, t)
+    table = c.table(lens)
+    c.fill(gn, table, lens)
+    q = rows(gn, 3, 8, 64, t)
+    want, got = (torch.empty(3, 8, 64, dtype=t, device=dev()) for _ in range(2))
+    call = lambda o: g.gqa_attn_decode_paged(q, c.k, c.v, table, i32(lens), max(lens), o)  # noqa: E731
+    call(want)
+    c.v[table[1, 7], 0, 3, 5] = float("inf")
+    q[2, 6, 1] = float("nan")
+    call(got)
+    assert not torch.isfinite(got[1, :4, 5]).any() and torch.isnan(got[2, 6]).all()
+    got[1, :4, 5], got[2, 6] = want[1, :4, 5], want[2, 6]
+    assert torch.equal(got, want)
+    q, k, v = rows(gn, 400, 8, 64, t), rows(gn, 400, 2, 64, t), rows(gn, 400, 2, 64, t)
+    want, got = (torch.empty(400, 8, 64, dtype=t, device=dev()) for _ in range(2))
+    cu = i32([0, 130, 260, 400])
+    g.gqa_attn_prefill_packed(q, k, v, cu, 140, want)
+    k[135], v[140, 1, 2], q[300, 3, 3] = float("nan"), float("inf"), float("nan")
+    g.gqa_attn_prefill_packed(q, k, v, cu, 140, got)
+    assert torch.equal(got[:130], want[:130]) and torch.isnan(got[135:260]).all()
+    assert torch.isnan(got[300, 3]).all()
+    got[300, 3] = want[300, 3]
+    assert torch.equal(got[260:], want[260:])
