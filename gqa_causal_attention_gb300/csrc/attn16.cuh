@@ -804,8 +804,6 @@ template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     attn16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const Args a) {
-  dependent_wait();
-  if (gated_off(a.skip)) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -815,9 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* sums = reinterpret_cast<float2*>(sout + C::kOut + 1024);
   static_assert(sizeof(Bars) <= 1024, "barriers fit behind the ring");
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  if (warp == 9) {
-    tc::tmem_alloc(&bars->tmem_base, kTmemCols);
-    tc::tmem_relinquish();
+  if (threadIdx.x == 32) {                     // ahead of the first loads, which would wait for them
+    tc::tma_prefetch(&tm_q);
+    tc::tma_prefetch(&tm_k);
+    tc::tma_prefetch(&tm_v);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
@@ -843,6 +842,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bars->abort = 0;
     tc::fence_mbar_init();
+  }
+  dependent_wait();
+  if (gated_off(a.skip)) return;
+  if (warp == 9) {
+    tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
