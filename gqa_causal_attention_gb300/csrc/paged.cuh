@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace gqa {
 
@@ -52,19 +53,28 @@ __device__ __forceinline__ float2 unpack(uint32_t x) {
   return two(*reinterpret_cast<const typename Pair<T>::type*>(&x));
 }
 template <class T>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&x)[4]) {   // in pairs
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = unpack<T>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    x[i] = tc::pack2(f.x, f.y);
   }
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack(uint64_t x) {
+  float a, b;
+  tc::unpack2(x, a, b);
+  return Pair<T>::pack(a, b);
 }
 template <class T>
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]),
                     Pair<T>::pack(x[4], x[5]), Pair<T>::pack(x[6], x[7]));
+}
+template <class T>
+__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4]) {
+  return make_uint4(pack<T>(x[0]), pack<T>(x[1]), pack<T>(x[2]), pack<T>(x[3]));
 }
 
 // The largest b in [0, n) with key(b) <= x for nondecreasing keys (-1: none), found by the whole
