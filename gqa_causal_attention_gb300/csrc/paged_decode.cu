@@ -20,7 +20,7 @@
 //   dealt out to the blocks in equal shares, whatever the lengths; a block's share is one run
 //   of tiles, so at most its first and last unit are shared with other blocks and joined by a
 //   second kernel, a warp per row and head. Where rows are short, one block does each unit
-//   and nothing is left to join (one row of 500 slots: 12.2 us shared out, see decode_paged_plan).
+//   and nothing is left to join (see decode_paged_plan).
 // * With a prefix that all rows share, either its partial results (from the tensor cores) are joined
 //   here too, or, where it is read a few times only, its tiles come before the row's own.
 #include <type_traits>
@@ -201,13 +201,15 @@ template <class T, bool PRE>
 __device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int head, int d, float4 y,
                                            float top, float sum) {
   const int64_t row = static_cast<int64_t>(b) * a.H + head, rows = static_cast<int64_t>(a.B) * a.H;
-  if (PRE)
+  if (PRE) {
+    dependent_wait();                         // for the prefix's kernel, if not yet
     add_parts(
         [&](unsigned i, const float2*& ml, const float*& o) {
           ml = a.prefix.ml + i * rows + row;
           o = a.prefix.o + (i * rows + row) * a.D;
         },
         a.prefix.nsplit, d, a.D, y, top, sum);
+  }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;      // (a NaN stays one)
   if (d < a.D)
     store_out<T>(a, b, head, d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -473,6 +475,12 @@ __device__ __forceinline__ S* aligned_smem(uint8_t* raw) {   // 1024 bytes: the 
   return reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
 }
 
+// With the prefix's parts (PRE) the kernel before is the prefix's, which lets this one start only
+// after its own wait, so all that came before it has ended. It writes nothing but those parts:
+// rows of their own are read while it ends, and only what uses the parts waits for it (with the
+// wait at the start, a prefix of 8192 and 64 rows of 1..500: 36.4 us for 34.1). Every block waits
+// before it ends: who waits for this kernel has waited for the prefix's.
+
 // One block per unit (row, kv head, group of up to 8 query heads).
 template <class T, int W, int DP, bool PRE>
 __global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? resident_of(DP) : 1)
@@ -485,24 +493,30 @@ __global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? resident_of(DP) : 
     tc::tma_prefetch(&tv);
   }
   init_rings(sm);
-  dependent_wait();
+  if (!PRE) dependent_wait();
   dependents_may_launch();
-  if (gated_off(a.skip)) return;
+  if (gated_off(a.skip)) {
+    if (PRE) dependent_wait();
+    return;
+  }
   const unsigned per_row = a.Hkv * a.HT;
   const int b = blockIdx.x / per_row, u = blockIdx.x % per_row;
   const Span sp = span_of(a, b);
   if (sp.n < 0) {
     if (threadIdx.x == 0) report(a.status, ATTN_DEV_LENGTH);
+    if (PRE) dependent_wait();
     return;
   }
   if (sp.nt == 0) {
     if (u == 0) empty_row<T, PRE>(a, b);
+    if (PRE) dependent_wait();
     return;
   }
   const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
   Ring ring;
   segment<T, W, DP, PRE>(a, &tk, &tv, sm, ring, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp, 0,
                          sp.nt, -1);
+  if (PRE) dependent_wait();
 }
 
 // prefix[b]: tiles of rows before b; returns their total. Whole block of W warps.
@@ -562,9 +576,12 @@ __global__ void __launch_bounds__(32 * warps_of(DP), resident_of(DP))
     tc::tma_prefetch(&tv);
   }
   init_rings(sm);
-  dependent_wait();
+  if (!PRE) dependent_wait();
   dependents_may_launch();
-  if (gated_off(a.skip)) return;
+  if (gated_off(a.skip)) {
+    if (PRE) dependent_wait();
+    return;
+  }
   const unsigned per_row = a.Hkv * a.HT;
   const unsigned total = scan_tiles<W>(a, prefix, blockIdx.x == 0) * per_row;
   for (int b = blockIdx.x; b < a.B; b += a.blocks) {
@@ -594,6 +611,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP), resident_of(DP))
     tc::fence_proxy_async();                  // the merge's writes come before the next tiles
     __syncthreads();
   }
+  if (PRE) dependent_wait();
 }
 
 // Joins the shares of a row and query head that several blocks had (nothing to do where one block
