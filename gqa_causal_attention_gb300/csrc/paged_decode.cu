@@ -17,12 +17,13 @@
 //     O[dim, head] += V^T P^T          A = value pairs, B = P, its 8 x 8 blocks transposed by movmatrix
 // * P is split in two 16-bit parts, so its rounding (2^-8 in bf16) does not add to the output's.
 // * The tiles (16 positions) of all rows and heads, counted from the lengths on the device, are
-//   dealt out to the blocks in equal shares, whatever the lengths; a block's share is one run
-//   of tiles, so at most its first and last unit are shared with other blocks and joined by a
-//   second kernel, a warp per row and head. Where rows are short, one block does each unit
-//   and nothing is left to join (see decode_paged_plan).
+//   dealt out to the blocks in shares of equal cost (tiles, and kStart for each row and head begun),
+//   whatever the lengths; a block's share is one run of tiles, so at most its first and last unit
+//   are shared with other blocks and joined by a second kernel, a warp per row and head. Where rows
+//   are short, one block does each unit and nothing is left to join (see decode_paged_plan).
 // * With a prefix that all rows share, either its partial results (from the tensor cores) are joined
 //   here too, or, where it is read a few times only, its tiles come before the row's own.
+#include <algorithm>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -45,6 +46,10 @@ __host__ __device__ constexpr int ring_of(int W, int D) {
   return W == warps_of(D) && D > 64 ? 2 : 3;
 }
 constexpr int kHeads = 8;                     // query heads of a unit
+// What a block's start of a unit costs, in tiles: a chain of loads (length, page, tile) and the warps'
+// merge. Shares are equal in tiles plus starts, or a block that meets many short rows ends last (64
+// rows of 1..1000 slots, shared out: 0 48.5 us, 6 32.6, 16 31; of 1..2000 65.6, 53.9, 51.5).
+constexpr unsigned kStart = 16;
 constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
 constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps
 
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(32 * W, W == warps_of(DP) ? resident_of(DP) : 
   if (PRE) dependent_wait();
 }
 
-// prefix[b]: tiles of rows before b; returns their total. Whole block of W warps.
+// prefix[b]: costs of a unit of each row before b; returns their total. Whole block of W warps.
 template <int W>
 __device__ unsigned scan_tiles(const DecodeArgs& a, unsigned* prefix, bool tell) {
   __shared__ unsigned warp_sum_of[W];
@@ -533,7 +538,7 @@ __device__ unsigned scan_tiles(const DecodeArgs& a, unsigned* prefix, bool tell)
     if (b < a.B) {
       const Span sp = span_of(a, b);
       if (sp.n < 0 && tell) report(a.status, ATTN_DEV_LENGTH);
-      n = sp.nt;
+      n = sp.nt > 0 ? kStart + sp.nt : 0;
     }
     unsigned s = n;
 #pragma unroll
@@ -552,7 +557,7 @@ __device__ unsigned scan_tiles(const DecodeArgs& a, unsigned* prefix, bool tell)
   return before;
 }
 
-// Block i's share of `total` tiles begins at share_begin(i): the first total % blocks blocks have
+// Block i's share of a total cost begins at share_begin(i): the first total % blocks blocks have
 // one more than the others.
 __device__ __forceinline__ unsigned share_begin(unsigned total, unsigned blocks, unsigned i) {
   const unsigned q = total / blocks, r = total - q * blocks;
@@ -593,21 +598,23 @@ __global__ void __launch_bounds__(32 * warps_of(DP), resident_of(DP))
   const unsigned end = share_begin(total, a.blocks, blockIdx.x + 1);
 #pragma unroll 1
   while (x < end) {
-    int b = 0, past = a.B;                    // the last row that begins at or before tile x
+    int b = 0, past = a.B;                    // the last row that begins at or before x
     while (past - b > 1) {
       const int mid = (b + past) / 2;
       if (prefix[mid] * per_row <= x) b = mid; else past = mid;
     }
     const Span sp = span_of(a, b);
-    const unsigned in_row = x - prefix[b] * per_row, u = in_row / sp.nt;
-    const int t0 = in_row - u * sp.nt, t1 = min(static_cast<unsigned>(sp.nt), t0 + (end - x));
+    const unsigned cost = kStart + sp.nt, in_row = x - prefix[b] * per_row, u = in_row / cost;
+    const unsigned c0 = in_row - u * cost, c1 = min(cost, c0 + (end - x));
+    x += c1 - c0;
+    if (c1 <= kStart) break;                  // the share ends before the unit's first tile
+    const int t0 = c0 > kStart ? c0 - kStart : 0, t1 = c1 - kStart;
     const int hk = u / a.HT, h0 = hk * a.G + (u % a.HT) * kHeads;
     // Slot 0: a unit begun by an earlier block (the share's first); slot 1: one begun here and
     // continued by the next (its last).
     const int slot = t0 > 0 ? 0 : (t1 < sp.nt ? 1 : -1);
     segment<T, W, DP, PRE>(a, &tk, &tv, sm, ring, b, hk, h0, min(kHeads, (hk + 1) * a.G - h0), sp,
                            t0, t1, slot);
-    x += t1 - t0;
     tc::fence_proxy_async();                  // the merge's writes come before the next tiles
     __syncthreads();
   }
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(256) decode_paged_join_kernel(const DecodeArgs
   const int hk = head / a.G, g = head - hk * a.G, h = g % kHeads;
   unsigned i0 = 0, own = 0;                   // first block, and how many had the unit
   if (sp.nt > 0) {
-    const unsigned x0 = prefix[b] * per_row + (hk * a.HT + g / kHeads) * sp.nt;
+    const unsigned x0 = prefix[b] * per_row + (hk * a.HT + g / kHeads) * (kStart + sp.nt) + kStart;
     i0 = share_of(total, a.blocks, x0);
     own = share_of(total, a.blocks, x0 + sp.nt - 1) - i0 + 1;
   }
@@ -756,26 +763,43 @@ cudaError_t launch_type(const DecodeArgs& a, int warps, cudaStream_t stream) {
 }
 }  // namespace
 
-// One block per unit where no row has more than 8 tiles a warp, the block alone on its SM where all
-// units can be; else blocks that share all tiles. Measured, one row, 8 kv heads of 4 heads of 128,
-// us with a wide block a unit and shared out: 500 slots 6.8, 9.7; 1000 10.3, 11; 2000 17, 11.1.
+// One block per unit where no row can have more than 16 tiles a warp (8, in a block twice as wide,
+// where that leaves each block an SM of its own), or 32 where there are units for every place; else
+// blocks that share all tiles. Measured, 4 heads of 128 a kv head, 8 kv heads, us with a block a unit
+// and shared out: one row of 500 slots 6.8, 9.7; of 1000 10.3, 11; of 2000 17, 11.1. 24 rows of 1000
+// 18, 19.2; of 1..2000 26.9, 17.2. 64 rows of 1..1000 27.9, 30.8; of 1..2000 48.6, 51.5; 256 of those
+// 148, 167. Heads of 64: 64 rows of 1..2000 29, 33; 23 rows of 1..5000 30, 21.
+namespace {
+struct PlanSizes {
+  int64_t units, tiles, places, shares;       // (shares: blocks, where tiles are shared)
+};
+PlanSizes plan_sizes(int B, int H, int Hkv, int D, int max_len, int window, int prefix_len) {
+  const int G = H / Hkv;
+  const int64_t own = window > 0 && window < max_len ? window + kTile - 1 : max_len;
+  PlanSizes s;
+  s.units = static_cast<int64_t>(B) * Hkv * ((G + kHeads - 1) / kHeads);
+  s.tiles = (own + kTile - 1) / kTile + (prefix_len + kTile - 1) / kTile;
+  s.places = kSms * resident_of(D);
+  s.shares = std::min((s.units * s.tiles + warps_of(D) - 1) / warps_of(D), s.places);
+  return s;
+}
+}  // namespace
+
 DecodePagedPlan decode_paged_plan(int B, int H, int Hkv, int D, int max_len, int window,
                                   int prefix_len) {
-  const int G = H / Hkv;
-  const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + kHeads - 1) / kHeads);
-  const int64_t own = window > 0 && window < max_len ? window + kTile - 1 : max_len;
-  const int64_t tiles = (own + kTile - 1) / kTile + (prefix_len + kTile - 1) / kTile;
+  const PlanSizes s = plan_sizes(B, H, Hkv, D, max_len, window, prefix_len);
   const int warps = warps_of(D), wide = wide_warps_of(D);
-  if (tiles <= 8 * wide && units <= kSms) return {0, wide};
-  if (tiles <= 8 * warps || B > kMaxScanRows) return {0, warps};
-  const int64_t most = kSms * resident_of(D), want = (units * tiles + warps - 1) / warps;
-  return {static_cast<int>(want < most ? want : most), warps};
+  if (s.tiles <= 8 * wide && s.units <= kSms) return {0, wide};
+  if (s.tiles <= (s.units >= s.places ? 32 : 16) * warps || B > kMaxScanRows) return {0, warps};
+  return {static_cast<int>(s.shares), warps};
 }
 
-// The partial results of the blocks' shares (part_ml follows part_o). Never shrinks as max_len grows.
+// The partial results of the blocks' shares (part_ml follows part_o). Never shrinks as max_len or B
+// grows, so it counts shares for batches that would do without too.
 size_t decode_paged_bytes(int B, int H, int Hkv, int D, int max_len, int window, int prefix_len) {
-  const size_t blocks = decode_paged_plan(B, H, Hkv, D, max_len, window, prefix_len).blocks;
-  return blocks * 2 * kHeads * (D + 2) * sizeof(float);
+  const PlanSizes s = plan_sizes(B, H, Hkv, D, max_len, window, prefix_len);
+  if (s.tiles <= 16 * warps_of(D)) return 0;
+  return static_cast<size_t>(s.shares) * 2 * kHeads * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
@@ -801,7 +825,7 @@ cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
   const DecodePagedPlan plan =
       decode_paged_plan(j.B, j.H, j.Hkv, j.D, j.max_len, j.window, j.prefix_len);
   // Shares are counted in 32 bits: rows that share pages could have more tiles than that.
-  const int64_t most = (static_cast<int64_t>(j.max_len) + j.prefix_len) / kTile + 2;
+  const int64_t most = (static_cast<int64_t>(j.max_len) + j.prefix_len) / kTile + 2 + kStart;
   a.blocks = static_cast<int64_t>(j.B) * j.Hkv * a.HT * most < (int64_t(1) << 32) ? plan.blocks : 0;
   a.part_o = j.partial;
   a.part_ml = reinterpret_cast<float2*>(j.partial + static_cast<size_t>(a.blocks) * 2 * kHeads * j.D);

@@ -708,7 +708,7 @@ int kv_cache_append_paged(int type, const attn_rows* q, const attn_rows* q_out, 
  *               request) gives +0.0. Outside: ATTN_DEV_LENGTH, the row is left untouched
  *   max_cache_len  host bound, at most table_width * page_size (ATTN_ERR_CAPACITY)
  *   workspace   gqa_attn_decode_paged_workspace_size bytes, 16-byte aligned (never
- *               shrinking as max_cache_len grows; 0, and NULL allowed, where one pass
+ *               shrinking as max_cache_len or B grows; 0, and NULL allowed, where one pass
  *               finishes). Calls that overlap on the GPU need workspaces of their own
  * Results do not depend on timing. B * H <= 2^24.
  */

@@ -165,6 +165,17 @@ def test_decode(t, H, Hkv, D, page, lens, window, softcap):
            layout=("slice", "heads", "whole")[len(lens) % 3], max_len=max(lens) + len(lens) % 2)
 
 
+@pytest.mark.parametrize("H,Hkv,D,page,lens,window", [
+    (32, 8, 128, 16, [b % 30 for b in range(90)] + [5000, 4001, 0, 2], 0),   # shares of many starts
+    (16, 4, 64, 32, [9000] + [b % 19 for b in range(200)], 0),
+    (8, 1, 128, 64, [1] * 500 + [2500], 0),                  # more starts than tiles
+    (6, 2, 96, 16, [0, 0, 2300] + [700, 16] * 30, 2200),
+    (32, 8, 128, 16, [31 * b for b in range(64)], 0),        # a block a unit: more units than places
+])
+def test_decode_short_rows_beside_long_ones(H, Hkv, D, page, lens, window):
+    decode(BF, H, Hkv, D, page, lens, window, seed=len(lens))
+
+
 @pytest.mark.parametrize("t", [BF, FP])
 def test_decode_where_the_reference_moves(t):
     """Keys that grow along the row: every tile holds a new maximum, by far more than 2^8."""
@@ -236,6 +247,15 @@ def shared(t, H, Hkv, D, page, prefix, lens, softcap=0.0, kscale=1.0, seed=1, ke
 ])
 def test_shared(t, H, Hkv, D, page, prefix, lens, softcap):
     shared(t, H, Hkv, D, page, prefix, lens, softcap, seed=prefix)
+
+
+@pytest.mark.parametrize("H,Hkv,D,page,prefix,lens", [
+    (32, 8, 128, 16, 3500, [b % 20 for b in range(44)] + [3001]),        # shares of many starts
+    (12, 4, 64, 64, 9001, [0] * 50 + [4200] + [1, 17] * 20),
+    (32, 8, 128, 32, 2500, [0] * 60),                        # nothing but the prefix
+])
+def test_shared_short_rows_beside_long_ones(H, Hkv, D, page, prefix, lens):
+    shared(BF, H, Hkv, D, page, prefix, lens, seed=prefix)
 
 
 @pytest.mark.parametrize("t", [BF, FP])

@@ -156,6 +156,14 @@ def test_workspaces_are_checked_and_do_not_shrink():
 
 
 @no_device
+def test_workspaces_of_larger_batches_serve_smaller_ones():
+    size = g.gqa_attn_decode_paged_workspace_size
+    for h, hkv, d, n in ((32, 8, 128, 2000), (32, 8, 128, 1000), (16, 4, 64, 4000), (8, 1, 40, 300)):
+        sizes = [size(b, h, hkv, d, n) for b in (1, 2, 5, 19, 20, 56, 57, 58, 100, 200, 8192, 8193, 20000)]
+        assert sizes == sorted(sizes)
+
+
+@no_device
 def test_shared_refusals():
     assert shared(pt=None) == NULL
     assert shared(prefix=0) == SHAPE and shared(prefix=-3) == SHAPE and shared(pwidth=0) == SHAPE
