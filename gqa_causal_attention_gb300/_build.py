@@ -7,7 +7,8 @@ linked statically, so the library loads on a machine without a GPU driver
 
 ``csrc/binding.cpp`` becomes ``_build/_gqa_binding-torch<version>...so``, a Python extension
 that only checks torch tensors and calls into the library (it links against torch, not against
-it). It belongs to one version of torch and Python, and only the 4-bit cache's calls need it.
+it). It belongs to one version of torch and Python, and only the calls of the 4-bit cache and of 16-bit
+paged serving need it.
 """
 from __future__ import annotations
 

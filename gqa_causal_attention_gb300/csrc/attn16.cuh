@@ -32,6 +32,11 @@
 //    next unit's products and softmax run meanwhile. The blocks walk one list of units (a
 //    pair of tiles each), heaviest first.
 //  * Every wait is bounded; one that runs out raises ATTN_DEV_TIMEOUT and the block winds down.
+//
+// Measured (32 heads of 128 over 8): one prompt of 8192 tokens 352 us, 1560 TFLOP/s of products
+// that are needed, 0.82 of the library product's rate measured on such a GPU; tensor pipe at 68 %
+// of its cycles, the rest lost where a tile's softmax and its products wait for one another. 16
+// prompts of 1..2048 tokens 117 us (tensor pipe 53 %): the start and the end of each unit.
 #pragma once
 
 #include <algorithm>
@@ -573,7 +578,7 @@ __device__ bool partial_rows(const Args& a, const Unit& u, uint32_t tmem, uint8_
 // while no |scale x / cap| of the warp is past 0.4, tanh's series to the ninth power (the next
 // term is 1e-6 of the value) on the paired multiply-add, 3 instructions a score, in place of
 // two on the exponential's pipe, four cycles each (9 prompts of 100..1800, window 512, 16
-// heads of 64: 68 us with those alone).
+// heads of 64: 68 us with those alone, 63 with the series).
 __device__ __forceinline__ void soft_cap(const Args& a, float (&x)[32], bool live) {
   float most = 0.f;
 #pragma unroll
