@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks)
     b = warp_find_last(j.B, t, [&](int x) { return static_cast<int64_t>(j.cu[x]); });
     if (b < 0) return;                       // before the first sequence
     const SeqRows s = seq_rows(j.cu, b, j.T);
-    if (s.n < 0) {
+    // Bounds that decrease can name a sequence that begins behind the token.
+    if (s.n < 0 || t < s.first) {
       if (lane == 0) report(j.status, ATTN_DEV_LENGTH);
       return;
     }
