@@ -38,9 +38,15 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks)
   dependents_may_launch();
   if (gated_off(j.skip)) return;
   const unsigned w = blockIdx.x * kWarps + threadIdx.x / 32;
-  if (w >= warps) return;
-  constexpr int HPW = 32 / LPH;
   const int lane = threadIdx.x & 31;
+  if (w >= warps) {
+    // A warp of its own looks every sequence's bounds over: one may have no row to find it bad.
+    if (w == warps && j.cu)
+      for (int b = lane; b < j.B; b += 32)
+        if (seq_rows(j.cu, b, j.T).n < 0) report(j.status, ATTN_DEV_LENGTH);
+    return;
+  }
+  constexpr int HPW = 32 / LPH;
   constexpr int kPer = HPW * kPasses;        // heads of a group, all queries, keys or values
   const int nq = j.q.p ? j.H : 0;
   const int gq = (nq + kPer - 1) / kPer, gk = (j.Hkv + kPer - 1) / kPer;
@@ -241,7 +247,8 @@ cudaError_t launch_rope(const AppendPagedJob& j, cudaStream_t stream) {
   if (static_cast<int64_t>(j.T) * all > kManyWarps) groups = all < kGroups ? all : kGroups;
   const int per_token = (all + groups - 1) / groups;
   const unsigned warps = static_cast<unsigned>(j.T) * per_token;
-  return launch_dependent(append_paged_kernel<T, LPH, ROPE>, (warps + kWarps - 1) / kWarps,
+  const unsigned all_warps = warps + (j.cu ? 1 : 0);   // and the one for the bounds
+  return launch_dependent(append_paged_kernel<T, LPH, ROPE>, (all_warps + kWarps - 1) / kWarps,
                           32 * kWarps, 0, stream, j, warps, per_token, groups);
 }
 

@@ -39,3 +39,18 @@ def test_append_with_bounds_that_decrease(R):
             assert not (torch.isfinite(pool).any(-1).any(1).cpu() & ~may).any()
         for x in (q_out, k_out):
             assert not ((x != 7.0).any(-1).any(1).cpu() & ~here).any()
+
+
+def test_append_reports_bad_bounds_that_no_row_meets():
+    gn, t, Hkv, D, page = gen(43), FP, 2, 64, 16
+    k, v = rows(gn, 5, Hkv, D, t), rows(gn, 5, Hkv, D, t)
+    for cu in ([0, 5, 3], [0, 5, 9], [0, 5] + [5] * 40 + [-1], [0, 5] + [6] * 70):
+        B = len(cu) - 1
+        c, st = Cache(gn, 4, Hkv, page, D, t), status()
+        table = torch.zeros(B, 1, dtype=torch.int32, device=dev())
+        g.kv_cache_append_paged(k, v, c.k, c.v, table, i32([0] * B), 15, cu_seqlens=i32(cu), status=st)
+        assert st.item() == g.DEV_LENGTH, cu
+        assert torch.equal(c.k[0, :, :5].transpose(0, 1), k) and int(torch.isfinite(c.k).sum()) == k.numel()
+    st = status()
+    g.kv_cache_append_paged(k, v, c.k, c.v, table, i32([0] * B), 15, cu_seqlens=i32([0, 5] + [5] * (B - 1)), status=st)
+    assert st.item() == 0
