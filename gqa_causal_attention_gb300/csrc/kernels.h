@@ -550,6 +550,7 @@ struct PrefixPlan {
   int parts() const { return split_keys ? 2 * splits : splits; }
 };
 PrefixPlan shared_prefix_plan(int B, int H, int Hkv, int prefix_len);
+size_t shared_prefix_rows(int B, int H, int Hkv, int prefix_len);   // bound on B * H * parts()
 cudaError_t launch_attn16_bf16(const Attn16Job& j, cudaStream_t stream);
 cudaError_t launch_attn16_fp16(const Attn16Job& j, cudaStream_t stream);
 

@@ -2,6 +2,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/gqa_attn.h"
 #include "kernels.h"
 
@@ -80,7 +82,9 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // Workspace of a shared-prefix call: the prefix's partial outputs and their weights, then the
 // decode's. `parts` 0: the prefix is read with each row's own positions, which costs
 // less than a kernel more where all rows together read at most kRereadBytes of it, mostly
-// from L2.
+// from L2. What a call's own layout takes moves both ways as rows come and go (parts go down where
+// another pair of tiles is begun); `total` is a bound on it that no smaller B, prefix_len or max_len
+// passes, so that the workspace of the largest batch serves every other.
 constexpr double kRereadBytes = 64 << 20;
 struct SharedLayout {
   size_t ml, decode, total;
@@ -88,15 +92,15 @@ struct SharedLayout {
 };
 SharedLayout shared_layout(int B, int H, int Hkv, int D, int prefix_len, int max_len) {
   SharedLayout y{};
-  if (4.0 * B * prefix_len * Hkv * D <= kRereadBytes) {
-    y.total = gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, prefix_len);
-    return y;
-  }
+  y.total = gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, prefix_len);
+  if (4.0 * B * prefix_len * Hkv * D <= kRereadBytes) return y;
   y.parts = gqa::shared_prefix_plan(B, H, Hkv, prefix_len).parts();
   const size_t rows = static_cast<size_t>(B) * H;
   y.ml = align256(rows * y.parts * D * sizeof(float));
   y.decode = y.ml + align256(rows * y.parts * 2 * sizeof(float));
-  y.total = y.decode + gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, 0);
+  const size_t most = gqa::shared_prefix_rows(B, H, Hkv, prefix_len);
+  y.total = std::max(y.total, align256(most * D * sizeof(float)) + align256(most * 2 * sizeof(float)) +
+                                  gqa::decode_paged_bytes(B, H, Hkv, D, max_len, 0, 0));
   return y;
 }
 

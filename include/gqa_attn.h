@@ -726,7 +726,8 @@ int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cac
  * (device int32 [prefix_width]), then its own cache_len[b] >= 0 in the pages of its block
  * table (position prefix_len + i of the row is slot i % page_size of entry
  * i / page_size). The prefix is read once for all rows, as a matrix product. No window.
- *   workspace   gqa_attn_decode_shared_workspace_size bytes, 16-byte aligned
+ *   workspace   gqa_attn_decode_shared_workspace_size bytes, 16-byte aligned (never
+ *               shrinking as B, prefix_len or max_cache_len grows)
  * A cache_len[b] outside [0, max_cache_len] sets ATTN_DEV_LENGTH and the row is left
  * untouched.
  */
