@@ -66,9 +66,9 @@ struct Args {
   uint64_t inv_tokens;                         // floor(2^64 / (2 TQ)) + 1: n / (2 TQ) by the product's high half
   uint32_t inv_G;                              // floor(2^16 / G) + 1: row / G, row < 128
   int units, splits, split_keys;               // shared: pairs of tiles, splits of the key blocks
-  int window, softcap_on;
-  float c_score, c_cap_in, c_cap_out;          // log2 units
-  float cap_series[5], cap_limit;              // softcap's series in a raw score (see softmax)
+  int window;
+  float c_score;                               // log2 units
+  CapArgs cap;
   void* out;
   int64_t o_token, o_head;
   float* part_o;
@@ -574,19 +574,18 @@ __device__ bool partial_rows(const Args& a, const Unit& u, uint32_t tmem, uint8_
   return true;
 }
 
-// cap tanh(scale x / cap) in log2 units, of 32 raw scores. Scores are mostly well below the cap:
-// while no |scale x / cap| of the warp is past 0.4, tanh's series to the ninth power (the next
-// term is 1e-6 of the value) on the paired multiply-add, 3 instructions a score, in place of
-// two on the exponential's pipe, four cycles each (9 prompts of 100..1800, window 512, 16
-// heads of 64: 68 us with those alone, 63 with the series).
+// The cap of 32 raw scores. They are mostly well below it: while none of the warp is past the
+// series' limit, the series on the paired multiply-add, 3 instructions a score, in place of two on the
+// exponential's pipe, four cycles each (9 prompts of 100..1800, window 512, 16 heads of 64: 68 us
+// with those alone, 63 with the series).
 __device__ __forceinline__ void soft_cap(const Args& a, float (&x)[32], bool live) {
   float most = 0.f;
 #pragma unroll
   for (int c = 0; c < 32; c += 2) most = tc::max3(most, fabsf(x[c]), fabsf(x[c + 1]));
-  if (!__any_sync(0xffffffffu, live && !(most <= a.cap_limit))) {
+  if (!__any_sync(0xffffffffu, live && !(most <= a.cap.limit))) {
     uint64_t k[5];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) k[i] = tc::pack2(a.cap_series[i], a.cap_series[i]);
+    for (int i = 0; i < 5; ++i) k[i] = tc::pack2(a.cap.series[i], a.cap.series[i]);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
       const uint64_t v = tc::pack2(x[c], x[c + 1]), z = tc::mul2(v, v);
@@ -600,8 +599,8 @@ __device__ __forceinline__ void soft_cap(const Args& a, float (&x)[32], bool liv
   }
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
-    const float e = tc::ex2(x[c] * a.c_cap_in);
-    x[c] = fmaf(-2.0f * a.c_cap_out, tc::rcp(e + 1.0f), a.c_cap_out);
+    const float e = tc::ex2(x[c] * a.cap.in);
+    x[c] = fmaf(-2.0f * a.cap.out, tc::rcp(e + 1.0f), a.cap.out);
   }
 }
 
@@ -625,7 +624,7 @@ __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sum
   const int local = tile * a.TQ + tok;         // token of the unit
   const bool live = tok < a.TQ && local < u.ntok;
   const int qpos = u.q0 + local;
-  const float cs = a.softcap_on ? 1.0f : a.c_score;
+  const float cs = a.cap.on ? 1.0f : a.c_score;
   constexpr float kLimit = 32768.0f;           // no weight can then be past fp16's range
   float m_ref = -INFINITY, l = 0.f;            // P = 2^(score - m_ref) with the bias inside m_ref
   // The warp's rows' first and last visible keys are ordered as their tokens are.
@@ -650,7 +649,7 @@ __device__ bool softmax(const Args& a, const Unit& u, uint32_t tmem, float2* sum
     const int hi = !edge ? kBK : (C::SHARED ? u.nk - 1 : min(qpos, u.nk - 1)) - k0;
     const int lo = edge && !C::SHARED && a.window > 0 ? qpos - a.window + 1 - k0 : 0;
     auto seen = [&](int c0) { return bits_below(hi + 1 - c0) & ~bits_below(lo - c0); };   // of 32 columns
-    if (a.softcap_on) {                        // in place, in tensor memory, where the tile has keys
+    if (a.cap.on) {                        // in place, in tensor memory, where the tile has keys
       const int chunks = min(4, (tile_keys - k0 + 31) / 32);
 #pragma unroll 1
       for (int i = 0; i < chunks; ++i) {
@@ -941,20 +940,8 @@ cudaError_t launch(const Attn16Job& j, cudaStream_t stream) {
   a.inv_tokens = ~0ull / (2 * a.TQ) + 1;
   a.inv_G = 65536 / a.G + 1;
   a.window = j.window;
-  a.softcap_on = j.softcap > 0.f;
   a.c_score = j.scale * kLog2e16;
-  a.c_cap_in = j.softcap > 0.f ? 2.0f * kLog2e16 * j.scale / j.softcap : 0.f;
-  a.c_cap_out = kLog2e16 * j.softcap;
-  if (a.softcap_on) {                          // tanh u = u (1 - u^2/3 + 2 u^4/15 - 17 u^6/315 + 62 u^8/2835 - ...)
-    const double c = static_cast<double>(j.scale) / j.softcap, z = c * c;
-    const double series[5] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315, 62.0 / 2835};
-    double power = static_cast<double>(j.scale) * 1.4426950408889634;
-    a.cap_limit = static_cast<float>(0.4 / c);
-    for (int i = 0; i < 5; ++i, power *= z) {
-      a.cap_series[i] = static_cast<float>(series[i] * power);
-      if (!std::isfinite(a.cap_series[i])) a.cap_limit = -1.f;   // a cap of next to nothing: no series
-    }
-  }
+  a.cap = cap_args(j.softcap, j.scale);
   a.out = j.out.p; a.o_token = j.out.token; a.o_head = j.out.head;
   a.part_o = j.part_o; a.part_ml = j.part_ml;
   a.status = j.status; a.skip = j.skip;

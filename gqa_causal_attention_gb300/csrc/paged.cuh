@@ -8,6 +8,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -94,6 +96,34 @@ __device__ __forceinline__ int warp_find_last(int n, int64_t x, F key) {
     n = min(step, n - (c - 1) * step);
   }
   return -1;
+}
+
+// cap tanh(scale x / cap) of a raw score x, in log2 units: where |scale x / cap| <= 0.4, tanh's series to
+// the ninth power (the next term is 1e-6 of the value); past it, out (1 - 2 / (2^(in x) + 1)), which
+// loses out's bits against a small x: a cap of 1e6 would leave a score of 1 off by 5%.
+struct CapArgs {
+  int on;
+  float in, out;
+  float series[5], limit;                      // limit: in a raw score; -1: no series
+};
+// A cap of 2^60 scales or more is none: it changes a score by fp32's rounding where that reaches 2^48,
+// and by less below.
+inline CapArgs cap_args(float softcap, float scale) {
+  CapArgs a{};
+  const double c = static_cast<double>(scale) / softcap;
+  a.on = softcap > 0.f && c > 0x1p-60;
+  if (!a.on) return a;
+  a.in = 2.0f * kLog2e16 * scale / softcap;
+  a.out = kLog2e16 * softcap;
+  a.limit = static_cast<float>(0.4 / c);
+  // tanh u = u (1 - u^2/3 + 2 u^4/15 - 17 u^6/315 + 62 u^8/2835 - ...)
+  const double series[5] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315, 62.0 / 2835};
+  double power = static_cast<double>(scale) * 1.4426950408889634;
+  for (int i = 0; i < 5; ++i, power *= c * c) {
+    a.series[i] = static_cast<float>(series[i] * power);
+    if (!std::isfinite(a.series[i])) a.limit = -1.f;   // a cap of next to nothing
+  }
+  return a;
 }
 
 // Sequence b's rows [first, first + n) of T packed rows; n < 0 where cu_seqlens breaks a rule.

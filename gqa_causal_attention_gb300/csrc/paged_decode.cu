@@ -65,8 +65,9 @@ struct DecodeArgs {
   int64_t width;
   const int32_t* cache_len;
   int max_len, B, H, Hkv, D, G, HT;           // HT: units per kv head
-  int window, softcap_on;
-  float c_score, c_cap_in, c_cap_out;         // log2 units
+  int window;
+  float c_score;                              // log2 units
+  CapArgs cap;
   const int32_t* prefix_table;                // prefix read here, before the row's own positions
   int prefix_len;
   PrefixParts prefix;                         // or its partial results
@@ -119,6 +120,32 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Four raw scores capped: by the series, and where one of the warp's is past its limit, that one by
+// 2^x and a reciprocal.
+__device__ __forceinline__ void soft_cap(const CapArgs& c, float (&x)[4]) {
+  float y[4];
+  bool past = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float z = x[e] * x[e];
+    float p = fmaf(c.series[4], z, c.series[3]);
+    p = fmaf(p, z, c.series[2]);
+    p = fmaf(p, z, c.series[1]);
+    p = fmaf(p, z, c.series[0]);
+    y[e] = p * x[e];
+    past |= !(fabsf(x[e]) <= c.limit);
+  }
+  if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float u = tc::ex2(x[e] * c.in);
+      if (!(fabsf(x[e]) <= c.limit)) y[e] = fmaf(-2.0f * c.out, tc::rcp(u + 1.0f), c.out);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = y[e];
 }
 
 template <int W, int DP>
@@ -315,14 +342,11 @@ __device__ void segment(const DecodeArgs& a, const CUtensorMap* tk, const CUtens
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         vf[h][r] = *reinterpret_cast<const uint4*>(base + (VH + h) * kBox + swizzled(row_v[r], g));
+    if (a.cap.on) {
+      soft_cap(a.cap, x);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (a.softcap_on) {
-        const float u = tc::ex2(x[e] * a.c_cap_in);
-        x[e] = fmaf(-2.0f * a.c_cap_out, tc::rcp(u + 1.0f), a.c_cap_out);
-      } else {
-        x[e] *= a.c_score;
-      }
+      for (int e = 0; e < 4; ++e) x[e] *= a.c_score;
     }
     const int tile0 = first_pos(tile), lo = tile < sp.pt ? 0 : sp.lo;
     const int end = tile < sp.pt ? a.prefix_len : sp.n;
@@ -815,10 +839,8 @@ cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
   a.B = j.B; a.H = j.H; a.Hkv = j.Hkv; a.D = j.D;
   a.G = j.H / j.Hkv; a.HT = (a.G + kHeads - 1) / kHeads;
   a.window = j.window;
-  a.softcap_on = j.softcap > 0.f;
   a.c_score = j.scale * kLog2e16;
-  a.c_cap_in = j.softcap > 0.f ? 2.0f * kLog2e16 * j.scale / j.softcap : 0.f;
-  a.c_cap_out = kLog2e16 * j.softcap;
+  a.cap = cap_args(j.softcap, j.scale);
   a.prefix_table = j.prefix_table;
   a.prefix_len = j.prefix_len;
   a.prefix = j.prefix;

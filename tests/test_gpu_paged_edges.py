@@ -1,12 +1,89 @@
-"""16-bit paged serving at its edges."""
+"""16-bit paged serving at its edges, against 64 bits: caps far above the scores, weights far below a row's
+largest, rows that see mostly their own positions behind a shared prefix, many short prompts.
+
+The bounds here are closer than paged_ref.py's: a score's error counts by the score, not by the cap, and an
+fp16 weight's by its own size and 2^-37 of its row's largest.
+"""
 import pytest
 import torch
 
 import gqa_causal_attention_gb300 as g
-from paged_ref import Cache, dev, gen, i32, rows, status
+from paged_ref import Cache, U, attend, attend_tol, check, dev, gen, half_step, i32, normal, rows, status
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
+
+
+def close_tol(q, k, v, seen, softcap, scale, t, parts=False):
+    """Exact output of q [Lq, H, D] over k, v [n, Hkv, D], and how far a result may be from it.
+
+    Scores: D + 4 roundings of the product's magnitudes (tanh only shrinks them). Cap: below 0.4 tanh's
+    series, cut off at 9.3e-7 = 16 u of the value, and 6 roundings; above it 2^x (4 u), a reciprocal (2 u),
+    and 1 - 2 / (e + 1), which is 0.38 at least: 14 u. Then a subtraction and 2^x: 2 u of the score, 8 u.
+    Weights: two 16-bit parts leave half a step squared (half a step where P is one part: `parts`), in fp16
+    half of its smallest step too, 2^-25 with the row's largest at 2^12 at least (2^7: `parts`). Sums: n u."""
+    n, D = k.shape[0], q.shape[-1]
+    out, vabs, _ = attend(q, k, v, seen, softcap, scale)
+    scale = D ** -0.5 if not scale else scale
+    G = q.shape[1] // k.shape[1]
+    qq = q.double().permute(1, 0, 2)                          # [H, Lq, D]
+    kk = k.double().permute(1, 2, 0).repeat_interleave(G, 0)  # [H, D, n]
+    s, mag = scale * (qq @ kk), scale * (qq.abs() @ kk.abs())
+    if softcap > 0:
+        s = softcap * torch.tanh(s / softcap)
+    unsure = torch.where(seen, (D + 4) * U * mag + 26 * U * s.abs() + 8 * U, 0.0).amax(-1).T[..., None]
+    w = half_step(t) if parts else half_step(t) ** 2
+    least = n * 2.0 ** (-32 if parts else -37) * v.double().abs().max() if t == FP else 0.0
+    tol = (half_step(t) * (1 + 2.0 ** -6) * out.abs() + (w * (1 + 2.0 ** -6) + 2 * unsure + n * U) * vabs
+           + least + (2.0 ** -24 if t == FP else 0.0))
+    return out, tol
+
+
+def all_seen(n):
+    return torch.ones(1, n, dtype=torch.bool, device=dev())
+
+
+# ---------------------------------------------------------------- softcap
+
+@pytest.mark.parametrize("t", [BF, FP])
+@pytest.mark.parametrize("cap", [30.0, 1e3, 1e4, 1e6, 1e8, 1e38])
+def test_decode_with_caps_far_above_the_scores(t, cap):
+    """A cap that no score comes near changes next to nothing, whatever its size."""
+    for D, lens, n_max in ((64, [40, 1, 150], 150), (128, [300, 17], 5000)):
+        gn = gen(int(cap) % 1000 + D)
+        c = Cache(gn, 60, 2, 16, D, t)
+        table = c.table(lens, extra=400)
+        kv = c.fill(gn, table, lens, 2.0)
+        q = rows(gn, len(lens), 8, D, t)
+        out, st = torch.empty(len(lens), 8, D, dtype=t, device=dev()), status()
+        g.gqa_attn_decode_paged(q, c.k, c.v, table, i32(lens), n_max, out, softcap=cap, status=st)
+        assert st.item() == 0
+        for b, n in enumerate(lens):
+            want, tol = close_tol(q[b][None], *kv[b], all_seen(n), cap, 0.0, t)
+            check(out[b], want[0], tol[0], f"cap {cap:g}, row {b} of {n}")
+
+
+@pytest.mark.parametrize("t", [BF, FP])
+@pytest.mark.parametrize("cap", [1e4, 1e8])
+def test_shared_with_caps_far_above_the_scores(t, cap):
+    """The prefix's part and a row's own are capped alike: by the tensor cores (many rows) and by the decode."""
+    H, Hkv, D, page, lens = 16, 8, 128, 16, [40, 0, 13, 5] * 5
+    for prefix, B, parts in ((3000, 20, True), (90, 3, False)):
+        gn = gen(prefix)
+        c = Cache(gn, -(-prefix // page) + 100, Hkv, page, D, t)
+        ptab = c.table([prefix])[0].contiguous()
+        (pk, pv), = c.fill(gn, ptab[None], [prefix], 2.0)
+        table = c.table(lens[:B])
+        kv = c.fill(gn, table, lens[:B], 2.0)
+        q = rows(gn, B, H, D, t)
+        out, st = torch.empty(B, H, D, dtype=t, device=dev()), status()
+        g.gqa_attn_decode_shared(q, c.k, c.v, ptab, prefix, table, i32(lens[:B]), 40, out, softcap=cap,
+                                 status=st)
+        assert st.item() == 0
+        for b in range(B):
+            k, v = torch.cat([pk, kv[b][0]]), torch.cat([pv, kv[b][1]])
+            want, tol = close_tol(q[b][None], k, v, all_seen(k.shape[0]), cap, 0.0, t, parts)
+            check(out[b], want[0], tol[0], f"cap {cap:g}, prefix {prefix}, row {b}")
 
 
 # ---------------------------------------------------------------- bounds that decrease
