@@ -574,15 +574,16 @@ __device__ bool partial_rows(const Args& a, const Unit& u, uint32_t tmem, uint8_
   return true;
 }
 
-// The cap of 32 raw scores. They are mostly well below it: while none of the warp is past the
-// series' limit, the series on the paired multiply-add, 3 instructions a score, in place of two on the
+// The cap of 32 raw scores of a row. They are mostly well below it: while none is past the series'
+// limit, the series on the paired multiply-add, 3 instructions a score, in place of two on the
 // exponential's pipe, four cycles each (9 prompts of 100..1800, window 512, 16 heads of 64: 68 us
-// with those alone, 63 with the series).
+// with those alone, 63 with the series). Row by row: the other form is off by 2^-22 of the cap,
+// which only a row that holds such a large score can do without.
 __device__ __forceinline__ void soft_cap(const Args& a, float (&x)[32], bool live) {
   float most = 0.f;
 #pragma unroll
   for (int c = 0; c < 32; c += 2) most = tc::max3(most, fabsf(x[c]), fabsf(x[c + 1]));
-  if (!__any_sync(0xffffffffu, live && !(most <= a.cap.limit))) {
+  if (!live || most <= a.cap.limit) {
     uint64_t k[5];
 #pragma unroll
     for (int i = 0; i < 5; ++i) k[i] = tc::pack2(a.cap.series[i], a.cap.series[i]);
@@ -595,13 +596,14 @@ __device__ __forceinline__ void soft_cap(const Args& a, float (&x)[32], bool liv
       p = tc::fma2(p, z, k[0]);
       tc::unpack2(tc::mul2(p, v), x[c], x[c + 1]);
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const float e = tc::ex2(x[c] * a.cap.in);
-    x[c] = fmaf(-2.0f * a.cap.out, tc::rcp(e + 1.0f), a.cap.out);
+    for (int c = 0; c < 32; ++c) {
+      const float e = tc::ex2(x[c] * a.cap.in);
+      x[c] = fmaf(-2.0f * a.cap.out, tc::rcp(e + 1.0f), a.cap.out);
+    }
   }
+  __syncwarp();                                // what follows is for the whole warp
 }
 
 // The n lowest bits (none for n <= 0, all for n >= 32).

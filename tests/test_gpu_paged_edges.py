@@ -86,6 +86,26 @@ def test_shared_with_caps_far_above_the_scores(t, cap):
             check(out[b], want[0], tol[0], f"cap {cap:g}, prefix {prefix}, row {b}")
 
 
+# ---------------------------------------------------------------- prompts with scores past the cap
+
+@pytest.mark.parametrize("t", [BF, FP])
+@pytest.mark.parametrize("cap", [1e4, 1e6])
+def test_prefill_where_scores_past_the_cap_stand_beside_small_ones(t, cap):
+    """Every 16th query is large enough for its scores to pass the cap; the others' stay exact."""
+    gn, n, H, Hkv, D = gen(int(cap)), 200, 4, 2, 64
+    q, k, v = rows(gn, n, H, D, t), rows(gn, n, Hkv, D, t), rows(gn, n, Hkv, D, t)
+    q[::16] *= 1e4 if t == FP else cap
+    out, st = torch.empty(n, H, D, dtype=t, device=dev()), status()
+    scale = 0.25 if t == BF else 0.25 * cap / 1e4
+    k /= max(1.0, 8 * scale)
+    g.gqa_attn_prefill_packed(q, k, v, i32([0, n]), n, out, softcap=cap, scale=scale, status=st)
+    assert st.item() == 0
+    i = torch.arange(n, device=dev())
+    want, tol = close_tol(q, k, v, i <= i[:, None], cap, scale, t, True)
+    small = i % 16 != 0
+    check(out[small], want[small], tol[small], f"cap {cap:g}")
+
+
 # ---------------------------------------------------------------- bounds that decrease
 
 @pytest.mark.parametrize("R", [None, 0, 20])                  # without RoPE; whole head dims; partner dims one by one
