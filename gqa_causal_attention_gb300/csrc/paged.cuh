@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "common.cuh"
@@ -113,7 +114,7 @@ inline CapArgs cap_args(float softcap, float scale) {
   const double c = static_cast<double>(scale) / softcap;
   a.on = softcap > 0.f && c > 0x1p-60;
   if (!a.on) return a;
-  a.in = 2.0f * kLog2e16 * scale / softcap;
+  a.in = static_cast<float>(std::fmin(2.0 * kLog2e16 * c, FLT_MAX));   // finite: 0 times it is 0
   a.out = kLog2e16 * softcap;
   a.limit = static_cast<float>(0.4 / c);
   // tanh u = u (1 - u^2/3 + 2 u^4/15 - 17 u^6/315 + 62 u^8/2835 - ...)

@@ -106,6 +106,28 @@ def test_prefill_where_scores_past_the_cap_stand_beside_small_ones(t, cap):
     check(out[small], want[small], tol[small], f"cap {cap:g}")
 
 
+# ---------------------------------------------------------------- the smallest caps
+
+@pytest.mark.parametrize("cap", [1e-38, 1e-39, 1e-45])
+def test_caps_below_the_smallest_normal_number(cap):
+    """2 scale / cap leaves fp32: a score of 0 is still 0 after the cap, and the weights are equal."""
+    t, n, H, Hkv, D = BF, 40, 4, 2, 64
+    gn = gen(7)
+    q = torch.zeros(n, H, D, dtype=t, device=dev())
+    k, v = rows(gn, n, Hkv, D, t), rows(gn, n, Hkv, D, t)
+    c = Cache(gn, 8, Hkv, 16, D, t)
+    table = c.table([n])
+    c.put(table[0].tolist(), 0, k, v)
+    one, out, st = torch.empty(1, H, D, dtype=t, device=dev()), torch.empty(n, H, D, dtype=t, device=dev()), status()
+    g.gqa_attn_decode_paged(q[:1], c.k, c.v, table, i32([n]), n, one, softcap=cap, scale=1.0, status=st)
+    g.gqa_attn_prefill_packed(q, k, v, i32([0, n]), n, out, softcap=cap, scale=1.0, status=st)
+    assert st.item() == 0
+    i = torch.arange(n, device=dev())
+    want, tol = close_tol(q, k, v, i <= i[:, None], 0.0, 1.0, t, True)
+    check(out, want, tol)
+    check(one, want[-1:], tol[-1:])
+
+
 # ---------------------------------------------------------------- bounds that decrease
 
 @pytest.mark.parametrize("R", [None, 0, 20])                  # without RoPE; whole head dims; partner dims one by one
