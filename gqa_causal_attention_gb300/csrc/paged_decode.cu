@@ -15,7 +15,8 @@
 //   and pairs of value rows made by one byte permutation a register.
 //     scores S[key, head] = K Q^T      A = 16 keys, B = 8 heads of Q
 //     O[dim, head] += V^T P^T          A = value pairs, B = P, its 8 x 8 blocks transposed by movmatrix
-// * P is split in two 16-bit parts, so its rounding (2^-8 in bf16) does not add to the output's.
+// * P is split in two 16-bit parts, so its rounding (2^-8 in bf16) does not add to the output's: a
+//   weight is off by 2^-16 of itself, in fp16 by 2^-22 of itself and 2^-37 of the row's largest.
 // * The tiles (16 positions) of all rows and heads, counted from the lengths on the device, are
 //   dealt out to the blocks in shares of equal cost (tiles, and kStart for each row and head begun),
 //   whatever the lengths; a block's share is one run of tiles, so at most its first and last unit
@@ -50,7 +51,12 @@ constexpr int kHeads = 8;                     // query heads of a unit
 // merge. Shares are equal in tiles plus starts, or a block that meets many short rows ends last (64
 // rows of 1..1000 slots, shared out: 0 48.5 us, 6 32.6, 16 31; of 1..2000 65.6, 53.9, 51.5).
 constexpr unsigned kStart = 16;
-constexpr float kGrow = 8.0f;                 // the reference moves when exceeded by 2^8
+// A row's reference lies kBias below the maximum that set it, in log2 units, and moves when exceeded by
+// kGrow. fp16 has few small numbers: with a bias of 12 a weight of 2^-25 of that maximum is known to
+// 2^-12 of itself (without one it came out as nothing, or twice its size), and what is lost of any is
+// 2^-37 of the maximum. Weights are at most 2^15 then.
+template <class T> constexpr float kBias = std::is_same<T, __half>::value ? 12.0f : 0.0f;
+template <class T> constexpr float kGrow = std::is_same<T, __half>::value ? 15.0f : 8.0f;
 constexpr int kMaxScanRows = 8192;            // rows whose tile counts a block keeps
 
 struct DecodeArgs {
@@ -367,7 +373,7 @@ __device__ void segment(const DecodeArgs& a, const CUtensorMap* tk, const CUtens
       ask(next);
       next += W;
     }
-    const float ref0 = m_ref[0] + kGrow, ref1 = m_ref[1] + kGrow;   // -inf stays -inf
+    const float ref0 = m_ref[0] + kGrow<T>, ref1 = m_ref[1] + kGrow<T>;   // -inf stays -inf
     const float max0 = fmaxf(x[0], x[2]), max1 = fmaxf(x[1], x[3]);
     if (__any_sync(0xffffffffu, max0 > ref0 || max1 > ref1)) {
       const float ref[2] = {ref0, ref1};
@@ -376,7 +382,7 @@ __device__ void segment(const DecodeArgs& a, const CUtensorMap* tk, const CUtens
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-        const float m_new = top[i] > ref[i] ? fmaxf(top[i], m_ref[i]) : m_ref[i];
+        const float m_new = top[i] > ref[i] ? top[i] - kBias<T> : m_ref[i];
         f[i] = m_new == -INFINITY ? 1.0f : tc::ex2(m_ref[i] - m_new);
         m_ref[i] = m_new;
         l[i] *= f[i];

@@ -128,6 +128,44 @@ def test_caps_below_the_smallest_normal_number(cap):
     check(one, want[-1:], tol[-1:])
 
 
+# ---------------------------------------------------------------- small weights
+
+@pytest.mark.parametrize("t", [BF, FP])
+@pytest.mark.parametrize("D,lens,prefix", [(64, [2000], 0), (128, [500, 7000], 0), (64, [30, 100], 300)])
+def test_small_weights_beside_a_key_whose_value_is_zero(t, D, lens, prefix):
+    """One key in 16 has nearly all of the weight and a value of zero: what is left of the output are keys
+    of 2^-24 .. 2^-27 of its weight."""
+    gn, H, Hkv, page = gen(D + prefix), 8, 2, 16
+    c = Cache(gn, sum(-(-n // page) for n in lens) + -(-prefix // page) + 4, Hkv, page, D, t)
+
+    def make(n):
+        k, v = torch.zeros(n, Hkv, D, device=dev()), 1000 + 100 * normal(gn, (n, Hkv, D))
+        first = torch.arange(n, device=dev()) % 16 == 3
+        k[..., 0] = torch.where(first, 0.0, -24 * 0.6931 - torch.rand(n, generator=gn, device=dev()) * 2)[:, None]
+        v[first] = 0
+        return k.to(t), v.to(t)
+
+    q = torch.zeros(len(lens), H, D, dtype=t, device=dev())
+    q[..., 0] = 1
+    table = c.table(lens)
+    kv = [make(n) for n in lens]
+    for b in range(len(lens)):
+        c.put(table[b].tolist(), 0, *kv[b])
+    out, st = torch.empty_like(q), status()
+    if prefix:
+        ptab = c.table([prefix])[0].contiguous()
+        pre = make(prefix)
+        c.put(ptab.tolist(), 0, *pre)
+        kv = [(torch.cat([pre[0], k]), torch.cat([pre[1], v])) for k, v in kv]
+        g.gqa_attn_decode_shared(q, c.k, c.v, ptab, prefix, table, i32(lens), max(lens), out, scale=1.0, status=st)
+    else:
+        g.gqa_attn_decode_paged(q, c.k, c.v, table, i32(lens), max(lens), out, scale=1.0, status=st)
+    assert st.item() == 0
+    for b in range(len(lens)):
+        want, tol = close_tol(q[b][None], *kv[b], all_seen(kv[b][0].shape[0]), 0.0, 1.0, t)
+        check(out[b], want[0], tol[0], f"row {b}")
+
+
 # ---------------------------------------------------------------- bounds that decrease
 
 @pytest.mark.parametrize("R", [None, 0, 20])                  # without RoPE; whole head dims; partner dims one by one
