@@ -30,7 +30,7 @@
 //  * Sixteen warps: softmax (2 x 4), loads, products (2), the list of units with the zeroing of V
 //    behind the last key, and four that bring finished rows out of tensor memory, so that the
 //    next unit's products and softmax run meanwhile. The blocks walk one list of units (a
-//    pair of tiles each), heaviest first.
+//    pair of tiles each).
 //  * Every wait is bounded; one that runs out raises ATTN_DEV_TIMEOUT and the block winds down.
 //
 // Measured (32 heads of 128 over 8): one prompt of 8192 tokens 352 us, 1560 TFLOP/s of products
@@ -144,7 +144,7 @@ __device__ __forceinline__ void tile_blocks(const Args& a, const Unit& u, int t,
 }
 
 // ---------------------------------------------------------------- producer (one warp)
-// The blocks walk one list of units, heaviest first, in snake order: unit x of round r for block c.
+// The blocks walk one list of units in snake order: unit x of round r for block c.
 __device__ __forceinline__ unsigned unit_at(unsigned c, unsigned r, unsigned blocks) {
   return r * blocks + ((r & 1) ? blocks - 1 - c : c);
 }
@@ -167,11 +167,22 @@ __device__ __forceinline__ int tiles_from(const Args& a, int i) {
   return __reduce_add_sync(0xffffffffu, n);
 }
 
-// Unit x of the list; false past its end. Whole warp. Packed prompts: tiles by their index within
-// their sequence, last first (a tile's keys grow with it), the kv heads of a tile side by
-// side. `past` tiles have an index of top or above (kept from unit to unit, which come in order).
+// Where the search for a block's next unit stands (they come in order).
+struct Search {
+  int top = 0, past = 0;                       // sorted: `past` tiles have an index of top or above
+  int b0 = 0;                                  // else: `past` tiles are of sequences before b0
+};
+
+// Unit x of the list; false past its end. Whole warp. Packed prompts: the kv heads of a tile side by
+// side. Up to kSorted sequences, tiles by their index within their sequence, last first (a tile's keys
+// grow with it), so that the blocks end together; each unit's search then reads every sequence's
+// bounds a few times. Past that many the sequences come in their own order, each one's last tile
+// first, and a block reads their bounds once in all. 32 heads of 128 over 8, us sorted and in order:
+// 16 of 1..2048 tokens 150, 163; 64 of 1..200 47, 43; 63 of 100 and one of 8192 385, 448; 96 such 403,
+// 400; 256 of 1..200 187, 136; 4096 22900, 1980; 16384 of 4 tokens, 8 heads of 64: 124000, 2840.
+constexpr int kSorted = 64;
 template <class C>
-__device__ bool find_unit(const Args& a, unsigned x, int& top, int& past, Unit& u) {
+__device__ bool find_unit(const Args& a, unsigned x, Search& at, Unit& u) {
   u.hk = x % a.Hkv;
   const int y = x / a.Hkv, tokens = 2 * a.TQ;
   if (C::SHARED) {
@@ -189,32 +200,54 @@ __device__ bool find_unit(const Args& a, unsigned x, int& top, int& past, Unit& 
     u.la = a.split_keys ? 2 : 1;
     return true;
   }
-  // The largest index lo < top with more than y tiles of index >= lo; then top = lo + 1.
-  int lo = -1;
+  int lo = -1, b = 0;                          // the unit is tile lo of sequence b
+  const int lane = threadIdx.x & 31;
+  if (a.B <= kSorted) {
+    // The largest index lo < top with more than y tiles of index >= lo; then top = lo + 1.
 #pragma unroll 1
-  while (top - lo > 1) {
-    const int mid = (lo + top) / 2, n = tiles_from(a, mid);
-    if (n > y) {
-      lo = mid;
-    } else {
-      top = mid;
-      past = n;
+    while (at.top - lo > 1) {
+      const int mid = (lo + at.top) / 2, n = tiles_from(a, mid);
+      if (n > y) {
+        lo = mid;
+      } else {
+        at.top = mid;
+        at.past = n;
+      }
     }
-  }
-  if (lo < 0) return false;
-  int k = y - past;                            // among the sequences that have a tile lo
-  int b = 0;
+    if (lo < 0) return false;
+    int k = y - at.past;                       // among the sequences that have a tile lo
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = b0 + (threadIdx.x & 31);
-    const bool has = mine < a.B && seq_tiles(a, mine, false) > lo;
-    const uint32_t all = __ballot_sync(0xffffffffu, has);
-    if (k < __popc(all)) {                     // the lane with k others before it
-      const int before = __popc(all & ((1u << (threadIdx.x & 31)) - 1));
-      b = b0 + __ffs(__ballot_sync(0xffffffffu, has && before == k)) - 1;
-      break;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int mine = b0 + lane;
+      const bool has = mine < a.B && seq_tiles(a, mine, false) > lo;
+      const uint32_t all = __ballot_sync(0xffffffffu, has);
+      if (k < __popc(all)) {                   // the lane with k others before it
+        const int before = __popc(all & ((1u << lane) - 1));
+        b = b0 + __ffs(__ballot_sync(0xffffffffu, has && before == k)) - 1;
+        break;
+      }
+      k -= __popc(all);
     }
-    k -= __popc(all);
+  } else {
+#pragma unroll 1
+    for (;; at.b0 += 32) {
+      if (at.b0 >= a.B) return false;
+      const int mine = at.b0 + lane, n = mine < a.B ? seq_tiles(a, mine, blockIdx.x == 0) : 0;
+      int to = n;                              // tiles of the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int before = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += before;
+      }
+      const int k = y - at.past, all = __shfl_sync(0xffffffffu, to, 31);
+      if (k < all) {                           // the first lane whose tiles pass k
+        const int src = __ffs(__ballot_sync(0xffffffffu, to > k)) - 1;
+        b = at.b0 + src;
+        lo = __shfl_sync(0xffffffffu, to, src) - 1 - k;
+        break;
+      }
+      at.past += all;
+    }
   }
   const SeqRows s = seq_rows(a.cu, b, a.T);
   u.q0 = lo * tokens;
@@ -258,17 +291,17 @@ __device__ __forceinline__ bool zero_tail(const Unit& u, uint8_t* skv, Bars* bar
 template <class C>
 __device__ void scheduler(const Args& a, uint8_t* skv, Bars* bars, int lane) {
   volatile int* abort = &bars->abort;
-  int top = 0, past = 0;
+  Search at;
   uint32_t loaded = 0, fills = 0;
-  if (!C::SHARED) {
+  if (!C::SHARED && a.B <= kSorted) {
 #pragma unroll 1
-    for (int b = lane; b < a.B; b += 32) top = max(top, seq_tiles(a, b, blockIdx.x == 0));
-    top = __reduce_max_sync(0xffffffffu, top);
+    for (int b = lane; b < a.B; b += 32) at.top = max(at.top, seq_tiles(a, b, blockIdx.x == 0));
+    at.top = __reduce_max_sync(0xffffffffu, at.top);
   }
   Unit before{};
   for (uint32_t r = 0;; ++r) {
     Unit u{};
-    const bool any = find_unit<C>(a, unit_at(blockIdx.x, r, gridDim.x), top, past, u);
+    const bool any = find_unit<C>(a, unit_at(blockIdx.x, r, gridDim.x), at, u);
     if (!any) u.nt = 0;
     bool ok = true;
     if (lane == 0) {

@@ -166,6 +166,79 @@ def test_small_weights_beside_a_key_whose_value_is_zero(t, D, lens, prefix):
         check(out[b], want[0], tol[0], f"row {b}")
 
 
+# ---------------------------------------------------------------- many prompts
+
+def prompts(gn, lens, H, Hkv, D, t):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return i32(cu), cu, [rows(gn, cu[-1] + 1, h, D, t, "whole") for h in (H, Hkv, Hkv)]
+
+
+@pytest.mark.parametrize("t,H,Hkv,D,lens", [
+    (BF, 4, 2, 64, [(7 * b) % 23 for b in range(3000)]),
+    (FP, 4, 1, 128, [(11 * b) % 9 for b in range(1500)] + [1300] + [0] * 40 + [3] * 60 + [700]),
+    (FP, 8, 8, 32, [0] * 1100 + [400, 0, 1] + [0] * 1000),
+    (BF, 8, 1, 64, [500] + [3] * 63),                         # the last number that is sorted,
+    (BF, 8, 1, 64, [3] * 63 + [500, 2]),                      # and the first that is not
+])
+def test_thousands_of_prompts(t, H, Hkv, D, lens):
+    gn = gen(len(lens))
+    ct, cu, (q, k, v) = prompts(gn, lens, H, Hkv, D, t)
+    out, st = torch.full_like(q, 7.0), status()
+    g.gqa_attn_prefill_packed(q, k, v, ct, max(lens), out, status=st)
+    assert st.item() == 0 and (out[cu[-1]:] == 7.0).all()
+    assert not (out[:cu[-1]] == 7.0).all(-1).any()
+    alone = torch.empty_like(out)
+    for b in [b for b, n in enumerate(lens) if n >= 400] + list(range(0, len(lens), 97)):
+        n, at = lens[b], slice(cu[b], cu[b + 1])
+        if n == 0:
+            continue
+        i = torch.arange(n, device=dev())
+        o, vabs, unsure = attend(q[at], k[at], v[at], i <= i[:, None])
+        check(out[at], o, attend_tol(o, vabs, unsure, t, True), f"sequence {b} of {n}")
+    # and every one of them as in calls of 60 prompts each
+    for b0 in range(0, len(lens), 60):
+        part = ct[b0:b0 + 61].contiguous()
+        g.gqa_attn_prefill_packed(q, k, v, part, max(lens), alone, status=st)
+    assert st.item() == 0 and torch.equal(alone[:cu[-1]], out[:cu[-1]])
+
+
+def test_thousands_of_prompts_with_bad_ones_among_them():
+    gn, lens = gen(2), [(5 * b) % 12 for b in range(2000)]
+    ct, cu, (q, k, v) = prompts(gn, lens, 4, 2, 64, BF)
+    want, out, st = torch.full_like(q, 7.0), torch.full_like(q, 7.0), status()
+    g.gqa_attn_prefill_packed(q, k, v, ct, 11, want)
+    g.gqa_attn_prefill_packed(q, k, v, ct, 10, out, status=st)   # the longest are skipped, and said
+    assert st.item() == g.DEV_LENGTH
+    long = torch.zeros(q.shape[0], dtype=torch.bool)
+    for b, n in enumerate(lens):
+        long[cu[b]:cu[b + 1]] = n > 10
+    long = long.to(dev())
+    assert (out[long] == 7.0).all() and torch.equal(out[~long], want[~long])
+
+
+def test_the_time_of_many_prompts_grows_as_their_number():
+    """16384 prompts of 4 tokens against 2048 of them: 8 times the work."""
+    gn, took = gen(3), []
+    for B in (2048, 16384):
+        ct, cu, (q, k, v) = prompts(gn, [4] * B, 8, 8, 64, BF)
+        out = torch.empty_like(q)
+        call = lambda: g.gqa_attn_prefill_packed(q, k, v, ct, 4, out)  # noqa: E731, B023
+        for _ in range(3):
+            call()
+        best = 1e9
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        took.append(best)
+    assert took[1] < 16 * took[0], took
+
+
 # ---------------------------------------------------------------- bounds that decrease
 
 @pytest.mark.parametrize("R", [None, 0, 20])                  # without RoPE; whole head dims; partner dims one by one
