@@ -166,6 +166,54 @@ def test_small_weights_beside_a_key_whose_value_is_zero(t, D, lens, prefix):
         check(out[b], want[0], tol[0], f"row {b}")
 
 
+# ---------------------------------------------------------------- shared prefixes
+
+@pytest.mark.parametrize("t", [BF, FP])
+@pytest.mark.parametrize("H,Hkv,D,page,prefix,lens", [
+    (28, 4, 64, 32, 2001, [0, 40, 7, 1]),                     # read with each row's own: P in two parts
+    (16, 8, 128, 16, 1500, [3, 0, 1, 200]),
+    (32, 8, 128, 16, 2560, [b % 6 for b in range(24)]),       # tensor cores: P in one
+    (8, 8, 64, 128, 9000, [b % 3 for b in range(40)]),
+])
+def test_a_rows_own_positions_weigh_beside_a_long_prefix(t, H, Hkv, D, page, prefix, lens):
+    """Own keys lie along their row's query, so that one of them outweighs the whole prefix; lost, or
+    counted twice, it would change the output by its own size. By the shared call and, with the
+    prefix's pages in every row's table, by the plain one."""
+    gn, B = gen(prefix + D), len(lens)
+    per = -(-prefix // page)
+    c = Cache(gn, per + sum(-(-n // page) for n in lens) + 2, Hkv, page, D, t)
+    ptab = c.table([prefix], extra=0)[0].contiguous()
+    (pk, pv), = c.fill(gn, ptab[None], [prefix])
+    q, own = rows(gn, B, H, D, t), c.table(lens)
+    kv = []
+    for b, n in enumerate(lens):
+        k, v = normal(gn, (n, Hkv, D)), normal(gn, (n, Hkv, D), t)
+        lead = q[b].float().view(Hkv, -1, D)[:, 0]            # the kv head's first query: |q|^2 / sqrt(D) ~ sqrt(D)
+        k = (lead * (1.3 if D <= 64 else 1.0) + 0.3 * k).to(t)
+        c.put(own[b].tolist(), 0, k, v)
+        kv.append((torch.cat([pk, k]), torch.cat([pv, v])))
+    st = status()
+    a, p = (torch.empty(B, H, D, dtype=t, device=dev()) for _ in range(2))
+    g.gqa_attn_decode_shared(q, c.k, c.v, ptab, prefix, own, i32(lens), max(lens), a, status=st)
+    # own positions begin at a page of their own: the plain call needs the prefix to end with one
+    whole = prefix % page == 0
+    if whole:
+        table = torch.cat([ptab.expand(B, -1), own], 1).contiguous()
+        g.gqa_attn_decode_paged(q, c.k, c.v, table, i32([prefix + n for n in lens]), prefix + max(lens), p, status=st)
+    assert st.item() == 0
+    parts = 4 * B * prefix * Hkv * D > 64 << 20
+    for b, n in enumerate(lens):
+        args = (q[b][None], *kv[b], all_seen(prefix + n), 0.0, 0.0, t)
+        want, tol = close_tol(*args, parts)
+        check(a[b], want[0], tol[0], f"row {b}")
+        if n:                                                 # what the test is for: losing one shows
+            less, _, _ = attend(q[b][None], kv[b][0][:-1], kv[b][1][:-1], all_seen(prefix + n - 1))
+            assert ((less - want).abs() / tol).max() > 4
+        if whole:
+            want, tol = close_tol(*args)
+            check(p[b], want[0], tol[0], f"row {b}, its own table")
+
+
 # ---------------------------------------------------------------- many prompts
 
 def prompts(gn, lens, H, Hkv, D, t):
