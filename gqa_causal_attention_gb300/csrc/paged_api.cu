@@ -13,6 +13,7 @@ using gqa::PagedKv;
 using gqa::RowsArg;
 
 constexpr int64_t kMaxStride = int64_t(1) << 38;   // elements: a tensor map holds 2^40 bytes
+constexpr int kMost = 0x7fffffff - 1024;           // positions, rows, sequences: a tile past them fits an int
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -20,6 +21,11 @@ bool type_ok(int type) { return type == ATTN_TYPE_FP16 || type == ATTN_TYPE_BF16
 
 bool heads_ok(int H, int Hkv, int D) {
   return H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= 128 && D >= 16 && D <= 128 && D % 8 == 0;
+}
+
+bool decode_sizes_ok(int H, int Hkv, int D, int B, int max_len) {
+  return heads_ok(H, Hkv, D) && B >= 1 && static_cast<int64_t>(B) * H <= 1 << 24 && max_len >= 0 &&
+         max_len <= kMost;
 }
 
 // Rows [T, heads, D]: strides of at least D (in whole 16-byte steps) along the axes that have more
@@ -119,7 +125,7 @@ struct DecodeCall {
 // What both decode calls check; fills the job but for its workspace.
 int decode_checks(const DecodeCall& c, gqa::DecodePagedJob* j) {
   if (!type_ok(c.type) || !heads_ok(c.H, c.Hkv, c.D) || c.B < 0 || c.window < 0 ||
-      c.max_cache_len < 0 || c.max_cache_len > 0x7fffffff - 1024 || c.table_width < 1 ||
+      c.max_cache_len < 0 || c.max_cache_len > kMost || c.table_width < 1 ||
       static_cast<int64_t>(c.B) * c.H > (1 << 24))
     return ATTN_ERR_SHAPE;
   if (!isfinite(c.softcap) || !isfinite(c.scale)) return ATTN_ERR_PARAM;
@@ -166,7 +172,7 @@ int kv_cache_append_paged(int type, const attn_rows* q, const attn_rows* q_out, 
                           const float* k_norm_w, float norm_eps, const attn_paged_kv* cache,
                           const int32_t* block_table, int table_width, int32_t* status,
                           void* stream) {
-  if (!type_ok(type) || !heads_ok(H, Hkv, D) || T < 0 || B < 0 || table_width < 1 ||
+  if (!type_ok(type) || !heads_ok(H, Hkv, D) || T < 0 || B < 0 || B > kMost || table_width < 1 ||
       static_cast<int64_t>(T) * (H + 2 * static_cast<int64_t>(Hkv)) > 0x7fffffff ||
       (!cu_seqlens && T != B))
     return ATTN_ERR_SHAPE;
@@ -211,7 +217,7 @@ int kv_cache_append_paged(int type, const attn_rows* q, const attn_rows* q_out, 
 
 size_t gqa_attn_decode_paged_workspace_size(int B, int H, int Hkv, int D, int32_t max_cache_len,
                                             int window) {
-  if (!heads_ok(H, Hkv, D) || B < 1 || max_cache_len < 0 || window < 0) return 0;
+  if (!decode_sizes_ok(H, Hkv, D, B, max_cache_len) || window < 0) return 0;
   return gqa::decode_paged_bytes(B, H, Hkv, D, max_cache_len, window, 0);
 }
 
@@ -238,7 +244,7 @@ int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cac
 
 size_t gqa_attn_decode_shared_workspace_size(int B, int H, int Hkv, int D, int32_t prefix_len,
                                              int32_t max_cache_len) {
-  if (!heads_ok(H, Hkv, D) || B < 1 || prefix_len < 1 || max_cache_len < 0) return 0;
+  if (!decode_sizes_ok(H, Hkv, D, B, max_cache_len) || prefix_len < 1 || prefix_len > kMost) return 0;
   return shared_layout(B, H, Hkv, D, prefix_len, max_cache_len).total;
 }
 
@@ -251,7 +257,7 @@ int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* ca
   gqa::DecodePagedJob j{};
   const DecodeCall c{type, q, out, cache, block_table, table_width, cache_len, max_cache_len,
                      B, H, Hkv, D, 0, softcap, scale};
-  if (prefix_len < 1 || prefix_len > 0x7fffffff - 1024 || prefix_width < 1) return ATTN_ERR_SHAPE;
+  if (prefix_len < 1 || prefix_len > kMost || prefix_width < 1) return ATTN_ERR_SHAPE;
   if (int rc = decode_checks(c, &j)) return rc;
   if (B == 0) return ATTN_OK;
   if (!prefix_table) return ATTN_ERR_NULL;
@@ -298,8 +304,8 @@ int gqa_attn_prefill_packed(int type, const attn_rows* q, const attn_rows* k, co
                             int B, int H, int Hkv, int D, int window, float softcap, float scale,
                             int32_t* status, void* stream) {
   if (!type_ok(type) || !heads_ok(H, Hkv, D) || T < 0 || B < 0 || max_len < 0 || window < 0 ||
-      static_cast<int64_t>(T) * H > 0x7fffffff ||
-      (static_cast<int64_t>(T) + B) * Hkv > 0x7fffffff)
+      T > kMost || static_cast<int64_t>(T) * H > 0x7fffffff ||
+      (static_cast<int64_t>(T) + B) * Hkv > kMost)
     return ATTN_ERR_SHAPE;
   if (!isfinite(softcap) || !isfinite(scale)) return ATTN_ERR_PARAM;
   if (T == 0 || B == 0) return ATTN_OK;

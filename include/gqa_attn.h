@@ -645,7 +645,8 @@ int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* ca
  * of one element they are not read), 16-byte aligned at the start (ATTN_ERR_ALIGN,
  * ATTN_ERR_SHAPE); an output's rows may not overlap each other (ATTN_ERR_PARAM). Outputs
  * must not overlap inputs, except where a call says so.
- * D is a multiple of 8, 16 <= D <= 128; H / Hkv <= 128.
+ * D is a multiple of 8, 16 <= D <= 128; H / Hkv <= 128. Rows, sequences and positions are at
+ * most 2^31 - 1025 (ATTN_ERR_SHAPE; workspace sizes past a call's limits are 0).
  */
 #define ATTN_TYPE_FP16 1
 #define ATTN_TYPE_BF16 2

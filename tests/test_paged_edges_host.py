@@ -3,7 +3,7 @@ visible)."""
 import itertools
 
 import gqa_causal_attention_gb300 as g
-from test_paged_host import ALIGN, D, H, HKV, P, WORKSPACE, no_device, shared
+from test_paged_host import ALIGN, CAPACITY, D, H, HKV, P, SHAPE, WORKSPACE, append, decode, no_device, prefill, rows, shared
 
 
 @no_device
@@ -36,3 +36,24 @@ def test_the_shared_call_takes_a_larger_batchs_workspace():
         assert call(wbytes=own - 1) == WORKSPACE and call(wbytes=own) == ALIGN
         for more, longer in ((b + 1, prefix), (b, prefix + 130), (300, 30000)):
             assert call(wbytes=need(more, H, HKV, D, longer, 100)) == ALIGN   # enough: the address is next
+
+
+@no_device
+def test_the_largest_sizes():
+    """Rows, sequences and positions whose last tile would pass 2^31 are refused, and no workspace is
+    named for them."""
+    top, most = (1 << 31) - 1, (1 << 31) - 1025
+    one = dict(q=rows(heads=1), k=rows(heads=1), v=rows(heads=1), out=rows(heads=1), h=1, hkv=1)
+    assert prefill(T=top, b=1, **one) == SHAPE and prefill(T=most + 1, b=1, **one) == SHAPE
+    assert prefill(T=5, b=most - 4, **one) == SHAPE
+    assert prefill(T=most - 1, b=1, **{**one, "q": rows(P + 8, heads=1)}) == ALIGN   # as far as the rows
+    assert append(b=most + 1) == SHAPE and append(b=most, max_pos=-1) != SHAPE
+    assert decode(max_len=most + 1) == SHAPE and decode(max_len=most) == CAPACITY
+    assert shared(prefix=most + 1) == SHAPE and shared(prefix=most) == CAPACITY
+    paged, both = g.gqa_attn_decode_paged_workspace_size, g.gqa_attn_decode_shared_workspace_size
+    assert paged(3, 8, 2, 64, most) > 0 and both(3, 8, 2, 64, most, most) > 0
+    for n in (most + 1, top):
+        assert paged(3, 8, 2, 64, n) == 0 and paged(3, 8, 2, 64, n, top) == 0
+        assert both(3, 8, 2, 64, n, 5) == 0 and both(3, 8, 2, 64, 100, n) == 0
+    assert paged((1 << 24) + 1, 1, 1, 64, 5000) == 0 and both((1 << 21) + 1, 8, 2, 64, 100, 5) == 0
+    assert paged(1 << 21, 8, 2, 64, 5000, most) > 0
