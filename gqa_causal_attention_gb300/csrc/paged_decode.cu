@@ -65,7 +65,7 @@ struct DecodeArgs {
   int64_t q_token, q_head, o_token, o_head;
   const void* k;
   const void* v;
-  int64_t page_stride, head_stride;
+  int64_t page_stride;
   int pages, page_shift;
   const int32_t* block_table;
   int64_t width;
@@ -838,7 +838,6 @@ cudaError_t launch_decode_paged(const DecodePagedJob& j, cudaStream_t stream) {
   a.out = j.out.p; a.o_token = j.out.token; a.o_head = j.out.head;
   a.k = j.cache.k; a.v = j.cache.v;
   a.page_stride = j.cache.page_stride;
-  a.head_stride = static_cast<int64_t>(j.D) << j.cache.page_shift;
   a.pages = j.cache.pages; a.page_shift = j.cache.page_shift;
   a.block_table = j.block_table; a.width = j.width;
   a.cache_len = j.cache_len; a.max_len = j.max_len;
