@@ -1013,7 +1013,8 @@ def gqa_attn_decode_shared(q, k_cache, v_cache, prefix_table, prefix_len: int, b
                            scale: float = 0.0, workspace=None, status=None, stream=None) -> None:
     """gqa_attn_decode_paged for rows that all begin with the prefix_len positions in the pages of
     prefix_table (int32 [pages]), followed by cache_len[b] of their own in the pages of
-    block_table; the prefix is read once for all rows. workspace:
+    block_table. A prefix that the rows together would read more than 64 MB of is read once for all
+    of them; another with each row's own positions. workspace:
     gqa_attn_decode_shared_workspace_size bytes, or None."""
     if workspace is None:
         B, H, D = q.shape
@@ -1031,7 +1032,8 @@ def gqa_attn_prefill_packed(q, k, v, cu_seqlens, max_len: int, out, window: int 
                             stream=None) -> None:
     """out [T, H, D] = causal (or windowed) attention of packed prompts: sequence b is rows
     cu_seqlens[b] .. cu_seqlens[b + 1] (int32 [B + 1], lengths at most max_len) of q [T, H, D] and
-    k, v [T, Hkv, D] (fp16 or bf16, rotated). Rows of no sequence are left alone."""
+    k, v [T, Hkv, D] (fp16 or bf16, rotated). A sequence sees its own tokens alone, nothing of a
+    cache. Rows of no sequence are left alone."""
     rc = (_ext or _native()).prefill_packed(q, k, v, cu_seqlens, max_len, out, window, softcap,
                                             scale, status, stream)
     if rc:

@@ -6,7 +6,9 @@
 //
 // over blocks of 128 keys with a running reference m per query row; products of 16-bit operands
 // with fp32 accumulation, softmax and sums in fp32, P rounded once to 16 bits for the second
-// product (half a step of the type, the size of the output's own rounding).
+// product: half a step of the type, the size of the output's own rounding (one prompt of 77 tokens in
+// fp16, against 64 bits: 2.2e-4 in norm, 2.0e-4 with fp32 weights). In two 16-bit parts it would cost
+// half as many products again.
 //
 // How, on GB300:
 //  * A tile is 128 rows: TQ = 128 / G tokens x the G query heads of one kv head, which share
@@ -33,10 +35,12 @@
 //    pair of tiles each).
 //  * Every wait is bounded; one that runs out raises ATTN_DEV_TIMEOUT and the block winds down.
 //
-// Measured (32 heads of 128 over 8): one prompt of 8192 tokens 352 us, 1560 TFLOP/s of products
-// that are needed, 0.82 of the library product's rate measured on such a GPU; tensor pipe at 68 %
-// of its cycles, the rest lost where a tile's softmax and its products wait for one another. 16
-// prompts of 1..2048 tokens 117 us (tensor pipe 53 %): the start and the end of each unit.
+// Measured (32 heads of 128 over 8): one prompt of 8192 tokens 353 us at 2070 MHz, 1560 TFLOP/s of
+// products that are needed, 0.82 of the library product's rate measured on such a GPU; call after
+// call for seconds, where the power limit takes the clock to 1927 MHz, 379 us. Tensor pipe at 68 % of
+// its cycles, the rest lost where a tile's softmax and its products wait for one another. 8 prompts of
+// 134..2013 tokens and 8 empty sequences 117..120 us (tensor pipe 53 %): the start and the end of each
+// unit.
 #pragma once
 
 #include <algorithm>
@@ -885,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   dependent_wait();
   if (gated_off(a.skip)) return;
   // The rows' own kernel finds room as these blocks end (after the wait: see paged_decode.cu). Another
-  // prefill that waits in these blocks' places gains nothing: 16 prompts, repeated, 118 -> 126 us.
+  // prefill that waits in these blocks' places gains nothing: 8 prompts of 134..2013, repeated, 118 -> 126 us.
   if (C::SHARED) dependents_may_launch();
   if (warp == 9) {
     tc::tmem_alloc(&bars->tmem_base, kTmemCols);

@@ -637,7 +637,10 @@ int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* ca
  * Serving in 16 bits from a paged cache. The four calls below take bf16 or fp16 tensors
  * (one type for all of a call's), prompts packed one after the other without padding, and
  * a KV cache in pages that rows of any length share; sums, softmax and rotation are fp32,
- * and each result is rounded once.
+ * and each result is rounded once. On the tensor cores (gqa_attn_prefill_packed, and a
+ * shared prefix that is read once for all rows) the softmax's weights are rounded to the
+ * call's type before they are applied to the values: half a step of each, beside the
+ * result's own. Elsewhere they are off by 2^-16 of themselves at most.
  *
  * Rows: queries, keys, values and outputs are [T, heads, D] with strides of their own in
  * elements, x[t * token_stride + h * head_stride + d], so that they may be slices of one
@@ -690,7 +693,8 @@ typedef struct attn_paged_kv {
  *   rp, table, norm weights (fp32) as for kv_cache_append (the norm's sum of squares in
  *               fp32, so not for rows whose squares leave fp32's normal numbers)
  * A sequence with bad bounds (ATTN_DEV_LENGTH) or positions outside [0, max_pos]
- * (ATTN_DEV_POSITION) is skipped. Two tokens for one slot leave either's.
+ * (ATTN_DEV_POSITION) is skipped; bounds that decrease set ATTN_DEV_LENGTH, and only
+ * sequences whose own bounds hold are written. Two tokens for one slot leave pieces of both.
  */
 int kv_cache_append_paged(int type, const attn_rows* q, const attn_rows* q_out, const attn_rows* k,
                           const attn_rows* k_out, const attn_rows* v, int T, int B, int H, int Hkv,
@@ -726,7 +730,9 @@ int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cac
  * prompt): row b's positions are the prefix's prefix_len >= 1, in the pages of prefix_table
  * (device int32 [prefix_width]), then its own cache_len[b] >= 0 in the pages of its block
  * table (position prefix_len + i of the row is slot i % page_size of entry
- * i / page_size). The prefix is read once for all rows, as a matrix product. No window.
+ * i / page_size). No window. A prefix that the rows together would read more than 64 MB
+ * of (4 * B * prefix_len * Hkv * D bytes) is read once for all of them, as a matrix product;
+ * a shorter one, or one of fewer rows, with each row's own positions, in one kernel.
  *   workspace   gqa_attn_decode_shared_workspace_size bytes, 16-byte aligned (never
  *               shrinking as B, prefix_len or max_cache_len grows)
  * A cache_len[b] outside [0, max_cache_len] sets ATTN_DEV_LENGTH and the row is left
@@ -750,6 +756,7 @@ int gqa_attn_decode_shared(int type, const attn_rows* q, const attn_paged_kv* ca
  * A sequence with bad bounds or longer than max_len sets ATTN_DEV_LENGTH and is skipped;
  * rows of no sequence are neither written nor have a part in any result, whatever they
  * hold. (An inf or NaN in a sequence's own v may reach rows of it that do not see it.)
+ * Positions already in a cache are not seen: a sequence is attended from its first token.
  */
 int gqa_attn_prefill_packed(int type, const attn_rows* q, const attn_rows* k, const attn_rows* v,
                             const int32_t* cu_seqlens, int32_t max_len, const attn_rows* out, int T,
