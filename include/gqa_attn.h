@@ -640,7 +640,8 @@ int kv_cache_evict_q4(const void* cache, const float* weights, const int32_t* ca
  * and each result is rounded once. On the tensor cores (gqa_attn_prefill_packed, and a
  * shared prefix that is read once for all rows) the softmax's weights are rounded to the
  * call's type before they are applied to the values: half a step of each, beside the
- * result's own. Elsewhere they are off by 2^-16 of themselves at most.
+ * result's own. Elsewhere a weight is off by 2^-16 of itself at most (in fp16 by 2^-22, and
+ * 2^-37 of its row's largest).
  *
  * Rows: queries, keys, values and outputs are [T, heads, D] with strides of their own in
  * elements, x[t * token_stride + h * head_stride + d], so that they may be slices of one
@@ -730,8 +731,8 @@ int gqa_attn_decode_paged(int type, const attn_rows* q, const attn_paged_kv* cac
  * prompt): row b's positions are the prefix's prefix_len >= 1, in the pages of prefix_table
  * (device int32 [prefix_width]), then its own cache_len[b] >= 0 in the pages of its block
  * table (position prefix_len + i of the row is slot i % page_size of entry
- * i / page_size). No window. A prefix that the rows together would read more than 64 MB
- * of (4 * B * prefix_len * Hkv * D bytes) is read once for all of them, as a matrix product;
+ * i / page_size). No window. A prefix that the rows together would read more than 2^26
+ * bytes of (4 * B * prefix_len * Hkv * D) is read once for all of them, as a matrix product;
  * a shorter one, or one of fewer rows, with each row's own positions, in one kernel.
  *   workspace   gqa_attn_decode_shared_workspace_size bytes, 16-byte aligned (never
  *               shrinking as B, prefix_len or max_cache_len grows)
